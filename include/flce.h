@@ -66,8 +66,9 @@ typedef enum flce_status {
     FLCE_ERR_CUDA = 6           /* a CUDA runtime or driver call failed */
 } flce_status;
 
-/* element type of x, W and dx; dW is always fp32, the loss always fp32 */
-enum { FLCE_DTYPE_BF16 = 0, FLCE_DTYPE_FP32 = 1 };
+/* element type of x, W and dx; dW is always fp32, the loss always fp32.
+ * FP16 is a type of router logits only. */
+enum { FLCE_DTYPE_BF16 = 0, FLCE_DTYPE_FP32 = 1, FLCE_DTYPE_FP16 = 2 };
 
 /* How the dlogits of a chunk are formed (fp32 handles run SLABS as asked and
  * every other mode in place).
@@ -196,7 +197,16 @@ enum {
                                     x, W and t into device memory, timed on the stream
                                     that runs them (the copy stream for flce_submit_host);
                                     `bytes` counts the bytes copied                   */
-    FLCE_K_NUM_KINDS = 15
+    FLCE_K_ROUTE = 15,           /* softmax, top-k, counts and sums of the router logits */
+    FLCE_K_ROUTE_FINISH = 16,    /* counts, slopes and losses from the blocks' sums     */
+    FLCE_K_ROUTE_BACKWARD = 17,  /* gradient of the router logits                       */
+    FLCE_K_MUON_MOMENTUM = 18,   /* momentum update and sum of squares                  */
+    FLCE_K_MUON_PREPARE = 19,    /* X = u / (|u| + eps) in two fp16 parts               */
+    FLCE_K_MUON_GRAM = 20,       /* A = X Xt (symmetric) on tcgen05                     */
+    FLCE_K_MUON_POLY = 21,       /* B = b A + c A^2 (symmetric) on tcgen05              */
+    FLCE_K_MUON_APPLY = 22,      /* X = a X + B X on tcgen05                            */
+    FLCE_K_MUON_RESULT = 23,     /* the last step's B X, written as update or weight    */
+    FLCE_K_NUM_KINDS = 24
 };
 
 typedef struct flce_kernel_profile {
@@ -425,6 +435,113 @@ const char* flce_last_error(flce_handle_t h);
 flce_status flce_loss_static(const void* x, const void* W, const int64_t* t, int64_t N,
                              int64_t H, int64_t V, int64_t ignore_index, float* loss,
                              float* token_loss, void* stream);
+
+/* ---- expert routing with its balance and z losses --------------------------
+ * The auxiliary losses of a model with experts, added to the LM loss, and the
+ * routing they belong to. Per token n of logits z (N x E): p = softmax(z), the
+ * k experts of largest z (ties to the lowest index), their probabilities as
+ * weights (renormalize: divided by their sum). A token is live if valid[n] is
+ * not zero (valid NULL: all are), some z is above -inf, and it lies in a
+ * document. Tokens are grouped into documents by offsets (documents + 1
+ * ascending int64 from 0 to N on the device; NULL: one document). With n_d
+ * live tokens in document d, n in all, c_de slots of its tokens that chose
+ * expert e and P_de the sum of p_e over them:
+ *   balance = sum_d (n_d / n) sum_e (E c_de / (k n_d)) (P_de / n_d)
+ *   z       = (1 / n) sum over live tokens of (log sum exp z)^2
+ * both 0 if n = 0. A slot whose z is -inf, and every slot of a token that is
+ * not live, gets expert -1 and weight 0 and is not counted. A NaN or +inf
+ * logit makes its token's weights and the losses NaN (its experts stay in
+ * [-1, E)). Arithmetic is fp32, sums over blocks fp64, results repeat bit for
+ * bit. No host synchronisation; capturable. */
+typedef struct flce_route_args {
+    const void* logits;          /* device, N rows of E, bf16, fp32 or fp16            */
+    int32_t dtype;               /* FLCE_DTYPE_* of logits                             */
+    int32_t k;                   /* 1 <= k <= min(E, 32)                               */
+    int64_t N, E;                /* 0 <= N < 2^31, 1 <= E <= 1024                      */
+    int64_t ld;                  /* row stride of logits, in elements, >= E            */
+    int32_t renormalize;         /* 1: weights of a token sum to one                   */
+    int32_t reserved;            /* 0                                                  */
+    const uint8_t* valid;        /* device, N bytes, or NULL                           */
+    const int64_t* offsets;      /* device, documents + 1, or NULL                     */
+    int64_t documents;           /* >= 1 (1 without offsets)                           */
+    float* weights;              /* device, N x k                                      */
+    int32_t* experts;            /* device, N x k                                      */
+    int64_t* counts;             /* device, documents x E: c_de                        */
+    float* stats;                /* device, N x 2, 8-byte aligned: largest z (-inf where
+                                    not live), log of the sum of exp(z - largest)       */
+    float* slope;                /* device, documents x E: E c_de / (k n_d)            */
+    float* result;               /* device, 4: balance, z, 1 / n, n (int32 bits)       */
+} flce_route_args;
+
+/* Workspace bytes of flce_route_forward (0: bad argument). Host only. */
+uint64_t flce_route_workspace_bytes(flce_handle_t h, int64_t N, int64_t E, int64_t documents);
+
+/* Fills weights, experts, counts, lse, slope and result on `stream`. The
+ * workspace (device, 256-byte aligned) is the caller's and free again when the
+ * call's work is done, so calls on several streams take one each. Offsets are
+ * not checked on the host; whatever they hold, no access leaves the buffers.
+ * Errors: INVALID_ARG, UNSUPPORTED (dtype), BUDGET (workspace), CUDA. */
+flce_status flce_route_forward(flce_handle_t h, const flce_route_args* args, void* workspace,
+                               uint64_t workspace_bytes, void* stream);
+
+/* d_logits (device, N x E, dtype of logits, row stride ld_d) from the
+ * gradients of weights (N x k fp32, or NULL), balance and z (one fp32 on the
+ * device each, or NULL). args are those of the forward, with its outputs
+ * unchanged. The counts carry no gradient. Rows that are not live get zeros.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+flce_status flce_route_backward(flce_handle_t h, const flce_route_args* args, const float* d_weights,
+                                const float* d_balance, const float* d_z, void* d_logits, int64_t ld_d,
+                                void* stream);
+
+/* ---- orthogonalised momentum update (Newton-Schulz) ------------------------
+ * For each of `count` matrices of rows x cols:
+ *   momentum given: buf = beta buf + (1 - beta) g (in place),
+ *                   u = nesterov ? beta buf + (1 - beta) g : buf;  else u = g
+ *   X = u / (|u|_F + eps); per step, on the short side of X,
+ *   A = X Xt, B = b A + c A^2, X = a X + B X;   O = scale X
+ *   weight given:   W = (1 - lr weight_decay) W - lr O (in place)
+ *   else            update = O, rounded once to its type
+ * The products run on the tensor cores with fp16 operands (X, A and B scaled
+ * by powers of two, X itself held in 22 bits, the diagonal of B in fp32) and
+ * fp32 accumulators: O is within about 2.5e-3 of its own norm of the exact
+ * result, the size of one bf16 rounding, whatever the spectrum. Momentum,
+ * norms and the weight update are fp32 (the norm fp64). Matrices of one call
+ * share sizes and types; strides may differ. No host synchronisation;
+ * capturable. A device-side wait that ran out is reported by
+ * flce_async_status; the outputs are then unspecified. */
+#define FLCE_MUON_MAX_STEPS 32
+typedef struct flce_muon_args {
+    int64_t rows, cols;          /* 1 .. 65536                                         */
+    int32_t grad_dtype;          /* FLCE_DTYPE_BF16 or FP32                            */
+    int32_t weight_dtype;        /* of weight, if given                                */
+    int32_t update_dtype;        /* of update, if no weight is given                   */
+    int32_t nesterov;
+    int32_t steps;               /* 1 .. FLCE_MUON_MAX_STEPS                           */
+    int32_t reserved;            /* 0                                                  */
+    const float* coefficients;   /* HOST, steps x 3 (a, b, c); NULL: 3.4445, -4.7750,
+                                    2.0315 at every step. Refused if they take X's
+                                    singular values above 3.9 before a step             */
+    double beta, eps, scale, lr, weight_decay;
+} flce_muon_args;
+
+typedef struct flce_muon_matrix {
+    const void* grad;            /* device, rows of cols elements, row stride ld_grad  */
+    float* momentum;             /* device fp32, or NULL (for all matrices)            */
+    void* weight;                /* device, or NULL (for all matrices)                 */
+    void* update;                /* device; used where weight is NULL                  */
+    int64_t ld_grad, ld_momentum, ld_weight, ld_update;
+} flce_muon_matrix;
+
+/* Workspace bytes of flce_muon_update (0: bad argument or count 0). Host only.
+ * Matrices go through it in groups, so it stops growing with count at about
+ * 2 GiB (or one matrix). */
+uint64_t flce_muon_workspace_bytes(int64_t rows, int64_t cols, int64_t count);
+
+/* mats: HOST array of count entries. The workspace (device, 1024-byte aligned)
+ * is the caller's, as for flce_route_forward. The tensors of one call must not
+ * overlap. Errors: INVALID_ARG, UNSUPPORTED, BUDGET (workspace), CUDA. */
+flce_status flce_muon_update(flce_handle_t h, const flce_muon_args* args, const flce_muon_matrix* mats,
+                             int32_t count, void* workspace, uint64_t workspace_bytes, void* stream);
 
 /* ---- checks of single parts (used by the tests) ------------------------- */
 

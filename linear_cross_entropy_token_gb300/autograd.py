@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import torch
 
+from . import routing
 from .flce import FLCE
 
 _handles = {}
@@ -100,3 +101,39 @@ def linear_cross_entropy(x: torch.Tensor, W: torch.Tensor, t: torch.Tensor,
     """
     return LinearCrossEntropyFunction.apply(x, W, t, ignore_index, chunk, reduction, handle,
                                             sync_free, dlogits_mode, hbm_budget_bytes)
+
+
+class RouteFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, k, valid, offsets, renormalize, handle):
+        r = routing.route(logits, k, valid=valid, offsets=offsets, renormalize=renormalize, handle=handle)
+        # the outputs are separate tensors: the losses of r are views of one
+        balance, z = r.balance.clone(), r.z.clone()
+        ctx.handle, ctx.k, ctx.renormalize = handle, k, renormalize
+        ctx.save_for_backward(logits, valid, offsets, r.weights, r.experts, r.counts, r.stats, r.slope, r.result)
+        ctx.mark_non_differentiable(r.experts, r.counts)
+        ctx.set_materialize_grads(False)
+        return r.weights, r.experts, r.counts, balance, z
+
+    @staticmethod
+    def backward(ctx, d_weights, _d_experts, _d_counts, d_balance, d_z):
+        r = routing.Routing()
+        (logits, r.valid, r.offsets, r.weights, r.experts, r.counts, r.stats, r.slope,
+         r.result) = ctx.saved_tensors
+        r.k, r.renormalize = ctx.k, ctx.renormalize
+        d = None
+        if ctx.needs_input_grad[0]:
+            if d_weights is not None:
+                d_weights = d_weights.contiguous()
+            d = routing.route_backward(r, logits, d_weights=d_weights, d_balance=d_balance, d_z=d_z,
+                                       handle=ctx.handle)
+        return d, None, None, None, None, None
+
+
+def route(logits: torch.Tensor, k: int, valid=None, offsets=None, renormalize: bool = True,
+          handle: FLCE = None):
+    """Expert routing as a differentiable call: (weights, experts, counts,
+    balance, z) of routing.route. Gradients reach logits from the weights and
+    the two losses; the experts and their counts carry none. Neither direction
+    synchronises the host."""
+    return RouteFunction.apply(logits, k, valid, offsets, renormalize, handle)

@@ -11,22 +11,13 @@
 // follow the pattern of "Unlocking asynchronicity in continuous batching"
 // (pogovet.com): all work is ordered on one caller stream and the host blocks
 // once per call, on the loss read-back.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <array>
-#include <cstdarg>
-#include <cstdio>
 #include <cstring>
-#include <map>
-#include <mutex>
 #include <string>
 #include <vector>
 
-#include <nvtx3/nvToolsExt.h>
-
-#include "../../include/flce.h"
-#include "flce_internal.h"
+#include "flce_handle.h"
 
 using namespace flce;
 
@@ -47,8 +38,6 @@ constexpr uint64_t kSlabBytes = static_cast<uint64_t>(FLCE_SLAB_MIB) << 20;
 constexpr int64_t kSlabAlign = 512;
 constexpr int64_t kMinSlab = 8192;
 constexpr int64_t kSlabMaxChunk = 4096;
-constexpr int64_t kMaxDim = (1ll << 31) - 1;
-constexpr uint64_t kAlign = 1024;
 // in-place and recompute modes run the dW GEMM beside the dx GEMM on a second
 // stream when the dx launch has fewer work units than this many waves of CTA
 // pairs (small problems, where dx leaves SMs idle)
@@ -56,41 +45,6 @@ constexpr uint64_t kAlign = 1024;
 #define FLCE_OVERLAP_WAVES 2
 #endif
 constexpr int kOverlapWaves = FLCE_OVERLAP_WAVES;
-
-uint64_t align_up(uint64_t v, uint64_t a) { return (v + a - 1) / a * a; }
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// ------------------------------------------------------------ driver entry
-
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
-
-bool get_encode() {
-  std::call_once(g_encode_once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
-  return g_encode != nullptr;
-}
-
-// --------------------------------------------------------------- profiling
-
-struct EventPair {
-  cudaEvent_t start = nullptr, stop = nullptr;
-  int kind = 0;
-  double flops = 0, bytes = 0;
-};
-
-struct Profiler {
-  bool enabled = false;
-  std::vector<EventPair> pool;
-  size_t used = 0;
-  flce_kernel_profile totals[FLCE_K_NUM_KINDS] = {};
-};
 
 // ------------------------------------------------------------- workspace
 
@@ -144,9 +98,6 @@ bool valid_cta_mode(int mode) {
   return mode == FLCE_CTA_AUTO || mode == FLCE_CTA_SINGLE || mode == FLCE_CTA_PAIR ||
          mode == FLCE_CTA_WIDE;
 }
-
-// Tile shapes of one GEMM launch
-enum Shape : int { kShapeSingle = 0, kShapePair = 1, kShapeWide = 2 };
 
 // A time model of one GEMM on CTA pairs, in SM cycles, for choosing between
 // wide (256 x 512, single-buffered accumulator) and pair (256 x 256, double-
@@ -527,108 +478,7 @@ flce_status plan_impl(const flce_config* cfg, int64_t N, int64_t H, int64_t V, i
 
 }  // namespace
 
-// ------------------------------------------------------------------ handle
-
-struct flce_handle_s {
-  flce_config cfg{};
-  int device = 0;
-  int num_sms = 0;
-  int pair_clusters = 0;  // clusters of two the pair kernels fit at once
-  int wide_clusters = 0;  // clusters of two the wide kernels fit at once
-  // tile shape of the handle's GEMMs; an AUTO handle (cfg.cta_pair stays
-  // FLCE_CTA_AUTO) runs each GEMM on the shape its plan names, wide or pair
-  int shape = kShapeSingle;
-  uint64_t timeout_ns = 0;
-  std::string err;
-  // workspace
-  void* ws = nullptr;
-  uint64_t ws_bytes = 0;
-  bool ws_external = false;
-  bool ws_fresh = true;  // the control block, sticky word included, needs zeroing
-  // staging for the host-buffer entry point
-  void* stage = nullptr;
-  uint64_t stage_bytes = 0;
-  uint32_t* host_ctrl = nullptr;  // pinned
-  // pipelined host-buffer entry: two staging slots, copies on their own stream
-  struct Slot {
-    void* stage = nullptr;
-    uint64_t bytes = 0;
-    cudaEvent_t copied = nullptr;  // the slot's inputs have landed (copy stream)
-    cudaEvent_t freed = nullptr;   // the call that read the slot has finished with it
-    cudaEvent_t done = nullptr;    // the call's control words are in host memory
-    uint32_t* host = nullptr;      // pinned copy of the control words
-    uint64_t ticket = 0;
-    bool pending = false;
-  };
-  Slot slots[2];
-  cudaStream_t copy_stream = nullptr;
-  // SLABS: the dW GEMM of a slab runs on a second stream beside the dx GEMM
-  // of the same slab, so each fills the other's last wave
-  cudaStream_t side_stream = nullptr;
-  cudaEvent_t slab_ready = nullptr;  // the slab's dlogits are in the buffer
-  cudaEvent_t slab_freed = nullptr;  // the slab's dW GEMM has read the buffer
-  uint64_t next_ticket = 1;
-  flce_plan last_plan{};
-  int64_t last_N = -1;
-  uint64_t token_loss_off = 0;
-  bool has_plan = false;
-  int64_t launches = 0;
-  Profiler prof;
-  std::map<std::array<int, 5>, int> group_cache;  // pick_group_m by (shape, num_m, num_n, num_s, slots)
-  // the plan of the last sizes planned (a training loop repeats them)
-  std::array<int64_t, 4> plan_key{-1, -1, -1, -1};
-  flce_plan plan_cached{};
-};
-
 namespace {
-
-flce_status fail(flce_handle_t h, flce_status st, const char* fmt, ...) {
-  if (h) {
-    char b[512];
-    va_list ap;
-    va_start(ap, fmt);
-    std::vsnprintf(b, sizeof b, fmt, ap);
-    va_end(ap);
-    h->err = b;
-  }
-  return st;
-}
-
-struct DeviceGuard {
-  int prev = -1;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-    if (prev != dev) cudaSetDevice(dev);
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-  }
-};
-
-void prof_begin(flce_handle_t h, int kind, cudaStream_t s) {
-  if (!h->prof.enabled) return;
-  Profiler& p = h->prof;
-  if (p.used == p.pool.size()) {
-    EventPair e;
-    cudaEventCreate(&e.start);
-    cudaEventCreate(&e.stop);
-    p.pool.push_back(e);
-  }
-  EventPair& e = p.pool[p.used];
-  e.kind = kind;
-  cudaEventRecord(e.start, s);
-}
-
-void prof_end(flce_handle_t h, cudaStream_t s, double flops, double bytes) {
-  if (!h->prof.enabled) return;
-  Profiler& p = h->prof;
-  EventPair& e = p.pool[p.used];
-  e.flops = flops;
-  e.bytes = bytes;
-  cudaEventRecord(e.stop, s);
-  ++p.used;
-}
 
 void prof_collect(flce_handle_t h) {
   Profiler& p = h->prof;
@@ -645,27 +495,6 @@ void prof_collect(flce_handle_t h) {
   }
   p.used = 0;
 }
-
-// NVTX range over the host-side enqueue of a call, a chunk or a launch, so a
-// timeline profiler can attribute the GPU work to the path's steps. Costs a
-// few nanoseconds when no profiler is attached.
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
-
-#define FLCE_LAUNCH(kind, flops, bytes, expr)                                                \
-  do {                                                                                      \
-    NvtxRange nvtx_(flce_kernel_name(kind));                                                \
-    prof_begin(h, (kind), s);                                                               \
-    cudaError_t e_ = (expr);                                                                \
-    prof_end(h, s, (flops), (bytes));                                                       \
-    ++h->launches;                                                                          \
-    if (e_ != cudaSuccess)                                                                  \
-      return fail(h, FLCE_ERR_CUDA, "%s: %s", flce_kernel_name(kind), cudaGetErrorString(e_)); \
-  } while (0)
 
 flce_status ensure_workspace(flce_handle_t h, uint64_t bytes) {
   if (h->ws_external) {
@@ -689,35 +518,6 @@ flce_status ensure_workspace(flce_handle_t h, uint64_t bytes) {
   h->ws_bytes = bytes;
   h->ws_fresh = true;
   return FLCE_OK;
-}
-
-bool encode_map(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void* base, int rank,
-                const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
-                std::string* why) {
-  if (!get_encode()) {
-    *why = "cuTensorMapEncodeTiled is not available from the driver";
-    return false;
-  }
-  cuuint64_t gd[3], gs[2];
-  cuuint32_t bx[3], es[3] = {1, 1, 1};
-  for (int i = 0; i < rank; ++i) {
-    gd[i] = dims[i];
-    bx[i] = box[i];
-  }
-  for (int i = 0; i < rank - 1; ++i) gs[i] = strides_bytes[i];
-  (void)esize;
-  CUresult r = g_encode(m, dt, static_cast<cuuint32_t>(rank), const_cast<void*>(base), gd, gs, bx, es,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) {
-    char b[160];
-    std::snprintf(b, sizeof b, "cuTensorMapEncodeTiled failed (%d), rank %d, dims %llu x %llu", int(r),
-                  rank, static_cast<unsigned long long>(dims[0]),
-                  static_cast<unsigned long long>(dims[1]));
-    *why = b;
-    return false;
-  }
-  return true;
 }
 
 // 2-D bf16 map over a row-major matrix (inner = contiguous extent)
@@ -1379,6 +1179,15 @@ const char* flce_kernel_name(int32_t kind) {
     case FLCE_K_DEVICE_RESULT: return "device_result";
     case FLCE_K_COMBINE_DLOGITS: return "combine_dlogits";
     case FLCE_K_H2D_COPY: return "h2d_copy";
+    case FLCE_K_ROUTE: return "route";
+    case FLCE_K_ROUTE_FINISH: return "route_finish";
+    case FLCE_K_ROUTE_BACKWARD: return "route_backward";
+    case FLCE_K_MUON_MOMENTUM: return "muon_momentum";
+    case FLCE_K_MUON_PREPARE: return "muon_prepare";
+    case FLCE_K_MUON_GRAM: return "muon_gram";
+    case FLCE_K_MUON_POLY: return "muon_poly";
+    case FLCE_K_MUON_APPLY: return "muon_apply";
+    case FLCE_K_MUON_RESULT: return "muon_result";
     default: return "?";
   }
 }
@@ -1437,6 +1246,7 @@ flce_status flce_create(flce_handle_t* out, const flce_config* cfg) {
     delete h;
     return FLCE_ERR_CUDA;
   }
+  std::memset(h->host_ctrl, 0, kCtrlWords * 4);
   *out = h;
   return FLCE_OK;
 }
@@ -1519,13 +1329,17 @@ flce_status flce_async_status(flce_handle_t h, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return fail(h, FLCE_ERR_CUDA, "async status: %s", cudaGetErrorString(e));
-  if (!h->ws || h->ws_fresh) return FLCE_OK;
+  // the training-step operators record their errors in the handle's pinned words
+  volatile uint32_t* host_sticky = h->host_ctrl + kCtrlSticky;
+  const uint32_t train = *host_sticky;
+  *host_sticky = 0;
+  if (!h->ws || h->ws_fresh) return device_status(h, train);
   uint32_t* sticky = static_cast<uint32_t*>(h->ws) + kCtrlSticky;  // the control block leads the workspace
   uint32_t code = 0;
   e = cudaMemcpy(&code, sticky, 4, cudaMemcpyDeviceToHost);
   if (e == cudaSuccess && code != 0) e = cudaMemset(sticky, 0, 4);
   if (e != cudaSuccess) return fail(h, FLCE_ERR_CUDA, "async status: %s", cudaGetErrorString(e));
-  return device_status(h, code);
+  return device_status(h, code != 0 ? code : train);
 }
 
 flce_status flce_count_valid(flce_handle_t h, const int64_t* t, int64_t N, int64_t ignore_index,

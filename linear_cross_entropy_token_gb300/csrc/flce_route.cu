@@ -1,0 +1,609 @@
+// Expert routing with its balance and z losses, forward and backward.
+//
+// Per token row of E logits z: p = softmax(z), lse = log sum exp z, the k
+// experts of largest z (ties to the lowest index) with their probabilities as
+// weights (divided by their sum if asked). Per document d with n_d live
+// tokens, c_de chosen slots and P_de = sum of p_e over its tokens, and n live
+// tokens in all:
+//   balance = sum_d (n_d / n) sum_e (E c_de / (k n_d)) (P_de / n_d)
+//   z       = (1 / n) sum lse^2
+// The counts carry no gradient, so with slope_de = E c_de / (k n_d n)
+//   d z_e = p_e (u_e - sum_j p_j u_j) + g_z 2 lse / n p_e,
+//   u_e = g_balance slope_de + (the gradient of the chosen weights).
+//
+// A row is held by G lanes with NPL consecutive experts each, in registers,
+// from the one load to the last use; the sums over tokens stay in registers
+// too (an expert's column belongs to one lane) until a block's piece of a
+// document ends. Sums over tokens are taken in a fixed order (per piece, then
+// over the pieces), so results repeat bit for bit; only integer counts use
+// atomics. All arithmetic is fp32; sums over blocks are fp64.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "flce_train.h"
+
+namespace flce {
+namespace {
+
+constexpr int kWarps = kRouteThreads / 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xFF800000); }
+
+// max that keeps a NaN, so that a row with one is not taken for a dead row
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+template <class T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+
+// NPL consecutive elements of a row from column c0 on; `fill` past column E.
+// 16-byte loads where the caller found the rows aligned and the whole vector
+// lies inside the row.
+template <class T, int NPL>
+__device__ __forceinline__ void load_row(const T* row, int c0, int E, bool vec, float fill, float (&z)[NPL]) {
+  constexpr int V = 16 / sizeof(T);
+#pragma unroll
+  for (int c = 0; c < NPL; c += V) {
+    if (vec && c0 + c + V <= E) {
+      union {
+        uint4 u;
+        T t[V];
+      } w;
+      w.u = *reinterpret_cast<const uint4*>(row + c0 + c);
+#pragma unroll
+      for (int i = 0; i < V; ++i) z[c + i] = to_f(w.t[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) z[c + i] = c0 + c + i < E ? to_f(row[c0 + c + i]) : fill;
+    }
+  }
+}
+
+template <class T, int NPL>
+__device__ __forceinline__ void store_row(T* row, int c0, int E, bool vec, const float (&z)[NPL]) {
+  constexpr int V = 16 / sizeof(T);
+#pragma unroll
+  for (int c = 0; c < NPL; c += V) {
+    if (vec && c0 + c + V <= E) {
+      union {
+        uint4 u;
+        T t[V];
+      } w;
+#pragma unroll
+      for (int i = 0; i < V; ++i) w.t[i] = from_f<T>(z[c + i]);
+      *reinterpret_cast<uint4*>(row + c0 + c) = w.u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (c0 + c + i < E) row[c0 + c + i] = from_f<T>(z[c + i]);
+    }
+  }
+}
+
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+
+template <int G>
+__device__ __forceinline__ float group_max_nan(float v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+
+// The first document whose end lies past row r (documents: none does). The
+// index stays in [0, documents] whatever the offsets hold.
+__device__ __forceinline__ int first_document(const int64_t* offsets, int documents, int64_t r) {
+  if (!offsets) return 0;
+  int lo = 0, hi = documents;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (offsets[mid + 1] > r)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+
+template <class T, int G, int NPL>
+__global__ void __launch_bounds__(kRouteThreads) route_forward_kernel(const RouteArgs a) {
+  constexpr int RPW = 32 / G;          // rows a warp holds at once
+  constexpr int kCols = G * NPL;
+  extern __shared__ uint8_t smem[];
+  float* red = reinterpret_cast<float*>(smem);                        // [kWarps * RPW][kCols]
+  int32_t* cnt = reinterpret_cast<int32_t*>(red + kWarps * RPW * kCols);  // [kCols]
+  float* stage_v = reinterpret_cast<float*>(cnt + kCols);             // [kWarps][RPW][k]
+  int32_t* stage_i = reinterpret_cast<int32_t*>(stage_v + kWarps * RPW * a.k);
+  __shared__ float sh_scale[kWarps * RPW];
+  __shared__ float sh_z[kWarps];
+  __shared__ int32_t sh_live[kWarps];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gl = lane % G, gr = lane / G;
+  const uint32_t gmask = (G == 32 ? kAll : ((1u << G) - 1u)) << (G == 32 ? 0 : gr * G);
+  const int c0 = gl * NPL;
+  const int k = a.k;
+  const T* logits = static_cast<const T*>(a.logits);
+  const bool vec = ((reinterpret_cast<uintptr_t>(logits) | (a.ld * sizeof(T))) & 15u) == 0;
+  float* my_v = stage_v + warp * RPW * k;
+  int32_t* my_i = stage_i + warp * RPW * k;
+  float* my_scale = sh_scale + warp * RPW;
+
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+
+  const int64_t r0 = blockIdx.x * a.rows_per_block;
+  const int64_t r1 = min(a.N, r0 + a.rows_per_block);
+  int doc = first_document(a.offsets, a.documents, r0);
+  int64_t r = r0;
+  while (r < r1) {
+    // the piece [r, end): of document doc, or between documents (dead rows)
+    int64_t end = r1;
+    bool outside = false;
+    if (a.offsets) {
+      while (doc < a.documents && a.offsets[doc + 1] <= r) ++doc;
+      if (doc == a.documents) {
+        outside = true;
+      } else {
+        const int64_t begin = a.offsets[doc];
+        outside = begin > r;
+        end = min(r1, outside ? begin : a.offsets[doc + 1]);
+      }
+    }
+    for (int e = threadIdx.x; e < kCols; e += kRouteThreads) cnt[e] = 0;
+    float acc[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) acc[i] = 0.f;
+    float zacc = 0.f;
+    int live_rows = 0;
+    __syncthreads();
+
+    for (int64_t base = r + warp * RPW; base < end; base += kWarps * RPW) {
+      const int64_t row = base + gr;
+      const bool in = row < end;
+      float z[NPL];
+      if (in) {
+        load_row<T, NPL>(logits + row * a.ld, c0, a.E, vec, neg_inf(), z);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) z[i] = neg_inf();
+      }
+      bool live = in && !outside && (!a.valid || a.valid[row] != 0);
+      float m = z[0];
+#pragma unroll
+      for (int i = 1; i < NPL; ++i) m = max_nan(m, z[i]);
+      m = group_max_nan<G>(m);
+      live = live && !(m == neg_inf());
+      const float mm = live ? m : 0.f;
+      float p[NPL], sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) {
+        p[i] = exp2_approx((z[i] - mm) * kLog2e);
+        sum += p[i];
+      }
+      sum = group_sum<G>(sum);
+      const float inv = 1.0f / sum;
+      if (live) {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) acc[i] = fmaf(p[i], inv, acc[i]);
+      }
+      if (in && gl == 0) {
+        const float log_sum = logf(sum);
+        // apart: their sum would lose log_sum's last bits where |m| is large,
+        // and with them the backward's softmax
+        a.stats[row] = make_float2(live ? m : neg_inf(), live ? log_sum : 0.f);
+        if (live) {
+          const float lse = mm + log_sum;
+          zacc = fmaf(lse, lse, zacc);
+          ++live_rows;
+        }
+      }
+      // k rounds: the group's largest logit, the lowest lane that has it (its
+      // experts come before the others'), the first of that lane's
+      float share = 0.f;
+      for (int j = 0; j < k; ++j) {
+        float bv = neg_inf();
+        int bi = 0;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+          if (z[i] > bv) {
+            bv = z[i];
+            bi = i;
+          }
+        }
+        const float g = group_max<G>(bv);
+        const uint32_t who = __ballot_sync(kAll, bv == g) & gmask;
+        const bool taken = live && g > neg_inf();
+        const float ex = taken ? exp2_approx((g - mm) * kLog2e) : 0.f;
+        share += ex;
+        if (__ffs(who) - 1 == lane) {
+          my_v[gr * k + j] = ex;
+          my_i[gr * k + j] = taken ? c0 + bi : -1;
+#pragma unroll
+          for (int i = 0; i < NPL; ++i)
+            if (i == bi) z[i] = neg_inf();
+        }
+      }
+      if (gl == 0) my_scale[gr] = a.renormalize ? (share == 0.f ? 0.f : 1.0f / share) : inv;
+      __syncwarp();
+      const int slots = static_cast<int>(min(static_cast<int64_t>(RPW), end - base)) * k;
+      for (int t = lane; t < slots; t += 32) {
+        const int e = my_i[t];
+        a.weights[base * k + t] = e >= 0 ? my_v[t] * my_scale[t / k] : 0.f;
+        a.experts[base * k + t] = e;
+        if (e >= 0) atomicAdd(&cnt[e], 1);
+      }
+      __syncwarp();
+    }
+
+    // the piece's sums, in a fixed order
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) red[(warp * RPW + gr) * kCols + c0 + i] = acc[i];
+    for (int o = 16; o > 0; o >>= 1) {
+      zacc += __shfl_xor_sync(kAll, zacc, o);
+      live_rows += __shfl_xor_sync(kAll, live_rows, o);
+    }
+    if (lane == 0) {
+      sh_z[warp] = zacc;
+      sh_live[warp] = live_rows;
+    }
+    __syncthreads();
+    if (!outside) {
+      const int64_t unit = static_cast<int64_t>(blockIdx.x) + doc;
+      for (int e = threadIdx.x; e < a.E; e += kRouteThreads) {
+        float s = 0.f;
+        for (int w = 0; w < kWarps * RPW; ++w) s += red[w * kCols + e];
+        a.unit_p[unit * a.E + e] = s;
+        a.unit_c[unit * a.E + e] = cnt[e];
+      }
+      if (threadIdx.x == 0) {
+        float s = 0.f;
+        int n = 0;
+        for (int w = 0; w < kWarps; ++w) {
+          s += sh_z[w];
+          n += sh_live[w];
+        }
+        a.unit_z[unit] = s;
+        a.unit_live[unit] = n;
+      }
+    }
+    __syncthreads();
+    r = end;
+  }
+}
+
+// The blocks whose rows meet document d: [*b0, *b1), empty if it has none.
+__device__ __forceinline__ void document_blocks(const RouteArgs& a, int d, int* b0, int* b1) {
+  int64_t lo = 0, hi = a.N;
+  if (a.offsets) {
+    lo = a.offsets[d];
+    hi = a.offsets[d + 1];
+  }
+  lo = max(lo, static_cast<int64_t>(0));
+  hi = min(hi, a.N);
+  if (lo >= hi) {
+    *b0 = *b1 = 0;
+    return;
+  }
+  *b0 = static_cast<int>(lo / a.rows_per_block);
+  *b1 = static_cast<int>((hi - 1) / a.rows_per_block) + 1;
+}
+
+// One block of R warps per (document, chunk of experts): counts, slopes and
+// the balance term of its experts from the units, in order. The last block to
+// finish adds the terms, in order, and writes the losses.
+template <int R>
+__global__ void __launch_bounds__(32 * R) route_finish_kernel(const RouteArgs a, int chunks, int chunk_size) {
+  __shared__ double sh_d[R][33];
+  __shared__ int32_t sh_c[R][33];
+  __shared__ double sh_t[3][R];
+  __shared__ bool last;
+  const int d = blockIdx.x / chunks, chunk = blockIdx.x - d * chunks;
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  int b0, b1;
+  document_blocks(a, d, &b0, &b1);
+
+  int n = 0;
+  double zs = 0.0;
+  for (int b = b0 + threadIdx.x; b < b1; b += 32 * R) {
+    n += a.unit_live[static_cast<int64_t>(b) + d];
+    zs += a.unit_z[static_cast<int64_t>(b) + d];
+  }
+  for (int o = 16; o > 0; o >>= 1) {
+    n += __shfl_xor_sync(kAll, n, o);
+    zs += __shfl_xor_sync(kAll, zs, o);
+  }
+  if (tx == 0) {
+    sh_t[0][ty] = n;
+    sh_t[1][ty] = zs;
+  }
+  __syncthreads();
+  n = 0;
+  zs = 0.0;
+  for (int w = 0; w < R; ++w) {
+    n += static_cast<int>(sh_t[0][w]);
+    zs += sh_t[1][w];
+  }
+  const double slope_n = n > 0 ? static_cast<double>(a.E) / (static_cast<double>(a.k) * n) : 0.0;
+
+  double term = 0.0;
+  const int e_end = min(a.E, (chunk + 1) * chunk_size);
+  for (int e0 = chunk * chunk_size; e0 < e_end; e0 += 32) {
+    const int e = e0 + tx;
+    double p = 0.0;
+    int c = 0;
+    if (e < e_end) {
+#pragma unroll 4
+      for (int b = b0 + ty; b < b1; b += R) {
+        const int64_t u = (static_cast<int64_t>(b) + d) * a.E + e;
+        p += a.unit_p[u];
+        c += a.unit_c[u];
+      }
+    }
+    sh_d[ty][tx] = p;
+    sh_c[ty][tx] = c;
+    __syncthreads();
+    if (ty == 0 && e < e_end) {
+      p = 0.0;
+      c = 0;
+      for (int w = 0; w < R; ++w) {
+        p += sh_d[w][tx];
+        c += sh_c[w][tx];
+      }
+      const int64_t o = static_cast<int64_t>(d) * a.E + e;
+      a.counts[o] = c;
+      a.slope[o] = static_cast<float>(slope_n * c);
+      term += slope_n * c * p;
+    }
+    __syncthreads();
+  }
+  if (ty == 0) {
+    for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(kAll, term, o);
+    if (tx == 0) {
+      a.terms[blockIdx.x] = term;
+      if (chunk == 0) {
+        a.doc_live[d] = n;
+        a.doc_z[d] = zs;
+      }
+    }
+  }
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+
+  // fixed order: a thread's stride, then the tree
+  double bal = 0.0, z = 0.0, live = 0.0;
+  const int64_t terms = static_cast<int64_t>(a.documents) * chunks;
+  for (int64_t i = threadIdx.x; i < terms; i += 32 * R) bal += __ldcg(a.terms + i);
+  for (int i = threadIdx.x; i < a.documents; i += 32 * R) {
+    live += __ldcg(a.doc_live + i);
+    z += __ldcg(a.doc_z + i);
+  }
+  for (int o = 16; o > 0; o >>= 1) {
+    bal += __shfl_xor_sync(kAll, bal, o);
+    z += __shfl_xor_sync(kAll, z, o);
+    live += __shfl_xor_sync(kAll, live, o);
+  }
+  if (tx == 0) {
+    sh_t[0][ty] = bal;
+    sh_t[1][ty] = z;
+    sh_t[2][ty] = live;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    bal = z = live = 0.0;
+    for (int w = 0; w < R; ++w) {
+      bal += sh_t[0][w];
+      z += sh_t[1][w];
+      live += sh_t[2][w];
+    }
+    const double inv = live > 0.0 ? 1.0 / live : 0.0;
+    a.result[0] = static_cast<float>(bal * inv);
+    a.result[1] = static_cast<float>(z * inv);
+    a.result[2] = static_cast<float>(inv);
+    a.result[3] = __int_as_float(static_cast<int32_t>(live));
+  }
+}
+
+template <class T, int G, int NPL>
+__global__ void __launch_bounds__(kRouteThreads)
+    route_backward_kernel(const RouteArgs a, const float* d_weights, const float* d_balance, const float* d_z,
+                          T* d_logits, int64_t ldd) {
+  constexpr int RPW = 32 / G;
+  constexpr int kCols = G * NPL;
+  extern __shared__ uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gl = lane % G, gr = lane / G;
+  const int c0 = gl * NPL;
+  const int k = a.k;
+  // what the chosen weights add to d_logits of this group's row
+  float* extra = reinterpret_cast<float*>(smem) + (warp * RPW + gr) * kCols;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) extra[c0 + i] = 0.f;
+  __syncwarp();
+  const T* logits = static_cast<const T*>(a.logits);
+  const bool vec = ((reinterpret_cast<uintptr_t>(logits) | (a.ld * sizeof(T))) & 15u) == 0;
+  const bool vec_d = ((reinterpret_cast<uintptr_t>(d_logits) | (ldd * sizeof(T))) & 15u) == 0;
+  const float inv_n = a.result[2];
+  const float gb = d_balance ? *d_balance * inv_n : 0.f;
+  const float gz = d_z ? 2.0f * *d_z * inv_n : 0.f;
+
+  const int64_t r0 = blockIdx.x * a.rows_per_block;
+  const int64_t r1 = min(a.N, r0 + a.rows_per_block);
+  int doc = first_document(a.offsets, a.documents, r0), held = -1;
+  float slope[NPL];
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) slope[i] = 0.f;
+  for (int64_t base = r0 + warp * RPW; base < r1; base += kWarps * RPW) {
+    const int64_t row = base + gr;
+    const bool in = row < r1;
+    const float2 stat = in ? a.stats[row] : make_float2(neg_inf(), 0.f);
+    const bool live = !(stat.x == neg_inf());
+    if (in && a.offsets)
+      while (doc < a.documents && a.offsets[doc + 1] <= row) ++doc;
+    if (live && doc != held && doc < a.documents) {
+      load_row<float, NPL>(a.slope + static_cast<int64_t>(doc) * a.E, c0, a.E, false, 0.f, slope);
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) slope[i] *= gb;
+      held = doc;
+    }
+    float z[NPL];
+    if (live) {
+      load_row<T, NPL>(logits + row * a.ld, c0, a.E, vec, neg_inf(), z);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) z[i] = neg_inf();
+    }
+    // chosen slots: w (g - [renormalised] sum g w) lands on the slot's expert
+    float gw = 0.f;
+    if (d_weights && live) {
+      for (int j = gl; j < k; j += G) gw = fmaf(d_weights[row * k + j], a.weights[row * k + j], gw);
+    }
+    gw = group_sum<G>(gw);
+    if (d_weights && live) {
+      for (int j = gl; j < k; j += G) {
+        const int e = a.experts[row * k + j];
+        if (e >= 0 && e < a.E)
+          extra[e] = a.weights[row * k + j] * (d_weights[row * k + j] - (a.renormalize ? gw : 0.f));
+      }
+    }
+    __syncwarp();
+    float p[NPL], dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      p[i] = live ? exp2_approx(((z[i] - stat.x) - stat.y) * kLog2e) : 0.f;
+      dot = fmaf(p[i], slope[i], dot);
+    }
+    dot = group_sum<G>(dot) + (a.renormalize ? 0.f : gw);
+    const float shift = live ? gz * (stat.x + stat.y) - dot : 0.f;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      p[i] = fmaf(p[i], slope[i] + shift, extra[c0 + i]);
+      extra[c0 + i] = 0.f;
+    }
+    if (in) store_row<T, NPL>(d_logits + row * ldd, c0, a.E, vec_d, p);
+    __syncwarp();
+  }
+}
+
+template <class T, int G, int NPL>
+cudaError_t forward_t(const RouteArgs& a, cudaStream_t s) {
+  const size_t rows = kWarps * (32 / G), cols = G * NPL;
+  const size_t smem = rows * cols * 4 + cols * 4 + rows * a.k * 8;
+  auto kern = route_forward_kernel<T, G, NPL>;
+  if (smem > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<a.blocks, kRouteThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <class T, int G, int NPL>
+cudaError_t backward_t(const RouteArgs& a, const float* dw, const float* db, const float* dz, void* out, int64_t ldd,
+                       cudaStream_t s) {
+  const size_t smem = kWarps * (32 / G) * static_cast<size_t>(G * NPL) * 4;
+  route_backward_kernel<T, G, NPL><<<a.blocks, kRouteThreads, smem, s>>>(a, dw, db, dz, static_cast<T*>(out), ldd);
+  return cudaGetLastError();
+}
+
+// f(G, NPL) for the geometry's instantiation, as integral constants
+template <class T, class F>
+cudaError_t for_geometry(const RouteGeometry& g, F&& f) {
+  if (g.per_lane == 8) {
+    switch (g.lanes) {
+      case 1: return f(std::integral_constant<int, 1>(), std::integral_constant<int, 8>());
+      case 2: return f(std::integral_constant<int, 2>(), std::integral_constant<int, 8>());
+      case 4: return f(std::integral_constant<int, 4>(), std::integral_constant<int, 8>());
+      case 8: return f(std::integral_constant<int, 8>(), std::integral_constant<int, 8>());
+      case 16: return f(std::integral_constant<int, 16>(), std::integral_constant<int, 8>());
+      default: return f(std::integral_constant<int, 32>(), std::integral_constant<int, 8>());
+    }
+  }
+  if (g.per_lane == 16) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 16>());
+  return f(std::integral_constant<int, 32>(), std::integral_constant<int, 32>());
+}
+
+}  // namespace
+
+RouteGeometry route_geometry(int64_t N, int64_t E, int64_t documents, int num_sms) {
+  RouteGeometry g;
+  g.per_lane = E <= 256 ? 8 : (E <= 512 ? 16 : 32);
+  g.lanes = 1;
+  while (g.lanes < 32 && static_cast<int64_t>(g.lanes) * g.per_lane < E) g.lanes *= 2;
+  const int64_t step = kWarps * (32 / g.lanes);
+  const int64_t most = 4 * static_cast<int64_t>(num_sms);
+  int64_t per = (N + most - 1) / most;
+  per = (per + step - 1) / step * step;
+  g.rows_per_block = per > 0 ? per : step;
+  g.blocks = static_cast<int>((N + g.rows_per_block - 1) / g.rows_per_block);
+  g.chunks = documents >= num_sms ? 1 : static_cast<int>((E + 31) / 32);
+  return g;
+}
+
+cudaError_t launch_route_forward(int dtype, const RouteGeometry& g, const RouteArgs& a, cudaStream_t s) {
+  auto run = [&](auto t) {
+    using T = decltype(t);
+    return for_geometry<T>(g, [&](auto G, auto NPL) { return forward_t<T, G.value, NPL.value>(a, s); });
+  };
+  return dtype == 0 ? run(__nv_bfloat16()) : dtype == 1 ? run(float()) : run(__half());
+}
+
+cudaError_t launch_route_finish(const RouteGeometry& g, const RouteArgs& a, cudaStream_t s) {
+  const int chunk_size = g.chunks == 1 ? a.E : 32;
+  // a document spread over many blocks has many units to add: more warps
+  if (a.blocks >= 64 * static_cast<int64_t>(a.documents))
+    route_finish_kernel<32><<<a.documents * g.chunks, 1024, 0, s>>>(a, g.chunks, chunk_size);
+  else
+    route_finish_kernel<8><<<a.documents * g.chunks, 256, 0, s>>>(a, g.chunks, chunk_size);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_route_backward(int dtype, const RouteGeometry& g, const RouteArgs& a, const float* d_weights,
+                                  const float* d_balance, const float* d_z, void* d_logits, int64_t ldd,
+                                  cudaStream_t s) {
+  auto run = [&](auto t) {
+    using T = decltype(t);
+    return for_geometry<T>(g, [&](auto G, auto NPL) {
+      return backward_t<T, G.value, NPL.value>(a, d_weights, d_balance, d_z, d_logits, ldd, s);
+    });
+  };
+  return dtype == 0 ? run(__nv_bfloat16()) : dtype == 1 ? run(float()) : run(__half());
+}
+
+}  // namespace flce

@@ -1,0 +1,112 @@
+// Declarations of the training-step operators beside the fused loss: expert
+// routing with its balance loss, and the orthogonalised momentum update.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace flce {
+
+// ------------------------------------------------------- flce_route.cu
+
+constexpr int kRouteMaxExperts = 1024;
+constexpr int kRouteMaxK = 32;
+constexpr int kRouteThreads = 256;
+
+// Unit u = b + d of the workspace holds what block b saw of document d: since
+// consecutive pieces of the token axis move to the next block, the next
+// document or both, the sum names a piece uniquely.
+struct RouteArgs {
+  const void* logits;
+  int64_t N, ld;
+  int32_t E, k;
+  int32_t renormalize;
+  int32_t documents;        // >= 1
+  const uint8_t* valid;     // [N] or null
+  const int64_t* offsets;   // [documents + 1] or null (one document)
+  float* weights;           // [N][k]
+  int32_t* experts;         // [N][k]
+  int64_t* counts;          // [documents][E]
+  float2* stats;            // [N]: largest logit m (-inf for a token that routes nowhere), log sum exp(z - m)
+  float* slope;             // [documents][E]: E c / (k n_d)
+  float* result;            // balance, z, 1 / n, n (int32 bits)
+  int64_t rows_per_block;
+  int32_t blocks;
+  // workspace
+  float* unit_p;            // [units][E] sums of probabilities
+  int32_t* unit_c;          // [units][E] chosen slots
+  int32_t* unit_live;       // [units]
+  float* unit_z;            // [units] sums of lse^2
+  double* terms;            // [documents * chunks]
+  int32_t* doc_live;        // [documents]
+  double* doc_z;            // [documents]
+  uint32_t* ticket;
+};
+
+struct RouteGeometry {
+  int lanes;                // lanes per token row
+  int per_lane;             // experts per lane
+  int64_t rows_per_block;
+  int blocks;
+  int chunks;               // expert chunks per document in the closing launch
+};
+RouteGeometry route_geometry(int64_t N, int64_t E, int64_t documents, int num_sms);
+
+cudaError_t launch_route_forward(int dtype, const RouteGeometry& g, const RouteArgs& a, cudaStream_t s);
+cudaError_t launch_route_finish(const RouteGeometry& g, const RouteArgs& a, cudaStream_t s);
+cudaError_t launch_route_backward(int dtype, const RouteGeometry& g, const RouteArgs& a, const float* d_weights,
+                                  const float* d_balance, const float* d_z, void* d_logits, int64_t ldd,
+                                  cudaStream_t s);
+
+// -------------------------------------------------------- flce_muon.cu
+
+constexpr int kMuonMaxMats = 32;     // matrices of one launch
+constexpr int kMuonNormBlocks = 256; // partial sums of squares per matrix
+
+struct MuonMat {
+  const void* grad;
+  float* momentum;                   // or null
+  void* weight;                      // or null: then `update` is written
+  void* update;
+  int64_t ld_grad, ld_momentum, ld_weight, ld_update;
+};
+
+struct MuonArgs {
+  MuonMat mat[kMuonMaxMats];
+  int32_t count, rows, cols;         // rows x cols matrices, as the caller holds them
+  int32_t m, n;                      // the short and the long side
+  int32_t transposed;                // rows > cols: X is the transpose of the update
+  int32_t grad_dtype, weight_dtype, update_dtype;
+  int32_t vec;                       // 16-byte (bf16: 8-byte) accesses of four elements are aligned
+  int32_t nesterov, norm_blocks;
+  float beta, one_minus_beta;
+  double eps;
+  float decay, lr;                   // W = decay W - lr scale O
+  float scale;
+  // workspace
+  uint32_t* ctrl;
+  uint32_t* host_error;              // pinned host word: first device-side error
+  double* norm;                      // [count][kMuonNormBlocks]
+  float* diag;                       // [count][m]: diagonal of B
+  uint16_t* hi[2];                   // [count][m][ldx] fp16, X scaled by 2^12, two buffers
+  uint16_t* lo;                      // [count][m][ldx] fp16 remainder of X
+  uint16_t* gram;                    // [count][m][lda] fp16, A scaled by 2^12
+  uint16_t* poly;                    // [count][m][lda] fp16, B scaled by 2^11, zero diagonal
+  int64_t ldx, lda;
+  uint64_t timeout_ns;
+};
+
+enum MuonPhase : int { kMuonGram = 0, kMuonPoly = 1, kMuonApply = 2, kMuonLast = 3 };
+
+struct MuonStep {
+  float a, b, c;                     // X = aX + (bA + cA^2) X
+  int32_t src;                       // hi[src] holds X; the next X goes to hi[1 - src]
+};
+
+cudaError_t launch_muon_momentum(const MuonArgs& a, cudaStream_t s);
+cudaError_t launch_muon_prepare(const MuonArgs& a, cudaStream_t s);
+cudaError_t launch_muon_gemm(int phase, const CUtensorMap& ta, const CUtensorMap& tb, const MuonArgs& a,
+                             const MuonStep& st, int pairs, cudaStream_t s);
+int muon_max_clusters();
+
+}  // namespace flce

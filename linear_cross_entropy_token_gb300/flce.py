@@ -19,7 +19,7 @@ HEADER = os.path.join(os.path.dirname(PKG), "include", "flce.h")
 FLCE_OK = 0
 STATUS = {0: "FLCE_OK", 1: "FLCE_ERR_INVALID_ARG", 2: "FLCE_ERR_UNSUPPORTED", 3: "FLCE_ERR_BUDGET",
           4: "FLCE_ERR_BAD_TARGET", 5: "FLCE_ERR_TIMEOUT", 6: "FLCE_ERR_CUDA"}
-DTYPE_BF16, DTYPE_FP32 = 0, 1
+DTYPE_BF16, DTYPE_FP32, DTYPE_FP16 = 0, 1, 2
 DLOGITS = {"auto": 0, "inplace": 1, "recompute": 2, "slabs": 3}
 DLOGITS_NAMES = {v: k for k, v in DLOGITS.items()}
 CTA = {"auto": 0, "single": 1, "pair": 2, "wide": 4}
@@ -27,7 +27,9 @@ BACKWARD = {"auto": 0, "separate": 1, "one_launch": 2}
 KERNEL_KINDS = ["count_valid", "gemm_logits_lse", "lse_combine", "dlogits_inplace",
                 "gemm_dlogits_recompute", "gemm_dx", "dx_split_reduce", "gemm_dw",
                 "loss_finalize", "simt_gemm_f32", "simt_tile_stats_f32", "gemm_dx_dw",
-                "device_result", "combine_dlogits", "h2d_copy"]
+                "device_result", "combine_dlogits", "h2d_copy", "route", "route_finish",
+                "route_backward", "muon_momentum", "muon_prepare", "muon_gram", "muon_poly",
+                "muon_apply", "muon_result"]
 
 
 class FlceError(RuntimeError):
@@ -63,6 +65,32 @@ class Plan(ctypes.Structure):
 class KernelProfile(ctypes.Structure):
     _fields_ = [("launches", ctypes.c_int64), ("total_ms", ctypes.c_double),
                 ("flops", ctypes.c_double), ("bytes", ctypes.c_double)]
+
+
+class RouteArgs(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("N", ctypes.c_int64), ("E", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("renormalize", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("valid", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+                ("documents", ctypes.c_int64), ("weights", ctypes.c_void_p),
+                ("experts", ctypes.c_void_p), ("counts", ctypes.c_void_p),
+                ("stats", ctypes.c_void_p), ("slope", ctypes.c_void_p), ("result", ctypes.c_void_p)]
+
+
+class MuonArgs(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("grad_dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("update_dtype", ctypes.c_int32),
+                ("nesterov", ctypes.c_int32), ("steps", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("coefficients", ctypes.POINTER(ctypes.c_float)), ("beta", ctypes.c_double),
+                ("eps", ctypes.c_double), ("scale", ctypes.c_double), ("lr", ctypes.c_double),
+                ("weight_decay", ctypes.c_double)]
+
+
+class MuonMatrix(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("momentum", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("update", ctypes.c_void_p), ("ld_grad", ctypes.c_int64),
+                ("ld_momentum", ctypes.c_int64), ("ld_weight", ctypes.c_int64),
+                ("ld_update", ctypes.c_int64)]
 
 
 _lib = None
@@ -111,6 +139,12 @@ def load() -> ctypes.CDLL:
         "flce_check_wait_timeout": (i32, [vp, u32, vp]),
         "flce_loss_static": (i32, [vp, vp, vp, i64, i64, i64, i64, ctypes.POINTER(ctypes.c_float),
                                    vp, vp]),
+        "flce_route_workspace_bytes": (u64, [vp, i64, i64, i64]),
+        "flce_route_forward": (i32, [vp, ctypes.POINTER(RouteArgs), vp, u64, vp]),
+        "flce_route_backward": (i32, [vp, ctypes.POINTER(RouteArgs), vp, vp, vp, vp, i64, vp]),
+        "flce_muon_workspace_bytes": (u64, [i64, i64, i64]),
+        "flce_muon_update": (i32, [vp, ctypes.POINTER(MuonArgs), ctypes.POINTER(MuonMatrix), i32, vp,
+                                   u64, vp]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(lib, name)
@@ -460,11 +494,16 @@ def loss_static(x, W, t, ignore_index: int = -100, token_loss=None):
 _handles = {}
 
 
+def cached_handle(device_index: int, dtype: str = "bf16") -> FLCE:
+    """The module-level calls' handle of a (device, dtype)."""
+    key = (device_index, dtype)
+    if key not in _handles:
+        _handles[key] = FLCE(dtype, key[0])
+    return _handles[key]
+
+
 def forward_backward(x, W, t, ignore_index: int = -100, chunk: int = 0):
     """Module-level call with a cached handle per (device, dtype)."""
     import torch
     dtype = "bf16" if x.dtype == torch.bfloat16 else "fp32"
-    key = (x.device.index or 0, dtype)
-    if key not in _handles:
-        _handles[key] = FLCE(dtype, key[0])
-    return _handles[key].forward_backward(x, W, t, ignore_index, chunk)
+    return cached_handle(x.device.index or 0, dtype).forward_backward(x, W, t, ignore_index, chunk)

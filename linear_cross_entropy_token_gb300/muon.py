@@ -1,0 +1,183 @@
+"""The orthogonalised momentum update of weight matrices (Newton-Schulz).
+
+``muon_update`` takes matrices of one shape through momentum, normalisation,
+the Newton-Schulz steps on the short side and the weight update in one group of
+launches; ``orthogonalize`` is the map alone; ``Muon`` is a torch optimizer on
+top. include/flce.h has the formulas and the precision (flce_muon_update).
+These functions only check and marshal; the computation runs in the library's
+kernels on torch's current stream, without a host synchronisation.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from .flce import DTYPE_BF16, DTYPE_FP32, FLCE, MuonArgs, MuonMatrix, _stream_ptr, load
+from .routing import _handle, _row_stride
+
+DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
+MAX_DIM = 65536
+MAX_STEPS = 32
+
+
+def check_muon_tensors(grads, momenta, weights, updates) -> None:
+    """Shapes, dtypes, devices and layout of one call's matrices, and that no
+    two that are written start at one address. Raises ValueError."""
+    rows, cols = grads[0].shape if grads[0].dim() == 2 else (0, 0)
+    if not (1 <= rows <= MAX_DIM and 1 <= cols <= MAX_DIM):
+        raise ValueError(f"the matrices must be 2-D with 1 to {MAX_DIM} rows and columns")
+    dev = grads[0].device
+    written = []
+    for name, group, dtypes in (("grads", grads, DTYPES), ("momenta", momenta, (torch.float32,)),
+                                ("weights", weights, DTYPES), ("updates", updates, DTYPES)):
+        if group is None:
+            continue
+        if len(group) != len(grads):
+            raise ValueError(f"{name} must have as many matrices as grads")
+        for t in group:
+            if tuple(t.shape) != (rows, cols) or t.dtype != group[0].dtype or t.dtype not in dtypes:
+                raise ValueError(f"{name} must all be of shape ({rows}, {cols}) and of one supported dtype")
+            if t.device != dev or (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+                raise ValueError(f"{name} must have contiguous rows that do not overlap, on {dev}")
+        if name != "grads":
+            written += [t.data_ptr() for t in group]
+    if dev.type != "meta" and len(set(written)) != len(written):
+        raise ValueError("a matrix that is written appears twice")
+
+
+def _coefficients(coefficients, steps):
+    if not 1 <= steps <= MAX_STEPS:
+        raise ValueError(f"steps must lie in 1 .. {MAX_STEPS}")
+    if coefficients is None:
+        return None
+    rows = list(coefficients)
+    if rows and not hasattr(rows[0], "__len__"):
+        rows = [rows] * steps
+    if len(rows) != steps or any(len(r) != 3 for r in rows):
+        raise ValueError("coefficients must be (a, b, c), or one such triple for every step")
+    return (ctypes.c_float * (3 * steps))(*(float(v) for r in rows for v in r))
+
+
+def muon_update(grads, momenta=None, weights=None, *, beta: float = 0.95, nesterov: bool = True,
+                steps: int = 5, coefficients=None, eps: float = 1e-7, scale: float = 1.0,
+                lr: float = 0.0, weight_decay: float = 0.0, updates=None,
+                update_dtype: torch.dtype = torch.bfloat16, handle: FLCE = None):
+    """One update of matrices of one shape.
+
+    grads: list of (rows, cols) float32 or bfloat16 tensors. momenta: list of
+    float32 tensors, updated in place, or None to orthogonalise the gradients
+    themselves. weights: list of float32 or bfloat16 tensors, updated in place
+    with lr and weight_decay (returned), or None: the updates scale * O are
+    written to `updates`, new tensors of update_dtype by default (returned).
+    """
+    grads = list(grads)
+    momenta = None if momenta is None else list(momenta)
+    weights = None if weights is None else list(weights)
+    if weights is not None and updates is not None:
+        raise ValueError("weights are updated in place: no updates are written")
+    table = _coefficients(coefficients, steps)
+    if not grads:
+        return [] if weights is None else weights
+    if updates is None and weights is None:
+        if update_dtype not in DTYPES:
+            raise ValueError("updates must be bfloat16 or float32")
+        updates = [torch.empty(g.shape, dtype=update_dtype, device=g.device) for g in grads]
+    updates = None if updates is None else list(updates)
+    check_muon_tensors(grads, momenta, weights, updates)
+    h = _handle(grads[0], handle)
+    dev = grads[0].device
+    rows, cols = grads[0].shape
+    a = MuonArgs(rows, cols, DTYPES[grads[0].dtype],
+                 DTYPE_FP32 if weights is None else DTYPES[weights[0].dtype],
+                 DTYPE_FP32 if updates is None else DTYPES[updates[0].dtype], int(nesterov), steps, 0,
+                 table, beta, eps, scale, lr, weight_decay)
+    mats = (MuonMatrix * len(grads))()
+    for i, m in enumerate(mats):
+        m.grad, m.ld_grad = grads[i].data_ptr(), _row_stride(grads[i])
+        if momenta is not None:
+            m.momentum, m.ld_momentum = momenta[i].data_ptr(), _row_stride(momenta[i])
+        if weights is not None:
+            m.weight, m.ld_weight = weights[i].data_ptr(), _row_stride(weights[i])
+        else:
+            m.update, m.ld_update = updates[i].data_ptr(), _row_stride(updates[i])
+    nbytes = h.lib.flce_muon_workspace_bytes(rows, cols, len(grads))
+    # torch's allocations are 512-byte aligned, the workspace 1024
+    ws = torch.empty(nbytes + 1024, dtype=torch.uint8, device=dev)
+    base = (ws.data_ptr() + 1023) // 1024 * 1024
+    h._check(h.lib.flce_muon_update(h.h, ctypes.byref(a), mats, len(grads), base, nbytes, _stream_ptr(dev)),
+             "flce_muon_update")
+    return updates if weights is None else weights
+
+
+def orthogonalize(G: torch.Tensor, *, steps: int = 5, coefficients=None, eps: float = 1e-7,
+                  scale: float = 1.0, dtype: torch.dtype = torch.bfloat16, handle: FLCE = None) -> torch.Tensor:
+    """scale * the Newton-Schulz map of G (..., rows, cols), matrix by matrix:
+    the singular vectors of G with singular values near one."""
+    if G.dim() < 2:
+        raise ValueError("G must have at least two dimensions")
+    out = torch.empty(G.shape, dtype=dtype, device=G.device)
+    if G.numel() == 0:
+        return out
+    flat = G.reshape(-1, *G.shape[-2:])
+    muon_update(list(flat.unbind(0)), steps=steps, coefficients=coefficients, eps=eps, scale=scale,
+                updates=list(out.view(-1, *G.shape[-2:]).unbind(0)), handle=handle)
+    return out
+
+
+def workspace_bytes(rows: int, cols: int, count: int = 1) -> int:
+    """Device workspace of muon_update for count matrices (host only)."""
+    return int(load().flce_muon_workspace_bytes(rows, cols, count))
+
+
+class Muon(torch.optim.Optimizer):
+    """Momentum, orthogonalisation and weight update for 2-D parameters.
+
+    Parameters of one shape and type go through one call. scale: "rms" for
+    0.2 sqrt(max(rows, cols)), which gives an update's entries the size of an
+    adaptive optimizer's, "spectral" for sqrt(max(1, rows / cols)), or a
+    number. Vectors, embeddings and the LM head belong to another optimizer.
+    """
+
+    def __init__(self, params, lr: float = 2e-2, beta: float = 0.95, weight_decay: float = 0.0,
+                 nesterov: bool = True, steps: int = 5, coefficients=None, eps: float = 1e-7,
+                 scale="rms"):
+        if not (lr >= 0.0 and 0.0 <= beta <= 1.0 and weight_decay >= 0.0 and eps >= 0.0):
+            raise ValueError("need lr, weight_decay, eps >= 0 and 0 <= beta <= 1")
+        if scale not in ("rms", "spectral") and not isinstance(scale, (int, float)):
+            raise ValueError("scale must be 'rms', 'spectral' or a number")
+        _coefficients(coefficients, steps)
+        super().__init__(params, dict(lr=lr, beta=beta, weight_decay=weight_decay, nesterov=nesterov,
+                                      steps=steps, coefficients=coefficients, eps=eps, scale=scale))
+        for group in self.param_groups:
+            for p in group["params"]:
+                if p.dim() != 2 or p.dtype not in DTYPES:
+                    raise ValueError("Muon takes 2-D float32 or bfloat16 parameters")
+
+    @torch.no_grad()
+    def step(self, closure=None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for group in self.param_groups:
+            alike = {}
+            for p in group["params"]:
+                if p.grad is None:
+                    continue
+                state = self.state[p]
+                if "momentum" not in state:
+                    state["momentum"] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
+                alike.setdefault((tuple(p.shape), p.dtype, p.grad.dtype, p.device), []).append(p)
+            for (shape, _, _, _), ps in alike.items():
+                scale = group["scale"]
+                if scale == "rms":
+                    scale = 0.2 * math.sqrt(max(shape))
+                elif scale == "spectral":
+                    scale = math.sqrt(max(1.0, shape[0] / shape[1]))
+                muon_update([p.grad for p in ps], [self.state[p]["momentum"] for p in ps], ps,
+                            beta=group["beta"], nesterov=group["nesterov"], steps=group["steps"],
+                            coefficients=group["coefficients"], eps=group["eps"], scale=scale,
+                            lr=group["lr"], weight_decay=group["weight_decay"])
+        return loss

@@ -1,0 +1,160 @@
+"""Expert routing with its balance and z losses, forward and backward.
+
+Per token of router logits: softmax, the k largest experts (ties to the lowest
+index) and their probabilities as weights. Over the live tokens: how many
+slots chose each expert, the balance loss (per document where documents are
+given, each weighted by its tokens) and the z loss. include/flce.h has the
+formulas (flce_route_forward). These functions only check and marshal; the
+computation runs in the library's kernels on torch's current stream, without a
+host synchronisation. ``autograd.route`` is the differentiable form.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from .flce import (DTYPE_BF16, DTYPE_FP16, DTYPE_FP32, FLCE, RouteArgs, _stream_ptr, cached_handle)
+
+LOGIT_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32, torch.float16: DTYPE_FP16}
+MAX_EXPERTS = 1024
+MAX_K = 32
+
+
+class Routing:
+    """What one routing call found, as device tensors.
+
+    weights (N, k) float32 and experts (N, k) int32: each token's slots, best
+    first; a slot that routes nowhere has expert -1 and weight 0.
+    counts int64: slots per expert, (E,), or (documents, E) with offsets.
+    balance, z: the losses, 0-dim float32. n_live: 0-dim int32.
+    """
+
+    __slots__ = ("weights", "experts", "counts", "stats", "slope", "result", "valid", "offsets", "k",
+                 "renormalize")
+
+    @property
+    def balance(self) -> torch.Tensor:
+        return self.result[0]
+
+    @property
+    def z(self) -> torch.Tensor:
+        return self.result[1]
+
+    @property
+    def n_live(self) -> torch.Tensor:
+        return self.result[3].view(torch.int32)
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def check_route_tensors(logits, k, valid, offsets) -> None:
+    """Shapes, dtypes, devices and layout of one call. Raises ValueError."""
+    if logits.dim() != 2 or logits.dtype not in LOGIT_DTYPES:
+        raise ValueError("logits must be 2-D bfloat16, float32 or float16")
+    N, E = logits.shape
+    if not 1 <= E <= MAX_EXPERTS:
+        raise ValueError(f"logits must have 1 to {MAX_EXPERTS} columns")
+    if N >= 2 ** 31:
+        raise ValueError("too many rows")
+    if (E > 1 and N > 0 and logits.stride(1) != 1) or (N > 1 and logits.stride(0) < E):
+        raise ValueError("the rows of logits must be contiguous and not overlap")
+    if not 1 <= k <= min(E, MAX_K):
+        raise ValueError(f"k must lie in 1 .. min(columns, {MAX_K})")
+    if valid is not None and (tuple(valid.shape) != (N,) or valid.dtype not in (torch.bool, torch.uint8)
+                              or valid.device != logits.device or not valid.is_contiguous()):
+        raise ValueError(f"valid must be a contiguous bool or uint8 tensor of shape ({N},) on {logits.device}")
+    if offsets is not None and (offsets.dim() != 1 or offsets.numel() < 2 or offsets.numel() > 2 ** 24
+                                or offsets.dtype != torch.int64 or offsets.device != logits.device
+                                or not offsets.is_contiguous()):
+        raise ValueError(f"offsets must be a contiguous 1-D int64 tensor of at least two entries on {logits.device}")
+
+
+def _args(logits, r: Routing) -> RouteArgs:
+    N, E = logits.shape
+    a = RouteArgs()
+    a.logits = logits.data_ptr()
+    a.dtype = LOGIT_DTYPES[logits.dtype]
+    a.k = r.k
+    a.N, a.E, a.ld = N, E, _row_stride(logits)
+    a.renormalize = int(r.renormalize)
+    a.valid = None if r.valid is None else r.valid.data_ptr()
+    a.offsets = None if r.offsets is None else r.offsets.data_ptr()
+    a.documents = 1 if r.offsets is None else r.offsets.numel() - 1
+    a.weights = r.weights.data_ptr()
+    a.experts = r.experts.data_ptr()
+    a.counts = r.counts.data_ptr()
+    a.stats = r.stats.data_ptr()
+    a.slope = r.slope.data_ptr()
+    a.result = r.result.data_ptr()
+    return a
+
+
+def _handle(t: torch.Tensor, handle) -> FLCE:
+    if t.device.type != "cuda":
+        raise ValueError("the tensors must be on a CUDA device")
+    h = handle if handle is not None else cached_handle(t.device.index or 0)
+    if h.device != (t.device.index or 0):
+        raise ValueError(f"the handle is on device {h.device}, the tensors on {t.device}")
+    return h
+
+
+def route(logits: torch.Tensor, k: int, valid=None, offsets=None, renormalize: bool = True,
+          handle: FLCE = None) -> Routing:
+    """Route every row of logits (N, E) to its k largest experts.
+
+    valid: (N,) bool, False for tokens that do not count (as ignored targets do
+    not). offsets: (documents + 1,) int64 ascending from 0 to N, to balance
+    each document by itself. renormalize: a token's weights sum to one.
+    """
+    check_route_tensors(logits, k, valid, offsets)
+    h = _handle(logits, handle)
+    N, E = logits.shape
+    dev = logits.device
+    documents = 1 if offsets is None else offsets.numel() - 1
+    r = Routing()
+    r.k, r.renormalize, r.valid, r.offsets = k, renormalize, valid, offsets
+    r.weights = torch.empty((N, k), dtype=torch.float32, device=dev)
+    r.experts = torch.empty((N, k), dtype=torch.int32, device=dev)
+    r.counts = torch.empty((E,) if offsets is None else (documents, E), dtype=torch.int64, device=dev)
+    r.stats = torch.empty((N, 2), dtype=torch.float32, device=dev)
+    r.slope = torch.empty((documents, E), dtype=torch.float32, device=dev)
+    r.result = torch.empty(4, dtype=torch.float32, device=dev)
+    nbytes = h.lib.flce_route_workspace_bytes(h.h, N, E, documents)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    a = _args(logits, r)
+    h._check(h.lib.flce_route_forward(h.h, ctypes.byref(a), ws.data_ptr(), nbytes, _stream_ptr(dev)),
+             "flce_route_forward")
+    return r
+
+
+def route_backward(r: Routing, logits: torch.Tensor, d_weights=None, d_balance=None, d_z=None,
+                   out=None, handle: FLCE = None) -> torch.Tensor:
+    """d logits (in the dtype of logits) from the gradients of r.weights
+    (N, k) float32, of r.balance and of r.z (one float32 element on the device
+    each); None stands for zero. logits are those that r was made from."""
+    check_route_tensors(logits, r.k, r.valid, r.offsets)
+    h = _handle(logits, handle)
+    N, E = logits.shape
+    dev = logits.device
+    if tuple(r.weights.shape) != (N, r.k) or r.slope.shape[1] != E or r.weights.device != dev:
+        raise ValueError("the routing was not made from these logits")
+    if d_weights is not None and (tuple(d_weights.shape) != (N, r.k) or d_weights.dtype != torch.float32
+                                  or d_weights.device != dev or not d_weights.is_contiguous()):
+        raise ValueError(f"d_weights must be contiguous float32 of shape ({N}, {r.k}) on {dev}")
+    for name, g in (("d_balance", d_balance), ("d_z", d_z)):
+        if g is not None and (g.numel() != 1 or g.dtype != torch.float32 or g.device != dev):
+            raise ValueError(f"{name} must be one float32 element on {dev}")
+    if out is None:
+        out = torch.empty((N, E), dtype=logits.dtype, device=dev)
+    elif (tuple(out.shape) != (N, E) or out.dtype != logits.dtype or out.device != dev
+          or (E > 1 and N > 0 and out.stride(1) != 1) or (N > 1 and out.stride(0) < E)):
+        raise ValueError(f"out must be {logits.dtype} of shape ({N}, {E}) with contiguous rows on {dev}")
+    a = _args(logits, r)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    h._check(h.lib.flce_route_backward(h.h, ctypes.byref(a), ptr(d_weights), ptr(d_balance), ptr(d_z),
+                                       out.data_ptr(), _row_stride(out), _stream_ptr(dev)),
+             "flce_route_backward")
+    return out
