@@ -110,7 +110,7 @@ class RouteFunction(torch.autograd.Function):
         # the outputs are separate tensors: the losses of r are views of one
         balance, z = r.balance.clone(), r.z.clone()
         ctx.handle, ctx.k, ctx.renormalize = handle, k, renormalize
-        ctx.save_for_backward(logits, valid, offsets, r.weights, r.experts, r.counts, r.stats, r.slope, r.result)
+        ctx.save_for_backward(logits, valid, offsets, r.weights, r.experts, r.counts, r.state)
         ctx.mark_non_differentiable(r.experts, r.counts)
         ctx.set_materialize_grads(False)
         return r.weights, r.experts, r.counts, balance, z
@@ -118,8 +118,7 @@ class RouteFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, d_weights, _d_experts, _d_counts, d_balance, d_z):
         r = routing.Routing()
-        (logits, r.valid, r.offsets, r.weights, r.experts, r.counts, r.stats, r.slope,
-         r.result) = ctx.saved_tensors
+        logits, r.valid, r.offsets, r.weights, r.experts, r.counts, r.state = ctx.saved_tensors
         r.k, r.renormalize = ctx.k, ctx.renormalize
         d = None
         if ctx.needs_input_grad[0]:

@@ -187,7 +187,7 @@ struct NvtxRange {
 
 inline bool encode_map(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void* base, int rank,
                 const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
-                std::string* why) {
+                std::string* why, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   if (!get_encode()) {
     *why = "cuTensorMapEncodeTiled is not available from the driver";
     return false;
@@ -201,7 +201,7 @@ inline bool encode_map(CUtensorMap* m, CUtensorMapDataType dt, int esize, const 
   for (int i = 0; i < rank - 1; ++i) gs[i] = strides_bytes[i];
   (void)esize;
   CUresult r = g_encode(m, dt, static_cast<cuuint32_t>(rank), const_cast<void*>(base), gd, gs, bx, es,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     char b[160];

@@ -41,6 +41,15 @@ constexpr float kPolyB = 0.5f;              // 2^12 A -> 2^11 A
 constexpr float kPolyC = 1.f / 8192.f;      // (2^12 A)^2 -> 2^11 A^2
 constexpr float kPolyInv = 1.f / 2048.f;    // 2^11 B -> B; (2^11 B)(2^12 X) -> 2^12 B X
 
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float2 unpack_half2(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
 // ------------------------------------------------- momentum and norm
 
 __device__ __forceinline__ void load4(const void* p, int dtype, int64_t i, float (&v)[4]) {
@@ -75,6 +84,25 @@ struct SquareSum {
   }
 };
 
+// Four elements of u from the gradient (and the momentum, updated in place).
+__device__ __forceinline__ void momentum4(const MuonArgs& a, float4& m, float (&g)[4]) {
+  m.x = m.x * a.beta + g[0] * a.one_minus_beta;
+  m.y = m.y * a.beta + g[1] * a.one_minus_beta;
+  m.z = m.z * a.beta + g[2] * a.one_minus_beta;
+  m.w = m.w * a.beta + g[3] * a.one_minus_beta;
+  if (a.nesterov) {
+    g[0] = m.x * a.beta + g[0] * a.one_minus_beta;
+    g[1] = m.y * a.beta + g[1] * a.one_minus_beta;
+    g[2] = m.z * a.beta + g[2] * a.one_minus_beta;
+    g[3] = m.w * a.beta + g[3] * a.one_minus_beta;
+  } else {
+    g[0] = m.x, g[1] = m.y, g[2] = m.z, g[3] = m.w;
+  }
+}
+
+// One pass over gradient and momentum: bound by HBM (10 or 12 bytes read and
+// written per element). Four vectors of four elements are in flight per
+// thread.
 __global__ void __launch_bounds__(256) muon_momentum_kernel(const __grid_constant__ MuonArgs a) {
   __shared__ double sh[8];
   const MuonMat& t = a.mat[blockIdx.y];
@@ -83,30 +111,39 @@ __global__ void __launch_bounds__(256) muon_momentum_kernel(const __grid_constan
   const uint32_t first = blockIdx.x * 256u + threadIdx.x;
   SquareSum q;
   if (a.vec) {
+    constexpr int kAhead = 4;
     const uint32_t per_row = a.cols / 4, total = per_row * static_cast<uint32_t>(a.rows);
-    for (uint32_t i = first; i < total; i += step) {
-      const uint32_t row = i / per_row, col = (i - row * per_row) * 4;
-      float g[4];
-      load4(t.grad, a.grad_dtype, row * t.ld_grad + col, g);
-      if (t.momentum) {
-        float4* mp = reinterpret_cast<float4*>(t.momentum + row * t.ld_momentum + col);
-        float4 m = *mp;
-        m.x = m.x * a.beta + g[0] * a.one_minus_beta;
-        m.y = m.y * a.beta + g[1] * a.one_minus_beta;
-        m.z = m.z * a.beta + g[2] * a.one_minus_beta;
-        m.w = m.w * a.beta + g[3] * a.one_minus_beta;
-        *mp = m;
-        if (a.nesterov) {
-          g[0] = m.x * a.beta + g[0] * a.one_minus_beta;
-          g[1] = m.y * a.beta + g[1] * a.one_minus_beta;
-          g[2] = m.z * a.beta + g[2] * a.one_minus_beta;
-          g[3] = m.w * a.beta + g[3] * a.one_minus_beta;
-        } else {
-          g[0] = m.x, g[1] = m.y, g[2] = m.z, g[3] = m.w;
+    for (uint32_t i0 = first; i0 < total; i0 += kAhead * step) {
+      float g[kAhead][4];
+      float4 m[kAhead];
+      int64_t at[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const uint32_t i = i0 + j * step;
+        if (i < total) {
+          uint32_t row = 0, col = i;  // a matrix without gaps is one long row
+          if (!a.flat) {
+            row = i / per_row;
+            col = i - row * per_row;
+          }
+          load4(t.grad, a.grad_dtype, row * t.ld_grad + 4 * static_cast<int64_t>(col), g[j]);
+          if (t.momentum) {
+            at[j] = row * t.ld_momentum + 4 * static_cast<int64_t>(col);
+            m[j] = *reinterpret_cast<const float4*>(t.momentum + at[j]);
+          }
         }
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) q.add(g[j]);
+      for (int j = 0; j < kAhead; ++j) {
+        if (i0 + j * step < total) {
+          if (t.momentum) {
+            momentum4(a, m[j], g[j]);
+            *reinterpret_cast<float4*>(t.momentum + at[j]) = m[j];
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) q.add(g[j][e]);
+        }
+      }
     }
   } else {
     const uint64_t total = static_cast<uint64_t>(a.rows) * a.cols;
@@ -138,6 +175,9 @@ __global__ void __launch_bounds__(256) muon_momentum_kernel(const __grid_constan
 
 constexpr int kTile = 64;
 
+// A 64 x 64 tile of u through shared memory, which also transposes it where X
+// is the transpose; whole 16-byte stores (a row of X has room to a multiple of
+// 64 elements, and the tile holds zeros past the matrix). Bound by HBM.
 __global__ void __launch_bounds__(256) muon_prepare_kernel(const __grid_constant__ MuonArgs a) {
   __shared__ float tile[kTile][kTile + 1];
   __shared__ double sh[8];
@@ -145,21 +185,43 @@ __global__ void __launch_bounds__(256) muon_prepare_kernel(const __grid_constant
   const int tiles_c = (a.cols + kTile - 1) / kTile;
   const int r0 = (blockIdx.x / tiles_c) * kTile, c0 = (blockIdx.x % tiles_c) * kTile;
   // u of this tile, unscaled
-  const int tc = threadIdx.x & (kTile - 1), tr = threadIdx.x / kTile;
-  for (int r = tr; r < kTile; r += 256 / kTile) {
-    float u = 0.f;
-    if (r0 + r < a.rows && c0 + tc < a.cols) {
-      const int64_t row = r0 + r, col = c0 + tc;
-      if (t.momentum) {
-        u = t.momentum[row * t.ld_momentum + col];
-        if (a.nesterov) u = u * a.beta + load1(t.grad, a.grad_dtype, row * t.ld_grad + col) * a.one_minus_beta;
-      } else {
-        u = load1(t.grad, a.grad_dtype, row * t.ld_grad + col);
+  if (a.vec) {
+    const int col = c0 + 4 * (threadIdx.x & 15);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = (threadIdx.x >> 4) + 16 * j;
+      const int64_t row = r0 + r;
+      float u[4] = {0.f, 0.f, 0.f, 0.f};
+      if (row < a.rows && col < a.cols) {
+        if (!t.momentum || a.nesterov) load4(t.grad, a.grad_dtype, row * t.ld_grad + col, u);
+        if (t.momentum) {
+          const float4 m = *reinterpret_cast<const float4*>(t.momentum + row * t.ld_momentum + col);
+          const float mv[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) u[e] = a.nesterov ? mv[e] * a.beta + u[e] * a.one_minus_beta : mv[e];
+        }
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tile[r][4 * (threadIdx.x & 15) + e] = u[e];
     }
-    tile[r][tc] = u;
+  } else {
+    const int tc = threadIdx.x & (kTile - 1), tr = threadIdx.x / kTile;
+    for (int r = tr; r < kTile; r += 256 / kTile) {
+      float u = 0.f;
+      if (r0 + r < a.rows && c0 + tc < a.cols) {
+        const int64_t row = r0 + r, col = c0 + tc;
+        if (t.momentum) {
+          u = t.momentum[row * t.ld_momentum + col];
+          if (a.nesterov) u = u * a.beta + load1(t.grad, a.grad_dtype, row * t.ld_grad + col) * a.one_minus_beta;
+        } else {
+          u = load1(t.grad, a.grad_dtype, row * t.ld_grad + col);
+        }
+      }
+      tile[r][tc] = u;
+    }
   }
-  double s = threadIdx.x < a.norm_blocks ? a.norm[blockIdx.y * kMuonNormBlocks + threadIdx.x] : 0.0;
+  double s = 0.0;
+  for (int i = threadIdx.x; i < a.norm_blocks; i += 256) s += a.norm[blockIdx.y * kMuonNormBlocks + i];
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
   __syncthreads();
@@ -170,15 +232,23 @@ __global__ void __launch_bounds__(256) muon_prepare_kernel(const __grid_constant
   const float f1 = inv < 1e-30 ? 0x1p-64f : 1.f;
   const float f2 = static_cast<float>(inv < 1e-30 ? inv * 0x1p64 : inv);
   const int64_t base = static_cast<int64_t>(blockIdx.y) * a.m * a.ldx;
-  for (int r = tr; r < kTile; r += 256 / kTile) {
-    const float x = (a.transposed ? tile[tc][r] : tile[r][tc]) * f1 * f2;
-    const int i = (a.transposed ? c0 : r0) + r, j = (a.transposed ? r0 : c0) + tc;
-    if (i < a.m && j < a.n) {
-      const __half h = __float2half_rn(x);
-      const __half l = __float2half_rn(x - __half2float(h));
+#pragma unroll
+  for (int it = 0; it < 2; ++it) {
+    const int idx = threadIdx.x + 256 * it, r = idx >> 3, c = (idx & 7) * 8;
+    const int i = (a.transposed ? c0 : r0) + r, j = (a.transposed ? r0 : c0) + c;
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float x0 = (a.transposed ? tile[c + 2 * q][r] : tile[r][c + 2 * q]) * f1 * f2;
+      const float x1 = (a.transposed ? tile[c + 2 * q + 1][r] : tile[r][c + 2 * q + 1]) * f1 * f2;
+      h[q] = pack_half2(x0, x1);
+      const float2 f = unpack_half2(h[q]);
+      l[q] = pack_half2(x0 - f.x, x1 - f.y);
+    }
+    if (i < a.m && j < a.ldx) {
       const int64_t o = base + static_cast<int64_t>(i) * a.ldx + j;
-      a.hi[0][o] = __half_as_ushort(h);
-      a.lo[o] = __half_as_ushort(l);
+      *reinterpret_cast<uint4*>(a.hi[0] + o) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(a.lo + o) = make_uint4(l[0], l[1], l[2], l[3]);
     }
   }
 }
@@ -186,15 +256,19 @@ __global__ void __launch_bounds__(256) muon_prepare_kernel(const __grid_constant
 // ------------------------------------------------------- the products
 
 constexpr int kTM = 256, kTN = 256;
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr uint32_t kABytes = 128 * kBK * 2;    // 16 KB: a CTA's 128 rows of A
 constexpr uint32_t kBBytes = 128 * kBK * 2;    // 16 KB: its 128 columns of B
 constexpr uint32_t kStageBytes = kABytes + kBBytes;
-constexpr uint32_t kSmemBytes = 1024 + kStages * kStageBytes + (2 * kStages + 5) * 8 + 16;
+// per epilogue warp two buffers of 32 rows x 64 fp16 columns, twice (X hi and
+// lo; a tile and its mirror image; one fp32 tile)
+constexpr uint32_t kEpiPart = 32 * 128;
+constexpr uint32_t kEpiBytes = 4 * 2 * 2 * kEpiPart;
+constexpr uint32_t kSmemBytes = 1024 + kStages * kStageBytes + kEpiBytes + (2 * kStages + 5 + 8) * 8 + 16;
+static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 constexpr uint32_t kTmemCols = 512;
 constexpr int kThreads = 192;
 constexpr int kEpiThreads = 128;
-constexpr uint32_t kEpiBar = 1;
 
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* m, uint32_t bar, int32_t c0,
                                                  int32_t c1, int32_t c2) {
@@ -205,18 +279,18 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int32_t c0, int32_t c1,
+                                            int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
 // fp16 operands: the type fields (bits 7-9 and 10-12) are 0
 __host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, uint32_t a_mn, uint32_t b_mn) {
   return (1u << 4) | (a_mn << 15) | (b_mn << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-__device__ __forceinline__ float2 unpack_half2(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
@@ -255,23 +329,8 @@ __device__ __forceinline__ MuonUnit muon_unit(int u, int tiles_m, int tiles_n) {
   return r;
 }
 
-// A row of 32 fp16 values as 16 words (16-byte aligned)
-__device__ __forceinline__ void load_half32(const uint16_t* p, uint32_t (&w)[16]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p + 8 * j);
-    w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
-  }
-}
-__device__ __forceinline__ void store_half32(uint16_t* p, const uint32_t (&w)[16]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    *reinterpret_cast<uint4*>(p + 8 * j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-}
-
 // One element of the result: the weight's update in place, or the update.
-__device__ __forceinline__ void write_result(const MuonArgs& a, const MuonMat& t, int i, int j, float o) {
-  const int64_t row = a.transposed ? j : i, col = a.transposed ? i : j;
+__device__ __forceinline__ void write_result(const MuonArgs& a, const MuonMat& t, int64_t row, int64_t col, float o) {
   if (t.weight) {
     const int64_t at = row * t.ld_weight + col;
     if (a.weight_dtype == 1) {
@@ -290,93 +349,206 @@ __device__ __forceinline__ void write_result(const MuonArgs& a, const MuonMat& t
   }
 }
 
-// The epilogue of 128 rows x 256 columns of an accumulator, one row per
-// thread; `release` hands the accumulator back after its last read.
-template <int PHASE, class Release>
-__device__ __forceinline__ void muon_epilogue(const MuonArgs& a, const MuonStep& st, int mat, int m0, int n0,
-                                              bool mirror, int row, uint32_t tbase, Release&& release) {
-  const int i = m0 + row;
-  const bool rvalid = i < a.m;
-  constexpr bool kSym = PHASE == kMuonGram || PHASE == kMuonPoly;
-  const int ncols = kSym ? a.m : a.n;
-  float factor = 0.f;
-  if (!kSym && rvalid) factor = st.a + a.diag[static_cast<int64_t>(mat) * a.m + i];
-#pragma unroll 1
-  for (int g = 0; g < kTN / 32; ++g) {
-    __syncwarp();  // rows past the last leave the loop body early; the TMEM read is the whole warp's
-    uint32_t r[32];
-    tmem_ld_32x32b_x32(tbase + g * 32, r);
-    tmem_ld_wait();
-    tmem_regs_ready(r);
-    const int c0 = n0 + g * 32;
-    if (g == kTN / 32 - 1) release();
-    if (!rvalid || c0 >= ncols) continue;
+// Two neighbours of a row at once, where the tensor's rows are aligned to pairs.
+__device__ __forceinline__ void write_result2(const MuonArgs& a, const MuonMat& t, int64_t row, int64_t col, float2 o) {
+  if (t.weight) {
+    const int64_t at = row * t.ld_weight + col;
+    if (a.weight_dtype == 1) {
+      float2* w = reinterpret_cast<float2*>(static_cast<float*>(t.weight) + at);
+      const float2 v = *w;
+      *w = make_float2(v.x * a.decay - a.lr * o.x, v.y * a.decay - a.lr * o.y);
+    } else {
+      __nv_bfloat162* w = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(t.weight) + at);
+      const float2 v = __bfloat1622float2(*w);
+      *w = __floats2bfloat162_rn(v.x * a.decay - a.lr * o.x, v.y * a.decay - a.lr * o.y);
+    }
+  } else {
+    const int64_t at = row * t.ld_update + col;
+    if (a.update_dtype == 1)
+      *reinterpret_cast<float2*>(static_cast<float*>(t.update) + at) = o;
+    else
+      *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(t.update) + at) = __floats2bfloat162_rn(o.x, o.y);
+  }
+}
+
+// The epilogue of one warp: its 32 rows (TMEM lanes) of a tile's 256 columns,
+// in groups of 64. What a group reads (X hi and lo, or A) comes by TMA into the
+// warp's own buffers, one group ahead and for a tile's first group before its
+// products are done; what it writes leaves the same buffers by TMA stores. So
+// global memory sees whole 128-byte rows, and no warp waits for another.
+// Written for the epilogue's bound: with each thread reading and writing its
+// own row in global memory, every access touched 32 lines, and B X of
+// 8 x 1024 x 1024 took 36.8 us where its products need 8.7.
+template <int PHASE>
+struct MuonEpilogue {
+  static constexpr bool kSym = PHASE == kMuonGram || PHASE == kMuonPoly;
+  static constexpr bool kLoads = PHASE != kMuonGram;
+  static constexpr bool kLoads2 = PHASE == kMuonApply || PHASE == kMuonLast;
+  static constexpr bool kStores = PHASE != kMuonLast;
+  const MuonArgs& a;
+  const MuonMaps& maps;
+  const MuonStep& st;
+  uint8_t* buf;        // this warp's 2 x 2 x kEpiPart
+  uint32_t bar;        // this warp's two load barriers
+  int lane;
+  uint32_t loads = 0, uses = 0;
+
+  // TMA loads of the group at column c0 into the next buffer
+  __device__ __forceinline__ void load(int mat, int row0, int c0) {
+    if (!kLoads) return;
+    if (lane == 0) {
+      if (kStores) bulk_wait_group_read<0>();  // the buffer's last stores have read it
+      const uint32_t b = loads & 1u;
+      const uint32_t dst = smem_u32(buf + b * 2 * kEpiPart), bb = bar + 8u * b;
+      mbar_arrive_expect_tx(bb, kLoads2 ? 2 * kEpiPart : kEpiPart);
+      tma_load_3d(dst, &maps.e0, bb, c0, row0, mat);
+      if (kLoads2) tma_load_3d(dst + kEpiPart, &maps.e1, bb, c0, row0, mat);
+    }
+    ++loads;
+  }
+
+  // columns c0 .. c0 + 63 of the warp's rows, accumulator values in v
+  __device__ __forceinline__ bool group(int mat, int row0, int c0, bool mirror, float factor, const uint32_t (&r0)[32],
+                                        const uint32_t (&r1)[32]) {
+    const uint32_t b = uses & 1u;
+    uint8_t* p0 = buf + b * 2 * kEpiPart;
+    uint8_t* p1 = p0 + kEpiPart;
+    if (kLoads) {
+      if (!__all_sync(kAll, mbar_wait_bounded(bar + 8u * b, (uses >> 1) & 1u, a.ctrl + kCtrlError, a.timeout_ns)))
+        return false;
+    } else {
+      if (lane == 0) bulk_wait_group_read<1>();
+      __syncwarp();
+    }
+    ++uses;
+    uint4* q0 = reinterpret_cast<uint4*>(p0 + lane * 128);
+    uint4* q1 = reinterpret_cast<uint4*>(p1 + lane * 128);
+    const int sw = lane & 7;   // 16-byte chunk j of a row sits at chunk j ^ (row % 8)
+    auto acc = [&](int i) { return __uint_as_float(i < 32 ? r0[i & 31] : r1[i & 31]); };
     if constexpr (kSym) {
-      const int64_t base = static_cast<int64_t>(mat) * a.m * a.lda;
-      uint16_t* out = (PHASE == kMuonGram ? a.gram : a.poly) + base;
-      float v[32];
-      if constexpr (PHASE == kMuonGram) {
+      const int i = row0 + lane;
+      uint16_t* mir = reinterpret_cast<uint16_t*>(p1) + lane;   // [64][32], its columns are this tile's rows
 #pragma unroll
-        for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(r[q]) * kGramScale;
-      } else {
-        uint32_t w[16];
-        load_half32(a.gram + base + static_cast<int64_t>(i) * a.lda + c0, w);
+      for (int j = 0; j < 8; ++j) {
+        float v[8];
+        if constexpr (PHASE == kMuonGram) {
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const float2 f = unpack_half2(w[q]);
-          v[2 * q] = st.b * kPolyB * f.x + st.c * kPolyC * __uint_as_float(r[2 * q]);
-          v[2 * q + 1] = st.b * kPolyB * f.y + st.c * kPolyC * __uint_as_float(r[2 * q + 1]);
-        }
-        if (i >= c0 && i < c0 + 32) {  // the diagonal stays in fp32, apart
+          for (int e = 0; e < 8; ++e) v[e] = acc(8 * j + e) * kGramScale;
+        } else {
+          const uint4 w = q0[j ^ sw];
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int q = 0; q < 32; ++q) {
-            if (c0 + q == i) {
-              a.diag[static_cast<int64_t>(mat) * a.m + i] = v[q] * kPolyInv;
-              v[q] = 0.f;
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack_half2(ww[e]);
+            v[2 * e] = st.b * kPolyB * f.x + st.c * kPolyC * acc(8 * j + 2 * e);
+            v[2 * e + 1] = st.b * kPolyB * f.y + st.c * kPolyC * acc(8 * j + 2 * e + 1);
+          }
+          const int d = i - (c0 + 8 * j);   // the diagonal stays in fp32, apart
+          if (d >= 0 && d < 8 && i < a.m) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              if (e == d) {
+                a.diag[static_cast<int64_t>(mat) * a.m + i] = v[e] * kPolyInv;
+                v[e] = 0.f;
+              }
             }
           }
         }
-      }
-      uint32_t w[16];
+        uint32_t w[4];
 #pragma unroll
-      for (int q = 0; q < 16; ++q) w[q] = pack_half2(v[2 * q], v[2 * q + 1]);
-      store_half32(out + static_cast<int64_t>(i) * a.lda + c0, w);
-      if (mirror) {
+        for (int e = 0; e < 4; ++e) w[e] = pack_half2(v[2 * e], v[2 * e + 1]);
+        q0[j ^ sw] = make_uint4(w[0], w[1], w[2], w[3]);
+        if (mirror) {
 #pragma unroll
-        for (int q = 0; q < 32; ++q)
-          if (c0 + q < a.m)
-            out[static_cast<int64_t>(c0 + q) * a.lda + i] = static_cast<uint16_t>(w[q / 2] >> (16 * (q & 1)));
+          for (int e = 0; e < 8; ++e) mir[(8 * j + e) * 32] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
+        }
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(&maps.o0, smem_u32(p0), c0, row0, mat);
+        if (mirror) tma_store_3d(&maps.o1, smem_u32(p1), row0, c0, mat);
+        bulk_commit_group();
+      }
+      __syncwarp();
     } else {
-      const int64_t at = (static_cast<int64_t>(mat) * a.m + i) * a.ldx + c0;
-      uint32_t h[16], l[16];
-      load_half32(a.hi[st.src] + at, h);
-      load_half32(a.lo + at, l);
-      float x[32];
 #pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const float2 fh = unpack_half2(h[q]), fl = unpack_half2(l[q]);
-        x[2 * q] = factor * (fh.x + fl.x) + __uint_as_float(r[2 * q]) * kPolyInv;
-        x[2 * q + 1] = factor * (fh.y + fl.y) + __uint_as_float(r[2 * q + 1]) * kPolyInv;
+      for (int j = 0; j < 8; ++j) {
+        const uint4 wh = q0[j ^ sw], wl = q1[j ^ sw];
+        uint32_t h[4] = {wh.x, wh.y, wh.z, wh.w}, l[4] = {wl.x, wl.y, wl.z, wl.w};
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 fh = unpack_half2(h[e]), fl = unpack_half2(l[e]);
+          x[2 * e] = factor * (fh.x + fl.x) + acc(8 * j + 2 * e) * kPolyInv;
+          x[2 * e + 1] = factor * (fh.y + fl.y) + acc(8 * j + 2 * e + 1) * kPolyInv;
+        }
+        if constexpr (PHASE == kMuonApply) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            h[e] = pack_half2(x[2 * e], x[2 * e + 1]);
+            const float2 f = unpack_half2(h[e]);
+            l[e] = pack_half2(x[2 * e] - f.x, x[2 * e + 1] - f.y);
+          }
+          q0[j ^ sw] = make_uint4(h[0], h[1], h[2], h[3]);
+          q1[j ^ sw] = make_uint4(l[0], l[1], l[2], l[3]);
+        } else if (a.transposed) {
+          // out[c0 + ..][row0 + lane]: the lanes' columns are neighbours
+          const int64_t i = row0 + lane;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (i < a.m && c0 + 8 * j + e < a.n)
+              write_result(a, a.mat[mat], c0 + 8 * j + e, i, x[e] * (a.scale * kXInv));
+        } else {
+          // as fp32 in place: columns 0..31 where hi was, 32..63 where lo was.
+          // Row `lane` is this lane's alone until the barrier below; its chunks
+          // 2 j, 2 j + 1 of the first half held hi and lo of columns 16 j .. :
+          // kept in registers until every chunk of the row has been read
+#pragma unroll
+          for (int e = 0; e < 8; ++e) out_[8 * j + e] = x[e] * (a.scale * kXInv);
+        }
       }
       if constexpr (PHASE == kMuonApply) {
-#pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          h[q] = pack_half2(x[2 * q], x[2 * q + 1]);
-          const float2 f = unpack_half2(h[q]);
-          l[q] = pack_half2(x[2 * q] - f.x, x[2 * q + 1] - f.y);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&maps.o0, smem_u32(p0), c0, row0, mat);
+          tma_store_3d(&maps.e1, smem_u32(p1), c0, row0, mat);
+          bulk_commit_group();
         }
-        store_half32(a.hi[1 - st.src] + at, h);
-        store_half32(a.lo + at, l);
-      } else {
-        const float sc = a.scale * kXInv;
+        __syncwarp();
+      } else if (!a.transposed) {
+        float4* f0 = reinterpret_cast<float4*>(q0);
+        float4* f1 = reinterpret_cast<float4*>(q1);
 #pragma unroll
-        for (int q = 0; q < 32; ++q)
-          if (c0 + q < a.n) write_result(a, a.mat[mat], i, c0 + q, x[q] * sc);
+        for (int j = 0; j < 8; ++j) {
+          f0[j ^ sw] = make_float4(out_[4 * j], out_[4 * j + 1], out_[4 * j + 2], out_[4 * j + 3]);
+          f1[j ^ sw] = make_float4(out_[32 + 4 * j], out_[33 + 4 * j], out_[34 + 4 * j], out_[35 + 4 * j]);
+        }
+        __syncwarp();
+        // a row at a time, two neighbouring columns per lane
+        const uint8_t* part = lane < 16 ? p0 : p1;
+        const int c = 2 * lane, chunk = (c & 31) >> 2;
+        const int64_t col = c0 + c;
+        const int rows = min(32, a.m - row0);
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r) {
+          const float2 o = *reinterpret_cast<const float2*>(part + r * 128 + ((chunk ^ (r & 7)) << 4) + (c & 3) * 4);
+          if (a.pairs && col + 1 < a.n) {
+            write_result2(a, a.mat[mat], row0 + r, col, o);
+          } else {
+            if (col < a.n) write_result(a, a.mat[mat], row0 + r, col, o.x);
+            if (col + 1 < a.n) write_result(a, a.mat[mat], row0 + r, col + 1, o.y);
+          }
+        }
+        fence_proxy_async_smem();  // the next load overwrites what was written here
+        __syncwarp();
       }
     }
+    return true;
   }
-}
+  float out_[PHASE == kMuonLast ? 64 : 1];
+};
 
 // A persistent kernel of CTA pairs on 256 x 256 tiles (tcgen05 cta_group::2,
 // each CTA holding its 128 rows of A and 128 columns of B per 64-deep
@@ -385,8 +557,8 @@ __device__ __forceinline__ void muon_epilogue(const MuonArgs& a, const MuonStep&
 // warps 2..5 run the epilogue. Every wait is bounded.
 template <int PHASE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    muon_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                     const __grid_constant__ MuonArgs a, const MuonStep st) {
+    muon_gemm_kernel(const __grid_constant__ MuonMaps maps, const __grid_constant__ MuonArgs a,
+                     const __grid_constant__ MuonStep st) {
   constexpr bool kSym = PHASE == kMuonGram || PHASE == kMuonPoly;
   constexpr int BMN = kSym ? 0 : 1;   // X as the right operand is contiguous along its columns
   extern __shared__ uint8_t smem_raw[];
@@ -394,8 +566,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + kStages * kABytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sB + kStages * kBBytes);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5);
+  uint8_t* sE = sB + kStages * kBBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sE + kEpiBytes);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5 + 8);
   const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };
@@ -418,10 +591,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(tempty_bar(acc), 2 * kEpiThreads);
     }
     mbar_init(drain_bar, 1);
+    for (int i = 0; i < 8; ++i) mbar_init(drain_bar + 8u * (1 + i), 1);  // the epilogue warps' loads
     fence_mbar_init();
     fence_proxy_async_smem();
-    tma_prefetch_map(&tmA);
-    tma_prefetch_map(&tmB);
+    tma_prefetch_map(&maps.a);
+    tma_prefetch_map(&maps.b);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
@@ -457,12 +631,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t sa = smem_u32(sA + stage * kABytes);
           const uint32_t sb = smem_u32(sB + stage * kBBytes);
           const int k0 = kb * kBK;
-          tma_load_3d_pair(sa, &tmA, fb, k0, mA, t.mat);
+          tma_load_3d_pair(sa, &maps.a, fb, k0, mA, t.mat);
           if (BMN == 0) {
-            tma_load_3d_pair(sb, &tmB, fb, k0, nB, t.mat);
+            tma_load_3d_pair(sb, &maps.b, fb, k0, nB, t.mat);
           } else {
-            tma_load_3d_pair(sb, &tmB, fb, nB, k0, t.mat);
-            tma_load_3d_pair(sb + 8192, &tmB, fb, nB + 64, k0, t.mat);
+            tma_load_3d_pair(sb, &maps.b, fb, nB, k0, t.mat);
+            tma_load_3d_pair(sb + 8192, &maps.b, fb, nB + 64, k0, t.mat);
           }
           ++n_issued;
         }
@@ -519,25 +693,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     const int wq = warp & 3;
-    const int row = wq * 32 + lane;
+    MuonEpilogue<PHASE> epi{a, maps, st, sE + wq * 4 * kEpiPart, drain_bar + 8u * (1 + 2 * wq), lane};
+    const int ncols = kSym ? a.m : a.n;
+    bool ok = true;
     int it = 0;
     for (int u = pair; u < num_units; u += npairs, ++it) {
       const int acc = it & 1;
       const uint32_t acc_phase = (it >> 1) & 1;
-      const bool ok = mbar_wait_bounded_cluster(tfull_bar(acc), acc_phase, err, a.timeout_ns);
-      if (named_bar_or(kEpiBar, kEpiThreads, !ok)) break;
-      tc_fence_after();
       const MuonUnit t = muon_unit<PHASE>(u, tiles_m, tiles_n);
+      const int row0 = t.tm * kTM + static_cast<int>(rank) * 128 + wq * 32, n0 = t.tn * kTN;
+      // this warp's groups of 64 columns that hold any of the output
+      const int groups = row0 < a.m ? min(kTN / 64, (ncols - n0 + 63) / 64) : 0;
+      float factor = 0.f;
+      if (groups > 0) {
+        epi.load(t.mat, row0, n0);
+        if (!kSym && row0 + lane < a.m) factor = st.a + a.diag[static_cast<int64_t>(t.mat) * a.m + row0 + lane];
+      }
+      ok = mbar_wait_bounded_cluster(tfull_bar(acc), acc_phase, err, a.timeout_ns);
+      ok = __all_sync(kAll, ok);
+      if (!ok) break;
+      tc_fence_after();
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(wq * 32) << 16) + acc * kTN;
-      muon_epilogue<PHASE>(a, st, t.mat, t.tm * kTM + static_cast<int>(rank) * 128, t.tn * kTN,
-                           kSym && t.tm != t.tn, row, tbase, [&] {
-                             tc_fence_before();
-                             if (rank == 0)
-                               mbar_arrive(tempty_bar(acc));
-                             else
-                               mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
-                           });
+      auto release = [&] {
+        tc_fence_before();
+        if (rank == 0)
+          mbar_arrive(tempty_bar(acc));
+        else
+          mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+      };
+      if (groups == 0) release();
+#pragma unroll 1
+      for (int g = 0; g < groups && ok; ++g) {
+        __syncwarp();
+        uint32_t r0[32], r1[32];
+        tmem_ld_32x32b_x32(tbase + g * 64, r0);
+        tmem_ld_32x32b_x32(tbase + g * 64 + 32, r1);
+        if (g + 1 < groups) epi.load(t.mat, row0, n0 + (g + 1) * 64);
+        tmem_ld_wait();
+        tmem_regs_ready(r0);
+        tmem_regs_ready(r1);
+        if (g == groups - 1) release();
+        ok = epi.group(t.mat, row0, n0 + g * 64, kSym && t.tm != t.tn, factor, r0, r1);
+      }
+      if (!ok) break;
     }
+    if (lane == 0) bulk_wait_group<0>();
+    // a load that is still in flight lands before the CTA leaves
+    if (!ok && MuonEpilogue<PHASE>::kLoads && lane == 0)
+      for (; epi.uses < epi.loads; ++epi.uses)
+        drain_wait(epi.bar + 8u * (epi.uses & 1u), (epi.uses >> 1) & 1u, a.timeout_ns);
   }
 
   __syncwarp();
@@ -554,8 +758,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 template <int PHASE>
-cudaError_t launch_phase(const CUtensorMap& ta, const CUtensorMap& tb, const MuonArgs& a, const MuonStep& st,
-                         int pairs, cudaStream_t s) {
+cudaError_t launch_phase(const MuonMaps& maps, const MuonArgs& a, const MuonStep& st, int pairs, cudaStream_t s) {
   auto kern = muon_gemm_kernel<PHASE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(kSmemBytes));
@@ -564,7 +767,7 @@ cudaError_t launch_phase(const CUtensorMap& ta, const CUtensorMap& tb, const Muo
   const bool sym = PHASE == kMuonGram || PHASE == kMuonPoly;
   const int64_t units = static_cast<int64_t>(a.count) * (sym ? tiles_m * (tiles_m + 1) / 2 : tiles_m * tiles_n);
   if (units < pairs) pairs = static_cast<int>(units);
-  kern<<<2 * pairs, kThreads, kSmemBytes, s>>>(ta, tb, a, st);
+  kern<<<2 * pairs, kThreads, kSmemBytes, s>>>(maps, a, st);
   return cudaGetLastError();
 }
 
@@ -581,13 +784,13 @@ cudaError_t launch_muon_prepare(const MuonArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_muon_gemm(int phase, const CUtensorMap& ta, const CUtensorMap& tb, const MuonArgs& a,
-                             const MuonStep& st, int pairs, cudaStream_t s) {
+cudaError_t launch_muon_gemm(int phase, const MuonMaps& maps, const MuonArgs& a, const MuonStep& st, int pairs,
+                             cudaStream_t s) {
   switch (phase) {
-    case kMuonGram: return launch_phase<kMuonGram>(ta, tb, a, st, pairs, s);
-    case kMuonPoly: return launch_phase<kMuonPoly>(ta, tb, a, st, pairs, s);
-    case kMuonApply: return launch_phase<kMuonApply>(ta, tb, a, st, pairs, s);
-    case kMuonLast: return launch_phase<kMuonLast>(ta, tb, a, st, pairs, s);
+    case kMuonGram: return launch_phase<kMuonGram>(maps, a, st, pairs, s);
+    case kMuonPoly: return launch_phase<kMuonPoly>(maps, a, st, pairs, s);
+    case kMuonApply: return launch_phase<kMuonApply>(maps, a, st, pairs, s);
+    case kMuonLast: return launch_phase<kMuonLast>(maps, a, st, pairs, s);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -23,6 +23,7 @@
 #include <type_traits>
 
 #include "flce_train.h"
+#include "ptx.cuh"
 
 namespace flce {
 namespace {
@@ -138,7 +139,16 @@ __device__ __forceinline__ int first_document(const int64_t* offsets, int docume
   return lo;
 }
 
-template <class T, int G, int NPL>
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// ONE: the grid is one cluster and there is one document without offsets: the
+// blocks' sums meet in the first block over distributed shared memory, which
+// closes the call. Otherwise the sums go to the workspace for the second launch.
+template <class T, int G, int NPL, bool ONE>
 __global__ void __launch_bounds__(kRouteThreads) route_forward_kernel(const RouteArgs a) {
   constexpr int RPW = 32 / G;          // rows a warp holds at once
   constexpr int kCols = G * NPL;
@@ -150,6 +160,10 @@ __global__ void __launch_bounds__(kRouteThreads) route_forward_kernel(const Rout
   __shared__ float sh_scale[kWarps * RPW];
   __shared__ float sh_z[kWarps];
   __shared__ int32_t sh_live[kWarps];
+  __shared__ float sh_sum[ONE ? kCols : 1];    // ONE: this block's sums, read by the first block
+  __shared__ float sh_block_z;
+  __shared__ int32_t sh_block_live;
+  __shared__ double sh_term[kWarps];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gl = lane % G, gr = lane / G;
@@ -162,7 +176,17 @@ __global__ void __launch_bounds__(kRouteThreads) route_forward_kernel(const Rout
   int32_t* my_i = stage_i + warp * RPW * k;
   float* my_scale = sh_scale + warp * RPW;
 
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+  if (!ONE && blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+  if (ONE && static_cast<int64_t>(blockIdx.x) * a.rows_per_block >= a.N) {  // a block without rows
+    for (int e = threadIdx.x; e < kCols; e += kRouteThreads) {
+      cnt[e] = 0;
+      sh_sum[e] = 0.f;
+    }
+    if (threadIdx.x == 0) {
+      sh_block_z = 0.f;
+      sh_block_live = 0;
+    }
+  }
 
   const int64_t r0 = blockIdx.x * a.rows_per_block;
   const int64_t r1 = min(a.N, r0 + a.rows_per_block);
@@ -285,8 +309,12 @@ __global__ void __launch_bounds__(kRouteThreads) route_forward_kernel(const Rout
       for (int e = threadIdx.x; e < a.E; e += kRouteThreads) {
         float s = 0.f;
         for (int w = 0; w < kWarps * RPW; ++w) s += red[w * kCols + e];
-        a.unit_p[unit * a.E + e] = s;
-        a.unit_c[unit * a.E + e] = cnt[e];
+        if (ONE) {
+          sh_sum[e] = s;
+        } else {
+          a.unit_p[unit * a.E + e] = s;
+          a.unit_c[unit * a.E + e] = cnt[e];
+        }
       }
       if (threadIdx.x == 0) {
         float s = 0.f;
@@ -295,12 +323,57 @@ __global__ void __launch_bounds__(kRouteThreads) route_forward_kernel(const Rout
           s += sh_z[w];
           n += sh_live[w];
         }
-        a.unit_z[unit] = s;
-        a.unit_live[unit] = n;
+        if (ONE) {
+          sh_block_z = s;
+          sh_block_live = n;
+        } else {
+          a.unit_z[unit] = s;
+          a.unit_live[unit] = n;
+        }
       }
     }
     __syncthreads();
     r = end;
+  }
+  if constexpr (ONE) {
+    cluster_sync();
+    if (blockIdx.x == 0) {
+      float zs = 0.f;
+      int n = 0;
+      for (uint32_t b = 0; b < gridDim.x; ++b) {
+        zs += __uint_as_float(ld_cluster_u32(mapa_shared(smem_u32(&sh_block_z), b)));
+        n += static_cast<int>(ld_cluster_u32(mapa_shared(smem_u32(&sh_block_live), b)));
+      }
+      const float slope_n = n > 0 ? static_cast<float>(a.E) / (static_cast<float>(a.k) * static_cast<float>(n)) : 0.f;
+      double term = 0.0;
+      for (int e = threadIdx.x; e < a.E; e += kRouteThreads) {
+        float p = 0.f;
+        int c = 0;
+        for (uint32_t b = 0; b < gridDim.x; ++b) {
+          p += __uint_as_float(ld_cluster_u32(mapa_shared(smem_u32(sh_sum + e), b)));
+          c += static_cast<int>(ld_cluster_u32(mapa_shared(smem_u32(cnt + e), b)));
+        }
+        a.counts[e] = c;
+        const float slope = slope_n * static_cast<float>(c);
+        a.slope[e] = slope;
+        term += static_cast<double>(slope * p);
+      }
+      for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(kAll, term, o);
+      if (lane == 0) sh_term[warp] = term;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        term = 0.0;
+        for (int w = 0; w < kWarps; ++w) term += sh_term[w];
+        const double inv = n > 0 ? 1.0 / n : 0.0;
+        a.result[0] = static_cast<float>(term * inv);
+        a.result[1] = static_cast<float>(zs * inv);
+        a.result[2] = static_cast<float>(inv);
+        a.result[3] = __int_as_float(n);
+      }
+    }
+    cluster_sync();  // the first block reads the others' shared memory until here
+  } else {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   }
 }
 
@@ -326,8 +399,10 @@ __device__ __forceinline__ void document_blocks(const RouteArgs& a, int d, int* 
 // finish adds the terms, in order, and writes the losses.
 template <int R>
 __global__ void __launch_bounds__(32 * R) route_finish_kernel(const RouteArgs a, int chunks, int chunk_size) {
-  __shared__ double sh_d[R][33];
-  __shared__ int32_t sh_c[R][33];
+  __shared__ float sh_p[32][R + 1];
+  __shared__ int32_t sh_c[32][R + 1];
+  // launched while the forward still runs: its results from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ double sh_t[3][R];
   __shared__ bool last;
   const int d = blockIdx.x / chunks, chunk = blockIdx.x - d * chunks;
@@ -356,47 +431,52 @@ __global__ void __launch_bounds__(32 * R) route_finish_kernel(const RouteArgs a,
     n += static_cast<int>(sh_t[0][w]);
     zs += sh_t[1][w];
   }
-  const double slope_n = n > 0 ? static_cast<double>(a.E) / (static_cast<double>(a.k) * n) : 0.0;
+  const float slope_n = n > 0 ? static_cast<float>(a.E) / (static_cast<float>(a.k) * static_cast<float>(n)) : 0.f;
 
   double term = 0.0;
   const int e_end = min(a.E, (chunk + 1) * chunk_size);
   for (int e0 = chunk * chunk_size; e0 < e_end; e0 += 32) {
     const int e = e0 + tx;
-    double p = 0.0;
+    // a lane's share of the units, then a tree over the lanes: fp32 in both
+    float p = 0.f;
     int c = 0;
     if (e < e_end) {
-#pragma unroll 4
+#pragma unroll 8
       for (int b = b0 + ty; b < b1; b += R) {
         const int64_t u = (static_cast<int64_t>(b) + d) * a.E + e;
         p += a.unit_p[u];
         c += a.unit_c[u];
       }
     }
-    sh_d[ty][tx] = p;
-    sh_c[ty][tx] = c;
+    sh_p[tx][ty] = p;
+    sh_c[tx][ty] = c;
     __syncthreads();
-    if (ty == 0 && e < e_end) {
-      p = 0.0;
-      c = 0;
-      for (int w = 0; w < R; ++w) {
-        p += sh_d[w][tx];
-        c += sh_c[w][tx];
+    for (int x = ty; x < 32 && e0 + x < e_end; x += R) {  // a warp per expert, its lanes over the shares
+      p = tx < R ? sh_p[x][tx] : 0.f;
+      c = tx < R ? sh_c[x][tx] : 0;
+      for (int o = 16; o > 0; o >>= 1) {
+        p += __shfl_xor_sync(kAll, p, o);
+        c += __shfl_xor_sync(kAll, c, o);
       }
-      const int64_t o = static_cast<int64_t>(d) * a.E + e;
-      a.counts[o] = c;
-      a.slope[o] = static_cast<float>(slope_n * c);
-      term += slope_n * c * p;
+      if (tx == 0) {
+        const int64_t o = static_cast<int64_t>(d) * a.E + e0 + x;
+        const float slope = slope_n * static_cast<float>(c);
+        a.counts[o] = c;
+        a.slope[o] = slope;
+        term += static_cast<double>(slope * p);
+      }
     }
     __syncthreads();
   }
-  if (ty == 0) {
-    for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(kAll, term, o);
-    if (tx == 0) {
-      a.terms[blockIdx.x] = term;
-      if (chunk == 0) {
-        a.doc_live[d] = n;
-        a.doc_z[d] = zs;
-      }
+  if (tx == 0) sh_t[2][ty] = term;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    term = 0.0;
+    for (int w = 0; w < R; ++w) term += sh_t[2][w];
+    a.terms[blockIdx.x] = term;
+    if (chunk == 0) {
+      a.doc_live[d] = n;
+      a.doc_z[d] = zs;
     }
   }
   __threadfence();
@@ -524,14 +604,25 @@ __global__ void __launch_bounds__(kRouteThreads)
 template <class T, int G, int NPL>
 cudaError_t forward_t(const RouteArgs& a, cudaStream_t s) {
   const size_t rows = kWarps * (32 / G), cols = G * NPL;
+  // at most 8 x 32 x 32 + 1024 floats and 8 x 32 slots: below the 48 KB that need no opt-in
   const size_t smem = rows * cols * 4 + cols * 4 + rows * a.k * 8;
-  auto kern = route_forward_kernel<T, G, NPL>;
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
+  if (!a.one_launch) {
+    route_forward_kernel<T, G, NPL, false><<<a.blocks, kRouteThreads, smem, s>>>(a);
+    return cudaGetLastError();
   }
-  kern<<<a.blocks, kRouteThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.blocks);
+  cfg.blockDim = dim3(kRouteThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = a.blocks;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, route_forward_kernel<T, G, NPL, true>, a);
 }
 
 template <class T, int G, int NPL>
@@ -561,17 +652,23 @@ cudaError_t for_geometry(const RouteGeometry& g, F&& f) {
 
 }  // namespace
 
-RouteGeometry route_geometry(int64_t N, int64_t E, int64_t documents, int num_sms) {
+RouteGeometry route_geometry(int64_t N, int64_t E, int64_t documents, bool offsets, int num_sms) {
   RouteGeometry g;
   g.per_lane = E <= 256 ? 8 : (E <= 512 ? 16 : 32);
   g.lanes = 1;
   while (g.lanes < 32 && static_cast<int64_t>(g.lanes) * g.per_lane < E) g.lanes *= 2;
   const int64_t step = kWarps * (32 / g.lanes);
-  const int64_t most = 4 * static_cast<int64_t>(num_sms);
+  // Short batches run as one cluster of up to 8 blocks that closes the call
+  // itself: one launch instead of two. Past 8 rounds of rows per block the
+  // whole GPU's width is worth the second launch.
+  g.one_launch = !offsets && N > 0 && N <= 8 * 8 * step;
+  const int64_t most = g.one_launch ? 8 : 4 * static_cast<int64_t>(num_sms);
   int64_t per = (N + most - 1) / most;
   per = (per + step - 1) / step * step;
   g.rows_per_block = per > 0 ? per : step;
   g.blocks = static_cast<int>((N + g.rows_per_block - 1) / g.rows_per_block);
+  if (g.one_launch)
+    while (g.blocks & (g.blocks - 1)) ++g.blocks;  // a power of two
   g.chunks = documents >= num_sms ? 1 : static_cast<int>((E + 31) / 32);
   return g;
 }
@@ -587,11 +684,18 @@ cudaError_t launch_route_forward(int dtype, const RouteGeometry& g, const RouteA
 cudaError_t launch_route_finish(const RouteGeometry& g, const RouteArgs& a, cudaStream_t s) {
   const int chunk_size = g.chunks == 1 ? a.E : 32;
   // a document spread over many blocks has many units to add: more warps
-  if (a.blocks >= 64 * static_cast<int64_t>(a.documents))
-    route_finish_kernel<32><<<a.documents * g.chunks, 1024, 0, s>>>(a, g.chunks, chunk_size);
-  else
-    route_finish_kernel<8><<<a.documents * g.chunks, 256, 0, s>>>(a, g.chunks, chunk_size);
-  return cudaGetLastError();
+  const bool many = a.blocks >= 64 * static_cast<int64_t>(a.documents);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.documents * g.chunks);
+  cfg.blockDim = dim3(many ? 1024 : 256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;  // may start while the forward drains
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return many ? cudaLaunchKernelEx(&cfg, route_finish_kernel<32>, a, g.chunks, chunk_size)
+              : cudaLaunchKernelEx(&cfg, route_finish_kernel<8>, a, g.chunks, chunk_size);
 }
 
 cudaError_t launch_route_backward(int dtype, const RouteGeometry& g, const RouteArgs& a, const float* d_weights,

@@ -32,6 +32,7 @@ struct RouteArgs {
   float* result;            // balance, z, 1 / n, n (int32 bits)
   int64_t rows_per_block;
   int32_t blocks;
+  int32_t one_launch;
   // workspace
   float* unit_p;            // [units][E] sums of probabilities
   int32_t* unit_c;          // [units][E] chosen slots
@@ -49,8 +50,9 @@ struct RouteGeometry {
   int64_t rows_per_block;
   int blocks;
   int chunks;               // expert chunks per document in the closing launch
+  bool one_launch;          // the forward is one cluster that closes the call itself
 };
-RouteGeometry route_geometry(int64_t N, int64_t E, int64_t documents, int num_sms);
+RouteGeometry route_geometry(int64_t N, int64_t E, int64_t documents, bool offsets, int num_sms);
 
 cudaError_t launch_route_forward(int dtype, const RouteGeometry& g, const RouteArgs& a, cudaStream_t s);
 cudaError_t launch_route_finish(const RouteGeometry& g, const RouteArgs& a, cudaStream_t s);
@@ -61,7 +63,7 @@ cudaError_t launch_route_backward(int dtype, const RouteGeometry& g, const Route
 // -------------------------------------------------------- flce_muon.cu
 
 constexpr int kMuonMaxMats = 32;     // matrices of one launch
-constexpr int kMuonNormBlocks = 256; // partial sums of squares per matrix
+constexpr int kMuonNormBlocks = 1024; // partial sums of squares per matrix
 
 struct MuonMat {
   const void* grad;
@@ -78,6 +80,8 @@ struct MuonArgs {
   int32_t transposed;                // rows > cols: X is the transpose of the update
   int32_t grad_dtype, weight_dtype, update_dtype;
   int32_t vec;                       // 16-byte (bf16: 8-byte) accesses of four elements are aligned
+  int32_t flat;                      // and the matrices' rows follow one another without gaps
+  int32_t pairs;                     // the results' rows are aligned to two elements
   int32_t nesterov, norm_blocks;
   float beta, one_minus_beta;
   double eps;
@@ -103,10 +107,18 @@ struct MuonStep {
   int32_t src;                       // hi[src] holds X; the next X goes to hi[1 - src]
 };
 
+// TMA descriptors of one product. Epilogue boxes: 64 columns x 32 rows, for a
+// mirror image 32 x 64.
+struct MuonMaps {
+  CUtensorMap a, b;                  // operands
+  CUtensorMap e0, e1;                // read by the epilogue: A, or X hi and lo (lo also written)
+  CUtensorMap o0, o1;                // written: the tile (X hi), its mirror image
+};
+
 cudaError_t launch_muon_momentum(const MuonArgs& a, cudaStream_t s);
 cudaError_t launch_muon_prepare(const MuonArgs& a, cudaStream_t s);
-cudaError_t launch_muon_gemm(int phase, const CUtensorMap& ta, const CUtensorMap& tb, const MuonArgs& a,
-                             const MuonStep& st, int pairs, cudaStream_t s);
+cudaError_t launch_muon_gemm(int phase, const MuonMaps& maps, const MuonArgs& a, const MuonStep& st, int pairs,
+                             cudaStream_t s);
 int muon_max_clusters();
 
 }  // namespace flce

@@ -83,6 +83,7 @@ RouteArgs route_args(const flce_route_args* r, const RouteGeometry& g) {
   a.result = r->result;
   a.rows_per_block = g.rows_per_block;
   a.blocks = g.blocks;
+  a.one_launch = g.one_launch;
   return a;
 }
 
@@ -170,11 +171,12 @@ void muon_map_bounds(double a, double b, double c, double r, double* poly, doubl
 }
 
 bool map_half_3d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t mats, uint64_t ld,
-                 uint32_t box_cols, uint32_t box_rows, std::string* why) {
+                 uint32_t box_cols, uint32_t box_rows, std::string* why,
+                 CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   const uint64_t dims[3] = {cols, rows, mats};
   const uint64_t strides[2] = {ld * 2, ld * 2 * rows};
   const uint32_t box[3] = {box_cols, box_rows, 1};
-  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, 3, dims, strides, box, why);
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, 3, dims, strides, box, why, swizzle);
 }
 
 // One group of matrices: momentum, X, the Newton-Schulz steps, the result.
@@ -183,7 +185,7 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
   const MuonSizes z = muon_sizes(q->rows, q->cols);
   const MuonLayout L = muon_layout(q->rows, q->cols, count);
   MuonArgs a{};
-  bool vec = q->cols % 4 == 0;
+  bool vec = q->cols % 4 == 0, flat = true, pairs = true;
   for (int i = 0; i < count; ++i) {
     MuonMat& t = a.mat[i];
     t.grad = mats[i].grad;
@@ -196,7 +198,13 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
     t.ld_update = mats[i].ld_update;
     const uint64_t gb = 4 * element_bytes(q->grad_dtype);
     vec = vec && addr(t.grad) % gb == 0 && t.ld_grad % 4 == 0;
-    if (t.momentum) vec = vec && addr(t.momentum) % 16 == 0 && t.ld_momentum % 4 == 0;
+    flat = flat && t.ld_grad == q->cols;
+    if (t.momentum) {
+      vec = vec && addr(t.momentum) % 16 == 0 && t.ld_momentum % 4 == 0;
+      flat = flat && t.ld_momentum == q->cols;
+    }
+    pairs = pairs && (t.weight ? addr(t.weight) % (2 * element_bytes(q->weight_dtype)) == 0 && t.ld_weight % 2 == 0
+                               : addr(t.update) % (2 * element_bytes(q->update_dtype)) == 0 && t.ld_update % 2 == 0);
   }
   a.count = count;
   a.rows = static_cast<int32_t>(q->rows);
@@ -208,8 +216,10 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
   a.weight_dtype = q->weight_dtype;
   a.update_dtype = q->update_dtype;
   a.vec = vec;
+  a.flat = flat;
+  a.pairs = pairs;
   a.nesterov = q->nesterov != 0;
-  // a block per 4096 elements, at most kMuonNormBlocks
+  // a block per 4096 elements (four vectors of four per thread), at most kMuonNormBlocks
   a.norm_blocks = static_cast<int32_t>(std::min<int64_t>(kMuonNormBlocks, cdiv(q->rows * q->cols, 4096)));
   a.beta = static_cast<float>(q->beta);
   a.one_minus_beta = static_cast<float>(1.0 - q->beta);
@@ -230,17 +240,24 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
   a.lda = z.lda;
   a.timeout_ns = h->timeout_ns;
 
-  // X as K-major operand (rows of 64 k), X as right operand of B X (64 columns
-  // by 64 k), A and B as K-major operands (both symmetric)
-  CUtensorMap mx[2], mxn[2], mg, mp;
+  // X as K-major operand (rows of 64 k) and as right operand of B X (64 columns
+  // by 64 k); A and B as K-major operands (both symmetric); and what the
+  // epilogues read and write
+  CUtensorMap xk[2], xn[2], xe[2], lo, gk, ge, gm, pk, pe, pm;
   std::string why;
   bool ok = true;
   for (int i = 0; i < 2; ++i) {
-    ok = ok && map_half_3d(&mx[i], a.hi[i], z.n, z.m, count, z.ldx, 64, 128, &why);
-    ok = ok && map_half_3d(&mxn[i], a.hi[i], z.n, z.m, count, z.ldx, 64, 64, &why);
+    ok = ok && map_half_3d(&xk[i], a.hi[i], z.n, z.m, count, z.ldx, 64, 128, &why);
+    ok = ok && map_half_3d(&xn[i], a.hi[i], z.n, z.m, count, z.ldx, 64, 64, &why);
+    ok = ok && map_half_3d(&xe[i], a.hi[i], z.n, z.m, count, z.ldx, 64, 32, &why);
   }
-  ok = ok && map_half_3d(&mg, a.gram, z.m, z.m, count, z.lda, 64, 128, &why);
-  ok = ok && map_half_3d(&mp, a.poly, z.m, z.m, count, z.lda, 64, 128, &why);
+  ok = ok && map_half_3d(&lo, a.lo, z.n, z.m, count, z.ldx, 64, 32, &why);
+  ok = ok && map_half_3d(&gk, a.gram, z.m, z.m, count, z.lda, 64, 128, &why);
+  ok = ok && map_half_3d(&ge, a.gram, z.m, z.m, count, z.lda, 64, 32, &why);
+  ok = ok && map_half_3d(&gm, a.gram, z.m, z.m, count, z.lda, 32, 64, &why, CU_TENSOR_MAP_SWIZZLE_NONE);
+  ok = ok && map_half_3d(&pk, a.poly, z.m, z.m, count, z.lda, 64, 128, &why);
+  ok = ok && map_half_3d(&pe, a.poly, z.m, z.m, count, z.lda, 64, 32, &why);
+  ok = ok && map_half_3d(&pm, a.poly, z.m, z.m, count, z.lda, 32, 64, &why, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (!ok) return fail(h, FLCE_ERR_CUDA, "%s", why.c_str());
 
   const double el = static_cast<double>(q->rows) * q->cols * count, dm = static_cast<double>(z.m), dn = static_cast<double>(z.n);
@@ -255,13 +272,14 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
     st.c = coefficients[3 * k + 2];
     st.src = k & 1;
     FLCE_LAUNCH(FLCE_K_MUON_GRAM, count * dm * (dm + 1) * dn, count * (2 * dm * dn + 2 * dm * dm),
-                launch_muon_gemm(kMuonGram, mx[st.src], mx[st.src], a, st, h->muon_clusters, s));
+                launch_muon_gemm(kMuonGram, {xk[st.src], xk[st.src], ge, ge, ge, gm}, a, st, h->muon_clusters, s));
     FLCE_LAUNCH(FLCE_K_MUON_POLY, count * dm * dm * (dm + 1), count * 4 * dm * dm,
-                launch_muon_gemm(kMuonPoly, mg, mg, a, st, h->muon_clusters, s));
+                launch_muon_gemm(kMuonPoly, {gk, gk, ge, ge, pe, pm}, a, st, h->muon_clusters, s));
     const bool last = k == q->steps - 1;
     FLCE_LAUNCH(last ? FLCE_K_MUON_RESULT : FLCE_K_MUON_APPLY, count * 2 * dm * dm * dn,
                 count * (2 * dm * dm + (last ? 8 : 10) * dm * dn),
-                launch_muon_gemm(last ? kMuonLast : kMuonApply, mp, mxn[st.src], a, st, h->muon_clusters, s));
+                launch_muon_gemm(last ? kMuonLast : kMuonApply, {pk, xn[st.src], xe[st.src], lo, xe[1 - st.src], lo}, a, st,
+                                 h->muon_clusters, s));
   }
   return FLCE_OK;
 }
@@ -272,7 +290,8 @@ extern "C" {
 
 uint64_t flce_route_workspace_bytes(flce_handle_t h, int64_t N, int64_t E, int64_t documents) {
   if (!h || N < 0 || N > kMaxDim || E < 1 || E > kRouteMaxExperts || documents < 1 || documents > (1 << 24)) return 0;
-  return route_layout(route_geometry(N, E, documents, h->num_sms), E, documents).total;
+  // without offsets a short batch needs less: one size for both
+  return route_layout(route_geometry(N, E, documents, true, h->num_sms), E, documents).total;
 }
 
 flce_status flce_route_forward(flce_handle_t h, const flce_route_args* r, void* workspace, uint64_t workspace_bytes,
@@ -281,8 +300,8 @@ flce_status flce_route_forward(flce_handle_t h, const flce_route_args* r, void* 
   h->err.clear();
   flce_status st = route_check(h, r);
   if (st != FLCE_OK) return st;
-  const RouteGeometry g = route_geometry(r->N, r->E, r->documents, h->num_sms);
-  const RouteLayout L = route_layout(g, r->E, r->documents);
+  const RouteGeometry g = route_geometry(r->N, r->E, r->documents, r->offsets != nullptr, h->num_sms);
+  const RouteLayout L = route_layout(route_geometry(r->N, r->E, r->documents, true, h->num_sms), r->E, r->documents);
   if (!workspace || addr(workspace) % 256 || workspace_bytes < L.total)
     return fail(h, FLCE_ERR_BUDGET, "the workspace must hold %llu bytes, 256-byte aligned",
                 static_cast<unsigned long long>(L.total));
@@ -306,8 +325,9 @@ flce_status flce_route_forward(flce_handle_t h, const flce_route_args* r, void* 
     const cudaError_t ce = cudaMemsetAsync(a.ticket, 0, 4, s);
     if (ce != cudaSuccess) return fail(h, FLCE_ERR_CUDA, "memset: %s", cudaGetErrorString(ce));
   }
-  FLCE_LAUNCH(FLCE_K_ROUTE_FINISH, 0.0, 8.0 * e * (static_cast<double>(g.blocks) + 2.0 * r->documents),
-              launch_route_finish(g, a, s));
+  if (!g.one_launch)
+    FLCE_LAUNCH(FLCE_K_ROUTE_FINISH, 0.0, 8.0 * e * (static_cast<double>(g.blocks) + 2.0 * r->documents),
+                launch_route_finish(g, a, s));
   return FLCE_OK;
 }
 
@@ -322,7 +342,7 @@ flce_status flce_route_backward(flce_handle_t h, const flce_route_args* r, const
   if (addr(d_logits) % element_bytes(r->dtype) || (addr(d_weights) | addr(d_balance) | addr(d_z)) % 4)
     return fail(h, FLCE_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
   if (r->N == 0) return FLCE_OK;
-  const RouteGeometry g = route_geometry(r->N, r->E, r->documents, h->num_sms);
+  const RouteGeometry g = route_geometry(r->N, r->E, r->documents, true, h->num_sms);
   DeviceGuard guard(h->device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const double n = static_cast<double>(r->N), e = static_cast<double>(r->E);

@@ -212,7 +212,10 @@ def check_call_tensors(x, W, t, dx, dW, dtype, in_device, out_device) -> None:
 
 def _stream_ptr(device) -> int:
     import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    if device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    # the same handle without the Stream object around it (2 us less per call)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 class FLCE:

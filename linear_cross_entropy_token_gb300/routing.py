@@ -30,20 +30,50 @@ class Routing:
     balance, z: the losses, 0-dim float32. n_live: 0-dim int32.
     """
 
-    __slots__ = ("weights", "experts", "counts", "stats", "slope", "result", "valid", "offsets", "k",
-                 "renormalize")
+    # `state` holds the call's small results and what the backward reads, one
+    # allocation: result (4 floats: balance, z, 1 / n, n), slope, stats, and
+    # the forward's workspace behind them
+    __slots__ = ("weights", "experts", "counts", "state", "valid", "offsets", "k", "renormalize")
 
     @property
     def balance(self) -> torch.Tensor:
-        return self.result[0]
+        return self.state[0]
 
     @property
     def z(self) -> torch.Tensor:
-        return self.result[1]
+        return self.state[1]
 
     @property
     def n_live(self) -> torch.Tensor:
-        return self.result[3].view(torch.int32)
+        return self.state[3].view(torch.int32)
+
+    def bind(self, logits) -> RouteArgs:
+        """The library's argument block for these logits (N, E)."""
+        N, E = logits.shape
+        a = RouteArgs()
+        a.logits = logits.data_ptr()
+        a.dtype = LOGIT_DTYPES[logits.dtype]
+        a.k = self.k
+        a.N, a.E, a.ld = N, E, _row_stride(logits)
+        a.renormalize = int(self.renormalize)
+        a.valid = None if self.valid is None else self.valid.data_ptr()
+        a.offsets = None if self.offsets is None else self.offsets.data_ptr()
+        a.documents = 1 if self.offsets is None else self.offsets.numel() - 1
+        a.weights = self.weights.data_ptr()
+        a.experts = self.experts.data_ptr()
+        a.counts = self.counts.data_ptr()
+        base = self.state.data_ptr()
+        slope, stats, _ = _state_layout(N, E, a.documents)
+        a.result = base
+        a.slope = base + 4 * slope
+        a.stats = base + 4 * stats
+        return a
+
+
+def _state_layout(N: int, E: int, documents: int):
+    """Offsets, in floats, of slope, stats and the workspace in Routing.state."""
+    stats = (4 + documents * E + 1) // 2 * 2          # pairs of floats, 8-byte aligned
+    return 4, stats, (stats + 2 * N + 63) // 64 * 64   # the workspace on 256 bytes
 
 
 def _row_stride(t: torch.Tensor) -> int:
@@ -70,26 +100,6 @@ def check_route_tensors(logits, k, valid, offsets) -> None:
                                 or offsets.dtype != torch.int64 or offsets.device != logits.device
                                 or not offsets.is_contiguous()):
         raise ValueError(f"offsets must be a contiguous 1-D int64 tensor of at least two entries on {logits.device}")
-
-
-def _args(logits, r: Routing) -> RouteArgs:
-    N, E = logits.shape
-    a = RouteArgs()
-    a.logits = logits.data_ptr()
-    a.dtype = LOGIT_DTYPES[logits.dtype]
-    a.k = r.k
-    a.N, a.E, a.ld = N, E, _row_stride(logits)
-    a.renormalize = int(r.renormalize)
-    a.valid = None if r.valid is None else r.valid.data_ptr()
-    a.offsets = None if r.offsets is None else r.offsets.data_ptr()
-    a.documents = 1 if r.offsets is None else r.offsets.numel() - 1
-    a.weights = r.weights.data_ptr()
-    a.experts = r.experts.data_ptr()
-    a.counts = r.counts.data_ptr()
-    a.stats = r.stats.data_ptr()
-    a.slope = r.slope.data_ptr()
-    a.result = r.result.data_ptr()
-    return a
 
 
 def _handle(t: torch.Tensor, handle) -> FLCE:
@@ -119,14 +129,13 @@ def route(logits: torch.Tensor, k: int, valid=None, offsets=None, renormalize: b
     r.weights = torch.empty((N, k), dtype=torch.float32, device=dev)
     r.experts = torch.empty((N, k), dtype=torch.int32, device=dev)
     r.counts = torch.empty((E,) if offsets is None else (documents, E), dtype=torch.int64, device=dev)
-    r.stats = torch.empty((N, 2), dtype=torch.float32, device=dev)
-    r.slope = torch.empty((documents, E), dtype=torch.float32, device=dev)
-    r.result = torch.empty(4, dtype=torch.float32, device=dev)
     nbytes = h.lib.flce_route_workspace_bytes(h.h, N, E, documents)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    a = _args(logits, r)
-    h._check(h.lib.flce_route_forward(h.h, ctypes.byref(a), ws.data_ptr(), nbytes, _stream_ptr(dev)),
-             "flce_route_forward")
+    ws = _state_layout(N, E, documents)[2]
+    r.state = torch.empty(ws + (nbytes + 3) // 4, dtype=torch.float32, device=dev)
+    a = r.bind(logits)
+    st = h.lib.flce_route_forward(h.h, ctypes.byref(a), a.result + 4 * ws, nbytes, _stream_ptr(dev))
+    if st:
+        h._check(st, "flce_route_forward")
     return r
 
 
@@ -139,7 +148,7 @@ def route_backward(r: Routing, logits: torch.Tensor, d_weights=None, d_balance=N
     h = _handle(logits, handle)
     N, E = logits.shape
     dev = logits.device
-    if tuple(r.weights.shape) != (N, r.k) or r.slope.shape[1] != E or r.weights.device != dev:
+    if tuple(r.weights.shape) != (N, r.k) or r.counts.shape[-1] != E or r.weights.device != dev:
         raise ValueError("the routing was not made from these logits")
     if d_weights is not None and (tuple(d_weights.shape) != (N, r.k) or d_weights.dtype != torch.float32
                                   or d_weights.device != dev or not d_weights.is_contiguous()):
@@ -152,9 +161,11 @@ def route_backward(r: Routing, logits: torch.Tensor, d_weights=None, d_balance=N
     elif (tuple(out.shape) != (N, E) or out.dtype != logits.dtype or out.device != dev
           or (E > 1 and N > 0 and out.stride(1) != 1) or (N > 1 and out.stride(0) < E)):
         raise ValueError(f"out must be {logits.dtype} of shape ({N}, {E}) with contiguous rows on {dev}")
-    a = _args(logits, r)
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    h._check(h.lib.flce_route_backward(h.h, ctypes.byref(a), ptr(d_weights), ptr(d_balance), ptr(d_z),
-                                       out.data_ptr(), _row_stride(out), _stream_ptr(dev)),
-             "flce_route_backward")
+    a = r.bind(logits)
+    st = h.lib.flce_route_backward(h.h, ctypes.byref(a), None if d_weights is None else d_weights.data_ptr(),
+                                   None if d_balance is None else d_balance.data_ptr(),
+                                   None if d_z is None else d_z.data_ptr(), out.data_ptr(), _row_stride(out),
+                                   _stream_ptr(dev))
+    if st:
+        h._check(st, "flce_route_backward")
     return out
