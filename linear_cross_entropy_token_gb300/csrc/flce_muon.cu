@@ -26,6 +26,9 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+#include <type_traits>
+
 #include "flce_internal.h"
 #include "flce_train.h"
 #include "ptx.cuh"
@@ -160,6 +163,7 @@ __global__ void __launch_bounds__(256) muon_momentum_kernel(const __grid_constan
       q.add(g);
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   double s = q.total();
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
@@ -180,7 +184,9 @@ constexpr int kTile = 64;
 // 64 elements, and the tile holds zeros past the matrix). Bound by HBM.
 __global__ void __launch_bounds__(256) muon_prepare_kernel(const __grid_constant__ MuonArgs a) {
   __shared__ float tile[kTile][kTile + 1];
-  __shared__ double sh[8];
+  __shared__ float sh[2];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const MuonMat& t = a.mat[blockIdx.y];
   const int tiles_c = (a.cols + kTile - 1) / kTile;
   const int r0 = (blockIdx.x / tiles_c) * kTile, c0 = (blockIdx.x % tiles_c) * kTile;
@@ -220,17 +226,22 @@ __global__ void __launch_bounds__(256) muon_prepare_kernel(const __grid_constant
       tile[r][tc] = u;
     }
   }
-  double s = 0.0;
-  for (int i = threadIdx.x; i < a.norm_blocks; i += 256) s += a.norm[blockIdx.y * kMuonNormBlocks + i];
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
+  // every block takes the factor from the partial sums itself, by one warp: the
+  // few fp64 units would make a block of 256 threads doing so the bound (302 us
+  // against HBM's 100 at 4096 x 16384)
+  if (threadIdx.x < 32) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < a.norm_blocks; i += 32) s += a.norm[blockIdx.y * kMuonNormBlocks + i];
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+    if (threadIdx.x == 0) {
+      const double inv = static_cast<double>(kXScale) / (sqrt(s) + a.eps);
+      // in two factors, so that neither leaves fp32's normal range
+      sh[0] = inv < 1e-30 ? 0x1p-64f : 1.f;
+      sh[1] = static_cast<float>(inv < 1e-30 ? inv * 0x1p64 : inv);
+    }
+  }
   __syncthreads();
-  s = 0.0;
-  for (int w = 0; w < 8; ++w) s += sh[w];
-  const double inv = static_cast<double>(kXScale) / (sqrt(s) + a.eps);
-  // in two factors, so that neither leaves fp32's normal range
-  const float f1 = inv < 1e-30 ? 0x1p-64f : 1.f;
-  const float f2 = static_cast<float>(inv < 1e-30 ? inv * 0x1p64 : inv);
+  const float f1 = sh[0], f2 = sh[1];
   const int64_t base = static_cast<int64_t>(blockIdx.y) * a.m * a.ldx;
 #pragma unroll
   for (int it = 0; it < 2; ++it) {
@@ -255,7 +266,8 @@ __global__ void __launch_bounds__(256) muon_prepare_kernel(const __grid_constant
 
 // ------------------------------------------------------- the products
 
-constexpr int kTM = 256, kTN = 256;
+// Output tiles: 256 x 256 on a CTA pair, 128 x 128 on one CTA
+constexpr int kPairTile = 256, kSingleTile = 128;
 constexpr int kStages = 5;
 constexpr uint32_t kABytes = 128 * kBK * 2;    // 16 KB: a CTA's 128 rows of A
 constexpr uint32_t kBBytes = 128 * kBK * 2;    // 16 KB: its 128 columns of B
@@ -266,7 +278,6 @@ constexpr uint32_t kEpiPart = 32 * 128;
 constexpr uint32_t kEpiBytes = 4 * 2 * 2 * kEpiPart;
 constexpr uint32_t kSmemBytes = 1024 + kStages * kStageBytes + kEpiBytes + (2 * kStages + 5 + 8) * 8 + 16;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-constexpr uint32_t kTmemCols = 512;
 constexpr int kThreads = 192;
 constexpr int kEpiThreads = 128;
 
@@ -329,45 +340,103 @@ __device__ __forceinline__ MuonUnit muon_unit(int u, int tiles_m, int tiles_n) {
   return r;
 }
 
-// One element of the result: the weight's update in place, or the update.
-__device__ __forceinline__ void write_result(const MuonArgs& a, const MuonMat& t, int64_t row, int64_t col, float o) {
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float2 to_float2(float2 v) { return v; }
+__device__ __forceinline__ float2 to_float2(__nv_bfloat162 v) { return __bfloat1622float2(v); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put(float2* p, float2 v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat162* p, float2 v) { *p = __floats2bfloat162_rn(v.x, v.y); }
+template <class T>
+struct PairOf;
+template <>
+struct PairOf<float> {
+  using type = float2;
+};
+template <>
+struct PairOf<__nv_bfloat16> {
+  using type = __nv_bfloat162;
+};
+
+// f(T*, W) for the result tensor of a matrix: its element type, whether it is
+// a weight to be updated (true) or the update itself (false), its row stride
+template <class F>
+__device__ __forceinline__ void with_result(const MuonArgs& a, const MuonMat& t, F&& f) {
   if (t.weight) {
-    const int64_t at = row * t.ld_weight + col;
-    if (a.weight_dtype == 1) {
-      float* w = static_cast<float*>(t.weight) + at;
-      *w = *w * a.decay - a.lr * o;
-    } else {
-      __nv_bfloat16* w = static_cast<__nv_bfloat16*>(t.weight) + at;
-      *w = __float2bfloat16_rn(__bfloat162float(*w) * a.decay - a.lr * o);
-    }
-  } else {
-    const int64_t at = row * t.ld_update + col;
-    if (a.update_dtype == 1)
-      static_cast<float*>(t.update)[at] = o;
+    if (a.weight_dtype == 1)
+      f(static_cast<float*>(t.weight), std::true_type(), t.ld_weight);
     else
-      static_cast<__nv_bfloat16*>(t.update)[at] = __float2bfloat16_rn(o);
+      f(static_cast<__nv_bfloat16*>(t.weight), std::true_type(), t.ld_weight);
+  } else {
+    if (a.update_dtype == 1)
+      f(static_cast<float*>(t.update), std::false_type(), t.ld_update);
+    else
+      f(static_cast<__nv_bfloat16*>(t.update), std::false_type(), t.ld_update);
   }
 }
 
-// Two neighbours of a row at once, where the tensor's rows are aligned to pairs.
-__device__ __forceinline__ void write_result2(const MuonArgs& a, const MuonMat& t, int64_t row, int64_t col, float2 o) {
-  if (t.weight) {
-    const int64_t at = row * t.ld_weight + col;
-    if (a.weight_dtype == 1) {
-      float2* w = reinterpret_cast<float2*>(static_cast<float*>(t.weight) + at);
-      const float2 v = *w;
-      *w = make_float2(v.x * a.decay - a.lr * o.x, v.y * a.decay - a.lr * o.y);
-    } else {
-      __nv_bfloat162* w = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(t.weight) + at);
-      const float2 v = __bfloat1622float2(*w);
-      *w = __floats2bfloat162_rn(v.x * a.decay - a.lr * o.x, v.y * a.decay - a.lr * o.y);
+// `rows` rows of 64 result columns from a warp's staged fp32 tile (columns
+// 0..31 at p0, 32..63 at p1, 128-byte swizzled), two columns per lane, a row
+// at a time; a weight's eight rows are read before the first is written.
+template <bool W, class T>
+__device__ __forceinline__ void write_rows(T* out, int64_t ld, int rows, int cols, bool pairs, float decay, float lr,
+                                           const uint8_t* p0, const uint8_t* p1, int lane) {
+  using T2 = typename PairOf<T>::type;
+  const int c = 2 * lane;
+  if (c >= cols) return;
+  const uint8_t* part = lane < 16 ? p0 : p1;
+  const int chunk = (c & 31) >> 2;
+  auto staged = [&](int r) {
+    return *reinterpret_cast<const float2*>(part + r * 128 + ((chunk ^ (r & 7)) << 4) + (c & 3) * 4);
+  };
+  T* p = out + c;
+  if (pairs && c + 1 < cols) {
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+      T2 w[8];
+      if (W) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (r0 + j < rows) w[j] = *reinterpret_cast<const T2*>(p + (r0 + j) * ld);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (r0 + j < rows) {
+          float2 o = staged(r0 + j);
+          if (W) {
+            const float2 v = to_float2(w[j]);
+            o = make_float2(v.x * decay - lr * o.x, v.y * decay - lr * o.y);
+          }
+          put(reinterpret_cast<T2*>(p + (r0 + j) * ld), o);
+        }
+      }
     }
   } else {
-    const int64_t at = row * t.ld_update + col;
-    if (a.update_dtype == 1)
-      *reinterpret_cast<float2*>(static_cast<float*>(t.update) + at) = o;
-    else
-      *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(t.update) + at) = __floats2bfloat162_rn(o.x, o.y);
+    for (int r = 0; r < rows; ++r) {
+      const float2 o = staged(r);
+      T* q = p + r * ld;
+      put(q, W ? to_float(q[0]) * decay - lr * o.x : o.x);
+      if (c + 1 < cols) put(q + 1, W ? to_float(q[1]) * decay - lr * o.y : o.y);
+    }
+  }
+}
+
+// The transpose: the lane's row of 64 values down one column of the result
+// (the lanes' columns are neighbours).
+template <bool W, class T>
+__device__ __forceinline__ void write_columns(T* out, int64_t ld, int rows, float decay, float lr,
+                                              const float (&o)[64]) {
+#pragma unroll
+  for (int r0 = 0; r0 < 64; r0 += 16) {
+    T w[16];
+    if (W) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (r0 + j < rows) w[j] = out[(r0 + j) * ld];
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (r0 + j < rows) put(out + (r0 + j) * ld, W ? to_float(w[j]) * decay - lr * o[r0 + j] : o[r0 + j]);
   }
 }
 
@@ -407,7 +476,23 @@ struct MuonEpilogue {
     ++loads;
   }
 
-  // columns c0 .. c0 + 63 of the warp's rows, accumulator values in v
+  // the weight's lines of this tile into L2, while its products run
+  __device__ __forceinline__ void prefetch_weight(int mat, int row0, int n0, int tile) {
+    const MuonMat& t = a.mat[mat];
+    if (!t.weight) return;
+    const int es = a.weight_dtype == 1 ? 4 : 2;
+    const char* w = static_cast<const char*>(t.weight);
+    const int cols = min(tile, a.n - n0), rows = min(32, a.m - row0);
+    if (a.transposed) {  // `cols` rows of `rows` elements
+      for (int r = lane; r < cols; r += 32)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(w + ((n0 + r) * t.ld_weight + row0) * es));
+    } else if (lane < rows) {
+      const char* p = w + ((row0 + lane) * t.ld_weight + n0) * es;
+      for (int b = 0; b < cols * es; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + b));
+    }
+  }
+
+  // columns c0 .. c0 + 63 of the warp's rows, accumulator values in r0 and r1
   __device__ __forceinline__ bool group(int mat, int row0, int c0, bool mirror, float factor, const uint32_t (&r0)[32],
                                         const uint32_t (&r1)[32]) {
     const uint32_t b = uses & 1u;
@@ -492,18 +577,7 @@ struct MuonEpilogue {
           }
           q0[j ^ sw] = make_uint4(h[0], h[1], h[2], h[3]);
           q1[j ^ sw] = make_uint4(l[0], l[1], l[2], l[3]);
-        } else if (a.transposed) {
-          // out[c0 + ..][row0 + lane]: the lanes' columns are neighbours
-          const int64_t i = row0 + lane;
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (i < a.m && c0 + 8 * j + e < a.n)
-              write_result(a, a.mat[mat], c0 + 8 * j + e, i, x[e] * (a.scale * kXInv));
         } else {
-          // as fp32 in place: columns 0..31 where hi was, 32..63 where lo was.
-          // Row `lane` is this lane's alone until the barrier below; its chunks
-          // 2 j, 2 j + 1 of the first half held hi and lo of columns 16 j .. :
-          // kept in registers until every chunk of the row has been read
 #pragma unroll
           for (int e = 0; e < 8; ++e) out_[8 * j + e] = x[e] * (a.scale * kXInv);
         }
@@ -517,7 +591,13 @@ struct MuonEpilogue {
           bulk_commit_group();
         }
         __syncwarp();
-      } else if (!a.transposed) {
+      } else if (a.transposed) {
+        with_result(a, a.mat[mat], [&](auto* out, auto W, int64_t ld) {
+          if (row0 + lane < a.m)
+            write_columns<decltype(W)::value>(out + c0 * ld + row0 + lane, ld, min(64, a.n - c0), a.decay, a.lr, out_);
+        });
+      } else {
+        // as fp32 in place: columns 0..31 where hi was, 32..63 where lo was
         float4* f0 = reinterpret_cast<float4*>(q0);
         float4* f1 = reinterpret_cast<float4*>(q1);
 #pragma unroll
@@ -526,21 +606,10 @@ struct MuonEpilogue {
           f1[j ^ sw] = make_float4(out_[32 + 4 * j], out_[33 + 4 * j], out_[34 + 4 * j], out_[35 + 4 * j]);
         }
         __syncwarp();
-        // a row at a time, two neighbouring columns per lane
-        const uint8_t* part = lane < 16 ? p0 : p1;
-        const int c = 2 * lane, chunk = (c & 31) >> 2;
-        const int64_t col = c0 + c;
-        const int rows = min(32, a.m - row0);
-#pragma unroll 8
-        for (int r = 0; r < rows; ++r) {
-          const float2 o = *reinterpret_cast<const float2*>(part + r * 128 + ((chunk ^ (r & 7)) << 4) + (c & 3) * 4);
-          if (a.pairs && col + 1 < a.n) {
-            write_result2(a, a.mat[mat], row0 + r, col, o);
-          } else {
-            if (col < a.n) write_result(a, a.mat[mat], row0 + r, col, o.x);
-            if (col + 1 < a.n) write_result(a, a.mat[mat], row0 + r, col + 1, o.y);
-          }
-        }
+        with_result(a, a.mat[mat], [&](auto* out, auto W, int64_t ld) {
+          write_rows<decltype(W)::value>(out + row0 * ld + c0, ld, min(32, a.m - row0), min(64, a.n - c0), a.pairs,
+                                         a.decay, a.lr, p0, p1, lane);
+        });
         fence_proxy_async_smem();  // the next load overwrites what was written here
         __syncwarp();
       }
@@ -550,15 +619,21 @@ struct MuonEpilogue {
   float out_[PHASE == kMuonLast ? 64 : 1];
 };
 
-// A persistent kernel of CTA pairs on 256 x 256 tiles (tcgen05 cta_group::2,
-// each CTA holding its 128 rows of A and 128 columns of B per 64-deep
-// k-block), the accumulator double-buffered in TMEM so that the epilogue of a
-// tile overlaps the next tile's products. Warp 0 loads by TMA, warp 1 issues,
-// warps 2..5 run the epilogue. Every wait is bounded.
-template <int PHASE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    muon_gemm_kernel(const __grid_constant__ MuonMaps maps, const __grid_constant__ MuonArgs a,
-                     const __grid_constant__ MuonStep st) {
+// The persistent kernel of one product. PAIR: CTA pairs on 256 x 256 tiles
+// (tcgen05 cta_group::2, each CTA holding its 128 rows of A and 128 columns of
+// B per 64-deep k-block); else one CTA per 128 x 128 tile, for outputs with too
+// few large tiles to fill the GPU (muon_tile has the rule). The accumulator is
+// double-buffered in TMEM, so that the epilogue of a tile overlaps the next
+// tile's products. Warp 0 loads by TMA, warp 1 issues, warps 2..5 run the
+// epilogue. Every wait is bounded.
+//
+// The kernels of a call form a chain of programmatic launches: each starts
+// while its predecessor drains, sets up its barriers and TMEM, and waits for it
+// before its first access to global memory.
+template <int PHASE, bool PAIR>
+__device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonArgs& a, const MuonStep& st) {
+  constexpr int kTile_ = PAIR ? kPairTile : kSingleTile;
+  constexpr uint32_t kCols = 2 * kTile_;   // TMEM: two accumulators
   constexpr bool kSym = PHASE == kMuonGram || PHASE == kMuonPoly;
   constexpr int BMN = kSym ? 0 : 1;   // X as the right operand is contiguous along its columns
   extern __shared__ uint8_t smem_raw[];
@@ -577,9 +652,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
-  const int pair = static_cast<int>(cluster_id_x()), npairs = static_cast<int>(num_clusters_x());
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const int first_unit = PAIR ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
+  const int unit_step = PAIR ? static_cast<int>(num_clusters_x()) : static_cast<int>(gridDim.x);
   uint32_t* err = a.ctrl + kCtrlError;
+  auto wait = [&](uint32_t bar, uint32_t parity, uint32_t* e, uint64_t ns) {
+    return PAIR ? mbar_wait_bounded_cluster(bar, parity, e, ns) : mbar_wait_bounded(bar, parity, e, ns);
+  };
+  // an arrival, when the products issued so far are done, in every CTA of the unit
+  auto commit = [&](uint32_t bar) {
+    if (PAIR)
+      tc_commit_pair_multicast(bar, 0x3);
+    else
+      tc_commit(bar);
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -588,7 +674,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int acc = 0; acc < 2; ++acc) {
       mbar_init(tfull_bar(acc), 1);
-      mbar_init(tempty_bar(acc), 2 * kEpiThreads);
+      mbar_init(tempty_bar(acc), (PAIR ? 2 : 1) * kEpiThreads);
     }
     mbar_init(drain_bar, 1);
     for (int i = 0; i < 8; ++i) mbar_init(drain_bar + 8u * (1 + i), 1);  // the epilogue warps' loads
@@ -598,16 +684,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_map(&maps.b);
   }
   if (warp == 1) {
-    tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
-    tmem_relinquish_pair();
+    if (PAIR) {
+      tmem_alloc_pair(smem_u32(tmem_slot), kCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), kCols);
+      tmem_relinquish();
+    }
   }
   __syncthreads();
-  cluster_sync();
+  if (PAIR) cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  const int tiles_m = (a.m + kTM - 1) / kTM;
-  const int tiles_n = kSym ? tiles_m : (a.n + kTN - 1) / kTN;
+  const int tiles_m = (a.m + kTile_ - 1) / kTile_;
+  const int tiles_n = kSym ? tiles_m : (a.n + kTile_ - 1) / kTile_;
   const int num_units = a.count * (kSym ? tiles_m * (tiles_m + 1) / 2 : tiles_m * tiles_n);
   const int num_kb = ((PHASE == kMuonGram ? a.n : a.m) + kBK - 1) / kBK;
 
@@ -615,28 +708,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       uint32_t n_issued = 0;
       bool failed = false;
-      for (int u = pair; u < num_units && !failed; u += npairs) {
+      for (int u = first_unit; u < num_units && !failed; u += unit_step) {
         const MuonUnit t = muon_unit<PHASE>(u, tiles_m, tiles_n);
-        const int mA = t.tm * kTM + static_cast<int>(rank) * 128;
-        const int nB = t.tn * kTN + static_cast<int>(rank) * 128;
+        const int mA = t.tm * kTile_ + static_cast<int>(rank) * 128;
+        const int nB = t.tn * kTile_ + static_cast<int>(rank) * 128;
         for (int kb = 0; kb < num_kb; ++kb) {
           const int stage = n_issued % kStages;
           const uint32_t phase = (n_issued / kStages) & 1u;
-          if (!mbar_wait_bounded_cluster(empty_bar(stage), phase ^ 1u, err, a.timeout_ns)) {
+          if (!wait(empty_bar(stage), phase ^ 1u, err, a.timeout_ns)) {
             failed = true;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * kStageBytes);
-          const uint32_t fb = mapa_shared(full_bar(stage), 0);
+          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), (PAIR ? 2 : 1) * kStageBytes);
+          const uint32_t fb = PAIR ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
           const uint32_t sa = smem_u32(sA + stage * kABytes);
           const uint32_t sb = smem_u32(sB + stage * kBBytes);
           const int k0 = kb * kBK;
-          tma_load_3d_pair(sa, &maps.a, fb, k0, mA, t.mat);
+          auto load = [&](uint32_t dst, const CUtensorMap* m, int c0, int c1) {
+            if (PAIR)
+              tma_load_3d_pair(dst, m, fb, c0, c1, t.mat);
+            else
+              tma_load_3d(dst, m, fb, c0, c1, t.mat);
+          };
+          load(sa, &maps.a, k0, mA);
           if (BMN == 0) {
-            tma_load_3d_pair(sb, &maps.b, fb, k0, nB, t.mat);
+            load(sb, &maps.b, k0, nB);
           } else {
-            tma_load_3d_pair(sb, &maps.b, fb, nB, k0, t.mat);
-            tma_load_3d_pair(sb + 8192, &maps.b, fb, nB + 64, k0, t.mat);
+            load(sb, &maps.b, nB, k0);
+            load(sb + 8192, &maps.b, nB + 64, k0);
           }
           ++n_issued;
         }
@@ -649,23 +748,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc = idesc_f16_f32(kTM, kTN, 0, BMN);
+      constexpr uint32_t idesc = idesc_f16_f32(kTile_, kTile_, 0, BMN);
       uint32_t n_consumed = 0;
       bool issued = false, failed = false;
       int it = 0;
-      for (int u = pair; u < num_units && !failed; u += npairs, ++it) {
+      for (int u = first_unit; u < num_units && !failed; u += unit_step, ++it) {
         const int acc = it & 1;
         const uint32_t acc_phase = (it >> 1) & 1;
-        if (!mbar_wait_bounded_cluster(tempty_bar(acc), acc_phase ^ 1u, err, a.timeout_ns)) {
+        if (!wait(tempty_bar(acc), acc_phase ^ 1u, err, a.timeout_ns)) {
           failed = true;
           break;
         }
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + acc * kTN;
+        const uint32_t d_tmem = tmem_base + acc * kTile_;
         for (int kb = 0; kb < num_kb; ++kb) {
           const int stage = n_consumed % kStages;
           const uint32_t phase = (n_consumed / kStages) & 1u;
-          if (!mbar_wait_bounded_cluster(full_bar(stage), phase, err, a.timeout_ns)) {
+          if (!wait(full_bar(stage), phase, err, a.timeout_ns)) {
             failed = true;
             break;
           }
@@ -677,17 +776,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint64_t ad = smem_desc_sw128(sa + 32u * k, 16u, 1024u);
             const uint64_t bd = BMN ? smem_desc_sw128(sb + 2048u * k, 8192u, 1024u)
                                     : smem_desc_sw128(sb + 32u * k, 16u, 1024u);
-            tc_mma_bf16_pair(d_tmem, ad, bd, idesc, (kb > 0 || k > 0) ? 1u : 0u);
+            // kind::f16: the descriptor's type fields say fp16
+            if (PAIR)
+              tc_mma_bf16_pair(d_tmem, ad, bd, idesc, (kb > 0 || k > 0) ? 1u : 0u);
+            else
+              tc_mma_bf16(d_tmem, ad, bd, idesc, (kb > 0 || k > 0) ? 1u : 0u);
           }
           issued = true;
-          tc_commit_pair_multicast(empty_bar(stage), 0x3);
+          commit(empty_bar(stage));
           ++n_consumed;
         }
         if (failed) break;
-        tc_commit_pair_multicast(tfull_bar(acc), 0x3);
+        commit(tfull_bar(acc));
       }
       if (failed && issued) {
-        tc_commit_pair(drain_bar);
+        if (PAIR)
+          tc_commit_pair(drain_bar);
+        else
+          tc_commit(drain_bar);
         drain_wait(drain_bar, 0, a.timeout_ns);
       }
     }
@@ -697,23 +803,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int ncols = kSym ? a.m : a.n;
     bool ok = true;
     int it = 0;
-    for (int u = pair; u < num_units; u += npairs, ++it) {
+    for (int u = first_unit; u < num_units; u += unit_step, ++it) {
       const int acc = it & 1;
       const uint32_t acc_phase = (it >> 1) & 1;
       const MuonUnit t = muon_unit<PHASE>(u, tiles_m, tiles_n);
-      const int row0 = t.tm * kTM + static_cast<int>(rank) * 128 + wq * 32, n0 = t.tn * kTN;
+      const int row0 = t.tm * kTile_ + static_cast<int>(rank) * 128 + wq * 32, n0 = t.tn * kTile_;
       // this warp's groups of 64 columns that hold any of the output
-      const int groups = row0 < a.m ? min(kTN / 64, (ncols - n0 + 63) / 64) : 0;
+      const int groups = row0 < a.m ? min(kTile_ / 64, (ncols - n0 + 63) / 64) : 0;
       float factor = 0.f;
       if (groups > 0) {
         epi.load(t.mat, row0, n0);
         if (!kSym && row0 + lane < a.m) factor = st.a + a.diag[static_cast<int64_t>(t.mat) * a.m + row0 + lane];
       }
-      ok = mbar_wait_bounded_cluster(tfull_bar(acc), acc_phase, err, a.timeout_ns);
+      if (PHASE == kMuonLast && groups > 0) epi.prefetch_weight(t.mat, row0, n0, kTile_);
+      ok = wait(tfull_bar(acc), acc_phase, err, a.timeout_ns);
       ok = __all_sync(kAll, ok);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(wq * 32) << 16) + acc * kTN;
+      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(wq * 32) << 16) + acc * kTile_;
       auto release = [&] {
         tc_fence_before();
         if (rank == 0)
@@ -746,10 +853,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   __syncwarp();
   __syncthreads();
-  cluster_sync();
+  if (PAIR) cluster_sync();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, kTmemCols);
+    if (PAIR)
+      tmem_dealloc_pair(tmem_base, kCols);
+    else
+      tmem_dealloc(tmem_base, kCols);
   }
   if (threadIdx.x == 0) {
     const uint32_t code = ld_volatile_u32(err);
@@ -758,20 +868,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 template <int PHASE>
-cudaError_t launch_phase(const MuonMaps& maps, const MuonArgs& a, const MuonStep& st, int pairs, cudaStream_t s) {
-  auto kern = muon_gemm_kernel<PHASE>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kSmemBytes));
-  if (e != cudaSuccess) return e;
-  const int tiles_m = (a.m + kTM - 1) / kTM, tiles_n = (a.n + kTN - 1) / kTN;
-  const bool sym = PHASE == kMuonGram || PHASE == kMuonPoly;
-  const int64_t units = static_cast<int64_t>(a.count) * (sym ? tiles_m * (tiles_m + 1) / 2 : tiles_m * tiles_n);
-  if (units < pairs) pairs = static_cast<int>(units);
-  kern<<<2 * pairs, kThreads, kSmemBytes, s>>>(maps, a, st);
-  return cudaGetLastError();
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    muon_pair_kernel(const __grid_constant__ MuonMaps maps, const __grid_constant__ MuonArgs a,
+                     const __grid_constant__ MuonStep st) {
+  muon_gemm_body<PHASE, true>(maps, a, st);
+}
+
+template <int PHASE>
+__global__ void __launch_bounds__(kThreads, 1)
+    muon_single_kernel(const __grid_constant__ MuonMaps maps, const __grid_constant__ MuonArgs a,
+                       const __grid_constant__ MuonStep st) {
+  muon_gemm_body<PHASE, false>(maps, a, st);
+}
+
+int64_t muon_units(int phase, const MuonArgs& a, int tile) {
+  const int64_t tm = (a.m + tile - 1) / tile, tn = (a.n + tile - 1) / tile;
+  return a.count * (phase == kMuonGram || phase == kMuonPoly ? tm * (tm + 1) / 2 : tm * tn);
+}
+
+// A launch that may start while the one before it drains
+template <class... P, class... A>
+cudaError_t launch_chained(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int PHASE>
+cudaError_t launch_phase(const MuonMaps& maps, const MuonArgs& a, const MuonStep& st, bool pair, int slots,
+                         cudaStream_t s) {
+  static const cudaError_t opted[2] = {
+      cudaFuncSetAttribute(muon_single_kernel<PHASE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(kSmemBytes)),
+      cudaFuncSetAttribute(muon_pair_kernel<PHASE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(kSmemBytes))};
+  if (opted[pair] != cudaSuccess) return opted[pair];
+  const int64_t units = muon_units(PHASE, a, pair ? kPairTile : kSingleTile);
+  const int n = static_cast<int>(units < slots ? units : slots);
+  return pair ? launch_chained(muon_pair_kernel<PHASE>, dim3(2 * n), kThreads, kSmemBytes, s, maps, a, st)
+              : launch_chained(muon_single_kernel<PHASE>, dim3(n), kThreads, kSmemBytes, s, maps, a, st);
 }
 
 }  // namespace
+
+// Which tile a product runs on: the one whose rounds of tiles over the GPU take
+// less time. A tile costs its k-blocks (clocks per 64-deep k-block) or its
+// epilogue, whichever is longer, and a fixed start.
+bool muon_pair_tile(int phase, const MuonArgs& a, int pairs, int sms) {
+  const int64_t kb = ((phase == kMuonGram ? a.n : a.m) + kBK - 1) / kBK;
+  const int64_t rp = (muon_units(phase, a, kPairTile) + pairs - 1) / pairs;
+  const int64_t rs = (muon_units(phase, a, kSingleTile) + sms - 1) / sms;
+  const int64_t pair = rp * std::max<int64_t>(kb * 530, 6000), single = rs * std::max<int64_t>(kb * 300, 3000);
+  return pair <= single;
+}
 
 cudaError_t launch_muon_momentum(const MuonArgs& a, cudaStream_t s) {
   muon_momentum_kernel<<<dim3(a.norm_blocks, a.count), 256, 0, s>>>(a);
@@ -780,17 +937,16 @@ cudaError_t launch_muon_momentum(const MuonArgs& a, cudaStream_t s) {
 
 cudaError_t launch_muon_prepare(const MuonArgs& a, cudaStream_t s) {
   const int tiles = ((a.rows + kTile - 1) / kTile) * ((a.cols + kTile - 1) / kTile);
-  muon_prepare_kernel<<<dim3(tiles, a.count), 256, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_chained(muon_prepare_kernel, dim3(tiles, a.count), 256, 0, s, a);
 }
 
-cudaError_t launch_muon_gemm(int phase, const MuonMaps& maps, const MuonArgs& a, const MuonStep& st, int pairs,
-                             cudaStream_t s) {
+cudaError_t launch_muon_gemm(int phase, const MuonMaps& maps, const MuonArgs& a, const MuonStep& st, bool pair,
+                             int slots, cudaStream_t s) {
   switch (phase) {
-    case kMuonGram: return launch_phase<kMuonGram>(maps, a, st, pairs, s);
-    case kMuonPoly: return launch_phase<kMuonPoly>(maps, a, st, pairs, s);
-    case kMuonApply: return launch_phase<kMuonApply>(maps, a, st, pairs, s);
-    case kMuonLast: return launch_phase<kMuonLast>(maps, a, st, pairs, s);
+    case kMuonGram: return launch_phase<kMuonGram>(maps, a, st, pair, slots, s);
+    case kMuonPoly: return launch_phase<kMuonPoly>(maps, a, st, pair, slots, s);
+    case kMuonApply: return launch_phase<kMuonApply>(maps, a, st, pair, slots, s);
+    case kMuonLast: return launch_phase<kMuonLast>(maps, a, st, pair, slots, s);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -808,7 +964,7 @@ int muon_max_clusters() {
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  auto kern = muon_gemm_kernel<kMuonApply>;
+  auto kern = muon_pair_kernel<kMuonApply>;
   int n = 0;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)) !=
           cudaSuccess ||

@@ -403,6 +403,8 @@ __global__ void __launch_bounds__(32 * R) route_finish_kernel(const RouteArgs a,
   __shared__ int32_t sh_c[32][R + 1];
   // launched while the forward still runs: its results from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ float sh_z[R];
+  __shared__ int32_t sh_n[R];
   __shared__ double sh_t[3][R];
   __shared__ bool last;
   const int d = blockIdx.x / chunks, chunk = blockIdx.x - d * chunks;
@@ -411,7 +413,7 @@ __global__ void __launch_bounds__(32 * R) route_finish_kernel(const RouteArgs a,
   document_blocks(a, d, &b0, &b1);
 
   int n = 0;
-  double zs = 0.0;
+  float zs = 0.f;  // (fp64 on every thread would be the bound: 36 us at 608 units of 128 experts)
   for (int b = b0 + threadIdx.x; b < b1; b += 32 * R) {
     n += a.unit_live[static_cast<int64_t>(b) + d];
     zs += a.unit_z[static_cast<int64_t>(b) + d];
@@ -421,19 +423,19 @@ __global__ void __launch_bounds__(32 * R) route_finish_kernel(const RouteArgs a,
     zs += __shfl_xor_sync(kAll, zs, o);
   }
   if (tx == 0) {
-    sh_t[0][ty] = n;
-    sh_t[1][ty] = zs;
+    sh_n[ty] = n;
+    sh_z[ty] = zs;
   }
   __syncthreads();
-  n = 0;
-  zs = 0.0;
-  for (int w = 0; w < R; ++w) {
-    n += static_cast<int>(sh_t[0][w]);
-    zs += sh_t[1][w];
+  n = tx < R ? sh_n[tx] : 0;
+  zs = tx < R ? sh_z[tx] : 0.f;
+  for (int o = 16; o > 0; o >>= 1) {
+    n += __shfl_xor_sync(kAll, n, o);
+    zs += __shfl_xor_sync(kAll, zs, o);
   }
   const float slope_n = n > 0 ? static_cast<float>(a.E) / (static_cast<float>(a.k) * static_cast<float>(n)) : 0.f;
 
-  double term = 0.0;
+  float term = 0.f;
   const int e_end = min(a.E, (chunk + 1) * chunk_size);
   for (int e0 = chunk * chunk_size; e0 < e_end; e0 += 32) {
     const int e = e0 + tx;
@@ -463,17 +465,17 @@ __global__ void __launch_bounds__(32 * R) route_finish_kernel(const RouteArgs a,
         const float slope = slope_n * static_cast<float>(c);
         a.counts[o] = c;
         a.slope[o] = slope;
-        term += static_cast<double>(slope * p);
+        term = fmaf(slope, p, term);
       }
     }
     __syncthreads();
   }
-  if (tx == 0) sh_t[2][ty] = term;
+  if (tx == 0) sh_z[ty] = term;
   __syncthreads();
   if (threadIdx.x == 0) {
-    term = 0.0;
-    for (int w = 0; w < R; ++w) term += sh_t[2][w];
-    a.terms[blockIdx.x] = term;
+    double sum = 0.0;
+    for (int w = 0; w < R; ++w) sum += sh_z[w];
+    a.terms[blockIdx.x] = sum;
     if (chunk == 0) {
       a.doc_live[d] = n;
       a.doc_z[d] = zs;
@@ -494,20 +496,24 @@ __global__ void __launch_bounds__(32 * R) route_finish_kernel(const RouteArgs a,
     live += __ldcg(a.doc_live + i);
     z += __ldcg(a.doc_z + i);
   }
-  for (int o = 16; o > 0; o >>= 1) {
-    bal += __shfl_xor_sync(kAll, bal, o);
-    z += __shfl_xor_sync(kAll, z, o);
-    live += __shfl_xor_sync(kAll, live, o);
-  }
-  if (tx == 0) {
-    sh_t[0][ty] = bal;
-    sh_t[1][ty] = z;
-    sh_t[2][ty] = live;
+  // (few documents fill few warps: the others have nothing to add)
+  const int busy = static_cast<int>(min(static_cast<int64_t>(R), (terms + 31) / 32));
+  if (ty < busy) {
+    for (int o = 16; o > 0; o >>= 1) {
+      bal += __shfl_xor_sync(kAll, bal, o);
+      z += __shfl_xor_sync(kAll, z, o);
+      live += __shfl_xor_sync(kAll, live, o);
+    }
+    if (tx == 0) {
+      sh_t[0][ty] = bal;
+      sh_t[1][ty] = z;
+      sh_t[2][ty] = live;
+    }
   }
   __syncthreads();
   if (threadIdx.x == 0) {
     bal = z = live = 0.0;
-    for (int w = 0; w < R; ++w) {
+    for (int w = 0; w < busy; ++w) {
       bal += sh_t[0][w];
       z += sh_t[1][w];
       live += sh_t[2][w];

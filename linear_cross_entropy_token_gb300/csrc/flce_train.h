@@ -117,8 +117,11 @@ struct MuonMaps {
 
 cudaError_t launch_muon_momentum(const MuonArgs& a, cudaStream_t s);
 cudaError_t launch_muon_prepare(const MuonArgs& a, cudaStream_t s);
-cudaError_t launch_muon_gemm(int phase, const MuonMaps& maps, const MuonArgs& a, const MuonStep& st, int pairs,
-                             cudaStream_t s);
+// One product on CTA-pair tiles (slots: pairs that fit at once) or single-CTA
+// tiles (slots: SMs); muon_pair_tile picks.
+cudaError_t launch_muon_gemm(int phase, const MuonMaps& maps, const MuonArgs& a, const MuonStep& st, bool pair,
+                             int slots, cudaStream_t s);
+bool muon_pair_tile(int phase, const MuonArgs& a, int pairs, int sms);
 int muon_max_clusters();
 
 }  // namespace flce

@@ -265,6 +265,14 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
   FLCE_LAUNCH(FLCE_K_MUON_MOMENTUM, 0.0, el * (gb + mb), launch_muon_momentum(a, s));
   FLCE_LAUNCH(FLCE_K_MUON_PREPARE, 0.0, el * ((mats[0].momentum ? 4.0 + (q->nesterov ? gb : 0.0) : gb) + 4.0),
               launch_muon_prepare(a, s));
+  // the handle's tile shape where it was given one, else by the rule
+  auto product = [&](int phase, const MuonMaps& maps, const MuonStep& st) {
+    const int mode = h->cfg.cta_pair;
+    const bool pair = mode == FLCE_CTA_SINGLE ? false
+                      : h->muon_tile_fixed    ? true
+                                              : muon_pair_tile(phase, a, h->muon_clusters, h->num_sms);
+    return launch_muon_gemm(phase, maps, a, st, pair, pair ? h->muon_clusters : h->num_sms, s);
+  };
   for (int k = 0; k < q->steps; ++k) {
     MuonStep st;
     st.a = coefficients[3 * k];
@@ -272,14 +280,13 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
     st.c = coefficients[3 * k + 2];
     st.src = k & 1;
     FLCE_LAUNCH(FLCE_K_MUON_GRAM, count * dm * (dm + 1) * dn, count * (2 * dm * dn + 2 * dm * dm),
-                launch_muon_gemm(kMuonGram, {xk[st.src], xk[st.src], ge, ge, ge, gm}, a, st, h->muon_clusters, s));
+                product(kMuonGram, {xk[st.src], xk[st.src], ge, ge, ge, gm}, st));
     FLCE_LAUNCH(FLCE_K_MUON_POLY, count * dm * dm * (dm + 1), count * 4 * dm * dm,
-                launch_muon_gemm(kMuonPoly, {gk, gk, ge, ge, pe, pm}, a, st, h->muon_clusters, s));
+                product(kMuonPoly, {gk, gk, ge, ge, pe, pm}, st));
     const bool last = k == q->steps - 1;
     FLCE_LAUNCH(last ? FLCE_K_MUON_RESULT : FLCE_K_MUON_APPLY, count * 2 * dm * dm * dn,
                 count * (2 * dm * dm + (last ? 8 : 10) * dm * dn),
-                launch_muon_gemm(last ? kMuonLast : kMuonApply, {pk, xn[st.src], xe[st.src], lo, xe[1 - st.src], lo}, a, st,
-                                 h->muon_clusters, s));
+                product(last ? kMuonLast : kMuonApply, {pk, xn[st.src], xe[st.src], lo, xe[1 - st.src], lo}, st));
   }
   return FLCE_OK;
 }
