@@ -119,9 +119,35 @@ __device__ __forceinline__ float group_max(float v) {
 
 template <int G>
 __device__ __forceinline__ float group_max_nan(float v) {
+  if (G == 32) {
+    float r;
+    asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+  }
 #pragma unroll
   for (int o = G / 2; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(kAll, v, o));
   return v;
+}
+
+template <int G>
+__device__ __forceinline__ uint32_t group_max_u32(uint32_t v) {
+  if (G == 32) return __reduce_max_sync(kAll, v);
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+
+constexpr int log2_of(int v) { return v <= 1 ? 0 : 1 + log2_of(v / 2); }
+
+// A 31-bit key that orders a row's experts: the leading bits of the logit (as
+// an ordered integer), then the expert, the lower the larger. 16-bit types fit
+// whole; of an fp32 logit the last 1 + IDX bits are cut.
+template <int IDX>
+__device__ __forceinline__ uint32_t expert_key(float z, int e) {
+  const uint32_t b = __float_as_uint(z + 0.0f);   // -0 ties with 0
+  const uint32_t ordered = b ^ ((b & 0x80000000u) ? 0xFFFFFFFFu : 0x80000000u);
+  constexpr uint32_t low = (1u << IDX) - 1u;
+  return ((ordered >> 1) & ~low) | (low - static_cast<uint32_t>(e));
 }
 
 // The first document whose end lies past row r (documents: none does). The
@@ -254,32 +280,79 @@ __global__ void __launch_bounds__(kRouteThreads) route_forward_kernel(const Rout
           ++live_rows;
         }
       }
-      // k rounds: the group's largest logit, the lowest lane that has it (its
-      // experts come before the others'), the first of that lane's
-      float share = 0.f;
-      for (int j = 0; j < k; ++j) {
-        float bv = neg_inf();
-        int bi = 0;
+      // The k largest by keys, all distinct: each round takes the group's
+      // largest key below the last one. key - last wraps to the top half for
+      // the keys below it and not for the others, so one unsigned maximum
+      // finds it, with no search for the winner and nothing to remove.
+      constexpr int IDX = log2_of(kCols);
+      uint32_t key[NPL];
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-          if (z[i] > bv) {
-            bv = z[i];
-            bi = i;
+      for (int i = 0; i < NPL; ++i)
+        key[i] = c0 + i < a.E ? expert_key<IDX>(z[i], c0 + i) : static_cast<uint32_t>(kCols - 1 - c0 - i);
+      uint32_t last = 0x80000000u;
+      // fp32: two keys alike in what they keep of the logit, and some logit of
+      // the lane's with bits in what they cut (logits rounded to 16 bits have
+      // none: their ties are true ties, in the keys' order)
+      bool unsure = false;
+      uint32_t bits = 0;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) bits |= __float_as_uint(z[i]);
+      const int rounds = sizeof(T) == 4 && k < a.E ? k + 1 : k;
+      for (int j = 0; j < rounds; ++j) {
+        uint32_t best = key[0] - last;
+#pragma unroll
+        for (int i = 1; i < NPL; ++i) best = max(best, key[i] - last);
+        best = group_max_u32<G>(best) + last;
+        if (sizeof(T) == 4) unsure |= ((best ^ last) >> IDX) == 0;
+        last = best;
+        if (j < k && gl == 0) my_i[gr * k + j] = static_cast<int>((kCols - 1) - (best & (kCols - 1)));
+      }
+      if (sizeof(T) == 4 && __any_sync(kAll, unsure) && __any_sync(kAll, (bits & ((2u << IDX) - 1u)) != 0)) {
+        // exact: the group's largest logit, the lowest lane that has it (its
+        // experts come before the others'), the first of that lane's
+        for (int j = 0; j < k; ++j) {
+          float bv = neg_inf();
+          int bi = 0;
+#pragma unroll
+          for (int i = 0; i < NPL; ++i) {
+            const float v = z[i] != z[i] ? __int_as_float(0x7F800000) : z[i];   // NaN before all, as in the keys
+            if (v > bv) {
+              bv = v;
+              bi = i;
+            }
           }
-        }
-        const float g = group_max<G>(bv);
-        const uint32_t who = __ballot_sync(kAll, bv == g) & gmask;
-        const bool taken = live && g > neg_inf();
-        const float ex = taken ? exp2_approx((g - mm) * kLog2e) : 0.f;
-        share += ex;
-        if (__ffs(who) - 1 == lane) {
-          my_v[gr * k + j] = ex;
-          my_i[gr * k + j] = taken ? c0 + bi : -1;
+          const uint32_t who = __ballot_sync(kAll, bv == group_max<G>(bv)) & gmask;
+          if (__ffs(who) - 1 == lane) {
+            my_i[gr * k + j] = bv > neg_inf() ? c0 + bi : 0;
 #pragma unroll
-          for (int i = 0; i < NPL; ++i)
-            if (i == bi) z[i] = neg_inf();
+            for (int i = 0; i < NPL; ++i)
+              if (i == bi) z[i] = neg_inf();
+          }
+          // a row without a logit left: its slots read a -inf again below
+          if (bv == neg_inf() && who == gmask && gl == 0) my_i[gr * k + j] = -1;
         }
       }
+      __syncwarp();
+      // the slots' weights, a lane per slot
+      float share = 0.f;
+      for (int j = gl; j < k; j += G) {
+        const int e = my_i[gr * k + j];
+        float ex = 0.f;
+        if (live && e >= 0) {
+          const float v = to_f(logits[row * a.ld + e]);
+          if (v == neg_inf()) {
+            my_i[gr * k + j] = -1;
+          } else {
+            ex = exp2_approx((v - mm) * kLog2e);
+            atomicAdd(&cnt[e], 1);
+          }
+        } else {
+          my_i[gr * k + j] = -1;
+        }
+        my_v[gr * k + j] = ex;
+        share += ex;
+      }
+      share = group_sum<G>(share);
       if (gl == 0) my_scale[gr] = a.renormalize ? (share == 0.f ? 0.f : 1.0f / share) : inv;
       __syncwarp();
       const int slots = static_cast<int>(min(static_cast<int64_t>(RPW), end - base)) * k;
@@ -287,7 +360,6 @@ __global__ void __launch_bounds__(kRouteThreads) route_forward_kernel(const Rout
         const int e = my_i[t];
         a.weights[base * k + t] = e >= 0 ? my_v[t] * my_scale[t / k] : 0.f;
         a.experts[base * k + t] = e;
-        if (e >= 0) atomicAdd(&cnt[e], 1);
       }
       __syncwarp();
     }

@@ -47,27 +47,17 @@ class Routing:
     def n_live(self) -> torch.Tensor:
         return self.state[3].view(torch.int32)
 
-    def bind(self, logits) -> RouteArgs:
-        """The library's argument block for these logits (N, E)."""
-        N, E = logits.shape
-        a = RouteArgs()
-        a.logits = logits.data_ptr()
-        a.dtype = LOGIT_DTYPES[logits.dtype]
-        a.k = self.k
-        a.N, a.E, a.ld = N, E, _row_stride(logits)
-        a.renormalize = int(self.renormalize)
-        a.valid = None if self.valid is None else self.valid.data_ptr()
-        a.offsets = None if self.offsets is None else self.offsets.data_ptr()
-        a.documents = 1 if self.offsets is None else self.offsets.numel() - 1
-        a.weights = self.weights.data_ptr()
-        a.experts = self.experts.data_ptr()
-        a.counts = self.counts.data_ptr()
+    def bind(self, logits, N, E, ld, code) -> RouteArgs:
+        """The library's argument block for these logits."""
+        offsets = self.offsets
+        documents = 1 if offsets is None else offsets.numel() - 1
+        slope, stats, _ = _state_layout(N, E, documents)
         base = self.state.data_ptr()
-        slope, stats, _ = _state_layout(N, E, a.documents)
-        a.result = base
-        a.slope = base + 4 * slope
-        a.stats = base + 4 * stats
-        return a
+        return RouteArgs(logits.data_ptr(), code, self.k, N, E, ld, self.renormalize, 0,
+                         None if self.valid is None else self.valid.data_ptr(),
+                         None if offsets is None else offsets.data_ptr(), documents, self.weights.data_ptr(),
+                         self.experts.data_ptr(), self.counts.data_ptr(), base + 4 * stats, base + 4 * slope,
+                         base)
 
 
 def _state_layout(N: int, E: int, documents: int):
@@ -80,35 +70,54 @@ def _row_stride(t: torch.Tensor) -> int:
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
-def check_route_tensors(logits, k, valid, offsets) -> None:
-    """Shapes, dtypes, devices and layout of one call. Raises ValueError."""
-    if logits.dim() != 2 or logits.dtype not in LOGIT_DTYPES:
+def check_route_tensors(logits, k, valid, offsets):
+    """Shapes, dtypes, devices and layout of one call. Raises ValueError;
+    returns (N, E, row stride, dtype code)."""
+    shape = logits.shape
+    code = LOGIT_DTYPES.get(logits.dtype)
+    if len(shape) != 2 or code is None:
         raise ValueError("logits must be 2-D bfloat16, float32 or float16")
-    N, E = logits.shape
+    N, E = shape
     if not 1 <= E <= MAX_EXPERTS:
         raise ValueError(f"logits must have 1 to {MAX_EXPERTS} columns")
     if N >= 2 ** 31:
         raise ValueError("too many rows")
-    if (E > 1 and N > 0 and logits.stride(1) != 1) or (N > 1 and logits.stride(0) < E):
+    ld, inner = logits.stride()
+    if N <= 1:
+        ld = E
+    if (E > 1 and N > 0 and inner != 1) or ld < E:
         raise ValueError("the rows of logits must be contiguous and not overlap")
     if not 1 <= k <= min(E, MAX_K):
         raise ValueError(f"k must lie in 1 .. min(columns, {MAX_K})")
-    if valid is not None and (tuple(valid.shape) != (N,) or valid.dtype not in (torch.bool, torch.uint8)
+    if valid is not None and (valid.shape != (N,) or valid.dtype not in (torch.bool, torch.uint8)
                               or valid.device != logits.device or not valid.is_contiguous()):
         raise ValueError(f"valid must be a contiguous bool or uint8 tensor of shape ({N},) on {logits.device}")
-    if offsets is not None and (offsets.dim() != 1 or offsets.numel() < 2 or offsets.numel() > 2 ** 24
+    if offsets is not None and (offsets.dim() != 1 or not 2 <= offsets.numel() <= 2 ** 24
                                 or offsets.dtype != torch.int64 or offsets.device != logits.device
                                 or not offsets.is_contiguous()):
         raise ValueError(f"offsets must be a contiguous 1-D int64 tensor of at least two entries on {logits.device}")
+    return N, E, ld, code
 
 
 def _handle(t: torch.Tensor, handle) -> FLCE:
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("the tensors must be on a CUDA device")
-    h = handle if handle is not None else cached_handle(t.device.index or 0)
-    if h.device != (t.device.index or 0):
-        raise ValueError(f"the handle is on device {h.device}, the tensors on {t.device}")
-    return h
+    index = t.device.index
+    if handle is None:
+        return cached_handle(index)
+    if handle.device != index:
+        raise ValueError(f"the handle is on device {handle.device}, the tensors on {t.device}")
+    return handle
+
+
+def _scalar(name, t, dev) -> int:
+    if t.numel() != 1 or t.dtype != torch.float32 or t.device != dev:
+        raise ValueError(f"{name} must be one float32 element on {dev}")
+    return t.data_ptr()
+
+
+def _workspace_bytes(h: FLCE, N: int, E: int, documents: int) -> int:
+    return int(h.lib.flce_route_workspace_bytes(h.h, N, E, documents))
 
 
 def route(logits: torch.Tensor, k: int, valid=None, offsets=None, renormalize: bool = True,
@@ -119,20 +128,20 @@ def route(logits: torch.Tensor, k: int, valid=None, offsets=None, renormalize: b
     not). offsets: (documents + 1,) int64 ascending from 0 to N, to balance
     each document by itself. renormalize: a token's weights sum to one.
     """
-    check_route_tensors(logits, k, valid, offsets)
+    N, E, ld, code = check_route_tensors(logits, k, valid, offsets)
     h = _handle(logits, handle)
-    N, E = logits.shape
     dev = logits.device
     documents = 1 if offsets is None else offsets.numel() - 1
     r = Routing()
-    r.k, r.renormalize, r.valid, r.offsets = k, renormalize, valid, offsets
-    r.weights = torch.empty((N, k), dtype=torch.float32, device=dev)
-    r.experts = torch.empty((N, k), dtype=torch.int32, device=dev)
-    r.counts = torch.empty((E,) if offsets is None else (documents, E), dtype=torch.int64, device=dev)
-    nbytes = h.lib.flce_route_workspace_bytes(h.h, N, E, documents)
+    r.k, r.renormalize, r.valid, r.offsets = k, bool(renormalize), valid, offsets
+    empty = torch.empty
+    r.weights = empty((N, k), dtype=torch.float32, device=dev)
+    r.experts = empty((N, k), dtype=torch.int32, device=dev)
+    r.counts = empty((E,) if offsets is None else (documents, E), dtype=torch.int64, device=dev)
+    nbytes = _workspace_bytes(h, N, E, documents)
     ws = _state_layout(N, E, documents)[2]
-    r.state = torch.empty(ws + (nbytes + 3) // 4, dtype=torch.float32, device=dev)
-    a = r.bind(logits)
+    r.state = empty(ws + (nbytes + 3) // 4, dtype=torch.float32, device=dev)
+    a = r.bind(logits, N, E, ld, code)
     st = h.lib.flce_route_forward(h.h, ctypes.byref(a), a.result + 4 * ws, nbytes, _stream_ptr(dev))
     if st:
         h._check(st, "flce_route_forward")
@@ -144,27 +153,32 @@ def route_backward(r: Routing, logits: torch.Tensor, d_weights=None, d_balance=N
     """d logits (in the dtype of logits) from the gradients of r.weights
     (N, k) float32, of r.balance and of r.z (one float32 element on the device
     each); None stands for zero. logits are those that r was made from."""
-    check_route_tensors(logits, r.k, r.valid, r.offsets)
+    k = r.k
+    N, E, ld, code = check_route_tensors(logits, k, r.valid, r.offsets)
     h = _handle(logits, handle)
-    N, E = logits.shape
     dev = logits.device
-    if tuple(r.weights.shape) != (N, r.k) or r.counts.shape[-1] != E or r.weights.device != dev:
+    if r.weights.shape != (N, k) or r.counts.shape[-1] != E or r.weights.device != dev:
         raise ValueError("the routing was not made from these logits")
-    if d_weights is not None and (tuple(d_weights.shape) != (N, r.k) or d_weights.dtype != torch.float32
-                                  or d_weights.device != dev or not d_weights.is_contiguous()):
-        raise ValueError(f"d_weights must be contiguous float32 of shape ({N}, {r.k}) on {dev}")
-    for name, g in (("d_balance", d_balance), ("d_z", d_z)):
-        if g is not None and (g.numel() != 1 or g.dtype != torch.float32 or g.device != dev):
-            raise ValueError(f"{name} must be one float32 element on {dev}")
+    p_weights = p_balance = p_z = None
+    if d_weights is not None:
+        if (d_weights.shape != (N, k) or d_weights.dtype != torch.float32 or d_weights.device != dev
+                or not d_weights.is_contiguous()):
+            raise ValueError(f"d_weights must be contiguous float32 of shape ({N}, {k}) on {dev}")
+        p_weights = d_weights.data_ptr()
+    if d_balance is not None:
+        p_balance = _scalar("d_balance", d_balance, dev)
+    if d_z is not None:
+        p_z = _scalar("d_z", d_z, dev)
     if out is None:
         out = torch.empty((N, E), dtype=logits.dtype, device=dev)
-    elif (tuple(out.shape) != (N, E) or out.dtype != logits.dtype or out.device != dev
-          or (E > 1 and N > 0 and out.stride(1) != 1) or (N > 1 and out.stride(0) < E)):
-        raise ValueError(f"out must be {logits.dtype} of shape ({N}, {E}) with contiguous rows on {dev}")
-    a = r.bind(logits)
-    st = h.lib.flce_route_backward(h.h, ctypes.byref(a), None if d_weights is None else d_weights.data_ptr(),
-                                   None if d_balance is None else d_balance.data_ptr(),
-                                   None if d_z is None else d_z.data_ptr(), out.data_ptr(), _row_stride(out),
+        ld_out = E
+    else:
+        if (out.shape != (N, E) or out.dtype != logits.dtype or out.device != dev
+                or (E > 1 and N > 0 and out.stride(1) != 1) or (N > 1 and out.stride(0) < E)):
+            raise ValueError(f"out must be {logits.dtype} of shape ({N}, {E}) with contiguous rows on {dev}")
+        ld_out = _row_stride(out)
+    a = r.bind(logits, N, E, ld, code)
+    st = h.lib.flce_route_backward(h.h, ctypes.byref(a), p_weights, p_balance, p_z, out.data_ptr(), ld_out,
                                    _stream_ptr(dev))
     if st:
         h._check(st, "flce_route_backward")
