@@ -206,7 +206,8 @@ enum {
     FLCE_K_MUON_POLY = 21,       /* B = b A + c A^2 (symmetric) on tcgen05              */
     FLCE_K_MUON_APPLY = 22,      /* X = a X + B X on tcgen05                            */
     FLCE_K_MUON_RESULT = 23,     /* the last step's B X, written as update or weight    */
-    FLCE_K_NUM_KINDS = 24
+    FLCE_K_MUON_SMALL = 24,      /* the whole update of matrices with a side up to 128  */
+    FLCE_K_NUM_KINDS = 25
 };
 
 typedef struct flce_kernel_profile {

@@ -18,8 +18,10 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libflce.so")
 SOURCES = ["flce_api.cu", "flce_umma.cu", "flce_rows.cu", "flce_simt.cu", "flce_static.cu",
-           "flce_route.cu", "flce_muon.cu", "flce_train_api.cu"]
-HEADERS = ["ptx.cuh", "flce_internal.h", "flce_handle.h", "flce_train.h"]
+           "flce_route.cu", "flce_muon.cu", "flce_muon_small.cu",
+           "flce_train_api.cu"]
+HEADERS = ["ptx.cuh", "flce_internal.h", "flce_handle.h", "flce_train.h",
+           "flce_muon.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",

@@ -1188,6 +1188,7 @@ const char* flce_kernel_name(int32_t kind) {
     case FLCE_K_MUON_POLY: return "muon_poly";
     case FLCE_K_MUON_APPLY: return "muon_apply";
     case FLCE_K_MUON_RESULT: return "muon_result";
+    case FLCE_K_MUON_SMALL: return "muon_small";
     default: return "?";
   }
 }

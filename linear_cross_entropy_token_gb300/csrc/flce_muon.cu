@@ -29,79 +29,12 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "flce_internal.h"
-#include "flce_train.h"
-#include "ptx.cuh"
+#include "flce_muon.cuh"
 
 namespace flce {
 namespace {
 
-constexpr uint32_t kAll = 0xFFFFFFFFu;
-constexpr float kXScale = 4096.f;           // hi + lo = 2^12 X
-constexpr float kXInv = 1.f / 4096.f;
-constexpr float kGramScale = 1.f / 4096.f;  // (2^12 X)(2^12 X)t -> 2^12 A
-constexpr float kPolyB = 0.5f;              // 2^12 A -> 2^11 A
-constexpr float kPolyC = 1.f / 8192.f;      // (2^12 A)^2 -> 2^11 A^2
-constexpr float kPolyInv = 1.f / 2048.f;    // 2^11 B -> B; (2^11 B)(2^12 X) -> 2^12 B X
-
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-__device__ __forceinline__ float2 unpack_half2(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-
 // ------------------------------------------------- momentum and norm
-
-__device__ __forceinline__ void load4(const void* p, int dtype, int64_t i, float (&v)[4]) {
-  if (dtype == 1) {
-    const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-  } else {
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i);
-    v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xFFFF0000u);
-    v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xFFFF0000u);
-  }
-}
-
-__device__ __forceinline__ float load1(const void* p, int dtype, int64_t i) {
-  return dtype == 1 ? static_cast<const float*>(p)[i]
-                    : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-
-// The squares of a thread's elements in three ranges of fp32, so that no sum
-// over- or underflows unnoticed; joined in fp64.
-struct SquareSum {
-  float mid = 0.f, big = 0.f, small = 0.f;
-  __device__ __forceinline__ void add(float v) {
-    mid = fmaf(v, v, mid);
-    const float b = v * 0x1p-64f, s = v * 0x1p64f;
-    big = fmaf(b, b, big);
-    small = fmaf(s, s, small);
-  }
-  __device__ __forceinline__ double total() const {
-    if (!(mid <= 3e38f)) return static_cast<double>(big) * 0x1p128;  // inf, or NaN (then big is too)
-    return mid < 0x1p-90f ? static_cast<double>(small) * 0x1p-128 : static_cast<double>(mid);
-  }
-};
-
-// Four elements of u from the gradient (and the momentum, updated in place).
-__device__ __forceinline__ void momentum4(const MuonArgs& a, float4& m, float (&g)[4]) {
-  m.x = m.x * a.beta + g[0] * a.one_minus_beta;
-  m.y = m.y * a.beta + g[1] * a.one_minus_beta;
-  m.z = m.z * a.beta + g[2] * a.one_minus_beta;
-  m.w = m.w * a.beta + g[3] * a.one_minus_beta;
-  if (a.nesterov) {
-    g[0] = m.x * a.beta + g[0] * a.one_minus_beta;
-    g[1] = m.y * a.beta + g[1] * a.one_minus_beta;
-    g[2] = m.z * a.beta + g[2] * a.one_minus_beta;
-    g[3] = m.w * a.beta + g[3] * a.one_minus_beta;
-  } else {
-    g[0] = m.x, g[1] = m.y, g[2] = m.z, g[3] = m.w;
-  }
-}
 
 // One pass over gradient and momentum: bound by HBM (10 or 12 bytes read and
 // written per element). Four vectors of four elements are in flight per
@@ -233,12 +166,7 @@ __global__ void __launch_bounds__(256) muon_prepare_kernel(const __grid_constant
     double s = 0.0;
     for (int i = threadIdx.x; i < a.norm_blocks; i += 32) s += a.norm[blockIdx.y * kMuonNormBlocks + i];
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-    if (threadIdx.x == 0) {
-      const double inv = static_cast<double>(kXScale) / (sqrt(s) + a.eps);
-      // in two factors, so that neither leaves fp32's normal range
-      sh[0] = inv < 1e-30 ? 0x1p-64f : 1.f;
-      sh[1] = static_cast<float>(inv < 1e-30 ? inv * 0x1p64 : inv);
-    }
+    if (threadIdx.x == 0) norm_factors(s, a.eps, sh);
   }
   __syncthreads();
   const float f1 = sh[0], f2 = sh[1];
@@ -252,9 +180,7 @@ __global__ void __launch_bounds__(256) muon_prepare_kernel(const __grid_constant
     for (int q = 0; q < 4; ++q) {
       const float x0 = (a.transposed ? tile[c + 2 * q][r] : tile[r][c + 2 * q]) * f1 * f2;
       const float x1 = (a.transposed ? tile[c + 2 * q + 1][r] : tile[r][c + 2 * q + 1]) * f1 * f2;
-      h[q] = pack_half2(x0, x1);
-      const float2 f = unpack_half2(h[q]);
-      l[q] = pack_half2(x0 - f.x, x1 - f.y);
+      split_half2(x0, x1, h[q], l[q]);
     }
     if (i < a.m && j < a.ldx) {
       const int64_t o = base + static_cast<int64_t>(i) * a.ldx + j;
@@ -299,19 +225,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
       : "memory");
 }
 
-// fp16 operands: the type fields (bits 7-9 and 10-12) are 0
-__host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, uint32_t a_mn, uint32_t b_mn) {
-  return (1u << 4) | (a_mn << 15) | (b_mn << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
-}
-
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
-  const uint64_t t0 = globaltimer_ns();
-#pragma unroll 1
-  while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer_ns() - t0 > timeout_ns) return;
-  }
-}
-
 struct MuonUnit {
   int mat, tm, tn;
 };
@@ -338,42 +251,6 @@ __device__ __forceinline__ MuonUnit muon_unit(int u, int tiles_m, int tiles_n) {
     r.tn = w / tiles_m;
   }
   return r;
-}
-
-__device__ __forceinline__ float to_float(float v) { return v; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float2 to_float2(float2 v) { return v; }
-__device__ __forceinline__ float2 to_float2(__nv_bfloat162 v) { return __bfloat1622float2(v); }
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void put(float2* p, float2 v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat162* p, float2 v) { *p = __floats2bfloat162_rn(v.x, v.y); }
-template <class T>
-struct PairOf;
-template <>
-struct PairOf<float> {
-  using type = float2;
-};
-template <>
-struct PairOf<__nv_bfloat16> {
-  using type = __nv_bfloat162;
-};
-
-// f(T*, W) for the result tensor of a matrix: its element type, whether it is
-// a weight to be updated (true) or the update itself (false), its row stride
-template <class F>
-__device__ __forceinline__ void with_result(const MuonArgs& a, const MuonMat& t, F&& f) {
-  if (t.weight) {
-    if (a.weight_dtype == 1)
-      f(static_cast<float*>(t.weight), std::true_type(), t.ld_weight);
-    else
-      f(static_cast<__nv_bfloat16*>(t.weight), std::true_type(), t.ld_weight);
-  } else {
-    if (a.update_dtype == 1)
-      f(static_cast<float*>(t.update), std::false_type(), t.ld_update);
-    else
-      f(static_cast<__nv_bfloat16*>(t.update), std::false_type(), t.ld_update);
-  }
 }
 
 // `rows` rows of 64 result columns from a warp's staged fp32 tile (columns
@@ -418,25 +295,6 @@ __device__ __forceinline__ void write_rows(T* out, int64_t ld, int rows, int col
       put(q, W ? to_float(q[0]) * decay - lr * o.x : o.x);
       if (c + 1 < cols) put(q + 1, W ? to_float(q[1]) * decay - lr * o.y : o.y);
     }
-  }
-}
-
-// The transpose: the lane's row of 64 values down one column of the result
-// (the lanes' columns are neighbours).
-template <bool W, class T>
-__device__ __forceinline__ void write_columns(T* out, int64_t ld, int rows, float decay, float lr,
-                                              const float (&o)[64]) {
-#pragma unroll
-  for (int r0 = 0; r0 < 64; r0 += 16) {
-    T w[16];
-    if (W) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (r0 + j < rows) w[j] = out[(r0 + j) * ld];
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (r0 + j < rows) put(out + (r0 + j) * ld, W ? to_float(w[j]) * decay - lr * o[r0 + j] : o[r0 + j]);
   }
 }
 
@@ -571,9 +429,7 @@ struct MuonEpilogue {
         if constexpr (PHASE == kMuonApply) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            h[e] = pack_half2(x[2 * e], x[2 * e + 1]);
-            const float2 f = unpack_half2(h[e]);
-            l[e] = pack_half2(x[2 * e] - f.x, x[2 * e + 1] - f.y);
+            split_half2(x[2 * e], x[2 * e + 1], h[e], l[e]);
           }
           q0[j ^ sw] = make_uint4(h[0], h[1], h[2], h[3]);
           q1[j ^ sw] = make_uint4(l[0], l[1], l[2], l[3]);
@@ -743,7 +599,7 @@ __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonA
       if (failed && rank == 0) {
         const uint32_t first = n_issued > kStages ? n_issued - kStages : 0;
         for (uint32_t i = first; i < n_issued; ++i)
-          drain_wait(full_bar(i % kStages), (i / kStages) & 1u, a.timeout_ns);
+          wait_limited(full_bar(i % kStages), (i / kStages) & 1u, a.timeout_ns);
       }
     }
   } else if (warp == 1) {
@@ -794,7 +650,7 @@ __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonA
           tc_commit_pair(drain_bar);
         else
           tc_commit(drain_bar);
-        drain_wait(drain_bar, 0, a.timeout_ns);
+        wait_limited(drain_bar, 0, a.timeout_ns);
       }
     }
   } else {
@@ -848,7 +704,7 @@ __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonA
     // a load that is still in flight lands before the CTA leaves
     if (!ok && MuonEpilogue<PHASE>::kLoads && lane == 0)
       for (; epi.uses < epi.loads; ++epi.uses)
-        drain_wait(epi.bar + 8u * (epi.uses & 1u), (epi.uses >> 1) & 1u, a.timeout_ns);
+        wait_limited(epi.bar + 8u * (epi.uses & 1u), (epi.uses >> 1) & 1u, a.timeout_ns);
   }
 
   __syncwarp();

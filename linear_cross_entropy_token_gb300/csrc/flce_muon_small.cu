@@ -1,0 +1,506 @@
+// The orthogonalised momentum update of matrices whose short side is at most
+// 128, in one launch: momentum, norm, all Newton-Schulz steps and the result.
+// (flce_muon.cu has the formulas and the choice of fp16 parts.)
+//
+// Such a matrix is bound by latency: a step's products take well under a
+// microsecond, and as 17 launches that pass X, A and B through global memory a
+// 128 x 128 matrix took 95 us. Here one cluster of C CTAs holds the matrix on
+// chip from the load to the result, each CTA a slab of up to 256 of its columns:
+//
+//   shared memory  X hi and lo, [64-column chunk][128 rows][128 bytes] with the
+//                  128-byte swizzle; that one copy is the K-major operand of
+//                  X Xt and the MN-major right operand of B X
+//                  A and B, [64-column chunk][128 rows][128 bytes]
+//   TMEM           columns 0..127 the accumulator of X Xt, then of A A;
+//                  columns 128.. the accumulator of B X
+//
+// X Xt sums over the slabs: each CTA sends the rows of its partial product to
+// their owner (128 / C rows each) over distributed shared memory, the owner
+// adds the C parts in order and sends the rounded rows to every CTA. A A and B
+// are the same small work in every CTA. Rows past the short side are zero.
+//
+// 256 threads; thread t works on row 32 (warp % 4) + lane of an accumulator,
+// and on one half of its columns. Every wait is bounded: one that runs out is
+// recorded, and the kernel goes on to its end (no CTA leaves a cluster barrier
+// waiting).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "flce_muon.cuh"
+
+namespace flce {
+namespace {
+
+constexpr int kSmallThreads = 256;
+constexpr uint32_t kChunkBytes = 128 * 128;   // 128 rows x 64 fp16
+constexpr uint32_t kPanelBytes = 2 * kChunkBytes;
+
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d)
+               : "memory");
+}
+__device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
+  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+}
+
+// byte offset of 16-byte chunk j (8 fp16) of row r in a [128 rows][128 bytes] tile
+__device__ __forceinline__ uint32_t tile16(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
+
+template <int NCH>
+__global__ void __launch_bounds__(kSmallThreads, 1)
+    muon_small_kernel(const __grid_constant__ MuonArgs a, const __grid_constant__ MuonSteps steps) {
+  constexpr int kSlab = 64 * NCH;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bar_word;
+  __shared__ uint32_t tmem_slot;
+  __shared__ float diag[128];
+  __shared__ double norm_warp[8], norm_part[16];
+  __shared__ float factor[2];
+
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sHi = smem;
+  uint8_t* sLo = sHi + NCH * kChunkBytes;
+  uint8_t* sA = sLo + NCH * kChunkBytes;
+  uint8_t* sB = sA + kPanelBytes;
+  uint8_t* sR = sB;   // the owner's received rows: read before B is written
+
+  const int C = static_cast<int>(a.cluster);
+  const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const MuonMat& t = a.mat[blockIdx.x / C];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = 32 * (warp & 3) + lane, half = warp >> 2;   // of the accumulators
+  const int slab0 = rank * kSlab;
+  const uint32_t bar = smem_u32(&bar_word);
+  uint32_t parity = 0;
+  auto wait_products = [&] {
+    if (!wait_limited(bar, parity, a.timeout_ns)) *reinterpret_cast<volatile uint32_t*>(a.host_error) = kErrTimeout;
+    parity ^= 1u;
+    tc_fence_after();
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar, 1);
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(&tmem_slot), 512);
+    tmem_relinquish();
+  }
+
+  if (C > 1) cluster_arrive();   // waited for before the first access to another CTA
+
+  // u of the slab into registers: a thread holds 32 neighbouring columns of one
+  // row per chunk. The rows of X are the rows of u, two threads per row, or its
+  // columns, a warp per 32 neighbours: either way global memory sees runs.
+  const int lrow = a.transposed ? (threadIdx.x & 127) : (threadIdx.x >> 1);
+  const int lhalf = a.transposed ? (threadIdx.x >> 7) : (threadIdx.x & 1);
+  float u[NCH][32];
+  SquareSum q;
+#pragma unroll
+  for (int ch = 0; ch < NCH; ++ch) {
+    const int j0 = slab0 + ch * 64 + lhalf * 32;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) u[ch][e] = 0.f;
+    if (lrow < a.m && j0 < a.n) {
+      if (!a.transposed && a.vec) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          if (j0 + e < a.n) {
+            float g[4];
+            load4(t.grad, a.grad_dtype, lrow * t.ld_grad + j0 + e, g);
+            if (t.momentum) {
+              float4* mp = reinterpret_cast<float4*>(t.momentum + lrow * t.ld_momentum + j0 + e);
+              float4 m = *mp;
+              momentum4(a, m, g);
+              *mp = m;
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) u[ch][e + x] = g[x];
+          }
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          if (j0 + e < a.n) {
+            const int64_t r = a.transposed ? j0 + e : lrow, c = a.transposed ? lrow : j0 + e;
+            float g = load1(t.grad, a.grad_dtype, r * t.ld_grad + c);
+            if (t.momentum) {
+              float* mp = t.momentum + r * t.ld_momentum + c;
+              const float m = *mp * a.beta + g * a.one_minus_beta;
+              *mp = m;
+              g = a.nesterov ? m * a.beta + g * a.one_minus_beta : m;
+            }
+            u[ch][e] = g;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 32; ++e) q.add(u[ch][e]);
+  }
+  {
+    double s = q.total();
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+    if (lane == 0) norm_warp[warp] = s;
+  }
+  __syncthreads();
+  if (C > 1) cluster_wait();
+  if (threadIdx.x == 0) {
+    double s = 0.0;
+    for (int w = 0; w < 8; ++w) s += norm_warp[w];
+    if (C == 1) {
+      norm_part[0] = s;
+    } else {
+      for (int c = 0; c < C; ++c) st_cluster_f64(mapa_shared(smem_u32(&norm_part[rank]), c), s);
+    }
+  }
+  if (C > 1) {
+    cluster_sync();
+  } else {
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    double s = 0.0;
+    for (int c = 0; c < C; ++c) s += norm_part[c];
+    norm_factors(s, a.eps, factor);
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem_row = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+  {
+    const float f1 = factor[0], f2 = factor[1];
+#pragma unroll
+    for (int ch = 0; ch < NCH; ++ch) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          split_half2(u[ch][8 * j + 2 * e] * f1 * f2, u[ch][8 * j + 2 * e + 1] * f1 * f2, h[e], l[e]);
+        const uint32_t at = ch * kChunkBytes + tile16(lrow, lhalf * 4 + j);
+        *reinterpret_cast<uint4*>(sHi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(sLo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+      }
+    }
+  }
+  fence_proxy_async_smem();
+  __syncthreads();
+
+  const uint32_t aHi = smem_u32(sHi), aA = smem_u32(sA), aB = smem_u32(sB);
+  for (int k = 0; k < steps.count; ++k) {
+    const float ca = steps.c[k][0], cb = steps.c[k][1], cc = steps.c[k][2];
+    // ---- A = X Xt
+    if (threadIdx.x == 0) {
+      tc_fence_after();
+      constexpr uint32_t idesc = idesc_f16_f32(128, 128, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4 * NCH; ++i) {
+        const uint64_t d = smem_desc_sw128(aHi + (i >> 2) * kChunkBytes + 32u * (i & 3), 16u, 1024u);
+        tc_mma_bf16(tmem, d, d, idesc, i > 0 ? 1u : 0u);
+      }
+      tc_commit(bar);
+    }
+    wait_products();
+    if (C == 1) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint32_t r[32];
+        __syncwarp();
+        tmem_ld_32x32b_x32(tmem_row + half * 64 + g * 32, r);
+        tmem_ld_wait();
+        tmem_regs_ready(r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack_half2(__uint_as_float(r[8 * j + 2 * e]) * kGramScale,
+                              __uint_as_float(r[8 * j + 2 * e + 1]) * kGramScale);
+          *reinterpret_cast<uint4*>(sA + half * kChunkBytes + tile16(row, g * 4 + j)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncthreads();
+    } else {
+      const int own_rows = 128 / C;
+      if (k > 0) cluster_wait();   // every CTA's B X is done with B, where the rows arrive
+      {
+        const int owner = row / own_rows;
+        const uint32_t to = mapa_shared(smem_u32(sR) + (rank * own_rows + row - owner * own_rows) * 512, owner);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld_32x32b_x32(tmem_row + half * 64 + g * 32, r);
+          tmem_ld_wait();
+          tmem_regs_ready(r);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int c16 = half * 16 + g * 8 + j;   // 16-byte chunk of the 512-byte row
+            st_cluster_v4(to + ((c16 ^ (row & 31)) << 4), __uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                          __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
+          }
+        }
+      }
+      tc_fence_before();
+      cluster_sync();
+      for (int i = threadIdx.x; i < own_rows * 32; i += kSmallThreads) {
+        const int r = i >> 5, c16 = i & 31, grow = rank * own_rows + r;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int src = 0; src < C; ++src) {
+          const float4 v =
+              *reinterpret_cast<const float4*>(sR + (src * own_rows + r) * 512 + ((c16 ^ (grow & 31)) << 4));
+          s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+        const uint32_t w0 = pack_half2(s.x * kGramScale, s.y * kGramScale);
+        const uint32_t w1 = pack_half2(s.z * kGramScale, s.w * kGramScale);
+        const uint32_t at = aA + (c16 >> 4) * kChunkBytes + tile16(grow, (c16 & 15) >> 1) + (c16 & 1) * 8;
+        for (int c = 0; c < C; ++c) st_cluster_v2(mapa_shared(at, c), w0, w1);
+      }
+      fence_proxy_async_all();
+      cluster_sync();
+      fence_proxy_async_all();
+      __syncthreads();
+    }
+    // ---- B = b A + c A A
+    if (threadIdx.x == 0) {
+      tc_fence_after();
+      constexpr uint32_t idesc = idesc_f16_f32(128, 128, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint64_t d = smem_desc_sw128(aA + (i >> 2) * kChunkBytes + 32u * (i & 3), 16u, 1024u);
+        tc_mma_bf16(tmem, d, d, idesc, i > 0 ? 1u : 0u);
+      }
+      tc_commit(bar);
+    }
+    wait_products();
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      uint32_t r[32];
+      __syncwarp();
+      tmem_ld_32x32b_x32(tmem_row + half * 64 + g * 32, r);
+      tmem_ld_wait();
+      tmem_regs_ready(r);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t at = half * kChunkBytes + tile16(row, g * 4 + j);
+        const uint4 av = *reinterpret_cast<const uint4*>(sA + at);
+        const uint32_t aw[4] = {av.x, av.y, av.z, av.w};
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack_half2(aw[e]);
+          v[2 * e] = cb * kPolyB * f.x + cc * kPolyC * __uint_as_float(r[8 * j + 2 * e]);
+          v[2 * e + 1] = cb * kPolyB * f.y + cc * kPolyC * __uint_as_float(r[8 * j + 2 * e + 1]);
+        }
+        const int d = row - (half * 64 + g * 32 + 8 * j);   // the diagonal stays in fp32, apart
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (e == d) {
+            diag[row] = v[e] * kPolyInv;
+            v[e] = 0.f;
+          }
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = pack_half2(v[2 * e], v[2 * e + 1]);
+        *reinterpret_cast<uint4*>(sB + at) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    // ---- X = a X + B X
+    if (threadIdx.x == 0) {
+      tc_fence_after();
+      constexpr uint32_t idesc = idesc_f16_f32(128, kSlab, 0, 1);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint64_t da = smem_desc_sw128(aB + (i >> 2) * kChunkBytes + 32u * (i & 3), 16u, 1024u);
+        const uint64_t db = smem_desc_sw128(aHi + 2048u * i, kChunkBytes, 1024u);
+        tc_mma_bf16(tmem + 128, da, db, idesc, i > 0 ? 1u : 0u);
+      }
+      tc_commit(bar);
+    }
+    wait_products();
+    const bool last = k == steps.count - 1;
+    if (C > 1 && !last) cluster_arrive();
+    const float f = ca + diag[row];
+    float o[NCH][32];
+#pragma unroll
+    for (int g = 0; g < NCH; ++g) {   // the thread's half of the slab, 32 columns at a time
+      const int col = half * 32 * NCH + g * 32;
+      uint32_t r[32];
+      __syncwarp();
+      tmem_ld_32x32b_x32(tmem_row + 128 + col, r);
+      tmem_ld_wait();
+      tmem_regs_ready(r);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t at = (col >> 6) * kChunkBytes + tile16(row, ((col & 63) >> 3) + j);
+        const uint4 hv = *reinterpret_cast<const uint4*>(sHi + at), lv = *reinterpret_cast<const uint4*>(sLo + at);
+        uint32_t h[4] = {hv.x, hv.y, hv.z, hv.w}, l[4] = {lv.x, lv.y, lv.z, lv.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 fh = unpack_half2(h[e]), fl = unpack_half2(l[e]);
+          const float x0 = f * (fh.x + fl.x) + __uint_as_float(r[8 * j + 2 * e]) * kPolyInv;
+          const float x1 = f * (fh.y + fl.y) + __uint_as_float(r[8 * j + 2 * e + 1]) * kPolyInv;
+          split_half2(x0, x1, h[e], l[e]);
+          o[g][8 * j + 2 * e] = x0;
+          o[g][8 * j + 2 * e + 1] = x1;
+        }
+        if (!last) {
+          *reinterpret_cast<uint4*>(sHi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(sLo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (!last) continue;
+    // ---- the result
+    const float sc = a.scale * kXInv;
+    if (a.transposed) {
+      if (row < a.m) {
+#pragma unroll
+        for (int g = 0; g < NCH; ++g) {
+          const int j0 = slab0 + half * 32 * NCH + g * 32;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[g][e] *= sc;
+          with_result(a, t, [&](auto* out, auto W, int64_t ld) {
+            write_columns<decltype(W)::value>(out + j0 * ld + row, ld, min(32, a.n - j0), a.decay, a.lr, o[g]);
+          });
+        }
+      }
+    } else {
+      // staged as fp32 [128 rows][slab] where X was (16-byte chunks swizzled by
+      // the row), then row by row, two neighbouring columns per lane
+#pragma unroll
+      for (int g = 0; g < NCH; ++g) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int c16 = (half * 32 * NCH + g * 32) / 4 + j;
+          *reinterpret_cast<float4*>(sHi + row * (kSlab * 4) + ((c16 ^ (row & 7)) << 4)) =
+              make_float4(o[g][4 * j] * sc, o[g][4 * j + 1] * sc, o[g][4 * j + 2] * sc, o[g][4 * j + 3] * sc);
+        }
+      }
+      __syncthreads();
+      const int cols = min(kSlab, a.n - slab0);
+      with_result(a, t, [&](auto* out, auto W, int64_t ld) {
+        for (int c = 2 * lane; c < cols; c += 64) {
+#pragma unroll 4
+          for (int r = warp; r < a.m; r += 8) {
+            const float2 v = *reinterpret_cast<const float2*>(sHi + r * (kSlab * 4) + (((c >> 2) ^ (r & 7)) << 4) +
+                                                              (c & 3) * 4);
+            auto* p = out + r * ld + slab0 + c;
+            constexpr bool kW = decltype(W)::value;
+            if (a.pairs && c + 1 < cols) {
+              using T2 = typename PairOf<std::remove_pointer_t<decltype(p)>>::type;
+              T2* p2 = reinterpret_cast<T2*>(p);
+              float2 w = v;
+              if (kW) {
+                const float2 old = to_float2(*p2);
+                w = make_float2(old.x * a.decay - a.lr * v.x, old.y * a.decay - a.lr * v.y);
+              }
+              put(p2, w);
+            } else {
+              put(p, kW ? to_float(p[0]) * a.decay - a.lr * v.x : v.x);
+              if (c + 1 < cols) put(p + 1, kW ? to_float(p[1]) * a.decay - a.lr * v.y : v.y);
+            }
+          }
+        }
+      });
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int NCH>
+cudaError_t launch_small_t(const MuonArgs& a, const MuonSteps& steps, cudaStream_t s, int* fits) {
+  // X, A, and B or, with a cluster, the rows received for X Xt
+  const size_t smem = 1024 + 2 * NCH * kChunkBytes + kPanelBytes + (a.cluster > 1 ? 2 : 1) * kPanelBytes;
+  auto kern = muon_small_kernel<NCH>;
+  static const cudaError_t opted = [&] {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(1024 + 2 * NCH * kChunkBytes + 3 * kPanelBytes));
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  }();
+  if (opted != cudaSuccess) return opted;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.count * a.cluster);
+  cfg.blockDim = dim3(kSmallThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = a.cluster;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (fits) return cudaOccupancyMaxActiveClusters(fits, kern, &cfg);
+  return cudaLaunchKernelEx(&cfg, kern, a, steps);
+}
+
+cudaError_t launch_small(const MuonArgs& a, const MuonSteps& steps, int chunks, cudaStream_t s, int* fits) {
+  switch (chunks) {
+    case 1: return launch_small_t<1>(a, steps, s, fits);
+    case 2: return launch_small_t<2>(a, steps, s, fits);
+    case 3: return launch_small_t<3>(a, steps, s, fits);
+    default: return launch_small_t<4>(a, steps, s, fits);
+  }
+}
+
+}  // namespace
+
+bool muon_small_shape(int64_t m, int64_t n, int64_t count, int* cluster, int* chunks) {
+  if (m > 128 || n > 16 * 256) return false;
+  // one CTA up to 256 columns (no sum over slabs); else slabs of 256, or of 128
+  // while the clusters then still fit the GPU at once
+  int c = 1;
+  while (c * 256 < n) c *= 2;
+  if (c > 1 && c < 16 && count * c * 2 <= 128) c *= 2;
+  *cluster = c;
+  *chunks = static_cast<int>(((n + c - 1) / c + 63) / 64);
+  return true;
+}
+
+cudaError_t launch_muon_small(const MuonArgs& a, const MuonSteps& steps, int chunks, cudaStream_t s) {
+  return launch_small(a, steps, chunks, s, nullptr);
+}
+
+// Whether a cluster of this size fits the device at all
+bool muon_small_fits(int cluster, int chunks) {
+  MuonArgs a{};
+  a.cluster = cluster;
+  a.count = 1;
+  int n = 0;
+  if (launch_small(a, MuonSteps{}, chunks, nullptr, &n) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return n > 0;
+}
+
+}  // namespace flce

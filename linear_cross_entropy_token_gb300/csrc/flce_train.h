@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/flce.h"
+
 namespace flce {
 
 // ------------------------------------------------------- flce_route.cu
@@ -98,9 +100,16 @@ struct MuonArgs {
   uint16_t* poly;                    // [count][m][lda] fp16, B scaled by 2^11, zero diagonal
   int64_t ldx, lda;
   uint64_t timeout_ns;
+  int32_t cluster;                   // small matrices: CTAs per matrix
 };
 
 enum MuonPhase : int { kMuonGram = 0, kMuonPoly = 1, kMuonApply = 2, kMuonLast = 3 };
+
+// All steps' coefficients, for the kernel that runs them in one launch
+struct MuonSteps {
+  int32_t count;
+  float c[FLCE_MUON_MAX_STEPS][3];
+};
 
 struct MuonStep {
   float a, b, c;                     // X = aX + (bA + cA^2) X
@@ -123,5 +132,10 @@ cudaError_t launch_muon_gemm(int phase, const MuonMaps& maps, const MuonArgs& a,
                              int slots, cudaStream_t s);
 bool muon_pair_tile(int phase, const MuonArgs& a, int pairs, int sms);
 int muon_max_clusters();
+
+// flce_muon_small.cu: matrices whose short side is at most 128, one launch
+bool muon_small_shape(int64_t m, int64_t n, int64_t count, int* cluster, int* chunks);
+bool muon_small_fits(int cluster, int chunks);
+cudaError_t launch_muon_small(const MuonArgs& a, const MuonSteps& steps, int chunks, cudaStream_t s);
 
 }  // namespace flce

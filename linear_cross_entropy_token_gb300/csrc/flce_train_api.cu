@@ -240,6 +240,25 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
   a.lda = z.lda;
   a.timeout_ns = h->timeout_ns;
 
+  const double el = static_cast<double>(q->rows) * q->cols * count, dm = static_cast<double>(z.m), dn = static_cast<double>(z.n);
+  const double gb = static_cast<double>(element_bytes(q->grad_dtype)), mb = mats[0].momentum ? 8.0 : 0.0;
+  const double ob = mats[0].weight ? 2.0 * element_bytes(q->weight_dtype) : 1.0 * element_bytes(q->update_dtype);
+  int cluster, chunks;
+  if (h->cfg.cta_pair == FLCE_CTA_AUTO && muon_small_shape(z.m, z.n, count, &cluster, &chunks)) {
+    auto known = h->muon_small.find({cluster, chunks});
+    if (known == h->muon_small.end())
+      known = h->muon_small.emplace(std::array<int, 2>{cluster, chunks}, muon_small_fits(cluster, chunks)).first;
+    if (known->second) {
+      a.cluster = cluster;
+      MuonSteps steps{};
+      steps.count = q->steps;
+      std::memcpy(steps.c, coefficients, sizeof(float) * 3 * q->steps);
+      FLCE_LAUNCH(FLCE_K_MUON_SMALL, q->steps * count * (dm * (dm + 1) * dn + dm * dm * (dm + 1) + 2 * dm * dm * dn),
+                  el * (gb + mb + ob), launch_muon_small(a, steps, chunks, s));
+      return FLCE_OK;
+    }
+  }
+
   // X as K-major operand (rows of 64 k) and as right operand of B X (64 columns
   // by 64 k); A and B as K-major operands (both symmetric); and what the
   // epilogues read and write
@@ -260,8 +279,6 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
   ok = ok && map_half_3d(&pm, a.poly, z.m, z.m, count, z.lda, 32, 64, &why, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (!ok) return fail(h, FLCE_ERR_CUDA, "%s", why.c_str());
 
-  const double el = static_cast<double>(q->rows) * q->cols * count, dm = static_cast<double>(z.m), dn = static_cast<double>(z.n);
-  const double gb = static_cast<double>(element_bytes(q->grad_dtype)), mb = mats[0].momentum ? 8.0 : 0.0;
   FLCE_LAUNCH(FLCE_K_MUON_MOMENTUM, 0.0, el * (gb + mb), launch_muon_momentum(a, s));
   FLCE_LAUNCH(FLCE_K_MUON_PREPARE, 0.0, el * ((mats[0].momentum ? 4.0 + (q->nesterov ? gb : 0.0) : gb) + 4.0),
               launch_muon_prepare(a, s));

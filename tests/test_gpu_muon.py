@@ -41,6 +41,7 @@ def gaussian(rows, cols, seed, scale=1e-3):
 
 
 SHAPES = [(1, 1), (1, 9), (9, 1), (5, 64), (64, 5), (33, 33), (64, 64), (65, 130), (128, 128), (129, 257), (257, 129),
+          (128, 256), (100, 257), (512, 128), (128, 1024), (1500, 60), (70, 2100), (4096, 128), (128, 4097),
           (256, 256), (300, 1000), (1000, 300), (512, 513), (700, 640), (1024, 96), (72, 5000), (2000, 1100)]
 
 
@@ -55,6 +56,22 @@ def test_orthogonalize_shapes(rows, cols):
     assert got.dtype == torch.bfloat16 and rel(got, want) <= ORTHO + 2.0 ** -8
     got = orthogonalize(G.bfloat16().cuda(), scale=0.5, dtype=torch.float32)
     assert rel(got, newton_schulz(G.bfloat16(), scale=0.5)) <= ORTHO
+
+
+@pytest.mark.parametrize("cta", ["single", "pair"])
+@pytest.mark.parametrize("rows,cols", SHAPES)
+def test_tile_shapes(rows, cols, cta):
+    """The tiled products on either tile shape, for sizes that the one-launch kernel takes too."""
+    from linear_cross_entropy_token_gb300 import FLCE, orthogonalize
+    h = FLCE("bf16", 0, cta=cta)
+    try:
+        G = torch.stack([gaussian(rows, cols, rows * 7 + cols + i) for i in range(2)])
+        got = orthogonalize(G.cuda(), dtype=torch.float32, handle=h)
+        for i in range(2):
+            assert rel(got[i], newton_schulz(G[i])) <= ORTHO
+        h.async_status()
+    finally:
+        h.close()
 
 
 @pytest.mark.parametrize("grad", [torch.float32, torch.bfloat16])
