@@ -97,12 +97,11 @@ __global__ void __launch_bounds__(256) muon_momentum_kernel(const __grid_constan
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  double s = q.total();
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
+  q.reduce_warp();
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = q.total();
   __syncthreads();
   if (threadIdx.x == 0) {
-    s = 0.0;
+    double s = 0.0;
     for (int w = 0; w < 8; ++w) s += sh[w];
     a.norm[blockIdx.y * kMuonNormBlocks + blockIdx.x] = s;
   }
@@ -370,6 +369,7 @@ struct MuonEpilogue {
     auto acc = [&](int i) { return __uint_as_float(i < 32 ? r0[i & 31] : r1[i & 31]); };
     if constexpr (kSym) {
       const int i = row0 + lane;
+      float on_diag = 0.f;
       uint16_t* mir = reinterpret_cast<uint16_t*>(p1) + lane;   // [64][32], its columns are this tile's rows
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -386,15 +386,13 @@ struct MuonEpilogue {
             v[2 * e] = st.b * kPolyB * f.x + st.c * kPolyC * acc(8 * j + 2 * e);
             v[2 * e + 1] = st.b * kPolyB * f.y + st.c * kPolyC * acc(8 * j + 2 * e + 1);
           }
-          const int d = i - (c0 + 8 * j);   // the diagonal stays in fp32, apart
-          if (d >= 0 && d < 8 && i < a.m) {
+          // the diagonal stays in fp32, apart (by selects: a branch per element
+          // costs more than the rest of the epilogue)
+          const int d = i - (c0 + 8 * j);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              if (e == d) {
-                a.diag[static_cast<int64_t>(mat) * a.m + i] = v[e] * kPolyInv;
-                v[e] = 0.f;
-              }
-            }
+          for (int e = 0; e < 8; ++e) {
+            on_diag = e == d ? v[e] : on_diag;
+            v[e] = e == d ? 0.f : v[e];
           }
         }
         uint32_t w[4];
@@ -406,6 +404,8 @@ struct MuonEpilogue {
           for (int e = 0; e < 8; ++e) mir[(8 * j + e) * 32] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
         }
       }
+      if (PHASE == kMuonPoly && i >= c0 && i < c0 + 64 && i < a.m)
+        a.diag[static_cast<int64_t>(mat) * a.m + i] = on_diag * kPolyInv;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {

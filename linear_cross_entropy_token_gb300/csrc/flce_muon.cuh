@@ -62,6 +62,15 @@ struct SquareSum {
     big = fmaf(b, b, big);
     small = fmaf(s, s, small);
   }
+  // the sum over the warp, valid in every lane; fp64 in lane 0's hands alone
+  // (fp64 runs at a sixty-fourth of fp32's rate)
+  __device__ __forceinline__ void reduce_warp() {
+    for (int o = 16; o > 0; o >>= 1) {
+      mid += __shfl_xor_sync(kAll, mid, o);
+      big += __shfl_xor_sync(kAll, big, o);
+      small += __shfl_xor_sync(kAll, small, o);
+    }
+  }
   __device__ __forceinline__ double total() const {
     if (!(mid <= 3e38f)) return static_cast<double>(big) * 0x1p160;  // inf, or NaN (then big is too)
     return mid < 0x1p-90f ? static_cast<double>(small) * 0x1p-160 : static_cast<double>(mid);
@@ -87,6 +96,12 @@ __device__ __forceinline__ void momentum4(const MuonArgs& a, float4& m, float (&
 // The factor 2^12 / (|u| + eps) of X from |u|^2, as two, so that neither leaves
 // fp32's normal range.
 __device__ __forceinline__ void norm_factors(double square_sum, double eps, float* f) {
+  const float s = static_cast<float>(square_sum);
+  if (s > 1e-30f && s < 1e38f) {  // fp32's own square root and quotient: exact to its last bits
+    f[0] = 1.f;
+    f[1] = kXScale / (sqrtf(s) + static_cast<float>(eps));
+    return;
+  }
   const double inv = static_cast<double>(kXScale) / (sqrt(square_sum) + eps);
   f[0] = inv < 1e-30 ? 0x1p-64f : 1.f;
   f[1] = static_cast<float>(inv < 1e-30 ? inv * 0x1p64 : inv);

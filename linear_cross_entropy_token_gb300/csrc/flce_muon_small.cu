@@ -19,8 +19,8 @@
 // adds the C parts in order and sends the rounded rows to every CTA. A A and B
 // are the same small work in every CTA. Rows past the short side are zero.
 //
-// 256 threads; thread t works on row 32 (warp % 4) + lane of an accumulator,
-// and on one half of its columns. Every wait is bounded: one that runs out is
+// 512 threads; thread t works on row 32 (warp % 4) + lane of an accumulator,
+// and on one quarter of its columns. Every wait is bounded: one that runs out is
 // recorded, and the kernel goes on to its end (no CTA leaves a cluster barrier
 // waiting).
 #include <cuda_bf16.h>
@@ -34,7 +34,8 @@
 namespace flce {
 namespace {
 
-constexpr int kSmallThreads = 256;
+constexpr int kSmallThreads = 512;
+constexpr int kSmallWarps = kSmallThreads / 32;
 constexpr uint32_t kChunkBytes = 128 * 128;   // 128 rows x 64 fp16
 constexpr uint32_t kPanelBytes = 2 * kChunkBytes;
 
@@ -54,6 +55,22 @@ __device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
   asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
 }
 
+// 32 lanes x 16 consecutive fp32 columns
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// as tmem_regs_ready: no use of the registers moves above the wait
+__device__ __forceinline__ void tmem_regs_ready16(uint32_t (&r)[16]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+
 // byte offset of 16-byte chunk j (8 fp16) of row r in a [128 rows][128 bytes] tile
 __device__ __forceinline__ uint32_t tile16(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
 
@@ -61,11 +78,12 @@ template <int NCH>
 __global__ void __launch_bounds__(kSmallThreads, 1)
     muon_small_kernel(const __grid_constant__ MuonArgs a, const __grid_constant__ MuonSteps steps) {
   constexpr int kSlab = 64 * NCH;
+  constexpr uint32_t kCols = NCH <= 2 ? 256 : 512;   // TMEM: 128 + the slab
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bar_word;
   __shared__ uint32_t tmem_slot;
   __shared__ float diag[128];
-  __shared__ double norm_warp[8], norm_part[16];
+  __shared__ double norm_warp[kSmallWarps], norm_part[16];
   __shared__ float factor[2];
 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -80,7 +98,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const MuonMat& t = a.mat[blockIdx.x / C];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = 32 * (warp & 3) + lane, half = warp >> 2;   // of the accumulators
+  const int row = 32 * (warp & 3) + lane, quarter = warp >> 2;   // of the accumulators
   const int slab0 = rank * kSlab;
   const uint32_t bar = smem_u32(&bar_word);
   uint32_t parity = 0;
@@ -96,74 +114,91 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     fence_proxy_async_smem();
   }
   if (warp == 0) {
-    tmem_alloc(smem_u32(&tmem_slot), 512);
+    tmem_alloc(smem_u32(&tmem_slot), kCols);
     tmem_relinquish();
   }
 
   if (C > 1) cluster_arrive();   // waited for before the first access to another CTA
 
-  // u of the slab into registers: a thread holds 32 neighbouring columns of one
-  // row per chunk. The rows of X are the rows of u, two threads per row, or its
-  // columns, a warp per 32 neighbours: either way global memory sees runs.
-  const int lrow = a.transposed ? (threadIdx.x & 127) : (threadIdx.x >> 1);
-  const int lhalf = a.transposed ? (threadIdx.x >> 7) : (threadIdx.x & 1);
-  float u[NCH][32];
+  // u of the slab, as fp32, to where X will be. A thread takes 16 neighbouring
+  // columns of one row of X per chunk. The rows of X are the rows of u, four
+  // threads per row, or its columns, a warp per 32 neighbours: either way
+  // global memory sees runs. (The loops are unrolled no further than their
+  // loads need: each instruction runs once or five times, and fetching a
+  // fully unrolled body was the kernel's bound.)
+  const int lrow = a.transposed ? (threadIdx.x & 127) : (threadIdx.x >> 2);
+  const int lq = a.transposed ? (threadIdx.x >> 7) : (threadIdx.x & 3);
+  // fp32 staging: the thread's 16 values of a chunk fill its 32 bytes of the hi
+  // tile and its 32 bytes of the lo tile, so no other thread's
+  auto staged = [&](int ch, int v4) {   // the v4-th of 4 vectors of four
+    return reinterpret_cast<float4*>((v4 < 2 ? sHi : sLo) + ch * kChunkBytes + tile16(lrow, lq * 2 + (v4 & 1)));
+  };
   SquareSum q;
-#pragma unroll
+#pragma unroll 1
   for (int ch = 0; ch < NCH; ++ch) {
-    const int j0 = slab0 + ch * 64 + lhalf * 32;
+    const int j0 = slab0 + ch * 64 + lq * 16;
+    const bool in = lrow < a.m && j0 < a.n;
+    if (!a.transposed && a.vec) {
+      float g[4][4];
+      float4 m[4];
 #pragma unroll
-    for (int e = 0; e < 32; ++e) u[ch][e] = 0.f;
-    if (lrow < a.m && j0 < a.n) {
-      if (!a.transposed && a.vec) {
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          if (j0 + e < a.n) {
-            float g[4];
-            load4(t.grad, a.grad_dtype, lrow * t.ld_grad + j0 + e, g);
-            if (t.momentum) {
-              float4* mp = reinterpret_cast<float4*>(t.momentum + lrow * t.ld_momentum + j0 + e);
-              float4 m = *mp;
-              momentum4(a, m, g);
-              *mp = m;
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x) u[ch][e + x] = g[x];
-          }
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          if (j0 + e < a.n) {
-            const int64_t r = a.transposed ? j0 + e : lrow, c = a.transposed ? lrow : j0 + e;
-            float g = load1(t.grad, a.grad_dtype, r * t.ld_grad + c);
-            if (t.momentum) {
-              float* mp = t.momentum + r * t.ld_momentum + c;
-              const float m = *mp * a.beta + g * a.one_minus_beta;
-              *mp = m;
-              g = a.nesterov ? m * a.beta + g * a.one_minus_beta : m;
-            }
-            u[ch][e] = g;
-          }
+      for (int e = 0; e < 4; ++e) {
+        g[e][0] = g[e][1] = g[e][2] = g[e][3] = 0.f;
+        if (in && j0 + 4 * e < a.n) {
+          load4(t.grad, a.grad_dtype, lrow * t.ld_grad + j0 + 4 * e, g[e]);
+          if (t.momentum) m[e] = *reinterpret_cast<const float4*>(t.momentum + lrow * t.ld_momentum + j0 + 4 * e);
         }
       }
-    }
 #pragma unroll
-    for (int e = 0; e < 32; ++e) q.add(u[ch][e]);
+      for (int e = 0; e < 4; ++e) {
+        if (t.momentum && in && j0 + 4 * e < a.n) {
+          momentum4(a, m[e], g[e]);
+          *reinterpret_cast<float4*>(t.momentum + lrow * t.ld_momentum + j0 + 4 * e) = m[e];
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) q.add(g[e][x]);
+        *staged(ch, e) = make_float4(g[e][0], g[e][1], g[e][2], g[e][3]);
+      }
+    } else {
+      const int64_t step = a.transposed ? 1 : 0;   // along u's rows or columns
+      const int64_t gs = step ? t.ld_grad : 1, ms = step ? t.ld_momentum : 1;
+      const int64_t g0 = step ? j0 * t.ld_grad + lrow : lrow * t.ld_grad + j0;
+      float* m0 = t.momentum + (step ? j0 * t.ld_momentum + lrow : lrow * t.ld_momentum + j0);
+      float g[16], m[16];
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        g[x] = m[x] = 0.f;
+        if (in && j0 + x < a.n) {
+          g[x] = load1(t.grad, a.grad_dtype, g0 + x * gs);
+          if (t.momentum) m[x] = m0[x * ms];
+        }
+      }
+      if (t.momentum) {
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          m[x] = m[x] * a.beta + g[x] * a.one_minus_beta;
+          g[x] = a.nesterov ? m[x] * a.beta + g[x] * a.one_minus_beta : m[x];
+          if (in && j0 + x < a.n) m0[x * ms] = m[x];
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 16; ++x) q.add(g[x]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) *staged(ch, e) = make_float4(g[4 * e], g[4 * e + 1], g[4 * e + 2], g[4 * e + 3]);
+    }
   }
-  {
-    double s = q.total();
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-    if (lane == 0) norm_warp[warp] = s;
-  }
+  q.reduce_warp();
+  if (lane == 0) norm_warp[warp] = q.total();
   __syncthreads();
   if (C > 1) cluster_wait();
   if (threadIdx.x == 0) {
     double s = 0.0;
-    for (int w = 0; w < 8; ++w) s += norm_warp[w];
+#pragma unroll 1
+    for (int w = 0; w < kSmallWarps; ++w) s += norm_warp[w];
     if (C == 1) {
       norm_part[0] = s;
     } else {
+#pragma unroll 1
       for (int c = 0; c < C; ++c) st_cluster_f64(mapa_shared(smem_u32(&norm_part[rank]), c), s);
     }
   }
@@ -174,6 +209,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   }
   if (threadIdx.x == 0) {
     double s = 0.0;
+#pragma unroll 1
     for (int c = 0; c < C; ++c) s += norm_part[c];
     norm_factors(s, a.eps, factor);
   }
@@ -183,15 +219,19 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   const uint32_t tmem_row = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
   {
     const float f1 = factor[0], f2 = factor[1];
+#pragma unroll 1
+    for (int ch = 0; ch < NCH; ++ch) {   // in place: a thread's values lie in its own bytes
+      float4 v[4];
 #pragma unroll
-    for (int ch = 0; ch < NCH; ++ch) {
+      for (int e = 0; e < 4; ++e) v[e] = *staged(ch, e);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 2; ++j) {
         uint32_t h[4], l[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          split_half2(u[ch][8 * j + 2 * e] * f1 * f2, u[ch][8 * j + 2 * e + 1] * f1 * f2, h[e], l[e]);
-        const uint32_t at = ch * kChunkBytes + tile16(lrow, lhalf * 4 + j);
+        split_half2(v[2 * j].x * f1 * f2, v[2 * j].y * f1 * f2, h[0], l[0]);
+        split_half2(v[2 * j].z * f1 * f2, v[2 * j].w * f1 * f2, h[1], l[1]);
+        split_half2(v[2 * j + 1].x * f1 * f2, v[2 * j + 1].y * f1 * f2, h[2], l[2]);
+        split_half2(v[2 * j + 1].z * f1 * f2, v[2 * j + 1].w * f1 * f2, h[3], l[3]);
+        const uint32_t at = ch * kChunkBytes + tile16(lrow, lq * 2 + j);
         *reinterpret_cast<uint4*>(sHi + at) = make_uint4(h[0], h[1], h[2], h[3]);
         *reinterpret_cast<uint4*>(sLo + at) = make_uint4(l[0], l[1], l[2], l[3]);
       }
@@ -201,6 +241,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   __syncthreads();
 
   const uint32_t aHi = smem_u32(sHi), aA = smem_u32(sA), aB = smem_u32(sB);
+#pragma unroll 1
   for (int k = 0; k < steps.count; ++k) {
     const float ca = steps.c[k][0], cb = steps.c[k][1], cc = steps.c[k][2];
     // ---- A = X Xt
@@ -216,23 +257,20 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     }
     wait_products();
     if (C == 1) {
+      uint32_t r[32];
+      __syncwarp();
+      tmem_ld_32x32b_x32(tmem_row + quarter * 32, r);
+      tmem_ld_wait();
+      tmem_regs_ready(r);
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        uint32_t r[32];
-        __syncwarp();
-        tmem_ld_32x32b_x32(tmem_row + half * 64 + g * 32, r);
-        tmem_ld_wait();
-        tmem_regs_ready(r);
+      for (int j = 0; j < 4; ++j) {
+        uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = pack_half2(__uint_as_float(r[8 * j + 2 * e]) * kGramScale,
-                              __uint_as_float(r[8 * j + 2 * e + 1]) * kGramScale);
-          *reinterpret_cast<uint4*>(sA + half * kChunkBytes + tile16(row, g * 4 + j)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        for (int e = 0; e < 4; ++e)
+          w[e] = pack_half2(__uint_as_float(r[8 * j + 2 * e]) * kGramScale,
+                            __uint_as_float(r[8 * j + 2 * e + 1]) * kGramScale);
+        *reinterpret_cast<uint4*>(sA + (quarter >> 1) * kChunkBytes + tile16(row, (quarter & 1) * 4 + j)) =
+            make_uint4(w[0], w[1], w[2], w[3]);
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -243,19 +281,16 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       {
         const int owner = row / own_rows;
         const uint32_t to = mapa_shared(smem_u32(sR) + (rank * own_rows + row - owner * own_rows) * 512, owner);
+        uint32_t r[32];
+        __syncwarp();
+        tmem_ld_32x32b_x32(tmem_row + quarter * 32, r);
+        tmem_ld_wait();
+        tmem_regs_ready(r);
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          uint32_t r[32];
-          __syncwarp();
-          tmem_ld_32x32b_x32(tmem_row + half * 64 + g * 32, r);
-          tmem_ld_wait();
-          tmem_regs_ready(r);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int c16 = half * 16 + g * 8 + j;   // 16-byte chunk of the 512-byte row
-            st_cluster_v4(to + ((c16 ^ (row & 31)) << 4), __uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
-                          __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
-          }
+        for (int j = 0; j < 8; ++j) {
+          const int c16 = quarter * 8 + j;   // 16-byte chunk of the 512-byte row
+          st_cluster_v4(to + ((c16 ^ (row & 31)) << 4), __uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                        __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
         }
       }
       tc_fence_before();
@@ -290,16 +325,16 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       tc_commit(bar);
     }
     wait_products();
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
+    {
       uint32_t r[32];
       __syncwarp();
-      tmem_ld_32x32b_x32(tmem_row + half * 64 + g * 32, r);
+      tmem_ld_32x32b_x32(tmem_row + quarter * 32, r);
       tmem_ld_wait();
       tmem_regs_ready(r);
+      float on_diag = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t at = half * kChunkBytes + tile16(row, g * 4 + j);
+        const uint32_t at = (quarter >> 1) * kChunkBytes + tile16(row, (quarter & 1) * 4 + j);
         const uint4 av = *reinterpret_cast<const uint4*>(sA + at);
         const uint32_t aw[4] = {av.x, av.y, av.z, av.w};
         float v[8];
@@ -309,19 +344,18 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
           v[2 * e] = cb * kPolyB * f.x + cc * kPolyC * __uint_as_float(r[8 * j + 2 * e]);
           v[2 * e + 1] = cb * kPolyB * f.y + cc * kPolyC * __uint_as_float(r[8 * j + 2 * e + 1]);
         }
-        const int d = row - (half * 64 + g * 32 + 8 * j);   // the diagonal stays in fp32, apart
+        const int d = row - (quarter * 32 + 8 * j);   // the diagonal stays in fp32, apart
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          if (e == d) {
-            diag[row] = v[e] * kPolyInv;
-            v[e] = 0.f;
-          }
+          on_diag = e == d ? v[e] : on_diag;
+          v[e] = e == d ? 0.f : v[e];
         }
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] = pack_half2(v[2 * e], v[2 * e + 1]);
         *reinterpret_cast<uint4*>(sB + at) = make_uint4(w[0], w[1], w[2], w[3]);
       }
+      if ((row >> 5) == quarter) diag[row] = on_diag * kPolyInv;
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -342,97 +376,89 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     const bool last = k == steps.count - 1;
     if (C > 1 && !last) cluster_arrive();
     const float f = ca + diag[row];
-    float o[NCH][32];
-#pragma unroll
-    for (int g = 0; g < NCH; ++g) {   // the thread's half of the slab, 32 columns at a time
-      const int col = half * 32 * NCH + g * 32;
-      uint32_t r[32];
+    const float sc = a.scale * kXInv;
+#pragma unroll 1
+    for (int g = 0; g < NCH; ++g) {   // the thread's quarter of the slab, 16 columns at a time
+      const int col = (quarter * NCH + g) * 16;
+      uint32_t r[16];
       __syncwarp();
-      tmem_ld_32x32b_x32(tmem_row + 128 + col, r);
+      tmem_ld_32x32b_x16(tmem_row + 128 + col, r);
+      const uint32_t at0 = (col >> 6) * kChunkBytes + tile16(row, (col & 63) >> 3);
+      const uint32_t at1 = (col >> 6) * kChunkBytes + tile16(row, ((col & 63) >> 3) + 1);
+      const uint4 h0 = *reinterpret_cast<const uint4*>(sHi + at0), h1 = *reinterpret_cast<const uint4*>(sHi + at1);
+      const uint4 l0 = *reinterpret_cast<const uint4*>(sLo + at0), l1 = *reinterpret_cast<const uint4*>(sLo + at1);
+      uint32_t h[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
+      uint32_t l[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
       tmem_ld_wait();
-      tmem_regs_ready(r);
+      tmem_regs_ready16(r);
+      float o[16];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t at = (col >> 6) * kChunkBytes + tile16(row, ((col & 63) >> 3) + j);
-        const uint4 hv = *reinterpret_cast<const uint4*>(sHi + at), lv = *reinterpret_cast<const uint4*>(sLo + at);
-        uint32_t h[4] = {hv.x, hv.y, hv.z, hv.w}, l[4] = {lv.x, lv.y, lv.z, lv.w};
+      for (int e = 0; e < 8; ++e) {
+        const float2 fh = unpack_half2(h[e]), fl = unpack_half2(l[e]);
+        o[2 * e] = f * (fh.x + fl.x) + __uint_as_float(r[2 * e]) * kPolyInv;
+        o[2 * e + 1] = f * (fh.y + fl.y) + __uint_as_float(r[2 * e + 1]) * kPolyInv;
+        split_half2(o[2 * e], o[2 * e + 1], h[e], l[e]);
+      }
+      if (!last) {
+        *reinterpret_cast<uint4*>(sHi + at0) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(sHi + at1) = make_uint4(h[4], h[5], h[6], h[7]);
+        *reinterpret_cast<uint4*>(sLo + at0) = make_uint4(l[0], l[1], l[2], l[3]);
+        *reinterpret_cast<uint4*>(sLo + at1) = make_uint4(l[4], l[5], l[6], l[7]);
+        continue;
+      }
+      // ---- the result
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 fh = unpack_half2(h[e]), fl = unpack_half2(l[e]);
-          const float x0 = f * (fh.x + fl.x) + __uint_as_float(r[8 * j + 2 * e]) * kPolyInv;
-          const float x1 = f * (fh.y + fl.y) + __uint_as_float(r[8 * j + 2 * e + 1]) * kPolyInv;
-          split_half2(x0, x1, h[e], l[e]);
-          o[g][8 * j + 2 * e] = x0;
-          o[g][8 * j + 2 * e + 1] = x1;
-        }
-        if (!last) {
-          *reinterpret_cast<uint4*>(sHi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(sLo + at) = make_uint4(l[0], l[1], l[2], l[3]);
-        }
+      for (int e = 0; e < 16; ++e) o[e] *= sc;
+      const int j0 = slab0 + col, cols = min(16, a.n - j0);
+      if (a.transposed) {
+        if (row < a.m && cols > 0)
+          with_result(a, t, [&](auto* out, auto W, int64_t ld) {
+            write_columns<decltype(W)::value>(out + j0 * ld + row, ld, cols, a.decay, a.lr, o);
+          });
+      } else {
+        // the warp's 32 x 16 block as fp32 where A was (2 KB per warp, 16-byte
+        // chunks swizzled by the row), then two rows at a time, a column per lane
+        float* block = reinterpret_cast<float*>(sA + warp * 2048);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<float4*>(block + lane * 16 + ((j ^ ((lane >> 1) & 3)) << 2)) =
+              make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        __syncwarp();
+        const int rows = min(32, a.m - 32 * (warp & 3));
+        const int c = lane & 15, r1 = lane >> 4;
+        if (c < cols)
+          with_result(a, t, [&](auto* out, auto W, int64_t ld) {
+            constexpr bool kW = decltype(W)::value;
+            auto* p = out + (static_cast<int64_t>(32 * (warp & 3)) + r1) * ld + j0 + c;
+#pragma unroll 1
+            for (int r0 = r1; r0 < rows; r0 += 16, p += 16 * ld) {
+              std::remove_pointer_t<decltype(p)> w[8];
+              if (kW) {
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                  if (r0 + 2 * x < rows) w[x] = p[2 * x * ld];
+              }
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const int rr = r0 + 2 * x;
+                if (rr < rows) {
+                  const float v = block[rr * 16 + (((c >> 2) ^ ((rr >> 1) & 3)) << 2) + (c & 3)];
+                  put(p + 2 * x * ld, kW ? to_float(w[x]) * a.decay - a.lr * v : v);
+                }
+              }
+            }
+          });
+        __syncwarp();
       }
     }
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
-    if (!last) continue;
-    // ---- the result
-    const float sc = a.scale * kXInv;
-    if (a.transposed) {
-      if (row < a.m) {
-#pragma unroll
-        for (int g = 0; g < NCH; ++g) {
-          const int j0 = slab0 + half * 32 * NCH + g * 32;
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[g][e] *= sc;
-          with_result(a, t, [&](auto* out, auto W, int64_t ld) {
-            write_columns<decltype(W)::value>(out + j0 * ld + row, ld, min(32, a.n - j0), a.decay, a.lr, o[g]);
-          });
-        }
-      }
-    } else {
-      // staged as fp32 [128 rows][slab] where X was (16-byte chunks swizzled by
-      // the row), then row by row, two neighbouring columns per lane
-#pragma unroll
-      for (int g = 0; g < NCH; ++g) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int c16 = (half * 32 * NCH + g * 32) / 4 + j;
-          *reinterpret_cast<float4*>(sHi + row * (kSlab * 4) + ((c16 ^ (row & 7)) << 4)) =
-              make_float4(o[g][4 * j] * sc, o[g][4 * j + 1] * sc, o[g][4 * j + 2] * sc, o[g][4 * j + 3] * sc);
-        }
-      }
-      __syncthreads();
-      const int cols = min(kSlab, a.n - slab0);
-      with_result(a, t, [&](auto* out, auto W, int64_t ld) {
-        for (int c = 2 * lane; c < cols; c += 64) {
-#pragma unroll 4
-          for (int r = warp; r < a.m; r += 8) {
-            const float2 v = *reinterpret_cast<const float2*>(sHi + r * (kSlab * 4) + (((c >> 2) ^ (r & 7)) << 4) +
-                                                              (c & 3) * 4);
-            auto* p = out + r * ld + slab0 + c;
-            constexpr bool kW = decltype(W)::value;
-            if (a.pairs && c + 1 < cols) {
-              using T2 = typename PairOf<std::remove_pointer_t<decltype(p)>>::type;
-              T2* p2 = reinterpret_cast<T2*>(p);
-              float2 w = v;
-              if (kW) {
-                const float2 old = to_float2(*p2);
-                w = make_float2(old.x * a.decay - a.lr * v.x, old.y * a.decay - a.lr * v.y);
-              }
-              put(p2, w);
-            } else {
-              put(p, kW ? to_float(p[0]) * a.decay - a.lr * v.x : v.x);
-              if (c + 1 < cols) put(p + 1, kW ? to_float(p[1]) * a.decay - a.lr * v.y : v.y);
-            }
-          }
-        }
-      });
-    }
   }
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, kCols);
   }
 }
 
