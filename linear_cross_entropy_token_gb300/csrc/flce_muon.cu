@@ -191,20 +191,42 @@ __global__ void __launch_bounds__(256) muon_prepare_kernel(const __grid_constant
 
 // ------------------------------------------------------- the products
 
-// Output tiles: 256 x 256 on a CTA pair, 128 x 128 on one CTA
-constexpr int kPairTile = 256, kSingleTile = 128;
-constexpr int kStages = 5;
-constexpr uint32_t kABytes = 128 * kBK * 2;    // 16 KB: a CTA's 128 rows of A
-constexpr uint32_t kBBytes = 128 * kBK * 2;    // 16 KB: its 128 columns of B
-constexpr uint32_t kStageBytes = kABytes + kBBytes;
-// per epilogue warp two buffers of 32 rows x 64 fp16 columns, twice (X hi and
+// Output tiles. SINGLE: 128 x 128 on one CTA. PAIR: 256 x 256 on a CTA pair
+// (tcgen05 cta_group::2, each CTA holding its 128 rows of A and 128 columns of
+// B). WIDE: 256 x 512 on a CTA pair, two products per k-step that share their A
+// operand through the tensor core's collector buffer.
+template <int SHAPE>
+struct MuonTile;
+template <>
+struct MuonTile<kMuonSingle> {
+  static constexpr int kM = 128, kN = 128, kAccs = 2, kStages = 5;
+};
+template <>
+struct MuonTile<kMuonPair> {
+  static constexpr int kM = 256, kN = 256, kAccs = 2, kStages = 5;
+};
+template <>
+struct MuonTile<kMuonWide> {
+  static constexpr int kM = 256, kN = 512, kAccs = 1, kStages = 3;
+};
+
+constexpr uint32_t kPartBytes = 128 * kBK * 2;  // 16 KB: 128 rows or columns of a 64-deep k-block
+constexpr int kThreads = 384;                   // warp 0 loads, warp 1 issues, warps 4..11 run the epilogue
+constexpr int kEpiThreads = 256;
+// per epilogue warp two buffers of 32 rows x 32 fp16 columns, twice (X hi and
 // lo; a tile and its mirror image; one fp32 tile)
-constexpr uint32_t kEpiPart = 32 * 128;
-constexpr uint32_t kEpiBytes = 4 * 2 * 2 * kEpiPart;
-constexpr uint32_t kSmemBytes = 1024 + kStages * kStageBytes + kEpiBytes + (2 * kStages + 5 + 8) * 8 + 16;
-static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-constexpr int kThreads = 192;
-constexpr int kEpiThreads = 128;
+constexpr uint32_t kEpiPart = 32 * 64;
+constexpr uint32_t kEpiBytes = 8 * 2 * 2 * kEpiPart;
+template <int SHAPE>
+constexpr uint32_t stage_bytes() {
+  return (SHAPE == kMuonWide ? 3 : 2) * kPartBytes;
+}
+template <int SHAPE>
+constexpr uint32_t smem_bytes() {
+  return 1024 + MuonTile<SHAPE>::kStages * stage_bytes<SHAPE>() + kEpiBytes + (2 * MuonTile<SHAPE>::kStages + 5 + 16) * 8 +
+         16;
+}
+static_assert(smem_bytes<kMuonSingle>() <= 232448 && smem_bytes<kMuonWide>() <= 232448, "shared memory per CTA");
 
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* m, uint32_t bar, int32_t c0,
                                                  int32_t c1, int32_t c2) {
@@ -228,83 +250,92 @@ struct MuonUnit {
   int mat, tm, tn;
 };
 
-// Work units: per matrix the tiles of the output, for the symmetric products
-// only those with tm <= tn (column by column: column tn has tn + 1 of them).
-template <int PHASE>
+// Work units: per matrix the tiles of the output. Of the symmetric products
+// only the tiles that reach the diagonal or lie above it, column by column:
+// tile column tn has the rows 0 .. R (tn + 1) - 1, R tile rows to a tile
+// column's width, but no more than there are (the last column).
+template <int SHAPE>
+__host__ __device__ __forceinline__ int muon_units_per_matrix(bool sym, int tiles_m, int tiles_n) {
+  if (!sym) return tiles_m * tiles_n;
+  constexpr int R = MuonTile<SHAPE>::kN / MuonTile<SHAPE>::kM;
+  return R * tiles_n * (tiles_n + 1) / 2 - (R * tiles_n - tiles_m);
+}
+
+template <int PHASE, int SHAPE>
 __device__ __forceinline__ MuonUnit muon_unit(int u, int tiles_m, int tiles_n) {
+  constexpr bool kSym = PHASE == kMuonGram || PHASE == kMuonPoly;
+  constexpr int R = MuonTile<SHAPE>::kN / MuonTile<SHAPE>::kM;
+  const int per = muon_units_per_matrix<SHAPE>(kSym, tiles_m, tiles_n);
   MuonUnit r;
-  if (PHASE == kMuonGram || PHASE == kMuonPoly) {
-    const int per = tiles_m * (tiles_m + 1) / 2;
-    r.mat = u / per;
-    const int w = u - r.mat * per;
-    int tn = static_cast<int>((sqrtf(8.f * w + 1.f) - 1.f) * 0.5f);
-    while (tn * (tn + 1) / 2 > w) --tn;
-    while ((tn + 1) * (tn + 2) / 2 <= w) ++tn;
+  r.mat = u / per;
+  const int w = u - r.mat * per;
+  if (kSym) {
+    // columns before tn hold R tn (tn + 1) / 2 tiles
+    int tn = static_cast<int>((sqrtf(8.f / R * w + 1.f) - 1.f) * 0.5f);
+    while (R * tn * (tn + 1) / 2 > w) --tn;
+    while (R * (tn + 1) * (tn + 2) / 2 <= w) ++tn;
     r.tn = tn;
-    r.tm = w - tn * (tn + 1) / 2;
+    r.tm = w - R * tn * (tn + 1) / 2;
   } else {
-    const int per = tiles_m * tiles_n;
-    r.mat = u / per;
-    const int w = u - r.mat * per;
     r.tm = w % tiles_m;
     r.tn = w / tiles_m;
   }
   return r;
 }
 
-// `rows` rows of 64 result columns from a warp's staged fp32 tile (columns
-// 0..31 at p0, 32..63 at p1, 128-byte swizzled), two columns per lane, a row
-// at a time; a weight's eight rows are read before the first is written.
+// `rows` rows of 32 result columns from a warp's staged fp32 block [32][32]
+// (16-byte chunks swizzled by the row): half a warp per row, two columns per
+// lane; a weight's eight rows are read before the first is written.
 template <bool W, class T>
 __device__ __forceinline__ void write_rows(T* out, int64_t ld, int rows, int cols, bool pairs, float decay, float lr,
-                                           const uint8_t* p0, const uint8_t* p1, int lane) {
+                                           const float* block, int lane) {
   using T2 = typename PairOf<T>::type;
-  const int c = 2 * lane;
+  const int c = 2 * (lane & 15), r1 = lane >> 4;
   if (c >= cols) return;
-  const uint8_t* part = lane < 16 ? p0 : p1;
-  const int chunk = (c & 31) >> 2;
   auto staged = [&](int r) {
-    return *reinterpret_cast<const float2*>(part + r * 128 + ((chunk ^ (r & 7)) << 4) + (c & 3) * 4);
+    return *reinterpret_cast<const float2*>(block + r * 32 + (((c >> 2) ^ (r & 7)) << 2) + (c & 3));
   };
-  T* p = out + c;
+  T* p = out + r1 * ld + c;
   if (pairs && c + 1 < cols) {
-    for (int r0 = 0; r0 < rows; r0 += 8) {
+#pragma unroll
+    for (int r0 = 0; r0 < 32; r0 += 16) {
       T2 w[8];
       if (W) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (r0 + j < rows) w[j] = *reinterpret_cast<const T2*>(p + (r0 + j) * ld);
+          if (r0 + r1 + 2 * j < rows) w[j] = *reinterpret_cast<const T2*>(p + (r0 + 2 * j) * ld);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (r0 + j < rows) {
-          float2 o = staged(r0 + j);
+        const int r = r0 + r1 + 2 * j;
+        if (r < rows) {
+          float2 o = staged(r);
           if (W) {
             const float2 v = to_float2(w[j]);
             o = make_float2(v.x * decay - lr * o.x, v.y * decay - lr * o.y);
           }
-          put(reinterpret_cast<T2*>(p + (r0 + j) * ld), o);
+          put(reinterpret_cast<T2*>(p + (r0 + 2 * j) * ld), o);
         }
       }
     }
   } else {
-    for (int r = 0; r < rows; ++r) {
+    for (int r = r1; r < rows; r += 2) {
       const float2 o = staged(r);
-      T* q = p + r * ld;
+      T* q = p + (r - r1) * ld;
       put(q, W ? to_float(q[0]) * decay - lr * o.x : o.x);
       if (c + 1 < cols) put(q + 1, W ? to_float(q[1]) * decay - lr * o.y : o.y);
     }
   }
 }
 
-// The epilogue of one warp: its 32 rows (TMEM lanes) of a tile's 256 columns,
-// in groups of 64. What a group reads (X hi and lo, or A) comes by TMA into the
-// warp's own buffers, one group ahead and for a tile's first group before its
-// products are done; what it writes leaves the same buffers by TMA stores. So
-// global memory sees whole 128-byte rows, and no warp waits for another.
-// Written for the epilogue's bound: with each thread reading and writing its
-// own row in global memory, every access touched 32 lines, and B X of
-// 8 x 1024 x 1024 took 36.8 us where its products need 8.7.
+// The epilogue of one warp: 32 rows (TMEM lanes) of one half of a tile's
+// columns, in groups of 32. What a group reads (X hi and lo, or A) comes by TMA
+// into the warp's own buffers, one group ahead and for a tile's first group
+// before its products are done; what it writes leaves the same buffers by TMA
+// stores. So global memory sees runs of 64 bytes and more, and no warp waits
+// for another. (With each thread reading and writing its own row in global
+// memory every access touched 32 lines: B X of 8 x 1024 x 1024 took 36.8 us,
+// its products 8.7.)
 template <int PHASE>
 struct MuonEpilogue {
   static constexpr bool kSym = PHASE == kMuonGram || PHASE == kMuonPoly;
@@ -333,25 +364,25 @@ struct MuonEpilogue {
     ++loads;
   }
 
-  // the weight's lines of this tile into L2, while its products run
-  __device__ __forceinline__ void prefetch_weight(int mat, int row0, int n0, int tile) {
+  // a weight's lines under this warp's rows and columns into L2, while the
+  // products run
+  __device__ __forceinline__ void prefetch_weight(int mat, int row0, int c0, int width) {
     const MuonMat& t = a.mat[mat];
     if (!t.weight) return;
     const int es = a.weight_dtype == 1 ? 4 : 2;
     const char* w = static_cast<const char*>(t.weight);
-    const int cols = min(tile, a.n - n0), rows = min(32, a.m - row0);
+    const int cols = min(width, a.n - c0), rows = min(32, a.m - row0);
     if (a.transposed) {  // `cols` rows of `rows` elements
       for (int r = lane; r < cols; r += 32)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(w + ((n0 + r) * t.ld_weight + row0) * es));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(w + ((c0 + r) * t.ld_weight + row0) * es));
     } else if (lane < rows) {
-      const char* p = w + ((row0 + lane) * t.ld_weight + n0) * es;
+      const char* p = w + ((row0 + lane) * t.ld_weight + c0) * es;
       for (int b = 0; b < cols * es; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + b));
     }
   }
 
-  // columns c0 .. c0 + 63 of the warp's rows, accumulator values in r0 and r1
-  __device__ __forceinline__ bool group(int mat, int row0, int c0, bool mirror, float factor, const uint32_t (&r0)[32],
-                                        const uint32_t (&r1)[32]) {
+  // columns c0 .. c0 + 31 of the warp's rows, accumulator values in r
+  __device__ __forceinline__ bool group(int mat, int row0, int c0, bool mirror, float factor, const uint32_t (&r)[32]) {
     const uint32_t b = uses & 1u;
     uint8_t* p0 = buf + b * 2 * kEpiPart;
     uint8_t* p1 = p0 + kEpiPart;
@@ -363,16 +394,16 @@ struct MuonEpilogue {
       __syncwarp();
     }
     ++uses;
-    uint4* q0 = reinterpret_cast<uint4*>(p0 + lane * 128);
-    uint4* q1 = reinterpret_cast<uint4*>(p1 + lane * 128);
-    const int sw = lane & 7;   // 16-byte chunk j of a row sits at chunk j ^ (row % 8)
-    auto acc = [&](int i) { return __uint_as_float(i < 32 ? r0[i & 31] : r1[i & 31]); };
+    uint4* q0 = reinterpret_cast<uint4*>(p0 + lane * 64);
+    uint4* q1 = reinterpret_cast<uint4*>(p1 + lane * 64);
+    const int sw = (lane >> 1) & 3;   // 64-byte swizzle: chunk j of a row sits at chunk j ^ (row / 2 % 4)
+    auto acc = [&](int i) { return __uint_as_float(r[i]); };
     if constexpr (kSym) {
       const int i = row0 + lane;
       float on_diag = 0.f;
-      uint16_t* mir = reinterpret_cast<uint16_t*>(p1) + lane;   // [64][32], its columns are this tile's rows
+      uint16_t* mir = reinterpret_cast<uint16_t*>(p1) + lane;   // [32][32], its columns are this tile's rows
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 4; ++j) {
         float v[8];
         if constexpr (PHASE == kMuonGram) {
 #pragma unroll
@@ -404,7 +435,7 @@ struct MuonEpilogue {
           for (int e = 0; e < 8; ++e) mir[(8 * j + e) * 32] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
         }
       }
-      if (PHASE == kMuonPoly && i >= c0 && i < c0 + 64 && i < a.m)
+      if (PHASE == kMuonPoly && i >= c0 && i < c0 + 32 && i < a.m)
         a.diag[static_cast<int64_t>(mat) * a.m + i] = on_diag * kPolyInv;
       fence_proxy_async_smem();
       __syncwarp();
@@ -415,27 +446,22 @@ struct MuonEpilogue {
       }
       __syncwarp();
     } else {
+      float x[32];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 4; ++j) {
         const uint4 wh = q0[j ^ sw], wl = q1[j ^ sw];
         uint32_t h[4] = {wh.x, wh.y, wh.z, wh.w}, l[4] = {wl.x, wl.y, wl.z, wl.w};
-        float x[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 fh = unpack_half2(h[e]), fl = unpack_half2(l[e]);
-          x[2 * e] = factor * (fh.x + fl.x) + acc(8 * j + 2 * e) * kPolyInv;
-          x[2 * e + 1] = factor * (fh.y + fl.y) + acc(8 * j + 2 * e + 1) * kPolyInv;
+          float* y = x + 8 * j + 2 * e;
+          y[0] = factor * (fh.x + fl.x) + acc(8 * j + 2 * e) * kPolyInv;
+          y[1] = factor * (fh.y + fl.y) + acc(8 * j + 2 * e + 1) * kPolyInv;
+          if constexpr (PHASE == kMuonApply) split_half2(y[0], y[1], h[e], l[e]);
         }
         if constexpr (PHASE == kMuonApply) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            split_half2(x[2 * e], x[2 * e + 1], h[e], l[e]);
-          }
           q0[j ^ sw] = make_uint4(h[0], h[1], h[2], h[3]);
           q1[j ^ sw] = make_uint4(l[0], l[1], l[2], l[3]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) out_[8 * j + e] = x[e] * (a.scale * kXInv);
         }
       }
       if constexpr (PHASE == kMuonApply) {
@@ -447,59 +473,61 @@ struct MuonEpilogue {
           bulk_commit_group();
         }
         __syncwarp();
-      } else if (a.transposed) {
-        with_result(a, a.mat[mat], [&](auto* out, auto W, int64_t ld) {
-          if (row0 + lane < a.m)
-            write_columns<decltype(W)::value>(out + c0 * ld + row0 + lane, ld, min(64, a.n - c0), a.decay, a.lr, out_);
-        });
       } else {
-        // as fp32 in place: columns 0..31 where hi was, 32..63 where lo was
-        float4* f0 = reinterpret_cast<float4*>(q0);
-        float4* f1 = reinterpret_cast<float4*>(q1);
+        const float sc = a.scale * kXInv;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          f0[j ^ sw] = make_float4(out_[4 * j], out_[4 * j + 1], out_[4 * j + 2], out_[4 * j + 3]);
-          f1[j ^ sw] = make_float4(out_[32 + 4 * j], out_[33 + 4 * j], out_[34 + 4 * j], out_[35 + 4 * j]);
+        for (int e = 0; e < 32; ++e) x[e] *= sc;
+        if (a.transposed) {
+          // out[c0 + ..][row0 + lane]: the lanes' columns are neighbours
+          with_result(a, a.mat[mat], [&](auto* out, auto W, int64_t ld) {
+            if (row0 + lane < a.m)
+              write_columns<decltype(W)::value>(out + c0 * ld + row0 + lane, ld, min(32, a.n - c0), a.decay, a.lr, x);
+          });
+        } else {
+          // as fp32 where hi and lo were (every lane has read its own)
+          float* block = reinterpret_cast<float*>(p0);
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<float4*>(block + lane * 32 + ((j ^ (lane & 7)) << 2)) =
+                make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+          __syncwarp();
+          with_result(a, a.mat[mat], [&](auto* out, auto W, int64_t ld) {
+            write_rows<decltype(W)::value>(out + row0 * ld + c0, ld, min(32, a.m - row0), min(32, a.n - c0), a.pairs,
+                                           a.decay, a.lr, block, lane);
+          });
+          fence_proxy_async_smem();  // the next load overwrites what was written here
+          __syncwarp();
         }
-        __syncwarp();
-        with_result(a, a.mat[mat], [&](auto* out, auto W, int64_t ld) {
-          write_rows<decltype(W)::value>(out + row0 * ld + c0, ld, min(32, a.m - row0), min(64, a.n - c0), a.pairs,
-                                         a.decay, a.lr, p0, p1, lane);
-        });
-        fence_proxy_async_smem();  // the next load overwrites what was written here
-        __syncwarp();
       }
     }
     return true;
   }
-  float out_[PHASE == kMuonLast ? 64 : 1];
 };
 
-// The persistent kernel of one product. PAIR: CTA pairs on 256 x 256 tiles
-// (tcgen05 cta_group::2, each CTA holding its 128 rows of A and 128 columns of
-// B per 64-deep k-block); else one CTA per 128 x 128 tile, for outputs with too
-// few large tiles to fill the GPU (muon_tile has the rule). The accumulator is
-// double-buffered in TMEM, so that the epilogue of a tile overlaps the next
-// tile's products. Warp 0 loads by TMA, warp 1 issues, warps 2..5 run the
-// epilogue. Every wait is bounded.
+// The persistent kernel of one product. PAIR and SINGLE tiles have two
+// accumulators in TMEM, so that the epilogue of a tile overlaps the next
+// tile's products; a WIDE tile fills TMEM, and the next tile's products wait
+// until its columns have been read. Every wait is bounded.
 //
 // The kernels of a call form a chain of programmatic launches: each starts
 // while its predecessor drains, sets up its barriers and TMEM, and waits for it
 // before its first access to global memory.
-template <int PHASE, bool PAIR>
+template <int PHASE, int SHAPE>
 __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonArgs& a, const MuonStep& st) {
-  constexpr int kTile_ = PAIR ? kPairTile : kSingleTile;
-  constexpr uint32_t kCols = 2 * kTile_;   // TMEM: two accumulators
+  using Tile = MuonTile<SHAPE>;
   constexpr bool kSym = PHASE == kMuonGram || PHASE == kMuonPoly;
+  constexpr bool kPaired = SHAPE != kMuonSingle, kWide = SHAPE == kMuonWide;
   constexpr int BMN = kSym ? 0 : 1;   // X as the right operand is contiguous along its columns
+  constexpr int kStages = Tile::kStages, kAccs = Tile::kAccs;
+  constexpr uint32_t kStageBytes = stage_bytes<SHAPE>();
+  constexpr uint32_t kTmemCols = kAccs * Tile::kN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* sA = smem;
-  uint8_t* sB = smem + kStages * kABytes;
-  uint8_t* sE = sB + kStages * kBBytes;
+  uint8_t* sE = smem + kStages * kStageBytes;   // a stage: A, B (wide: B of either half)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sE + kEpiBytes);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5 + 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5 + 16);
   const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };
@@ -508,16 +536,17 @@ __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonA
   const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
-  const int first_unit = PAIR ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
-  const int unit_step = PAIR ? static_cast<int>(num_clusters_x()) : static_cast<int>(gridDim.x);
+  const uint32_t rank = kPaired ? cluster_ctarank() : 0u;
+  const int first_unit = kPaired ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
+  const int unit_step = kPaired ? static_cast<int>(num_clusters_x()) : static_cast<int>(gridDim.x);
   uint32_t* err = a.ctrl + kCtrlError;
-  auto wait = [&](uint32_t bar, uint32_t parity, uint32_t* e, uint64_t ns) {
-    return PAIR ? mbar_wait_bounded_cluster(bar, parity, e, ns) : mbar_wait_bounded(bar, parity, e, ns);
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    return kPaired ? mbar_wait_bounded_cluster(bar, parity, err, a.timeout_ns)
+                   : mbar_wait_bounded(bar, parity, err, a.timeout_ns);
   };
   // an arrival, when the products issued so far are done, in every CTA of the unit
   auto commit = [&](uint32_t bar) {
-    if (PAIR)
+    if (kPaired)
       tc_commit_pair_multicast(bar, 0x3);
     else
       tc_commit(bar);
@@ -528,36 +557,40 @@ __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonA
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
-    for (int acc = 0; acc < 2; ++acc) {
+    for (int acc = 0; acc < kAccs; ++acc) {
       mbar_init(tfull_bar(acc), 1);
-      mbar_init(tempty_bar(acc), (PAIR ? 2 : 1) * kEpiThreads);
+      mbar_init(tempty_bar(acc), (kPaired ? 2 : 1) * kEpiThreads);
     }
     mbar_init(drain_bar, 1);
-    for (int i = 0; i < 8; ++i) mbar_init(drain_bar + 8u * (1 + i), 1);  // the epilogue warps' loads
+    for (int i = 0; i < 16; ++i) mbar_init(drain_bar + 8u * (1 + i), 1);  // the epilogue warps' loads
     fence_mbar_init();
     fence_proxy_async_smem();
     tma_prefetch_map(&maps.a);
     tma_prefetch_map(&maps.b);
+    tma_prefetch_map(&maps.e0);
+    tma_prefetch_map(&maps.e1);
+    tma_prefetch_map(&maps.o0);
+    tma_prefetch_map(&maps.o1);
   }
   if (warp == 1) {
-    if (PAIR) {
-      tmem_alloc_pair(smem_u32(tmem_slot), kCols);
+    if (kPaired) {
+      tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
       tmem_relinquish_pair();
     } else {
-      tmem_alloc(smem_u32(tmem_slot), kCols);
+      tmem_alloc(smem_u32(tmem_slot), kTmemCols);
       tmem_relinquish();
     }
   }
   __syncthreads();
-  if (PAIR) cluster_sync();
+  if (kPaired) cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  const int tiles_m = (a.m + kTile_ - 1) / kTile_;
-  const int tiles_n = kSym ? tiles_m : (a.n + kTile_ - 1) / kTile_;
-  const int num_units = a.count * (kSym ? tiles_m * (tiles_m + 1) / 2 : tiles_m * tiles_n);
+  const int tiles_m = (a.m + Tile::kM - 1) / Tile::kM;
+  const int tiles_n = ((kSym ? a.m : a.n) + Tile::kN - 1) / Tile::kN;
+  const int num_units = a.count * muon_units_per_matrix<SHAPE>(kSym, tiles_m, tiles_n);
   const int num_kb = ((PHASE == kMuonGram ? a.n : a.m) + kBK - 1) / kBK;
 
   if (warp == 0) {
@@ -565,33 +598,37 @@ __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonA
       uint32_t n_issued = 0;
       bool failed = false;
       for (int u = first_unit; u < num_units && !failed; u += unit_step) {
-        const MuonUnit t = muon_unit<PHASE>(u, tiles_m, tiles_n);
-        const int mA = t.tm * kTile_ + static_cast<int>(rank) * 128;
-        const int nB = t.tn * kTile_ + static_cast<int>(rank) * 128;
+        const MuonUnit t = muon_unit<PHASE, SHAPE>(u, tiles_m, tiles_n);
+        const int mA = t.tm * Tile::kM + static_cast<int>(rank) * 128;
+        const int nB = t.tn * Tile::kN + static_cast<int>(rank) * 128;
         for (int kb = 0; kb < num_kb; ++kb) {
           const int stage = n_issued % kStages;
           const uint32_t phase = (n_issued / kStages) & 1u;
-          if (!wait(empty_bar(stage), phase ^ 1u, err, a.timeout_ns)) {
+          if (!wait(empty_bar(stage), phase ^ 1u)) {
             failed = true;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), (PAIR ? 2 : 1) * kStageBytes);
-          const uint32_t fb = PAIR ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
-          const uint32_t sa = smem_u32(sA + stage * kABytes);
-          const uint32_t sb = smem_u32(sB + stage * kBBytes);
+          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), (kPaired ? 2 : 1) * kStageBytes);
+          const uint32_t fb = kPaired ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
+          const uint32_t sa = smem_u32(smem + stage * kStageBytes);
           const int k0 = kb * kBK;
           auto load = [&](uint32_t dst, const CUtensorMap* m, int c0, int c1) {
-            if (PAIR)
+            if (kPaired)
               tma_load_3d_pair(dst, m, fb, c0, c1, t.mat);
             else
               tma_load_3d(dst, m, fb, c0, c1, t.mat);
           };
           load(sa, &maps.a, k0, mA);
-          if (BMN == 0) {
-            load(sb, &maps.b, k0, nB);
-          } else {
-            load(sb, &maps.b, nB, k0);
-            load(sb + 8192, &maps.b, nB + 64, k0);
+#pragma unroll
+          for (int h = 0; h < (kWide ? 2 : 1); ++h) {
+            const uint32_t sb = sa + (1 + h) * kPartBytes;
+            const int n = nB + 256 * h;
+            if (BMN == 0) {
+              load(sb, &maps.b, k0, n);
+            } else {
+              load(sb, &maps.b, n, k0);
+              load(sb + 8192, &maps.b, n + 64, k0);
+            }
           }
           ++n_issued;
         }
@@ -604,39 +641,45 @@ __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonA
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc = idesc_f16_f32(kTile_, kTile_, 0, BMN);
+      // kind::f16; the descriptor's type fields say fp16
+      constexpr uint32_t idesc = idesc_f16_f32(Tile::kM, kWide ? 256 : Tile::kN, 0, BMN);
       uint32_t n_consumed = 0;
       bool issued = false, failed = false;
       int it = 0;
       for (int u = first_unit; u < num_units && !failed; u += unit_step, ++it) {
-        const int acc = it & 1;
-        const uint32_t acc_phase = (it >> 1) & 1;
-        if (!wait(tempty_bar(acc), acc_phase ^ 1u, err, a.timeout_ns)) {
+        const int acc = it % kAccs;
+        const uint32_t acc_phase = (it / kAccs) & 1;
+        if (!wait(tempty_bar(acc), acc_phase ^ 1u)) {
           failed = true;
           break;
         }
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + acc * kTile_;
+        const uint32_t d_tmem = tmem_base + acc * Tile::kN;
         for (int kb = 0; kb < num_kb; ++kb) {
           const int stage = n_consumed % kStages;
           const uint32_t phase = (n_consumed / kStages) & 1u;
-          if (!wait(full_bar(stage), phase, err, a.timeout_ns)) {
+          if (!wait(full_bar(stage), phase)) {
             failed = true;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(sA + stage * kABytes);
-          const uint32_t sb = smem_u32(sB + stage * kBBytes);
+          const uint32_t sa = smem_u32(smem + stage * kStageBytes);
+          const uint32_t sb = sa + kPartBytes;
 #pragma unroll
           for (int k = 0; k < kBK / 16; ++k) {
+            const uint32_t in = (kb > 0 || k > 0) ? 1u : 0u;
             const uint64_t ad = smem_desc_sw128(sa + 32u * k, 16u, 1024u);
-            const uint64_t bd = BMN ? smem_desc_sw128(sb + 2048u * k, 8192u, 1024u)
-                                    : smem_desc_sw128(sb + 32u * k, 16u, 1024u);
-            // kind::f16: the descriptor's type fields say fp16
-            if (PAIR)
-              tc_mma_bf16_pair(d_tmem, ad, bd, idesc, (kb > 0 || k > 0) ? 1u : 0u);
-            else
-              tc_mma_bf16(d_tmem, ad, bd, idesc, (kb > 0 || k > 0) ? 1u : 0u);
+            auto bdesc = [&](uint32_t at) {
+              return BMN ? smem_desc_sw128(at + 2048u * k, 8192u, 1024u) : smem_desc_sw128(at + 32u * k, 16u, 1024u);
+            };
+            if (kWide) {
+              tc_mma_bf16_pair_a_fill(d_tmem, ad, bdesc(sb), idesc, in);
+              tc_mma_bf16_pair_a_lastuse(d_tmem + 256, ad, bdesc(sb + kPartBytes), idesc, in);
+            } else if (kPaired) {
+              tc_mma_bf16_pair(d_tmem, ad, bdesc(sb), idesc, in);
+            } else {
+              tc_mma_bf16(d_tmem, ad, bdesc(sb), idesc, in);
+            }
           }
           issued = true;
           commit(empty_bar(stage));
@@ -646,37 +689,44 @@ __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonA
         commit(tfull_bar(acc));
       }
       if (failed && issued) {
-        if (PAIR)
+        if (kPaired)
           tc_commit_pair(drain_bar);
         else
           tc_commit(drain_bar);
         wait_limited(drain_bar, 0, a.timeout_ns);
       }
     }
-  } else {
-    const int wq = warp & 3;
-    MuonEpilogue<PHASE> epi{a, maps, st, sE + wq * 4 * kEpiPart, drain_bar + 8u * (1 + 2 * wq), lane};
+  } else if (warp >= 4) {
+    constexpr int kHalf = Tile::kN / 2;                     // columns of an epilogue warp
+    constexpr int kBlock = SHAPE == kMuonSingle ? 128 : 256;  // the symmetric products' unit of "above the diagonal"
+    const int wq = warp & 3, half = (warp - 4) >> 2;
+    MuonEpilogue<PHASE> epi{a, maps, st, sE + (warp - 4) * 4 * kEpiPart, drain_bar + 8u * (1 + 2 * (warp - 4)), lane};
     const int ncols = kSym ? a.m : a.n;
     bool ok = true;
     int it = 0;
     for (int u = first_unit; u < num_units; u += unit_step, ++it) {
-      const int acc = it & 1;
-      const uint32_t acc_phase = (it >> 1) & 1;
-      const MuonUnit t = muon_unit<PHASE>(u, tiles_m, tiles_n);
-      const int row0 = t.tm * kTile_ + static_cast<int>(rank) * 128 + wq * 32, n0 = t.tn * kTile_;
-      // this warp's groups of 64 columns that hold any of the output
-      const int groups = row0 < a.m ? min(kTile_ / 64, (ncols - n0 + 63) / 64) : 0;
+      const int acc = it % kAccs;
+      const uint32_t acc_phase = (it / kAccs) & 1;
+      const MuonUnit t = muon_unit<PHASE, SHAPE>(u, tiles_m, tiles_n);
+      const int row0 = t.tm * Tile::kM + static_cast<int>(rank) * 128 + wq * 32;
+      const int col0 = t.tn * Tile::kN + half * kHalf;
+      // below the diagonal blocks a tile of a symmetric product repeats what
+      // another tile mirrors
+      const int block_m = t.tm * Tile::kM / kBlock, block_n = col0 / kBlock;
+      const bool skip = row0 >= a.m || col0 >= ncols || (kSym && block_n < block_m);
+      const int groups = skip ? 0 : min(kHalf / 32, (ncols - col0 + 31) / 32);
       float factor = 0.f;
       if (groups > 0) {
-        epi.load(t.mat, row0, n0);
+        epi.load(t.mat, row0, col0);
         if (!kSym && row0 + lane < a.m) factor = st.a + a.diag[static_cast<int64_t>(t.mat) * a.m + row0 + lane];
+        if (PHASE == kMuonLast) epi.prefetch_weight(t.mat, row0, col0, kHalf);
       }
-      if (PHASE == kMuonLast && groups > 0) epi.prefetch_weight(t.mat, row0, n0, kTile_);
-      ok = wait(tfull_bar(acc), acc_phase, err, a.timeout_ns);
+      ok = wait(tfull_bar(acc), acc_phase);
       ok = __all_sync(kAll, ok);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(wq * 32) << 16) + acc * kTile_;
+      const uint32_t tbase =
+          tmem_base + (static_cast<uint32_t>(wq * 32) << 16) + acc * Tile::kN + half * kHalf;
       auto release = [&] {
         tc_fence_before();
         if (rank == 0)
@@ -688,15 +738,13 @@ __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonA
 #pragma unroll 1
       for (int g = 0; g < groups && ok; ++g) {
         __syncwarp();
-        uint32_t r0[32], r1[32];
-        tmem_ld_32x32b_x32(tbase + g * 64, r0);
-        tmem_ld_32x32b_x32(tbase + g * 64 + 32, r1);
-        if (g + 1 < groups) epi.load(t.mat, row0, n0 + (g + 1) * 64);
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tbase + g * 32, r);
+        if (g + 1 < groups) epi.load(t.mat, row0, col0 + (g + 1) * 32);
         tmem_ld_wait();
-        tmem_regs_ready(r0);
-        tmem_regs_ready(r1);
+        tmem_regs_ready(r);
         if (g == groups - 1) release();
-        ok = epi.group(t.mat, row0, n0 + g * 64, kSym && t.tm != t.tn, factor, r0, r1);
+        ok = epi.group(t.mat, row0, col0 + g * 32, kSym && block_n > block_m, factor, r);
       }
       if (!ok) break;
     }
@@ -709,13 +757,13 @@ __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonA
 
   __syncwarp();
   __syncthreads();
-  if (PAIR) cluster_sync();
+  if (kPaired) cluster_sync();
   if (warp == 1) {
     tc_fence_after();
-    if (PAIR)
-      tmem_dealloc_pair(tmem_base, kCols);
+    if (kPaired)
+      tmem_dealloc_pair(tmem_base, kTmemCols);
     else
-      tmem_dealloc(tmem_base, kCols);
+      tmem_dealloc(tmem_base, kTmemCols);
   }
   if (threadIdx.x == 0) {
     const uint32_t code = ld_volatile_u32(err);
@@ -723,23 +771,25 @@ __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonA
   }
 }
 
-template <int PHASE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    muon_pair_kernel(const __grid_constant__ MuonMaps maps, const __grid_constant__ MuonArgs a,
+template <int PHASE, int SHAPE>
+__global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bounds__(kThreads, 1)
+    muon_gemm_kernel(const __grid_constant__ MuonMaps maps, const __grid_constant__ MuonArgs a,
                      const __grid_constant__ MuonStep st) {
-  muon_gemm_body<PHASE, true>(maps, a, st);
+  muon_gemm_body<PHASE, SHAPE>(maps, a, st);
 }
 
-template <int PHASE>
-__global__ void __launch_bounds__(kThreads, 1)
-    muon_single_kernel(const __grid_constant__ MuonMaps maps, const __grid_constant__ MuonArgs a,
-                       const __grid_constant__ MuonStep st) {
-  muon_gemm_body<PHASE, false>(maps, a, st);
+template <int SHAPE>
+int64_t muon_units_t(int phase, const MuonArgs& a) {
+  using Tile = MuonTile<SHAPE>;
+  const bool sym = phase == kMuonGram || phase == kMuonPoly;
+  const int tm = (a.m + Tile::kM - 1) / Tile::kM, tn = ((sym ? a.m : a.n) + Tile::kN - 1) / Tile::kN;
+  return static_cast<int64_t>(a.count) * muon_units_per_matrix<SHAPE>(sym, tm, tn);
 }
 
-int64_t muon_units(int phase, const MuonArgs& a, int tile) {
-  const int64_t tm = (a.m + tile - 1) / tile, tn = (a.n + tile - 1) / tile;
-  return a.count * (phase == kMuonGram || phase == kMuonPoly ? tm * (tm + 1) / 2 : tm * tn);
+int64_t muon_units(int phase, const MuonArgs& a, int shape) {
+  return shape == kMuonSingle ? muon_units_t<kMuonSingle>(phase, a)
+         : shape == kMuonPair ? muon_units_t<kMuonPair>(phase, a)
+                              : muon_units_t<kMuonWide>(phase, a);
 }
 
 // A launch that may start while the one before it drains
@@ -758,32 +808,38 @@ cudaError_t launch_chained(void (*kern)(P...), dim3 grid, int threads, size_t sm
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+template <int PHASE, int SHAPE>
+cudaError_t launch_product(const MuonMaps& maps, const MuonArgs& a, const MuonStep& st, int slots, cudaStream_t s) {
+  auto kern = muon_gemm_kernel<PHASE, SHAPE>;
+  static const cudaError_t opted = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                        static_cast<int>(smem_bytes<SHAPE>()));
+  if (opted != cudaSuccess) return opted;
+  const int n = static_cast<int>(std::min<int64_t>(muon_units_t<SHAPE>(PHASE, a), slots));
+  return launch_chained(kern, dim3(SHAPE == kMuonSingle ? n : 2 * n), kThreads, smem_bytes<SHAPE>(), s, maps, a, st);
+}
+
 template <int PHASE>
-cudaError_t launch_phase(const MuonMaps& maps, const MuonArgs& a, const MuonStep& st, bool pair, int slots,
+cudaError_t launch_phase(int shape, const MuonMaps& maps, const MuonArgs& a, const MuonStep& st, int slots,
                          cudaStream_t s) {
-  static const cudaError_t opted[2] = {
-      cudaFuncSetAttribute(muon_single_kernel<PHASE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(kSmemBytes)),
-      cudaFuncSetAttribute(muon_pair_kernel<PHASE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(kSmemBytes))};
-  if (opted[pair] != cudaSuccess) return opted[pair];
-  const int64_t units = muon_units(PHASE, a, pair ? kPairTile : kSingleTile);
-  const int n = static_cast<int>(units < slots ? units : slots);
-  return pair ? launch_chained(muon_pair_kernel<PHASE>, dim3(2 * n), kThreads, kSmemBytes, s, maps, a, st)
-              : launch_chained(muon_single_kernel<PHASE>, dim3(n), kThreads, kSmemBytes, s, maps, a, st);
+  return shape == kMuonSingle ? launch_product<PHASE, kMuonSingle>(maps, a, st, slots, s)
+         : shape == kMuonPair ? launch_product<PHASE, kMuonPair>(maps, a, st, slots, s)
+                              : launch_product<PHASE, kMuonWide>(maps, a, st, slots, s);
 }
 
 }  // namespace
 
 // Which tile a product runs on: the one whose rounds of tiles over the GPU take
-// less time. A tile costs its k-blocks (clocks per 64-deep k-block) or its
-// epilogue, whichever is longer, and a fixed start.
-bool muon_pair_tile(int phase, const MuonArgs& a, int pairs, int sms) {
+// least. A tile costs its k-blocks (clocks per 64-deep k-block) or its
+// epilogue, whichever is longer (a wide tile both: it has one accumulator), and
+// a launch the time to fill and drain.
+int muon_tile(int phase, const MuonArgs& a, int pairs, int sms) {
   const int64_t kb = ((phase == kMuonGram ? a.n : a.m) + kBK - 1) / kBK;
-  const int64_t rp = (muon_units(phase, a, kPairTile) + pairs - 1) / pairs;
-  const int64_t rs = (muon_units(phase, a, kSingleTile) + sms - 1) / sms;
-  const int64_t pair = rp * std::max<int64_t>(kb * 530, 6000), single = rs * std::max<int64_t>(kb * 300, 3000);
-  return pair <= single;
+  auto rounds = [&](int shape, int slots) { return (muon_units(phase, a, shape) + slots - 1) / slots; };
+  const int64_t single = rounds(kMuonSingle, sms) * std::max<int64_t>(kb * 450, 2500);
+  const int64_t pair = rounds(kMuonPair, pairs) * std::max<int64_t>(kb * 700, 4000);
+  const int64_t wide = rounds(kMuonWide, pairs) * (kb * 1100 + 4000);
+  if (single <= pair && single <= wide) return kMuonSingle;
+  return pair <= wide ? kMuonPair : kMuonWide;
 }
 
 cudaError_t launch_muon_momentum(const MuonArgs& a, cudaStream_t s) {
@@ -796,23 +852,24 @@ cudaError_t launch_muon_prepare(const MuonArgs& a, cudaStream_t s) {
   return launch_chained(muon_prepare_kernel, dim3(tiles, a.count), 256, 0, s, a);
 }
 
-cudaError_t launch_muon_gemm(int phase, const MuonMaps& maps, const MuonArgs& a, const MuonStep& st, bool pair,
+cudaError_t launch_muon_gemm(int phase, int shape, const MuonMaps& maps, const MuonArgs& a, const MuonStep& st,
                              int slots, cudaStream_t s) {
   switch (phase) {
-    case kMuonGram: return launch_phase<kMuonGram>(maps, a, st, pair, slots, s);
-    case kMuonPoly: return launch_phase<kMuonPoly>(maps, a, st, pair, slots, s);
-    case kMuonApply: return launch_phase<kMuonApply>(maps, a, st, pair, slots, s);
-    case kMuonLast: return launch_phase<kMuonLast>(maps, a, st, pair, slots, s);
+    case kMuonGram: return launch_phase<kMuonGram>(shape, maps, a, st, slots, s);
+    case kMuonPoly: return launch_phase<kMuonPoly>(shape, maps, a, st, slots, s);
+    case kMuonApply: return launch_phase<kMuonApply>(shape, maps, a, st, slots, s);
+    case kMuonLast: return launch_phase<kMuonLast>(shape, maps, a, st, slots, s);
     default: return cudaErrorInvalidValue;
   }
 }
 
-// Clusters of two that fit on the device at once
+// CTA pairs that fit on the device at once (the three shapes take an SM each)
 int muon_max_clusters() {
+  auto kern = muon_gemm_kernel<kMuonApply, kMuonPair>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = smem_bytes<kMuonPair>();
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = 2;
@@ -820,10 +877,9 @@ int muon_max_clusters() {
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  auto kern = muon_pair_kernel<kMuonApply>;
   int n = 0;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)) !=
-          cudaSuccess ||
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem_bytes<kMuonPair>())) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;

@@ -103,6 +103,8 @@ struct MuonArgs {
   int32_t cluster;                   // small matrices: CTAs per matrix
 };
 
+enum MuonTileShape : int { kMuonSingle = 0, kMuonPair = 1, kMuonWide = 2 };
+
 enum MuonPhase : int { kMuonGram = 0, kMuonPoly = 1, kMuonApply = 2, kMuonLast = 3 };
 
 // All steps' coefficients, for the kernel that runs them in one launch
@@ -116,8 +118,7 @@ struct MuonStep {
   int32_t src;                       // hi[src] holds X; the next X goes to hi[1 - src]
 };
 
-// TMA descriptors of one product. Epilogue boxes: 64 columns x 32 rows, for a
-// mirror image 32 x 64.
+// TMA descriptors of one product. Epilogue boxes: 32 columns x 32 rows.
 struct MuonMaps {
   CUtensorMap a, b;                  // operands
   CUtensorMap e0, e1;                // read by the epilogue: A, or X hi and lo (lo also written)
@@ -126,11 +127,11 @@ struct MuonMaps {
 
 cudaError_t launch_muon_momentum(const MuonArgs& a, cudaStream_t s);
 cudaError_t launch_muon_prepare(const MuonArgs& a, cudaStream_t s);
-// One product on CTA-pair tiles (slots: pairs that fit at once) or single-CTA
-// tiles (slots: SMs); muon_pair_tile picks.
-cudaError_t launch_muon_gemm(int phase, const MuonMaps& maps, const MuonArgs& a, const MuonStep& st, bool pair,
+// One product on tiles of one shape (slots: CTA pairs that fit at once, or SMs
+// for single tiles); muon_tile picks the shape.
+cudaError_t launch_muon_gemm(int phase, int shape, const MuonMaps& maps, const MuonArgs& a, const MuonStep& st,
                              int slots, cudaStream_t s);
-bool muon_pair_tile(int phase, const MuonArgs& a, int pairs, int sms);
+int muon_tile(int phase, const MuonArgs& a, int pairs, int sms);
 int muon_max_clusters();
 
 // flce_muon_small.cu: matrices whose short side is at most 128, one launch

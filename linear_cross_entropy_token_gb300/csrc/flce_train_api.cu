@@ -244,7 +244,7 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
   const double gb = static_cast<double>(element_bytes(q->grad_dtype)), mb = mats[0].momentum ? 8.0 : 0.0;
   const double ob = mats[0].weight ? 2.0 * element_bytes(q->weight_dtype) : 1.0 * element_bytes(q->update_dtype);
   int cluster, chunks;
-  if (h->cfg.cta_pair == FLCE_CTA_AUTO && muon_small_shape(z.m, z.n, count, &cluster, &chunks)) {
+  if (h->muon_shape < 0 && muon_small_shape(z.m, z.n, count, &cluster, &chunks)) {
     auto known = h->muon_small.find({cluster, chunks});
     if (known == h->muon_small.end())
       known = h->muon_small.emplace(std::array<int, 2>{cluster, chunks}, muon_small_fits(cluster, chunks)).first;
@@ -268,15 +268,15 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
   for (int i = 0; i < 2; ++i) {
     ok = ok && map_half_3d(&xk[i], a.hi[i], z.n, z.m, count, z.ldx, 64, 128, &why);
     ok = ok && map_half_3d(&xn[i], a.hi[i], z.n, z.m, count, z.ldx, 64, 64, &why);
-    ok = ok && map_half_3d(&xe[i], a.hi[i], z.n, z.m, count, z.ldx, 64, 32, &why);
+    ok = ok && map_half_3d(&xe[i], a.hi[i], z.n, z.m, count, z.ldx, 32, 32, &why, CU_TENSOR_MAP_SWIZZLE_64B);
   }
-  ok = ok && map_half_3d(&lo, a.lo, z.n, z.m, count, z.ldx, 64, 32, &why);
+  ok = ok && map_half_3d(&lo, a.lo, z.n, z.m, count, z.ldx, 32, 32, &why, CU_TENSOR_MAP_SWIZZLE_64B);
   ok = ok && map_half_3d(&gk, a.gram, z.m, z.m, count, z.lda, 64, 128, &why);
-  ok = ok && map_half_3d(&ge, a.gram, z.m, z.m, count, z.lda, 64, 32, &why);
-  ok = ok && map_half_3d(&gm, a.gram, z.m, z.m, count, z.lda, 32, 64, &why, CU_TENSOR_MAP_SWIZZLE_NONE);
+  ok = ok && map_half_3d(&ge, a.gram, z.m, z.m, count, z.lda, 32, 32, &why, CU_TENSOR_MAP_SWIZZLE_64B);
+  ok = ok && map_half_3d(&gm, a.gram, z.m, z.m, count, z.lda, 32, 32, &why, CU_TENSOR_MAP_SWIZZLE_NONE);
   ok = ok && map_half_3d(&pk, a.poly, z.m, z.m, count, z.lda, 64, 128, &why);
-  ok = ok && map_half_3d(&pe, a.poly, z.m, z.m, count, z.lda, 64, 32, &why);
-  ok = ok && map_half_3d(&pm, a.poly, z.m, z.m, count, z.lda, 32, 64, &why, CU_TENSOR_MAP_SWIZZLE_NONE);
+  ok = ok && map_half_3d(&pe, a.poly, z.m, z.m, count, z.lda, 32, 32, &why, CU_TENSOR_MAP_SWIZZLE_64B);
+  ok = ok && map_half_3d(&pm, a.poly, z.m, z.m, count, z.lda, 32, 32, &why, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (!ok) return fail(h, FLCE_ERR_CUDA, "%s", why.c_str());
 
   FLCE_LAUNCH(FLCE_K_MUON_MOMENTUM, 0.0, el * (gb + mb), launch_muon_momentum(a, s));
@@ -284,11 +284,8 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
               launch_muon_prepare(a, s));
   // the handle's tile shape where it was given one, else by the rule
   auto product = [&](int phase, const MuonMaps& maps, const MuonStep& st) {
-    const int mode = h->cfg.cta_pair;
-    const bool pair = mode == FLCE_CTA_SINGLE ? false
-                      : h->muon_tile_fixed    ? true
-                                              : muon_pair_tile(phase, a, h->muon_clusters, h->num_sms);
-    return launch_muon_gemm(phase, maps, a, st, pair, pair ? h->muon_clusters : h->num_sms, s);
+    const int shape = h->muon_shape >= 0 ? h->muon_shape : muon_tile(phase, a, h->muon_clusters, h->num_sms);
+    return launch_muon_gemm(phase, shape, maps, a, st, shape == kMuonSingle ? h->num_sms : h->muon_clusters, s);
   };
   for (int k = 0; k < q->steps; ++k) {
     MuonStep st;

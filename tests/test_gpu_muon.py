@@ -58,10 +58,10 @@ def test_orthogonalize_shapes(rows, cols):
     assert rel(got, newton_schulz(G.bfloat16(), scale=0.5)) <= ORTHO
 
 
-@pytest.mark.parametrize("cta", ["single", "pair"])
+@pytest.mark.parametrize("cta", ["single", "pair", "wide"])
 @pytest.mark.parametrize("rows,cols", SHAPES)
 def test_tile_shapes(rows, cols, cta):
-    """The tiled products on either tile shape, for sizes that the one-launch kernel takes too."""
+    """The tiled products on each tile shape, for sizes that the one-launch kernel takes too."""
     from linear_cross_entropy_token_gb300 import FLCE, orthogonalize
     h = FLCE("bf16", 0, cta=cta)
     try:
