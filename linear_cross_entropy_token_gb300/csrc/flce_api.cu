@@ -1218,7 +1218,10 @@ flce_status flce_create(flce_handle_t* out, const flce_config* cfg) {
   if (prop.sharedMemPerBlockOptin < static_cast<size_t>(umma_smem_bytes())) return FLCE_ERR_UNSUPPORTED;
   flce_handle_t h = new flce_handle_s();
   h->cfg = *cfg;
-  h->muon_shape = cfg->cta_pair == FLCE_CTA_SINGLE ? 0 : cfg->cta_pair == FLCE_CTA_PAIR ? 1 : cfg->cta_pair == FLCE_CTA_WIDE ? 2 : -1;
+  h->muon_shape = cfg->cta_pair == FLCE_CTA_SINGLE ? 0
+                  : cfg->cta_pair == FLCE_CTA_PAIR ? 1
+                  : cfg->cta_pair == FLCE_CTA_WIDE ? 2
+                                                   : -1;
   h->device = cfg->device;
   h->num_sms = prop.multiProcessorCount;
   h->timeout_ns = static_cast<uint64_t>(cfg->timeout_ms > 0 ? cfg->timeout_ms : 2000) * 1000000ull;

@@ -223,8 +223,8 @@ constexpr uint32_t stage_bytes() {
 }
 template <int SHAPE>
 constexpr uint32_t smem_bytes() {
-  return 1024 + MuonTile<SHAPE>::kStages * stage_bytes<SHAPE>() + kEpiBytes + (2 * MuonTile<SHAPE>::kStages + 5 + 16) * 8 +
-         16;
+  constexpr int stages = MuonTile<SHAPE>::kStages;
+  return 1024 + stages * stage_bytes<SHAPE>() + kEpiBytes + (2 * stages + 5 + 16) * 8 + 16;
 }
 static_assert(smem_bytes<kMuonSingle>() <= 232448 && smem_bytes<kMuonWide>() <= 232448, "shared memory per CTA");
 

@@ -20,6 +20,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "flce_train.h"
@@ -177,13 +178,15 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 template <class T, int G, int NPL, bool ONE>
 __global__ void __launch_bounds__(kRouteThreads) route_forward_kernel(const RouteArgs a) {
   constexpr int RPW = 32 / G;          // rows a warp holds at once
+  constexpr int kTurns = RPW >= 4 ? 1 : 4 / RPW;   // of such, before the slots of all are worked out
+  constexpr int kRows = RPW * kTurns;
   constexpr int kCols = G * NPL;
   extern __shared__ uint8_t smem[];
   float* red = reinterpret_cast<float*>(smem);                        // [kWarps * RPW][kCols]
   int32_t* cnt = reinterpret_cast<int32_t*>(red + kWarps * RPW * kCols);  // [kCols]
-  float* stage_v = reinterpret_cast<float*>(cnt + kCols);             // [kWarps][RPW][k]
-  int32_t* stage_i = reinterpret_cast<int32_t*>(stage_v + kWarps * RPW * a.k);
-  __shared__ float sh_scale[kWarps * RPW];
+  float* stage_v = reinterpret_cast<float*>(cnt + kCols);             // [kWarps][kRows][k]
+  int32_t* stage_i = reinterpret_cast<int32_t*>(stage_v + kWarps * kRows * a.k);
+  __shared__ float2 sh_row[kWarps * kRows];    // the rows' largest logit (NaN where not live) and 1 / sum
   __shared__ float sh_z[kWarps];
   __shared__ int32_t sh_live[kWarps];
   __shared__ float sh_sum[ONE ? kCols : 1];    // ONE: this block's sums, read by the first block
@@ -198,9 +201,10 @@ __global__ void __launch_bounds__(kRouteThreads) route_forward_kernel(const Rout
   const int k = a.k;
   const T* logits = static_cast<const T*>(a.logits);
   const bool vec = ((reinterpret_cast<uintptr_t>(logits) | (a.ld * sizeof(T))) & 15u) == 0;
-  float* my_v = stage_v + warp * RPW * k;
-  int32_t* my_i = stage_i + warp * RPW * k;
-  float* my_scale = sh_scale + warp * RPW;
+  float* my_v = stage_v + warp * kRows * k;
+  int32_t* my_i = stage_i + warp * kRows * k;
+  float2* my_row = sh_row + warp * kRows;
+  const uint32_t inv_k = 65536u / k + 1u;      // t / k as t inv_k / 2^16, exact for t < 2048
 
   if (!ONE && blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
   if (ONE && static_cast<int64_t>(blockIdx.x) * a.rows_per_block >= a.N) {  // a block without rows
@@ -240,125 +244,151 @@ __global__ void __launch_bounds__(kRouteThreads) route_forward_kernel(const Rout
     int live_rows = 0;
     __syncthreads();
 
-    for (int64_t base = r + warp * RPW; base < end; base += kWarps * RPW) {
-      const int64_t row = base + gr;
-      const bool in = row < end;
-      float z[NPL];
-      if (in) {
-        load_row<T, NPL>(logits + row * a.ld, c0, a.E, vec, neg_inf(), z);
-      } else {
+    constexpr bool kAhead = NPL == 8;
+    float next[NPL];   // the row after this one, loaded a turn ahead
+    if (kAhead && r + warp * kRows + gr < end)
+      load_row<T, NPL>(logits + (r + warp * kRows + gr) * a.ld, c0, a.E, vec, neg_inf(), next);
+    for (int64_t base = r + warp * kRows; base < end; base += kWarps * kRows) {
+#pragma unroll 1
+      for (int turn = 0; turn < kTurns && base + turn * RPW < end; ++turn) {
+        const int64_t row = base + turn * RPW + gr;
+        const bool in = row < end;
+        float z[NPL];
+        if (kAhead) {
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) z[i] = neg_inf();
-      }
-      bool live = in && !outside && (!a.valid || a.valid[row] != 0);
-      float m = z[0];
+          for (int i = 0; i < NPL; ++i) z[i] = in ? next[i] : neg_inf();
+          const int64_t then = turn + 1 < kTurns ? row + RPW : row - turn * RPW + kWarps * kRows;
+          if (then < end) load_row<T, NPL>(logits + then * a.ld, c0, a.E, vec, neg_inf(), next);
+        } else if (in) {
+          load_row<T, NPL>(logits + row * a.ld, c0, a.E, vec, neg_inf(), z);
+        } else {
 #pragma unroll
-      for (int i = 1; i < NPL; ++i) m = max_nan(m, z[i]);
-      m = group_max_nan<G>(m);
-      live = live && !(m == neg_inf());
-      const float mm = live ? m : 0.f;
-      float p[NPL], sum = 0.f;
+          for (int i = 0; i < NPL; ++i) z[i] = neg_inf();
+        }
+        bool live = in && !outside && (!a.valid || a.valid[row] != 0);
+        float m = z[0];
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        p[i] = exp2_approx((z[i] - mm) * kLog2e);
-        sum += p[i];
-      }
-      sum = group_sum<G>(sum);
-      const float inv = 1.0f / sum;
-      if (live) {
+        for (int i = 1; i < NPL; ++i) m = max_nan(m, z[i]);
+        m = group_max_nan<G>(m);
+        live = live && !(m == neg_inf());
+        const float mm = live ? m : 0.f;
+        float p[NPL], sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) acc[i] = fmaf(p[i], inv, acc[i]);
-      }
-      if (in && gl == 0) {
-        const float log_sum = logf(sum);
-        // apart: their sum would lose log_sum's last bits where |m| is large,
-        // and with them the backward's softmax
-        a.stats[row] = make_float2(live ? m : neg_inf(), live ? log_sum : 0.f);
+        for (int i = 0; i < NPL; ++i) {
+          p[i] = exp2_approx((z[i] - mm) * kLog2e);
+          sum += p[i];
+        }
+        sum = group_sum<G>(sum);
+        const float inv = 1.0f / sum;
         if (live) {
-          const float lse = mm + log_sum;
-          zacc = fmaf(lse, lse, zacc);
-          ++live_rows;
+#pragma unroll
+          for (int i = 0; i < NPL; ++i) acc[i] = fmaf(p[i], inv, acc[i]);
         }
-      }
-      // The k largest by keys, all distinct: each round takes the group's
-      // largest key below the last one. key - last wraps to the top half for
-      // the keys below it and not for the others, so one unsigned maximum
-      // finds it, with no search for the winner and nothing to remove.
-      constexpr int IDX = log2_of(kCols);
-      uint32_t key[NPL];
+        if (in && gl == 0) {
+          const float log_sum = logf(sum);
+          // apart: their sum would lose log_sum's last bits where |m| is large,
+          // and with them the backward's softmax
+          a.stats[row] = make_float2(live ? m : neg_inf(), live ? log_sum : 0.f);
+          if (live) {
+            const float lse = mm + log_sum;
+            zacc = fmaf(lse, lse, zacc);
+            ++live_rows;
+          }
+        }
+        // The k largest by keys, all distinct: each round takes the group's
+        // largest key below the last one.
+        constexpr int IDX = log2_of(kCols);
+        uint32_t key[NPL];
+        if (a.E == kCols) {
 #pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        key[i] = c0 + i < a.E ? expert_key<IDX>(z[i], c0 + i) : static_cast<uint32_t>(kCols - 1 - c0 - i);
-      uint32_t last = 0x80000000u;
-      // fp32: two keys alike in what they keep of the logit, and some logit of
-      // the lane's with bits in what they cut (logits rounded to 16 bits have
-      // none: their ties are true ties, in the keys' order)
-      bool unsure = false;
-      uint32_t bits = 0;
+          for (int i = 0; i < NPL; ++i) key[i] = expert_key<IDX>(z[i], c0 + i);
+        } else {
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) bits |= __float_as_uint(z[i]);
-      const int rounds = sizeof(T) == 4 && k < a.E ? k + 1 : k;
-      for (int j = 0; j < rounds; ++j) {
-        uint32_t best = key[0] - last;
+          for (int i = 0; i < NPL; ++i)
+            key[i] = c0 + i < a.E ? expert_key<IDX>(z[i], c0 + i) : static_cast<uint32_t>(kCols - 1 - c0 - i);
+        }
+        int32_t* slot = my_i + (turn * RPW + gr) * k;
+        uint32_t last = 0x80000000u;
+        // fp32: two keys alike in what they keep of the logit, and some logit of
+        // the lane's with bits in what they cut (logits rounded to 16 bits have
+        // none: their ties are true ties, in the keys' order)
+        bool unsure = false;
+        uint32_t bits = 0;
 #pragma unroll
-        for (int i = 1; i < NPL; ++i) best = max(best, key[i] - last);
-        best = group_max_u32<G>(best) + last;
-        if (sizeof(T) == 4) unsure |= ((best ^ last) >> IDX) == 0;
-        last = best;
-        if (j < k && gl == 0) my_i[gr * k + j] = static_cast<int>((kCols - 1) - (best & (kCols - 1)));
-      }
-      if (sizeof(T) == 4 && __any_sync(kAll, unsure) && __any_sync(kAll, (bits & ((2u << IDX) - 1u)) != 0)) {
-        // exact: the group's largest logit, the lowest lane that has it (its
-        // experts come before the others'), the first of that lane's
-        for (int j = 0; j < k; ++j) {
-          float bv = neg_inf();
-          int bi = 0;
+        for (int i = 0; i < NPL; ++i) bits |= __float_as_uint(z[i]);
+        const int rounds = sizeof(T) == 4 && k < a.E ? k + 1 : k;
+        for (int j = 0; j < rounds; ++j) {
+          // key - last wraps to the top half for the keys below it and not for
+          // the others, so one unsigned maximum finds it, with no search for the
+          // winner and nothing to remove
+          uint32_t best = key[0] - last;
 #pragma unroll
-          for (int i = 0; i < NPL; ++i) {
-            const float v = z[i] != z[i] ? __int_as_float(0x7F800000) : z[i];   // NaN before all, as in the keys
-            if (v > bv) {
-              bv = v;
-              bi = i;
+          for (int i = 1; i < NPL; ++i) best = max(best, key[i] - last);
+          best = group_max_u32<G>(best) + last;
+          if (sizeof(T) == 4) unsure |= ((best ^ last) >> IDX) == 0;
+          last = best;
+          if (j < k && gl == 0) slot[j] = static_cast<int>((kCols - 1) - (best & (kCols - 1)));
+        }
+        if (sizeof(T) == 4 && __any_sync(kAll, unsure) && __any_sync(kAll, (bits & ((2u << IDX) - 1u)) != 0)) {
+          // (the fast rounds' slots were written by other lanes than these will be)
+          __syncwarp();
+          // exact: the group's largest logit, the lowest lane that has it (its
+          // experts come before the others'), the first of that lane's
+          for (int j = 0; j < k; ++j) {
+            float bv = neg_inf();
+            int bi = 0;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+              const float v = z[i] != z[i] ? __int_as_float(0x7F800000) : z[i];   // NaN before all, as in the keys
+              if (v > bv) {
+                bv = v;
+                bi = i;
+              }
             }
-          }
-          const uint32_t who = __ballot_sync(kAll, bv == group_max<G>(bv)) & gmask;
-          if (__ffs(who) - 1 == lane) {
-            my_i[gr * k + j] = bv > neg_inf() ? c0 + bi : 0;
+            const uint32_t who = __ballot_sync(kAll, bv == group_max<G>(bv)) & gmask;
+            if (__ffs(who) - 1 == lane) {
+              slot[j] = bv > neg_inf() ? c0 + bi : 0;
 #pragma unroll
-            for (int i = 0; i < NPL; ++i)
-              if (i == bi) z[i] = neg_inf();
+              for (int i = 0; i < NPL; ++i)
+                if (i == bi) z[i] = neg_inf();
+            }
+            // a row without a logit left: its slots read a -inf again below
+            if (bv == neg_inf() && who == gmask && gl == 0) slot[j] = -1;
           }
-          // a row without a logit left: its slots read a -inf again below
-          if (bv == neg_inf() && who == gmask && gl == 0) my_i[gr * k + j] = -1;
         }
+        if (gl == 0) my_row[turn * RPW + gr] = make_float2(live ? mm : __int_as_float(0x7FFFFFFF), live ? inv : -1.f);
       }
       __syncwarp();
-      // the slots' weights, a lane per slot
-      float share = 0.f;
-      for (int j = gl; j < k; j += G) {
-        const int e = my_i[gr * k + j];
+      // the slots of all these rows, a lane per slot: exp, then the weights
+      const int slots = static_cast<int>(min(static_cast<int64_t>(kRows), end - base)) * k;
+      for (int t = lane; t < slots; t += 32) {
+        const int b = (t * inv_k) >> 16;
+        const float2 rw = my_row[b];
+        const int e = my_i[t];
         float ex = 0.f;
-        if (live && e >= 0) {
-          const float v = to_f(logits[row * a.ld + e]);
-          if (v == neg_inf()) {
-            my_i[gr * k + j] = -1;
-          } else {
-            ex = exp2_approx((v - mm) * kLog2e);
+        int keep = -1;
+        if (e >= 0 && rw.y != -1.f) {   // live
+          const float v = to_f(logits[(base + b) * a.ld + e]);
+          if (v != neg_inf()) {
+            ex = exp2_approx((v - rw.x) * kLog2e);
+            keep = e;
             atomicAdd(&cnt[e], 1);
           }
-        } else {
-          my_i[gr * k + j] = -1;
         }
-        my_v[gr * k + j] = ex;
-        share += ex;
+        my_v[t] = ex;
+        my_i[t] = keep;
       }
-      share = group_sum<G>(share);
-      if (gl == 0) my_scale[gr] = a.renormalize ? (share == 0.f ? 0.f : 1.0f / share) : inv;
       __syncwarp();
-      const int slots = static_cast<int>(min(static_cast<int64_t>(RPW), end - base)) * k;
       for (int t = lane; t < slots; t += 32) {
+        const int b = (t * inv_k) >> 16;
+        float scale = my_row[b].y;
+        if (a.renormalize) {
+          float share = 0.f;
+          for (int j = 0; j < k; ++j) share += my_v[b * k + j];
+          scale = 1.0f / share;
+        }
         const int e = my_i[t];
-        a.weights[base * k + t] = e >= 0 ? my_v[t] * my_scale[t / k] : 0.f;
+        a.weights[base * k + t] = e >= 0 ? my_v[t] * scale : 0.f;
         a.experts[base * k + t] = e;
       }
       __syncwarp();
@@ -544,18 +574,19 @@ __global__ void __launch_bounds__(32 * R) route_finish_kernel(const RouteArgs a,
   }
   if (tx == 0) sh_z[ty] = term;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    double sum = 0.0;
-    for (int w = 0; w < R; ++w) sum += sh_z[w];
-    a.terms[blockIdx.x] = sum;
-    if (chunk == 0) {
-      a.doc_live[d] = n;
-      a.doc_z[d] = zs;
+  if (ty == 0) {
+    term = tx < R ? sh_z[tx] : 0.f;
+    for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(kAll, term, o);
+    if (tx == 0) {
+      a.terms[blockIdx.x] = term;
+      if (chunk == 0) {
+        a.doc_live[d] = n;
+        a.doc_z[d] = zs;
+      }
+      __threadfence();   // these three are all the last block reads
+      last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
     }
   }
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
   __syncthreads();
   if (!last) return;
   __threadfence();
@@ -627,10 +658,37 @@ __global__ void __launch_bounds__(kRouteThreads)
   float slope[NPL];
 #pragma unroll
   for (int i = 0; i < NPL; ++i) slope[i] = 0.f;
+  // A round ahead: the row and what belongs to it. The loads of one row alone
+  // left the kernel waiting for memory (70 us at 131072 x 256 fp32).
+  constexpr bool kAhead = NPL == 8;
+  float next[NPL];
+  float2 next_stat = make_float2(neg_inf(), 0.f);
+  int next_e = -1;
+  float next_w = 0.f, next_d = 0.f;
+  auto fetch = [&](int64_t row) {
+    next_stat = make_float2(neg_inf(), 0.f);
+    if (row < r1) {
+      next_stat = a.stats[row];
+      load_row<T, NPL>(logits + row * a.ld, c0, a.E, vec, neg_inf(), next);
+      if (d_weights && gl < k) {
+        next_e = a.experts[row * k + gl];
+        next_w = a.weights[row * k + gl];
+        next_d = d_weights[row * k + gl];
+      }
+    }
+  };
+  if (kAhead) fetch(r0 + warp * RPW + gr);
   for (int64_t base = r0 + warp * RPW; base < r1; base += kWarps * RPW) {
     const int64_t row = base + gr;
     const bool in = row < r1;
-    const float2 stat = in ? a.stats[row] : make_float2(neg_inf(), 0.f);
+    if (!kAhead) fetch(row);
+    const float2 stat = next_stat;
+    const int slot_e = next_e;
+    const float slot_w = next_w, slot_d = next_d;
+    float z[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) z[i] = next[i];
+    if (kAhead) fetch(row + kWarps * RPW);
     const bool live = !(stat.x == neg_inf());
     if (in && a.offsets)
       while (doc < a.documents && a.offsets[doc + 1] <= row) ++doc;
@@ -640,24 +698,21 @@ __global__ void __launch_bounds__(kRouteThreads)
       for (int i = 0; i < NPL; ++i) slope[i] *= gb;
       held = doc;
     }
-    float z[NPL];
-    if (live) {
-      load_row<T, NPL>(logits + row * a.ld, c0, a.E, vec, neg_inf(), z);
-    } else {
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) z[i] = neg_inf();
-    }
     // chosen slots: w (g - [renormalised] sum g w) lands on the slot's expert
     float gw = 0.f;
     if (d_weights && live) {
-      for (int j = gl; j < k; j += G) gw = fmaf(d_weights[row * k + j], a.weights[row * k + j], gw);
+      // (a slot without an expert has weight 0, whatever gradient came for it)
+      if (gl < k && slot_e >= 0) gw = slot_d * slot_w;
+      for (int j = gl + G; j < k; j += G)
+        if (a.experts[row * k + j] >= 0) gw = fmaf(d_weights[row * k + j], a.weights[row * k + j], gw);
     }
     gw = group_sum<G>(gw);
     if (d_weights && live) {
-      for (int j = gl; j < k; j += G) {
+      const float off = a.renormalize ? gw : 0.f;
+      if (gl < k && slot_e >= 0 && slot_e < a.E) extra[slot_e] = slot_w * (slot_d - off);
+      for (int j = gl + G; j < k; j += G) {
         const int e = a.experts[row * k + j];
-        if (e >= 0 && e < a.E)
-          extra[e] = a.weights[row * k + j] * (d_weights[row * k + j] - (a.renormalize ? gw : 0.f));
+        if (e >= 0 && e < a.E) extra[e] = a.weights[row * k + j] * (d_weights[row * k + j] - off);
       }
     }
     __syncwarp();
@@ -682,8 +737,16 @@ __global__ void __launch_bounds__(kRouteThreads)
 template <class T, int G, int NPL>
 cudaError_t forward_t(const RouteArgs& a, cudaStream_t s) {
   const size_t rows = kWarps * (32 / G), cols = G * NPL;
-  // at most 8 x 32 x 32 + 1024 floats and 8 x 32 slots: below the 48 KB that need no opt-in
-  const size_t smem = rows * cols * 4 + cols * 4 + rows * a.k * 8;
+  // at most 8 x 32 x 32 + 1024 floats and 8 x 4 x 32 slots, 44 KB (beside 4 KB of static memory)
+  const size_t smem = rows * cols * 4 + cols * 4 + std::max<size_t>(rows, 4 * kWarps) * a.k * 8;
+  static const cudaError_t opted = [] {
+    const cudaError_t e =
+        cudaFuncSetAttribute(route_forward_kernel<T, G, NPL, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 45056);
+    return e != cudaSuccess ? e
+                            : cudaFuncSetAttribute(route_forward_kernel<T, G, NPL, false>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, 45056);
+  }();
+  if (opted != cudaSuccess) return opted;
   if (!a.one_launch) {
     route_forward_kernel<T, G, NPL, false><<<a.blocks, kRouteThreads, smem, s>>>(a);
     return cudaGetLastError();
@@ -735,11 +798,11 @@ RouteGeometry route_geometry(int64_t N, int64_t E, int64_t documents, bool offse
   g.per_lane = E <= 256 ? 8 : (E <= 512 ? 16 : 32);
   g.lanes = 1;
   while (g.lanes < 32 && static_cast<int64_t>(g.lanes) * g.per_lane < E) g.lanes *= 2;
-  const int64_t step = kWarps * (32 / g.lanes);
+  const int64_t step = kWarps * std::max(32 / g.lanes, 4);
   // Short batches run as one cluster of up to 8 blocks that closes the call
-  // itself: one launch instead of two. Past 8 rounds of rows per block the
+  // itself: one launch instead of two. Past 8 turns of rows per warp the
   // whole GPU's width is worth the second launch.
-  g.one_launch = !offsets && N > 0 && N <= 8 * 8 * step;
+  g.one_launch = !offsets && N > 0 && N <= 8 * 8 * kWarps * (32 / g.lanes);
   const int64_t most = g.one_launch ? 8 : 4 * static_cast<int64_t>(num_sms);
   int64_t per = (N + most - 1) / most;
   per = (per + step - 1) / step * step;

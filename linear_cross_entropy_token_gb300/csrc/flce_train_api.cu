@@ -240,7 +240,8 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
   a.lda = z.lda;
   a.timeout_ns = h->timeout_ns;
 
-  const double el = static_cast<double>(q->rows) * q->cols * count, dm = static_cast<double>(z.m), dn = static_cast<double>(z.n);
+  const double el = static_cast<double>(q->rows) * q->cols * count;
+  const double dm = static_cast<double>(z.m), dn = static_cast<double>(z.n);
   const double gb = static_cast<double>(element_bytes(q->grad_dtype)), mb = mats[0].momentum ? 8.0 : 0.0;
   const double ob = mats[0].weight ? 2.0 * element_bytes(q->weight_dtype) : 1.0 * element_bytes(q->update_dtype);
   int cluster, chunks;
@@ -415,7 +416,8 @@ flce_status flce_muon_update(flce_handle_t h, const flce_muon_args* q, const flc
     const flce_muon_matrix& t = mats[i];
     if (!t.grad || (!t.weight && !t.update))
       return fail(h, FLCE_ERR_INVALID_ARG, "matrix %d: a gradient, and a weight or an update, are needed", i);
-    if ((t.momentum != nullptr) != (mats[0].momentum != nullptr) || (t.weight != nullptr) != (mats[0].weight != nullptr))
+    if ((t.momentum != nullptr) != (mats[0].momentum != nullptr) ||
+        (t.weight != nullptr) != (mats[0].weight != nullptr))
       return fail(h, FLCE_ERR_INVALID_ARG, "either all matrices have momentum (weights) or none");
     if (t.ld_grad < q->cols || (t.momentum && t.ld_momentum < q->cols) || (t.weight && t.ld_weight < q->cols) ||
         (!t.weight && t.ld_update < q->cols))
