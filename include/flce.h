@@ -202,12 +202,10 @@ enum {
     FLCE_K_ROUTE_BACKWARD = 17,  /* gradient of the router logits                       */
     FLCE_K_MUON_MOMENTUM = 18,   /* momentum update and sum of squares                  */
     FLCE_K_MUON_PREPARE = 19,    /* X = u / (|u| + eps) in two fp16 parts               */
-    FLCE_K_MUON_GRAM = 20,       /* A = X Xt (symmetric) on tcgen05                     */
-    FLCE_K_MUON_POLY = 21,       /* B = b A + c A^2 (symmetric) on tcgen05              */
-    FLCE_K_MUON_APPLY = 22,      /* X = a X + B X on tcgen05                            */
-    FLCE_K_MUON_RESULT = 23,     /* the last step's B X, written as update or weight    */
-    FLCE_K_MUON_SMALL = 24,      /* the whole update of matrices with a side up to 128  */
-    FLCE_K_NUM_KINDS = 25
+    FLCE_K_MUON_STEPS = 20,      /* all products (A = X Xt, B = b A + c A^2, a X + B X)
+                                    on tcgen05, and the update or weight              */
+    FLCE_K_MUON_SMALL = 21,      /* the whole update of matrices with a side up to 128  */
+    FLCE_K_NUM_KINDS = 22
 };
 
 typedef struct flce_kernel_profile {

@@ -1184,10 +1184,7 @@ const char* flce_kernel_name(int32_t kind) {
     case FLCE_K_ROUTE_BACKWARD: return "route_backward";
     case FLCE_K_MUON_MOMENTUM: return "muon_momentum";
     case FLCE_K_MUON_PREPARE: return "muon_prepare";
-    case FLCE_K_MUON_GRAM: return "muon_gram";
-    case FLCE_K_MUON_POLY: return "muon_poly";
-    case FLCE_K_MUON_APPLY: return "muon_apply";
-    case FLCE_K_MUON_RESULT: return "muon_result";
+    case FLCE_K_MUON_STEPS: return "muon_steps";
     case FLCE_K_MUON_SMALL: return "muon_small";
     default: return "?";
   }

@@ -42,7 +42,10 @@ namespace {
 __global__ void __launch_bounds__(256) muon_momentum_kernel(const __grid_constant__ MuonArgs a) {
   __shared__ double sh[8];
   const MuonMat& t = a.mat[blockIdx.y];
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.ctrl[kCtrlError] = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (blockIdx.y == 0) a.ctrl[kCtrlError] = 0;
+    a.done[blockIdx.y] = 0;
+  }
   const uint32_t step = a.norm_blocks * 256u;
   const uint32_t first = blockIdx.x * 256u + threadIdx.x;
   SquareSum q;
@@ -261,26 +264,88 @@ __host__ __device__ __forceinline__ int muon_units_per_matrix(bool sym, int tile
   return R * tiles_n * (tiles_n + 1) / 2 - (R * tiles_n - tiles_m);
 }
 
-template <int PHASE, int SHAPE>
-__device__ __forceinline__ MuonUnit muon_unit(int u, int tiles_m, int tiles_n) {
-  constexpr bool kSym = PHASE == kMuonGram || PHASE == kMuonPoly;
-  constexpr int R = MuonTile<SHAPE>::kN / MuonTile<SHAPE>::kM;
-  const int per = muon_units_per_matrix<SHAPE>(kSym, tiles_m, tiles_n);
-  MuonUnit r;
-  r.mat = u / per;
-  const int w = u - r.mat * per;
-  if (kSym) {
-    // columns before tn hold R tn (tn + 1) / 2 tiles
-    int tn = static_cast<int>((sqrtf(8.f / R * w + 1.f) - 1.f) * 0.5f);
-    while (R * tn * (tn + 1) / 2 > w) --tn;
-    while (R * (tn + 1) * (tn + 2) / 2 <= w) ++tn;
-    r.tn = tn;
-    r.tm = w - R * tn * (tn + 1) / 2;
-  } else {
-    r.tm = w % tiles_m;
-    r.tn = w / tiles_m;
+// The work of one launch, as one sequence: steps, in each the three products,
+// in each the matrices one after another, and their tiles. Unit g of it is
+// slot g mod (number of slots)'s. Every role of a CTA walks it by itself.
+template <int SHAPE>
+struct MuonWalk {
+  using Tile = MuonTile<SHAPE>;
+  int tiles_m, tiles_s, tiles_n;   // tile rows; tile columns of the symmetric products and of B X
+  int per_s, per_x;                // tiles per matrix of either
+  int count, slots, steps;
+  int step = 0, phase = 0, u;
+  int mat, tm, tn;
+
+  __device__ __forceinline__ MuonWalk(const MuonArgs& a, int steps_, int slot, int slots_)
+      : count(a.count), slots(slots_), steps(steps_), u(slot) {
+    tiles_m = (a.m + Tile::kM - 1) / Tile::kM;
+    tiles_s = (a.m + Tile::kN - 1) / Tile::kN;
+    tiles_n = (a.n + Tile::kN - 1) / Tile::kN;
+    per_s = muon_units_per_matrix<SHAPE>(true, tiles_m, tiles_s);
+    per_x = muon_units_per_matrix<SHAPE>(false, tiles_m, tiles_n);
   }
-  return r;
+  __device__ __forceinline__ bool symmetric() const { return phase < kMuonApply; }
+  // to the unit at u; false past the last
+  __device__ __forceinline__ bool locate() {
+    for (;;) {
+      const int units = count * (symmetric() ? per_s : per_x);
+      if (u < units) break;
+      u -= units;
+      if (++phase == 3) {
+        phase = 0;
+        if (++step == steps) return false;
+      }
+    }
+    const int per = symmetric() ? per_s : per_x;
+    mat = u / per;
+    const int w = u - mat * per;
+    if (symmetric()) {
+      // columns before tn hold R tn (tn + 1) / 2 tiles
+      constexpr int R = Tile::kN / Tile::kM;
+      tn = static_cast<int>((sqrtf(8.f / R * w + 1.f) - 1.f) * 0.5f);
+      while (R * tn * (tn + 1) / 2 > w) --tn;
+      while (R * (tn + 1) * (tn + 2) / 2 <= w) ++tn;
+      tm = w - R * tn * (tn + 1) / 2;
+    } else {
+      tm = w % tiles_m;
+      tn = w / tiles_m;
+    }
+    return true;
+  }
+  __device__ __forceinline__ void advance() { u += slots; }
+  // tiles of this matrix that come before this product: all of them are read by it
+  __device__ __forceinline__ uint32_t needed() const {
+    return static_cast<uint32_t>(step * (2 * per_s + per_x) + phase * per_s);
+  }
+};
+
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void add_release(uint32_t* p, uint32_t v) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+// Waits until a matrix's count of finished tile parts has reached `target`
+// (it only grows), bounded like every other wait; then later TMA accesses of
+// this thread are ordered behind what the count stands for.
+__device__ __forceinline__ bool wait_done(const uint32_t* done, uint32_t target, uint32_t* err, uint64_t timeout_ns) {
+  if (ld_acquire(done) < target) {
+    const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+    for (uint32_t it = 0; ld_acquire(done) < target; ++it) {
+      if ((it & 31u) != 31u) continue;
+      if (ld_volatile_u32(err) != 0u) return false;
+      if (globaltimer_ns() - t0 > timeout_ns) {
+        atomicCAS(err, 0u, kErrTimeout);
+        return false;
+      }
+    }
+  }
+  asm volatile("fence.proxy.async;" ::: "memory");
+  return true;
 }
 
 // `rows` rows of 32 result columns from a warp's staged fp32 block [32][32]
@@ -336,30 +401,22 @@ __device__ __forceinline__ void write_rows(T* out, int64_t ld, int rows, int col
 // for another. (With each thread reading and writing its own row in global
 // memory every access touched 32 lines: B X of 8 x 1024 x 1024 took 36.8 us,
 // its products 8.7.)
-template <int PHASE>
 struct MuonEpilogue {
-  static constexpr bool kSym = PHASE == kMuonGram || PHASE == kMuonPoly;
-  static constexpr bool kLoads = PHASE != kMuonGram;
-  static constexpr bool kLoads2 = PHASE == kMuonApply || PHASE == kMuonLast;
-  static constexpr bool kStores = PHASE != kMuonLast;
   const MuonArgs& a;
-  const MuonMaps& maps;
-  const MuonStep& st;
   uint8_t* buf;        // this warp's 2 x 2 x kEpiPart
   uint32_t bar;        // this warp's two load barriers
   int lane;
-  uint32_t loads = 0, uses = 0;
+  uint32_t loads = 0, uses = 0;   // groups loaded, groups taken
 
-  // TMA loads of the group at column c0 into the next buffer
-  __device__ __forceinline__ void load(int mat, int row0, int c0) {
-    if (!kLoads) return;
+  // TMA loads of the group at column c0 into the next buffer: X hi and lo, or A
+  __device__ __forceinline__ void load(const CUtensorMap* e0, const CUtensorMap* e1, int mat, int row0, int c0) {
     if (lane == 0) {
-      if (kStores) bulk_wait_group_read<0>();  // the buffer's last stores have read it
+      bulk_wait_group_read<0>();  // the buffer's last stores have read it
       const uint32_t b = loads & 1u;
       const uint32_t dst = smem_u32(buf + b * 2 * kEpiPart), bb = bar + 8u * b;
-      mbar_arrive_expect_tx(bb, kLoads2 ? 2 * kEpiPart : kEpiPart);
-      tma_load_3d(dst, &maps.e0, bb, c0, row0, mat);
-      if (kLoads2) tma_load_3d(dst + kEpiPart, &maps.e1, bb, c0, row0, mat);
+      mbar_arrive_expect_tx(bb, e1 ? 2 * kEpiPart : kEpiPart);
+      tma_load_3d(dst, e0, bb, c0, row0, mat);
+      if (e1) tma_load_3d(dst + kEpiPart, e1, bb, c0, row0, mat);
     }
     ++loads;
   }
@@ -381,19 +438,29 @@ struct MuonEpilogue {
     }
   }
 
-  // columns c0 .. c0 + 31 of the warp's rows, accumulator values in r
-  __device__ __forceinline__ bool group(int mat, int row0, int c0, bool mirror, float factor, const uint32_t (&r)[32]) {
-    const uint32_t b = uses & 1u;
+  // columns c0 .. c0 + 31 of the warp's rows, accumulator values in r; written
+  // to o0 and, a mirror image or X lo, to o1
+  template <int PHASE>
+  __device__ __forceinline__ bool group(const MuonStep& st, const CUtensorMap* o0, const CUtensorMap* o1, int g, int mat,
+                                        int row0, int c0, bool mirror, float factor, const uint32_t (&r)[32]) {
+    constexpr bool kSym = PHASE == kMuonGram || PHASE == kMuonPoly;
+    const uint32_t b = PHASE == kMuonGram ? (g & 1) : (uses & 1u);
     uint8_t* p0 = buf + b * 2 * kEpiPart;
     uint8_t* p1 = p0 + kEpiPart;
-    if (kLoads) {
+    if (PHASE != kMuonGram) {
       if (!__all_sync(kAll, mbar_wait_bounded(bar + 8u * b, (uses >> 1) & 1u, a.ctrl + kCtrlError, a.timeout_ns)))
         return false;
+      ++uses;
     } else {
-      if (lane == 0) bulk_wait_group_read<1>();
+      // the buffer's last stores have read it (other products left either buffer's)
+      if (lane == 0) {
+        if (g == 0)
+          bulk_wait_group_read<0>();
+        else
+          bulk_wait_group_read<1>();
+      }
       __syncwarp();
     }
-    ++uses;
     uint4* q0 = reinterpret_cast<uint4*>(p0 + lane * 64);
     uint4* q1 = reinterpret_cast<uint4*>(p1 + lane * 64);
     const int sw = (lane >> 1) & 3;   // 64-byte swizzle: chunk j of a row sits at chunk j ^ (row / 2 % 4)
@@ -419,11 +486,13 @@ struct MuonEpilogue {
           }
           // the diagonal stays in fp32, apart (by selects: a branch per element
           // costs more than the rest of the epilogue)
-          const int d = i - (c0 + 8 * j);
+          if (c0 == row0) {
+            const int d = lane - 8 * j;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            on_diag = e == d ? v[e] : on_diag;
-            v[e] = e == d ? 0.f : v[e];
+            for (int e = 0; e < 8; ++e) {
+              on_diag = e == d ? v[e] : on_diag;
+              v[e] = e == d ? 0.f : v[e];
+            }
           }
         }
         uint32_t w[4];
@@ -435,13 +504,13 @@ struct MuonEpilogue {
           for (int e = 0; e < 8; ++e) mir[(8 * j + e) * 32] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
         }
       }
-      if (PHASE == kMuonPoly && i >= c0 && i < c0 + 32 && i < a.m)
+      if (PHASE == kMuonPoly && c0 == row0 && i < a.m)
         a.diag[static_cast<int64_t>(mat) * a.m + i] = on_diag * kPolyInv;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        tma_store_3d(&maps.o0, smem_u32(p0), c0, row0, mat);
-        if (mirror) tma_store_3d(&maps.o1, smem_u32(p1), row0, c0, mat);
+        tma_store_3d(o0, smem_u32(p0), c0, row0, mat);
+        if (mirror) tma_store_3d(o1, smem_u32(p1), row0, c0, mat);
         bulk_commit_group();
       }
       __syncwarp();
@@ -468,8 +537,8 @@ struct MuonEpilogue {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_3d(&maps.o0, smem_u32(p0), c0, row0, mat);
-          tma_store_3d(&maps.e1, smem_u32(p1), c0, row0, mat);
+          tma_store_3d(o0, smem_u32(p0), c0, row0, mat);
+          tma_store_3d(o1, smem_u32(p1), c0, row0, mat);
           bulk_commit_group();
         }
         __syncwarp();
@@ -505,23 +574,30 @@ struct MuonEpilogue {
   }
 };
 
-// The persistent kernel of one product. PAIR and SINGLE tiles have two
-// accumulators in TMEM, so that the epilogue of a tile overlaps the next
-// tile's products; a WIDE tile fills TMEM, and the next tile's products wait
-// until its columns have been read. Every wait is bounded.
+// All steps of a group of matrices in one persistent launch. PAIR and SINGLE
+// tiles have two accumulators in TMEM, so that the epilogue of a tile overlaps
+// the next tile's products; a WIDE tile fills TMEM, and the next tile's
+// products wait until its columns have been read.
 //
-// The kernels of a call form a chain of programmatic launches: each starts
-// while its predecessor drains, sets up its barriers and TMEM, and waits for it
-// before its first access to global memory.
-template <int PHASE, int SHAPE>
-__device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonArgs& a, const MuonStep& st) {
+// A product reads what the products before it wrote for the same matrix. Each
+// epilogue warp adds to the matrix's counter when its part of a tile is in
+// global memory, and a tile's loads wait for the counter to reach all earlier
+// tiles of that matrix. So one matrix's tiles fill the time in which another's
+// are still to finish (as a launch per product, 8 x 1024 x 1024 took 57 us a
+// step, of which its products need 17), and a product starts a flag's latency
+// after its predecessor instead of a launch's. Every slot takes its units in
+// the order of the sequence and all slots are resident (a cooperative launch),
+// so a unit only ever waits for units that run. Every wait is bounded.
+template <int SHAPE>
+__global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bounds__(kThreads, 1)
+    muon_steps_kernel(const __grid_constant__ MuonMaps maps, const __grid_constant__ MuonArgs a,
+                      const __grid_constant__ MuonSteps steps) {
   using Tile = MuonTile<SHAPE>;
-  constexpr bool kSym = PHASE == kMuonGram || PHASE == kMuonPoly;
   constexpr bool kPaired = SHAPE != kMuonSingle, kWide = SHAPE == kMuonWide;
-  constexpr int BMN = kSym ? 0 : 1;   // X as the right operand is contiguous along its columns
   constexpr int kStages = Tile::kStages, kAccs = Tile::kAccs;
   constexpr uint32_t kStageBytes = stage_bytes<SHAPE>();
   constexpr uint32_t kTmemCols = kAccs * Tile::kN;
+  constexpr uint32_t kParts = 8 * (kPaired ? 2 : 1);   // epilogue warps of a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -537,8 +613,8 @@ __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonA
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = kPaired ? cluster_ctarank() : 0u;
-  const int first_unit = kPaired ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
-  const int unit_step = kPaired ? static_cast<int>(num_clusters_x()) : static_cast<int>(gridDim.x);
+  const int slot = kPaired ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
+  const int slots = kPaired ? static_cast<int>(num_clusters_x()) : static_cast<int>(gridDim.x);
   uint32_t* err = a.ctrl + kCtrlError;
   auto wait = [&](uint32_t bar, uint32_t parity) {
     return kPaired ? mbar_wait_bounded_cluster(bar, parity, err, a.timeout_ns)
@@ -565,12 +641,6 @@ __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonA
     for (int i = 0; i < 16; ++i) mbar_init(drain_bar + 8u * (1 + i), 1);  // the epilogue warps' loads
     fence_mbar_init();
     fence_proxy_async_smem();
-    tma_prefetch_map(&maps.a);
-    tma_prefetch_map(&maps.b);
-    tma_prefetch_map(&maps.e0);
-    tma_prefetch_map(&maps.e1);
-    tma_prefetch_map(&maps.o0);
-    tma_prefetch_map(&maps.o1);
   }
   if (warp == 1) {
     if (kPaired) {
@@ -581,26 +651,38 @@ __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonA
       tmem_relinquish();
     }
   }
+  if (warp == 2 && lane < static_cast<int>(sizeof(MuonMaps) / sizeof(CUtensorMap)))
+    tma_prefetch_map(reinterpret_cast<const CUtensorMap*>(&maps) + lane);
   __syncthreads();
   if (kPaired) cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  const int tiles_m = (a.m + Tile::kM - 1) / Tile::kM;
-  const int tiles_n = ((kSym ? a.m : a.n) + Tile::kN - 1) / Tile::kN;
-  const int num_units = a.count * muon_units_per_matrix<SHAPE>(kSym, tiles_m, tiles_n);
-  const int num_kb = ((PHASE == kMuonGram ? a.n : a.m) + kBK - 1) / kBK;
+  const int kb_n = (a.n + kBK - 1) / kBK, kb_m = (a.m + kBK - 1) / kBK;   // k-blocks of X Xt, of the others
+  MuonWalk<SHAPE> w(a, steps.count, slot, slots);
 
   if (warp == 0) {
     if (lane == 0) {
       uint32_t n_issued = 0;
       bool failed = false;
-      for (int u = first_unit; u < num_units && !failed; u += unit_step) {
-        const MuonUnit t = muon_unit<PHASE, SHAPE>(u, tiles_m, tiles_n);
-        const int mA = t.tm * Tile::kM + static_cast<int>(rank) * 128;
-        const int nB = t.tn * Tile::kN + static_cast<int>(rank) * 128;
+      int seen_mat = -1;
+      uint32_t seen = 0;
+      for (; !failed && w.locate(); w.advance()) {
+        const int src = w.step & 1;
+        const CUtensorMap* ma = w.phase == kMuonGram ? &maps.xk[src] : w.phase == kMuonPoly ? &maps.gk : &maps.pk;
+        const CUtensorMap* mb = w.phase == kMuonGram ? &maps.xk[src] : w.phase == kMuonPoly ? &maps.gk : &maps.xn[src];
+        const uint32_t needed = w.needed() * kParts;
+        if (w.mat != seen_mat || needed != seen) {
+          if (needed > 0 && !wait_done(a.done + w.mat, needed, err, a.timeout_ns)) {
+            failed = true;
+            break;
+          }
+          seen_mat = w.mat;
+          seen = needed;
+        }
+        const int mA = w.tm * Tile::kM + static_cast<int>(rank) * 128;
+        const int nB = w.tn * Tile::kN + static_cast<int>(rank) * 128;
+        const int num_kb = w.phase == kMuonGram ? kb_n : kb_m;
         for (int kb = 0; kb < num_kb; ++kb) {
           const int stage = n_issued % kStages;
           const uint32_t phase = (n_issued / kStages) & 1u;
@@ -614,20 +696,20 @@ __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonA
           const int k0 = kb * kBK;
           auto load = [&](uint32_t dst, const CUtensorMap* m, int c0, int c1) {
             if (kPaired)
-              tma_load_3d_pair(dst, m, fb, c0, c1, t.mat);
+              tma_load_3d_pair(dst, m, fb, c0, c1, w.mat);
             else
-              tma_load_3d(dst, m, fb, c0, c1, t.mat);
+              tma_load_3d(dst, m, fb, c0, c1, w.mat);
           };
-          load(sa, &maps.a, k0, mA);
+          load(sa, ma, k0, mA);
 #pragma unroll
           for (int h = 0; h < (kWide ? 2 : 1); ++h) {
             const uint32_t sb = sa + (1 + h) * kPartBytes;
             const int n = nB + 256 * h;
-            if (BMN == 0) {
-              load(sb, &maps.b, k0, n);
-            } else {
-              load(sb, &maps.b, n, k0);
-              load(sb + 8192, &maps.b, n + 64, k0);
+            if (w.symmetric()) {
+              load(sb, mb, k0, n);
+            } else {   // X as the right operand is contiguous along its columns
+              load(sb, mb, n, k0);
+              load(sb + 8192, mb, n + 64, k0);
             }
           }
           ++n_issued;
@@ -641,26 +723,19 @@ __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonA
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      // kind::f16; the descriptor's type fields say fp16
-      constexpr uint32_t idesc = idesc_f16_f32(Tile::kM, kWide ? 256 : Tile::kN, 0, BMN);
       uint32_t n_consumed = 0;
       bool issued = false, failed = false;
       int it = 0;
-      for (int u = first_unit; u < num_units && !failed; u += unit_step, ++it) {
-        const int acc = it % kAccs;
-        const uint32_t acc_phase = (it / kAccs) & 1;
-        if (!wait(tempty_bar(acc), acc_phase ^ 1u)) {
-          failed = true;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + acc * Tile::kN;
+      // the k-blocks of one tile; kind::f16, the descriptor's type fields say fp16
+      auto products = [&](auto mn, int num_kb, uint32_t d_tmem) {
+        constexpr int BMN = decltype(mn)::value;
+        constexpr uint32_t idesc = idesc_f16_f32(Tile::kM, kWide ? 256 : Tile::kN, 0, BMN);
         for (int kb = 0; kb < num_kb; ++kb) {
           const int stage = n_consumed % kStages;
           const uint32_t phase = (n_consumed / kStages) & 1u;
           if (!wait(full_bar(stage), phase)) {
             failed = true;
-            break;
+            return;
           }
           tc_fence_after();
           const uint32_t sa = smem_u32(smem + stage * kStageBytes);
@@ -685,6 +760,20 @@ __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonA
           commit(empty_bar(stage));
           ++n_consumed;
         }
+      };
+      for (; !failed && w.locate(); w.advance(), ++it) {
+        const int acc = it % kAccs;
+        const uint32_t acc_phase = (it / kAccs) & 1;
+        if (!wait(tempty_bar(acc), acc_phase ^ 1u)) {
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * Tile::kN;
+        if (w.symmetric())
+          products(std::integral_constant<int, 0>(), w.phase == kMuonGram ? kb_n : kb_m, d_tmem);
+        else
+          products(std::integral_constant<int, 1>(), kb_m, d_tmem);
         if (failed) break;
         commit(tfull_bar(acc));
       }
@@ -700,33 +789,45 @@ __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonA
     constexpr int kHalf = Tile::kN / 2;                     // columns of an epilogue warp
     constexpr int kBlock = SHAPE == kMuonSingle ? 128 : 256;  // the symmetric products' unit of "above the diagonal"
     const int wq = warp & 3, half = (warp - 4) >> 2;
-    MuonEpilogue<PHASE> epi{a, maps, st, sE + (warp - 4) * 4 * kEpiPart, drain_bar + 8u * (1 + 2 * (warp - 4)), lane};
-    const int ncols = kSym ? a.m : a.n;
+    MuonEpilogue epi{a, sE + (warp - 4) * 4 * kEpiPart, drain_bar + 8u * (1 + 2 * (warp - 4)), lane};
     bool ok = true;
     int it = 0;
-    for (int u = first_unit; u < num_units; u += unit_step, ++it) {
+    auto unit = [&](auto phase_c) {
+      constexpr int PHASE = decltype(phase_c)::value;
+      constexpr bool kSym = PHASE == kMuonGram || PHASE == kMuonPoly;
+      const int src = w.step & 1;
+      const MuonStep st{steps.c[w.step][0], steps.c[w.step][1], steps.c[w.step][2]};
+      const CUtensorMap* e0 = PHASE == kMuonPoly ? &maps.ge : &maps.xe[src];
+      const CUtensorMap* e1 = PHASE == kMuonPoly ? nullptr : &maps.lo;
+      const CUtensorMap* o0 = PHASE == kMuonGram ? &maps.ge : PHASE == kMuonPoly ? &maps.pe : &maps.xe[1 - src];
+      const CUtensorMap* o1 = PHASE == kMuonGram ? &maps.gm : PHASE == kMuonPoly ? &maps.pm : &maps.lo;
       const int acc = it % kAccs;
       const uint32_t acc_phase = (it / kAccs) & 1;
-      const MuonUnit t = muon_unit<PHASE, SHAPE>(u, tiles_m, tiles_n);
-      const int row0 = t.tm * Tile::kM + static_cast<int>(rank) * 128 + wq * 32;
-      const int col0 = t.tn * Tile::kN + half * kHalf;
+      const int ncols = kSym ? a.m : a.n;
+      const int row0 = w.tm * Tile::kM + static_cast<int>(rank) * 128 + wq * 32;
+      const int col0 = w.tn * Tile::kN + half * kHalf;
       // below the diagonal blocks a tile of a symmetric product repeats what
       // another tile mirrors
-      const int block_m = t.tm * Tile::kM / kBlock, block_n = col0 / kBlock;
+      const int block_m = w.tm * Tile::kM / kBlock, block_n = col0 / kBlock;
       const bool skip = row0 >= a.m || col0 >= ncols || (kSym && block_n < block_m);
       const int groups = skip ? 0 : min(kHalf / 32, (ncols - col0 + 31) / 32);
       float factor = 0.f;
-      if (groups > 0) {
-        epi.load(t.mat, row0, col0);
-        if (!kSym && row0 + lane < a.m) factor = st.a + a.diag[static_cast<int64_t>(t.mat) * a.m + row0 + lane];
-        if (PHASE == kMuonLast) epi.prefetch_weight(t.mat, row0, col0, kHalf);
+      if (PHASE != kMuonGram && groups > 0) {
+        ok = true;
+        if (lane == 0) ok = wait_done(a.done + w.mat, w.needed() * kParts, err, a.timeout_ns);
+        ok = __all_sync(kAll, ok);
+        if (!ok) return;
+        epi.load(e0, e1, w.mat, row0, col0);
+        if (groups > 1) epi.load(e0, e1, w.mat, row0, col0 + 32);
+        if (!kSym && row0 + lane < a.m)
+          factor = st.a + __ldcg(a.diag + static_cast<int64_t>(w.mat) * a.m + row0 + lane);
+        if (PHASE == kMuonLast) epi.prefetch_weight(w.mat, row0, col0, kHalf);
       }
       ok = wait(tfull_bar(acc), acc_phase);
       ok = __all_sync(kAll, ok);
-      if (!ok) break;
+      if (!ok) return;
       tc_fence_after();
-      const uint32_t tbase =
-          tmem_base + (static_cast<uint32_t>(wq * 32) << 16) + acc * Tile::kN + half * kHalf;
+      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(wq * 32) << 16) + acc * Tile::kN + half * kHalf;
       auto release = [&] {
         tc_fence_before();
         if (rank == 0)
@@ -740,17 +841,35 @@ __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonA
         __syncwarp();
         uint32_t r[32];
         tmem_ld_32x32b_x32(tbase + g * 32, r);
-        if (g + 1 < groups) epi.load(t.mat, row0, col0 + (g + 1) * 32);
         tmem_ld_wait();
         tmem_regs_ready(r);
         if (g == groups - 1) release();
-        ok = epi.group(t.mat, row0, col0 + g * 32, kSym && block_n > block_m, factor, r);
+        ok = epi.group<PHASE>(st, o0, o1, g, w.mat, row0, col0 + g * 32, kSym && block_n > block_m, factor, r);
+        if (PHASE != kMuonGram && g + 2 < groups) epi.load(e0, e1, w.mat, row0, col0 + (g + 2) * 32);
       }
-      if (!ok) break;
+      if (!ok) return;
+      if (PHASE != kMuonLast) {
+        // this part of the tile is in global memory: say so
+        __syncwarp();
+        if (lane == 0) {
+          bulk_wait_group<0>();
+          add_release(a.done + w.mat, 1);
+        }
+      }
+    };
+    for (; ok && w.locate(); w.advance(), ++it) {
+      if (w.phase == kMuonGram)
+        unit(std::integral_constant<int, kMuonGram>());
+      else if (w.phase == kMuonPoly)
+        unit(std::integral_constant<int, kMuonPoly>());
+      else if (w.step + 1 < steps.count)
+        unit(std::integral_constant<int, kMuonApply>());
+      else
+        unit(std::integral_constant<int, kMuonLast>());
     }
     if (lane == 0) bulk_wait_group<0>();
     // a load that is still in flight lands before the CTA leaves
-    if (!ok && MuonEpilogue<PHASE>::kLoads && lane == 0)
+    if (!ok && lane == 0)
       for (; epi.uses < epi.loads; ++epi.uses)
         wait_limited(epi.bar + 8u * (epi.uses & 1u), (epi.uses >> 1) & 1u, a.timeout_ns);
   }
@@ -771,25 +890,12 @@ __device__ __forceinline__ void muon_gemm_body(const MuonMaps& maps, const MuonA
   }
 }
 
-template <int PHASE, int SHAPE>
-__global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bounds__(kThreads, 1)
-    muon_gemm_kernel(const __grid_constant__ MuonMaps maps, const __grid_constant__ MuonArgs a,
-                     const __grid_constant__ MuonStep st) {
-  muon_gemm_body<PHASE, SHAPE>(maps, a, st);
-}
-
 template <int SHAPE>
-int64_t muon_units_t(int phase, const MuonArgs& a) {
+int64_t muon_units(int phase, const MuonArgs& a) {
   using Tile = MuonTile<SHAPE>;
   const bool sym = phase == kMuonGram || phase == kMuonPoly;
   const int tm = (a.m + Tile::kM - 1) / Tile::kM, tn = ((sym ? a.m : a.n) + Tile::kN - 1) / Tile::kN;
   return static_cast<int64_t>(a.count) * muon_units_per_matrix<SHAPE>(sym, tm, tn);
-}
-
-int64_t muon_units(int phase, const MuonArgs& a, int shape) {
-  return shape == kMuonSingle ? muon_units_t<kMuonSingle>(phase, a)
-         : shape == kMuonPair ? muon_units_t<kMuonPair>(phase, a)
-                              : muon_units_t<kMuonWide>(phase, a);
 }
 
 // A launch that may start while the one before it drains
@@ -808,36 +914,48 @@ cudaError_t launch_chained(void (*kern)(P...), dim3 grid, int threads, size_t sm
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int PHASE, int SHAPE>
-cudaError_t launch_product(const MuonMaps& maps, const MuonArgs& a, const MuonStep& st, int slots, cudaStream_t s) {
-  auto kern = muon_gemm_kernel<PHASE, SHAPE>;
+template <int SHAPE>
+cudaError_t launch_steps(const MuonMaps& maps, const MuonArgs& a, const MuonSteps& steps, int slots, cudaStream_t s) {
+  auto kern = muon_steps_kernel<SHAPE>;
   static const cudaError_t opted = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                         static_cast<int>(smem_bytes<SHAPE>()));
   if (opted != cudaSuccess) return opted;
-  const int n = static_cast<int>(std::min<int64_t>(muon_units_t<SHAPE>(PHASE, a), slots));
-  return launch_chained(kern, dim3(SHAPE == kMuonSingle ? n : 2 * n), kThreads, smem_bytes<SHAPE>(), s, maps, a, st);
-}
-
-template <int PHASE>
-cudaError_t launch_phase(int shape, const MuonMaps& maps, const MuonArgs& a, const MuonStep& st, int slots,
-                         cudaStream_t s) {
-  return shape == kMuonSingle ? launch_product<PHASE, kMuonSingle>(maps, a, st, slots, s)
-         : shape == kMuonPair ? launch_product<PHASE, kMuonPair>(maps, a, st, slots, s)
-                              : launch_product<PHASE, kMuonWide>(maps, a, st, slots, s);
+  const int64_t most = std::max(muon_units<SHAPE>(kMuonGram, a), muon_units<SHAPE>(kMuonApply, a));
+  const int n = static_cast<int>(std::min<int64_t>(most, slots));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(SHAPE == kMuonSingle ? n : 2 * n);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<SHAPE>();
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeCooperative;
+  attr.val.cooperative = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, maps, a, steps);
 }
 
 }  // namespace
 
-// Which tile a product runs on: the one whose rounds of tiles over the GPU take
-// least. A tile costs its k-blocks (clocks per 64-deep k-block) or its
-// epilogue, whichever is longer (a wide tile both: it has one accumulator), and
-// a launch the time to fill and drain.
-int muon_tile(int phase, const MuonArgs& a, int pairs, int sms) {
-  const int64_t kb = ((phase == kMuonGram ? a.n : a.m) + kBK - 1) / kBK;
-  auto rounds = [&](int shape, int slots) { return (muon_units(phase, a, shape) + slots - 1) / slots; };
-  const int64_t single = rounds(kMuonSingle, sms) * std::max<int64_t>(kb * 450, 2500);
-  const int64_t pair = rounds(kMuonPair, pairs) * std::max<int64_t>(kb * 700, 4000);
-  const int64_t wide = rounds(kMuonWide, pairs) * (kb * 1100 + 4000);
+// Which tile the products run on: the one that takes least by this model. A
+// step's units are spread evenly over the slots (units of several matrices
+// overlap; a single matrix's products follow one another); a unit costs its
+// k-blocks (clocks per 64-deep k-block), a wide one its epilogue too, and each
+// product its time to fill and drain.
+int muon_tile(const MuonArgs& a, int pairs, int sms) {
+  const int64_t kb_n = (a.n + kBK - 1) / kBK, kb_m = (a.m + kBK - 1) / kBK;
+  auto cost = [&](int64_t ug, int64_t ux, int64_t slots, int64_t per_kb, int64_t epilogue, int64_t fill) {
+    auto product = [&](int64_t units, int64_t kb) {
+      const int64_t unit = kb * per_kb + epilogue;
+      const int64_t rounds = (units + slots - 1) / slots;
+      // with several matrices a partly filled round is filled by another's units
+      return a.count > 1 ? std::max(unit, units * unit / slots) : rounds * unit;
+    };
+    return product(ug, kb_n) + product(ug, kb_m) + product(ux, kb_m) + 3 * fill;
+  };
+  const int64_t single = cost(muon_units<kMuonSingle>(kMuonGram, a), muon_units<kMuonSingle>(kMuonApply, a), sms, 600, 0, 9000);
+  const int64_t pair = cost(muon_units<kMuonPair>(kMuonGram, a), muon_units<kMuonPair>(kMuonApply, a), pairs, 680, 0, 13000);
+  const int64_t wide = cost(muon_units<kMuonWide>(kMuonGram, a), muon_units<kMuonWide>(kMuonApply, a), pairs, 1080, 14000, 8000);
   if (single <= pair && single <= wide) return kMuonSingle;
   return pair <= wide ? kMuonPair : kMuonWide;
 }
@@ -852,20 +970,16 @@ cudaError_t launch_muon_prepare(const MuonArgs& a, cudaStream_t s) {
   return launch_chained(muon_prepare_kernel, dim3(tiles, a.count), 256, 0, s, a);
 }
 
-cudaError_t launch_muon_gemm(int phase, int shape, const MuonMaps& maps, const MuonArgs& a, const MuonStep& st,
-                             int slots, cudaStream_t s) {
-  switch (phase) {
-    case kMuonGram: return launch_phase<kMuonGram>(shape, maps, a, st, slots, s);
-    case kMuonPoly: return launch_phase<kMuonPoly>(shape, maps, a, st, slots, s);
-    case kMuonApply: return launch_phase<kMuonApply>(shape, maps, a, st, slots, s);
-    case kMuonLast: return launch_phase<kMuonLast>(shape, maps, a, st, slots, s);
-    default: return cudaErrorInvalidValue;
-  }
+cudaError_t launch_muon_steps(int shape, const MuonMaps& maps, const MuonArgs& a, const MuonSteps& steps, int slots,
+                              cudaStream_t s) {
+  return shape == kMuonSingle ? launch_steps<kMuonSingle>(maps, a, steps, slots, s)
+         : shape == kMuonPair ? launch_steps<kMuonPair>(maps, a, steps, slots, s)
+                              : launch_steps<kMuonWide>(maps, a, steps, slots, s);
 }
 
 // CTA pairs that fit on the device at once (the three shapes take an SM each)
 int muon_max_clusters() {
-  auto kern = muon_gemm_kernel<kMuonApply, kMuonPair>;
+  auto kern = muon_steps_kernel<kMuonPair>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);

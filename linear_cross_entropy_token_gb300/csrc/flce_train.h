@@ -91,6 +91,7 @@ struct MuonArgs {
   float scale;
   // workspace
   uint32_t* ctrl;
+  uint32_t* done;                    // [count] finished tile parts of the products so far
   uint32_t* host_error;              // pinned host word: first device-side error
   double* norm;                      // [count][kMuonNormBlocks]
   float* diag;                       // [count][m]: diagonal of B
@@ -115,23 +116,23 @@ struct MuonSteps {
 
 struct MuonStep {
   float a, b, c;                     // X = aX + (bA + cA^2) X
-  int32_t src;                       // hi[src] holds X; the next X goes to hi[1 - src]
 };
 
-// TMA descriptors of one product. Epilogue boxes: 32 columns x 32 rows.
+// TMA descriptors of the products: X (either buffer) as K-major operand and as
+// right operand of B X, A and B as K-major operands, and what the epilogues
+// read and write in boxes of 32 x 32: X hi, X lo, A, B and the mirror images
+// of A and B. Step k reads X from buffer k % 2 and writes it to the other.
 struct MuonMaps {
-  CUtensorMap a, b;                  // operands
-  CUtensorMap e0, e1;                // read by the epilogue: A, or X hi and lo (lo also written)
-  CUtensorMap o0, o1;                // written: the tile (X hi), its mirror image
+  CUtensorMap xk[2], xn[2], xe[2], lo, gk, ge, gm, pk, pe, pm;
 };
 
 cudaError_t launch_muon_momentum(const MuonArgs& a, cudaStream_t s);
 cudaError_t launch_muon_prepare(const MuonArgs& a, cudaStream_t s);
-// One product on tiles of one shape (slots: CTA pairs that fit at once, or SMs
+// All steps on tiles of one shape (slots: CTA pairs that fit at once, or SMs
 // for single tiles); muon_tile picks the shape.
-cudaError_t launch_muon_gemm(int phase, int shape, const MuonMaps& maps, const MuonArgs& a, const MuonStep& st,
-                             int slots, cudaStream_t s);
-int muon_tile(int phase, const MuonArgs& a, int pairs, int sms);
+cudaError_t launch_muon_steps(int shape, const MuonMaps& maps, const MuonArgs& a, const MuonSteps& steps, int slots,
+                              cudaStream_t s);
+int muon_tile(const MuonArgs& a, int pairs, int sms);
 int muon_max_clusters();
 
 // flce_muon_small.cu: matrices whose short side is at most 128, one launch

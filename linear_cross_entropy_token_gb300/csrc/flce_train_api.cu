@@ -95,7 +95,7 @@ constexpr int64_t kMuonMaxDim = 65536;
 constexpr uint64_t kMuonGroupBytes = 2ull << 30;
 
 struct MuonLayout {
-  uint64_t ctrl = 0, norm = 0, diag = 0, hi[2] = {0, 0}, lo = 0, gram = 0, poly = 0, total = 0;
+  uint64_t ctrl = 0, done = 0, norm = 0, diag = 0, hi[2] = {0, 0}, lo = 0, gram = 0, poly = 0, total = 0;
 };
 
 struct MuonSizes {
@@ -121,6 +121,7 @@ MuonLayout muon_layout(int64_t rows, int64_t cols, int64_t count) {
     return at;
   };
   l.ctrl = take(kCtrlWords * 4);
+  l.done = take(kMuonMaxMats * 4);
   l.norm = take(static_cast<uint64_t>(count) * kMuonNormBlocks * 8);
   l.diag = take(static_cast<uint64_t>(count) * z.m * 4);
   const uint64_t x = static_cast<uint64_t>(count) * z.m * z.ldx * 2;
@@ -171,8 +172,7 @@ void muon_map_bounds(double a, double b, double c, double r, double* poly, doubl
 }
 
 bool map_half_3d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t mats, uint64_t ld,
-                 uint32_t box_cols, uint32_t box_rows, std::string* why,
-                 CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+                 uint32_t box_cols, uint32_t box_rows, std::string* why, CUtensorMapSwizzle swizzle) {
   const uint64_t dims[3] = {cols, rows, mats};
   const uint64_t strides[2] = {ld * 2, ld * 2 * rows};
   const uint32_t box[3] = {box_cols, box_rows, 1};
@@ -228,6 +228,7 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
   a.lr = static_cast<float>(q->lr);
   a.scale = static_cast<float>(q->scale);
   a.ctrl = reinterpret_cast<uint32_t*>(ws + L.ctrl);
+  a.done = reinterpret_cast<uint32_t*>(ws + L.done);
   a.host_error = h->host_ctrl + kCtrlSticky;
   a.norm = reinterpret_cast<double*>(ws + L.norm);
   a.diag = reinterpret_cast<float*>(ws + L.diag);
@@ -244,6 +245,10 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
   const double dm = static_cast<double>(z.m), dn = static_cast<double>(z.n);
   const double gb = static_cast<double>(element_bytes(q->grad_dtype)), mb = mats[0].momentum ? 8.0 : 0.0;
   const double ob = mats[0].weight ? 2.0 * element_bytes(q->weight_dtype) : 1.0 * element_bytes(q->update_dtype);
+  const double flops = q->steps * count * (dm * (dm + 1) * dn + dm * dm * (dm + 1) + 2 * dm * dm * dn);
+  MuonSteps steps{};
+  steps.count = q->steps;
+  std::memcpy(steps.c, coefficients, sizeof(float) * 3 * q->steps);
   int cluster, chunks;
   if (h->muon_shape < 0 && muon_small_shape(z.m, z.n, count, &cluster, &chunks)) {
     auto known = h->muon_small.find({cluster, chunks});
@@ -251,58 +256,41 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
       known = h->muon_small.emplace(std::array<int, 2>{cluster, chunks}, muon_small_fits(cluster, chunks)).first;
     if (known->second) {
       a.cluster = cluster;
-      MuonSteps steps{};
-      steps.count = q->steps;
-      std::memcpy(steps.c, coefficients, sizeof(float) * 3 * q->steps);
-      FLCE_LAUNCH(FLCE_K_MUON_SMALL, q->steps * count * (dm * (dm + 1) * dn + dm * dm * (dm + 1) + 2 * dm * dm * dn),
-                  el * (gb + mb + ob), launch_muon_small(a, steps, chunks, s));
+      FLCE_LAUNCH(FLCE_K_MUON_SMALL, flops, el * (gb + mb + ob), launch_muon_small(a, steps, chunks, s));
       return FLCE_OK;
     }
   }
 
-  // X as K-major operand (rows of 64 k) and as right operand of B X (64 columns
-  // by 64 k); A and B as K-major operands (both symmetric); and what the
-  // epilogues read and write
-  CUtensorMap xk[2], xn[2], xe[2], lo, gk, ge, gm, pk, pe, pm;
+  MuonMaps maps;
   std::string why;
   bool ok = true;
+  auto operand = [&](CUtensorMap* m, const void* base, uint64_t cols, uint64_t ld, uint32_t box_rows) {
+    ok = ok && map_half_3d(m, base, cols, z.m, count, ld, 64, box_rows, &why, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  auto block = [&](CUtensorMap* m, const void* base, uint64_t cols, uint64_t ld, CUtensorMapSwizzle swizzle) {
+    ok = ok && map_half_3d(m, base, cols, z.m, count, ld, 32, 32, &why, swizzle);
+  };
   for (int i = 0; i < 2; ++i) {
-    ok = ok && map_half_3d(&xk[i], a.hi[i], z.n, z.m, count, z.ldx, 64, 128, &why);
-    ok = ok && map_half_3d(&xn[i], a.hi[i], z.n, z.m, count, z.ldx, 64, 64, &why);
-    ok = ok && map_half_3d(&xe[i], a.hi[i], z.n, z.m, count, z.ldx, 32, 32, &why, CU_TENSOR_MAP_SWIZZLE_64B);
+    operand(&maps.xk[i], a.hi[i], z.n, z.ldx, 128);
+    operand(&maps.xn[i], a.hi[i], z.n, z.ldx, 64);
+    block(&maps.xe[i], a.hi[i], z.n, z.ldx, CU_TENSOR_MAP_SWIZZLE_64B);
   }
-  ok = ok && map_half_3d(&lo, a.lo, z.n, z.m, count, z.ldx, 32, 32, &why, CU_TENSOR_MAP_SWIZZLE_64B);
-  ok = ok && map_half_3d(&gk, a.gram, z.m, z.m, count, z.lda, 64, 128, &why);
-  ok = ok && map_half_3d(&ge, a.gram, z.m, z.m, count, z.lda, 32, 32, &why, CU_TENSOR_MAP_SWIZZLE_64B);
-  ok = ok && map_half_3d(&gm, a.gram, z.m, z.m, count, z.lda, 32, 32, &why, CU_TENSOR_MAP_SWIZZLE_NONE);
-  ok = ok && map_half_3d(&pk, a.poly, z.m, z.m, count, z.lda, 64, 128, &why);
-  ok = ok && map_half_3d(&pe, a.poly, z.m, z.m, count, z.lda, 32, 32, &why, CU_TENSOR_MAP_SWIZZLE_64B);
-  ok = ok && map_half_3d(&pm, a.poly, z.m, z.m, count, z.lda, 32, 32, &why, CU_TENSOR_MAP_SWIZZLE_NONE);
+  block(&maps.lo, a.lo, z.n, z.ldx, CU_TENSOR_MAP_SWIZZLE_64B);
+  operand(&maps.gk, a.gram, z.m, z.lda, 128);
+  block(&maps.ge, a.gram, z.m, z.lda, CU_TENSOR_MAP_SWIZZLE_64B);
+  block(&maps.gm, a.gram, z.m, z.lda, CU_TENSOR_MAP_SWIZZLE_NONE);
+  operand(&maps.pk, a.poly, z.m, z.lda, 128);
+  block(&maps.pe, a.poly, z.m, z.lda, CU_TENSOR_MAP_SWIZZLE_64B);
+  block(&maps.pm, a.poly, z.m, z.lda, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (!ok) return fail(h, FLCE_ERR_CUDA, "%s", why.c_str());
 
   FLCE_LAUNCH(FLCE_K_MUON_MOMENTUM, 0.0, el * (gb + mb), launch_muon_momentum(a, s));
   FLCE_LAUNCH(FLCE_K_MUON_PREPARE, 0.0, el * ((mats[0].momentum ? 4.0 + (q->nesterov ? gb : 0.0) : gb) + 4.0),
               launch_muon_prepare(a, s));
   // the handle's tile shape where it was given one, else by the rule
-  auto product = [&](int phase, const MuonMaps& maps, const MuonStep& st) {
-    const int shape = h->muon_shape >= 0 ? h->muon_shape : muon_tile(phase, a, h->muon_clusters, h->num_sms);
-    return launch_muon_gemm(phase, shape, maps, a, st, shape == kMuonSingle ? h->num_sms : h->muon_clusters, s);
-  };
-  for (int k = 0; k < q->steps; ++k) {
-    MuonStep st;
-    st.a = coefficients[3 * k];
-    st.b = coefficients[3 * k + 1];
-    st.c = coefficients[3 * k + 2];
-    st.src = k & 1;
-    FLCE_LAUNCH(FLCE_K_MUON_GRAM, count * dm * (dm + 1) * dn, count * (2 * dm * dn + 2 * dm * dm),
-                product(kMuonGram, {xk[st.src], xk[st.src], ge, ge, ge, gm}, st));
-    FLCE_LAUNCH(FLCE_K_MUON_POLY, count * dm * dm * (dm + 1), count * 4 * dm * dm,
-                product(kMuonPoly, {gk, gk, ge, ge, pe, pm}, st));
-    const bool last = k == q->steps - 1;
-    FLCE_LAUNCH(last ? FLCE_K_MUON_RESULT : FLCE_K_MUON_APPLY, count * 2 * dm * dm * dn,
-                count * (2 * dm * dm + (last ? 8 : 10) * dm * dn),
-                product(last ? kMuonLast : kMuonApply, {pk, xn[st.src], xe[st.src], lo, xe[1 - st.src], lo}, st));
-  }
+  const int shape = h->muon_shape >= 0 ? h->muon_shape : muon_tile(a, h->muon_clusters, h->num_sms);
+  FLCE_LAUNCH(FLCE_K_MUON_STEPS, flops, q->steps * count * (12.0 * dm * dn + 6.0 * dm * dm),
+              launch_muon_steps(shape, maps, a, steps, shape == kMuonSingle ? h->num_sms : h->muon_clusters, s));
   return FLCE_OK;
 }
 

@@ -28,8 +28,7 @@ KERNEL_KINDS = ["count_valid", "gemm_logits_lse", "lse_combine", "dlogits_inplac
                 "gemm_dlogits_recompute", "gemm_dx", "dx_split_reduce", "gemm_dw",
                 "loss_finalize", "simt_gemm_f32", "simt_tile_stats_f32", "gemm_dx_dw",
                 "device_result", "combine_dlogits", "h2d_copy", "route", "route_finish",
-                "route_backward", "muon_momentum", "muon_prepare", "muon_gram", "muon_poly",
-                "muon_apply", "muon_result", "muon_small"]
+                "route_backward", "muon_momentum", "muon_prepare", "muon_steps", "muon_small"]
 
 
 class FlceError(RuntimeError):
