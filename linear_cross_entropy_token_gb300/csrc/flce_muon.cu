@@ -27,6 +27,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "flce_muon.cuh"
@@ -45,6 +46,7 @@ __global__ void __launch_bounds__(256) muon_momentum_kernel(const __grid_constan
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     if (blockIdx.y == 0) a.ctrl[kCtrlError] = 0;
     a.done[blockIdx.y] = 0;
+    a.partial[blockIdx.y] = 0;
   }
   const uint32_t step = a.norm_blocks * 256u;
   const uint32_t first = blockIdx.x * 256u + threadIdx.x;
@@ -272,12 +274,12 @@ struct MuonWalk {
   using Tile = MuonTile<SHAPE>;
   int tiles_m, tiles_s, tiles_n;   // tile rows; tile columns of the symmetric products and of B X
   int per_s, per_x;                // tiles per matrix of either
-  int count, slots, steps;
+  int count, slots, steps, splits;
   int step = 0, phase = 0, u;
-  int mat, tm, tn;
+  int mat, tile, split, tm, tn;
 
   __device__ __forceinline__ MuonWalk(const MuonArgs& a, int steps_, int slot, int slots_)
-      : count(a.count), slots(slots_), steps(steps_), u(slot) {
+      : count(a.count), slots(slots_), steps(steps_), splits(a.splits), u(slot) {
     tiles_m = (a.m + Tile::kM - 1) / Tile::kM;
     tiles_s = (a.m + Tile::kN - 1) / Tile::kN;
     tiles_n = (a.n + Tile::kN - 1) / Tile::kN;
@@ -285,10 +287,16 @@ struct MuonWalk {
     per_x = muon_units_per_matrix<SHAPE>(false, tiles_m, tiles_n);
   }
   __device__ __forceinline__ bool symmetric() const { return phase < kMuonApply; }
+  // Units of a matrix: X Xt, whose sum may be split over several units per
+  // tile, has its tiles once per split, the last split (which adds the others)
+  // last.
+  __device__ __forceinline__ int per_matrix() const {
+    return phase == kMuonGram ? per_s * splits : phase == kMuonPoly ? per_s : per_x;
+  }
   // to the unit at u; false past the last
   __device__ __forceinline__ bool locate() {
     for (;;) {
-      const int units = count * (symmetric() ? per_s : per_x);
+      const int units = count * per_matrix();
       if (u < units) break;
       u -= units;
       if (++phase == 3) {
@@ -296,9 +304,15 @@ struct MuonWalk {
         if (++step == steps) return false;
       }
     }
-    const int per = symmetric() ? per_s : per_x;
+    const int per = per_matrix();
     mat = u / per;
-    const int w = u - mat * per;
+    int w = u - mat * per;
+    split = splits - 1;
+    if (phase == kMuonGram && splits > 1) {
+      split = w / per_s;
+      w -= split * per_s;
+    }
+    tile = w;
     if (symmetric()) {
       // columns before tn hold R tn (tn + 1) / 2 tiles
       constexpr int R = Tile::kN / Tile::kM;
@@ -658,7 +672,9 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  const int kb_n = (a.n + kBK - 1) / kBK, kb_m = (a.m + kBK - 1) / kBK;   // k-blocks of X Xt, of the others
+  // k-blocks of X Xt, of one of its splits, of the other products
+  const int kb_n = (a.n + kBK - 1) / kBK, kb_split = (kb_n + a.splits - 1) / a.splits, kb_m = (a.m + kBK - 1) / kBK;
+  auto gram_blocks = [&](int split) { return min(kb_split, kb_n - split * kb_split); };
   MuonWalk<SHAPE> w(a, steps.count, slot, slots);
 
   if (warp == 0) {
@@ -682,7 +698,8 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
         }
         const int mA = w.tm * Tile::kM + static_cast<int>(rank) * 128;
         const int nB = w.tn * Tile::kN + static_cast<int>(rank) * 128;
-        const int num_kb = w.phase == kMuonGram ? kb_n : kb_m;
+        const int num_kb = w.phase == kMuonGram ? gram_blocks(w.split) : kb_m;
+        const int k_first = w.phase == kMuonGram ? w.split * kb_split * kBK : 0;
         for (int kb = 0; kb < num_kb; ++kb) {
           const int stage = n_issued % kStages;
           const uint32_t phase = (n_issued / kStages) & 1u;
@@ -693,7 +710,7 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
           if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), (kPaired ? 2 : 1) * kStageBytes);
           const uint32_t fb = kPaired ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
           const uint32_t sa = smem_u32(smem + stage * kStageBytes);
-          const int k0 = kb * kBK;
+          const int k0 = k_first + kb * kBK;
           auto load = [&](uint32_t dst, const CUtensorMap* m, int c0, int c1) {
             if (kPaired)
               tma_load_3d_pair(dst, m, fb, c0, c1, w.mat);
@@ -771,7 +788,7 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * Tile::kN;
         if (w.symmetric())
-          products(std::integral_constant<int, 0>(), w.phase == kMuonGram ? kb_n : kb_m, d_tmem);
+          products(std::integral_constant<int, 0>(), w.phase == kMuonGram ? gram_blocks(w.split) : kb_m, d_tmem);
         else
           products(std::integral_constant<int, 1>(), kb_m, d_tmem);
         if (failed) break;
@@ -836,6 +853,23 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
           mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
       };
       if (groups == 0) release();
+      // X Xt in splits: every split but the last leaves its fp32 sums, a 32 x 32
+      // block per warp and group as [8][lane][4], where the last split's same
+      // warps and lanes read them, in the order of the splits
+      const bool partial = PHASE == kMuonGram && w.split + 1 < w.splits;
+      const bool joins = PHASE == kMuonGram && w.splits > 1 && !partial;
+      float4* sums = nullptr;
+      if (partial || joins) {
+        const int64_t tile = (static_cast<int64_t>(w.mat) * (w.splits - 1) + (partial ? w.split : 0)) * w.per_s + w.tile;
+        const int block = ((static_cast<int>(rank) * 4 + wq) * 2 + half) * (kHalf / 32);
+        sums = reinterpret_cast<float4*>(a.sums) + (tile * (Tile::kM * Tile::kN / 1024) + block) * 256 + lane;
+      }
+      if (joins && groups > 0) {
+        const uint32_t parts = static_cast<uint32_t>((w.step + 1) * (w.splits - 1) * w.per_s) * kParts;
+        if (lane == 0) ok = wait_done(a.partial + w.mat, parts, err, a.timeout_ns);
+        ok = __all_sync(kAll, ok);
+        if (!ok) return;
+      }
 #pragma unroll 1
       for (int g = 0; g < groups && ok; ++g) {
         __syncwarp();
@@ -844,6 +878,31 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
         tmem_ld_wait();
         tmem_regs_ready(r);
         if (g == groups - 1) release();
+        if constexpr (PHASE == kMuonGram) {
+          if (partial) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              __stcg(sums + g * 256 + j * 32,
+                     make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]), __uint_as_float(r[4 * j + 2]),
+                                 __uint_as_float(r[4 * j + 3])));
+            continue;
+          }
+          if (joins) {
+            for (int s = 0; s + 1 < w.splits; ++s) {   // onto this split's own, in order
+              float4 v[8];
+              const float4* from = sums + static_cast<int64_t>(s) * w.per_s * (Tile::kM * Tile::kN / 4) + g * 256;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[j] = __ldcg(from + j * 32);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) + v[j].x);
+                r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) + v[j].y);
+                r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) + v[j].z);
+                r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) + v[j].w);
+              }
+            }
+          }
+        }
         ok = epi.group<PHASE>(st, o0, o1, g, w.mat, row0, col0 + g * 32, kSym && block_n > block_m, factor, r);
         if (PHASE != kMuonGram && g + 2 < groups) epi.load(e0, e1, w.mat, row0, col0 + (g + 2) * 32);
       }
@@ -853,7 +912,7 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
         __syncwarp();
         if (lane == 0) {
           bulk_wait_group<0>();
-          add_release(a.done + w.mat, 1);
+          add_release((partial ? a.partial : a.done) + w.mat, 1);
         }
       }
     };
@@ -920,7 +979,7 @@ cudaError_t launch_steps(const MuonMaps& maps, const MuonArgs& a, const MuonStep
   static const cudaError_t opted = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                         static_cast<int>(smem_bytes<SHAPE>()));
   if (opted != cudaSuccess) return opted;
-  const int64_t most = std::max(muon_units<SHAPE>(kMuonGram, a), muon_units<SHAPE>(kMuonApply, a));
+  const int64_t most = std::max(a.splits * muon_units<SHAPE>(kMuonGram, a), muon_units<SHAPE>(kMuonApply, a));
   const int n = static_cast<int>(std::min<int64_t>(most, slots));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(SHAPE == kMuonSingle ? n : 2 * n);
@@ -937,27 +996,55 @@ cudaError_t launch_steps(const MuonMaps& maps, const MuonArgs& a, const MuonStep
 
 }  // namespace
 
-// Which tile the products run on: the one that takes least by this model. A
-// step's units are spread evenly over the slots (units of several matrices
-// overlap; a single matrix's products follow one another); a unit costs its
-// k-blocks (clocks per 64-deep k-block), a wide one its epilogue too, and each
-// product its time to fill and drain.
-int muon_tile(const MuonArgs& a, int pairs, int sms) {
-  const int64_t kb_n = (a.n + kBK - 1) / kBK, kb_m = (a.m + kBK - 1) / kBK;
-  auto cost = [&](int64_t ug, int64_t ux, int64_t slots, int64_t per_kb, int64_t epilogue, int64_t fill) {
-    auto product = [&](int64_t units, int64_t kb) {
-      const int64_t unit = kb * per_kb + epilogue;
-      const int64_t rounds = (units + slots - 1) / slots;
-      // with several matrices a partly filled round is filled by another's units
-      return a.count > 1 ? std::max(unit, units * unit / slots) : rounds * unit;
-    };
-    return product(ug, kb_n) + product(ug, kb_m) + product(ux, kb_m) + 3 * fill;
+// Tile shape and splits of X Xt: those that take least by this model of a
+// step, in nanoseconds. A unit costs its k-blocks (more per block the more of
+// the GPU reads L2 at once); a product follows its predecessor after its
+// epilogue and a flag's latency, with one matrix in whole rounds of units,
+// while several matrices fill each other's rounds; a wide tile's epilogue is
+// not overlapped. Splitting X Xt shortens its units where there are few of
+// them (a long X), and costs the last split the reading of the others' sums.
+MuonPlan muon_plan(const MuonArgs& a, int fixed_shape, int pairs, int sms) {
+  struct Cost {
+    double per_kb, full, epilogue;
+    bool overlapped;
+    int groups;   // 32-column groups of an epilogue warp
   };
-  const int64_t single = cost(muon_units<kMuonSingle>(kMuonGram, a), muon_units<kMuonSingle>(kMuonApply, a), sms, 600, 0, 9000);
-  const int64_t pair = cost(muon_units<kMuonPair>(kMuonGram, a), muon_units<kMuonPair>(kMuonApply, a), pairs, 680, 0, 13000);
-  const int64_t wide = cost(muon_units<kMuonWide>(kMuonGram, a), muon_units<kMuonWide>(kMuonApply, a), pairs, 1080, 14000, 8000);
-  if (single <= pair && single <= wide) return kMuonSingle;
-  return pair <= wide ? kMuonPair : kMuonWide;
+  static const Cost costs[3] = {{270, 180, 2000, true, 2}, {330, 60, 4500, true, 4}, {540, 20, 9000, false, 8}};
+  const double latency = 3500, join = 1200, join_group = 600;
+  const int kb_n = (a.n + kBK - 1) / kBK, kb_m = (a.m + kBK - 1) / kBK;
+  MuonPlan best;
+  double best_ns = 0;
+  for (int shape = 0; shape < 3; ++shape) {
+    if (fixed_shape >= 0 && shape != fixed_shape) continue;
+    const Cost& c = costs[shape];
+    const double slots = shape == kMuonSingle ? sms : pairs;
+    const int64_t sym = shape == kMuonSingle ? muon_units<kMuonSingle>(kMuonGram, a)
+                        : shape == kMuonPair ? muon_units<kMuonPair>(kMuonGram, a)
+                                             : muon_units<kMuonWide>(kMuonGram, a);
+    const int64_t full = shape == kMuonSingle ? muon_units<kMuonSingle>(kMuonApply, a)
+                         : shape == kMuonPair ? muon_units<kMuonPair>(kMuonApply, a)
+                                              : muon_units<kMuonWide>(kMuonApply, a);
+    auto product = [&](double units, double kb) {
+      const double unit = kb * (c.per_kb + c.full * std::min(1.0, units / slots)) + (c.overlapped ? 0 : c.epilogue);
+      const double rounds = a.count > 1 ? std::max(1.0, units / slots) : std::ceil(units / slots);
+      return rounds * unit + (c.overlapped ? c.epilogue : 0) + latency;
+    };
+    for (int splits = 1; splits <= kMuonMaxSplits; ++splits) {
+      const int kb = (kb_n + splits - 1) / splits;
+      if (splits > 1 && (kb < kMuonMinSplitBlocks || (kb_n + kb - 1) / kb != splits || sym * splits > slots)) continue;
+      const int64_t tile_bytes = 4ll * (shape == kMuonSingle ? 128 * 128 : shape == kMuonPair ? 256 * 256 : 256 * 512);
+      if ((splits - 1) * sym * tile_bytes > a.sums_bytes) continue;
+      const double ns = product(static_cast<double>(sym) * splits, kb) +
+                        (splits > 1 ? join + (splits - 1) * join_group * c.groups : 0) +
+                        product(static_cast<double>(sym), kb_m) + product(static_cast<double>(full), kb_m);
+      if (best.shape < 0 || ns < best_ns) {
+        best.shape = shape;
+        best.splits = splits;
+        best_ns = ns;
+      }
+    }
+  }
+  return best;
 }
 
 cudaError_t launch_muon_momentum(const MuonArgs& a, cudaStream_t s) {

@@ -92,6 +92,10 @@ struct MuonArgs {
   // workspace
   uint32_t* ctrl;
   uint32_t* done;                    // [count] finished tile parts of the products so far
+  uint32_t* partial;                 // [count] finished parts of the splits of X Xt but the last
+  float* sums;                       // fp32 sums of those splits
+  int64_t sums_bytes;
+  int32_t splits;                    // units per tile of X Xt
   uint32_t* host_error;              // pinned host word: first device-side error
   double* norm;                      // [count][kMuonNormBlocks]
   float* diag;                       // [count][m]: diagonal of B
@@ -129,10 +133,14 @@ struct MuonMaps {
 cudaError_t launch_muon_momentum(const MuonArgs& a, cudaStream_t s);
 cudaError_t launch_muon_prepare(const MuonArgs& a, cudaStream_t s);
 // All steps on tiles of one shape (slots: CTA pairs that fit at once, or SMs
-// for single tiles); muon_tile picks the shape.
+// for single tiles); muon_plan picks it and a.splits.
 cudaError_t launch_muon_steps(int shape, const MuonMaps& maps, const MuonArgs& a, const MuonSteps& steps, int slots,
                               cudaStream_t s);
-int muon_tile(const MuonArgs& a, int pairs, int sms);
+constexpr int kMuonMaxSplits = 8, kMuonMinSplitBlocks = 8;   // and the k-blocks of a split at least
+struct MuonPlan {
+  int shape = -1, splits = 1;
+};
+MuonPlan muon_plan(const MuonArgs& a, int fixed_shape, int pairs, int sms);
 int muon_max_clusters();
 
 // flce_muon_small.cu: matrices whose short side is at most 128, one launch

@@ -93,9 +93,10 @@ constexpr int64_t kMuonMaxDim = 65536;
 // matrices per group of launches: as many as fit this much workspace (one at
 // least); a larger group only saves launches once the GPU is full
 constexpr uint64_t kMuonGroupBytes = 2ull << 30;
+constexpr uint64_t kMuonSumsBytes = 40ull << 20;
 
 struct MuonLayout {
-  uint64_t ctrl = 0, done = 0, norm = 0, diag = 0, hi[2] = {0, 0}, lo = 0, gram = 0, poly = 0, total = 0;
+  uint64_t ctrl = 0, done = 0, sums = 0, sums_bytes = 0, norm = 0, diag = 0, hi[2] = {0, 0}, lo = 0, gram = 0, poly = 0, total = 0;
 };
 
 struct MuonSizes {
@@ -121,7 +122,7 @@ MuonLayout muon_layout(int64_t rows, int64_t cols, int64_t count) {
     return at;
   };
   l.ctrl = take(kCtrlWords * 4);
-  l.done = take(kMuonMaxMats * 4);
+  l.done = take(2 * kMuonMaxMats * 4);
   l.norm = take(static_cast<uint64_t>(count) * kMuonNormBlocks * 8);
   l.diag = take(static_cast<uint64_t>(count) * z.m * 4);
   const uint64_t x = static_cast<uint64_t>(count) * z.m * z.ldx * 2;
@@ -131,6 +132,15 @@ MuonLayout muon_layout(int64_t rows, int64_t cols, int64_t count) {
   l.lo = take(x);
   l.gram = take(g);
   l.poly = take(g);
+  // Splits of X Xt: their tiles' fp32 sums, at most a tile for every slot of
+  // the GPU (bounded here without knowing it)
+  const int64_t blocks = cdiv(z.n, 64);
+  const int64_t splits = std::min<int64_t>(kMuonMaxSplits, blocks / kMuonMinSplitBlocks);
+  if (splits > 1) {
+    const uint64_t area = align_up(z.m, 256) * align_up(z.m, 512);
+    l.sums_bytes = std::min<uint64_t>(4 * area * count * (splits - 1), kMuonSumsBytes);
+    l.sums = take(l.sums_bytes);
+  }
   l.total = off;
   return l;
 }
@@ -229,6 +239,9 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
   a.scale = static_cast<float>(q->scale);
   a.ctrl = reinterpret_cast<uint32_t*>(ws + L.ctrl);
   a.done = reinterpret_cast<uint32_t*>(ws + L.done);
+  a.partial = a.done + kMuonMaxMats;
+  a.sums = reinterpret_cast<float*>(ws + L.sums);
+  a.sums_bytes = static_cast<int64_t>(L.sums_bytes);
   a.host_error = h->host_ctrl + kCtrlSticky;
   a.norm = reinterpret_cast<double*>(ws + L.norm);
   a.diag = reinterpret_cast<float*>(ws + L.diag);
@@ -287,10 +300,12 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
   FLCE_LAUNCH(FLCE_K_MUON_MOMENTUM, 0.0, el * (gb + mb), launch_muon_momentum(a, s));
   FLCE_LAUNCH(FLCE_K_MUON_PREPARE, 0.0, el * ((mats[0].momentum ? 4.0 + (q->nesterov ? gb : 0.0) : gb) + 4.0),
               launch_muon_prepare(a, s));
-  // the handle's tile shape where it was given one, else by the rule
-  const int shape = h->muon_shape >= 0 ? h->muon_shape : muon_tile(a, h->muon_clusters, h->num_sms);
+  // on the handle's tile shape where it was given one
+  const MuonPlan plan = muon_plan(a, h->muon_shape, h->muon_clusters, h->num_sms);
+  a.splits = plan.splits;
   FLCE_LAUNCH(FLCE_K_MUON_STEPS, flops, q->steps * count * (12.0 * dm * dn + 6.0 * dm * dm),
-              launch_muon_steps(shape, maps, a, steps, shape == kMuonSingle ? h->num_sms : h->muon_clusters, s));
+              launch_muon_steps(plan.shape, maps, a, steps,
+                                plan.shape == kMuonSingle ? h->num_sms : h->muon_clusters, s));
   return FLCE_OK;
 }
 

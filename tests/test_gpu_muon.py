@@ -42,7 +42,7 @@ def gaussian(rows, cols, seed, scale=1e-3):
 
 SHAPES = [(1, 1), (1, 9), (9, 1), (5, 64), (64, 5), (33, 33), (64, 64), (65, 130), (128, 128), (129, 257), (257, 129),
           (128, 256), (100, 257), (512, 128), (128, 1024), (1500, 60), (70, 2100), (4096, 128), (128, 4097),
-          (256, 256), (300, 1000), (1000, 300), (512, 513), (700, 640), (1024, 96), (72, 5000), (2000, 1100)]
+          (200, 3000), (5000, 300), (40, 4600), (256, 256), (300, 1000), (1000, 300), (512, 513), (700, 640), (1024, 96), (72, 5000), (2000, 1100)]
 
 
 @pytest.mark.parametrize("rows,cols", SHAPES)

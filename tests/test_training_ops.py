@@ -130,10 +130,11 @@ def test_coefficients_and_options():
 def test_workspaces_and_null_handles():
     lib = flce.load()
     one = workspace_bytes(1024, 4096)
-    # X in three fp16 buffers, A and B: 3 m n + 2 m^2 halves
-    assert 0 <= one - 2 * (3 * 1024 * 4096 + 2 * 1024 * 1024) <= 16384
+    # X in three fp16 buffers, A and B: 3 m n + 2 m^2 halves; and the splits of X Xt: up to seven
+    # fp32 sums of A, at most 40 MiB
+    assert 0 <= one - 2 * (3 * 1024 * 4096 + 2 * 1024 * 1024) - 7 * 4 * 1024 * 1024 <= 16384
     assert workspace_bytes(4096, 1024) == one
-    assert workspace_bytes(1024, 4096, 10) > 9 * one
+    assert workspace_bytes(1024, 4096, 10) > 10 * 2 * (3 * 1024 * 4096 + 2 * 1024 * 1024)
     assert workspace_bytes(1024, 4096, 10000) <= 2 << 30
     assert workspace_bytes(65536, 65536) > 0
     for bad in ((0, 4, 1), (4, 0, 1), (65537, 4, 1), (4, 4, 0), (4, 4, -1)):
