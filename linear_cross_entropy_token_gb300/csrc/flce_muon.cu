@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(256) muon_momentum_kernel(const __grid_constan
   if (threadIdx.x == 0) {
     double s = 0.0;
     for (int w = 0; w < 8; ++w) s += sh[w];
-    a.norm[blockIdx.y * kMuonNormBlocks + blockIdx.x] = s;
+    a.norm[blockIdx.y * kMuonNormBlocks + blockIdx.x] = pack_sum(s);
   }
 }
 
@@ -116,81 +116,133 @@ __global__ void __launch_bounds__(256) muon_momentum_kernel(const __grid_constan
 
 constexpr int kTile = 64;
 
-// A 64 x 64 tile of u through shared memory, which also transposes it where X
-// is the transpose; whole 16-byte stores (a row of X has room to a multiple of
-// 64 elements, and the tile holds zeros past the matrix). Bound by HBM.
+// Where rows stay rows (and are aligned), 16 rows x 256 columns per turn of a
+// block, 8 neighbours per thread. Else 64 x 64 tiles through shared memory,
+// which transposes them where X is the transpose. Whole 16-byte stores either
+// way: a row of X has room to a multiple of 64 elements, and what lies past the
+// matrix is zero. Bound by HBM (10 or 8 bytes read, 4 written per element).
 __global__ void __launch_bounds__(256) muon_prepare_kernel(const __grid_constant__ MuonArgs a) {
   __shared__ float tile[kTile][kTile + 1];
-  __shared__ float sh[2];
+  __shared__ float sh[2], sh_m[8];
+  __shared__ int sh_e[8];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const MuonMat& t = a.mat[blockIdx.y];
-  const int tiles_c = (a.cols + kTile - 1) / kTile;
-  const int r0 = (blockIdx.x / tiles_c) * kTile, c0 = (blockIdx.x % tiles_c) * kTile;
-  // u of this tile, unscaled
-  if (a.vec) {
-    const int col = c0 + 4 * (threadIdx.x & 15);
+  // Every block takes the factor from the partial sums itself, once, in 32-bit
+  // arithmetic: fp64 runs at a sixty-fourth of fp32's rate (a block per 64 x 64
+  // tile, each with one warp's fp64 sum, took 163 us at 4096 x 16384; this 140,
+  // where HBM's bound is 99).
+  float mant[kMuonNormBlocks / 256];
+  int expo[kMuonNormBlocks / 256], top = -30000;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = (threadIdx.x >> 4) + 16 * j;
-      const int64_t row = r0 + r;
-      float u[4] = {0.f, 0.f, 0.f, 0.f};
-      if (row < a.rows && col < a.cols) {
-        if (!t.momentum || a.nesterov) load4(t.grad, a.grad_dtype, row * t.ld_grad + col, u);
-        if (t.momentum) {
-          const float4 m = *reinterpret_cast<const float4*>(t.momentum + row * t.ld_momentum + col);
-          const float mv[4] = {m.x, m.y, m.z, m.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) u[e] = a.nesterov ? mv[e] * a.beta + u[e] * a.one_minus_beta : mv[e];
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) tile[r][4 * (threadIdx.x & 15) + e] = u[e];
-    }
-  } else {
-    const int tc = threadIdx.x & (kTile - 1), tr = threadIdx.x / kTile;
-    for (int r = tr; r < kTile; r += 256 / kTile) {
-      float u = 0.f;
-      if (r0 + r < a.rows && c0 + tc < a.cols) {
-        const int64_t row = r0 + r, col = c0 + tc;
-        if (t.momentum) {
-          u = t.momentum[row * t.ld_momentum + col];
-          if (a.nesterov) u = u * a.beta + load1(t.grad, a.grad_dtype, row * t.ld_grad + col) * a.one_minus_beta;
-        } else {
-          u = load1(t.grad, a.grad_dtype, row * t.ld_grad + col);
-        }
-      }
-      tile[r][tc] = u;
-    }
+  for (int j = 0; j < kMuonNormBlocks / 256; ++j) {
+    const int i = threadIdx.x + 256 * j;
+    const float2 v =
+        i < a.norm_blocks ? a.norm[blockIdx.y * kMuonNormBlocks + i] : make_float2(0.f, __int_as_float(-30000));
+    mant[j] = v.x;
+    expo[j] = __float_as_int(v.y);
+    top = max(top, expo[j]);
   }
-  // every block takes the factor from the partial sums itself, by one warp: the
-  // few fp64 units would make a block of 256 threads doing so the bound (302 us
-  // against HBM's 100 at 4096 x 16384)
-  if (threadIdx.x < 32) {
-    double s = 0.0;
-    for (int i = threadIdx.x; i < a.norm_blocks; i += 32) s += a.norm[blockIdx.y * kMuonNormBlocks + i];
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-    if (threadIdx.x == 0) norm_factors(s, a.eps, sh);
+  top = __reduce_max_sync(kAll, top);
+  if ((threadIdx.x & 31) == 0) sh_e[threadIdx.x >> 5] = top;
+  __syncthreads();
+  top = __reduce_max_sync(kAll, sh_e[threadIdx.x & 7]);
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < kMuonNormBlocks / 256; ++j) s += mant[j] * exp2f(static_cast<float>(max(expo[j] - top, -200)));
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+  if ((threadIdx.x & 31) == 0) sh_m[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = 0.f;
+    for (int w = 0; w < 8; ++w) s += sh_m[w];
+    norm_factors(ldexp(static_cast<double>(s), top), a.eps, sh);
   }
   __syncthreads();
   const float f1 = sh[0], f2 = sh[1];
-  const int64_t base = static_cast<int64_t>(blockIdx.y) * a.m * a.ldx;
+
+  // four neighbours of u at (row, col), unscaled
+  auto u4 = [&](int64_t row, int64_t col, float (&u)[4]) {
+    u[0] = u[1] = u[2] = u[3] = 0.f;
+    if (row < a.rows && col < a.cols) {
+      if (!t.momentum || a.nesterov) load4(t.grad, a.grad_dtype, row * t.ld_grad + col, u);
+      if (t.momentum) {
+        const float4 m = *reinterpret_cast<const float4*>(t.momentum + row * t.ld_momentum + col);
+        const float mv[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
-  for (int it = 0; it < 2; ++it) {
-    const int idx = threadIdx.x + 256 * it, r = idx >> 3, c = (idx & 7) * 8;
-    const int i = (a.transposed ? c0 : r0) + r, j = (a.transposed ? r0 : c0) + c;
+        for (int e = 0; e < 4; ++e) u[e] = a.nesterov ? mv[e] * a.beta + u[e] * a.one_minus_beta : mv[e];
+      }
+    }
+  };
+  // eight neighbours of X at (i, j)
+  const int64_t base = static_cast<int64_t>(blockIdx.y) * a.m * a.ldx;
+  auto x8 = [&](int i, int j, const float (&u)[8]) {
+    if (i >= a.m || j >= a.ldx) return;
     uint32_t h[4], l[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float x0 = (a.transposed ? tile[c + 2 * q][r] : tile[r][c + 2 * q]) * f1 * f2;
-      const float x1 = (a.transposed ? tile[c + 2 * q + 1][r] : tile[r][c + 2 * q + 1]) * f1 * f2;
-      split_half2(x0, x1, h[q], l[q]);
+    for (int q = 0; q < 4; ++q) split_half2(u[2 * q] * f1 * f2, u[2 * q + 1] * f1 * f2, h[q], l[q]);
+    const int64_t o = base + static_cast<int64_t>(i) * a.ldx + j;
+    *reinterpret_cast<uint4*>(a.hi[0] + o) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(a.lo + o) = make_uint4(l[0], l[1], l[2], l[3]);
+  };
+
+  if (a.vec && !a.transposed) {
+    const int tiles_c = (a.cols + 255) / 256, tiles = tiles_c * ((a.rows + 15) / 16);
+    for (int tl = blockIdx.x; tl < tiles; tl += gridDim.x) {
+      const int r = (tl / tiles_c) * 16 + (threadIdx.x >> 5), c = (tl % tiles_c) * 256 + (threadIdx.x & 31) * 8;
+      float u[2][2][4];
+#pragma unroll
+      for (int it = 0; it < 2; ++it) {
+        u4(r + 8 * it, c, u[it][0]);
+        u4(r + 8 * it, c + 4, u[it][1]);
+      }
+#pragma unroll
+      for (int it = 0; it < 2; ++it) {
+        const float v[8] = {u[it][0][0], u[it][0][1], u[it][0][2], u[it][0][3],
+                            u[it][1][0], u[it][1][1], u[it][1][2], u[it][1][3]};
+        x8(r + 8 * it, c, v);
+      }
     }
-    if (i < a.m && j < a.ldx) {
-      const int64_t o = base + static_cast<int64_t>(i) * a.ldx + j;
-      *reinterpret_cast<uint4*>(a.hi[0] + o) = make_uint4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<uint4*>(a.lo + o) = make_uint4(l[0], l[1], l[2], l[3]);
+    return;
+  }
+  const int tiles_c = (a.cols + kTile - 1) / kTile, tiles = tiles_c * ((a.rows + kTile - 1) / kTile);
+  for (int tl = blockIdx.x; tl < tiles; tl += gridDim.x) {
+    const int r0 = (tl / tiles_c) * kTile, c0 = (tl % tiles_c) * kTile;
+    if (a.vec) {
+      const int c = 4 * (threadIdx.x & 15);
+      float u[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u4(r0 + (threadIdx.x >> 4) + 16 * j, c0 + c, u[j]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tile[(threadIdx.x >> 4) + 16 * j][c + e] = u[j][e];
+    } else {
+      const int tc = threadIdx.x & (kTile - 1), tr = threadIdx.x / kTile;
+#pragma unroll 8
+      for (int r = tr; r < kTile; r += 256 / kTile) {
+        float u = 0.f;
+        if (r0 + r < a.rows && c0 + tc < a.cols) {
+          const int64_t row = r0 + r, col = c0 + tc;
+          if (t.momentum) {
+            u = t.momentum[row * t.ld_momentum + col];
+            if (a.nesterov) u = u * a.beta + load1(t.grad, a.grad_dtype, row * t.ld_grad + col) * a.one_minus_beta;
+          } else {
+            u = load1(t.grad, a.grad_dtype, row * t.ld_grad + col);
+          }
+        }
+        tile[r][tc] = u;
+      }
     }
+    __syncthreads();
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+      const int idx = threadIdx.x + 256 * it, r = idx >> 3, c = (idx & 7) * 8;
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = a.transposed ? tile[c + q][r] : tile[r][c + q];
+      x8((a.transposed ? c0 : r0) + r, (a.transposed ? r0 : c0) + c, v);
+    }
+    __syncthreads();
   }
 }
 
@@ -1052,9 +1104,13 @@ cudaError_t launch_muon_momentum(const MuonArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_muon_prepare(const MuonArgs& a, cudaStream_t s) {
-  const int tiles = ((a.rows + kTile - 1) / kTile) * ((a.cols + kTile - 1) / kTile);
-  return launch_chained(muon_prepare_kernel, dim3(tiles, a.count), 256, 0, s, a);
+cudaError_t launch_muon_prepare(const MuonArgs& a, int sms, cudaStream_t s) {
+  // eight blocks of 256 threads per SM, each over many tiles
+  const int64_t tiles = a.vec && !a.transposed
+                            ? static_cast<int64_t>((a.rows + 15) / 16) * ((a.cols + 255) / 256)
+                            : static_cast<int64_t>((a.rows + kTile - 1) / kTile) * ((a.cols + kTile - 1) / kTile);
+  const int64_t most = std::max<int64_t>(1, 8ll * sms / a.count);
+  return launch_chained(muon_prepare_kernel, dim3(static_cast<unsigned>(std::min(tiles, most)), a.count), 256, 0, s, a);
 }
 
 cudaError_t launch_muon_steps(int shape, const MuonMaps& maps, const MuonArgs& a, const MuonSteps& steps, int slots,

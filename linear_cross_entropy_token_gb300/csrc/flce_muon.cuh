@@ -107,6 +107,15 @@ __device__ __forceinline__ void norm_factors(double square_sum, double eps, floa
   f[1] = static_cast<float>(inv < 1e-30 ? inv * 0x1p64 : inv);
 }
 
+// A sum of squares as mantissa and exponent (int bits in y): 32-bit values that
+// neither over- nor underflow, for a sum that many blocks repeat.
+__device__ __forceinline__ float2 pack_sum(double s) {
+  int e = -30000;
+  double m = s;
+  if (s > 0.0 && s < 1e300) m = frexp(s, &e);
+  return make_float2(static_cast<float>(m), __int_as_float(e));
+}
+
 // fp16 operands: the type fields (bits 7-9 and 10-12) are 0
 __host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, uint32_t a_mn, uint32_t b_mn) {
   return (1u << 4) | (a_mn << 15) | (b_mn << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);

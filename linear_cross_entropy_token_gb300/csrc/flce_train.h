@@ -97,7 +97,7 @@ struct MuonArgs {
   int64_t sums_bytes;
   int32_t splits;                    // units per tile of X Xt
   uint32_t* host_error;              // pinned host word: first device-side error
-  double* norm;                      // [count][kMuonNormBlocks]
+  float2* norm;                      // [count][kMuonNormBlocks]: mantissa, exponent
   float* diag;                       // [count][m]: diagonal of B
   uint16_t* hi[2];                   // [count][m][ldx] fp16, X scaled by 2^12, two buffers
   uint16_t* lo;                      // [count][m][ldx] fp16 remainder of X
@@ -131,7 +131,7 @@ struct MuonMaps {
 };
 
 cudaError_t launch_muon_momentum(const MuonArgs& a, cudaStream_t s);
-cudaError_t launch_muon_prepare(const MuonArgs& a, cudaStream_t s);
+cudaError_t launch_muon_prepare(const MuonArgs& a, int sms, cudaStream_t s);
 // All steps on tiles of one shape (slots: CTA pairs that fit at once, or SMs
 // for single tiles); muon_plan picks it and a.splits.
 cudaError_t launch_muon_steps(int shape, const MuonMaps& maps, const MuonArgs& a, const MuonSteps& steps, int slots,

@@ -243,7 +243,7 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
   a.sums = reinterpret_cast<float*>(ws + L.sums);
   a.sums_bytes = static_cast<int64_t>(L.sums_bytes);
   a.host_error = h->host_ctrl + kCtrlSticky;
-  a.norm = reinterpret_cast<double*>(ws + L.norm);
+  a.norm = reinterpret_cast<float2*>(ws + L.norm);
   a.diag = reinterpret_cast<float*>(ws + L.diag);
   a.hi[0] = reinterpret_cast<uint16_t*>(ws + L.hi[0]);
   a.hi[1] = reinterpret_cast<uint16_t*>(ws + L.hi[1]);
@@ -299,7 +299,7 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
 
   FLCE_LAUNCH(FLCE_K_MUON_MOMENTUM, 0.0, el * (gb + mb), launch_muon_momentum(a, s));
   FLCE_LAUNCH(FLCE_K_MUON_PREPARE, 0.0, el * ((mats[0].momentum ? 4.0 + (q->nesterov ? gb : 0.0) : gb) + 4.0),
-              launch_muon_prepare(a, s));
+              launch_muon_prepare(a, h->num_sms, s));
   // on the handle's tile shape where it was given one
   const MuonPlan plan = muon_plan(a, h->muon_shape, h->muon_clusters, h->num_sms);
   a.splits = plan.splits;
