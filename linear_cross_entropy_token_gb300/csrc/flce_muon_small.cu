@@ -14,10 +14,13 @@
 //   TMEM           columns 0..127 the accumulator of X Xt, then of A A;
 //                  columns 128.. the accumulator of B X
 //
-// X Xt sums over the slabs: each CTA sends the rows of its partial product to
-// their owner (128 / C rows each) over distributed shared memory, the owner
-// adds the C parts in order and sends the rounded rows to every CTA. A A and B
-// are the same small work in every CTA. Rows past the short side are zero.
+// X Xt sums over the slabs: each CTA leaves its partial product in global memory
+// (L2), adds its share of the 128 x 128 elements over the C partial products in
+// order, leaves the rounded values as the image of A's tile, and loads that
+// whole; cluster barriers order the three. (An SM sends only about 15 bytes per
+// clock to its peers' shared memories: the same exchange that way, by stores or
+// bulk copies, took 8.6 and 7.6 us a step at 128 x 1024, this SUM_US.) A A and
+// B are the same small work in every CTA. Rows past the short side are zero.
 //
 // 512 threads; thread t works on row 32 (warp % 4) + lane of an accumulator,
 // and on one quarter of its columns. Every wait is bounded: one that runs out is
@@ -44,13 +47,6 @@ __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, float c, float d) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d)
-               : "memory");
-}
-__device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t a, uint32_t b) {
-  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
-}
 __device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
   asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
 }
@@ -71,6 +67,13 @@ __device__ __forceinline__ void tmem_regs_ready16(uint32_t (&r)[16]) {
                  "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
 
+// bulk copy from global to this CTA's shared memory, completing on its barrier
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
 // byte offset of 16-byte chunk j (8 fp16) of row r in a [128 rows][128 bytes] tile
 __device__ __forceinline__ uint32_t tile16(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
 
@@ -80,7 +83,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   constexpr int kSlab = 64 * NCH;
   constexpr uint32_t kCols = NCH <= 2 ? 256 : 512;   // TMEM: 128 + the slab
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bar_word;
+  __shared__ __align__(8) uint64_t bar_word[2];   // products done; A loaded
   __shared__ uint32_t tmem_slot;
   __shared__ float diag[128];
   __shared__ double norm_warp[kSmallWarps], norm_part[16];
@@ -92,24 +95,29 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   uint8_t* sLo = sHi + NCH * kChunkBytes;
   uint8_t* sA = sLo + NCH * kChunkBytes;
   uint8_t* sB = sA + kPanelBytes;
-  uint8_t* sR = sB;   // the owner's received rows: read before B is written
-
   const int C = static_cast<int>(a.cluster);
   const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const MuonMat& t = a.mat[blockIdx.x / C];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = 32 * (warp & 3) + lane, quarter = warp >> 2;   // of the accumulators
   const int slab0 = rank * kSlab;
-  const uint32_t bar = smem_u32(&bar_word);
+  const uint32_t bar = smem_u32(&bar_word[0]), bar_gram = smem_u32(&bar_word[1]);
+  // this matrix's partial products [C][16 warps][8][32 lanes] of four, and A's image
+  float4* partials = reinterpret_cast<float4*>(a.sums) + static_cast<int64_t>(blockIdx.x / C) * (C * 4096 + 2048);
+  uint8_t* image = reinterpret_cast<uint8_t*>(partials + C * 4096);
   uint32_t parity = 0;
+  auto wait_for = [&](uint32_t b, uint32_t par) {
+    if (!wait_limited(b, par, a.timeout_ns)) *reinterpret_cast<volatile uint32_t*>(a.host_error) = kErrTimeout;
+  };
   auto wait_products = [&] {
-    if (!wait_limited(bar, parity, a.timeout_ns)) *reinterpret_cast<volatile uint32_t*>(a.host_error) = kErrTimeout;
+    wait_for(bar, parity);
     parity ^= 1u;
     tc_fence_after();
   };
 
   if (threadIdx.x == 0) {
     mbar_init(bar, 1);
+    mbar_init(bar_gram, 1);
     fence_mbar_init();
     fence_proxy_async_smem();
   }
@@ -276,42 +284,43 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       tc_fence_before();
       __syncthreads();
     } else {
-      const int own_rows = 128 / C;
-      if (k > 0) cluster_wait();   // every CTA's B X is done with B, where the rows arrive
       {
-        const int owner = row / own_rows;
-        const uint32_t to = mapa_shared(smem_u32(sR) + (rank * own_rows + row - owner * own_rows) * 512, owner);
         uint32_t r[32];
         __syncwarp();
         tmem_ld_32x32b_x32(tmem_row + quarter * 32, r);
         tmem_ld_wait();
         tmem_regs_ready(r);
+        float4* to = partials + rank * 4096 + warp * 256 + lane;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int c16 = quarter * 8 + j;   // 16-byte chunk of the 512-byte row
-          st_cluster_v4(to + ((c16 ^ (row & 31)) << 4), __uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
-                        __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
-        }
+        for (int j = 0; j < 8; ++j)
+          __stcg(to + j * 32, make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                                          __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])));
       }
       tc_fence_before();
       cluster_sync();
-      for (int i = threadIdx.x; i < own_rows * 32; i += kSmallThreads) {
-        const int r = i >> 5, c16 = i & 31, grow = rank * own_rows + r;
+      // 128 runs of 32 lanes: run b is warp b / 8's vector b % 8, columns 4 (b % 8)
+      // of that warp's quarter, a row per lane
+      for (int b = rank * (128 / C) + warp; b < (rank + 1) * (128 / C); b += kSmallWarps) {
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4* from = partials + b * 32 + lane;
+#pragma unroll 8
         for (int src = 0; src < C; ++src) {
-          const float4 v =
-              *reinterpret_cast<const float4*>(sR + (src * own_rows + r) * 512 + ((c16 ^ (grow & 31)) << 4));
+          const float4 v = __ldcg(from + src * 4096);
           s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
         }
-        const uint32_t w0 = pack_half2(s.x * kGramScale, s.y * kGramScale);
-        const uint32_t w1 = pack_half2(s.z * kGramScale, s.w * kGramScale);
-        const uint32_t at = aA + (c16 >> 4) * kChunkBytes + tile16(grow, (c16 & 15) >> 1) + (c16 & 1) * 8;
-        for (int c = 0; c < C; ++c) st_cluster_v2(mapa_shared(at, c), w0, w1);
+        const int w = b >> 3, grow = 32 * (w & 3) + lane, col = (w >> 2) * 32 + (b & 7) * 4;
+        const uint32_t at = (col >> 6) * kChunkBytes + tile16(grow, (col & 63) >> 3) + (col & 4) * 2;
+        __stcg(reinterpret_cast<uint2*>(image + at), make_uint2(pack_half2(s.x * kGramScale, s.y * kGramScale),
+                                                                pack_half2(s.z * kGramScale, s.w * kGramScale)));
       }
       fence_proxy_async_all();
       cluster_sync();
-      fence_proxy_async_all();
-      __syncthreads();
+      if (threadIdx.x == 0) {
+        fence_proxy_async_all();
+        mbar_arrive_expect_tx(bar_gram, kPanelBytes);
+        bulk_load(smem_u32(sA), image, kPanelBytes, bar_gram);
+      }
+      wait_for(bar_gram, k & 1u);
     }
     // ---- B = b A + c A A
     if (threadIdx.x == 0) {
@@ -374,7 +383,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     }
     wait_products();
     const bool last = k == steps.count - 1;
-    if (C > 1 && !last) cluster_arrive();
     const float f = ca + diag[row];
     const float sc = a.scale * kXInv;
 #pragma unroll 1
@@ -464,12 +472,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
 
 template <int NCH>
 cudaError_t launch_small_t(const MuonArgs& a, const MuonSteps& steps, cudaStream_t s, int* fits) {
-  // X, A, and B or, with a cluster, the rows received for X Xt
-  const size_t smem = 1024 + 2 * NCH * kChunkBytes + kPanelBytes + (a.cluster > 1 ? 2 : 1) * kPanelBytes;
+  constexpr size_t smem = 1024 + 2 * NCH * kChunkBytes + 2 * kPanelBytes;   // X, A, B
   auto kern = muon_small_kernel<NCH>;
   static const cudaError_t opted = [&] {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(1024 + 2 * NCH * kChunkBytes + 3 * kPanelBytes));
+                                               static_cast<int>(smem));
     return e != cudaSuccess ? e : cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   }();
   if (opted != cudaSuccess) return opted;
@@ -500,33 +507,30 @@ cudaError_t launch_small(const MuonArgs& a, const MuonSteps& steps, int chunks, 
 
 }  // namespace
 
-bool muon_small_shape(int64_t m, int64_t n, int64_t count, int* cluster, int* chunks) {
-  if (m > 128 || n > 16 * 256) return false;
-  // one CTA up to 256 columns (no sum over slabs); else slabs of 256, or of 128
-  // while the clusters then still fit the GPU at once
+int muon_small_cluster(int64_t m, int64_t n) {
+  if (m > 128 || n > 16 * 256) return 0;
   int c = 1;
   while (c * 256 < n) c *= 2;
-  if (c > 1 && c < 16 && count * c * 2 <= 128) c *= 2;
-  *cluster = c;
-  *chunks = static_cast<int>(((n + c - 1) / c + 63) / 64);
-  return true;
+  return c;
 }
+
+int muon_small_chunks(int64_t n, int cluster) { return static_cast<int>(((n + cluster - 1) / cluster + 63) / 64); }
 
 cudaError_t launch_muon_small(const MuonArgs& a, const MuonSteps& steps, int chunks, cudaStream_t s) {
   return launch_small(a, steps, chunks, s, nullptr);
 }
 
-// Whether a cluster of this size fits the device at all
-bool muon_small_fits(int cluster, int chunks) {
+// Clusters of this size that fit the device at once
+int muon_small_clusters(int cluster, int chunks) {
   MuonArgs a{};
   a.cluster = cluster;
   a.count = 1;
   int n = 0;
   if (launch_small(a, MuonSteps{}, chunks, nullptr, &n) != cudaSuccess) {
     cudaGetLastError();
-    return false;
+    return 0;
   }
-  return n > 0;
+  return n;
 }
 
 }  // namespace flce

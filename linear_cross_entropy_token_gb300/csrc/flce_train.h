@@ -144,8 +144,11 @@ MuonPlan muon_plan(const MuonArgs& a, int fixed_shape, int pairs, int sms);
 int muon_max_clusters();
 
 // flce_muon_small.cu: matrices whose short side is at most 128, one launch
-bool muon_small_shape(int64_t m, int64_t n, int64_t count, int* cluster, int* chunks);
-bool muon_small_fits(int cluster, int chunks);
+// (long side at most 4096). The least CTAs per matrix (0: not such a shape),
+// 64-column chunks of a CTA's slab, clusters that fit the device at once.
+int muon_small_cluster(int64_t m, int64_t n);
+int muon_small_chunks(int64_t n, int cluster);
+int muon_small_clusters(int cluster, int chunks);
 cudaError_t launch_muon_small(const MuonArgs& a, const MuonSteps& steps, int chunks, cudaStream_t s);
 
 }  // namespace flce

@@ -139,8 +139,12 @@ MuonLayout muon_layout(int64_t rows, int64_t cols, int64_t count) {
   if (splits > 1) {
     const uint64_t area = align_up(z.m, 256) * align_up(z.m, 512);
     l.sums_bytes = std::min<uint64_t>(4 * area * count * (splits - 1), kMuonSumsBytes);
-    l.sums = take(l.sums_bytes);
   }
+  // or, in the one-launch kernel, a cluster's partial products of X Xt and A
+  // (16 CTAs at most: the device is not known here)
+  if (muon_small_cluster(z.m, z.n) > 1)
+    l.sums_bytes = std::max<uint64_t>(l.sums_bytes, static_cast<uint64_t>(count) * (16 * 65536 + 32768));
+  l.sums = take(l.sums_bytes);
   l.total = off;
   return l;
 }
@@ -262,12 +266,21 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
   MuonSteps steps{};
   steps.count = q->steps;
   std::memcpy(steps.c, coefficients, sizeof(float) * 3 * q->steps);
-  int cluster, chunks;
-  if (h->muon_shape < 0 && muon_small_shape(z.m, z.n, count, &cluster, &chunks)) {
-    auto known = h->muon_small.find({cluster, chunks});
-    if (known == h->muon_small.end())
-      known = h->muon_small.emplace(std::array<int, 2>{cluster, chunks}, muon_small_fits(cluster, chunks)).first;
-    if (known->second) {
+  // CTAs per matrix of the one-launch kernel: one up to 256 columns (no sum over
+  // slabs), else slabs of at most 256 and down to 64 while all matrices still
+  // run at once: a slab's epilogues and an element's share of the sum shrink
+  // with it (128 x 512: 41 us on eight CTAs, 51 on four)
+  int cluster = h->muon_shape < 0 ? muon_small_cluster(z.m, z.n) : 0;
+  if (cluster > 0) {
+    auto at_once = [&](int c) {
+      const std::array<int, 2> key{c, muon_small_chunks(z.n, c)};
+      const auto known = h->muon_small.find(key);
+      if (known != h->muon_small.end()) return known->second;
+      return h->muon_small.emplace(key, muon_small_clusters(c, key[1])).first->second;
+    };
+    while (cluster > 1 && cluster < 16 && cluster * 64 < z.n && count <= at_once(2 * cluster)) cluster *= 2;
+    if (at_once(cluster) > 0) {
+      const int chunks = muon_small_chunks(z.n, cluster);
       a.cluster = cluster;
       FLCE_LAUNCH(FLCE_K_MUON_SMALL, flops, el * (gb + mb + ob), launch_muon_small(a, steps, chunks, s));
       return FLCE_OK;

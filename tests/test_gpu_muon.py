@@ -204,8 +204,9 @@ def test_batches_repeats_and_streams():
     a = orthogonalize(G, dtype=torch.float32)
     for i in range(0, 40, 13):
         one = orthogonalize(G.view(40, 90, 300)[i], dtype=torch.float32)
-        assert torch.equal(one, a.view(40, 90, 300)[i])
-        assert rel(one, newton_schulz(G.view(40, 90, 300)[i].cpu())) <= ORTHO
+        # (the number of matrices sets the CTAs per matrix, and with them the order of sums)
+        for got in (one, a.view(40, 90, 300)[i]):
+            assert rel(got, newton_schulz(G.view(40, 90, 300)[i].cpu())) <= ORTHO
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
