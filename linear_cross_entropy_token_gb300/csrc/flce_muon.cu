@@ -270,6 +270,7 @@ struct MuonTile<kMuonWide> {
 constexpr uint32_t kPartBytes = 128 * kBK * 2;  // 16 KB: 128 rows or columns of a 64-deep k-block
 constexpr int kThreads = 384;                   // warp 0 loads, warp 1 issues, warps 4..11 run the epilogue
 constexpr int kEpiThreads = 256;
+constexpr uint32_t kEpiBar = 1;                 // their named barrier
 // per epilogue warp two buffers of 32 rows x 32 fp16 columns, twice (X hi and
 // lo; a tile and its mirror image; one fp32 tile)
 constexpr uint32_t kEpiPart = 32 * 64;
@@ -663,7 +664,7 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
   constexpr int kStages = Tile::kStages, kAccs = Tile::kAccs;
   constexpr uint32_t kStageBytes = stage_bytes<SHAPE>();
   constexpr uint32_t kTmemCols = kAccs * Tile::kN;
-  constexpr uint32_t kParts = 8 * (kPaired ? 2 : 1);   // epilogue warps of a tile
+  constexpr uint32_t kParts = kPaired ? 2 : 1;   // CTAs of a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -881,91 +882,95 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
       const bool skip = row0 >= a.m || col0 >= ncols || (kSym && block_n < block_m);
       const int groups = skip ? 0 : min(kHalf / 32, (ncols - col0 + 31) / 32);
       float factor = 0.f;
+      bool good = true;
       if (PHASE != kMuonGram && groups > 0) {
-        ok = true;
-        if (lane == 0) ok = wait_done(a.done + w.mat, w.needed() * kParts, err, a.timeout_ns);
-        ok = __all_sync(kAll, ok);
-        if (!ok) return;
-        epi.load(e0, e1, w.mat, row0, col0);
-        if (groups > 1) epi.load(e0, e1, w.mat, row0, col0 + 32);
-        if (!kSym && row0 + lane < a.m)
-          factor = st.a + __ldcg(a.diag + static_cast<int64_t>(w.mat) * a.m + row0 + lane);
-        if (PHASE == kMuonLast) epi.prefetch_weight(w.mat, row0, col0, kHalf);
+        if (lane == 0) good = wait_done(a.done + w.mat, w.needed() * kParts, err, a.timeout_ns);
+        good = __all_sync(kAll, good);
+        if (good) {
+          epi.load(e0, e1, w.mat, row0, col0);
+          if (groups > 1) epi.load(e0, e1, w.mat, row0, col0 + 32);
+          if (!kSym && row0 + lane < a.m)
+            factor = st.a + __ldcg(a.diag + static_cast<int64_t>(w.mat) * a.m + row0 + lane);
+          if (PHASE == kMuonLast) epi.prefetch_weight(w.mat, row0, col0, kHalf);
+        }
       }
-      ok = wait(tfull_bar(acc), acc_phase);
-      ok = __all_sync(kAll, ok);
-      if (!ok) return;
-      tc_fence_after();
-      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(wq * 32) << 16) + acc * Tile::kN + half * kHalf;
-      auto release = [&] {
-        tc_fence_before();
-        if (rank == 0)
-          mbar_arrive(tempty_bar(acc));
-        else
-          mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
-      };
-      if (groups == 0) release();
+      if (good) good = wait(tfull_bar(acc), acc_phase);
+      good = __all_sync(kAll, good);
       // X Xt in splits: every split but the last leaves its fp32 sums, a 32 x 32
       // block per warp and group as [8][lane][4], where the last split's same
       // warps and lanes read them, in the order of the splits
       const bool partial = PHASE == kMuonGram && w.split + 1 < w.splits;
       const bool joins = PHASE == kMuonGram && w.splits > 1 && !partial;
-      float4* sums = nullptr;
-      if (partial || joins) {
-        const int64_t tile = (static_cast<int64_t>(w.mat) * (w.splits - 1) + (partial ? w.split : 0)) * w.per_s + w.tile;
-        const int block = ((static_cast<int>(rank) * 4 + wq) * 2 + half) * (kHalf / 32);
-        sums = reinterpret_cast<float4*>(a.sums) + (tile * (Tile::kM * Tile::kN / 1024) + block) * 256 + lane;
-      }
-      if (joins && groups > 0) {
+      if (good && joins && groups > 0) {
         const uint32_t parts = static_cast<uint32_t>((w.step + 1) * (w.splits - 1) * w.per_s) * kParts;
-        if (lane == 0) ok = wait_done(a.partial + w.mat, parts, err, a.timeout_ns);
-        ok = __all_sync(kAll, ok);
-        if (!ok) return;
+        if (lane == 0) good = wait_done(a.partial + w.mat, parts, err, a.timeout_ns);
+        good = __all_sync(kAll, good);
       }
+      if (good) {
+        tc_fence_after();
+        const uint32_t tbase = tmem_base + (static_cast<uint32_t>(wq * 32) << 16) + acc * Tile::kN + half * kHalf;
+        auto release = [&] {
+          tc_fence_before();
+          if (rank == 0)
+            mbar_arrive(tempty_bar(acc));
+          else
+            mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+        };
+        float4* sums = nullptr;
+        if (partial || joins) {
+          const int64_t tile =
+              (static_cast<int64_t>(w.mat) * (w.splits - 1) + (partial ? w.split : 0)) * w.per_s + w.tile;
+          const int block = ((static_cast<int>(rank) * 4 + wq) * 2 + half) * (kHalf / 32);
+          sums = reinterpret_cast<float4*>(a.sums) + (tile * (Tile::kM * Tile::kN / 1024) + block) * 256 + lane;
+        }
+        if (groups == 0) release();
 #pragma unroll 1
-      for (int g = 0; g < groups && ok; ++g) {
-        __syncwarp();
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(tbase + g * 32, r);
-        tmem_ld_wait();
-        tmem_regs_ready(r);
-        if (g == groups - 1) release();
-        if constexpr (PHASE == kMuonGram) {
-          if (partial) {
+        for (int g = 0; g < groups && good; ++g) {
+          __syncwarp();
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(tbase + g * 32, r);
+          tmem_ld_wait();
+          tmem_regs_ready(r);
+          if (g == groups - 1) release();
+          if constexpr (PHASE == kMuonGram) {
+            if (partial) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              __stcg(sums + g * 256 + j * 32,
-                     make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]), __uint_as_float(r[4 * j + 2]),
-                                 __uint_as_float(r[4 * j + 3])));
-            continue;
-          }
-          if (joins) {
-            for (int s = 0; s + 1 < w.splits; ++s) {   // onto this split's own, in order
-              float4 v[8];
-              const float4* from = sums + static_cast<int64_t>(s) * w.per_s * (Tile::kM * Tile::kN / 4) + g * 256;
+              for (int j = 0; j < 8; ++j)
+                __stcg(sums + g * 256 + j * 32,
+                       make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                                   __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])));
+              continue;
+            }
+            if (joins) {
+              for (int s = 0; s + 1 < w.splits; ++s) {   // onto this split's own, in order
+                float4 v[8];
+                const float4* from = sums + static_cast<int64_t>(s) * w.per_s * (Tile::kM * Tile::kN / 4) + g * 256;
 #pragma unroll
-              for (int j = 0; j < 8; ++j) v[j] = __ldcg(from + j * 32);
+                for (int j = 0; j < 8; ++j) v[j] = __ldcg(from + j * 32);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) + v[j].x);
-                r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) + v[j].y);
-                r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) + v[j].z);
-                r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) + v[j].w);
+                for (int j = 0; j < 8; ++j) {
+                  r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) + v[j].x);
+                  r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) + v[j].y);
+                  r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) + v[j].z);
+                  r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) + v[j].w);
+                }
               }
             }
           }
+          good = epi.group<PHASE>(st, o0, o1, g, w.mat, row0, col0 + g * 32, kSym && block_n > block_m, factor, r);
+          if (PHASE != kMuonGram && good && g + 2 < groups) epi.load(e0, e1, w.mat, row0, col0 + (g + 2) * 32);
         }
-        ok = epi.group<PHASE>(st, o0, o1, g, w.mat, row0, col0 + g * 32, kSym && block_n > block_m, factor, r);
-        if (PHASE != kMuonGram && g + 2 < groups) epi.load(e0, e1, w.mat, row0, col0 + (g + 2) * 32);
       }
-      if (!ok) return;
       if (PHASE != kMuonLast) {
-        // this part of the tile is in global memory: say so
+        // This CTA's part of the tile is in global memory: say so, once for its
+        // eight warps (an atomic per warp queues a hundred on one counter). All
+        // eight come here whatever happened, and leave together if a wait failed.
         __syncwarp();
-        if (lane == 0) {
-          bulk_wait_group<0>();
-          add_release((partial ? a.partial : a.done) + w.mat, 1);
-        }
+        if (lane == 0) bulk_wait_group<0>();
+        ok = !named_bar_or(kEpiBar, kEpiThreads, !good);
+        if (ok && warp == 4 && lane == 0) add_release((partial ? a.partial : a.done) + w.mat, 1);
+      } else {
+        ok = good;
       }
     };
     for (; ok && w.locate(); w.advance(), ++it) {
