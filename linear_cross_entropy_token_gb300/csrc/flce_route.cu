@@ -30,6 +30,7 @@ namespace flce {
 namespace {
 
 constexpr int kWarps = kRouteThreads / 32;
+constexpr int kForwardBlocks = 3, kBackwardBlocks = 4;   // resident per SM
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
@@ -175,8 +176,13 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 // ONE: the grid is one cluster and there is one document without offsets: the
 // blocks' sums meet in the first block over distributed shared memory, which
 // closes the call. Otherwise the sums go to the workspace for the second launch.
+//
+// Bound by integer issue, not by memory: at 131072 x 256 fp32, k = 8 about 500
+// warp instructions a row (the keys and nine rounds are half of them) take 83 us,
+// where HBM needs 21. Three blocks per SM (80 registers): four spill, and with
+// the compiler's own 102 registers only two fit (91 us either way).
 template <class T, int G, int NPL, bool ONE>
-__global__ void __launch_bounds__(kRouteThreads) route_forward_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kRouteThreads, NPL == 8 ? kForwardBlocks : 1) route_forward_kernel(const RouteArgs a) {
   constexpr int RPW = 32 / G;          // rows a warp holds at once
   constexpr int kTurns = RPW >= 4 ? 1 : 4 / RPW;   // of such, before the slots of all are worked out
   constexpr int kRows = RPW * kTurns;
@@ -793,7 +799,7 @@ cudaError_t for_geometry(const RouteGeometry& g, F&& f) {
 
 }  // namespace
 
-RouteGeometry route_geometry(int64_t N, int64_t E, int64_t documents, bool offsets, int num_sms) {
+RouteGeometry route_geometry(int64_t N, int64_t E, int64_t documents, bool offsets, bool backward, int num_sms) {
   RouteGeometry g;
   g.per_lane = E <= 256 ? 8 : (E <= 512 ? 16 : 32);
   g.lanes = 1;
@@ -802,8 +808,8 @@ RouteGeometry route_geometry(int64_t N, int64_t E, int64_t documents, bool offse
   // Short batches run as one cluster of up to 8 blocks that closes the call
   // itself: one launch instead of two. Past 8 turns of rows per warp the
   // whole GPU's width is worth the second launch.
-  g.one_launch = !offsets && N > 0 && N <= 8 * 8 * kWarps * (32 / g.lanes);
-  const int64_t most = g.one_launch ? 8 : 4 * static_cast<int64_t>(num_sms);
+  g.one_launch = !backward && !offsets && N > 0 && N <= 8 * 8 * kWarps * (32 / g.lanes);
+  const int64_t most = g.one_launch ? 8 : (backward ? kBackwardBlocks : kForwardBlocks) * static_cast<int64_t>(num_sms);
   int64_t per = (N + most - 1) / most;
   per = (per + step - 1) / step * step;
   g.rows_per_block = per > 0 ? per : step;
