@@ -49,6 +49,13 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// within 1 ulp; sums of exp lie in [1, 1024]
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
@@ -139,6 +146,14 @@ __device__ __forceinline__ uint32_t group_max_u32(uint32_t v) {
   return v;
 }
 
+template <int G>
+__device__ __forceinline__ int32_t group_max_s32(int32_t v) {
+  if (G == 32) return __reduce_max_sync(kAll, v);
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+
 constexpr int log2_of(int v) { return v <= 1 ? 0 : 1 + log2_of(v / 2); }
 
 // A 31-bit key that orders a row's experts: the leading bits of the logit (as
@@ -150,6 +165,61 @@ __device__ __forceinline__ uint32_t expert_key(float z, int e) {
   const uint32_t ordered = b ^ ((b & 0x80000000u) ? 0xFFFFFFFFu : 0x80000000u);
   constexpr uint32_t low = (1u << IDX) - 1u;
   return ((ordered >> 1) & ~low) | (low - static_cast<uint32_t>(e));
+}
+
+// The same order in all 32 bits of a signed integer: one bit less is cut.
+template <int IDX>
+__device__ __forceinline__ int32_t expert_key_signed(float z, int e) {
+  const int32_t b = __float_as_int(z + 0.0f);
+  constexpr int32_t low = (1 << IDX) - 1;
+  return ((b ^ ((b >> 31) & 0x7FFFFFFF)) & ~low) | (low - e);
+}
+
+// Eight values, largest first: Batcher's odd-even merge sort, 19 exchanges.
+__device__ __forceinline__ void sort8(int32_t (&v)[8]) {
+  auto order = [&](int i, int j) {
+    const int32_t hi = max(v[i], v[j]), lo = min(v[i], v[j]);
+    v[i] = hi;
+    v[j] = lo;
+  };
+  order(0, 1), order(2, 3), order(4, 5), order(6, 7);
+  order(0, 2), order(1, 3), order(4, 6), order(5, 7);
+  order(1, 2), order(5, 6);
+  order(0, 4), order(1, 5), order(2, 6), order(3, 7);
+  order(2, 4), order(3, 5);
+  order(1, 2), order(3, 4), order(5, 6);
+}
+
+// The largest keys of a group of G lanes, each lane's eight sorted: a round
+// takes the largest of the lanes' heads, and its lane moves up the next of its
+// first D. G = 32: round j's key goes to lane j (`mine`), otherwise its expert
+// to slot[j]. Returns whether a lane gave all its D and had more.
+template <int G, int IDX, int D>
+__device__ __forceinline__ bool take_largest(const int32_t (&sorted)[8], int k, int rounds, int32_t* slot, int32_t& mine,
+                                             int32_t& last, bool& unsure) {
+  constexpr int32_t kNone = INT32_MIN;
+  const int lane = threadIdx.x & 31;
+  int32_t h[D];
+#pragma unroll
+  for (int i = 0; i < D; ++i) h[i] = sorted[i];
+  last = 0x7FFFFFFF;
+  unsure = false;
+  for (int j = 0; j < rounds; ++j) {
+    const int32_t best = group_max_s32<G>(h[0]);
+    if (h[0] == best) {
+#pragma unroll
+      for (int i = 0; i + 1 < D; ++i) h[i] = h[i + 1];
+      h[D - 1] = kNone;
+    }
+    if (G == 32) {
+      if (lane == j) mine = best;
+    } else {
+      if (j > 0) unsure |= ((best ^ last) >> IDX) == 0;
+      if (j < k && (lane % G) == 0) slot[j] = ((1 << IDX) - 1) - (best & ((1 << IDX) - 1));
+    }
+    last = best;
+  }
+  return D < 8 && h[0] == kNone;
 }
 
 // The first document whose end lies past row r (documents: none does). The
@@ -177,10 +247,11 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 // blocks' sums meet in the first block over distributed shared memory, which
 // closes the call. Otherwise the sums go to the workspace for the second launch.
 //
-// Bound by integer issue, not by memory: at 131072 x 256 fp32, k = 8 about 500
-// warp instructions a row (the keys and nine rounds are half of them) take 83 us,
-// where HBM needs 21. Three blocks per SM (80 registers): four spill, and with
-// the compiler's own 102 registers only two fit (91 us either way).
+// Bound by issue and by the rounds' latency, not by memory: at 131072 x 256
+// fp32, k = 8 this takes 67 us where HBM needs 21. Sorting a lane's eight keys
+// once and taking heads costs a third of searching all keys in every round (83
+// us); rows whose largest all lie in one lane take both (81 us). Three blocks
+// per SM (80 registers): four spill, two wait more.
 template <class T, int G, int NPL, bool ONE>
 __global__ void __launch_bounds__(kRouteThreads, NPL == 8 ? kForwardBlocks : 1) route_forward_kernel(const RouteArgs a) {
   constexpr int RPW = 32 / G;          // rows a warp holds at once
@@ -192,7 +263,7 @@ __global__ void __launch_bounds__(kRouteThreads, NPL == 8 ? kForwardBlocks : 1) 
   int32_t* cnt = reinterpret_cast<int32_t*>(red + kWarps * RPW * kCols);  // [kCols]
   float* stage_v = reinterpret_cast<float*>(cnt + kCols);             // [kWarps][kRows][k]
   int32_t* stage_i = reinterpret_cast<int32_t*>(stage_v + kWarps * kRows * a.k);
-  __shared__ float2 sh_row[kWarps * kRows];    // the rows' largest logit (NaN where not live) and 1 / sum
+  __shared__ float2 sh_row[kWarps * kRows];    // the rows' largest logit and sum of exp (-1 where not live)
   __shared__ float sh_z[kWarps];
   __shared__ int32_t sh_live[kWarps];
   __shared__ float sh_sum[ONE ? kCols : 1];    // ONE: this block's sums, read by the first block
@@ -285,36 +356,14 @@ __global__ void __launch_bounds__(kRouteThreads, NPL == 8 ? kForwardBlocks : 1) 
           sum += p[i];
         }
         sum = group_sum<G>(sum);
-        const float inv = 1.0f / sum;
         if (live) {
+          const float inv = rcp_approx(sum);   // one more error of 2^-23, as in each exp
 #pragma unroll
           for (int i = 0; i < NPL; ++i) acc[i] = fmaf(p[i], inv, acc[i]);
         }
-        if (in && gl == 0) {
-          const float log_sum = logf(sum);
-          // apart: their sum would lose log_sum's last bits where |m| is large,
-          // and with them the backward's softmax
-          a.stats[row] = make_float2(live ? m : neg_inf(), live ? log_sum : 0.f);
-          if (live) {
-            const float lse = mm + log_sum;
-            zacc = fmaf(lse, lse, zacc);
-            ++live_rows;
-          }
-        }
-        // The k largest by keys, all distinct: each round takes the group's
-        // largest key below the last one.
+        // The k largest by keys, all distinct.
         constexpr int IDX = log2_of(kCols);
-        uint32_t key[NPL];
-        if (a.E == kCols) {
-#pragma unroll
-          for (int i = 0; i < NPL; ++i) key[i] = expert_key<IDX>(z[i], c0 + i);
-        } else {
-#pragma unroll
-          for (int i = 0; i < NPL; ++i)
-            key[i] = c0 + i < a.E ? expert_key<IDX>(z[i], c0 + i) : static_cast<uint32_t>(kCols - 1 - c0 - i);
-        }
         int32_t* slot = my_i + (turn * RPW + gr) * k;
-        uint32_t last = 0x80000000u;
         // fp32: two keys alike in what they keep of the logit, and some logit of
         // the lane's with bits in what they cut (logits rounded to 16 bits have
         // none: their ties are true ties, in the keys' order)
@@ -323,17 +372,60 @@ __global__ void __launch_bounds__(kRouteThreads, NPL == 8 ? kForwardBlocks : 1) 
 #pragma unroll
         for (int i = 0; i < NPL; ++i) bits |= __float_as_uint(z[i]);
         const int rounds = sizeof(T) == 4 && k < a.E ? k + 1 : k;
-        for (int j = 0; j < rounds; ++j) {
-          // key - last wraps to the top half for the keys below it and not for
-          // the others, so one unsigned maximum finds it, with no search for the
-          // winner and nothing to remove
-          uint32_t best = key[0] - last;
+        if constexpr (NPL == 8) {
+          int32_t key[8];
+          if (a.E == kCols) {
 #pragma unroll
-          for (int i = 1; i < NPL; ++i) best = max(best, key[i] - last);
-          best = group_max_u32<G>(best) + last;
-          if (sizeof(T) == 4) unsure |= ((best ^ last) >> IDX) == 0;
-          last = best;
-          if (j < k && gl == 0) slot[j] = static_cast<int>((kCols - 1) - (best & (kCols - 1)));
+            for (int i = 0; i < 8; ++i) key[i] = expert_key_signed<IDX>(z[i], c0 + i);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              key[i] = c0 + i < a.E ? expert_key_signed<IDX>(z[i], c0 + i) : INT32_MIN + (kCols - 1 - c0 - i);
+          }
+          sort8(key);
+          if constexpr (G == 1) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if (j < k) slot[j] = (kCols - 1) - (key[j] & (kCols - 1));
+              if (j > 0 && j < rounds) unsure |= ((key[j] ^ key[j - 1]) >> IDX) == 0;
+            }
+          } else {
+            // Few lanes give more than four of the k, so a round moves four; a
+            // warp with one that does starts again with all eight.
+            constexpr int D = G >= 16 ? 4 : 8;
+            int32_t mine = 0, last;
+            const bool more = take_largest<G, IDX, D>(key, k, rounds, slot, mine, last, unsure);
+            if (D < 8 && __any_sync(kAll, more)) take_largest<G, IDX, 8>(key, k, rounds, slot, mine, last, unsure);
+            if (G == 32) {
+              const int32_t below = __shfl_down_sync(kAll, mine, 1);
+              unsure = lane + 1 < rounds && (((lane == 31 ? last : below) ^ mine) >> IDX) == 0;
+              if (lane < k) slot[lane] = (kCols - 1) - (mine & (kCols - 1));
+            }
+          }
+        } else {
+          // each round takes the group's largest key below the last one
+          uint32_t key[NPL];
+          if (a.E == kCols) {
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) key[i] = expert_key<IDX>(z[i], c0 + i);
+          } else {
+#pragma unroll
+            for (int i = 0; i < NPL; ++i)
+              key[i] = c0 + i < a.E ? expert_key<IDX>(z[i], c0 + i) : static_cast<uint32_t>(kCols - 1 - c0 - i);
+          }
+          uint32_t last = 0x80000000u;
+          for (int j = 0; j < rounds; ++j) {
+            // key - last wraps to the top half for the keys below it and not for
+            // the others, so one unsigned maximum finds it, with no search for the
+            // winner and nothing to remove
+            uint32_t best = key[0] - last;
+#pragma unroll
+            for (int i = 1; i < NPL; ++i) best = max(best, key[i] - last);
+            best = group_max_u32<G>(best) + last;
+            if (sizeof(T) == 4) unsure |= ((best ^ last) >> IDX) == 0;
+            last = best;
+            if (j < k && gl == 0) slot[j] = static_cast<int>((kCols - 1) - (best & (kCols - 1)));
+          }
         }
         if (sizeof(T) == 4 && __any_sync(kAll, unsure) && __any_sync(kAll, (bits & ((2u << IDX) - 1u)) != 0)) {
           // (the fast rounds' slots were written by other lanes than these will be)
@@ -362,11 +454,26 @@ __global__ void __launch_bounds__(kRouteThreads, NPL == 8 ? kForwardBlocks : 1) 
             if (bv == neg_inf() && who == gmask && gl == 0) slot[j] = -1;
           }
         }
-        if (gl == 0) my_row[turn * RPW + gr] = make_float2(live ? mm : __int_as_float(0x7FFFFFFF), live ? inv : -1.f);
+        if (gl == 0) my_row[turn * RPW + gr] = make_float2(live ? m : neg_inf(), live ? sum : -1.f);
       }
       __syncwarp();
-      // the slots of all these rows, a lane per slot: exp, then the weights
-      const int slots = static_cast<int>(min(static_cast<int64_t>(kRows), end - base)) * k;
+      // these rows' statistics, a lane per row
+      const int rows = static_cast<int>(min(static_cast<int64_t>(kRows), end - base));
+      if (lane < rows) {
+        const float2 rw = my_row[lane];
+        const bool live = rw.y != -1.f;
+        const float log_sum = live ? logf(rw.y) : 0.f;
+        // apart: their sum would lose log_sum's last bits where |m| is large,
+        // and with them the backward's softmax
+        a.stats[base + lane] = make_float2(rw.x, log_sum);
+        if (live) {
+          const float lse = rw.x + log_sum;
+          zacc = fmaf(lse, lse, zacc);
+          ++live_rows;
+        }
+      }
+      // and their slots, a lane per slot: exp, then the weights
+      const int slots = rows * k;
       for (int t = lane; t < slots; t += 32) {
         const int b = (t * inv_k) >> 16;
         const float2 rw = my_row[b];
@@ -387,14 +494,13 @@ __global__ void __launch_bounds__(kRouteThreads, NPL == 8 ? kForwardBlocks : 1) 
       __syncwarp();
       for (int t = lane; t < slots; t += 32) {
         const int b = (t * inv_k) >> 16;
-        float scale = my_row[b].y;
+        float share = my_row[b].y;
         if (a.renormalize) {
-          float share = 0.f;
+          share = 0.f;
           for (int j = 0; j < k; ++j) share += my_v[b * k + j];
-          scale = 1.0f / share;
         }
         const int e = my_i[t];
-        a.weights[base * k + t] = e >= 0 ? my_v[t] * scale : 0.f;
+        a.weights[base * k + t] = e >= 0 ? my_v[t] * (1.0f / share) : 0.f;
         a.experts[base * k + t] = e;
       }
       __syncwarp();
