@@ -16,7 +16,7 @@
 // too (an expert's column belongs to one lane) until a block's piece of a
 // document ends. Sums over tokens are taken in a fixed order (per piece, then
 // over the pieces), so results repeat bit for bit; only integer counts use
-// atomics. All arithmetic is fp32; sums over blocks are fp64.
+// atomics. All arithmetic is fp32, but for the sums over documents (fp64).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(32 * R) route_finish_kernel(const RouteArgs a,
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ float sh_z[R];
   __shared__ int32_t sh_n[R];
-  __shared__ double sh_t[3][R];
+  __shared__ float sh_t[2][R];
   __shared__ bool last;
   const int d = blockIdx.x / chunks, chunk = blockIdx.x - d * chunks;
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
@@ -640,6 +640,23 @@ __global__ void __launch_bounds__(32 * R) route_finish_kernel(const RouteArgs a,
     sh_n[ty] = n;
     sh_z[ty] = zs;
   }
+  // a lane's share of the units of expert e (a tree over the lanes follows:
+  // fp32 in both); the first ones are on their way over the barrier
+  const int e_end = min(a.E, (chunk + 1) * chunk_size);
+  float p = 0.f;
+  int c = 0;
+  auto load_share = [&](int e) {
+    p = 0.f;
+    c = 0;
+    if (e >= e_end) return;
+#pragma unroll 16
+    for (int b = b0 + ty; b < b1; b += R) {
+      const int64_t u = (static_cast<int64_t>(b) + d) * a.E + e;
+      p += a.unit_p[u];
+      c += a.unit_c[u];
+    }
+  };
+  load_share(chunk * chunk_size + tx);
   __syncthreads();
   n = tx < R ? sh_n[tx] : 0;
   zs = tx < R ? sh_z[tx] : 0.f;
@@ -650,20 +667,8 @@ __global__ void __launch_bounds__(32 * R) route_finish_kernel(const RouteArgs a,
   const float slope_n = n > 0 ? static_cast<float>(a.E) / (static_cast<float>(a.k) * static_cast<float>(n)) : 0.f;
 
   float term = 0.f;
-  const int e_end = min(a.E, (chunk + 1) * chunk_size);
   for (int e0 = chunk * chunk_size; e0 < e_end; e0 += 32) {
-    const int e = e0 + tx;
-    // a lane's share of the units, then a tree over the lanes: fp32 in both
-    float p = 0.f;
-    int c = 0;
-    if (e < e_end) {
-#pragma unroll 8
-      for (int b = b0 + ty; b < b1; b += R) {
-        const int64_t u = (static_cast<int64_t>(b) + d) * a.E + e;
-        p += a.unit_p[u];
-        c += a.unit_c[u];
-      }
-    }
+    if (e0 != chunk * chunk_size) load_share(e0 + tx);
     sh_p[tx][ty] = p;
     sh_c[tx][ty] = c;
     __syncthreads();
@@ -704,15 +709,18 @@ __global__ void __launch_bounds__(32 * R) route_finish_kernel(const RouteArgs a,
   __threadfence();
 
   // fixed order: a thread's stride, then the tree
-  double bal = 0.0, z = 0.0, live = 0.0;
+  // (the strides in fp64: a thread has many only where there are many documents)
+  double bal_sum = 0.0, z_sum = 0.0;
+  int live = 0;
   const int64_t terms = static_cast<int64_t>(a.documents) * chunks;
-  for (int64_t i = threadIdx.x; i < terms; i += 32 * R) bal += __ldcg(a.terms + i);
+  for (int64_t i = threadIdx.x; i < terms; i += 32 * R) bal_sum += __ldcg(a.terms + i);
   for (int i = threadIdx.x; i < a.documents; i += 32 * R) {
     live += __ldcg(a.doc_live + i);
-    z += __ldcg(a.doc_z + i);
+    z_sum += __ldcg(a.doc_z + i);
   }
   // (few documents fill few warps: the others have nothing to add)
   const int busy = static_cast<int>(min(static_cast<int64_t>(R), (terms + 31) / 32));
+  float bal = static_cast<float>(bal_sum), z = static_cast<float>(z_sum);
   if (ty < busy) {
     for (int o = 16; o > 0; o >>= 1) {
       bal += __shfl_xor_sync(kAll, bal, o);
@@ -722,22 +730,21 @@ __global__ void __launch_bounds__(32 * R) route_finish_kernel(const RouteArgs a,
     if (tx == 0) {
       sh_t[0][ty] = bal;
       sh_t[1][ty] = z;
-      sh_t[2][ty] = live;
+      sh_n[ty] = live;
     }
   }
   __syncthreads();
   if (threadIdx.x == 0) {
-    bal = z = live = 0.0;
-    for (int w = 0; w < busy; ++w) {
+    for (int w = 1; w < busy; ++w) {
       bal += sh_t[0][w];
       z += sh_t[1][w];
-      live += sh_t[2][w];
+      live += sh_n[w];
     }
-    const double inv = live > 0.0 ? 1.0 / live : 0.0;
+    const double inv = live > 0 ? 1.0 / live : 0.0;
     a.result[0] = static_cast<float>(bal * inv);
     a.result[1] = static_cast<float>(z * inv);
     a.result[2] = static_cast<float>(inv);
-    a.result[3] = __int_as_float(static_cast<int32_t>(live));
+    a.result[3] = __int_as_float(live);
   }
 }
 
