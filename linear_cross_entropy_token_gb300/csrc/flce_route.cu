@@ -139,14 +139,6 @@ __device__ __forceinline__ float group_max_nan(float v) {
 }
 
 template <int G>
-__device__ __forceinline__ uint32_t group_max_u32(uint32_t v) {
-  if (G == 32) return __reduce_max_sync(kAll, v);
-#pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
-  return v;
-}
-
-template <int G>
 __device__ __forceinline__ int32_t group_max_s32(int32_t v) {
   if (G == 32) return __reduce_max_sync(kAll, v);
 #pragma unroll
@@ -156,46 +148,38 @@ __device__ __forceinline__ int32_t group_max_s32(int32_t v) {
 
 constexpr int log2_of(int v) { return v <= 1 ? 0 : 1 + log2_of(v / 2); }
 
-// A 31-bit key that orders a row's experts: the leading bits of the logit (as
-// an ordered integer), then the expert, the lower the larger. 16-bit types fit
-// whole; of an fp32 logit the last 1 + IDX bits are cut.
+// A key that orders a row's experts: the leading bits of the logit (as an
+// ordered integer), then the expert, the lower the larger. 16-bit types fit
+// whole; of an fp32 logit the last IDX bits are cut.
 template <int IDX>
-__device__ __forceinline__ uint32_t expert_key(float z, int e) {
-  const uint32_t b = __float_as_uint(z + 0.0f);   // -0 ties with 0
-  const uint32_t ordered = b ^ ((b & 0x80000000u) ? 0xFFFFFFFFu : 0x80000000u);
-  constexpr uint32_t low = (1u << IDX) - 1u;
-  return ((ordered >> 1) & ~low) | (low - static_cast<uint32_t>(e));
-}
-
-// The same order in all 32 bits of a signed integer: one bit less is cut.
-template <int IDX>
-__device__ __forceinline__ int32_t expert_key_signed(float z, int e) {
-  const int32_t b = __float_as_int(z + 0.0f);
+__device__ __forceinline__ int32_t expert_key(float z, int e) {
+  const int32_t b = __float_as_int(z + 0.0f);   // -0 ties with 0
   constexpr int32_t low = (1 << IDX) - 1;
   return ((b ^ ((b >> 31) & 0x7FFFFFFF)) & ~low) | (low - e);
 }
 
-// Eight values, largest first: Batcher's odd-even merge sort, 19 exchanges.
-__device__ __forceinline__ void sort8(int32_t (&v)[8]) {
-  auto order = [&](int i, int j) {
-    const int32_t hi = max(v[i], v[j]), lo = min(v[i], v[j]);
-    v[i] = hi;
-    v[j] = lo;
-  };
-  order(0, 1), order(2, 3), order(4, 5), order(6, 7);
-  order(0, 2), order(1, 3), order(4, 6), order(5, 7);
-  order(1, 2), order(5, 6);
-  order(0, 4), order(1, 5), order(2, 6), order(3, 7);
-  order(2, 4), order(3, 5);
-  order(1, 2), order(3, 4), order(5, 6);
+// N values, largest first: Batcher's odd-even merge sort (8: 19 exchanges, 16: 63, 32: 191)
+template <int N>
+__device__ __forceinline__ void sort_down(int32_t (&v)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int d = p; d >= 1; d /= 2)
+#pragma unroll
+      for (int i = 0; i + d < N; ++i)
+        if (i >= d % p && (i - d % p) / d % 2 == 0 && i / (2 * p) == (i + d) / (2 * p)) {
+          const int32_t hi = max(v[i], v[i + d]), lo = min(v[i], v[i + d]);
+          v[i] = hi;
+          v[i + d] = lo;
+        }
 }
 
-// The largest keys of a group of G lanes, each lane's eight sorted: a round
+// The largest keys of a group of G lanes, each lane's NPL sorted: a round
 // takes the largest of the lanes' heads, and its lane moves up the next of its
 // first D. G = 32: round j's key goes to lane j (`mine`), otherwise its expert
 // to slot[j]. Returns whether a lane gave all its D and had more.
-template <int G, int IDX, int D>
-__device__ __forceinline__ bool take_largest(const int32_t (&sorted)[8], int k, int rounds, int32_t* slot, int32_t& mine,
+template <int G, int IDX, int D, int NPL>
+__device__ __forceinline__ bool take_largest(const int32_t (&sorted)[NPL], int k, int rounds, int32_t* slot, int32_t& mine,
                                              int32_t& last, bool& unsure) {
   constexpr int32_t kNone = INT32_MIN;
   const int lane = threadIdx.x & 31;
@@ -219,7 +203,7 @@ __device__ __forceinline__ bool take_largest(const int32_t (&sorted)[8], int k, 
     }
     last = best;
   }
-  return D < 8 && h[0] == kNone;
+  return D < NPL && h[0] == kNone;
 }
 
 // The first document whose end lies past row r (documents: none does). The
@@ -253,7 +237,7 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 // us); rows whose largest all lie in one lane take both (81 us). Three blocks
 // per SM (80 registers): four spill, two wait more.
 template <class T, int G, int NPL, bool ONE>
-__global__ void __launch_bounds__(kRouteThreads, NPL == 8 ? kForwardBlocks : 1) route_forward_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kRouteThreads, NPL == 8 ? kForwardBlocks : NPL == 16 ? 2 : 1) route_forward_kernel(const RouteArgs a) {
   constexpr int RPW = 32 / G;          // rows a warp holds at once
   constexpr int kTurns = RPW >= 4 ? 1 : 4 / RPW;   // of such, before the slots of all are worked out
   constexpr int kRows = RPW * kTurns;
@@ -372,59 +356,33 @@ __global__ void __launch_bounds__(kRouteThreads, NPL == 8 ? kForwardBlocks : 1) 
 #pragma unroll
         for (int i = 0; i < NPL; ++i) bits |= __float_as_uint(z[i]);
         const int rounds = sizeof(T) == 4 && k < a.E ? k + 1 : k;
-        if constexpr (NPL == 8) {
-          int32_t key[8];
-          if (a.E == kCols) {
+        int32_t key[NPL];
+        if (a.E == kCols) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) key[i] = expert_key_signed<IDX>(z[i], c0 + i);
-          } else {
+          for (int i = 0; i < NPL; ++i) key[i] = expert_key<IDX>(z[i], c0 + i);
+        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              key[i] = c0 + i < a.E ? expert_key_signed<IDX>(z[i], c0 + i) : INT32_MIN + (kCols - 1 - c0 - i);
-          }
-          sort8(key);
-          if constexpr (G == 1) {
+          for (int i = 0; i < NPL; ++i)
+            key[i] = c0 + i < a.E ? expert_key<IDX>(z[i], c0 + i) : INT32_MIN + (kCols - 1 - c0 - i);
+        }
+        sort_down(key);
+        if constexpr (G == 1) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              if (j < k) slot[j] = (kCols - 1) - (key[j] & (kCols - 1));
-              if (j > 0 && j < rounds) unsure |= ((key[j] ^ key[j - 1]) >> IDX) == 0;
-            }
-          } else {
-            // Few lanes give more than four of the k, so a round moves four; a
-            // warp with one that does starts again with all eight.
-            constexpr int D = G >= 16 ? 4 : 8;
-            int32_t mine = 0, last;
-            const bool more = take_largest<G, IDX, D>(key, k, rounds, slot, mine, last, unsure);
-            if (D < 8 && __any_sync(kAll, more)) take_largest<G, IDX, 8>(key, k, rounds, slot, mine, last, unsure);
-            if (G == 32) {
-              const int32_t below = __shfl_down_sync(kAll, mine, 1);
-              unsure = lane + 1 < rounds && (((lane == 31 ? last : below) ^ mine) >> IDX) == 0;
-              if (lane < k) slot[lane] = (kCols - 1) - (mine & (kCols - 1));
-            }
+          for (int j = 0; j < NPL; ++j) {
+            if (j < k) slot[j] = (kCols - 1) - (key[j] & (kCols - 1));
+            if (j > 0 && j < rounds) unsure |= ((key[j] ^ key[j - 1]) >> IDX) == 0;
           }
         } else {
-          // each round takes the group's largest key below the last one
-          uint32_t key[NPL];
-          if (a.E == kCols) {
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) key[i] = expert_key<IDX>(z[i], c0 + i);
-          } else {
-#pragma unroll
-            for (int i = 0; i < NPL; ++i)
-              key[i] = c0 + i < a.E ? expert_key<IDX>(z[i], c0 + i) : static_cast<uint32_t>(kCols - 1 - c0 - i);
-          }
-          uint32_t last = 0x80000000u;
-          for (int j = 0; j < rounds; ++j) {
-            // key - last wraps to the top half for the keys below it and not for
-            // the others, so one unsigned maximum finds it, with no search for the
-            // winner and nothing to remove
-            uint32_t best = key[0] - last;
-#pragma unroll
-            for (int i = 1; i < NPL; ++i) best = max(best, key[i] - last);
-            best = group_max_u32<G>(best) + last;
-            if (sizeof(T) == 4) unsure |= ((best ^ last) >> IDX) == 0;
-            last = best;
-            if (j < k && gl == 0) slot[j] = static_cast<int>((kCols - 1) - (best & (kCols - 1)));
+          // Few lanes give more than four of the k, so a round moves four; a
+          // warp with one that does starts again with all.
+          constexpr int D = G >= 16 ? 4 : NPL;
+          int32_t mine = 0, last;
+          const bool more = take_largest<G, IDX, D>(key, k, rounds, slot, mine, last, unsure);
+          if (D < NPL && __any_sync(kAll, more)) take_largest<G, IDX, NPL>(key, k, rounds, slot, mine, last, unsure);
+          if (G == 32) {
+            const int32_t below = __shfl_down_sync(kAll, mine, 1);
+            unsure = lane + 1 < rounds && (((lane == 31 ? last : below) ^ mine) >> IDX) == 0;
+            if (lane < k) slot[lane] = (kCols - 1) - (mine & (kCols - 1));
           }
         }
         if (sizeof(T) == 4 && __any_sync(kAll, unsure) && __any_sync(kAll, (bits & ((2u << IDX) - 1u)) != 0)) {
