@@ -30,7 +30,13 @@ namespace flce {
 namespace {
 
 constexpr int kWarps = kRouteThreads / 32;
-constexpr int kForwardBlocks = 3, kBackwardBlocks = 4;   // resident per SM
+// Blocks resident per SM. Forward: two with 16 experts a lane, one with 32; and
+// three for fp32 rows of 129 to 256 experts (131072 x 256: 76 us, with four 80;
+// x 128: 63 and 61).
+constexpr int kBackwardBlocks = 4;
+constexpr int forward_blocks(int element_bytes, int lanes, int per_lane) {
+  return per_lane == 32 ? 1 : per_lane == 16 ? 2 : element_bytes == 4 && lanes == 32 ? 3 : 4;
+}
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
@@ -90,6 +96,45 @@ __device__ __forceinline__ void load_row(const T* row, int c0, int E, bool vec, 
     }
   }
 }
+
+// The same as they are in memory, for a row that waits a turn.
+template <class T, int NPL>
+struct RawRow {
+  static constexpr int V = 16 / sizeof(T);
+  union Vector {
+    uint4 u;
+    uint16_t h[8];
+    uint32_t w[4];
+  };
+  Vector v[NPL / V];
+
+  __device__ __forceinline__ void load(const T* row, int c0, int E, bool vec, T fill) {
+#pragma unroll
+    for (int c = 0; c < NPL; c += V) {
+      if (vec && c0 + c + V <= E) {
+        v[c / V].u = *reinterpret_cast<const uint4*>(row + c0 + c);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const T x = c0 + c + i < E ? row[c0 + c + i] : fill;
+          if constexpr (sizeof(T) == 2)
+            v[c / V].h[i] = reinterpret_cast<const uint16_t&>(x);
+          else
+            v[c / V].w[i] = reinterpret_cast<const uint32_t&>(x);
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ float operator[](int i) const {
+    T x;
+    if constexpr (sizeof(T) == 2)
+      reinterpret_cast<uint16_t&>(x) = v[i / V].h[i % V];
+    else
+      reinterpret_cast<uint32_t&>(x) = v[i / V].w[i % V];
+    return to_f(x);
+  }
+};
 
 template <class T, int NPL>
 __device__ __forceinline__ void store_row(T* row, int c0, int E, bool vec, const float (&z)[NPL]) {
@@ -239,12 +284,11 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 // closes the call. Otherwise the sums go to the workspace for the second launch.
 //
 // Bound by issue and by the rounds' latency, not by memory: at 131072 x 256
-// fp32, k = 8 this takes 67 us where HBM needs 21. Sorting a lane's eight keys
-// once and taking heads costs a third of searching all keys in every round (83
-// us); rows whose largest all lie in one lane take both (81 us). Three blocks
-// per SM (80 registers): four spill, two wait more.
+// fp32, k = 8 this takes 66 us where HBM needs 21 (bf16: 57 and 11). Sorting a
+// lane's keys once and taking heads costs a third of searching all keys in
+// every round (83 us); rows whose largest all lie in one lane take both (81).
 template <class T, int G, int NPL, bool ONE>
-__global__ void __launch_bounds__(kRouteThreads, NPL == 8 ? kForwardBlocks : NPL == 16 ? 2 : 1) route_forward_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kRouteThreads, forward_blocks(sizeof(T), G, NPL)) route_forward_kernel(const RouteArgs a) {
   constexpr int RPW = 32 / G;          // rows a warp holds at once
   constexpr int kTurns = RPW >= 4 ? 1 : 4 / RPW;   // of such, before the slots of all are worked out
   constexpr int kRows = RPW * kTurns;
@@ -313,9 +357,9 @@ __global__ void __launch_bounds__(kRouteThreads, NPL == 8 ? kForwardBlocks : NPL
     __syncthreads();
 
     constexpr bool kAhead = NPL == 8;
-    float next[NPL];   // the row after this one, loaded a turn ahead
+    RawRow<T, NPL> next;   // the row after this one, loaded a turn ahead
     if (kAhead && r + warp * kRows + gr < end)
-      load_row<T, NPL>(logits + (r + warp * kRows + gr) * a.ld, c0, a.E, vec, neg_inf(), next);
+      next.load(logits + (r + warp * kRows + gr) * a.ld, c0, a.E, vec, from_f<T>(neg_inf()));
     for (int64_t base = r + warp * kRows; base < end; base += kWarps * kRows) {
 #pragma unroll 1
       for (int turn = 0; turn < kTurns && base + turn * RPW < end; ++turn) {
@@ -326,7 +370,7 @@ __global__ void __launch_bounds__(kRouteThreads, NPL == 8 ? kForwardBlocks : NPL
 #pragma unroll
           for (int i = 0; i < NPL; ++i) z[i] = in ? next[i] : neg_inf();
           const int64_t then = turn + 1 < kTurns ? row + RPW : row - turn * RPW + kWarps * kRows;
-          if (then < end) load_row<T, NPL>(logits + then * a.ld, c0, a.E, vec, neg_inf(), next);
+          if (then < end) next.load(logits + then * a.ld, c0, a.E, vec, from_f<T>(neg_inf()));
         } else if (in) {
           load_row<T, NPL>(logits + row * a.ld, c0, a.E, vec, neg_inf(), z);
         } else {
@@ -877,20 +921,25 @@ cudaError_t for_geometry(const RouteGeometry& g, F&& f) {
 
 }  // namespace
 
-RouteGeometry route_geometry(int64_t N, int64_t E, int64_t documents, bool offsets, bool backward, int num_sms) {
+RouteGeometry route_geometry(int64_t N, int64_t E, int element_bytes, int64_t documents, bool offsets, bool backward,
+                             int num_sms) {
   RouteGeometry g;
   g.per_lane = E <= 256 ? 8 : (E <= 512 ? 16 : 32);
   g.lanes = 1;
   while (g.lanes < 32 && static_cast<int64_t>(g.lanes) * g.per_lane < E) g.lanes *= 2;
-  const int64_t step = kWarps * std::max(32 / g.lanes, 4);
+  const int64_t step = std::max(32 / g.lanes, 4);   // a warp's rows before their slots
   // Short batches run as one cluster of up to 8 blocks that closes the call
   // itself: one launch instead of two. Past 8 turns of rows per warp the
   // whole GPU's width is worth the second launch.
   g.one_launch = !backward && !offsets && N > 0 && N <= 8 * 8 * kWarps * (32 / g.lanes);
-  const int64_t most = g.one_launch ? 8 : (backward ? kBackwardBlocks : kForwardBlocks) * static_cast<int64_t>(num_sms);
-  int64_t per = (N + most - 1) / most;
+  // as many blocks as are resident
+  const int resident = backward ? kBackwardBlocks : forward_blocks(element_bytes, g.lanes, g.per_lane);
+  const int64_t most = g.one_launch ? 8 : resident * static_cast<int64_t>(num_sms);
+  // Rows to a warp's step, not a block's (20000 x 128 bf16: 18 us, else 20),
+  // but a step for every warp (5000 x 256 fp32: 15 us, else 18)
+  int64_t per = std::max((N + most - 1) / most, kWarps * step);
   per = (per + step - 1) / step * step;
-  g.rows_per_block = per > 0 ? per : step;
+  g.rows_per_block = per;
   g.blocks = static_cast<int>((N + g.rows_per_block - 1) / g.rows_per_block);
   if (g.one_launch)
     while (g.blocks & (g.blocks - 1)) ++g.blocks;  // a power of two

@@ -54,7 +54,9 @@ struct RouteGeometry {
   int chunks;               // expert chunks per document in the closing launch
   bool one_launch;          // the forward is one cluster that closes the call itself
 };
-RouteGeometry route_geometry(int64_t N, int64_t E, int64_t documents, bool offsets, bool backward, int num_sms);
+// with 2-byte elements the most blocks: what the workspace is sized for
+RouteGeometry route_geometry(int64_t N, int64_t E, int element_bytes, int64_t documents, bool offsets, bool backward,
+                             int num_sms);
 
 cudaError_t launch_route_forward(int dtype, const RouteGeometry& g, const RouteArgs& a, cudaStream_t s);
 cudaError_t launch_route_finish(const RouteGeometry& g, const RouteArgs& a, cudaStream_t s);

@@ -329,7 +329,7 @@ extern "C" {
 uint64_t flce_route_workspace_bytes(flce_handle_t h, int64_t N, int64_t E, int64_t documents) {
   if (!h || N < 0 || N > kMaxDim || E < 1 || E > kRouteMaxExperts || documents < 1 || documents > (1 << 24)) return 0;
   // without offsets a short batch needs less: one size for both
-  return route_layout(route_geometry(N, E, documents, true, false, h->num_sms), E, documents).total;
+  return route_layout(route_geometry(N, E, 2, documents, true, false, h->num_sms), E, documents).total;
 }
 
 flce_status flce_route_forward(flce_handle_t h, const flce_route_args* r, void* workspace, uint64_t workspace_bytes,
@@ -338,8 +338,10 @@ flce_status flce_route_forward(flce_handle_t h, const flce_route_args* r, void* 
   h->err.clear();
   flce_status st = route_check(h, r);
   if (st != FLCE_OK) return st;
-  const RouteGeometry g = route_geometry(r->N, r->E, r->documents, r->offsets != nullptr, false, h->num_sms);
-  const RouteLayout L = route_layout(route_geometry(r->N, r->E, r->documents, true, false, h->num_sms), r->E, r->documents);
+  const RouteGeometry g =
+      route_geometry(r->N, r->E, element_bytes(r->dtype), r->documents, r->offsets != nullptr, false, h->num_sms);
+  const RouteLayout L =
+      route_layout(route_geometry(r->N, r->E, 2, r->documents, true, false, h->num_sms), r->E, r->documents);
   if (!workspace || addr(workspace) % 256 || workspace_bytes < L.total)
     return fail(h, FLCE_ERR_BUDGET, "the workspace must hold %llu bytes, 256-byte aligned",
                 static_cast<unsigned long long>(L.total));
@@ -380,7 +382,7 @@ flce_status flce_route_backward(flce_handle_t h, const flce_route_args* r, const
   if (addr(d_logits) % element_bytes(r->dtype) || (addr(d_weights) | addr(d_balance) | addr(d_z)) % 4)
     return fail(h, FLCE_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
   if (r->N == 0) return FLCE_OK;
-  const RouteGeometry g = route_geometry(r->N, r->E, r->documents, true, true, h->num_sms);
+  const RouteGeometry g = route_geometry(r->N, r->E, element_bytes(r->dtype), r->documents, true, true, h->num_sms);
   DeviceGuard guard(h->device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const double n = static_cast<double>(r->N), e = static_cast<double>(r->E);
