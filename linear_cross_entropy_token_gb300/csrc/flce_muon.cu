@@ -251,30 +251,36 @@ __global__ void __launch_bounds__(256) muon_prepare_kernel(const __grid_constant
 // Output tiles. SINGLE: 128 x 128 on one CTA. PAIR: 256 x 256 on a CTA pair
 // (tcgen05 cta_group::2, each CTA holding its 128 rows of A and 128 columns of
 // B). WIDE: 256 x 512 on a CTA pair, two products per k-step that share their A
-// operand through the tensor core's collector buffer.
+// operand through the tensor core's collector buffer. kBufs: 32-column groups
+// that an epilogue warp holds at once. PAIR has all its four, so that all loads
+// run while the products do, for two stages less (2048 x 2048: 317 us, with two
+// groups and five stages 322; 4096 x 4096, which is WIDE's: 1214 and 1142).
 template <int SHAPE>
 struct MuonTile;
 template <>
 struct MuonTile<kMuonSingle> {
-  static constexpr int kM = 128, kN = 128, kAccs = 2, kStages = 5;
+  static constexpr int kM = 128, kN = 128, kAccs = 2, kStages = 5, kBufs = 2;
 };
 template <>
 struct MuonTile<kMuonPair> {
-  static constexpr int kM = 256, kN = 256, kAccs = 2, kStages = 5;
+  static constexpr int kM = 256, kN = 256, kAccs = 2, kStages = 3, kBufs = 4;
 };
 template <>
 struct MuonTile<kMuonWide> {
-  static constexpr int kM = 256, kN = 512, kAccs = 1, kStages = 3;
+  static constexpr int kM = 256, kN = 512, kAccs = 1, kStages = 3, kBufs = 2;
 };
 
 constexpr uint32_t kPartBytes = 128 * kBK * 2;  // 16 KB: 128 rows or columns of a 64-deep k-block
 constexpr int kThreads = 384;                   // warp 0 loads, warp 1 issues, warps 4..11 run the epilogue
 constexpr int kEpiThreads = 256;
 constexpr uint32_t kEpiBar = 1;                 // their named barrier
-// per epilogue warp two buffers of 32 rows x 32 fp16 columns, twice (X hi and
+// per epilogue warp kBufs buffers of 32 rows x 32 fp16 columns, twice (X hi and
 // lo; a tile and its mirror image; one fp32 tile)
 constexpr uint32_t kEpiPart = 32 * 64;
-constexpr uint32_t kEpiBytes = 8 * 2 * 2 * kEpiPart;
+template <int SHAPE>
+constexpr uint32_t epi_bytes() {
+  return 8 * MuonTile<SHAPE>::kBufs * 2 * kEpiPart;
+}
 template <int SHAPE>
 constexpr uint32_t stage_bytes() {
   return (SHAPE == kMuonWide ? 3 : 2) * kPartBytes;
@@ -282,9 +288,9 @@ constexpr uint32_t stage_bytes() {
 template <int SHAPE>
 constexpr uint32_t smem_bytes() {
   constexpr int stages = MuonTile<SHAPE>::kStages;
-  return 1024 + stages * stage_bytes<SHAPE>() + kEpiBytes + (2 * stages + 5 + 16) * 8 + 16;
+  return 1024 + stages * stage_bytes<SHAPE>() + epi_bytes<SHAPE>() + (2 * stages + 5 + 8 * MuonTile<SHAPE>::kBufs) * 8 + 16;
 }
-static_assert(smem_bytes<kMuonSingle>() <= 232448 && smem_bytes<kMuonWide>() <= 232448, "shared memory per CTA");
+static_assert(smem_bytes<kMuonSingle>() <= 232448 && smem_bytes<kMuonPair>() <= 232448 && smem_bytes<kMuonWide>() <= 232448, "shared memory per CTA");
 
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* m, uint32_t bar, int32_t c0,
                                                  int32_t c1, int32_t c2) {
@@ -462,16 +468,16 @@ __device__ __forceinline__ void write_rows(T* out, int64_t ld, int rows, int col
 
 // The epilogue of one warp: 32 rows (TMEM lanes) of one half of a tile's
 // columns, in groups of 32. What a group reads (X hi and lo, or A) comes by TMA
-// into the warp's own buffers, one group ahead and for a tile's first group
-// before its products are done; what it writes leaves the same buffers by TMA
-// stores. So global memory sees runs of 64 bytes and more, and no warp waits
-// for another. (With each thread reading and writing its own row in global
-// memory every access touched 32 lines: B X of 8 x 1024 x 1024 took 36.8 us,
-// its products 8.7.)
+// into the warp's own buffers, for a tile's first groups before its products
+// are done; what it writes leaves the same buffers by TMA stores. So global
+// memory sees runs of 64 bytes and more, and no warp waits for another. (With
+// each thread reading and writing its own row in global memory every access
+// touched 32 lines: B X of 8 x 1024 x 1024 took 36.8 us, its products 8.7.)
+template <uint32_t BUFS>
 struct MuonEpilogue {
   const MuonArgs& a;
-  uint8_t* buf;        // this warp's 2 x 2 x kEpiPart
-  uint32_t bar;        // this warp's two load barriers
+  uint8_t* buf;        // this warp's BUFS x 2 x kEpiPart
+  uint32_t bar;        // this warp's BUFS load barriers
   int lane;
   uint32_t loads = 0, uses = 0;   // groups loaded, groups taken
 
@@ -479,7 +485,7 @@ struct MuonEpilogue {
   __device__ __forceinline__ void load(const CUtensorMap* e0, const CUtensorMap* e1, int mat, int row0, int c0) {
     if (lane == 0) {
       bulk_wait_group_read<0>();  // the buffer's last stores have read it
-      const uint32_t b = loads & 1u;
+      const uint32_t b = loads % BUFS;
       const uint32_t dst = smem_u32(buf + b * 2 * kEpiPart), bb = bar + 8u * b;
       mbar_arrive_expect_tx(bb, e1 ? 2 * kEpiPart : kEpiPart);
       tma_load_3d(dst, e0, bb, c0, row0, mat);
@@ -511,11 +517,11 @@ struct MuonEpilogue {
   __device__ __forceinline__ bool group(const MuonStep& st, const CUtensorMap* o0, const CUtensorMap* o1, int g, int mat,
                                         int row0, int c0, bool mirror, float factor, const uint32_t (&r)[32]) {
     constexpr bool kSym = PHASE == kMuonGram || PHASE == kMuonPoly;
-    const uint32_t b = PHASE == kMuonGram ? (g & 1) : (uses & 1u);
+    const uint32_t b = PHASE == kMuonGram ? g % BUFS : uses % BUFS;
     uint8_t* p0 = buf + b * 2 * kEpiPart;
     uint8_t* p1 = p0 + kEpiPart;
     if (PHASE != kMuonGram) {
-      if (!__all_sync(kAll, mbar_wait_bounded(bar + 8u * b, (uses >> 1) & 1u, a.ctrl + kCtrlError, a.timeout_ns)))
+      if (!__all_sync(kAll, mbar_wait_bounded(bar + 8u * b, (uses / BUFS) & 1u, a.ctrl + kCtrlError, a.timeout_ns)))
         return false;
       ++uses;
     } else {
@@ -524,7 +530,7 @@ struct MuonEpilogue {
         if (g == 0)
           bulk_wait_group_read<0>();
         else
-          bulk_wait_group_read<1>();
+          bulk_wait_group_read<BUFS - 1>();
       }
       __syncwarp();
     }
@@ -650,8 +656,8 @@ struct MuonEpilogue {
 // epilogue warp adds to the matrix's counter when its part of a tile is in
 // global memory, and a tile's loads wait for the counter to reach all earlier
 // tiles of that matrix. So one matrix's tiles fill the time in which another's
-// are still to finish (as a launch per product, 8 x 1024 x 1024 took 57 us a
-// step, of which its products need 17), and a product starts a flag's latency
+// are still to finish (8 x 1024 x 1024 takes 43 us a step, of which its
+// products need 17; as a launch per product it took 57), and a product starts a flag's latency
 // after its predecessor instead of a launch's. Every slot takes its units in
 // the order of the sequence and all slots are resident (a cooperative launch),
 // so a unit only ever waits for units that run. Every wait is bounded.
@@ -661,7 +667,7 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
                       const __grid_constant__ MuonSteps steps) {
   using Tile = MuonTile<SHAPE>;
   constexpr bool kPaired = SHAPE != kMuonSingle, kWide = SHAPE == kMuonWide;
-  constexpr int kStages = Tile::kStages, kAccs = Tile::kAccs;
+  constexpr int kStages = Tile::kStages, kAccs = Tile::kAccs, kBufs = Tile::kBufs;
   constexpr uint32_t kStageBytes = stage_bytes<SHAPE>();
   constexpr uint32_t kTmemCols = kAccs * Tile::kN;
   constexpr uint32_t kParts = kPaired ? 2 : 1;   // CTAs of a tile
@@ -669,8 +675,8 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sE = smem + kStages * kStageBytes;   // a stage: A, B (wide: B of either half)
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sE + kEpiBytes);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5 + 16);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sE + epi_bytes<SHAPE>());
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5 + 8 * kBufs);
   const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };
@@ -705,7 +711,7 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
       mbar_init(tempty_bar(acc), (kPaired ? 2 : 1) * kEpiThreads);
     }
     mbar_init(drain_bar, 1);
-    for (int i = 0; i < 16; ++i) mbar_init(drain_bar + 8u * (1 + i), 1);  // the epilogue warps' loads
+    for (int i = 0; i < 8 * kBufs; ++i) mbar_init(drain_bar + 8u * (1 + i), 1);  // the epilogue warps' loads
     fence_mbar_init();
     fence_proxy_async_smem();
   }
@@ -859,7 +865,7 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
     constexpr int kHalf = Tile::kN / 2;                     // columns of an epilogue warp
     constexpr int kBlock = SHAPE == kMuonSingle ? 128 : 256;  // the symmetric products' unit of "above the diagonal"
     const int wq = warp & 3, half = (warp - 4) >> 2;
-    MuonEpilogue epi{a, sE + (warp - 4) * 4 * kEpiPart, drain_bar + 8u * (1 + 2 * (warp - 4)), lane};
+    MuonEpilogue<kBufs> epi{a, sE + (warp - 4) * kBufs * 2 * kEpiPart, drain_bar + 8u * (1 + kBufs * (warp - 4)), lane};
     bool ok = true;
     int it = 0;
     auto unit = [&](auto phase_c) {
@@ -887,8 +893,7 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
         if (lane == 0) good = wait_done(a.done + w.mat, w.needed() * kParts, err, a.timeout_ns);
         good = __all_sync(kAll, good);
         if (good) {
-          epi.load(e0, e1, w.mat, row0, col0);
-          if (groups > 1) epi.load(e0, e1, w.mat, row0, col0 + 32);
+          for (int g = 0; g < min(groups, kBufs); ++g) epi.load(e0, e1, w.mat, row0, col0 + g * 32);
           if (!kSym && row0 + lane < a.m)
             factor = st.a + __ldcg(a.diag + static_cast<int64_t>(w.mat) * a.m + row0 + lane);
           if (PHASE == kMuonLast) epi.prefetch_weight(w.mat, row0, col0, kHalf);
@@ -957,8 +962,8 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
               }
             }
           }
-          good = epi.group<PHASE>(st, o0, o1, g, w.mat, row0, col0 + g * 32, kSym && block_n > block_m, factor, r);
-          if (PHASE != kMuonGram && good && g + 2 < groups) epi.load(e0, e1, w.mat, row0, col0 + (g + 2) * 32);
+          good = epi.template group<PHASE>(st, o0, o1, g, w.mat, row0, col0 + g * 32, kSym && block_n > block_m, factor, r);
+          if (PHASE != kMuonGram && good && g + kBufs < groups) epi.load(e0, e1, w.mat, row0, col0 + (g + kBufs) * 32);
         }
       }
       if (PHASE != kMuonLast) {
@@ -987,7 +992,7 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
     // a load that is still in flight lands before the CTA leaves
     if (!ok && lane == 0)
       for (; epi.uses < epi.loads; ++epi.uses)
-        wait_limited(epi.bar + 8u * (epi.uses & 1u), (epi.uses >> 1) & 1u, a.timeout_ns);
+        wait_limited(epi.bar + 8u * (epi.uses % kBufs), (epi.uses / kBufs) & 1u, a.timeout_ns);
   }
 
   __syncwarp();

@@ -19,7 +19,7 @@
 // order, leaves the rounded values as the image of A's tile, and loads that
 // whole; cluster barriers order the three. (An SM sends only about 15 bytes per
 // clock to its peers' shared memories: the same exchange that way, by stores or
-// bulk copies, took 8.6 and 7.6 us a step at 128 x 1024, this SUM_US.) A A and
+// bulk copies, took 8.6 and 7.6 us a step at 128 x 1024, this 7.0.) A A and
 // B are the same small work in every CTA. Rows past the short side are zero.
 //
 // 512 threads; thread t works on row 32 (warp % 4) + lane of an accumulator,
