@@ -258,17 +258,20 @@ __device__ __forceinline__ bool take_largest(const int32_t (&sorted)[NPL], int k
   return D < NPL && h[0] == kNone;
 }
 
-// The first document whose end lies past row r (documents: none does). The
+// The first document whose end lies past row r (documents: none does), by whole
+// warps with one r: 32 ends a step, since the loads' latency is all of it. The
 // index stays in [0, documents] whatever the offsets hold.
 __device__ __forceinline__ int first_document(const int64_t* offsets, int documents, int64_t r) {
   if (!offsets) return 0;
   int lo = 0, hi = documents;
   while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (offsets[mid + 1] > r)
-      hi = mid;
-    else
-      lo = mid + 1;
+    const int stride = (hi - lo + 31) / 32;
+    const int probe = lo + static_cast<int>(threadIdx.x & 31) * stride;
+    const uint32_t past = __ballot_sync(kAll, probe < hi && offsets[probe + 1] > r);
+    const int first = past ? __ffs(past) - 1 : 32;
+    const int probes = (hi - lo + stride - 1) / stride;
+    if (first < probes) hi = lo + first * stride;
+    if (first > 0) lo += (min(first, probes) - 1) * stride + 1;
   }
   return lo;
 }
