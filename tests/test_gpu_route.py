@@ -189,6 +189,33 @@ def test_ties_go_to_the_lowest_expert():
         assert torch.equal(r.experts.cpu().long(), want)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("E", [5, 8, 16, 27, 64, 128, 200, 256, 384, 512, 1024])
+def test_selection_where_the_largest_lie_together(E, dtype):
+    """Which experts are chosen is exact, whatever their order: the largest side by side (in few lanes of a
+    warp), last bits that differ, ties, signed zeros, -inf among them; one expert to 32."""
+    from linear_cross_entropy_token_gb300 import route
+    g = torch.Generator().manual_seed(E)
+    N = 150
+    up = torch.arange(E).float().repeat(N, 1) / 16
+    together = torch.randn(N, E, generator=g)
+    first = torch.randint(0, max(E - 9, 1), (N, 1), generator=g) + torch.arange(min(E, 9))
+    together.scatter_add_(1, first, torch.full((N, first.shape[1]), 8.0))
+    close = 1.0 + torch.randint(0, 40, (N, E), generator=g).float() * 2.0 ** -23
+    few = torch.randint(0, 3, (N, E), generator=g).float() - 1.0
+    zeros = torch.randint(0, 2, (N, E), generator=g).float() * -0.0
+    zeros[:, ::2] *= -1.0
+    holes = torch.where(torch.rand(N, E, generator=g) < 0.9, torch.full((), -math.inf), together)
+    for rows in (up, -up, together, close, -close, few, zeros, holes, torch.zeros(N, E)):
+        z = rows.to(DT[dtype])
+        order = torch.sort(z.double(), dim=1, descending=True, stable=True).indices
+        for k in sorted({1, min(E, 3), min(E, 8), min(E, 32)}):
+            want = order[:, :k]
+            want = torch.where(z.double().gather(1, want) > -math.inf, want, torch.full_like(want, -1))
+            got = route(z.cuda(), k).experts.cpu().long()
+            assert torch.equal(got, want), (k, int((got != want).any(1).nonzero()[0]))
+
+
 @pytest.mark.parametrize("value", [math.nan, math.inf])
 def test_nan_and_infinite_logits_show(value):
     import linear_cross_entropy_token_gb300 as flce
