@@ -324,6 +324,8 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
 
 }  // namespace
 
+// No exception leaves a C entry: what can throw here is a host allocation (a
+// message, the table of cluster sizes).
 extern "C" {
 
 uint64_t flce_route_workspace_bytes(flce_handle_t h, int64_t N, int64_t E, int64_t documents) {
@@ -333,7 +335,7 @@ uint64_t flce_route_workspace_bytes(flce_handle_t h, int64_t N, int64_t E, int64
 }
 
 flce_status flce_route_forward(flce_handle_t h, const flce_route_args* r, void* workspace, uint64_t workspace_bytes,
-                               void* stream) {
+                               void* stream) try {
   if (!h) return FLCE_ERR_INVALID_ARG;
   h->err.clear();
   flce_status st = route_check(h, r);
@@ -369,10 +371,13 @@ flce_status flce_route_forward(flce_handle_t h, const flce_route_args* r, void* 
     FLCE_LAUNCH(FLCE_K_ROUTE_FINISH, 0.0, 8.0 * e * (static_cast<double>(g.blocks) + 2.0 * r->documents),
                 launch_route_finish(g, a, s));
   return FLCE_OK;
+} catch (...) {
+  return FLCE_ERR_BUDGET;
 }
 
 flce_status flce_route_backward(flce_handle_t h, const flce_route_args* r, const float* d_weights,
-                                const float* d_balance, const float* d_z, void* d_logits, int64_t ld_d, void* stream) {
+                                const float* d_balance, const float* d_z, void* d_logits, int64_t ld_d,
+                                void* stream) try {
   if (!h) return FLCE_ERR_INVALID_ARG;
   h->err.clear();
   flce_status st = route_check(h, r);
@@ -390,6 +395,8 @@ flce_status flce_route_backward(flce_handle_t h, const flce_route_args* r, const
               n * (2.0 * e * element_bytes(r->dtype) + 8.0 + (d_weights ? 12.0 * r->k : 0.0)),
               launch_route_backward(r->dtype, g, route_args(r, g), d_weights, d_balance, d_z, d_logits, ld_d, s));
   return FLCE_OK;
+} catch (...) {
+  return FLCE_ERR_BUDGET;
 }
 
 uint64_t flce_muon_workspace_bytes(int64_t rows, int64_t cols, int64_t count) {
@@ -398,7 +405,7 @@ uint64_t flce_muon_workspace_bytes(int64_t rows, int64_t cols, int64_t count) {
 }
 
 flce_status flce_muon_update(flce_handle_t h, const flce_muon_args* q, const flce_muon_matrix* mats, int32_t count,
-                             void* workspace, uint64_t workspace_bytes, void* stream) {
+                             void* workspace, uint64_t workspace_bytes, void* stream) try {
   if (!h) return FLCE_ERR_INVALID_ARG;
   h->err.clear();
   if (!q || count < 0 || (count > 0 && !mats)) return fail(h, FLCE_ERR_INVALID_ARG, "null pointer or bad count");
@@ -461,6 +468,8 @@ flce_status flce_muon_update(flce_handle_t h, const flce_muon_args* q, const flc
     if (st != FLCE_OK) return st;
   }
   return FLCE_OK;
+} catch (...) {
+  return FLCE_ERR_BUDGET;
 }
 
 }  // extern "C"

@@ -108,6 +108,8 @@ def muon_update(grads, momenta=None, weights=None, *, beta: float = 0.95, nester
     base = (ws.data_ptr() + 1023) // 1024 * 1024
     h._check(h.lib.flce_muon_update(h.h, ctypes.byref(a), mats, len(grads), base, nbytes, _stream_ptr(dev)),
              "flce_muon_update")
+    # written behind autograd's back: a backward that saved one of these must fail
+    torch.autograd.graph.increment_version([*(momenta or ()), *(weights or ()), *(updates or ())])
     return updates if weights is None else weights
 
 

@@ -169,7 +169,8 @@ def route_backward(r: Routing, logits: torch.Tensor, d_weights=None, d_balance=N
         p_balance = _scalar("d_balance", d_balance, dev)
     if d_z is not None:
         p_z = _scalar("d_z", d_z, dev)
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty((N, E), dtype=logits.dtype, device=dev)
         ld_out = E
     else:
@@ -182,4 +183,6 @@ def route_backward(r: Routing, logits: torch.Tensor, d_weights=None, d_balance=N
                                    _stream_ptr(dev))
     if st:
         h._check(st, "flce_route_backward")
+    if given:
+        torch.autograd.graph.increment_version(out)
     return out

@@ -262,3 +262,20 @@ def test_optimizer_steps_parameters_of_several_shapes():
             w[i] = (1 - 0.02 * 0.1) * w[i] - 0.02 * o
             assert float((ps[i].detach().cpu().double() - w[i]).norm()) <= (it + 1) * 0.02 * ORTHO * float(o.norm()) + 1e-5
     assert torch.equal(ps[-1].detach(), kept)
+
+
+def test_a_backward_over_updated_weights_fails():
+    """Weights and momenta change in place: autograd must not use the new values for an old forward."""
+    from linear_cross_entropy_token_gb300 import muon_update
+    w = torch.nn.Parameter(torch.randn(32, 48, device="cuda"))
+    m = torch.zeros(32, 48, device="cuda")
+    x = torch.randn(8, 48, device="cuda", requires_grad=True)
+    before = w._version, m._version
+    loss = (x @ w.T).square().sum()
+    muon_update([torch.randn(32, 48, device="cuda")], [m], [w.detach()], lr=0.1)
+    assert w._version > before[0] and m._version > before[1]
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    u = torch.empty(32, 48, device="cuda", dtype=torch.bfloat16)
+    muon_update([torch.randn(32, 48, device="cuda")], updates=[u])
+    assert u._version == 1

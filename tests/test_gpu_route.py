@@ -337,3 +337,13 @@ def test_autograd_against_formula_and_differences():
     (route(zc, k)[0] * m.cuda()).sum().backward()
     ref = reference(z, k, d_weights=m)
     assert bool(((zc.grad.cpu().double() - ref["d"]).abs() <= (3 * tol + 8 * U) * ref["mag"] + 1e-44).all())
+
+
+def test_a_given_output_counts_as_modified():
+    import linear_cross_entropy_token_gb300 as flce
+    z = torch.randn(20, 16, device="cuda")
+    out = torch.zeros_like(z)
+    r = flce.route(z, 2)
+    before = out._version
+    assert flce.route_backward(r, z, d_z=torch.ones((), device="cuda"), out=out) is out
+    assert out._version > before
