@@ -13,6 +13,7 @@ kernels ("Unsloth ì‹¬ì¸µ ì•„í‚¤í…ì²˜ â€¦", section "ì†ŒìŠ¤ì½”ë“œ ë ˆë²¨ ì•„í‚¤í
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import routing
 from .flce import FLCE
@@ -116,6 +117,7 @@ class RouteFunction(torch.autograd.Function):
         return r.weights, r.experts, r.counts, balance, z
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_weights, _d_experts, _d_counts, d_balance, d_z):
         r = routing.Routing()
         logits, r.valid, r.offsets, r.weights, r.experts, r.counts, r.state = ctx.saved_tensors

@@ -347,3 +347,12 @@ def test_a_given_output_counts_as_modified():
     before = out._version
     assert flce.route_backward(r, z, d_z=torch.ones((), device="cuda"), out=out) is out
     assert out._version > before
+
+
+def test_a_second_derivative_is_refused():
+    from linear_cross_entropy_token_gb300.autograd import route
+    z = torch.randn(20, 16, device="cuda", requires_grad=True)
+    # (the gradient that reaches the weights depends on z as well)
+    d, = torch.autograd.grad(route(z, 2)[0].square().sum(), z, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        d.sum().backward()
