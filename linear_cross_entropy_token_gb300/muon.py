@@ -140,6 +140,7 @@ class Muon(torch.optim.Optimizer):
     0.2 sqrt(max(rows, cols)), which gives an update's entries the size of an
     adaptive optimizer's, "spectral" for sqrt(max(1, rows / cols)), or a
     number. Vectors, embeddings and the LM head belong to another optimizer.
+    Momenta are float32 whatever the parameters' type, in checkpoints too.
     """
 
     def __init__(self, params, lr: float = 2e-2, beta: float = 0.95, weight_decay: float = 0.0,
@@ -156,6 +157,32 @@ class Muon(torch.optim.Optimizer):
             for p in group["params"]:
                 if p.dim() != 2 or p.dtype not in DTYPES:
                     raise ValueError("Muon takes 2-D float32 or bfloat16 parameters")
+
+    def load_state_dict(self, state_dict) -> None:
+        """As torch's, but the momenta stay float32: torch gives floating-point
+        state the parameter's type, which for bfloat16 parameters drops bits
+        that no cast back returns. They are taken from the saved tensors."""
+        loaded = []
+
+        def note(_, given):   # after every other such hook: what is really loaded
+            loaded[:] = [given]
+
+        def restore(_):       # before every other: they see the final state
+            given, = loaded
+            ids = [i for group in given["param_groups"] for i in group["params"]]
+            params = [p for group in self.param_groups for p in group["params"]]
+            for i, p in zip(ids, params):
+                momentum = given["state"].get(i, {}).get("momentum")
+                if momentum is not None:
+                    self.state[p]["momentum"] = momentum.to(dtype=torch.float32, device=p.device)
+
+        hooks = (self.register_load_state_dict_pre_hook(note),
+                 self.register_load_state_dict_post_hook(restore, prepend=True))
+        try:
+            super().load_state_dict(state_dict)
+        finally:
+            for hook in hooks:
+                hook.remove()
 
     @torch.no_grad()
     def step(self, closure=None):
