@@ -146,17 +146,32 @@ class Muon(torch.optim.Optimizer):
     def __init__(self, params, lr: float = 2e-2, beta: float = 0.95, weight_decay: float = 0.0,
                  nesterov: bool = True, steps: int = 5, coefficients=None, eps: float = 1e-7,
                  scale="rms"):
-        if not (lr >= 0.0 and 0.0 <= beta <= 1.0 and weight_decay >= 0.0 and eps >= 0.0):
+        defaults = dict(lr=lr, beta=beta, weight_decay=weight_decay, nesterov=nesterov, steps=steps,
+                        coefficients=coefficients, eps=eps, scale=scale)
+        self._check_group({"params": (), **defaults})
+        super().__init__(params, defaults)
+
+    def add_param_group(self, param_group) -> None:
+        """As torch's (the constructor's groups come here too), refused where
+        step could not take the group: the optimizer then stays as it was."""
+        super().add_param_group(param_group)
+        try:
+            self._check_group(self.param_groups[-1])
+        except ValueError:
+            self.param_groups.pop()
+            raise
+
+    @staticmethod
+    def _check_group(group) -> None:
+        if not (group["lr"] >= 0.0 and 0.0 <= group["beta"] <= 1.0 and group["weight_decay"] >= 0.0
+                and group["eps"] >= 0.0):
             raise ValueError("need lr, weight_decay, eps >= 0 and 0 <= beta <= 1")
-        if scale not in ("rms", "spectral") and not isinstance(scale, (int, float)):
+        if group["scale"] not in ("rms", "spectral") and not isinstance(group["scale"], (int, float)):
             raise ValueError("scale must be 'rms', 'spectral' or a number")
-        _coefficients(coefficients, steps)
-        super().__init__(params, dict(lr=lr, beta=beta, weight_decay=weight_decay, nesterov=nesterov,
-                                      steps=steps, coefficients=coefficients, eps=eps, scale=scale))
-        for group in self.param_groups:
-            for p in group["params"]:
-                if p.dim() != 2 or p.dtype not in DTYPES:
-                    raise ValueError("Muon takes 2-D float32 or bfloat16 parameters")
+        _coefficients(group["coefficients"], group["steps"])
+        for p in group["params"]:
+            if p.dim() != 2 or p.dtype not in DTYPES:
+                raise ValueError("Muon takes 2-D float32 or bfloat16 parameters")
 
     def load_state_dict(self, state_dict) -> None:
         """As torch's, but the momenta stay float32: torch gives floating-point
