@@ -1043,8 +1043,9 @@ cudaError_t launch_chained(void (*kern)(P...), dim3 grid, int threads, size_t sm
 template <int SHAPE>
 cudaError_t launch_steps(const MuonMaps& maps, const MuonArgs& a, const MuonSteps& steps, int slots, cudaStream_t s) {
   auto kern = muon_steps_kernel<SHAPE>;
-  static const cudaError_t opted = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                        static_cast<int>(smem_bytes<SHAPE>()));
+  // at every launch: the attribute belongs to the current device, and a process may use several
+  const cudaError_t opted = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(smem_bytes<SHAPE>()));
   if (opted != cudaSuccess) return opted;
   const int64_t most = std::max(a.splits * muon_units<SHAPE>(kMuonGram, a), muon_units<SHAPE>(kMuonApply, a));
   const int n = static_cast<int>(std::min<int64_t>(most, slots));

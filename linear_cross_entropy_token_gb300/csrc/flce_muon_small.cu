@@ -474,11 +474,10 @@ template <int NCH>
 cudaError_t launch_small_t(const MuonArgs& a, const MuonSteps& steps, cudaStream_t s, int* fits) {
   constexpr size_t smem = 1024 + 2 * NCH * kChunkBytes + 2 * kPanelBytes;   // X, A, B
   auto kern = muon_small_kernel<NCH>;
-  static const cudaError_t opted = [&] {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
-    return e != cudaSuccess ? e : cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  }();
+  // at every launch: the attributes belong to the current device, and a process may use several
+  cudaError_t opted = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (opted == cudaSuccess && a.cluster > 8)
+    opted = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (opted != cudaSuccess) return opted;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.count * a.cluster);

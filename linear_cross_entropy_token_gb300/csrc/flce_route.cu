@@ -878,14 +878,13 @@ cudaError_t forward_t(const RouteArgs& a, cudaStream_t s) {
   const size_t rows = kWarps * (32 / G), cols = G * NPL;
   // at most 8 x 32 x 32 + 1024 floats and 8 x 4 x 32 slots, 44 KB (beside 4 KB of static memory)
   const size_t smem = rows * cols * 4 + cols * 4 + std::max<size_t>(rows, 4 * kWarps) * a.k * 8;
-  static const cudaError_t opted = [] {
-    const cudaError_t e =
-        cudaFuncSetAttribute(route_forward_kernel<T, G, NPL, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 45056);
-    return e != cudaSuccess ? e
-                            : cudaFuncSetAttribute(route_forward_kernel<T, G, NPL, false>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, 45056);
-  }();
-  if (opted != cudaSuccess) return opted;
+  // only with the static memory can that pass the default 48 KB; per launch,
+  // since the attribute belongs to the current device
+  if (smem > 40960) {
+    auto kern = a.one_launch ? route_forward_kernel<T, G, NPL, true> : route_forward_kernel<T, G, NPL, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 45056);
+    if (e != cudaSuccess) return e;
+  }
   if (!a.one_launch) {
     route_forward_kernel<T, G, NPL, false><<<a.blocks, kRouteThreads, smem, s>>>(a);
     return cudaGetLastError();
