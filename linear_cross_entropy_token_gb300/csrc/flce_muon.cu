@@ -483,6 +483,7 @@ struct MuonEpilogue {
 
   // TMA loads of the group at column c0 into the next buffer: X hi and lo, or A
   __device__ __forceinline__ void load(const CUtensorMap* e0, const CUtensorMap* e1, int mat, int row0, int c0) {
+    __syncwarp();   // every lane has read what the buffer held
     if (lane == 0) {
       bulk_wait_group_read<0>();  // the buffer's last stores have read it
       const uint32_t b = loads % BUFS;
