@@ -900,7 +900,7 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
         good = __all_sync(kAll, good);
         if (good) {
           for (int g = 0; g < min(groups, kBufs); ++g) epi.load(e0, e1, w.mat, row0, col0 + g * 32);
-          if (!kSym && row0 + lane < a.m)
+          if (!kSym && row0 + lane < a.m)   // (behind lane 0's wait, by the loads' barrier)
             factor = st.a + __ldcg(a.diag + static_cast<int64_t>(w.mat) * a.m + row0 + lane);
           if (PHASE == kMuonLast) epi.prefetch_weight(w.mat, row0, col0, kHalf);
         }
