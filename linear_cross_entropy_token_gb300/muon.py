@@ -72,6 +72,13 @@ def muon_update(grads, momenta=None, weights=None, *, beta: float = 0.95, nester
     with lr and weight_decay (returned), or None: the updates scale * O are
     written to `updates`, new tensors of update_dtype by default (returned).
     """
+    return _update(*_marshal(grads, momenta, weights, beta, nesterov, steps, coefficients, eps, scale, lr, weight_decay,
+                             updates, update_dtype, handle))
+
+
+def _marshal(grads, momenta, weights, beta, nesterov, steps, coefficients, eps, scale, lr, weight_decay, updates=None,
+             update_dtype=torch.bfloat16, handle=None):
+    """The checks of one call, and its library arguments: what _update takes."""
     grads = list(grads)
     momenta = None if momenta is None else list(momenta)
     weights = None if weights is None else list(weights)
@@ -79,7 +86,7 @@ def muon_update(grads, momenta=None, weights=None, *, beta: float = 0.95, nester
         raise ValueError("weights are updated in place: no updates are written")
     table = _coefficients(coefficients, steps)
     if not grads:
-        return [] if weights is None else weights
+        return None, None, (), None, [] if weights is None else weights, ()
     if updates is None and weights is None:
         if update_dtype not in DTYPES:
             raise ValueError("updates must be bfloat16 or float32")
@@ -87,7 +94,6 @@ def muon_update(grads, momenta=None, weights=None, *, beta: float = 0.95, nester
     updates = None if updates is None else list(updates)
     check_muon_tensors(grads, momenta, weights, updates)
     h = _handle(grads[0], handle)
-    dev = grads[0].device
     rows, cols = grads[0].shape
     a = MuonArgs(rows, cols, DTYPES[grads[0].dtype],
                  DTYPE_FP32 if weights is None else DTYPES[weights[0].dtype],
@@ -102,15 +108,22 @@ def muon_update(grads, momenta=None, weights=None, *, beta: float = 0.95, nester
             m.weight, m.ld_weight = weights[i].data_ptr(), _row_stride(weights[i])
         else:
             m.update, m.ld_update = updates[i].data_ptr(), _row_stride(updates[i])
-    nbytes = h.lib.flce_muon_workspace_bytes(rows, cols, len(grads))
+    # written behind autograd's back: a backward that saved one of these must fail
+    written = [*(momenta or ()), *(weights or ()), *(updates or ())]
+    return h, a, mats, grads[0].device, updates if weights is None else weights, written
+
+
+def _update(h, a, mats, dev, result, written):
+    if not mats:
+        return result
+    nbytes = h.lib.flce_muon_workspace_bytes(a.rows, a.cols, len(mats))
     # torch's allocations are 512-byte aligned, the workspace 1024
     ws = torch.empty(nbytes + 1024, dtype=torch.uint8, device=dev)
     base = (ws.data_ptr() + 1023) // 1024 * 1024
-    h._check(h.lib.flce_muon_update(h.h, ctypes.byref(a), mats, len(grads), base, nbytes, _stream_ptr(dev)),
+    h._check(h.lib.flce_muon_update(h.h, ctypes.byref(a), mats, len(mats), base, nbytes, _stream_ptr(dev)),
              "flce_muon_update")
-    # written behind autograd's back: a backward that saved one of these must fail
-    torch.autograd.graph.increment_version([*(momenta or ()), *(weights or ()), *(updates or ())])
-    return updates if weights is None else weights
+    torch.autograd.graph.increment_version(written)
+    return result
 
 
 def orthogonalize(G: torch.Tensor, *, steps: int = 5, coefficients=None, eps: float = 1e-7,
@@ -205,6 +218,9 @@ class Muon(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        # every group is checked before the first is launched, so that a step
+        # that is refused changes nothing
+        calls = []
         for group in self.param_groups:
             alike = {}
             for p in group["params"]:
@@ -220,8 +236,13 @@ class Muon(torch.optim.Optimizer):
                     scale = 0.2 * math.sqrt(max(shape))
                 elif scale == "spectral":
                     scale = math.sqrt(max(1.0, shape[0] / shape[1]))
-                muon_update([p.grad for p in ps], [self.state[p]["momentum"] for p in ps], ps,
-                            beta=group["beta"], nesterov=group["nesterov"], steps=group["steps"],
-                            coefficients=group["coefficients"], eps=group["eps"], scale=scale,
-                            lr=group["lr"], weight_decay=group["weight_decay"])
+                call = _marshal([p.grad for p in ps], [self.state[p]["momentum"] for p in ps], ps, group["beta"],
+                                group["nesterov"], group["steps"], group["coefficients"], group["eps"], scale,
+                                group["lr"], group["weight_decay"])
+                # the library's own checks of the options: with no matrices it makes those alone
+                h, args = call[:2]
+                h._check(h.lib.flce_muon_update(h.h, ctypes.byref(args), None, 0, None, 0, None), "flce_muon_update")
+                calls.append(call)
+        for call in calls:
+            _update(*call)
         return loss
