@@ -23,28 +23,60 @@ MAX_STEPS = 32
 
 
 def check_muon_tensors(grads, momenta, weights, updates) -> None:
-    """Shapes, dtypes, devices and layout of one call's matrices, and that no
-    two that are written start at one address. Raises ValueError."""
+    """Shapes, dtypes, devices and layout of one call's matrices, and that none
+    that is written shares memory with another. Raises ValueError."""
     rows, cols = grads[0].shape if grads[0].dim() == 2 else (0, 0)
     if not (1 <= rows <= MAX_DIM and 1 <= cols <= MAX_DIM):
         raise ValueError(f"the matrices must be 2-D with 1 to {MAX_DIM} rows and columns")
     dev = grads[0].device
-    written = []
+    spans = []   # first byte, one past the last, row stride and row length in bytes, whether it is written
     for name, group, dtypes in (("grads", grads, DTYPES), ("momenta", momenta, (torch.float32,)),
                                 ("weights", weights, DTYPES), ("updates", updates, DTYPES)):
         if group is None:
             continue
         if len(group) != len(grads):
             raise ValueError(f"{name} must have as many matrices as grads")
+        dtype = group[0].dtype
+        if dtype not in dtypes:
+            raise ValueError(f"{name} must be of a supported dtype")
+        size = group[0].element_size()
+        length, reach, is_written = cols * size, (rows - 1) * size, name != "grads"
         for t in group:
-            if tuple(t.shape) != (rows, cols) or t.dtype != group[0].dtype or t.dtype not in dtypes:
+            if tuple(t.shape) != (rows, cols) or t.dtype != dtype:
                 raise ValueError(f"{name} must all be of shape ({rows}, {cols}) and of one supported dtype")
-            if t.device != dev or (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+            stride, inner = t.stride()
+            if t.device != dev or (cols > 1 and inner != 1) or (rows > 1 and stride < cols):
                 raise ValueError(f"{name} must have contiguous rows that do not overlap, on {dev}")
-        if name != "grads":
-            written += [t.data_ptr() for t in group]
-    if dev.type != "meta" and len(set(written)) != len(written):
-        raise ValueError("a matrix that is written appears twice")
+            start = t.data_ptr()
+            spans.append((start, start + reach * stride + length, stride * size, length, is_written))
+    spans.sort()
+    if dev.type == "meta" or all(one[1] <= two[0] for one, two in zip(spans, spans[1:])):
+        return
+    open_spans = []   # that reach past the current one's first byte: slices of one tensor, or gradients
+    for span in spans:
+        open_spans = [other for other in open_spans if other[1] > span[0]]
+        if any((span[4] or other[4]) and _meet(other, span) for other in open_spans):
+            raise ValueError("a matrix that is written overlaps another of the call")
+        open_spans.append(span)
+
+
+def _meet(a, b) -> bool:
+    """Whether two matrices whose address ranges meet, the second starting no
+    earlier than the first, share a byte."""
+    (start_a, end_a, stride_a, length_a, _), (start_b, end_b, stride_b, length_b, _) = a, b
+    if end_a - start_a == length_a and end_b - start_b == length_b:   # one row each
+        return True
+    if stride_a == stride_b:   # slices of one tensor: each row of b stands alike to a row of a and the next
+        row, into = divmod(start_b - start_a, stride_a)
+        return into < length_a or (into + length_b > stride_a and start_a + (row + 1) * stride_a < end_a)
+    while start_a < end_a and start_b < end_b:   # row by row
+        if start_a + length_a <= start_b:
+            start_a += stride_a
+        elif start_b + length_b <= start_a:
+            start_b += stride_b
+        else:
+            return True
+    return False
 
 
 def _coefficients(coefficients, steps):
