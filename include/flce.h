@@ -299,8 +299,8 @@ flce_status flce_forward_backward_async(flce_handle_t h, const void* x, const vo
                                         void* stream);
 
 /* Waits for `stream` and returns the first device-side error that
- * flce_forward_backward_async and flce_forward_backward_shard calls recorded
- * since the last flce_async_status
+ * flce_forward_backward_async, flce_forward_backward_shard and flce_muon_update
+ * calls recorded since the last flce_async_status
  * (FLCE_OK if none), then clears it. It reads the workspace the handle holds
  * now: an error recorded before the workspace was replaced is lost. */
 flce_status flce_async_status(flce_handle_t h, void* stream);
@@ -507,7 +507,8 @@ flce_status flce_route_backward(flce_handle_t h, const flce_route_args* args, co
  * norms and the weight update are fp32 (the norm fp64). Matrices of one call
  * share sizes and types; strides may differ. No host synchronisation;
  * capturable. A device-side wait that ran out is reported by
- * flce_async_status; the outputs are then unspecified. */
+ * flce_async_status or the handle's next update; the outputs are then
+ * unspecified. */
 #define FLCE_MUON_MAX_STEPS 32
 typedef struct flce_muon_args {
     int64_t rows, cols;          /* 1 .. 65536                                         */
@@ -538,7 +539,10 @@ uint64_t flce_muon_workspace_bytes(int64_t rows, int64_t cols, int64_t count);
 
 /* mats: HOST array of count entries. The workspace (device, 1024-byte aligned)
  * is the caller's, as for flce_route_forward. The tensors of one call must not
- * overlap. Errors: INVALID_ARG, UNSUPPORTED, BUDGET (workspace), CUDA. */
+ * overlap. Errors: INVALID_ARG, UNSUPPORTED, BUDGET (workspace), CUDA; TIMEOUT
+ * if a device-side wait of an earlier update on this handle ran out and
+ * flce_async_status has not told so (this call then launches nothing, and the
+ * next one runs). */
 flce_status flce_muon_update(flce_handle_t h, const flce_muon_args* args, const flce_muon_matrix* mats,
                              int32_t count, void* workspace, uint64_t workspace_bytes, void* stream);
 
@@ -559,6 +563,16 @@ flce_status flce_check_gemm(flce_handle_t h, int32_t a_mn_major, int32_t b_mn_ma
  * expected result (the kernel gave up, recorded the error and returned
  * normally; the context stays usable). Synchronises. */
 flce_status flce_check_wait_timeout(flce_handle_t h, uint32_t timeout_us, void* stream);
+
+/* flce_muon_update on the tiled kernels (both sides above 128), each wait
+ * limited to timeout_us microseconds, where every product asks for one finished
+ * tile more than there are before it: the first waits run out, the kernel
+ * records that and returns normally, and the matrices stay unspecified.
+ * flce_async_status, or the handle's next flce_muon_update, reports TIMEOUT.
+ * timeout_us >= 1000. Does not synchronise. */
+flce_status flce_check_muon_timeout(flce_handle_t h, const flce_muon_args* args, const flce_muon_matrix* mats,
+                                    int32_t count, void* workspace, uint64_t workspace_bytes, uint32_t timeout_us,
+                                    void* stream);
 
 #ifdef __cplusplus
 }

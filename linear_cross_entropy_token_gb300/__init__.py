@@ -8,10 +8,10 @@ expert routing with its balance loss (``route``, ``route_backward``) and the
 orthogonalised momentum update of weight matrices (``muon_update``,
 ``orthogonalize``, the optimizer ``Muon``).
 """
-from .flce import (FLCE, FlceError, KERNEL_KINDS, forward_backward, header_functions, load,
+from .flce import (FLCE, FlceError, KERNEL_KINDS, async_status, forward_backward, header_functions, load,
                    loss_static, plan)
 
-__all__ = ["FLCE", "FlceError", "KERNEL_KINDS", "Muon", "Routing", "forward_backward",
+__all__ = ["FLCE", "FlceError", "KERNEL_KINDS", "Muon", "Routing", "async_status", "forward_backward",
            "header_functions", "load", "loss_static", "muon_update", "orthogonalize", "plan", "route",
            "route_backward"]
 

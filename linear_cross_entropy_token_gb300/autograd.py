@@ -16,9 +16,10 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import routing
-from .flce import FLCE
+from .flce import FLCE, _caches
 
 _handles = {}
+_caches.append(_handles)
 
 
 def _handle(device: torch.device, dtype: torch.dtype, dlogits_mode: str = "auto",
@@ -91,10 +92,10 @@ def linear_cross_entropy(x: torch.Tensor, W: torch.Tensor, t: torch.Tensor,
 
     sync_free=True never blocks the host (a step can then be captured in a
     CUDA graph): the loss is NaN after a device-side error, which
-    FLCE.async_status() reports, and the backward always scales dx and dW by
-    the incoming gradient (one extra pass over dW). The default synchronises
-    once per call, raises on errors at once, and skips that pass when the
-    incoming gradient is 1.
+    FLCE.async_status() and async_status() report, and the backward always
+    scales dx and dW by the incoming gradient (one extra pass over dW). The
+    default synchronises once per call, raises on errors at once, and skips
+    that pass when the incoming gradient is 1.
 
     Without a `handle`, one is kept per (device, dtype, dlogits_mode,
     hbm_budget_bytes): dlogits_mode "slabs" with a small budget gives the

@@ -754,7 +754,7 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
         const CUtensorMap* mb = w.phase == kMuonGram ? &maps.xk[src] : w.phase == kMuonPoly ? &maps.gk : &maps.xn[src];
         const uint32_t needed = w.needed() * kParts;
         if (w.mat != seen_mat || needed != seen) {
-          if (needed > 0 && !wait_done(a.done + w.mat, needed, err, a.timeout_ns)) {
+          if (needed > 0 && !wait_done(a.done + w.mat, needed + a.hold, err, a.timeout_ns)) {
             failed = true;
             break;
           }
@@ -896,7 +896,7 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
       float factor = 0.f;
       bool good = true;
       if (PHASE != kMuonGram && groups > 0) {
-        if (lane == 0) good = wait_done(a.done + w.mat, w.needed() * kParts, err, a.timeout_ns);
+        if (lane == 0) good = wait_done(a.done + w.mat, w.needed() * kParts + a.hold, err, a.timeout_ns);
         good = __all_sync(kAll, good);
         if (good) {
           for (int g = 0; g < min(groups, kBufs); ++g) epi.load(e0, e1, w.mat, row0, col0 + g * 32);

@@ -107,6 +107,7 @@ struct MuonArgs {
   uint16_t* poly;                    // [count][m][lda] fp16, B scaled by 2^11, zero diagonal
   int64_t ldx, lda;
   uint64_t timeout_ns;
+  uint32_t hold;                     // finished parts waited for beyond those there are: 0, but where waits are to run out
   int32_t cluster;                   // small matrices: CTAs per matrix
 };
 

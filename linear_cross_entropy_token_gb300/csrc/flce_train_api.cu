@@ -195,7 +195,7 @@ bool map_half_3d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
 
 // One group of matrices: momentum, X, the Newton-Schulz steps, the result.
 flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_muon_matrix* mats, int count,
-                           const float* coefficients, uint8_t* ws, cudaStream_t s) {
+                           const float* coefficients, uint8_t* ws, uint32_t hold, uint64_t timeout_ns, cudaStream_t s) {
   const MuonSizes z = muon_sizes(q->rows, q->cols);
   const MuonLayout L = muon_layout(q->rows, q->cols, count);
   MuonArgs a{};
@@ -256,7 +256,8 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
   a.poly = reinterpret_cast<uint16_t*>(ws + L.poly);
   a.ldx = z.ldx;
   a.lda = z.lda;
-  a.timeout_ns = h->timeout_ns;
+  a.timeout_ns = timeout_ns;
+  a.hold = hold;
 
   const double el = static_cast<double>(q->rows) * q->cols * count;
   const double dm = static_cast<double>(z.m), dn = static_cast<double>(z.n);
@@ -319,6 +320,80 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
   FLCE_LAUNCH(FLCE_K_MUON_STEPS, flops, q->steps * count * (12.0 * dm * dn + 6.0 * dm * dm),
               launch_muon_steps(plan.shape, maps, a, steps,
                                 plan.shape == kMuonSingle ? h->num_sms : h->muon_clusters, s));
+  return FLCE_OK;
+}
+
+// flce_muon_update, its waits limited to timeout_ns, for `hold` finished parts more than there are
+flce_status muon_run(flce_handle_t h, const flce_muon_args* q, const flce_muon_matrix* mats, int32_t count,
+                     void* workspace, uint64_t workspace_bytes, uint32_t hold, uint64_t timeout_ns, void* stream) {
+  if (!h) return FLCE_ERR_INVALID_ARG;
+  h->err.clear();
+  if (!q || count < 0 || (count > 0 && !mats)) return fail(h, FLCE_ERR_INVALID_ARG, "null pointer or bad count");
+  if (!muon_size_ok(q->rows, q->cols, count))
+    return fail(h, FLCE_ERR_INVALID_ARG, "need 1 <= rows, cols <= %lld", (long long)kMuonMaxDim);
+  auto is_type = [](int d) { return d == FLCE_DTYPE_BF16 || d == FLCE_DTYPE_FP32; };
+  if (!is_type(q->grad_dtype) || !is_type(q->weight_dtype) || !is_type(q->update_dtype))
+    return fail(h, FLCE_ERR_UNSUPPORTED, "gradients, weights and updates must be bf16 or fp32");
+  if (q->steps < 1 || q->steps > FLCE_MUON_MAX_STEPS)
+    return fail(h, FLCE_ERR_INVALID_ARG, "need 1 <= steps <= %d", FLCE_MUON_MAX_STEPS);
+  const double numbers[] = {q->beta, q->eps, q->scale, q->lr, q->weight_decay};
+  for (double v : numbers)
+    if (!std::isfinite(v)) return fail(h, FLCE_ERR_INVALID_ARG, "beta, eps, scale, lr and weight_decay must be finite");
+  if (q->beta < 0.0 || q->beta > 1.0 || q->eps < 0.0)
+    return fail(h, FLCE_ERR_INVALID_ARG, "need 0 <= beta <= 1 and eps >= 0");
+  float coefficients[3 * FLCE_MUON_MAX_STEPS];
+  double reach = 1.0;  // bound of X's singular values before the step
+  for (int k = 0; k < q->steps; ++k) {
+    static const float standard[3] = {3.4445f, -4.7750f, 2.0315f};
+    const float* c = q->coefficients ? q->coefficients + 3 * k : standard;
+    for (int i = 0; i < 3; ++i) {
+      coefficients[3 * k + i] = c[i];
+      if (!std::isfinite(c[i])) return fail(h, FLCE_ERR_INVALID_ARG, "coefficients must be finite");
+    }
+    double poly, next;
+    muon_map_bounds(c[0], c[1], c[2], reach, &poly, &next);
+    // 2^12 X, 2^12 A and 2^11 B are held in fp16 (65504)
+    if (reach > 3.9 || poly > 30.0)
+      return fail(h, FLCE_ERR_INVALID_ARG, "the coefficients of step %d take X out of the products' range", k);
+    reach = next;
+  }
+  for (int i = 0; i < count; ++i) {
+    const flce_muon_matrix& t = mats[i];
+    if (!t.grad || (!t.weight && !t.update))
+      return fail(h, FLCE_ERR_INVALID_ARG, "matrix %d: a gradient, and a weight or an update, are needed", i);
+    if ((t.momentum != nullptr) != (mats[0].momentum != nullptr) ||
+        (t.weight != nullptr) != (mats[0].weight != nullptr))
+      return fail(h, FLCE_ERR_INVALID_ARG, "either all matrices have momentum (weights) or none");
+    if (t.ld_grad < q->cols || (t.momentum && t.ld_momentum < q->cols) || (t.weight && t.ld_weight < q->cols) ||
+        (!t.weight && t.ld_update < q->cols))
+      return fail(h, FLCE_ERR_INVALID_ARG, "matrix %d: a row stride is below cols", i);
+    if (addr(t.grad) % element_bytes(q->grad_dtype) || addr(t.momentum) % 4 ||
+        (t.weight && addr(t.weight) % element_bytes(q->weight_dtype)) ||
+        (!t.weight && addr(t.update) % element_bytes(q->update_dtype)))
+      return fail(h, FLCE_ERR_INVALID_ARG, "matrix %d: a pointer is not aligned to its elements", i);
+  }
+  if (count == 0) return FLCE_OK;
+  const int64_t group = muon_group(q->rows, q->cols, count);
+  const uint64_t need = muon_layout(q->rows, q->cols, group).total;
+  if (!workspace || addr(workspace) % kAlign || workspace_bytes < need)
+    return fail(h, FLCE_ERR_BUDGET, "the workspace must hold %llu bytes, %llu-byte aligned",
+                static_cast<unsigned long long>(need), static_cast<unsigned long long>(kAlign));
+  // the matrices of an update whose wait ran out are unspecified, and most likely
+  // this one's too: told once, here or by flce_async_status
+  volatile uint32_t* earlier = h->host_ctrl + kCtrlSticky;
+  if (*earlier != 0) {
+    *earlier = 0;
+    return fail(h, FLCE_ERR_TIMEOUT, "a device-side wait of an earlier update ran out: its results are unspecified");
+  }
+  DeviceGuard guard(h->device);
+  if (h->muon_clusters == 0) h->muon_clusters = muon_max_clusters();
+  if (h->muon_clusters <= 0) return fail(h, FLCE_ERR_UNSUPPORTED, "no CTA pair fits the device");
+  for (int64_t i = 0; i < count; i += group) {
+    const flce_status st = muon_group_run(h, q, mats + i, static_cast<int>(std::min<int64_t>(group, count - i)),
+                                          coefficients, static_cast<uint8_t*>(workspace), hold, timeout_ns,
+                                          static_cast<cudaStream_t>(stream));
+    if (st != FLCE_OK) return st;
+  }
   return FLCE_OK;
 }
 
@@ -406,68 +481,17 @@ uint64_t flce_muon_workspace_bytes(int64_t rows, int64_t cols, int64_t count) {
 
 flce_status flce_muon_update(flce_handle_t h, const flce_muon_args* q, const flce_muon_matrix* mats, int32_t count,
                              void* workspace, uint64_t workspace_bytes, void* stream) try {
-  if (!h) return FLCE_ERR_INVALID_ARG;
-  h->err.clear();
-  if (!q || count < 0 || (count > 0 && !mats)) return fail(h, FLCE_ERR_INVALID_ARG, "null pointer or bad count");
-  if (!muon_size_ok(q->rows, q->cols, count))
-    return fail(h, FLCE_ERR_INVALID_ARG, "need 1 <= rows, cols <= %lld", (long long)kMuonMaxDim);
-  auto is_type = [](int d) { return d == FLCE_DTYPE_BF16 || d == FLCE_DTYPE_FP32; };
-  if (!is_type(q->grad_dtype) || !is_type(q->weight_dtype) || !is_type(q->update_dtype))
-    return fail(h, FLCE_ERR_UNSUPPORTED, "gradients, weights and updates must be bf16 or fp32");
-  if (q->steps < 1 || q->steps > FLCE_MUON_MAX_STEPS)
-    return fail(h, FLCE_ERR_INVALID_ARG, "need 1 <= steps <= %d", FLCE_MUON_MAX_STEPS);
-  const double numbers[] = {q->beta, q->eps, q->scale, q->lr, q->weight_decay};
-  for (double v : numbers)
-    if (!std::isfinite(v)) return fail(h, FLCE_ERR_INVALID_ARG, "beta, eps, scale, lr and weight_decay must be finite");
-  if (q->beta < 0.0 || q->beta > 1.0 || q->eps < 0.0)
-    return fail(h, FLCE_ERR_INVALID_ARG, "need 0 <= beta <= 1 and eps >= 0");
-  float coefficients[3 * FLCE_MUON_MAX_STEPS];
-  double reach = 1.0;  // bound of X's singular values before the step
-  for (int k = 0; k < q->steps; ++k) {
-    static const float standard[3] = {3.4445f, -4.7750f, 2.0315f};
-    const float* c = q->coefficients ? q->coefficients + 3 * k : standard;
-    for (int i = 0; i < 3; ++i) {
-      coefficients[3 * k + i] = c[i];
-      if (!std::isfinite(c[i])) return fail(h, FLCE_ERR_INVALID_ARG, "coefficients must be finite");
-    }
-    double poly, next;
-    muon_map_bounds(c[0], c[1], c[2], reach, &poly, &next);
-    // 2^12 X, 2^12 A and 2^11 B are held in fp16 (65504)
-    if (reach > 3.9 || poly > 30.0)
-      return fail(h, FLCE_ERR_INVALID_ARG, "the coefficients of step %d take X out of the products' range", k);
-    reach = next;
-  }
-  for (int i = 0; i < count; ++i) {
-    const flce_muon_matrix& t = mats[i];
-    if (!t.grad || (!t.weight && !t.update))
-      return fail(h, FLCE_ERR_INVALID_ARG, "matrix %d: a gradient, and a weight or an update, are needed", i);
-    if ((t.momentum != nullptr) != (mats[0].momentum != nullptr) ||
-        (t.weight != nullptr) != (mats[0].weight != nullptr))
-      return fail(h, FLCE_ERR_INVALID_ARG, "either all matrices have momentum (weights) or none");
-    if (t.ld_grad < q->cols || (t.momentum && t.ld_momentum < q->cols) || (t.weight && t.ld_weight < q->cols) ||
-        (!t.weight && t.ld_update < q->cols))
-      return fail(h, FLCE_ERR_INVALID_ARG, "matrix %d: a row stride is below cols", i);
-    if (addr(t.grad) % element_bytes(q->grad_dtype) || addr(t.momentum) % 4 ||
-        (t.weight && addr(t.weight) % element_bytes(q->weight_dtype)) ||
-        (!t.weight && addr(t.update) % element_bytes(q->update_dtype)))
-      return fail(h, FLCE_ERR_INVALID_ARG, "matrix %d: a pointer is not aligned to its elements", i);
-  }
-  if (count == 0) return FLCE_OK;
-  const int64_t group = muon_group(q->rows, q->cols, count);
-  const uint64_t need = muon_layout(q->rows, q->cols, group).total;
-  if (!workspace || addr(workspace) % kAlign || workspace_bytes < need)
-    return fail(h, FLCE_ERR_BUDGET, "the workspace must hold %llu bytes, %llu-byte aligned",
-                static_cast<unsigned long long>(need), static_cast<unsigned long long>(kAlign));
-  DeviceGuard guard(h->device);
-  if (h->muon_clusters == 0) h->muon_clusters = muon_max_clusters();
-  if (h->muon_clusters <= 0) return fail(h, FLCE_ERR_UNSUPPORTED, "no CTA pair fits the device");
-  for (int64_t i = 0; i < count; i += group) {
-    const flce_status st = muon_group_run(h, q, mats + i, static_cast<int>(std::min<int64_t>(group, count - i)),
-                                          coefficients, static_cast<uint8_t*>(workspace),
-                                          static_cast<cudaStream_t>(stream));
-    if (st != FLCE_OK) return st;
-  }
-  return FLCE_OK;
+  return muon_run(h, q, mats, count, workspace, workspace_bytes, 0, h ? h->timeout_ns : 0, stream);
+} catch (...) {
+  return FLCE_ERR_BUDGET;
+}
+
+flce_status flce_check_muon_timeout(flce_handle_t h, const flce_muon_args* q, const flce_muon_matrix* mats,
+                                    int32_t count, void* workspace, uint64_t workspace_bytes, uint32_t timeout_us,
+                                    void* stream) try {
+  // a CTA whose wait ran out waits as long for its own copies in flight
+  if (timeout_us < 1000) return h ? fail(h, FLCE_ERR_INVALID_ARG, "need timeout_us >= 1000") : FLCE_ERR_INVALID_ARG;
+  return muon_run(h, q, mats, count, workspace, workspace_bytes, 1, timeout_us * 1000ull, stream);
 } catch (...) {
   return FLCE_ERR_BUDGET;
 }

@@ -142,6 +142,8 @@ def load() -> ctypes.CDLL:
         "flce_route_forward": (i32, [vp, ctypes.POINTER(RouteArgs), vp, u64, vp]),
         "flce_route_backward": (i32, [vp, ctypes.POINTER(RouteArgs), vp, vp, vp, vp, i64, vp]),
         "flce_muon_workspace_bytes": (u64, [i64, i64, i64]),
+        "flce_check_muon_timeout": (i32, [vp, ctypes.POINTER(MuonArgs), ctypes.POINTER(MuonMatrix), i32, vp,
+                                          u64, u32, vp]),
         "flce_muon_update": (i32, [vp, ctypes.POINTER(MuonArgs), ctypes.POINTER(MuonMatrix), i32, vp,
                                    u64, vp]),
     }
@@ -352,7 +354,8 @@ class FLCE:
 
     def async_status(self) -> None:
         """Wait for the current stream; raise FlceError for a device-side
-        error recorded by forward_backward_async calls since the last check."""
+        error recorded by forward_backward_async, forward_backward_shard and
+        muon_update calls on this handle since the last check."""
         import torch
         st = self.lib.flce_async_status(self.h, _stream_ptr(torch.device("cuda", self.device)))
         self._check(st, "flce_async_status")
@@ -494,6 +497,7 @@ def loss_static(x, W, t, ignore_index: int = -100, token_loss=None):
 
 
 _handles = {}
+_caches = [_handles]   # every module's handles, by keys that start with the device
 
 
 def cached_handle(device_index: int, dtype: str = "bf16") -> FLCE:
@@ -502,6 +506,28 @@ def cached_handle(device_index: int, dtype: str = "bf16") -> FLCE:
     if key not in _handles:
         _handles[key] = FLCE(dtype, key[0])
     return _handles[key]
+
+
+def async_status(device=None) -> None:
+    """Wait for the device's current stream; raise FlceError for a device-side
+    error that a call without a handle of its own (muon_update, Muon.step, the
+    autograd functions) recorded since the last check. Such calls do not wait
+    for their work, so their errors show here, or for an update in the next
+    update."""
+    import torch
+    index = torch.device("cuda" if device is None else device).index
+    if index is None:
+        index = torch.cuda.current_device()
+    first = None
+    for cache in _caches:
+        for key, h in list(cache.items()):
+            if key[0] == index:
+                try:
+                    h.async_status()
+                except FlceError as e:
+                    first = first or e
+    if first:
+        raise first
 
 
 def forward_backward(x, W, t, ignore_index: int = -100, chunk: int = 0):

@@ -103,6 +103,10 @@ def muon_update(grads, momenta=None, weights=None, *, beta: float = 0.95, nester
     themselves. weights: list of float32 or bfloat16 tensors, updated in place
     with lr and weight_decay (returned), or None: the updates scale * O are
     written to `updates`, new tensors of update_dtype by default (returned).
+
+    The call returns once its work is enqueued. A device-side wait that ran out
+    (a GPU that no longer makes progress) leaves the results unspecified:
+    async_status() raises for it, or the next update does.
     """
     return _update(*_marshal(grads, momenta, weights, beta, nesterov, steps, coefficients, eps, scale, lr, weight_decay,
                              updates, update_dtype, handle))
