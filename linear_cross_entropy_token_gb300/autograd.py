@@ -112,7 +112,10 @@ class RouteFunction(torch.autograd.Function):
         # the outputs are separate tensors: the losses of r are views of one
         balance, z = r.balance.clone(), r.z.clone()
         ctx.handle, ctx.k, ctx.renormalize = handle, k, renormalize
-        ctx.save_for_backward(logits, valid, offsets, r.weights, r.experts, r.counts, r.state)
+        # counts and valid are not read by the backward, so callers may change
+        # them (counts summed over ranks, a mask's buffer filled again)
+        ctx.counts = r.counts
+        ctx.save_for_backward(logits, offsets, r.weights, r.experts, r.state)
         ctx.mark_non_differentiable(r.experts, r.counts)
         ctx.set_materialize_grads(False)
         return r.weights, r.experts, r.counts, balance, z
@@ -121,8 +124,8 @@ class RouteFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, d_weights, _d_experts, _d_counts, d_balance, d_z):
         r = routing.Routing()
-        logits, r.valid, r.offsets, r.weights, r.experts, r.counts, r.state = ctx.saved_tensors
-        r.k, r.renormalize = ctx.k, ctx.renormalize
+        logits, r.offsets, r.weights, r.experts, r.state = ctx.saved_tensors
+        r.valid, r.counts, r.k, r.renormalize = None, ctx.counts, ctx.k, ctx.renormalize
         d = None
         if ctx.needs_input_grad[0]:
             if d_weights is not None:
