@@ -450,8 +450,10 @@ flce_status flce_loss_static(const void* x, const void* W, const int64_t* t, int
  * both 0 if n = 0. A slot whose z is -inf, and every slot of a token that is
  * not live, gets expert -1 and weight 0 and is not counted. A NaN or +inf
  * logit makes its token's weights and the losses NaN (its experts stay in
- * [-1, E)). Arithmetic is fp32, sums over blocks fp64, results repeat bit for
- * bit. No host synchronisation; capturable. */
+ * [-1, E)). Arithmetic and sums are fp32; the sums run in a fixed order (a
+ * lane's rows, a block's lanes, the blocks in a tree), so results repeat bit for
+ * bit, and fp64 joins only what many documents or experts add to the balance
+ * and z losses. No host synchronisation; capturable. */
 typedef struct flce_route_args {
     const void* logits;          /* device, N rows of E, bf16, fp32 or fp16            */
     int32_t dtype;               /* FLCE_DTYPE_* of logits                             */
@@ -475,7 +477,7 @@ typedef struct flce_route_args {
 /* Workspace bytes of flce_route_forward (0: bad argument). Host only. */
 uint64_t flce_route_workspace_bytes(flce_handle_t h, int64_t N, int64_t E, int64_t documents);
 
-/* Fills weights, experts, counts, lse, slope and result on `stream`. The
+/* Fills weights, experts, counts, stats, slope and result on `stream`. The
  * workspace (device, 256-byte aligned) is the caller's and free again when the
  * call's work is done, so calls on several streams take one each. Offsets are
  * not checked on the host; whatever they hold, no access leaves the buffers.
@@ -486,7 +488,8 @@ flce_status flce_route_forward(flce_handle_t h, const flce_route_args* args, voi
 /* d_logits (device, N x E, dtype of logits, row stride ld_d) from the
  * gradients of weights (N x k fp32, or NULL), balance and z (one fp32 on the
  * device each, or NULL). args are those of the forward, with its outputs
- * unchanged. The counts carry no gradient. Rows that are not live get zeros.
+ * unchanged, but for counts and valid, which it does not read. The counts carry
+ * no gradient. Rows that are not live get zeros.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 flce_status flce_route_backward(flce_handle_t h, const flce_route_args* args, const float* d_weights,
                                 const float* d_balance, const float* d_z, void* d_logits, int64_t ld_d,
@@ -502,9 +505,12 @@ flce_status flce_route_backward(flce_handle_t h, const flce_route_args* args, co
  *   else            update = O, rounded once to its type
  * The products run on the tensor cores with fp16 operands (X, A and B scaled
  * by powers of two, X itself held in 22 bits, the diagonal of B in fp32) and
- * fp32 accumulators: O is within about 2.5e-3 of its own norm of the exact
- * result, the size of one bf16 rounding, whatever the spectrum. Momentum,
- * norms and the weight update are fp32 (the norm fp64). Matrices of one call
+ * fp32 accumulators: O is within 5e-3 of its own norm of the exact result
+ * whatever the spectrum (2e-4 to 2.5e-3 was seen; iterates in fp32 are about
+ * 1e-4 off). That is the size of one rounding of O to bf16 (1.7e-3); where the
+ * updates or weights are fp32 it is all of O's error. Momentum, norms and the
+ * weight update are fp32 (squares summed in three ranges, so that no sum over-
+ * or underflows; a block's warps joined in fp64). Matrices of one call
  * share sizes and types; strides may differ. No host synchronisation;
  * capturable. A device-side wait that ran out is reported by
  * flce_async_status or the handle's next update; the outputs are then
@@ -538,8 +544,8 @@ typedef struct flce_muon_matrix {
 uint64_t flce_muon_workspace_bytes(int64_t rows, int64_t cols, int64_t count);
 
 /* mats: HOST array of count entries. The workspace (device, 1024-byte aligned)
- * is the caller's, as for flce_route_forward. The tensors of one call must not
- * overlap. Errors: INVALID_ARG, UNSUPPORTED, BUDGET (workspace), CUDA; TIMEOUT
+ * is the caller's, as for flce_route_forward. A matrix that is written must
+ * share no element with another of the call. Errors: INVALID_ARG, UNSUPPORTED, BUDGET (workspace), CUDA; TIMEOUT
  * if a device-side wait of an earlier update on this handle ran out and
  * flce_async_status has not told so (this call then launches nothing, and the
  * next one runs). */

@@ -16,7 +16,8 @@
 // too (an expert's column belongs to one lane) until a block's piece of a
 // document ends. Sums over tokens are taken in a fixed order (per piece, then
 // over the pieces), so results repeat bit for bit; only integer counts use
-// atomics. All arithmetic is fp32, but for the sums over documents (fp64).
+// atomics. All arithmetic is fp32, but for a thread's share of the documents'
+// terms in the closing pass, and the terms of the one-cluster form (fp64).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
