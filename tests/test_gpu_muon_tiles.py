@@ -48,3 +48,15 @@ def test_more_tiles_than_fit_at_once(rows, cols, cta, weight_dtype):
     """X has more tiles than the GPU holds at once (90 of 256 x 512 on 76 pairs); the last step of a tall matrix writes its columns, and on the
     widest tiles loads the next group into the buffer that it has just read."""
     check_updates(rows, cols, 1, weight_dtype, cta)
+
+
+@pytest.mark.parametrize("rows,cols,count", [(300, 1000, 8), (150, 200, 35), (256, 4096, 3), (5000, 300, 3), (129, 130, 33)])
+def test_many_matrices_and_groups(rows, cols, count):
+    """Different matrices side by side in one launch, their sums split, and more of them than one group holds
+    (32), so that the second group takes over the first one's workspace."""
+    check_updates(rows, cols, count, torch.float32)
+
+
+@pytest.mark.parametrize("cta", ["single", "pair", "wide"])
+def test_groups_on_each_tile_shape(cta):
+    check_updates(300, 500, 34, torch.bfloat16, cta)
