@@ -40,9 +40,9 @@ struct RouteArgs {
   int32_t* unit_c;          // [units][E] chosen slots
   int32_t* unit_live;       // [units]
   float* unit_z;            // [units] sums of lse^2
-  double* terms;            // [documents * chunks]
+  float* terms;             // [documents * chunks] balance terms
   int32_t* doc_live;        // [documents]
-  double* doc_z;            // [documents]
+  float* doc_z;             // [documents]
   uint32_t* ticket;
 };
 

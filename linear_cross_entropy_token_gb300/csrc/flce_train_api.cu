@@ -35,9 +35,9 @@ RouteLayout route_layout(const RouteGeometry& g, int64_t E, int64_t documents) {
   l.unit_c = take(units * E * 4);
   l.unit_live = take(units * 4);
   l.unit_z = take(units * 4);
-  l.terms = take(static_cast<uint64_t>(documents) * g.chunks * 8);
+  l.terms = take(static_cast<uint64_t>(documents) * g.chunks * 4);
   l.doc_live = take(static_cast<uint64_t>(documents) * 4);
-  l.doc_z = take(static_cast<uint64_t>(documents) * 8);
+  l.doc_z = take(static_cast<uint64_t>(documents) * 4);
   l.ticket = take(4);
   l.total = off;
   return l;
@@ -430,9 +430,9 @@ flce_status flce_route_forward(flce_handle_t h, const flce_route_args* r, void* 
   a.unit_c = reinterpret_cast<int32_t*>(ws + L.unit_c);
   a.unit_live = reinterpret_cast<int32_t*>(ws + L.unit_live);
   a.unit_z = reinterpret_cast<float*>(ws + L.unit_z);
-  a.terms = reinterpret_cast<double*>(ws + L.terms);
+  a.terms = reinterpret_cast<float*>(ws + L.terms);
   a.doc_live = reinterpret_cast<int32_t*>(ws + L.doc_live);
-  a.doc_z = reinterpret_cast<double*>(ws + L.doc_z);
+  a.doc_z = reinterpret_cast<float*>(ws + L.doc_z);
   a.ticket = reinterpret_cast<uint32_t*>(ws + L.ticket);
   const double n = static_cast<double>(r->N), e = static_cast<double>(r->E);
   if (r->N > 0) {
