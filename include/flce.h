@@ -505,10 +505,13 @@ flce_status flce_route_backward(flce_handle_t h, const flce_route_args* args, co
  *   else            update = O, rounded once to its type
  * The products run on the tensor cores with fp16 operands (X, A and B scaled
  * by powers of two, X itself held in 22 bits, the diagonal of B in fp32) and
- * fp32 accumulators: O is within 5e-3 of its own norm of the exact result
- * whatever the spectrum (2e-4 to 2.5e-3 was seen; iterates in fp32 are about
- * 1e-4 off). That is the size of one rounding of O to bf16 (1.7e-3); where the
- * updates or weights are fp32 it is all of O's error. Momentum, norms and the
+ * fp32 accumulators. With five standard steps O is 1e-4 to 5e-3 of its own norm
+ * off the exact result, whatever the spectrum, about as much as one rounding of
+ * O to bf16 (1.7e-3), and up to 1.5e-2 where all roundings add up (rank one or
+ * two, elements of one magnitude: 1e-2). Iterates in fp32 are 1e-6 to 4e-4 off,
+ * in bf16 1e-2 to 1; an update in fp32 or an fp32 weight is no closer than O is.
+ * Each further step may raise the error as the map raises small singular values
+ * (3.4 times). Momentum, norms and the
  * weight update are fp32 (squares summed in three ranges, so that no sum over-
  * or underflows; a block's warps joined in fp64). Matrices of one call
  * share sizes and types; strides may differ. No host synchronisation;

@@ -17,12 +17,14 @@
 // lo, 22 bits together): the map multiplies small singular values by a = 3.4
 // per step, 480 times in five steps, and with them whatever rounding put into
 // those directions. B X is small there (B is), so B may meet the rounded hi;
-// a X must not. The same holds for the diagonal of B, the largest part of it:
-// it multiplies the whole X in fp32 in the epilogue, and the product runs on B
-// with a zero diagonal. In a float emulation this leaves 2e-4 to 2.5e-3
-// relative error (rank 1, rank 16, 1/i and 1/i^2 spectra, Gaussian), of the
-// order of one bf16 rounding of the result (1.7e-3); iterates rounded to bf16
-// are 1e-2 off on Gaussian matrices and 0.15 to 1 on the others.
+// a X must not. The diagonal of B, the largest part of it, multiplies X's high
+// part in fp32 in the epilogue, and of the low part what is common to 32 rows
+// (part_factors; all of B meets the same matrix), and the product runs on B
+// with a zero diagonal. So what the roundings of A, B and X's high part add
+// stays in the row and column spaces that X has, and is not raised. This leaves
+// 1e-4 to 4.3e-3 relative error (Gaussian, decaying and low-rank spectra), of the order
+// of one bf16 rounding of the result (1.7e-3); iterates rounded to bf16 are
+// 1e-2 off on Gaussian matrices and 0.15 to 1 on the others.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -516,7 +518,7 @@ struct MuonEpilogue {
   // to o0 and, a mirror image or X lo, to o1
   template <int PHASE>
   __device__ __forceinline__ bool group(const MuonStep& st, const CUtensorMap* o0, const CUtensorMap* o1, int g, int mat,
-                                        int row0, int c0, bool mirror, float factor, const uint32_t (&r)[32]) {
+                                        int row0, int c0, bool mirror, float2 factor, const uint32_t (&r)[32]) {
     constexpr bool kSym = PHASE == kMuonGram || PHASE == kMuonPoly;
     const uint32_t b = PHASE == kMuonGram ? g % BUFS : uses % BUFS;
     uint8_t* p0 = buf + b * 2 * kEpiPart;
@@ -598,8 +600,8 @@ struct MuonEpilogue {
         for (int e = 0; e < 4; ++e) {
           const float2 fh = unpack_half2(h[e]), fl = unpack_half2(l[e]);
           float* y = x + 8 * j + 2 * e;
-          y[0] = factor * (fh.x + fl.x) + acc(8 * j + 2 * e) * kPolyInv;
-          y[1] = factor * (fh.y + fl.y) + acc(8 * j + 2 * e + 1) * kPolyInv;
+          y[0] = factor.x * fh.x + (factor.y * fl.x + acc(8 * j + 2 * e) * kPolyInv);
+          y[1] = factor.x * fh.y + (factor.y * fl.y + acc(8 * j + 2 * e + 1) * kPolyInv);
           if constexpr (PHASE == kMuonApply) split_half2(y[0], y[1], h[e], l[e]);
         }
         if constexpr (PHASE == kMuonApply) {
@@ -893,15 +895,17 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
       const int block_m = w.tm * Tile::kM / kBlock, block_n = col0 / kBlock;
       const bool skip = row0 >= a.m || col0 >= ncols || (kSym && block_n < block_m);
       const int groups = skip ? 0 : min(kHalf / 32, (ncols - col0 + 31) / 32);
-      float factor = 0.f;
+      float2 factor = make_float2(0.f, 0.f);
       bool good = true;
       if (PHASE != kMuonGram && groups > 0) {
         if (lane == 0) good = wait_done(a.done + w.mat, w.needed() * kParts + a.hold, err, a.timeout_ns);
         good = __all_sync(kAll, good);
         if (good) {
           for (int g = 0; g < min(groups, kBufs); ++g) epi.load(e0, e1, w.mat, row0, col0 + g * 32);
-          if (!kSym && row0 + lane < a.m)   // (behind lane 0's wait, by the loads' barrier)
-            factor = st.a + __ldcg(a.diag + static_cast<int64_t>(w.mat) * a.m + row0 + lane);
+          if (!kSym) {   // (behind lane 0's wait, by the loads' barrier)
+            const float d = row0 + lane < a.m ? __ldcg(a.diag + static_cast<int64_t>(w.mat) * a.m + row0 + lane) : 0.f;
+            factor = part_factors(st.a, d, row0 + 32 <= a.m);
+          }
           if (PHASE == kMuonLast) epi.prefetch_weight(w.mat, row0, col0, kHalf);
         }
       }

@@ -116,6 +116,22 @@ __device__ __forceinline__ float2 pack_sum(double s) {
   return make_float2(static_cast<float>(m), __int_as_float(e));
 }
 
+// The factors of X's two parts in a X + B X, for a warp of 32 rows with B's
+// diagonal d: the high part meets all of B, the low part only a and what the
+// rows' diagonals have in common. Applied to the low part alone, without the
+// rest of B, a diagonal that varies puts rounding noise into every direction,
+// and the small ones are raised up to 3.4 times a step (rank one on 3 x 3
+// entries: 5.6e-2 off, 7e-4 without); left off the low part altogether, it costs
+// Gaussian matrices half of their accuracy (128 x 128: 1.5e-3, 1.0e-3 with what
+// is common). `whole`: the warp's rows all lie in the matrix.
+__device__ __forceinline__ float2 part_factors(float a, float d, bool whole) {
+  float least, most;
+  asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(least) : "f"(d));
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(most) : "f"(d));
+  const float common = !whole ? 0.f : least > 0.f ? least : most < 0.f ? most : 0.f;
+  return make_float2(a + d, a + common);
+}
+
 // fp16 operands: the type fields (bits 7-9 and 10-12) are 0
 __host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, uint32_t a_mn, uint32_t b_mn) {
   return (1u << 4) | (a_mn << 15) | (b_mn << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);

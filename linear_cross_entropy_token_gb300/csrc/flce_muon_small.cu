@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     }
     wait_products();
     const bool last = k == steps.count - 1;
-    const float f = ca + diag[row];
+    const float2 f = part_factors(ca, diag[row], 32 * (warp & 3) + 32 <= a.m);
     const float sc = a.scale * kXInv;
 #pragma unroll 1
     for (int g = 0; g < NCH; ++g) {   // the thread's quarter of the slab, 16 columns at a time
@@ -403,8 +403,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float2 fh = unpack_half2(h[e]), fl = unpack_half2(l[e]);
-        o[2 * e] = f * (fh.x + fl.x) + __uint_as_float(r[2 * e]) * kPolyInv;
-        o[2 * e + 1] = f * (fh.y + fl.y) + __uint_as_float(r[2 * e + 1]) * kPolyInv;
+        o[2 * e] = f.x * fh.x + (f.y * fl.x + __uint_as_float(r[2 * e]) * kPolyInv);
+        o[2 * e + 1] = f.x * fh.y + (f.y * fl.y + __uint_as_float(r[2 * e + 1]) * kPolyInv);
         split_half2(o[2 * e], o[2 * e + 1], h[e], l[e]);
       }
       if (!last) {

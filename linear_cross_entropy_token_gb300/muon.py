@@ -106,9 +106,9 @@ def muon_update(grads, momenta=None, weights=None, *, beta: float = 0.95, nester
     Gradients may share memory; a matrix that is written may share no element
     with another. No result carries a gradient.
 
-    The products round their operands to fp16: O is within 5e-3 of its own norm
-    of the exact map, one bfloat16 rounding's size, and in float32 updates and
-    weights no closer.
+    The products round their operands to fp16: O is 1e-4 to 5e-3 of its own norm
+    off the exact result (1.5e-2 at most, include/flce.h), one bfloat16
+    rounding's size, and in float32 updates and weights no closer.
 
     The call returns once its work is enqueued. A device-side wait that ran out
     (a GPU that no longer makes progress) leaves the results unspecified:
