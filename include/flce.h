@@ -508,8 +508,10 @@ flce_status flce_route_backward(flce_handle_t h, const flce_route_args* args, co
  * fp32 accumulators. With five standard steps O is 1e-4 to 5e-3 of its own norm
  * off the exact result, whatever the spectrum, about as much as one rounding of
  * O to bf16 (1.7e-3), and up to 1.5e-2 where all roundings add up (rank one or
- * two, elements of one magnitude: 1e-2). Iterates in fp32 are 1e-6 to 4e-4 off,
- * in bf16 1e-2 to 1; an update in fp32 or an fp32 weight is no closer than O is.
+ * two, elements of one magnitude: 1e-2). Where rows or cols are at most 32 the
+ * products run on both parts of X, A and B: 1e-6 to 6e-5. Iterates in fp32 are
+ * 1e-6 to 4e-4 off, in bf16 1e-2 to 1; an update in fp32 or an fp32 weight is no
+ * closer than O is.
  * Each further step may raise the error as the map raises small singular values
  * (3.4 times). Momentum, norms and the
  * weight update are fp32 (squares summed in three ranges, so that no sum over-

@@ -68,7 +68,7 @@ struct flce_handle_s {
   int num_sms = 0;
   int pair_clusters = 0;  // clusters of two the pair kernels fit at once
   int wide_clusters = 0;  // clusters of two the wide kernels fit at once
-  std::map<std::array<int, 2>, int> muon_small;  // clusters (size, chunks) that fit at once
+  std::map<std::array<int, 3>, int> muon_small;  // clusters (size, chunks, kernel) that fit at once
   int muon_shape = -1;    // tile shape of the muon products (created with FLCE_CTA_AUTO: picked by size)
   int muon_clusters = 0;  // clusters of two the muon kernels fit at once (0: not asked yet)
   // tile shape of the handle's GEMMs; an AUTO handle (cfg.cta_pair stays

@@ -475,7 +475,8 @@ __device__ __forceinline__ void write_rows(T* out, int64_t ld, int rows, int col
 // memory sees runs of 64 bytes and more, and no warp waits for another. (With
 // each thread reading and writing its own row in global memory every access
 // touched 32 lines: B X of 8 x 1024 x 1024 took 36.8 us, its products 8.7.)
-template <uint32_t BUFS>
+// BOTH: A and B are one block of 32 x 32, in two parts as X is.
+template <uint32_t BUFS, bool BOTH>
 struct MuonEpilogue {
   const MuonArgs& a;
   uint8_t* buf;        // this warp's BUFS x 2 x kEpiPart
@@ -515,7 +516,7 @@ struct MuonEpilogue {
   }
 
   // columns c0 .. c0 + 31 of the warp's rows, accumulator values in r; written
-  // to o0 and, a mirror image or X lo, to o1
+  // to o0 and, a mirror image or the low part, to o1
   template <int PHASE>
   __device__ __forceinline__ bool group(const MuonStep& st, const CUtensorMap* o0, const CUtensorMap* o1, int g, int mat,
                                         int row0, int c0, bool mirror, float2 factor, const uint32_t (&r)[32]) {
@@ -554,9 +555,16 @@ struct MuonEpilogue {
         } else {
           const uint4 w = q0[j ^ sw];
           const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+          uint4 wl = make_uint4(0, 0, 0, 0);
+          if constexpr (BOTH) wl = q1[j ^ sw];
+          const uint32_t wwl[4] = {wl.x, wl.y, wl.z, wl.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack_half2(ww[e]);
+            float2 f = unpack_half2(ww[e]);
+            if constexpr (BOTH) {
+              const float2 fl = unpack_half2(wwl[e]);
+              f.x += fl.x, f.y += fl.y;
+            }
             v[2 * e] = st.b * kPolyB * f.x + st.c * kPolyC * acc(8 * j + 2 * e);
             v[2 * e + 1] = st.b * kPolyB * f.y + st.c * kPolyC * acc(8 * j + 2 * e + 1);
           }
@@ -572,10 +580,17 @@ struct MuonEpilogue {
           }
         }
         uint32_t w[4];
+        if constexpr (BOTH) {
+          uint32_t l[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = pack_half2(v[2 * e], v[2 * e + 1]);
+          for (int e = 0; e < 4; ++e) split_half2(v[2 * e], v[2 * e + 1], w[e], l[e]);
+          q1[j ^ sw] = make_uint4(l[0], l[1], l[2], l[3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = pack_half2(v[2 * e], v[2 * e + 1]);
+        }
         q0[j ^ sw] = make_uint4(w[0], w[1], w[2], w[3]);
-        if (mirror) {
+        if (!BOTH && mirror) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) mir[(8 * j + e) * 32] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
         }
@@ -586,7 +601,10 @@ struct MuonEpilogue {
       __syncwarp();
       if (lane == 0) {
         tma_store_3d(o0, smem_u32(p0), c0, row0, mat);
-        if (mirror) tma_store_3d(o1, smem_u32(p1), row0, c0, mat);
+        if (BOTH)
+          tma_store_3d(o1, smem_u32(p1), c0, row0, mat);
+        else if (mirror)
+          tma_store_3d(o1, smem_u32(p1), row0, c0, mat);
         bulk_commit_group();
       }
       __syncwarp();
@@ -669,10 +687,16 @@ struct MuonEpilogue {
 // 256 takes 16. Large ones by the tensor cores: 4096 x 4096, five steps of 1.37
 // TFLOP together, in 1.0 ms (80 % of the library's sustained bf16 rate), 4096 x
 // 16384 in 3.07 ms (85 %).
-template <int SHAPE>
+//
+// BOTH (a short side up to kMuonPairSide): each product is three, high x high, low
+// x high and high x low parts, into one accumulator. X Xt and A A take them from
+// one loaded k-block, high part as A and low part as B (X and A are one tile high);
+// B X, which is a single k-block, loads it three times. 32 x 8192: 156 us, with one
+// product each 119 and 1e-3 more error. (Shorter matrices run in one launch.)
+template <int SHAPE, bool BOTH>
 __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bounds__(kThreads, 1)
-    muon_steps_kernel(const __grid_constant__ MuonMaps maps, const __grid_constant__ MuonArgs a,
-                      const __grid_constant__ MuonSteps steps) {
+    muon_steps_kernel(const __grid_constant__ std::conditional_t<BOTH, MuonPairMaps, MuonMaps> maps,
+                      const __grid_constant__ MuonArgs a, const __grid_constant__ MuonSteps steps) {
   using Tile = MuonTile<SHAPE>;
   constexpr bool kPaired = SHAPE != kMuonSingle, kWide = SHAPE == kMuonWide;
   constexpr int kStages = Tile::kStages, kAccs = Tile::kAccs, kBufs = Tile::kBufs;
@@ -732,7 +756,7 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
       tmem_relinquish();
     }
   }
-  if (warp == 2 && lane < static_cast<int>(sizeof(MuonMaps) / sizeof(CUtensorMap)))
+  if (warp == 2 && lane < static_cast<int>(sizeof(maps) / sizeof(CUtensorMap)))
     tma_prefetch_map(reinterpret_cast<const CUtensorMap*>(&maps) + lane);
   __syncthreads();
   if (kPaired) cluster_sync();
@@ -767,7 +791,7 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
         const int nB = w.tn * Tile::kN + static_cast<int>(rank) * 128;
         const int num_kb = w.phase == kMuonGram ? gram_blocks(w.split) : kb_m;
         const int k_first = w.phase == kMuonGram ? w.split * kb_split * kBK : 0;
-        for (int kb = 0; kb < num_kb; ++kb) {
+        for (int kb = 0, blocks = num_kb * (BOTH && !w.symmetric() ? 3 : 1); kb < blocks; ++kb) {
           const int stage = n_issued % kStages;
           const uint32_t phase = (n_issued / kStages) & 1u;
           if (!wait(empty_bar(stage), phase ^ 1u)) {
@@ -777,23 +801,30 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
           if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), (kPaired ? 2 : 1) * kStageBytes);
           const uint32_t fb = kPaired ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
           const uint32_t sa = smem_u32(smem + stage * kStageBytes);
-          const int k0 = k_first + kb * kBK;
+          const int k0 = k_first + (BOTH && !w.symmetric() ? 0 : kb) * kBK;
+          const CUtensorMap *pa = ma, *pb = mb;
+          if constexpr (BOTH) {
+            if (w.symmetric())
+              pb = w.phase == kMuonGram ? &maps.lk : &maps.glk;
+            else
+              pa = kb == 1 ? &maps.plk : ma, pb = kb == 2 ? &maps.ln : mb;
+          }
           auto load = [&](uint32_t dst, const CUtensorMap* m, int c0, int c1) {
             if (kPaired)
               tma_load_3d_pair(dst, m, fb, c0, c1, w.mat);
             else
               tma_load_3d(dst, m, fb, c0, c1, w.mat);
           };
-          load(sa, ma, k0, mA);
+          load(sa, pa, k0, mA);
 #pragma unroll
           for (int h = 0; h < (kWide ? 2 : 1); ++h) {
             const uint32_t sb = sa + (1 + h) * kPartBytes;
             const int n = nB + 256 * h;
             if (w.symmetric()) {
-              load(sb, mb, k0, n);
+              load(sb, pb, k0, n);
             } else {   // X as the right operand is contiguous along its columns
-              load(sb, mb, n, k0);
-              load(sb + 8192, mb, n + 64, k0);
+              load(sb, pb, n, k0);
+              load(sb + 8192, pb, n + 64, k0);
             }
           }
           ++n_issued;
@@ -824,8 +855,16 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
           tc_fence_after();
           const uint32_t sa = smem_u32(smem + stage * kStageBytes);
           const uint32_t sb = sa + kPartBytes;
+          if constexpr (BOTH && !BMN) {
 #pragma unroll
-          for (int k = 0; k < kBK / 16; ++k) {
+            for (int i = 0; i < 3 * (kBK / 16); ++i) {
+              const int term = i / (kBK / 16), k = i % (kBK / 16);
+              tc_mma_bf16(d_tmem, smem_desc_sw128((term == 1 ? sb : sa) + 32u * k, 16u, 1024u),
+                          smem_desc_sw128((term == 2 ? sb : sa) + 32u * k, 16u, 1024u), idesc, kb > 0 || i > 0 ? 1u : 0u);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < (BOTH && !BMN ? 0 : kBK / 16); ++k) {
             const uint32_t in = (kb > 0 || k > 0) ? 1u : 0u;
             const uint64_t ad = smem_desc_sw128(sa + 32u * k, 16u, 1024u);
             auto bdesc = [&](uint32_t at) {
@@ -857,7 +896,7 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
         if (w.symmetric())
           products(std::integral_constant<int, 0>(), w.phase == kMuonGram ? gram_blocks(w.split) : kb_m, d_tmem);
         else
-          products(std::integral_constant<int, 1>(), kb_m, d_tmem);
+          products(std::integral_constant<int, 1>(), BOTH ? 3 : kb_m, d_tmem);
         if (failed) break;
         commit(tfull_bar(acc));
       }
@@ -873,18 +912,22 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
     constexpr int kHalf = Tile::kN / 2;                     // columns of an epilogue warp
     constexpr int kBlock = SHAPE == kMuonSingle ? 128 : 256;  // the symmetric products' unit of "above the diagonal"
     const int wq = warp & 3, half = (warp - 4) >> 2;
-    MuonEpilogue<kBufs> epi{a, sE + (warp - 4) * kBufs * 2 * kEpiPart, drain_bar + 8u * (1 + kBufs * (warp - 4)), lane};
+    MuonEpilogue<kBufs, BOTH> epi{a, sE + (warp - 4) * kBufs * 2 * kEpiPart, drain_bar + 8u * (1 + kBufs * (warp - 4)), lane};
     bool ok = true;
     int it = 0;
+    const CUtensorMap *gram_lo = nullptr, *poly_lo = nullptr;
+    if constexpr (BOTH) gram_lo = &maps.gle, poly_lo = &maps.ple;
     auto unit = [&](auto phase_c) {
       constexpr int PHASE = decltype(phase_c)::value;
       constexpr bool kSym = PHASE == kMuonGram || PHASE == kMuonPoly;
       const int src = w.step & 1;
       const MuonStep st{steps.c[w.step][0], steps.c[w.step][1], steps.c[w.step][2]};
       const CUtensorMap* e0 = PHASE == kMuonPoly ? &maps.ge : &maps.xe[src];
-      const CUtensorMap* e1 = PHASE == kMuonPoly ? nullptr : &maps.lo;
+      const CUtensorMap* e1 = PHASE == kMuonPoly ? gram_lo : &maps.lo;
       const CUtensorMap* o0 = PHASE == kMuonGram ? &maps.ge : PHASE == kMuonPoly ? &maps.pe : &maps.xe[1 - src];
-      const CUtensorMap* o1 = PHASE == kMuonGram ? &maps.gm : PHASE == kMuonPoly ? &maps.pm : &maps.lo;
+      const CUtensorMap* o1 = PHASE == kMuonGram   ? (BOTH ? gram_lo : &maps.gm)
+                              : PHASE == kMuonPoly ? (BOTH ? poly_lo : &maps.pm)
+                                                   : &maps.lo;
       const int acc = it % kAccs;
       const uint32_t acc_phase = (it / kAccs) & 1;
       const int ncols = kSym ? a.m : a.n;
@@ -904,7 +947,7 @@ __global__ void __cluster_dims__(SHAPE == kMuonSingle ? 1 : 2, 1, 1) __launch_bo
           for (int g = 0; g < min(groups, kBufs); ++g) epi.load(e0, e1, w.mat, row0, col0 + g * 32);
           if (!kSym) {   // (behind lane 0's wait, by the loads' barrier)
             const float d = row0 + lane < a.m ? __ldcg(a.diag + static_cast<int64_t>(w.mat) * a.m + row0 + lane) : 0.f;
-            factor = part_factors(st.a, d, row0 + 32 <= a.m);
+            factor = BOTH ? make_float2(st.a + d, st.a + d) : part_factors(st.a, d, row0 + 32 <= a.m);
           }
           if (PHASE == kMuonLast) epi.prefetch_weight(w.mat, row0, col0, kHalf);
         }
@@ -1045,9 +1088,9 @@ cudaError_t launch_chained(void (*kern)(P...), dim3 grid, int threads, size_t sm
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int SHAPE>
-cudaError_t launch_steps(const MuonMaps& maps, const MuonArgs& a, const MuonSteps& steps, int slots, cudaStream_t s) {
-  auto kern = muon_steps_kernel<SHAPE>;
+template <int SHAPE, bool BOTH, class Maps>
+cudaError_t launch_steps(const Maps& maps, const MuonArgs& a, const MuonSteps& steps, int slots, cudaStream_t s) {
+  auto kern = muon_steps_kernel<SHAPE, BOTH>;
   // at every launch: the attribute belongs to the current device, and a process may use several
   const cudaError_t opted = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  static_cast<int>(smem_bytes<SHAPE>()));
@@ -1136,14 +1179,19 @@ cudaError_t launch_muon_prepare(const MuonArgs& a, int sms, cudaStream_t s) {
 
 cudaError_t launch_muon_steps(int shape, const MuonMaps& maps, const MuonArgs& a, const MuonSteps& steps, int slots,
                               cudaStream_t s) {
-  return shape == kMuonSingle ? launch_steps<kMuonSingle>(maps, a, steps, slots, s)
-         : shape == kMuonPair ? launch_steps<kMuonPair>(maps, a, steps, slots, s)
-                              : launch_steps<kMuonWide>(maps, a, steps, slots, s);
+  return shape == kMuonSingle ? launch_steps<kMuonSingle, false>(maps, a, steps, slots, s)
+         : shape == kMuonPair ? launch_steps<kMuonPair, false>(maps, a, steps, slots, s)
+                              : launch_steps<kMuonWide, false>(maps, a, steps, slots, s);
+}
+
+cudaError_t launch_muon_steps_pairs(const MuonPairMaps& maps, const MuonArgs& a, const MuonSteps& steps, int slots,
+                                    cudaStream_t s) {
+  return launch_steps<kMuonSingle, true>(maps, a, steps, slots, s);
 }
 
 // CTA pairs that fit on the device at once (the three shapes take an SM each)
 int muon_max_clusters() {
-  auto kern = muon_steps_kernel<kMuonPair>;
+  auto kern = muon_steps_kernel<kMuonPair, false>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);

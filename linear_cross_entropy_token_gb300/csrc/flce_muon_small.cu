@@ -22,6 +22,13 @@
 // bulk copies, took 8.6 and 7.6 us a step at 128 x 1024, this 7.0.) A A and
 // B are the same small work in every CTA. Rows past the short side are zero.
 //
+// A short side up to kMuonPairSide (BOTH) runs each product as three, high x high, low
+// x high and high x low parts, into one accumulator: A and B are one block of 32 x
+// 32 then, their low part where otherwise B is, and take 32 of 128 columns and of
+// the depth, so that this costs no more (32 x 32: 19.3 us, one product of whole
+// tiles each 19.7). Their partial products are 4 KB, which every CTA adds for itself,
+// behind one cluster barrier instead of two (32 x 1024: 28 us, 43).
+//
 // 512 threads; thread t works on row 32 (warp % 4) + lane of an accumulator,
 // and on one quarter of its columns. Every wait is bounded: one that runs out is
 // recorded, and the kernel goes on to its end (no CTA leaves a cluster barrier
@@ -77,7 +84,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 // byte offset of 16-byte chunk j (8 fp16) of row r in a [128 rows][128 bytes] tile
 __device__ __forceinline__ uint32_t tile16(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
 
-template <int NCH>
+template <int NCH, bool BOTH>
 __global__ void __launch_bounds__(kSmallThreads, 1)
     muon_small_kernel(const __grid_constant__ MuonArgs a, const __grid_constant__ MuonSteps steps) {
   constexpr int kSlab = 64 * NCH;
@@ -248,23 +255,82 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   fence_proxy_async_smem();
   __syncthreads();
 
-  const uint32_t aHi = smem_u32(sHi), aA = smem_u32(sA), aB = smem_u32(sB);
+  const uint32_t aHi = smem_u32(sHi), aLo = smem_u32(sLo), aA = smem_u32(sA), aB = smem_u32(sB);
+  // BOTH: the terms' products of `steps` 16-deep slices, `a` and `b` the operands' slices (part, slice)
+  auto terms = [&](uint32_t d, uint32_t idesc, auto count, auto&& da, auto&& db) {
+#pragma unroll 1
+    for (int term = 0; term < 3; ++term) {
+#pragma unroll
+      for (int i = 0; i < decltype(count)::value; ++i)
+        tc_mma_bf16(d, da(term == 1, i), db(term == 2, i), idesc, term > 0 || i > 0 ? 1u : 0u);
+    }
+  };
+  // BOTH: this lane's row of A or B, four values from column c on, to its place in either part
+  auto put_pair4 = [&](int c, float v0, float v1, float v2, float v3) {
+    uint2 h, l;
+    split_half2(v0, v1, h.x, l.x);
+    split_half2(v2, v3, h.y, l.y);
+    const uint32_t at = tile16(lane, c >> 3) + (c & 4) * 2;
+    *reinterpret_cast<uint2*>(sA + at) = h;
+    *reinterpret_cast<uint2*>(sB + at) = l;
+  };
 #pragma unroll 1
   for (int k = 0; k < steps.count; ++k) {
     const float ca = steps.c[k][0], cb = steps.c[k][1], cc = steps.c[k][2];
     // ---- A = X Xt
     if (threadIdx.x == 0) {
       tc_fence_after();
-      constexpr uint32_t idesc = idesc_f16_f32(128, 128, 0, 0);
+      if constexpr (BOTH) {
+        auto slice = [&](bool low, int i) {
+          return smem_desc_sw128((low ? aLo : aHi) + (i >> 2) * kChunkBytes + 32u * (i & 3), 16u, 1024u);
+        };
+        terms(tmem, idesc_f16_f32(128, kMuonPairSide, 0, 0), std::integral_constant<int, 4 * NCH>(), slice, slice);
+      } else {
+        constexpr uint32_t idesc = idesc_f16_f32(128, 128, 0, 0);
 #pragma unroll
-      for (int i = 0; i < 4 * NCH; ++i) {
-        const uint64_t d = smem_desc_sw128(aHi + (i >> 2) * kChunkBytes + 32u * (i & 3), 16u, 1024u);
-        tc_mma_bf16(tmem, d, d, idesc, i > 0 ? 1u : 0u);
+        for (int i = 0; i < 4 * NCH; ++i) {
+          const uint64_t d = smem_desc_sw128(aHi + (i >> 2) * kChunkBytes + 32u * (i & 3), 16u, 1024u);
+          tc_mma_bf16(tmem, d, d, idesc, i > 0 ? 1u : 0u);
+        }
       }
       tc_commit(bar);
     }
     wait_products();
-    if (C == 1) {
+    if constexpr (BOTH) {
+      // a step's partial products in one half of their room, the next step's in the other:
+      // a CTA writes a half again only behind a barrier that all readers have passed
+      float4* mine = partials + (k & 1) * C * 256;
+      if (warp == 0) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tmem_row, r);
+        tmem_ld_wait();
+        tmem_regs_ready(r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float v[4] = {__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]), __uint_as_float(r[4 * j + 2]),
+                              __uint_as_float(r[4 * j + 3])};
+          if (C == 1)
+            put_pair4(4 * j, v[0] * kGramScale, v[1] * kGramScale, v[2] * kGramScale, v[3] * kGramScale);
+          else
+            __stcg(mine + rank * 256 + j * 32 + lane, make_float4(v[0], v[1], v[2], v[3]));
+        }
+      }
+      tc_fence_before();
+      if (C > 1) {
+        cluster_sync();
+        if (warp < 8) {   // columns 4 warp .. of a row per lane, over the CTAs in order
+          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+          for (int src = 0; src < C; ++src) {
+            const float4 v = __ldcg(mine + src * 256 + warp * 32 + lane);
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+          }
+          put_pair4(4 * warp, s.x * kGramScale, s.y * kGramScale, s.z * kGramScale, s.w * kGramScale);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncthreads();
+    } else if (C == 1) {
       uint32_t r[32];
       __syncwarp();
       tmem_ld_32x32b_x32(tmem_row + quarter * 32, r);
@@ -325,16 +391,44 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     // ---- B = b A + c A A
     if (threadIdx.x == 0) {
       tc_fence_after();
-      constexpr uint32_t idesc = idesc_f16_f32(128, 128, 0, 0);
+      if constexpr (BOTH) {
+        auto slice = [&](bool low, int i) { return smem_desc_sw128((low ? aB : aA) + 32u * i, 16u, 1024u); };
+        terms(tmem, idesc_f16_f32(128, kMuonPairSide, 0, 0), std::integral_constant<int, kMuonPairSide / 16>(), slice, slice);
+      } else {
+        constexpr uint32_t idesc = idesc_f16_f32(128, 128, 0, 0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint64_t d = smem_desc_sw128(aA + (i >> 2) * kChunkBytes + 32u * (i & 3), 16u, 1024u);
-        tc_mma_bf16(tmem, d, d, idesc, i > 0 ? 1u : 0u);
+        for (int i = 0; i < 8; ++i) {
+          const uint64_t d = smem_desc_sw128(aA + (i >> 2) * kChunkBytes + 32u * (i & 3), 16u, 1024u);
+          tc_mma_bf16(tmem, d, d, idesc, i > 0 ? 1u : 0u);
+        }
       }
       tc_commit(bar);
     }
     wait_products();
-    {
+    if constexpr (BOTH) {
+      if (warp == 0) {   // B in A's place
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tmem_row, r);
+        tmem_ld_wait();
+        tmem_regs_ready(r);
+        float on_diag = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t at = tile16(lane, j >> 1) + (j & 1) * 8;
+          const uint2 h = *reinterpret_cast<const uint2*>(sA + at), l = *reinterpret_cast<const uint2*>(sB + at);
+          const float2 h0 = unpack_half2(h.x), h1 = unpack_half2(h.y), l0 = unpack_half2(l.x), l1 = unpack_half2(l.y);
+          float v[4] = {h0.x + l0.x, h0.y + l0.y, h1.x + l1.x, h1.y + l1.y};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = cb * kPolyB * v[e] + cc * kPolyC * __uint_as_float(r[4 * j + e]);
+            on_diag = 4 * j + e == lane ? v[e] : on_diag;   // the diagonal stays in fp32, apart
+            v[e] = 4 * j + e == lane ? 0.f : v[e];
+          }
+          put_pair4(4 * j, v[0], v[1], v[2], v[3]);
+        }
+        diag[lane] = on_diag * kPolyInv;
+      }
+    } else {
       uint32_t r[32];
       __syncwarp();
       tmem_ld_32x32b_x32(tmem_row + quarter * 32, r);
@@ -373,20 +467,28 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     if (threadIdx.x == 0) {
       tc_fence_after();
       constexpr uint32_t idesc = idesc_f16_f32(128, kSlab, 0, 1);
+      if constexpr (BOTH) {
+        terms(tmem + 128, idesc, std::integral_constant<int, kMuonPairSide / 16>(),
+              [&](bool low, int i) { return smem_desc_sw128((low ? aB : aA) + 32u * i, 16u, 1024u); },
+              [&](bool low, int i) { return smem_desc_sw128((low ? aLo : aHi) + 2048u * i, kChunkBytes, 1024u); });
+      } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint64_t da = smem_desc_sw128(aB + (i >> 2) * kChunkBytes + 32u * (i & 3), 16u, 1024u);
-        const uint64_t db = smem_desc_sw128(aHi + 2048u * i, kChunkBytes, 1024u);
-        tc_mma_bf16(tmem + 128, da, db, idesc, i > 0 ? 1u : 0u);
+        for (int i = 0; i < 8; ++i) {
+          const uint64_t da = smem_desc_sw128(aB + (i >> 2) * kChunkBytes + 32u * (i & 3), 16u, 1024u);
+          const uint64_t db = smem_desc_sw128(aHi + 2048u * i, kChunkBytes, 1024u);
+          tc_mma_bf16(tmem + 128, da, db, idesc, i > 0 ? 1u : 0u);
+        }
       }
       tc_commit(bar);
     }
     wait_products();
     const bool last = k == steps.count - 1;
-    const float2 f = part_factors(ca, diag[row], 32 * (warp & 3) + 32 <= a.m);
+    const float2 f = BOTH ? make_float2(ca + diag[lane], ca + diag[lane])
+                          : part_factors(ca, diag[row], 32 * (warp & 3) + 32 <= a.m);
     const float sc = a.scale * kXInv;
 #pragma unroll 1
     for (int g = 0; g < NCH; ++g) {   // the thread's quarter of the slab, 16 columns at a time
+      if (BOTH && (warp & 3) != 0) break;   // (rows past the matrix)
       const int col = (quarter * NCH + g) * 16;
       uint32_t r[16];
       __syncwarp();
@@ -470,10 +572,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   }
 }
 
-template <int NCH>
+template <int NCH, bool BOTH>
 cudaError_t launch_small_t(const MuonArgs& a, const MuonSteps& steps, cudaStream_t s, int* fits) {
   constexpr size_t smem = 1024 + 2 * NCH * kChunkBytes + 2 * kPanelBytes;   // X, A, B
-  auto kern = muon_small_kernel<NCH>;
+  auto kern = muon_small_kernel<NCH, BOTH>;
   // at every launch: the attributes belong to the current device, and a process may use several
   cudaError_t opted = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (opted == cudaSuccess && a.cluster > 8)
@@ -495,12 +597,13 @@ cudaError_t launch_small_t(const MuonArgs& a, const MuonSteps& steps, cudaStream
   return cudaLaunchKernelEx(&cfg, kern, a, steps);
 }
 
+template <bool BOTH>
 cudaError_t launch_small(const MuonArgs& a, const MuonSteps& steps, int chunks, cudaStream_t s, int* fits) {
   switch (chunks) {
-    case 1: return launch_small_t<1>(a, steps, s, fits);
-    case 2: return launch_small_t<2>(a, steps, s, fits);
-    case 3: return launch_small_t<3>(a, steps, s, fits);
-    default: return launch_small_t<4>(a, steps, s, fits);
+    case 1: return launch_small_t<1, BOTH>(a, steps, s, fits);
+    case 2: return launch_small_t<2, BOTH>(a, steps, s, fits);
+    case 3: return launch_small_t<3, BOTH>(a, steps, s, fits);
+    default: return launch_small_t<4, BOTH>(a, steps, s, fits);
   }
 }
 
@@ -516,16 +619,18 @@ int muon_small_cluster(int64_t m, int64_t n) {
 int muon_small_chunks(int64_t n, int cluster) { return static_cast<int>(((n + cluster - 1) / cluster + 63) / 64); }
 
 cudaError_t launch_muon_small(const MuonArgs& a, const MuonSteps& steps, int chunks, cudaStream_t s) {
-  return launch_small(a, steps, chunks, s, nullptr);
+  return a.m <= kMuonPairSide ? launch_small<true>(a, steps, chunks, s, nullptr)
+                              : launch_small<false>(a, steps, chunks, s, nullptr);
 }
 
 // Clusters of this size that fit the device at once
-int muon_small_clusters(int cluster, int chunks) {
+int muon_small_clusters(int cluster, int chunks, bool pairs) {
   MuonArgs a{};
   a.cluster = cluster;
   a.count = 1;
   int n = 0;
-  if (launch_small(a, MuonSteps{}, chunks, nullptr, &n) != cudaSuccess) {
+  if ((pairs ? launch_small<true>(a, MuonSteps{}, chunks, nullptr, &n)
+             : launch_small<false>(a, MuonSteps{}, chunks, nullptr, &n)) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }

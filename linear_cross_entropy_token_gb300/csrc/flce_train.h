@@ -68,6 +68,12 @@ cudaError_t launch_route_backward(int dtype, const RouteGeometry& g, const Route
 
 constexpr int kMuonMaxMats = 32;     // matrices of one launch
 constexpr int kMuonNormBlocks = 1024; // partial sums of squares per matrix
+// Short sides up to this run their products on both parts of X, A and B: what
+// the roundings to fp16 leave falls with the rows over which it spreads, and on few
+// rows comes to 1.2e-3 to 3.4e-3 of O (8 x 8 to 32 x 32; with both parts 1e-6). A
+// warp's 32 rows, which are then A and B whole; with 128, 128 x 128 took 37 us
+// instead of 25 for an error of 1e-3.
+constexpr int kMuonPairSide = 32;
 
 struct MuonMat {
   const void* grad;
@@ -105,6 +111,8 @@ struct MuonArgs {
   uint16_t* lo;                      // [count][m][ldx] fp16 remainder of X
   uint16_t* gram;                    // [count][m][lda] fp16, A scaled by 2^12
   uint16_t* poly;                    // [count][m][lda] fp16, B scaled by 2^11, zero diagonal
+  uint16_t* gram_lo;                 // [count][m][lda] fp16 remainders of A and B (short sides up to kMuonPairSide)
+  uint16_t* poly_lo;
   int64_t ldx, lda;
   uint64_t timeout_ns;
   uint32_t hold;                     // finished parts waited for beyond those there are: 0, but where waits are to run out
@@ -132,6 +140,11 @@ struct MuonStep {
 struct MuonMaps {
   CUtensorMap xk[2], xn[2], xe[2], lo, gk, ge, gm, pk, pe, pm;
 };
+// and, where the products run on both parts, X lo as either operand, and the
+// remainders of A and B as operand and as block
+struct MuonPairMaps : MuonMaps {
+  CUtensorMap lk, ln, glk, gle, plk, ple;
+};
 
 cudaError_t launch_muon_momentum(const MuonArgs& a, cudaStream_t s);
 cudaError_t launch_muon_prepare(const MuonArgs& a, int sms, cudaStream_t s);
@@ -139,6 +152,9 @@ cudaError_t launch_muon_prepare(const MuonArgs& a, int sms, cudaStream_t s);
 // for single tiles); muon_plan picks it and a.splits.
 cudaError_t launch_muon_steps(int shape, const MuonMaps& maps, const MuonArgs& a, const MuonSteps& steps, int slots,
                               cudaStream_t s);
+// on single tiles, for short sides up to kMuonPairSide
+cudaError_t launch_muon_steps_pairs(const MuonPairMaps& maps, const MuonArgs& a, const MuonSteps& steps, int slots,
+                                    cudaStream_t s);
 constexpr int kMuonMaxSplits = 8, kMuonMinSplitBlocks = 8;   // and the k-blocks of a split at least
 struct MuonPlan {
   int shape = -1, splits = 1;
@@ -148,10 +164,11 @@ int muon_max_clusters();
 
 // flce_muon_small.cu: matrices whose short side is at most 128, one launch
 // (long side at most 4096). The least CTAs per matrix (0: not such a shape),
-// 64-column chunks of a CTA's slab, clusters that fit the device at once.
+// 64-column chunks of a CTA's slab, clusters that fit the device at once
+// (pairs: of the kernel for short sides up to kMuonPairSide).
 int muon_small_cluster(int64_t m, int64_t n);
 int muon_small_chunks(int64_t n, int cluster);
-int muon_small_clusters(int cluster, int chunks);
+int muon_small_clusters(int cluster, int chunks, bool pairs);
 cudaError_t launch_muon_small(const MuonArgs& a, const MuonSteps& steps, int chunks, cudaStream_t s);
 
 }  // namespace flce

@@ -96,7 +96,8 @@ constexpr uint64_t kMuonGroupBytes = 2ull << 30;
 constexpr uint64_t kMuonSumsBytes = 40ull << 20;
 
 struct MuonLayout {
-  uint64_t ctrl = 0, done = 0, sums = 0, sums_bytes = 0, norm = 0, diag = 0, hi[2] = {0, 0}, lo = 0, gram = 0, poly = 0, total = 0;
+  uint64_t ctrl = 0, done = 0, sums = 0, sums_bytes = 0, norm = 0, diag = 0, hi[2] = {0, 0}, lo = 0, gram = 0, poly = 0, gram_lo = 0,
+           poly_lo = 0, total = 0;
 };
 
 struct MuonSizes {
@@ -132,6 +133,10 @@ MuonLayout muon_layout(int64_t rows, int64_t cols, int64_t count) {
   l.lo = take(x);
   l.gram = take(g);
   l.poly = take(g);
+  if (z.m <= kMuonPairSide) {
+    l.gram_lo = take(g);
+    l.poly_lo = take(g);
+  }
   // Splits of X Xt: their tiles' fp32 sums, at most a tile for every slot of
   // the GPU (bounded here without knowing it)
   const int64_t blocks = cdiv(z.n, 64);
@@ -140,8 +145,8 @@ MuonLayout muon_layout(int64_t rows, int64_t cols, int64_t count) {
     const uint64_t area = align_up(z.m, 256) * align_up(z.m, 512);
     l.sums_bytes = std::min<uint64_t>(4 * area * count * (splits - 1), kMuonSumsBytes);
   }
-  // or, in the one-launch kernel, a cluster's partial products of X Xt and A
-  // (16 CTAs at most: the device is not known here)
+  // or, in the one-launch kernel, a cluster's partial products of X Xt and A (16
+  // CTAs at most: the device is not known here)
   if (muon_small_cluster(z.m, z.n) > 1)
     l.sums_bytes = std::max<uint64_t>(l.sums_bytes, static_cast<uint64_t>(count) * (16 * 65536 + 32768));
   l.sums = take(l.sums_bytes);
@@ -254,6 +259,9 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
   a.lo = reinterpret_cast<uint16_t*>(ws + L.lo);
   a.gram = reinterpret_cast<uint16_t*>(ws + L.gram);
   a.poly = reinterpret_cast<uint16_t*>(ws + L.poly);
+  const bool both = z.m <= kMuonPairSide;
+  a.gram_lo = both ? reinterpret_cast<uint16_t*>(ws + L.gram_lo) : nullptr;
+  a.poly_lo = both ? reinterpret_cast<uint16_t*>(ws + L.poly_lo) : nullptr;
   a.ldx = z.ldx;
   a.lda = z.lda;
   a.timeout_ns = timeout_ns;
@@ -274,10 +282,10 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
   int cluster = h->muon_shape < 0 ? muon_small_cluster(z.m, z.n) : 0;
   if (cluster > 0) {
     auto at_once = [&](int c) {
-      const std::array<int, 2> key{c, muon_small_chunks(z.n, c)};
+      const std::array<int, 3> key{c, muon_small_chunks(z.n, c), both};
       const auto known = h->muon_small.find(key);
       if (known != h->muon_small.end()) return known->second;
-      return h->muon_small.emplace(key, muon_small_clusters(c, key[1])).first->second;
+      return h->muon_small.emplace(key, muon_small_clusters(c, key[1], both)).first->second;
     };
     while (cluster > 1 && cluster < 16 && cluster * 64 < z.n && count <= at_once(2 * cluster)) cluster *= 2;
     if (at_once(cluster) > 0) {
@@ -288,7 +296,7 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
     }
   }
 
-  MuonMaps maps;
+  MuonPairMaps maps;
   std::string why;
   bool ok = true;
   auto operand = [&](CUtensorMap* m, const void* base, uint64_t cols, uint64_t ld, uint32_t box_rows) {
@@ -309,17 +317,26 @@ flce_status muon_group_run(flce_handle_t h, const flce_muon_args* q, const flce_
   operand(&maps.pk, a.poly, z.m, z.lda, 128);
   block(&maps.pe, a.poly, z.m, z.lda, CU_TENSOR_MAP_SWIZZLE_64B);
   block(&maps.pm, a.poly, z.m, z.lda, CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (both) {
+    operand(&maps.lk, a.lo, z.n, z.ldx, 128);
+    operand(&maps.ln, a.lo, z.n, z.ldx, 64);
+    operand(&maps.glk, a.gram_lo, z.m, z.lda, 128);
+    block(&maps.gle, a.gram_lo, z.m, z.lda, CU_TENSOR_MAP_SWIZZLE_64B);
+    operand(&maps.plk, a.poly_lo, z.m, z.lda, 128);
+    block(&maps.ple, a.poly_lo, z.m, z.lda, CU_TENSOR_MAP_SWIZZLE_64B);
+  }
   if (!ok) return fail(h, FLCE_ERR_CUDA, "%s", why.c_str());
 
   FLCE_LAUNCH(FLCE_K_MUON_MOMENTUM, 0.0, el * (gb + mb), launch_muon_momentum(a, s));
   FLCE_LAUNCH(FLCE_K_MUON_PREPARE, 0.0, el * ((mats[0].momentum ? 4.0 + (q->nesterov ? gb : 0.0) : gb) + 4.0),
               launch_muon_prepare(a, h->num_sms, s));
-  // on the handle's tile shape where it was given one
-  const MuonPlan plan = muon_plan(a, h->muon_shape, h->muon_clusters, h->num_sms);
+  // on the handle's tile shape where it was given one, but for the products on both parts
+  const MuonPlan plan = muon_plan(a, both ? kMuonSingle : h->muon_shape, h->muon_clusters, h->num_sms);
   a.splits = plan.splits;
   FLCE_LAUNCH(FLCE_K_MUON_STEPS, flops, q->steps * count * (12.0 * dm * dn + 6.0 * dm * dm),
-              launch_muon_steps(plan.shape, maps, a, steps,
-                                plan.shape == kMuonSingle ? h->num_sms : h->muon_clusters, s));
+              both ? launch_muon_steps_pairs(maps, a, steps, h->num_sms, s)
+                   : launch_muon_steps(plan.shape, maps, a, steps,
+                                       plan.shape == kMuonSingle ? h->num_sms : h->muon_clusters, s));
   return FLCE_OK;
 }
 

@@ -108,13 +108,19 @@ int main() {
     MuonSteps steps{};
     steps.count = 1;
     for (int shape = 0; shape < 3; ++shape) expect(launch_muon_steps(shape, maps, a, steps, 4, nullptr), "muon_steps shape", shape);
+    static MuonPairMaps pair_maps;
+    expect(launch_muon_steps_pairs(pair_maps, a, steps, 4, nullptr), "muon_steps_pairs", 0);
     expect(launch_muon_momentum(a, nullptr), "muon_momentum", 0);
     expect(launch_muon_prepare(a, 152, nullptr), "muon_prepare", 0);
     if (muon_max_clusters() <= 0) expect(cudaErrorUnknown, "muon_max_clusters", 0);
     for (int chunks = 1; chunks <= 4; ++chunks) {
       a.cluster = 16;
-      expect(launch_muon_small(a, steps, chunks, nullptr), "muon_small chunks", chunks);
-      if (muon_small_clusters(16, chunks) <= 0) expect(cudaErrorUnknown, "muon_small_clusters", chunks);
+      for (int side : {20, 100}) {   // the products on both parts, and on the high ones
+        a.m = side;
+        expect(launch_muon_small(a, steps, chunks, nullptr), "muon_small chunks", chunks);
+      }
+      for (bool pairs : {false, true})
+        if (muon_small_clusters(16, chunks, pairs) <= 0) expect(cudaErrorUnknown, "muon_small_clusters", chunks);
     }
     for (int E : {8, 40, 128, 256, 512, 1024})
       for (int64_t N : {100, 100000})

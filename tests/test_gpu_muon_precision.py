@@ -14,6 +14,11 @@ pytestmark = pytest.mark.gpu
 # singular values settle), as long as none of it goes into the small directions
 COHERENT = 15 * 2.0 ** -11 * 2
 
+# Up to this short side the products run on both fp16 parts of X, A and B: 22
+# bits, five steps of three roundings, and the most that the map can raise them by
+PAIR_SIDE = 32
+PAIRS = 15 * 2.0 ** -22 * 485
+
 
 def low_rank(m, n, rank, rows, cols, seed, kind="gaussian"):
     g = torch.Generator().manual_seed(seed)
@@ -60,7 +65,36 @@ def test_small_matrices(m, n):
     for seed in range(5):
         for rank in sorted({1, min(2, m, n), min(m, n)}):
             G = low_rank(m, n, rank, m, n, seed)
-            assert rel(orthogonalize(G.cuda(), dtype=torch.float32), newton_schulz(G)) <= COHERENT
+            limit = PAIRS if min(m, n) <= PAIR_SIDE else COHERENT
+            for g in (G, G.t().contiguous()):
+                assert rel(orthogonalize(g.cuda(), dtype=torch.float32), newton_schulz(g)) <= limit
+
+
+@pytest.mark.parametrize("cta", ["auto", "single", "pair", "wide"])
+@pytest.mark.parametrize("m,n,count", [(2, 9, 3), (8, 8, 1), (17, 400, 3), (32, 32, 2), (32, 1500, 1), (31, 9000, 2), (12, 4096, 40)])
+def test_a_side_up_to_32_is_more_exact(m, n, count, cta):
+    """On each kernel, with momentum and fp32 weights, repeated bit for bit."""
+    from linear_cross_entropy_token_gb300 import FLCE, muon_update
+    h = FLCE("bf16", 0, cta=cta)
+    try:
+        g = torch.Generator().manual_seed(m + n)
+        G = [torch.randn(m, n, generator=g) * torch.exp(torch.randn(m, 1, generator=g)) for _ in range(count)]
+        M = [torch.randn(m, n, generator=g) for _ in range(count)]
+        for transposed in (False, True):
+            flip = (lambda t: t.t().contiguous()) if transposed else (lambda t: t)
+            first = None
+            for _ in range(3):
+                got = muon_update([flip(t).cuda() for t in G], [flip(t).cuda() for t in M], beta=0.9,
+                                  update_dtype=torch.float32, handle=h)
+                first = first or got
+                assert all(torch.equal(a, b) for a, b in zip(got, first))
+            for a, gi, mi in zip(first, G, M):
+                gi, mi = gi.double(), mi.double()
+                want = newton_schulz(0.9 * (0.9 * mi + 0.1 * gi) + 0.1 * gi)
+                # (and the momentum's two roundings, raised as any difference is)
+                assert rel(flip(a) if transposed else a, want) <= PAIRS + 2 * 2.0 ** -24 * 485
+    finally:
+        h.close()
 
 
 @pytest.mark.parametrize("m,n", [(33, 47), (64, 64), (128, 128), (333, 1000), (512, 512), (1024, 700)])
