@@ -74,6 +74,7 @@ constexpr int kMuonNormBlocks = 1024; // partial sums of squares per matrix
 // warp's 32 rows, which are then A and B whole; with 128, 128 x 128 took 37 us
 // instead of 25 for an error of 1e-3.
 constexpr int kMuonPairSide = 32;
+static_assert(kMuonPairSide == 32, "A and B are one warp's block");
 
 struct MuonMat {
   const void* grad;
