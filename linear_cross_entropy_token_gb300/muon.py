@@ -121,7 +121,8 @@ def muon_update(grads, momenta=None, weights=None, *, beta: float = 0.95, nester
 
 def _marshal(grads, momenta, weights, beta, nesterov, steps, coefficients, eps, scale, lr, weight_decay, updates=None,
              update_dtype=torch.bfloat16, handle=None):
-    """The checks of one call, and its library arguments: what _update takes."""
+    """The checks of one call, and its library arguments: what _update takes,
+    the tensors that must live until it has launched among it."""
     grads = list(grads)
     momenta = None if momenta is None else list(momenta)
     weights = None if weights is None else list(weights)
@@ -129,7 +130,7 @@ def _marshal(grads, momenta, weights, beta, nesterov, steps, coefficients, eps, 
         raise ValueError("weights are updated in place: no updates are written")
     table = _coefficients(coefficients, steps)
     if not grads:
-        return None, None, (), None, [] if weights is None else weights, ()
+        return None, None, (), grads, [] if weights is None else weights, ()
     if updates is None and weights is None:
         if update_dtype not in DTYPES:
             raise ValueError("updates must be bfloat16 or float32")
@@ -153,12 +154,13 @@ def _marshal(grads, momenta, weights, beta, nesterov, steps, coefficients, eps, 
             m.update, m.ld_update = updates[i].data_ptr(), _row_stride(updates[i])
     # written behind autograd's back: a backward that saved one of these must fail
     written = [*(momenta or ()), *(weights or ()), *(updates or ())]
-    return h, a, mats, grads[0].device, updates if weights is None else weights, written
+    return h, a, mats, grads, updates if weights is None else weights, written
 
 
-def _update(h, a, mats, dev, result, written):
+def _update(h, a, mats, grads, result, written):
     if not mats:
         return result
+    dev = grads[0].device
     nbytes = h.lib.flce_muon_workspace_bytes(a.rows, a.cols, len(mats))
     # torch's allocations are 512-byte aligned, the workspace 1024
     ws = torch.empty(nbytes + 1024, dtype=torch.uint8, device=dev)

@@ -40,6 +40,21 @@ def test_a_refused_step_changes_nothing(case):
     _untouched(ps, before, opt)
 
 
+def test_tensors_that_only_the_call_holds():
+    """An iterator's temporaries live until the launch: their memory, which would hold the workspace, is not
+    taken for it (80 matrices go through it in three groups, so later ones would be overwritten)."""
+    from linear_cross_entropy_token_gb300 import muon_update
+    from linear_cross_entropy_token_gb300.muon import workspace_bytes
+    rows, cols, count = 160, 256, 80
+    g = torch.randn(count, rows, cols, device="cuda")
+    assert workspace_bytes(rows, cols, count) + 1024 < g.numel() * 4
+    want = muon_update(list((g * 3).unbind(0)))
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    got = muon_update(t for t in (g * 3).unbind(0))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_a_step_after_a_refused_one():
     from linear_cross_entropy_token_gb300 import Muon
     ps, qs = _parameters(), _parameters()
