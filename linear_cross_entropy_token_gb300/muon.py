@@ -249,7 +249,8 @@ class Muon(torch.optim.Optimizer):
             for i, p in zip(ids, params):
                 momentum = given["state"].get(i, {}).get("momentum")
                 if momentum is not None:
-                    self.state[p]["momentum"] = momentum.to(dtype=torch.float32, device=p.device)
+                    # a copy: momenta are updated in place, the saved ones may be another optimizer's
+                    self.state[p]["momentum"] = momentum.to(dtype=torch.float32, device=p.device, copy=True)
 
         hooks = (self.register_load_state_dict_pre_hook(note),
                  self.register_load_state_dict_post_hook(restore, prepend=True))

@@ -35,6 +35,8 @@ def test_a_checkpoint_keeps_the_momenta_bit_for_bit(through):
     for p, q in zip(ps, qs):
         got = new.state[q]["momentum"]
         assert got.dtype == torch.float32 and torch.equal(got, opt.state[p]["momentum"])
+        # updated in place from here on, and not the one that was saved
+        assert got.data_ptr() != opt.state[p]["momentum"].data_ptr()
     assert new.param_groups[0]["lr"] == 0.1
 
 
