@@ -205,7 +205,13 @@ enum {
     FLCE_K_MUON_STEPS = 20,      /* all products (A = X Xt, B = b A + c A^2, a X + B X)
                                     on tcgen05, and the update or weight              */
     FLCE_K_MUON_SMALL = 21,      /* the whole update of matrices with a side up to 128  */
-    FLCE_K_NUM_KINDS = 22
+    FLCE_K_SCORE_STATS = 22,     /* x·Wᵀ with the statistics of softmax and entropy     */
+    FLCE_K_SCORE_GRADIENT = 23,  /* x·Wᵀ with the gradient of the logits as epilogue    */
+    FLCE_K_SCORE_ROWS = 24,      /* log probabilities, entropy and alternatives per row */
+    FLCE_K_SCORE_DLOGITS = 25,   /* gradient of the logits from kept ones               */
+    FLCE_K_SCORE_OTHER = 26,     /* row constants, masked copies, casts, reports        */
+    FLCE_K_DISTILL_ROWS = 27,    /* distillation's losses and gradient rows             */
+    FLCE_K_NUM_KINDS = 28
 };
 
 typedef struct flce_kernel_profile {
@@ -299,8 +305,8 @@ flce_status flce_forward_backward_async(flce_handle_t h, const void* x, const vo
                                         void* stream);
 
 /* Waits for `stream` and returns the first device-side error that
- * flce_forward_backward_async, flce_forward_backward_shard and flce_muon_update
- * calls recorded since the last flce_async_status
+ * flce_forward_backward_async, flce_forward_backward_shard, flce_muon_update,
+ * flce_logprobs_* and flce_distill calls recorded since the last flce_async_status
  * (FLCE_OK if none), then clears it. It reads the workspace the handle holds
  * now: an error recorded before the workspace was replaced is lost. */
 flce_status flce_async_status(flce_handle_t h, void* stream);
@@ -556,6 +562,113 @@ uint64_t flce_muon_workspace_bytes(int64_t rows, int64_t cols, int64_t count);
  * next one runs). */
 flce_status flce_muon_update(flce_handle_t h, const flce_muon_args* args, const flce_muon_matrix* mats,
                              int32_t count, void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* ---- log probabilities of given tokens, with entropy and alternatives ------
+ * The head's operator for scoring, and for training on log probabilities
+ * (policy gradients), where each token has a weight of its own. Per token of
+ * z = x·Wᵀ / temperature (N x V, never held unless asked to):
+ *   logprob = z_t - lse,  lse = log sum exp z;   entropy = -sum p log p
+ *   the `top` largest z (ties to the lowest id): their ids and z - lse
+ * Products and sums over the vocabulary are fp32 (bf16 handles: of bf16 x and
+ * W on the tensor cores); the logits of the given token and of the
+ * alternatives are summed again in at least twice the bits of fp32, so their
+ * order does not depend on the sizes of a call. (Only where more than 128
+ * logits lie as near to the border as their fp32 sums can tell is the choice
+ * theirs.) A token whose t is ignore_index gets zeros, ids -1 and no gradient,
+ * whatever its row of x holds; a t out of [0, V) gets NaN, and
+ * flce_async_status reports BAD_TARGET. A NaN or infinite logit makes its
+ * row's results NaN (the ids stay in [0, V)). Results repeat bit for bit. No
+ * host synchronisation; capturable. */
+#define FLCE_SCORE_MAX_TOP 64
+typedef struct flce_logprobs_args {
+    const void* x;               /* device, N x H, the handle's dtype                  */
+    const void* W;               /* device, V x H                                      */
+    const int64_t* t;            /* device, N; NULL (forward only): no given tokens    */
+    int64_t N, H, V;
+    int64_t ignore_index;
+    double temperature;          /* > 0                                                */
+    int32_t top;                 /* 0 .. min(V, FLCE_SCORE_MAX_TOP)                    */
+    int32_t reserved;            /* 0                                                  */
+    float* logprobs;             /* device, N (with t)                                 */
+    float* entropy;              /* device, N                                          */
+    float* stats;                /* device, N x 2, 8-byte aligned: largest x·Wᵀ of the row,
+                                    log of the sum of exp(z - largest / temperature)   */
+    float* top_logprobs;         /* device, N x top                                    */
+    int64_t* top_ids;            /* device, N x top                                    */
+    void* kept;                  /* device, flce_logprobs_kept_bytes(), 256-byte aligned,
+                                    or NULL: what spares the backward its product      */
+} flce_logprobs_args;
+
+/* Bytes of `kept` for N tokens on handle h: N x V logits in fp16 relative to
+ * their 64 columns' largest, and those (fp32 handles: fp32 logits). 0: bad
+ * argument. Host only. */
+uint64_t flce_logprobs_kept_bytes(flce_handle_t h, int64_t N, int64_t V);
+
+/* Workspace bytes of the forward (backward 0) or the backward (1; dw_dtype as
+ * there, -1: no dW) with these sizes, top and kept. Chunks of tokens are
+ * planned for the handle's HBM budget, as for the loss, but for what does not
+ * shrink with them. 0: bad argument. Host only. */
+uint64_t flce_logprobs_workspace_bytes(flce_handle_t h, const flce_logprobs_args* args, int32_t backward,
+                                       int32_t dw_dtype);
+
+/* Fills logprobs, entropy, stats, top_logprobs, top_ids and kept. The workspace
+ * (device, 256-byte aligned) is the caller's and free again when the call's
+ * work is done. Layout rules as flce_forward_backward.
+ * Errors: INVALID_ARG, UNSUPPORTED, BUDGET (workspace), CUDA. */
+flce_status flce_logprobs_forward(flce_handle_t h, const flce_logprobs_args* args, void* workspace,
+                                  uint64_t workspace_bytes, void* stream);
+
+/* dx (N x H, the handle's dtype) and dW (V x H, dw_dtype: FLCE_DTYPE_FP32, or
+ * BF16 on a bf16 handle) from the gradients of logprobs and entropy (N fp32
+ * each, or NULL). Either output may be NULL, and its product is not run. args
+ * are those of the forward with stats, entropy (read where d_entropy is given)
+ * and kept unchanged; without kept the logits are computed again.
+ *   d z_j = (1 / temperature) (d_logprob (1(j = t) - p_j)
+ *                              - d_entropy p_j (log p_j + entropy))
+ * rounded to bf16 on a bf16 handle (the target's entry in full for dx), sums
+ * in fp32. The alternatives carry no gradient.
+ * Errors: INVALID_ARG, UNSUPPORTED, BUDGET (workspace), CUDA; flce_async_status. */
+flce_status flce_logprobs_backward(flce_handle_t h, const flce_logprobs_args* args, const float* d_logprobs,
+                                   const float* d_entropy, void* dx, void* dW, int32_t dw_dtype, void* workspace,
+                                   uint64_t workspace_bytes, void* stream);
+
+/* ---- distillation from a teacher's top logits -------------------------------
+ * Per token K entries of a teacher, ids and logits. An entry counts unless its
+ * id is -1 or its logit -inf; a token counts if an entry does. With q the
+ * softmax of a token's teacher logits / temperature over its entries, p that of
+ * z = x·Wᵀ / temperature over the vocabulary, n the tokens that count:
+ *   loss = (temperature^2 / n) sum over tokens and entries of q (log q - log p_id)
+ *   d (x·Wᵀ)_j = (temperature / n) (p_j - sum of q over entries with id j)
+ * 0 if n = 0. Entries may share an id. An id out of [0, V) makes the loss NaN,
+ * and flce_async_status reports BAD_TARGET; so does a NaN or +inf teacher
+ * logit, without a report. Rows of x that do not count may hold anything.
+ * Precision as for flce_logprobs_forward. Results repeat bit for bit. No host
+ * synchronisation; capturable. */
+#define FLCE_DISTILL_MAX_K 256
+typedef struct flce_distill_args {
+    const void* x;               /* device, N x H, the handle's dtype                  */
+    const void* W;               /* device, V x H                                      */
+    const int64_t* ids;          /* device, N rows of K                                */
+    const void* logits;          /* device, N rows of K, logits_dtype                  */
+    int64_t N, H, V, K;          /* 1 <= K <= FLCE_DISTILL_MAX_K                       */
+    int64_t ld_ids, ld_logits;   /* row strides, in elements, >= K                     */
+    int32_t logits_dtype;        /* FLCE_DTYPE_*                                       */
+    int32_t dw_dtype;            /* FLCE_DTYPE_FP32, or BF16 on a bf16 handle          */
+    double temperature;          /* > 0                                                */
+    float* loss;                 /* device, one fp32                                   */
+    float* token_loss;           /* device, N: each token's loss before the mean       */
+    void* dx;                    /* device, N x H, or NULL                             */
+    void* dW;                    /* device, V x H, or NULL                             */
+} flce_distill_args;
+
+/* Workspace bytes of flce_distill (0: bad argument). Host only. */
+uint64_t flce_distill_workspace_bytes(flce_handle_t h, const flce_distill_args* args);
+
+/* The loss, and the gradients whose pointers are given. The workspace (device,
+ * 256-byte aligned) is the caller's.
+ * Errors: INVALID_ARG, UNSUPPORTED, BUDGET (workspace), CUDA; flce_async_status. */
+flce_status flce_distill(flce_handle_t h, const flce_distill_args* args, void* workspace, uint64_t workspace_bytes,
+                         void* stream);
 
 /* ---- checks of single parts (used by the tests) ------------------------- */
 

@@ -15,7 +15,7 @@ from __future__ import annotations
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import routing
+from . import routing, scoring
 from .flce import FLCE, _caches
 
 _handles = {}
@@ -142,3 +142,75 @@ def route(logits: torch.Tensor, k: int, valid=None, offsets=None, renormalize: b
     the two losses; the experts and their counts carry none. Neither direction
     synchronises the host."""
     return RouteFunction.apply(logits, k, valid, offsets, renormalize, handle)
+
+
+class TokenLogprobsFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, W, t, temperature, top, ignore_index, keep_logits, handle):
+        x, W, t = x.contiguous(), W.contiguous(), t.contiguous()
+        keep = keep_logits and (ctx.needs_input_grad[0] or ctx.needs_input_grad[1])
+        r = scoring.token_logprobs(x, W, t, temperature=temperature, top=top, ignore_index=ignore_index,
+                                   keep_logits=keep, handle=handle)
+        ctx.handle, ctx.temperature, ctx.ignore_index = handle, r.temperature, ignore_index
+        ctx.save_for_backward(x, W, t, r.logprobs, r.entropy, r.stats, r.kept)
+        ctx.set_materialize_grads(False)
+        if top:
+            ctx.mark_non_differentiable(r.top_logprobs, r.top_ids)
+        return r.logprobs, r.entropy, r.top_logprobs, r.top_ids
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_logprobs, d_entropy, _d_top_logprobs, _d_top_ids):
+        none = (None,) * 6
+        if d_logprobs is None and d_entropy is None:
+            return (None, None) + none
+        r = scoring.TokenLogprobs()
+        x, W, t, r.logprobs, r.entropy, r.stats, r.kept = ctx.saved_tensors
+        r.top_logprobs = r.top_ids = None
+        r.temperature, r.ignore_index = ctx.temperature, ctx.ignore_index
+        need_x, need_W = ctx.needs_input_grad[:2]
+        if d_logprobs is not None:
+            d_logprobs = d_logprobs.contiguous()
+        if d_entropy is not None:
+            d_entropy = d_entropy.contiguous()
+        dx, dW = scoring.token_logprobs_backward(r, x, W, t, d_logprobs=d_logprobs, d_entropy=d_entropy,
+                                                 dx=need_x, dW=need_W, handle=ctx.handle)
+        return (dx, dW) + none
+
+
+def token_logprobs(x: torch.Tensor, W: torch.Tensor, t: torch.Tensor, temperature: float = 1.0, top: int = 0,
+                   ignore_index: int = -100, keep_logits: bool = False, handle: FLCE = None):
+    """Scoring as a differentiable call: (logprobs, entropy, top_logprobs,
+    top_ids) of scoring.token_logprobs (the latter two None with top 0).
+    Gradients reach x and W from logprobs and entropy; the alternatives carry
+    none. Neither direction synchronises the host; an input that needs no
+    gradient costs no product. keep_logits holds the logits until the backward,
+    which else computes them again."""
+    return TokenLogprobsFunction.apply(x, W, t, temperature, top, ignore_index, keep_logits, handle)
+
+
+class LinearDistillationFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, W, ids, logits, temperature, handle):
+        need_x, need_W = ctx.needs_input_grad[:2]
+        loss, dx, dW = scoring.distill(x.contiguous(), W.contiguous(), ids, logits, temperature=temperature,
+                                       backward=need_x or need_W, dx=need_x, dW=need_W, handle=handle)
+        ctx.save_for_backward(dx, dW)
+        return loss
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_out):
+        dx, dW = ctx.saved_tensors
+        # the factor meets the gradients in their own type, as in the fused loss
+        return (None if dx is None else dx * grad_out.to(dx.dtype), None if dW is None else dW * grad_out.to(dW.dtype),
+                None, None, None, None)
+
+
+def linear_distillation(x: torch.Tensor, W: torch.Tensor, ids: torch.Tensor, logits: torch.Tensor,
+                        temperature: float = 1.0, handle: FLCE = None) -> torch.Tensor:
+    """Distillation from a teacher's top logits, fused as linear_cross_entropy is:
+    the forward computes the gradients too and the backward scales them. Returns
+    the loss of scoring.distill, a 0-dim float32 tensor; never synchronises the
+    host. The teacher gets no gradient."""
+    return LinearDistillationFunction.apply(x, W, ids, logits, temperature, handle)

@@ -520,6 +520,10 @@ flce_status ensure_workspace(flce_handle_t h, uint64_t bytes) {
   return FLCE_OK;
 }
 
+}  // namespace
+
+namespace flce {
+
 // 2-D bf16 map over a row-major matrix (inner = contiguous extent)
 bool map_bf16_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                  uint32_t box_inner, uint32_t box_outer, std::string* why) {
@@ -537,6 +541,10 @@ bool map_f32_3d(CUtensorMap* m, void* base, uint64_t cols, uint64_t rows, uint64
   const uint32_t box[3] = {32, 128, 1};
   return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, 3, dims, strides, box, why);
 }
+
+}  // namespace flce
+
+namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -568,8 +576,11 @@ flce_status read_back(flce_handle_t h, uint32_t* ctrl_dev, cudaStream_t s, float
   return decode_ctrl(h, h->host_ctrl, loss);
 }
 
-// One GEMM on the handle's tile shape; sets num_m from the M extent and the
-// grid from the work units (persistent CTAs, or CTA pairs).
+}  // namespace
+
+namespace flce {
+
+// The tile rows per group of a GEMM in grouped order (UmmaArgs::raster 2), kept per handle.
 int group_for(flce_handle_t h, int shape, int num_m, int num_n, int num_s, int slots) {
   const std::array<int, 5> key{shape, num_m, num_n, num_s, slots};
   auto it = h->group_cache.find(key);
@@ -580,11 +591,19 @@ int group_for(flce_handle_t h, int shape, int num_m, int num_n, int num_s, int s
   return g;
 }
 
+}  // namespace flce
+
+namespace {
+
 // The shape a GEMM with tile_n output columns (from its plan) runs on.
 int shape_for(flce_handle_t h, int64_t tile_n) {
   if (h->cfg.cta_pair != FLCE_CTA_AUTO || h->shape == kShapeSingle) return h->shape;
   return tile_n == 2 * kBN ? kShapeWide : kShapePair;
 }
+
+}  // namespace
+
+namespace flce {
 
 // One GEMM on tile shape `shape`; sets num_m and num_n from the extents (M
 // rows, args.cols columns) and the grid from the work units (persistent
@@ -603,6 +622,10 @@ cudaError_t launch_gemm(flce_handle_t h, int shape, int kind, const CUtensorMap&
   if (shape == kShapePair) return launch_umma_pair(kind, a, b, o, args, slots, s);
   return launch_umma(kind, a, b, o, args, slots, s);
 }
+
+}  // namespace flce
+
+namespace {
 
 // Device copies of a call's host inputs, in one buffer (grown as needed).
 struct Staged {
@@ -1186,6 +1209,12 @@ const char* flce_kernel_name(int32_t kind) {
     case FLCE_K_MUON_PREPARE: return "muon_prepare";
     case FLCE_K_MUON_STEPS: return "muon_steps";
     case FLCE_K_MUON_SMALL: return "muon_small";
+    case FLCE_K_SCORE_STATS: return "score_stats";
+    case FLCE_K_SCORE_GRADIENT: return "score_gradient";
+    case FLCE_K_SCORE_ROWS: return "score_rows";
+    case FLCE_K_SCORE_DLOGITS: return "score_dlogits";
+    case FLCE_K_SCORE_OTHER: return "score_other";
+    case FLCE_K_DISTILL_ROWS: return "distill_rows";
     default: return "?";
   }
 }
@@ -1333,8 +1362,12 @@ flce_status flce_async_status(flce_handle_t h, void* stream) {
   if (e != cudaSuccess) return fail(h, FLCE_ERR_CUDA, "async status: %s", cudaGetErrorString(e));
   // the training-step operators record their errors in the handle's pinned words
   volatile uint32_t* host_sticky = h->host_ctrl + kCtrlSticky;
-  const uint32_t train = *host_sticky;
+  uint32_t train = *host_sticky;
   *host_sticky = 0;
+  // and so do the head's operators, in a word of their own
+  volatile uint32_t* host_score = h->host_ctrl + kHostScoreError;
+  if (train == 0) train = *host_score;
+  *host_score = 0;
   if (!h->ws || h->ws_fresh) return device_status(h, train);
   uint32_t* sticky = static_cast<uint32_t*>(h->ws) + kCtrlSticky;  // the control block leads the workspace
   uint32_t code = 0;

@@ -70,6 +70,7 @@ struct flce_handle_s {
   int wide_clusters = 0;  // clusters of two the wide kernels fit at once
   std::map<std::array<int, 3>, int> muon_small;  // clusters (size, chunks, kernel) that fit at once
   int muon_shape = -1;    // tile shape of the muon products (created with FLCE_CTA_AUTO: picked by size)
+  int score_clusters = 0; // pairs of the head's operators that fit at once (0: not asked yet)
   int muon_clusters = 0;  // clusters of two the muon kernels fit at once (0: not asked yet)
   // tile shape of the handle's GEMMs; an AUTO handle (cfg.cta_pair stays
   // FLCE_CTA_AUTO) runs each GEMM on the shape its plan names, wide or pair
@@ -129,6 +130,19 @@ inline flce_status fail(flce_handle_t h, flce_status st, const char* fmt, ...) {
   }
   return st;
 }
+
+// Word of the handle's pinned memory where the head's operators record a
+// device-side error (kCtrlSticky is the training-step operators').
+constexpr int kHostScoreError = 14;
+
+// flce_api.cu: pieces of the loss's backward that other operators run too
+bool map_bf16_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes, uint32_t box_inner,
+                 uint32_t box_outer, std::string* why);
+bool map_f32_3d(CUtensorMap* m, void* base, uint64_t cols, uint64_t rows, uint64_t planes, uint64_t row_bytes,
+                uint64_t plane_bytes, std::string* why);
+int group_for(flce_handle_t h, int shape, int num_m, int num_n, int num_s, int slots);
+cudaError_t launch_gemm(flce_handle_t h, int shape, int kind, const CUtensorMap& a, const CUtensorMap& b,
+                        const CUtensorMap& o, UmmaArgs args, int64_t M, cudaStream_t s);
 
 struct DeviceGuard {
   int prev = -1;

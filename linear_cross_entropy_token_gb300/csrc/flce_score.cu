@@ -1,0 +1,810 @@
+// Row kernels of the LM-head operators (flce_score.h): what the product's
+// per-group statistics become per token (log probability, entropy, the top
+// alternatives), the gradient's rows, and distillation's rows.
+//
+// A row's softmax over all columns from its groups' (largest m, sum l of 2^y, sum
+// s of y 2^y), y = (z - m) c, c = log2(e) / temperature: with M the largest m and
+// w = 2^((m - M) c),  L = sum w l,  logprob = (z_t - M) / temperature - log L,
+// entropy = log L - (1 / L) sum w (ln2 s + (m - M) / temperature l).
+// M and log L are kept apart: one fp32 sum of both would lose log L's last bits
+// where logits are large.
+//
+// A single logit (the given token's, an alternative's, a teacher's entry's) is
+// summed again, in twice the bits of fp32: products of bf16 are exact in fp32 and
+// every addition's rounding error is carried along. So equal logits stay equal and
+// the order of near-equal ones does not depend on how the product was tiled.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "flce_internal.h"
+#include "flce_score.h"
+#include "ptx.cuh"
+
+namespace flce {
+namespace {
+
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// ------------------------------------------------------- fp32 statistics
+
+// A warp per (row, group): what the product's epilogue does of its accumulators.
+__global__ void __launch_bounds__(256) score_stats_f32_kernel(const float* __restrict__ z, int64_t ldv, int rows, int64_t V,
+                                                              int groups, float c, float2* __restrict__ partials,
+                                                              float* __restrict__ part_s) {
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (u >= static_cast<int64_t>(rows) * groups) return;
+  const int64_t r = u / groups, g = u - r * groups;
+  const float* at = z + r * ldv;
+  const int64_t j = g * kScoreGroup + lane;
+  const float z0 = j < V ? at[j] : -INFINITY, z1 = j + 32 < V ? at[j + 32] : -INFINITY;
+  float m = max_nan(z0, z1);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float y0 = max_nan((z0 - m) * c, -1000.f), y1 = max_nan((z1 - m) * c, -1000.f);
+  const float e0 = exp2f(y0), e1 = exp2f(y1);
+  float l = e0 + e1, s = fmaf(y0, e0, y1 * e1);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    l += __shfl_xor_sync(0xffffffffu, l, o);
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+  }
+  if (lane == 0) {
+    partials[u] = make_float2(m, l);
+    part_s[u] = s;
+  }
+}
+
+// --------------------------------------------------------- shared pieces
+
+template <int THREADS>
+__device__ __forceinline__ float block_max(float v, float* s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = s[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 32; ++w) v = max_nan(v, s[w]);
+  __syncthreads();
+  return v;
+}
+
+template <int THREADS>
+__device__ __forceinline__ float block_sum(float v, float* s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = s[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 32; ++w) v += s[w];
+  __syncthreads();
+  return v;
+}
+
+// x . w in twice the bits of fp32, the same in all lanes of the warp
+__device__ __forceinline__ void two_sum(float& hi, float& lo, float p) {
+  const float s = __fadd_rn(hi, p);
+  const float b = __fsub_rn(s, hi);
+  lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(p, b)));
+  hi = s;
+}
+
+__device__ __forceinline__ double warp_dot(const __nv_bfloat16* x, const __nv_bfloat16* w, int64_t H, int lane) {
+  float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int64_t h = lane * 8; h < H; h += 256) {
+    const uint4 a = *reinterpret_cast<const uint4*>(x + h);
+    const uint4 b = *reinterpret_cast<const uint4*>(w + h);
+    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      two_sum(hi[i], lo[i], __fmul_rn(__uint_as_float(av[i] << 16), __uint_as_float(bv[i] << 16)));
+      two_sum(hi[i], lo[i], __fmul_rn(__uint_as_float(av[i] & 0xFFFF0000u), __uint_as_float(bv[i] & 0xFFFF0000u)));
+    }
+  }
+  double d = 0.0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d += static_cast<double>(hi[i]) + static_cast<double>(lo[i]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+  return d;
+}
+
+__device__ __forceinline__ double warp_dot(const float* x, const float* w, int64_t H, int lane) {
+  double d = 0.0;
+  for (int64_t h = lane; h < H; h += 32) d = fma(static_cast<double>(x[h]), static_cast<double>(w[h]), d);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+  return d;
+}
+
+// A key that orders floats (NaN above all, 0 below every value's)
+__device__ __forceinline__ uint32_t order_key(float v) {
+  if (v != v) return 0xFFFFFFFFu;
+  const uint32_t b = __float_as_uint(v);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+// doubles likewise
+__device__ __forceinline__ uint64_t order_key(double v) {
+  if (v != v) return ~0ull;
+  if (v == 0.0) v = 0.0;  // one zero
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v));
+  return (b >> 63) ? ~b : (b | (1ull << 63));
+}
+
+constexpr int kRowThreads = 256;
+constexpr int kMaxCandidates = 128;
+constexpr int kMaxValues = kScoreMaxTop * kScoreGroup;
+
+struct SelectSmem {
+  int hist[256];
+  int digit, above;
+  int warp_cnt[kRowThreads / 32];
+  int count, ties;
+};
+
+// The k-th largest of n keys (k <= n) by its bytes from the top; `above` gets how
+// many are larger.
+template <class Key>
+__device__ __forceinline__ uint32_t block_select(int64_t n, int k, SelectSmem& s, int& above, Key&& key) {
+  uint32_t prefix = 0;
+  int rest = k;  // rank among the keys with the prefix
+#pragma unroll 1
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = threadIdx.x; i < 256; i += kRowThreads) s.hist[i] = 0;
+    __syncthreads();
+    for (int64_t i = threadIdx.x; i < n; i += kRowThreads) {
+      const uint32_t v = key(i);
+      if (shift == 24 || (v >> (shift + 8)) == prefix) atomicAdd(&s.hist[(v >> shift) & 255u], 1);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      // lane i holds digits 255 - 8 i down to 248 - 8 i
+      const int lane = threadIdx.x;
+      int own = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) own += s.hist[255 - 8 * lane - j];
+      int upto = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      int before = upto - own;
+      if (before < rest && rest <= upto) {
+        int d = 255 - 8 * lane;
+        while (before + s.hist[d] < rest) before += s.hist[d--];
+        s.digit = d;
+        s.above = before;
+      }
+    }
+    __syncthreads();
+    prefix = (prefix << 8) | static_cast<uint32_t>(s.digit);
+    rest -= s.above;
+    __syncthreads();
+  }
+  above = k - rest;
+  return prefix;
+}
+
+// Positions 0 .. n - 1, in order, that `take` wants (2: always, 1: the first
+// `quota` of them), at most `room`; put(slot, position). Returns how many.
+template <class Take, class Put>
+__device__ __forceinline__ int block_collect(int64_t n, int quota, int room, SelectSmem& s, Take&& take, Put&& put) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t below = (1u << lane) - 1u;
+  int done = 0, tied = 0;
+  for (int64_t base = 0; base < n; base += kRowThreads) {
+    const int64_t i = base + threadIdx.x;
+    const int want = i < n ? take(i) : 0;
+    const uint32_t tie = __ballot_sync(0xffffffffu, want == 1);
+    if (__syncthreads_or(want) == 0) continue;
+    if (lane == 0) s.warp_cnt[warp] = __popc(tie);
+    __syncthreads();
+    int rank = tied;
+    for (int w = 0; w < kRowThreads / 32; ++w) {
+      if (w < warp) rank += s.warp_cnt[w];
+      tied += s.warp_cnt[w];
+    }
+    rank += __popc(tie & below);
+    const bool in = want == 2 || (want == 1 && rank < quota);
+    const uint32_t chosen = __ballot_sync(0xffffffffu, in);
+    __syncthreads();
+    if (lane == 0) s.warp_cnt[warp] = __popc(chosen);
+    __syncthreads();
+    int slot = done;
+    for (int w = 0; w < kRowThreads / 32; ++w) {
+      if (w < warp) slot += s.warp_cnt[w];
+      done += s.warp_cnt[w];
+    }
+    slot += __popc(chosen & below);
+    if (in && slot < room) put(slot, i);
+    __syncthreads();
+  }
+  return min(done, room);
+}
+
+// ------------------------------------------------- log probabilities
+
+// A block per row. The top k logits lie in the k groups with the largest maxima
+// (ties to the lower group: each of those groups holds an element that comes
+// before any of another group). Their stored values, rounded, bound the logits
+// from both sides; whatever may be among the k largest is summed again exactly,
+// with the given token, and ordered by (logit, lowest id).
+//
+// Bound by the latency of the selections and of the candidates' rows of W: about
+// k + 1 rows of W a token through L2, beside a product that costs V of them.
+template <class E, class Z, bool TOP>
+__global__ void __launch_bounds__(kRowThreads) score_rows_kernel(const ScoreRowsArgs a) {
+  __shared__ float s_red[kRowThreads / 32];
+  __shared__ SelectSmem s_sel;
+  __shared__ int s_group[kScoreMaxTop];
+  __shared__ float s_value[TOP ? kMaxValues : 1];
+  __shared__ float s_gmax[kScoreMaxTop];
+  __shared__ int64_t s_id[kMaxCandidates];
+  __shared__ double s_dot[kMaxCandidates + 1];
+  const int64_t r = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (r == 0 && threadIdx.x == 0) {
+    const uint32_t code = ld_volatile_u32(a.ctrl);
+    if (code != 0) *reinterpret_cast<volatile uint32_t*>(a.host_error) = code;
+  }
+  const int64_t t = a.t ? a.t[r] : -1;
+  if (a.t && t == a.ignore_index) {
+    if (threadIdx.x == 0) {
+      a.logprobs[r] = 0.f;
+      a.entropy[r] = 0.f;
+      a.stats[r] = make_float2(0.f, 0.f);
+    }
+    if (TOP && threadIdx.x < a.top) {
+      a.top_logprobs[r * a.top + threadIdx.x] = 0.f;
+      a.top_ids[r * a.top + threadIdx.x] = -1;
+    }
+    return;
+  }
+  const bool bad = a.t && (t < 0 || t >= a.V);
+  const float2* part = a.partials + r * a.groups;
+  const float* part_s = a.part_s + r * a.groups;
+  float m = -INFINITY;
+  for (int g = threadIdx.x; g < a.groups; g += kRowThreads) m = max_nan(m, part[g].x);
+  const float M = block_max<kRowThreads>(m, s_red);
+  float L = 0.f, S = 0.f;
+  for (int g = threadIdx.x; g < a.groups; g += kRowThreads) {
+    const float2 p = part[g];
+    const float d = max_nan((p.x - M) * a.c, -1000.f), w = ex2(d);
+    L = fmaf(w, p.y, L);
+    S = fmaf(w, fmaf(d, p.y, part_s[g]), S);
+  }
+  L = block_sum<kRowThreads>(L, s_red);
+  S = block_sum<kRowThreads>(S, s_red);
+  const float log_L = logf(L);
+  const E* x = static_cast<const E*>(a.x) + r * a.H;
+  const E* W = static_cast<const E*>(a.W);
+
+  int n = 0;
+  if constexpr (TOP) {
+    const int kg = min(a.top, a.groups);
+    int above;
+    const uint32_t gkey = block_select(a.groups, kg, s_sel, above, [&](int64_t g) { return order_key(part[g].x); });
+    block_collect(a.groups, kg - above, kg, s_sel,
+                  [&](int64_t g) {
+                    const uint32_t v = order_key(part[g].x);
+                    return v > gkey ? 2 : (v == gkey ? 1 : 0);
+                  },
+                  [&](int slot, int64_t g) {
+                    s_group[slot] = static_cast<int>(g);
+                    s_gmax[slot] = part[g].x;
+                  });
+    __syncthreads();
+    const int nv = kg * kScoreGroup;
+    const Z* z = static_cast<const Z*>(a.z) + r * a.ldv;
+    for (int i = threadIdx.x; i < nv; i += kRowThreads) {
+      const int64_t j = static_cast<int64_t>(s_group[i >> 6]) * kScoreGroup + (i & 63);
+      float v = -INFINITY;
+      if (j < a.V) {
+        if constexpr (sizeof(Z) == 2)
+          v = fmaf(__half2float(z[j]), a.inv_c, s_gmax[i >> 6]);
+        else
+          v = z[j];
+      }
+      s_value[i] = v;
+    }
+    __syncthreads();
+    // a stored value's bounds: half a step of fp16 (with the fp32 steps around it)
+    // and the product's own sum; -inf lies below fp16's range
+    auto bound = [&](int i, float sign) {
+      const float gm = s_gmax[i >> 6], v = s_value[i];
+      if (sizeof(Z) == 2 && v == -INFINITY) return sign < 0.f ? v : fmaf(-65500.f, a.inv_c, gm);
+      float reach = fmaxf(fabsf(M), fabsf(v)) * 6.1e-5f;
+      if (sizeof(Z) == 2) reach = fmaf(gm - v, 5.5e-4f, fmaf(1.2e-7f, a.inv_c, reach));
+      return reach < INFINITY ? fmaf(sign, reach, v) : v;
+    };
+    auto there = [&](int i) { return static_cast<int64_t>(s_group[i >> 6]) * kScoreGroup + (i & 63) < a.V; };
+    const uint32_t least =
+        block_select(nv, a.top, s_sel, above, [&](int64_t i) { return there(i) ? order_key(bound(static_cast<int>(i), -1.f)) : 0u; });
+    auto maybe = [&](int64_t i) { return there(i) && order_key(bound(static_cast<int>(i), 1.f)) >= least ? 2 : 0; };
+    auto put = [&](int slot, int64_t i) { s_id[slot] = static_cast<int64_t>(s_group[i >> 6]) * kScoreGroup + (i & 63); };
+    int many = 0;
+    for (int i = threadIdx.x; i < nv; i += kRowThreads) many += maybe(i) != 0;
+    many = static_cast<int>(block_sum<kRowThreads>(static_cast<float>(many), s_red));
+    if (many <= kMaxCandidates) {
+      n = block_collect(nv, 0, kMaxCandidates, s_sel, maybe, put);
+    } else {
+      // more than can be summed again (nearly equal logits): the largest stored
+      // ones, ties to the lowest id
+      const uint32_t key = block_select(nv, kMaxCandidates, s_sel, above,
+                                        [&](int64_t i) { return there(i) ? order_key(s_value[i]) : 0u; });
+      n = block_collect(nv, kMaxCandidates - above, kMaxCandidates, s_sel,
+                        [&](int64_t i) {
+                          if (!there(i)) return 0;
+                          const uint32_t v = order_key(s_value[i]);
+                          return v > key ? 2 : (v == key ? 1 : 0);
+                        },
+                        put);
+    }
+    __syncthreads();
+  }
+  // the given token's logit behind the candidates'
+  const int dots = n + (a.t && !bad ? 1 : 0);
+  for (int i = warp; i < dots; i += kRowThreads / 32) {
+    const double d = warp_dot(x, W + (i < n ? s_id[i] : t) * a.H, a.H, lane);
+    if (lane == 0) s_dot[i] = d;
+  }
+  __syncthreads();
+  auto log_p = [&](double z) {
+    return static_cast<float>((z - static_cast<double>(M)) * a.inv_temperature - static_cast<double>(log_L));
+  };
+  if constexpr (TOP) {
+    if (threadIdx.x < n) {
+      const uint64_t own = order_key(s_dot[threadIdx.x]);
+      const int64_t id = s_id[threadIdx.x];
+      int rank = 0;
+      for (int i = 0; i < n; ++i) {
+        const uint64_t v = order_key(s_dot[i]);
+        rank += v > own || (v == own && s_id[i] < id);
+      }
+      if (rank < a.top) {
+        a.top_logprobs[r * a.top + rank] = log_p(s_dot[threadIdx.x]);
+        a.top_ids[r * a.top + rank] = id;
+      }
+    }
+  }
+  if (threadIdx.x == 0) {
+    if (a.t) a.logprobs[r] = bad ? NAN : log_p(s_dot[n]);
+    a.entropy[r] = log_L - kLn2 * S / L;
+    a.stats[r] = make_float2(M, log_L);
+    if (bad) *reinterpret_cast<volatile uint32_t*>(a.host_error) = kErrBadTarget;
+  }
+}
+
+// ------------------------------------------------------------ gradients
+
+// Copies 16-byte pieces, or 4-byte ones where a row is not made of those
+__device__ __forceinline__ void copy_row(const uint8_t* from, uint8_t* to, int64_t bytes, bool live) {
+  if (bytes % 16 == 0) {
+    for (int64_t i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16)
+      *reinterpret_cast<uint4*>(to + i) = live ? *reinterpret_cast<const uint4*>(from + i) : make_uint4(0, 0, 0, 0);
+  } else {
+    for (int64_t i = threadIdx.x * 4; i < bytes; i += blockDim.x * 4)
+      *reinterpret_cast<uint32_t*>(to + i) = live ? *reinterpret_cast<const uint32_t*>(from + i) : 0u;
+  }
+}
+
+// d_j = (1 / temperature) (g [j = t] - p_j (g + h (log p_j + H))), as a + b log2 p.
+// Rows that do not count get zeros, and a zero row of x, so that nothing that
+// stands there (it may be NaN) reaches dW.
+__global__ void __launch_bounds__(128) score_prepare_kernel(const ScorePrepareArgs a) {
+  const int64_t r = blockIdx.x;
+  const int64_t t = a.t[r];
+  const bool ignored = t == a.ignore_index, bad = !ignored && (t < 0 || t >= a.V);
+  const bool live = !ignored && !bad;
+  if (threadIdx.x == 0) {
+    if (bad) atomicCAS(a.ctrl, 0u, kErrBadTarget);
+    ScoreRow q{0.f, 0.f, 0.f, 0.f, 0.f, -1};
+    if (live) {
+      const float2 st = a.stats[r];
+      const float inv = static_cast<float>(1.0 / a.temperature);
+      const float g = a.d_logprobs ? a.d_logprobs[r] : 0.f;
+      const float h = a.d_entropy ? a.d_entropy[r] : 0.f;
+      q.largest = st.x;
+      q.log2_total = st.y * kLog2e;
+      q.a = -inv * (a.d_entropy ? fmaf(h, a.entropy[r], g) : g);
+      q.b = -inv * h * kLn2;
+      q.add = inv * g;
+      q.target = static_cast<int32_t>(t);
+      // what the exponentials' lower limit would hide
+      if (!(fabsf(q.log2_total) < INFINITY) || !(fabsf(q.largest) < INFINITY)) q.a = NAN;
+    }
+    a.row[r] = q;
+    a.dcorr[r] = 0.f;
+  }
+  if (a.xm) {
+    const int64_t bytes = a.H * (a.bf16 ? 2 : 4);
+    copy_row(static_cast<const uint8_t*>(a.x) + r * bytes, static_cast<uint8_t*>(a.xm) + r * bytes, bytes, live);
+  }
+}
+
+// Eight columns of a row's gradient from the stored logits. The padding behind the
+// last column (ldv is a multiple of 64) becomes zero.
+__device__ __forceinline__ void dlogits8(const __half* z, __nv_bfloat16* d, int64_t j, int64_t V, float gmax, float c,
+                                         const ScoreRow& q, float* dcorr) {
+  const uint4 in = *reinterpret_cast<const uint4*>(z + j);
+  const uint32_t iv[4] = {in.x, in.y, in.z, in.w};
+  const float shift = fmaf(gmax - q.largest, c, -q.log2_total);
+  uint32_t ov[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&iv[i]));
+    float v[2] = {y.x, y.y};
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t col = j + 2 * i + u;
+      const float t = max_nan(v[u] + shift, -1000.f);
+      v[u] = col < V ? ex2(t) * fmaf(q.b, t, q.a) : 0.f;
+      if (col == q.target) {
+        v[u] += q.add;
+        if (dcorr) *dcorr = v[u] - __bfloat162float(__float2bfloat16_rn(v[u]));
+      }
+    }
+    __nv_bfloat162 o = __floats2bfloat162_rn(v[0], v[1]);
+    ov[i] = *reinterpret_cast<uint32_t*>(&o);
+  }
+  *reinterpret_cast<uint4*>(d + j) = make_uint4(ov[0], ov[1], ov[2], ov[3]);
+}
+
+__device__ __forceinline__ void dlogits4(const float* z, float* d, int64_t j, int64_t V, float c, const ScoreRow& q) {
+  const float4 in = *reinterpret_cast<const float4*>(z + j);
+  float v[4] = {in.x, in.y, in.z, in.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float t = max_nan(fmaf(v[i] - q.largest, c, -q.log2_total), -1000.f);
+    v[i] = j + i < V ? exp2f(t) * fmaf(q.b, t, q.a) : 0.f;
+    if (j + i == q.target) v[i] += q.add;
+  }
+  *reinterpret_cast<float4*>(d + j) = make_float4(v[0], v[1], v[2], v[3]);
+}
+
+// Reads 2 and writes 2 bytes a logit (fp32: 4 and 4): HBM bounds it.
+constexpr int kDlogitsThreads = 256;
+
+__global__ void __launch_bounds__(kDlogitsThreads) score_dlogits_bf16_kernel(
+    const __half* z, const float2* __restrict__ partials, int groups, __nv_bfloat16* d, int64_t ldv, int64_t V, float c,
+    const ScoreRow* __restrict__ row, float* __restrict__ dcorr) {
+  const int64_t r = blockIdx.x;
+  const ScoreRow q = row[r];
+  const int64_t j = (static_cast<int64_t>(blockIdx.y) * kDlogitsThreads + threadIdx.x) * 8;
+  if (j >= ldv) return;
+  if (q.a == 0.f && q.b == 0.f && q.add == 0.f) {
+    *reinterpret_cast<uint4*>(d + r * ldv + j) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  dlogits8(z + r * ldv, d + r * ldv, j, V, partials[r * groups + j / kScoreGroup].x, c, q, dcorr + r);
+}
+
+__global__ void __launch_bounds__(kDlogitsThreads) score_dlogits_f32_kernel(const float* z, float* d, int64_t ldv, int64_t V,
+                                                                           float c, const ScoreRow* __restrict__ row) {
+  const int64_t r = blockIdx.x;
+  const ScoreRow q = row[r];
+  const int64_t j = (static_cast<int64_t>(blockIdx.y) * kDlogitsThreads + threadIdx.x) * 4;
+  if (j >= ldv) return;
+  if (q.a == 0.f && q.b == 0.f && q.add == 0.f) {
+    *reinterpret_cast<float4*>(d + r * ldv + j) = make_float4(0.f, 0.f, 0.f, 0.f);
+    return;
+  }
+  dlogits4(z + r * ldv, d + r * ldv, j, V, c, q);
+}
+
+// dx: the sum of the splits in their order, with the target's entry put right,
+// rounded once. H % 8 == 0.
+__global__ void __launch_bounds__(128) score_dx_kernel(const float* __restrict__ part, int splits, int64_t split_stride,
+                                                       int64_t H, const __nv_bfloat16* __restrict__ W,
+                                                       const ScoreRow* __restrict__ row, const float* __restrict__ dcorr,
+                                                       __nv_bfloat16* __restrict__ dx) {
+  const int64_t r = blockIdx.x;
+  const int64_t h = (static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * 4;
+  if (h >= H) return;
+  const int64_t i = r * H + h;
+  float4 acc = *reinterpret_cast<const float4*>(part + i);
+  for (int s = 1; s < splits; ++s) {
+    const float4 v = *reinterpret_cast<const float4*>(part + s * split_stride + i);
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
+  }
+  const int32_t t = row ? row[r].target : -1;
+  if (t >= 0) {
+    const float c = dcorr[r];
+    const uint2 wv = *reinterpret_cast<const uint2*>(W + t * H + h);
+    acc.x = fmaf(__uint_as_float(wv.x << 16), c, acc.x);
+    acc.y = fmaf(__uint_as_float(wv.x & 0xFFFF0000u), c, acc.y);
+    acc.z = fmaf(__uint_as_float(wv.y << 16), c, acc.z);
+    acc.w = fmaf(__uint_as_float(wv.y & 0xFFFF0000u), c, acc.w);
+  }
+  __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
+  *reinterpret_cast<uint2*>(dx + i) = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+}
+
+// fp32 to bf16, eight a thread (n % 8 == 0)
+__global__ void __launch_bounds__(256) score_cast_kernel(const float4* __restrict__ in, uint4* __restrict__ out, int64_t n8) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i >= n8) return;
+  const float4 a = __ldcs(in + 2 * i), b = __ldcs(in + 2 * i + 1);
+  __nv_bfloat162 v[4] = {__floats2bfloat162_rn(a.x, a.y), __floats2bfloat162_rn(a.z, a.w), __floats2bfloat162_rn(b.x, b.y),
+                         __floats2bfloat162_rn(b.z, b.w)};
+  __stcs(out + i, *reinterpret_cast<uint4*>(v));
+}
+
+__global__ void score_report_kernel(const uint32_t* ctrl, uint32_t* host_error) {
+  const uint32_t code = ld_volatile_u32(ctrl);
+  if (code != 0) *reinterpret_cast<volatile uint32_t*>(host_error) = code;
+}
+
+// --------------------------------------------------------- distillation
+
+__device__ __forceinline__ float teacher_logit(const void* p, int64_t i, int dtype) {
+  if (dtype == FLCE_DTYPE_FP32) return static_cast<const float*>(p)[i];
+  if (dtype == FLCE_DTYPE_FP16) return __half2float(static_cast<const __half*>(p)[i]);
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+// An entry counts if its id is not -1 and its logit is above -inf (a NaN does).
+__device__ __forceinline__ bool teacher_there(int64_t id, float logit) { return id != -1 && !(logit == -INFINITY); }
+
+// A warp per row
+__global__ void __launch_bounds__(256) distill_live_kernel(const int64_t* __restrict__ ids, int64_t ld_ids,
+                                                           const void* __restrict__ logits, int64_t ld_logits, int dtype,
+                                                           int64_t N, int k, int64_t V, uint8_t* __restrict__ live,
+                                                           uint32_t* ctrl) {
+  __shared__ int s_live[8];
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  bool any = false, bad = false;
+  if (r < N)
+    for (int e = lane; e < k; e += 32) {
+      const int64_t id = ids[r * ld_ids + e];
+      if (!teacher_there(id, teacher_logit(logits, r * ld_logits + e, dtype))) continue;
+      any = true;
+      bad = bad || id < 0 || id >= V;
+    }
+  any = __any_sync(0xffffffffu, any);
+  bad = __any_sync(0xffffffffu, bad);
+  if (lane == 0) {
+    s_live[threadIdx.x >> 5] = r < N && any;
+    if (r < N) live[r] = any && !bad;
+    if (bad) atomicCAS(ctrl + kCtrlError, 0u, kErrBadTarget);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int n = 0;
+    for (int w = 0; w < 8; ++w) n += s_live[w];
+    if (n) atomicAdd(ctrl + kCtrlNValid, static_cast<uint32_t>(n));
+  }
+}
+
+__global__ void __launch_bounds__(128) distill_mask_kernel(const uint8_t* __restrict__ x, uint8_t* __restrict__ xm,
+                                                           const uint8_t* __restrict__ live, int64_t row_bytes) {
+  const int64_t r = blockIdx.x;
+  copy_row(x + r * row_bytes, xm + r * row_bytes, row_bytes, live[r] != 0);
+}
+
+constexpr int kDistillThreads = 512;
+
+// A block per row: the row's log-sum-exp from its groups, the entries' logits, the
+// loss T^2 sum_e q_e (log q_e - log p_e), and with the gradient the row of stored
+// logits overwritten by d = (T / n) (p - q), first everywhere, then at the entries
+// (from their exact logits; entries that share an id add up).
+// Bound by the stored logits' way through HBM (2 bytes read, 2 written a logit) and,
+// where there are many entries, by their rows of W through L2.
+template <class E, bool GRADIENT>
+__global__ void __launch_bounds__(kDistillThreads) distill_rows_kernel(const DistillArgs a) {
+  __shared__ float s_red[kDistillThreads / 32];
+  __shared__ double s_z[kScoreMaxTeacher];
+  __shared__ int64_t s_id[kScoreMaxTeacher];
+  __shared__ float s_q[kScoreMaxTeacher];
+  const int64_t r = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr bool bf16 = sizeof(E) == 2;
+  constexpr int kVec = bf16 ? 8 : 4;
+  uint8_t* zrow = static_cast<uint8_t*>(a.z) + r * a.ldv * sizeof(E);
+  if (!a.live[r]) {
+    if (threadIdx.x == 0) a.token_loss[r] = 0.f;
+    if (GRADIENT)
+      for (int64_t j = threadIdx.x * kVec; j < a.ldv; j += kDistillThreads * kVec)
+        *reinterpret_cast<uint4*>(zrow + j * sizeof(E)) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  // entries that do not count have id -1 from here on
+  float top = -INFINITY;
+  for (int e = threadIdx.x; e < a.k; e += kDistillThreads) {
+    const int64_t id = a.ids[r * a.ld_ids + e];
+    const float v = teacher_logit(a.logits, r * a.ld_logits + e, a.dtype);
+    const bool there = teacher_there(id, v);
+    s_id[e] = there ? id : -1;
+    s_q[e] = v;
+    if (there) top = max_nan(top, v);
+  }
+  top = block_max<kDistillThreads>(top, s_red);
+  const E* x = static_cast<const E*>(a.x) + r * a.H;
+  for (int e = warp; e < a.k; e += kDistillThreads / 32)
+    if (s_id[e] >= 0) {
+      const double d = warp_dot(x, static_cast<const E*>(a.W) + s_id[e] * a.H, a.H, lane);
+      if (lane == 0) s_z[e] = d;
+    }
+  const float2* part = a.partials + r * a.groups;
+  float m = -INFINITY;
+  for (int g = threadIdx.x; g < a.groups; g += kDistillThreads) m = max_nan(m, part[g].x);
+  const float M = block_max<kDistillThreads>(m, s_red);
+  float L = 0.f;
+  for (int g = threadIdx.x; g < a.groups; g += kDistillThreads) {
+    const float2 p = part[g];
+    L = fmaf(ex2(max_nan((p.x - M) * a.c, -1000.f)), p.y, L);
+  }
+  L = block_sum<kDistillThreads>(L, s_red);
+  const float log_L = logf(L);
+  const float inv = static_cast<float>(1.0 / a.temperature);
+  float q = 0.f;
+  const int e = threadIdx.x;  // k <= kScoreMaxTeacher <= kDistillThreads
+  const bool there = e < a.k && s_id[e] >= 0;
+  const float rel = there ? (s_q[e] - top) * inv : 0.f;
+  if (there) q = expf(rel);
+  const float total = block_sum<kDistillThreads>(q, s_red);
+  q /= total;
+  float log_p = 0.f, term = 0.f;
+  if (there) {
+    log_p = static_cast<float>((s_z[e] - static_cast<double>(M)) / a.temperature - static_cast<double>(log_L));
+    term = q > 0.f || q != q ? q * (rel - logf(total) - log_p) : 0.f;
+    s_q[e] = q;
+  }
+  term = block_sum<kDistillThreads>(term, s_red);
+  if (threadIdx.x == 0) a.token_loss[r] = static_cast<float>(a.temperature * a.temperature) * term;
+  if constexpr (GRADIENT) {
+    const float scale = static_cast<float>(a.temperature / static_cast<double>(a.ctrl[kCtrlNValid]));
+    ScoreRow row{M, log_L * kLog2e, scale, 0.f, 0.f, -1};
+    if (!(fabsf(row.log2_total) < INFINITY) || !(fabsf(M) < INFINITY)) row.a = NAN;
+    for (int64_t j = threadIdx.x * kVec; j < a.ldv; j += kDistillThreads * kVec) {
+      if constexpr (bf16)
+        dlogits8(reinterpret_cast<const __half*>(zrow), reinterpret_cast<__nv_bfloat16*>(zrow), j, a.V,
+                 part[j / kScoreGroup].x, a.c, row, nullptr);
+      else
+        dlogits4(reinterpret_cast<const float*>(zrow), reinterpret_cast<float*>(zrow), j, a.V, a.c, row);
+    }
+    __syncthreads();
+    if (there) {
+      float all = 0.f;
+      for (int i = 0; i < a.k; ++i)
+        if (s_id[i] == s_id[e]) all += s_q[i];
+      const float d = scale * (expf(log_p) - all);
+      if constexpr (bf16)
+        reinterpret_cast<__nv_bfloat16*>(zrow)[s_id[e]] = __float2bfloat16_rn(d);
+      else
+        reinterpret_cast<float*>(zrow)[s_id[e]] = d;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(1024) distill_finish_kernel(const float* __restrict__ token_loss, int64_t N,
+                                                              const uint32_t* ctrl, float* loss, uint32_t* host_error) {
+  __shared__ double s_sum[32];
+  double s = 0.0;
+  for (int64_t i = threadIdx.x; i < N; i += 1024) s += static_cast<double>(token_loss[i]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = 0.0;
+    for (int w = 0; w < 32; ++w) s += s_sum[w];
+    const uint32_t n = ctrl[kCtrlNValid], code = ctrl[kCtrlError];
+    *loss = code != 0 ? NAN : (n > 0 ? static_cast<float>(s / static_cast<double>(n)) : 0.f);
+    if (code != 0) *reinterpret_cast<volatile uint32_t*>(host_error) = code;
+  }
+}
+
+template <class E, class Z>
+cudaError_t launch_rows(const ScoreRowsArgs& a, cudaStream_t s) {
+  if (a.top > 0)
+    score_rows_kernel<E, Z, true><<<a.rows, kRowThreads, 0, s>>>(a);
+  else
+    score_rows_kernel<E, Z, false><<<a.rows, kRowThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+unsigned blocks_of(int64_t n, int64_t per) { return static_cast<unsigned>((n + per - 1) / per); }
+
+}  // namespace
+
+cudaError_t launch_score_stats_f32(const float* z, int64_t ldv, int rows, int64_t V, int groups, float c, float2* partials,
+                                   float* part_s, cudaStream_t s) {
+  score_stats_f32_kernel<<<blocks_of(static_cast<int64_t>(rows) * groups, 8), 256, 0, s>>>(z, ldv, rows, V, groups, c,
+                                                                                         partials, part_s);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_score_rows(const ScoreRowsArgs& a, cudaStream_t s) {
+  return a.bf16 ? launch_rows<__nv_bfloat16, __half>(a, s) : launch_rows<float, float>(a, s);
+}
+
+cudaError_t launch_score_prepare(const ScorePrepareArgs& a, cudaStream_t s) {
+  score_prepare_kernel<<<a.rows, 128, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_score_dlogits(int bf16, const void* z, const float2* partials, int groups, void* d, int64_t ldv, int rows,
+                                 int64_t V, float c, const ScoreRow* row, float* dcorr, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(rows), blocks_of(ldv, kDlogitsThreads * (bf16 ? 8 : 4)));
+  if (bf16)
+    score_dlogits_bf16_kernel<<<grid, kDlogitsThreads, 0, s>>>(static_cast<const __half*>(z), partials, groups,
+                                                              static_cast<__nv_bfloat16*>(d), ldv, V, c, row, dcorr);
+  else
+    score_dlogits_f32_kernel<<<grid, kDlogitsThreads, 0, s>>>(static_cast<const float*>(z), static_cast<float*>(d), ldv, V, c,
+                                                             row);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_score_dx(const float* part, int splits, int64_t split_stride, int rows, int64_t H, const void* W,
+                            const ScoreRow* row, const float* dcorr, void* dx, cudaStream_t s) {
+  score_dx_kernel<<<dim3(static_cast<unsigned>(rows), blocks_of(H, 512)), 128, 0, s>>>(
+      part, splits, split_stride, H, static_cast<const __nv_bfloat16*>(W), row, dcorr, static_cast<__nv_bfloat16*>(dx));
+  return cudaGetLastError();
+}
+
+cudaError_t launch_score_cast(const float* in, void* out, int64_t n, cudaStream_t s) {
+  score_cast_kernel<<<blocks_of(n / 8, 256), 256, 0, s>>>(reinterpret_cast<const float4*>(in), static_cast<uint4*>(out), n / 8);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_score_report(const uint32_t* ctrl, uint32_t* host_error, cudaStream_t s) {
+  score_report_kernel<<<1, 1, 0, s>>>(ctrl, host_error);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_distill_rows(const DistillArgs& a, cudaStream_t s) {
+  if (a.bf16) {
+    if (a.gradient)
+      distill_rows_kernel<__nv_bfloat16, true><<<a.rows, kDistillThreads, 0, s>>>(a);
+    else
+      distill_rows_kernel<__nv_bfloat16, false><<<a.rows, kDistillThreads, 0, s>>>(a);
+  } else {
+    if (a.gradient)
+      distill_rows_kernel<float, true><<<a.rows, kDistillThreads, 0, s>>>(a);
+    else
+      distill_rows_kernel<float, false><<<a.rows, kDistillThreads, 0, s>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_distill_live(const int64_t* ids, int64_t ld_ids, const void* logits, int64_t ld_logits, int dtype,
+                                int64_t N, int k, int64_t V, uint8_t* live, uint32_t* ctrl, cudaStream_t s) {
+  distill_live_kernel<<<blocks_of(N, 8), 256, 0, s>>>(ids, ld_ids, logits, ld_logits, dtype, N, k, V, live, ctrl);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_distill_mask(const void* x, void* xm, const uint8_t* live, int rows, int64_t row_bytes, cudaStream_t s) {
+  distill_mask_kernel<<<rows, 128, 0, s>>>(static_cast<const uint8_t*>(x), static_cast<uint8_t*>(xm), live, row_bytes);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_distill_finish(const float* token_loss, int64_t N, const uint32_t* ctrl, float* loss, uint32_t* host_error,
+                                  cudaStream_t s) {
+  distill_finish_kernel<<<1, 1024, 0, s>>>(token_loss, N, ctrl, loss, host_error);
+  return cudaGetLastError();
+}
+
+}  // namespace flce

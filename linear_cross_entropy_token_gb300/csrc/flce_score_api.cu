@@ -1,0 +1,680 @@
+// Host side of the LM-head operators' entry points: argument checks, chunks of
+// tokens, workspace layout, TMA descriptors, launches.
+#include <algorithm>
+#include <cmath>
+
+#include "flce_handle.h"
+#include "flce_score.h"
+
+using namespace flce;
+
+namespace {
+
+constexpr double kLog2e = 1.4426950408889634;
+constexpr uint64_t kDefaultBudget = 5ull << 28;  // as the loss's planner
+constexpr int64_t kMaxChunk = 32768;
+constexpr uint64_t kPointerAlign = 256;          // of the workspace and of kept logits
+constexpr int64_t kTileRows = 2 * kBM;
+
+uint64_t addr(const void* p) { return reinterpret_cast<uint64_t>(p); }
+
+bool is_bf16(flce_handle_t h) { return h->cfg.dtype == FLCE_DTYPE_BF16; }
+
+// The logits of a row in memory, in elements (fp16 / fp32)
+int64_t row_elements(int64_t V) { return static_cast<int64_t>(align_up(static_cast<uint64_t>(V), 64)); }
+
+struct Kept {
+  uint64_t partials = 0, total = 0;  // the logits lead
+};
+
+Kept kept_layout(bool bf16, int64_t N, int64_t V) {
+  Kept k;
+  k.partials = align_up(static_cast<uint64_t>(N) * row_elements(V) * (bf16 ? 2 : 4), kAlign);
+  k.total = k.partials + align_up(static_cast<uint64_t>(N) * cdiv(V, kScoreGroup) * 8, kAlign);
+  return k;
+}
+
+// What a call needs: tokens per chunk, splits of dx's sum over V, and the
+// workspace's parts.
+struct Plan {
+  int64_t chunk = 0, ldv = 0, groups = 0, splits = 1;
+  int64_t tile_n_dx = 0, tile_n_dw = 0;  // columns of the backward products' tiles
+  uint64_t ctrl = 0, z = 0, partials = 0, part_s = 0, row = 0, dcorr = 0, xm = 0, live = 0, dw = 0, total = 0;
+};
+
+struct Needs {
+  bool z, stats, gradient, dx, dw_cast, live;
+};
+
+// Gradients: chunks, tile shapes and splits are the loss's plan with both
+// products in one launch. Forward alone: as many tokens as the budget holds, in
+// whole tiles, the chunks evened out.
+flce_status make_plan(flce_handle_t h, int64_t N, int64_t H, int64_t V, const Needs& q, Plan* out) {
+  const bool bf16 = is_bf16(h);
+  const uint64_t es = bf16 ? 2 : 4;
+  Plan p;
+  p.ldv = row_elements(V);
+  p.groups = cdiv(V, kScoreGroup);
+  if (q.gradient) {
+    flce_config cfg = h->cfg;
+    cfg.dlogits_mode = FLCE_DLOGITS_INPLACE;
+    cfg.cta_pair = FLCE_CTA_AUTO;
+    cfg.backward_launch = FLCE_BACKWARD_ONE_LAUNCH;
+    flce_plan lp;
+    const flce_status st = flce_make_plan(&cfg, N, H, V, 0, h->num_sms, &lp);
+    if (st != FLCE_OK) return fail(h, st, "no chunk of these sizes fits the HBM budget");
+    p.chunk = lp.chunk;
+    p.splits = lp.dx_splits;
+    p.tile_n_dx = lp.tile_n_dx;
+    p.tile_n_dw = lp.tile_n_dw;
+  } else {
+    const uint64_t budget = h->cfg.hbm_budget_bytes ? h->cfg.hbm_budget_bytes : kDefaultBudget;
+    const uint64_t a_row = (q.z ? p.ldv * es : 0) + (q.stats ? p.groups * 12ull : 0);
+    int64_t most = std::min<int64_t>(kMaxChunk, static_cast<int64_t>(budget / std::max<uint64_t>(a_row, 1)));
+    if (most < std::min<int64_t>(N, kBM)) return fail(h, FLCE_ERR_BUDGET, "not even one %d-token chunk fits the HBM budget", kBM);
+    if (N > most) {
+      const int64_t unit = most >= kTileRows ? kTileRows : kBM;
+      most = most / unit * unit;
+      most = std::min(most, static_cast<int64_t>(align_up(static_cast<uint64_t>(cdiv(N, cdiv(N, most))), unit)));
+    }
+    p.chunk = std::min(N, most);
+  }
+  uint64_t off = 0;
+  auto take = [&](uint64_t bytes) {
+    const uint64_t at = off;
+    off = align_up(off + bytes, kAlign);
+    return at;
+  };
+  const uint64_t c = static_cast<uint64_t>(p.chunk);
+  p.ctrl = take(kCtrlWords * 4);
+  if (q.z) p.z = take(c * p.ldv * es);
+  // the statistics' partials are last read before dx's partial sums are written
+  const bool dx_parts = q.dx && (bf16 || p.splits > 1);
+  p.partials = take(std::max<uint64_t>(q.stats ? c * p.groups * 8 : 0,
+                                       dx_parts ? static_cast<uint64_t>(p.splits) * c * H * 4 : 0));
+  if (q.stats) p.part_s = take(c * p.groups * 4);
+  if (q.gradient) {
+    p.row = take(c * sizeof(ScoreRow));
+    p.dcorr = take(c * 4);
+    p.xm = take(c * H * es);
+    if (q.dw_cast) p.dw = take(static_cast<uint64_t>(V) * H * 4);
+  }
+  if (q.live) p.live = take(static_cast<uint64_t>(std::max<int64_t>(N, 1)));
+  p.total = off;
+  *out = p;
+  return FLCE_OK;
+}
+
+// Sizes, pointers and alignment of x and W
+flce_status check_product(flce_handle_t h, const void* x, const void* W, int64_t N, int64_t H, int64_t V, double temperature) {
+  if (N < 0 || H < 1 || V < 1 || N > kMaxDim || H > kMaxDim || V > kMaxDim)
+    return fail(h, FLCE_ERR_INVALID_ARG, "sizes must satisfy 0 <= N, 1 <= H, 1 <= V, all below 2^31");
+  if (!(temperature > 0.0) || !std::isfinite(temperature) || !(1.0 / temperature < 1e30) || !(temperature < 1e30))
+    return fail(h, FLCE_ERR_INVALID_ARG, "the temperature must be positive and finite");
+  if (!W || (N > 0 && !x)) return fail(h, FLCE_ERR_INVALID_ARG, "null pointer argument");
+  if (is_bf16(h)) {
+    if (H % 8 != 0) return fail(h, FLCE_ERR_INVALID_ARG, "bf16 needs H %% 8 == 0 (H = %lld)", static_cast<long long>(H));
+    if ((addr(x) | addr(W)) % 16) return fail(h, FLCE_ERR_INVALID_ARG, "x and W must be 16-byte aligned");
+  } else if ((addr(x) | addr(W)) % 4) {
+    return fail(h, FLCE_ERR_INVALID_ARG, "x and W must be 4-byte aligned");
+  }
+  return FLCE_OK;
+}
+
+flce_status check_gradients(flce_handle_t h, const void* dx, const void* dW, int32_t dw_dtype) {
+  if (dW && dw_dtype != FLCE_DTYPE_FP32 && !(dw_dtype == FLCE_DTYPE_BF16 && is_bf16(h)))
+    return fail(h, FLCE_ERR_UNSUPPORTED, "dW must be fp32, or bf16 on a bf16 handle");
+  if ((addr(dx) | addr(dW)) % (is_bf16(h) ? 16 : 4))
+    return fail(h, FLCE_ERR_INVALID_ARG, "dx and dW are not aligned (16 bytes on a bf16 handle, else 4)");
+  return FLCE_OK;
+}
+
+flce_status check_workspace(flce_handle_t h, const void* ws, uint64_t bytes, uint64_t need) {
+  if (!ws || addr(ws) % kPointerAlign || bytes < need)
+    return fail(h, FLCE_ERR_BUDGET, "the workspace must hold %llu bytes, %llu-byte aligned",
+                static_cast<unsigned long long>(need), static_cast<unsigned long long>(kPointerAlign));
+  return FLCE_OK;
+}
+
+// The pairs that run at once. The backward's products run on both pair shapes,
+// whatever shape the handle's loss was created with.
+flce_status ensure_clusters(flce_handle_t h) {
+  if (!is_bf16(h)) return FLCE_OK;
+  if (h->score_clusters == 0) {
+    if (h->wide_clusters <= 0) h->wide_clusters = umma_wide_max_clusters();
+    if (h->pair_clusters <= 0) h->pair_clusters = umma_pair_max_clusters();
+    h->score_clusters = score_gemm_max_clusters();
+  }
+  if (h->score_clusters <= 0 || h->wide_clusters <= 0 || h->pair_clusters <= 0)
+    return fail(h, FLCE_ERR_UNSUPPORTED, "no CTA pair fits the device");
+  return FLCE_OK;
+}
+
+flce_status clear_ctrl(flce_handle_t h, uint32_t* ctrl, cudaStream_t s) {
+  const cudaError_t e = cudaMemsetAsync(ctrl, 0, kCtrlWords * 4, s);
+  return e == cudaSuccess ? FLCE_OK : fail(h, FLCE_ERR_CUDA, "memset: %s", cudaGetErrorString(e));
+}
+
+struct Product {
+  const void* x;
+  const void* W;
+  int rows;
+  int64_t H, V;
+  const Plan* p;
+  float c;
+  uint32_t* ctrl;
+};
+
+// z of a chunk and its statistics: stored to z where given
+flce_status run_stats(flce_handle_t h, const Product& q, void* z, float2* partials, float* part_s, cudaStream_t s) {
+  const double dr = q.rows, dH = static_cast<double>(q.H), dV = static_cast<double>(q.V);
+  const int groups = static_cast<int>(q.p->groups);
+  if (!is_bf16(h)) {
+    float* zf = static_cast<float*>(z);
+    FLCE_LAUNCH(FLCE_K_SIMT_GEMM, 2 * dr * dH * dV, 4 * (dr * dH + dV * dH + dr * dV),
+                launch_simt_gemm_f32(static_cast<const float*>(q.x), q.H, 1, static_cast<const float*>(q.W), 1, q.H, zf,
+                                     q.p->ldv, q.rows, q.V, q.H, 0, 1, nullptr, s));
+    if (partials)
+      FLCE_LAUNCH(FLCE_K_SCORE_STATS, 0.0, 4 * dr * dV + 12 * dr * groups,
+                  launch_score_stats_f32(zf, q.p->ldv, q.rows, q.V, groups, q.c, partials, part_s, s));
+    return FLCE_OK;
+  }
+  CUtensorMap mx, mw, mz;
+  std::string why;
+  if (!map_bf16_2d(&mx, q.x, q.H, q.rows, q.H * 2, 64, 128, &why) || !map_bf16_2d(&mw, q.W, q.H, q.V, q.H * 2, 64, 128, &why))
+    return fail(h, FLCE_ERR_INVALID_ARG, "%s", why.c_str());
+  mz = mx;  // not used without a store
+  if (z && !map_bf16_2d(&mz, z, q.V, q.rows, q.p->ldv * 2, 64, 128, &why))
+    return fail(h, FLCE_ERR_INVALID_ARG, "%s", why.c_str());
+  ScoreGemmArgs a{};
+  a.num_m = static_cast<int>(cdiv(q.rows, kTileRows));
+  a.num_n = static_cast<int>(cdiv(q.V, 2 * kBN));
+  a.kb_total = static_cast<int>(cdiv(q.H, kBK));
+  a.rows = q.rows;
+  a.cols = static_cast<int>(q.V);
+  a.groups = groups;
+  a.store = z != nullptr;
+  a.c = q.c;
+  a.partials = partials;
+  a.part_s = part_s;
+  a.ctrl = q.ctrl;
+  a.timeout_ns = h->timeout_ns;
+  FLCE_LAUNCH(FLCE_K_SCORE_STATS, 2 * dr * dH * dV, 2 * (dr + dV) * dH + (z ? 2 * dr * dV : 0) + 12 * dr * groups,
+              launch_score_gemm(0, mx, mw, mz, a, std::min(a.num_m * a.num_n, h->score_clusters), s));
+  return FLCE_OK;
+}
+
+// d of a chunk straight from the product
+flce_status run_gradient(flce_handle_t h, const Product& q, void* d, const ScoreRow* row, float* dcorr, cudaStream_t s) {
+  const double dr = q.rows, dH = static_cast<double>(q.H), dV = static_cast<double>(q.V);
+  CUtensorMap mx, mw, md;
+  std::string why;
+  if (!map_bf16_2d(&mx, q.x, q.H, q.rows, q.H * 2, 64, 128, &why) ||
+      !map_bf16_2d(&mw, q.W, q.H, q.V, q.H * 2, 64, 128, &why) ||
+      !map_bf16_2d(&md, d, q.V, q.rows, q.p->ldv * 2, 64, 128, &why))
+    return fail(h, FLCE_ERR_INVALID_ARG, "%s", why.c_str());
+  ScoreGemmArgs a{};
+  a.num_m = static_cast<int>(cdiv(q.rows, kTileRows));
+  a.num_n = static_cast<int>(cdiv(q.V, 2 * kBN));
+  a.kb_total = static_cast<int>(cdiv(q.H, kBK));
+  a.rows = q.rows;
+  a.cols = static_cast<int>(q.V);
+  a.groups = static_cast<int>(q.p->groups);
+  a.c = q.c;
+  a.row = row;
+  a.dcorr = dcorr;
+  a.ctrl = q.ctrl;
+  a.timeout_ns = h->timeout_ns;
+  FLCE_LAUNCH(FLCE_K_SCORE_GRADIENT, 2 * dr * dH * dV, 2 * (dr + dV) * dH + 2 * dr * dV,
+              launch_score_gemm(1, mx, mw, md, a, std::min(a.num_m * a.num_n, h->score_clusters), s));
+  return FLCE_OK;
+}
+
+// dx = d W and dW (+)= dt x of a chunk, whichever is asked for. q.x: rows that do
+// not count are zero. row null: no entry to put right.
+struct Backward {
+  const void* d;
+  float* part;         // dx's partial sums
+  void* dx;            // this chunk's rows, or null
+  float* dW;           // fp32, or null
+  const ScoreRow* row;
+  const float* dcorr;
+  bool first;          // the call's first chunk
+  int32_t* claims;     // of the call's one-launch backwards so far
+};
+
+flce_status run_backward(flce_handle_t h, const Product& q, const Backward& b, cudaStream_t s) {
+  const double dr = q.rows, dH = static_cast<double>(q.H), dV = static_cast<double>(q.V);
+  const int64_t H = q.H, V = q.V, ldv = q.p->ldv;
+  const int rows = q.rows;
+  const double dx_bytes = 2 * dr * dV + 2 * dV * dH + 4.0 * q.p->splits * dr * dH;
+  const double dw_bytes = 2 * dr * dV + 2 * dr * dH + (b.first ? 4.0 : 8.0) * dV * dH;
+  if (!is_bf16(h)) {
+    const float* d = static_cast<const float*>(b.d);
+    if (b.dx)
+      FLCE_LAUNCH(FLCE_K_SIMT_GEMM, 2 * dr * dV * dH, 2 * dx_bytes,
+                  launch_simt_gemm_f32(d, ldv, 1, static_cast<const float*>(q.W), H, 1, static_cast<float*>(b.dx), H, rows, H,
+                                       V, 0, static_cast<int>(q.p->splits), b.part, s));
+    if (b.dW)
+      FLCE_LAUNCH(FLCE_K_SIMT_GEMM, 2 * dr * dV * dH, 2 * dw_bytes,
+                  launch_simt_gemm_f32(d, 1, ldv, static_cast<const float*>(q.x), H, 1, b.dW, H, V, H, rows, b.first ? 0 : 1,
+                                       1, nullptr, s));
+    return FLCE_OK;
+  }
+  std::string why;
+  DualMaps maps;
+  const int kb_v = static_cast<int>(cdiv(V, kBK));
+  const int kbps = static_cast<int>(cdiv(kb_v, q.p->splits));
+  const int S = static_cast<int>(cdiv(kb_v, kbps));
+  if (!map_bf16_2d(&maps.a[0], b.d, V, rows, ldv * 2, 64, 128, &why) ||
+      !map_bf16_2d(&maps.b[0], q.W, H, V, H * 2, 64, 64, &why) ||
+      (b.dx && !map_f32_3d(&maps.o[0], b.part, H, rows, S, H * 4, static_cast<uint64_t>(q.p->chunk) * H * 4, &why)) ||
+      !map_bf16_2d(&maps.a[1], b.d, V, rows, ldv * 2, 64, 64, &why) ||
+      !map_bf16_2d(&maps.b[1], q.x, H, rows, H * 2, 64, 64, &why) ||
+      (b.dW && !map_f32_3d(&maps.o[1], b.dW, H, V, 1, H * 4, static_cast<uint64_t>(V) * H * 4, &why)))
+    return fail(h, FLCE_ERR_INVALID_ARG, "%s", why.c_str());
+  DualArgs a{};
+  UmmaArgs& dx = a.p[0];
+  dx.num_s = S;
+  dx.kb_total = kb_v;
+  dx.kb_per_split = kbps;
+  dx.raster = 2;
+  dx.rows = rows;
+  dx.cols = static_cast<int>(H);
+  dx.ctrl = q.ctrl;
+  dx.timeout_ns = h->timeout_ns;
+  UmmaArgs& dw = a.p[1];
+  dw = dx;
+  dw.num_s = 1;
+  dw.kb_total = dw.kb_per_split = static_cast<int>(cdiv(rows, kBK));
+  dw.raster = 1;
+  dw.rows = static_cast<int>(V);
+  dw.reduce_add = b.first ? 0 : 1;
+  auto shape_of = [](int64_t cols) { return cols == 2 * kBN ? kShapeWide : kShapePair; };
+  if (b.dx && b.dW) {
+    const int shape = shape_of(q.p->tile_n_dx);
+    const bool wide = shape == kShapeWide;
+    const int64_t tile = wide ? 2 * kBN : kBN;
+    const int slots = wide ? h->wide_clusters : h->pair_clusters;
+    dx.num_m = static_cast<int>(cdiv(rows, kTileRows));
+    dw.num_m = static_cast<int>(cdiv(V, kTileRows));
+    dx.num_n = dw.num_n = static_cast<int>(cdiv(H, tile));
+    a.units0 = dx.num_m * dx.num_n * S;
+    dx.group_m = group_for(h, shape, dx.num_m, dx.num_n, S, std::min(a.units0, slots));
+    a.sched_ctr = reinterpret_cast<int32_t*>(q.ctrl + kCtrlSched);
+    a.sched_base = *b.claims;
+    const int units = a.units0 + dw.num_m * dw.num_n;
+    const int pairs = std::min(units, slots);
+    FLCE_LAUNCH(FLCE_K_GEMM_DX_DW, 4 * dr * dV * dH, dx_bytes + dw_bytes,
+                wide ? launch_umma_wide_dual(maps, a, pairs, s) : launch_umma_pair_dual(maps, a, pairs, s));
+    *b.claims += units + pairs;
+  } else if (b.dx) {
+    FLCE_LAUNCH(FLCE_K_GEMM_DX, 2 * dr * dV * dH, dx_bytes,
+                launch_gemm(h, shape_of(q.p->tile_n_dx), kUmmaDxF32, maps.a[0], maps.b[0], maps.o[0], dx, rows, s));
+  } else if (b.dW) {
+    FLCE_LAUNCH(FLCE_K_GEMM_DW, 2 * dr * dV * dH, dw_bytes,
+                launch_gemm(h, shape_of(q.p->tile_n_dw), kUmmaDw, maps.a[1], maps.b[1], maps.o[1], dw, V, s));
+  }
+  if (b.dx)
+    FLCE_LAUNCH(FLCE_K_DX_REDUCE, 0.0, 4.0 * S * dr * dH + 4 * dr * dH,
+                launch_score_dx(b.part, S, q.p->chunk * H, rows, H, q.W, b.row, b.dcorr, b.dx, s));
+  return FLCE_OK;
+}
+
+// dW where no token is: zeros
+flce_status zero_dw(flce_handle_t h, void* dW, int32_t dtype, int64_t V, int64_t H, cudaStream_t s) {
+  if (!dW) return FLCE_OK;
+  const cudaError_t e = cudaMemsetAsync(dW, 0, static_cast<size_t>(V) * H * (dtype == FLCE_DTYPE_FP32 ? 4 : 2), s);
+  return e == cudaSuccess ? FLCE_OK : fail(h, FLCE_ERR_CUDA, "memset: %s", cudaGetErrorString(e));
+}
+
+// ------------------------------------------------------- log probabilities
+
+flce_status logprobs_check(flce_handle_t h, const flce_logprobs_args* r, bool backward) {
+  if (!r) return fail(h, FLCE_ERR_INVALID_ARG, "null pointer argument");
+  flce_status st = check_product(h, r->x, r->W, r->N, r->H, r->V, r->temperature);
+  if (st != FLCE_OK) return st;
+  if (r->top < 0 || r->top > std::min<int64_t>(r->V, kScoreMaxTop))
+    return fail(h, FLCE_ERR_INVALID_ARG, "need 0 <= top <= min(V, %d)", kScoreMaxTop);
+  if (r->N > 0 && (!r->entropy || !r->stats || (r->t && !r->logprobs) || (backward && !r->t) ||
+                   (r->top > 0 && !backward && (!r->top_logprobs || !r->top_ids))))
+    return fail(h, FLCE_ERR_INVALID_ARG, "null pointer argument");
+  if ((addr(r->t) | addr(r->stats) | addr(r->top_ids)) % 8 ||
+      (addr(r->logprobs) | addr(r->entropy) | addr(r->top_logprobs)) % 4 || addr(r->kept) % kPointerAlign)
+    return fail(h, FLCE_ERR_INVALID_ARG, "a pointer is not aligned to its elements (kept: to %d bytes)", static_cast<int>(kPointerAlign));
+  return FLCE_OK;
+}
+
+flce_status logprobs_plan(flce_handle_t h, const flce_logprobs_args* r, bool backward, int32_t dw_dtype, bool dx, Plan* p) {
+  Needs q{};
+  if (backward) {
+    q.z = q.gradient = true;
+    q.dx = dx;
+    q.dw_cast = dw_dtype == FLCE_DTYPE_BF16;
+  } else {
+    q.z = !r->kept && (r->top > 0 || !is_bf16(h));
+    q.stats = true;
+  }
+  return make_plan(h, r->N, r->H, r->V, q, p);
+}
+
+}  // namespace
+
+// No exception leaves a C entry: what can throw here is a host allocation (a
+// message, the table of tile orders).
+extern "C" {
+
+uint64_t flce_logprobs_kept_bytes(flce_handle_t h, int64_t N, int64_t V) {
+  if (!h || N < 0 || V < 1 || N > kMaxDim || V > kMaxDim) return 0;
+  return kept_layout(is_bf16(h), N, V).total;
+}
+
+uint64_t flce_logprobs_workspace_bytes(flce_handle_t h, const flce_logprobs_args* r, int32_t backward, int32_t dw_dtype) try {
+  if (!h) return 0;
+  h->err.clear();
+  Plan p;
+  if (!r || r->N < 0 || r->H < 1 || r->V < 1 || r->N > kMaxDim || r->H > kMaxDim || r->V > kMaxDim) {
+    fail(h, FLCE_ERR_INVALID_ARG, "null argument or bad size");
+    return 0;
+  }
+  return logprobs_plan(h, r, backward != 0, dw_dtype, true, &p) == FLCE_OK ? p.total : 0;
+} catch (...) {
+  return 0;
+}
+
+flce_status flce_logprobs_forward(flce_handle_t h, const flce_logprobs_args* r, void* workspace, uint64_t workspace_bytes,
+                                  void* stream) try {
+  if (!h) return FLCE_ERR_INVALID_ARG;
+  h->err.clear();
+  NvtxRange nvtx("flce_logprobs_forward");
+  flce_status st = logprobs_check(h, r, false);
+  if (st != FLCE_OK) return st;
+  Plan p;
+  st = logprobs_plan(h, r, false, -1, false, &p);
+  if (st == FLCE_OK) st = check_workspace(h, workspace, workspace_bytes, p.total);
+  if (st != FLCE_OK) return st;
+  if (r->N == 0) return FLCE_OK;
+  DeviceGuard guard(h->device);
+  st = ensure_clusters(h);
+  if (st != FLCE_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool bf16 = is_bf16(h);
+  const uint64_t es = bf16 ? 2 : 4;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* kept = static_cast<uint8_t*>(r->kept);
+  uint32_t* ctrl = reinterpret_cast<uint32_t*>(ws + p.ctrl);
+  st = clear_ctrl(h, ctrl, s);
+  if (st != FLCE_OK) return st;
+  const Kept K = kept_layout(bf16, r->N, r->V);
+  const double c = kLog2e / r->temperature;
+  for (int64_t off = 0; off < r->N; off += p.chunk) {
+    const int rows = static_cast<int>(std::min(p.chunk, r->N - off));
+    const Product q{static_cast<const uint8_t*>(r->x) + off * r->H * es, r->W, rows, r->H, r->V, &p, static_cast<float>(c), ctrl};
+    void* z = kept ? kept + off * p.ldv * es : (r->top > 0 || !bf16) ? ws + p.z : nullptr;
+    float2* partials = reinterpret_cast<float2*>(kept ? kept + K.partials + off * p.groups * 8 : ws + p.partials);
+    float* part_s = reinterpret_cast<float*>(ws + p.part_s);
+    st = run_stats(h, q, z, partials, part_s, s);
+    if (st != FLCE_OK) return st;
+    ScoreRowsArgs a{};
+    a.rows = rows;
+    a.top = r->top;
+    a.groups = static_cast<int>(p.groups);
+    a.bf16 = bf16;
+    a.H = r->H;
+    a.V = r->V;
+    a.ldv = p.ldv;
+    a.ignore_index = r->ignore_index;
+    a.c = static_cast<float>(c);
+    a.inv_c = static_cast<float>(1.0 / c);
+    a.inv_temperature = 1.0 / r->temperature;
+    a.x = q.x;
+    a.W = r->W;
+    a.t = r->t ? r->t + off : nullptr;
+    a.partials = partials;
+    a.part_s = part_s;
+    a.z = z;
+    a.logprobs = r->logprobs ? r->logprobs + off : nullptr;
+    a.entropy = r->entropy + off;
+    a.stats = reinterpret_cast<float2*>(r->stats) + off;
+    a.top_logprobs = r->top_logprobs ? r->top_logprobs + off * r->top : nullptr;
+    a.top_ids = r->top_ids ? r->top_ids + off * r->top : nullptr;
+    a.ctrl = ctrl;
+    a.host_error = h->host_ctrl + kHostScoreError;
+    FLCE_LAUNCH(FLCE_K_SCORE_ROWS, 0.0, rows * (12.0 * p.groups + (r->top + 1.0) * r->H * es + 12.0 * r->top + 28.0),
+                launch_score_rows(a, s));
+  }
+  return FLCE_OK;
+} catch (...) {
+  return FLCE_ERR_BUDGET;
+}
+
+flce_status flce_logprobs_backward(flce_handle_t h, const flce_logprobs_args* r, const float* d_logprobs,
+                                   const float* d_entropy, void* dx, void* dW, int32_t dw_dtype, void* workspace,
+                                   uint64_t workspace_bytes, void* stream) try {
+  if (!h) return FLCE_ERR_INVALID_ARG;
+  h->err.clear();
+  NvtxRange nvtx("flce_logprobs_backward");
+  flce_status st = logprobs_check(h, r, true);
+  if (st == FLCE_OK) st = check_gradients(h, dx, dW, dw_dtype);
+  if (st != FLCE_OK) return st;
+  if ((addr(d_logprobs) | addr(d_entropy)) % 4) return fail(h, FLCE_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+  if (!dx && !dW) return FLCE_OK;
+  Plan p;
+  st = logprobs_plan(h, r, true, dW ? dw_dtype : -1, dx != nullptr, &p);
+  if (st == FLCE_OK) st = check_workspace(h, workspace, workspace_bytes, p.total);
+  if (st != FLCE_OK) return st;
+  DeviceGuard guard(h->device);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (r->N == 0) return zero_dw(h, dW, dw_dtype, r->V, r->H, s);
+  st = ensure_clusters(h);
+  if (st != FLCE_OK) return st;
+  const bool bf16 = is_bf16(h);
+  const uint64_t es = bf16 ? 2 : 4;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const uint8_t* kept = static_cast<const uint8_t*>(r->kept);
+  uint32_t* ctrl = reinterpret_cast<uint32_t*>(ws + p.ctrl);
+  st = clear_ctrl(h, ctrl, s);
+  if (st != FLCE_OK) return st;
+  const Kept K = kept_layout(bf16, r->N, r->V);
+  const float c = static_cast<float>(kLog2e / r->temperature);
+  const bool cast = dW && dw_dtype == FLCE_DTYPE_BF16;
+  ScoreRow* row = reinterpret_cast<ScoreRow*>(ws + p.row);
+  float* dcorr = reinterpret_cast<float*>(ws + p.dcorr);
+  void* d = ws + p.z;
+  int32_t claims = 0;
+  for (int64_t off = 0; off < r->N; off += p.chunk) {
+    const int rows = static_cast<int>(std::min(p.chunk, r->N - off));
+    const double dr = rows, dV = static_cast<double>(r->V);
+    ScorePrepareArgs a{};
+    a.rows = rows;
+    a.bf16 = bf16;
+    a.H = r->H;
+    a.V = r->V;
+    a.ignore_index = r->ignore_index;
+    a.temperature = r->temperature;
+    a.x = static_cast<const uint8_t*>(r->x) + off * r->H * es;
+    a.xm = ws + p.xm;
+    a.t = r->t + off;
+    a.stats = reinterpret_cast<const float2*>(r->stats) + off;
+    a.entropy = r->entropy + off;
+    a.d_logprobs = d_logprobs ? d_logprobs + off : nullptr;
+    a.d_entropy = d_entropy ? d_entropy + off : nullptr;
+    a.row = row;
+    a.dcorr = dcorr;
+    a.ctrl = ctrl;
+    FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 2.0 * dr * r->H * es + 50.0 * dr, launch_score_prepare(a, s));
+    const Product q{ws + p.xm, r->W, rows, r->H, r->V, &p, c, ctrl};
+    if (kept) {
+      FLCE_LAUNCH(FLCE_K_SCORE_DLOGITS, 0.0, 2.0 * es * dr * dV,
+                  launch_score_dlogits(bf16, kept + off * p.ldv * es,
+                                       reinterpret_cast<const float2*>(kept + K.partials) + off * p.groups,
+                                       static_cast<int>(p.groups), d, p.ldv, rows, r->V, c, row, dcorr, s));
+    } else if (bf16) {
+      st = run_gradient(h, q, d, row, dcorr, s);
+      if (st != FLCE_OK) return st;
+    } else {
+      st = run_stats(h, q, d, nullptr, nullptr, s);
+      if (st != FLCE_OK) return st;
+      FLCE_LAUNCH(FLCE_K_SCORE_DLOGITS, 0.0, 2.0 * es * dr * dV,
+                  launch_score_dlogits(0, d, nullptr, 0, d, p.ldv, rows, r->V, c, row, dcorr, s));
+    }
+    const Backward b{d,
+                     reinterpret_cast<float*>(ws + p.partials),
+                     dx ? static_cast<uint8_t*>(dx) + off * r->H * es : nullptr,
+                     !dW ? nullptr : cast ? reinterpret_cast<float*>(ws + p.dw) : static_cast<float*>(dW),
+                     row,
+                     dcorr,
+                     off == 0,
+                     &claims};
+    st = run_backward(h, q, b, s);
+    if (st != FLCE_OK) return st;
+  }
+  const double el = static_cast<double>(r->V) * r->H;
+  if (cast)
+    FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 6.0 * el, launch_score_cast(reinterpret_cast<float*>(ws + p.dw), dW, r->V * r->H, s));
+  FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 4.0, launch_score_report(ctrl, h->host_ctrl + kHostScoreError, s));
+  return FLCE_OK;
+} catch (...) {
+  return FLCE_ERR_BUDGET;
+}
+
+// ------------------------------------------------------------ distillation
+
+static flce_status distill_check(flce_handle_t h, const flce_distill_args* r) {
+  if (!r) return fail(h, FLCE_ERR_INVALID_ARG, "null pointer argument");
+  flce_status st = check_product(h, r->x, r->W, r->N, r->H, r->V, r->temperature);
+  if (st == FLCE_OK) st = check_gradients(h, r->dx, r->dW, r->dw_dtype);
+  if (st != FLCE_OK) return st;
+  if (r->logits_dtype != FLCE_DTYPE_BF16 && r->logits_dtype != FLCE_DTYPE_FP32 && r->logits_dtype != FLCE_DTYPE_FP16)
+    return fail(h, FLCE_ERR_UNSUPPORTED, "the teacher's logits must be bf16, fp32 or fp16");
+  if (r->K < 1 || r->K > kScoreMaxTeacher) return fail(h, FLCE_ERR_INVALID_ARG, "need 1 <= K <= %d", kScoreMaxTeacher);
+  if (r->ld_ids < r->K || r->ld_logits < r->K) return fail(h, FLCE_ERR_INVALID_ARG, "a row stride is below K");
+  if (!r->loss || (r->N > 0 && (!r->ids || !r->logits || !r->token_loss)))
+    return fail(h, FLCE_ERR_INVALID_ARG, "null pointer argument");
+  if (addr(r->ids) % 8 || addr(r->logits) % (r->logits_dtype == FLCE_DTYPE_FP32 ? 4 : 2) ||
+      (addr(r->loss) | addr(r->token_loss)) % 4)
+    return fail(h, FLCE_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+  return FLCE_OK;
+}
+
+static flce_status distill_plan(flce_handle_t h, const flce_distill_args* r, Plan* p) {
+  Needs q{};
+  q.stats = q.live = true;
+  q.gradient = r->dx || r->dW;
+  q.z = q.gradient || !is_bf16(h);
+  q.dx = r->dx != nullptr;
+  q.dw_cast = r->dW && r->dw_dtype == FLCE_DTYPE_BF16;
+  return make_plan(h, r->N, r->H, r->V, q, p);
+}
+
+uint64_t flce_distill_workspace_bytes(flce_handle_t h, const flce_distill_args* r) try {
+  if (!h) return 0;
+  h->err.clear();
+  Plan p;
+  if (!r || r->N < 0 || r->H < 1 || r->V < 1 || r->N > kMaxDim || r->H > kMaxDim || r->V > kMaxDim) {
+    fail(h, FLCE_ERR_INVALID_ARG, "null argument or bad size");
+    return 0;
+  }
+  return distill_plan(h, r, &p) == FLCE_OK ? p.total : 0;
+} catch (...) {
+  return 0;
+}
+
+flce_status flce_distill(flce_handle_t h, const flce_distill_args* r, void* workspace, uint64_t workspace_bytes,
+                         void* stream) try {
+  if (!h) return FLCE_ERR_INVALID_ARG;
+  h->err.clear();
+  NvtxRange nvtx("flce_distill");
+  flce_status st = distill_check(h, r);
+  if (st != FLCE_OK) return st;
+  Plan p;
+  st = distill_plan(h, r, &p);
+  if (st == FLCE_OK) st = check_workspace(h, workspace, workspace_bytes, p.total);
+  if (st != FLCE_OK) return st;
+  DeviceGuard guard(h->device);
+  st = ensure_clusters(h);
+  if (st != FLCE_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool bf16 = is_bf16(h);
+  const uint64_t es = bf16 ? 2 : 4, ls = r->logits_dtype == FLCE_DTYPE_FP32 ? 4 : 2;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint32_t* ctrl = reinterpret_cast<uint32_t*>(ws + p.ctrl);
+  uint8_t* live = ws + p.live;
+  st = clear_ctrl(h, ctrl, s);
+  if (st != FLCE_OK) return st;
+  const bool gradient = r->dx || r->dW;
+  const bool cast = r->dW && r->dw_dtype == FLCE_DTYPE_BF16;
+  const float c = static_cast<float>(kLog2e / r->temperature);
+  int32_t claims = 0;
+  if (r->N == 0) {
+    st = zero_dw(h, r->dW, r->dw_dtype, r->V, r->H, s);
+    if (st != FLCE_OK) return st;
+  } else {
+    FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, static_cast<double>(r->N) * r->K * (8 + ls),
+                launch_distill_live(r->ids, r->ld_ids, r->logits, r->ld_logits, r->logits_dtype, r->N, static_cast<int>(r->K),
+                                    r->V, live, ctrl, s));
+  }
+  for (int64_t off = 0; off < r->N; off += p.chunk) {
+    const int rows = static_cast<int>(std::min(p.chunk, r->N - off));
+    const double dr = rows, dV = static_cast<double>(r->V);
+    const void* x = static_cast<const uint8_t*>(r->x) + off * r->H * es;
+    if (gradient) {
+      FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 2.0 * dr * r->H * es,
+                  launch_distill_mask(x, ws + p.xm, live + off, rows, r->H * es, s));
+      x = ws + p.xm;
+    }
+    const Product q{x, r->W, rows, r->H, r->V, &p, c, ctrl};
+    void* z = gradient || !bf16 ? ws + p.z : nullptr;
+    float2* partials = reinterpret_cast<float2*>(ws + p.partials);
+    st = run_stats(h, q, z, partials, reinterpret_cast<float*>(ws + p.part_s), s);
+    if (st != FLCE_OK) return st;
+    DistillArgs a{};
+    a.rows = rows;
+    a.k = static_cast<int>(r->K);
+    a.groups = static_cast<int>(p.groups);
+    a.bf16 = bf16;
+    a.dtype = r->logits_dtype;
+    a.gradient = gradient;
+    a.H = r->H;
+    a.V = r->V;
+    a.ldv = p.ldv;
+    a.ld_ids = r->ld_ids;
+    a.ld_logits = r->ld_logits;
+    a.c = c;
+    a.temperature = r->temperature;
+    a.x = x;
+    a.W = r->W;
+    a.ids = r->ids + off * r->ld_ids;
+    a.logits = static_cast<const uint8_t*>(r->logits) + off * r->ld_logits * ls;
+    a.partials = partials;
+    a.z = z;
+    a.live = live + off;
+    a.token_loss = r->token_loss + off;
+    a.ctrl = ctrl;
+    FLCE_LAUNCH(FLCE_K_DISTILL_ROWS, 0.0,
+                dr * (r->K * (8.0 + ls + static_cast<double>(r->H) * es) + 8.0 * p.groups) + (gradient ? 2.0 * es * dr * dV : 0.0),
+                launch_distill_rows(a, s));
+    if (gradient) {
+      const Backward b{z,
+                       reinterpret_cast<float*>(ws + p.partials),
+                       r->dx ? static_cast<uint8_t*>(r->dx) + off * r->H * es : nullptr,
+                       !r->dW ? nullptr : cast ? reinterpret_cast<float*>(ws + p.dw) : static_cast<float*>(r->dW),
+                       nullptr,
+                       nullptr,
+                       off == 0,
+                       &claims};
+      st = run_backward(h, q, b, s);
+      if (st != FLCE_OK) return st;
+    }
+  }
+  if (cast && r->N > 0)
+    FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 6.0 * r->V * r->H,
+                launch_score_cast(reinterpret_cast<float*>(ws + p.dw), r->dW, r->V * r->H, s));
+  FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 4.0 * r->N,
+              launch_distill_finish(r->token_loss, r->N, ctrl, r->loss, h->host_ctrl + kHostScoreError, s));
+  return FLCE_OK;
+} catch (...) {
+  return FLCE_ERR_BUDGET;
+}
+
+}  // extern "C"

@@ -1,0 +1,474 @@
+// The product z = x Wt of the LM-head operators (flce_score.h) on tcgen05, with
+// what becomes of z in its epilogue: the statistics of each row's softmax and
+// entropy, or the gradient of the logits.
+//
+// 256 x 512 tiles on CTA pairs, as the loss runs them: per 16-deep step two
+// tcgen05.mma.cta_group::2 (M 256, N 256) share A through the collector, a
+// four-stage ring of TMA loads, the 512 accumulator columns filling TMEM. The
+// accumulator is handed back in two halves of 256 columns. Each of the two
+// epilogue warpgroups takes 128 columns of a half into registers (128 of its 224
+// a thread), hands the half back and only then computes: the exponentials of the
+// first half run while the next tile's first products already do, those of the
+// second half under the next tile's main loop. The loss's epilogue rounds z to
+// bf16 to hold a row's 256 columns in registers at once; here every sum is of the
+// fp32 accumulators, since log probabilities are compared with each other.
+//
+// Mathematics. With c = log2(e) / temperature and, per 64 columns, the largest m:
+// y = (z - m) c, and the sums l of 2^y and s of y 2^y give the log-sum-exp and
+// E[y] of the row (joined over the columns by flce_score.cu). The gradient of a
+// row is d = p (a + b log2 p) with p = 2^((z - M) c - log2 L), plus `add` at the
+// target: ScoreRow.
+//
+// What bounds it: the tensor cores (and the power cap) from some 256 rows on,
+// below that the reads of W. The exponentials take 4096 of a tile's cycles at 16 a
+// clock, against some 1060 for each 64 of H.
+//
+// Every wait is bounded (ScoreGemmArgs.timeout_ns); one that runs out records
+// FLCE_ERR_TIMEOUT, the CTA waits for its own loads and products in flight, frees
+// its TMEM and returns.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "flce_internal.h"
+#include "flce_score.h"
+#include "ptx.cuh"
+
+namespace flce {
+namespace {
+
+constexpr int kStages = 4;
+constexpr uint32_t kABytes = kBM * kBK * 2;       // 128 rows of x
+constexpr uint32_t kBBytes = kBN * kBK * 2;       // 256 columns (rows of W)
+constexpr uint32_t kBHalf = kBBytes / 2;
+constexpr uint32_t kStageBytes = kABytes + kBBytes;
+constexpr uint32_t kEpiBytes = 128 * 128;         // 128 rows x 128 bytes
+constexpr uint32_t kSmemBytes = 1024 + kStages * kStageBytes + 2 * kEpiBytes + (2 * kStages + 4) * 8 + 16;
+static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+constexpr uint32_t kTmemCols = 512;
+constexpr int kThreads = 384;
+constexpr int kEpiThreads = 128;
+// registers move from the loading and issuing warpgroup to the two epilogues;
+// the split must fit what the launch holds (checked on the host)
+constexpr uint32_t kRegsCtl = 56, kRegsEpi = 224;
+constexpr int kLaunchRegs = 168;
+static_assert(128 * kRegsCtl + 256 * kRegsEpi <= kThreads * kLaunchRegs, "register split");
+
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// the larger, NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > timeout_ns) return;
+}
+
+// One row of a 128-row x 128-byte staging tile in the 128-byte swizzle
+__device__ __forceinline__ void stage_row(uint8_t* buf, int r, const uint32_t (&w)[32]) {
+  uint4* at = reinterpret_cast<uint4*>(buf + r * 128);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) at[j ^ (r & 7)] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+}
+
+// 64 columns from two 32-register loads
+struct Group {
+  uint32_t (&lo)[32];
+  uint32_t (&hi)[32];
+};
+
+// The statistics of 64 columns of this thread's row, ncv of them valid; with
+// w, y packed as fp16.
+template <bool STORE>
+__device__ __forceinline__ void group_stats(Group g, int ncv, float c, float2* part, float* part_s, bool rvalid,
+                                            uint32_t (&w)[32]) {
+  if (ncv < 64) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (i >= ncv) g.lo[i] = 0xFF800000u;  // -inf: adds nothing
+      if (i + 32 >= ncv) g.hi[i] = 0xFF800000u;
+    }
+  }
+  float m4[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m4[j] = max_nan(__uint_as_float(g.lo[j]), __uint_as_float(g.hi[j]));
+#pragma unroll
+  for (int i = 4; i < 32; ++i)
+    m4[i & 3] = max_nan(m4[i & 3], max_nan(__uint_as_float(g.lo[i]), __uint_as_float(g.hi[i])));
+  const float m = max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3]));
+  float l[4] = {0.f, 0.f, 0.f, 0.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t (&r)[32] = half ? g.hi : g.lo;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float d0 = (__uint_as_float(r[i]) - m) * c, d1 = (__uint_as_float(r[i + 1]) - m) * c;
+      // at -1000 the exponential is 0 and y 2^y is too, which -inf would make NaN
+      const float y0 = max_nan(d0, -1000.f), y1 = max_nan(d1, -1000.f);
+      const float e0 = ex2(y0), e1 = ex2(y1);
+      l[i & 3] += e0;
+      l[(i + 1) & 3] += e1;
+      s[i & 3] = fmaf(y0, e0, s[i & 3]);
+      s[(i + 1) & 3] = fmaf(y1, e1, s[(i + 1) & 3]);
+      if (STORE) {
+        // 11 bits of a distance to the group's largest: what the gradient's
+        // exponentials and the search for alternatives need of it
+        __half2 h = __floats2half2_rn(d0, d1);
+        w[half * 16 + i / 2] = *reinterpret_cast<uint32_t*>(&h);
+      }
+    }
+  }
+  if (rvalid) {
+    *part = make_float2(m, (l[0] + l[1]) + (l[2] + l[3]));
+    *part_s = (s[0] + s[1]) + (s[2] + s[3]);
+  }
+}
+
+// The gradient of 64 columns of this thread's row as bf16; k: the target's
+// column among them, or -1.
+__device__ __forceinline__ void group_gradient(Group g, const ScoreRow& q, float c, int k, float* dcorr, bool rvalid,
+                                               uint32_t (&w)[32]) {
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t (&r)[32] = half ? g.hi : g.lo;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float t = max_nan(fmaf(__uint_as_float(r[i]) - q.largest, c, -q.log2_total), -1000.f);
+      r[i] = __float_as_uint(ex2(t) * fmaf(q.b, t, q.a));
+    }
+  }
+  if (k >= 0) {
+    // the fp32 part of the target's entry that bf16 leaves goes to dx
+    float left = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (i == k) {
+        const float v = __uint_as_float(g.lo[i]) + q.add;
+        g.lo[i] = __float_as_uint(v);
+        left = v - __bfloat162float(__float2bfloat16_rn(v));
+      }
+      if (i + 32 == k) {
+        const float v = __uint_as_float(g.hi[i]) + q.add;
+        g.hi[i] = __float_as_uint(v);
+        left = v - __bfloat162float(__float2bfloat16_rn(v));
+      }
+    }
+    if (rvalid) *dcorr = left;
+  }
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t (&r)[32] = half ? g.hi : g.lo;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+      w[half * 16 + i] = *reinterpret_cast<uint32_t*>(&v);
+    }
+  }
+}
+
+template <int GRADIENT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    score_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmO, const ScoreGemmArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + kStages * kABytes;
+  uint8_t* sE = sB + kStages * kBBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sE + 2 * kEpiBytes);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4);
+
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };
+  const uint32_t tfull_bar = bar0 + 8u * (2 * kStages);
+  const uint32_t tempty0_bar = bar0 + 8u * (2 * kStages + 1);
+  const uint32_t tempty1_bar = bar0 + 8u * (2 * kStages + 2);
+  const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 3);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();  // 0: the CTA that issues the products
+  const int pair = static_cast<int>(cluster_id_x());
+  const int npairs = static_cast<int>(num_clusters_x());
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full_bar(s), 1);   // used in CTA 0: both CTAs' loads land here
+      mbar_init(empty_bar(s), 1);  // each CTA's own, released by the products' commit
+    }
+    mbar_init(tfull_bar, 1);
+    mbar_init(tempty0_bar, 2 * 2 * kEpiThreads);  // used in CTA 0: both CTAs' two epilogues
+    mbar_init(tempty1_bar, 2 * 2 * kEpiThreads);
+    mbar_init(drain_bar, 1);
+    fence_mbar_init();
+    fence_proxy_async_smem();
+    tma_prefetch_map(&tmA);
+    tma_prefetch_map(&tmB);
+    tma_prefetch_map(&tmO);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish_pair();
+  }
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are there before the other uses them
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  // rows fastest: the pairs that run together share columns of W
+  const int units = a.num_m * a.num_n;
+  if (warp < 4) {
+    warpgroup_regs_dec<kRegsCtl>();
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------- loads
+      uint32_t n_issued = 0;
+      bool failed = false;
+      for (int u = pair; u < units && !failed; u += npairs) {
+        const int mA = (u % a.num_m) * 2 * kBM + static_cast<int>(rank) * kBM;
+        const int nB = (u / a.num_m) * 2 * kBN + static_cast<int>(rank) * (kBN / 2);
+        for (int kb = 0; kb < a.kb_total; ++kb) {
+          const uint32_t stage = n_issued % kStages;
+          if (!mbar_wait_bounded_cluster(empty_bar(stage), ((n_issued / kStages) & 1u) ^ 1u, a.ctrl, a.timeout_ns)) {
+            failed = true;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * kStageBytes);
+          const uint32_t fb = mapa_shared(full_bar(stage), 0);
+          const uint32_t sb = smem_u32(sB + stage * kBBytes);
+          tma_load_2d_pair(smem_u32(sA + stage * kABytes), &tmA, fb, kb * kBK, mA);
+          tma_load_2d_pair(sb, &tmB, fb, kb * kBK, nB);
+          tma_load_2d_pair(sb + kBHalf, &tmB, fb, kb * kBK, nB + kBN);
+          ++n_issued;
+        }
+      }
+      if (failed && rank == 0) {
+        const uint32_t first = n_issued > kStages ? n_issued - kStages : 0;
+        for (uint32_t i = first; i < n_issued; ++i) drain_wait(full_bar(i % kStages), (i / kStages) & 1u, a.timeout_ns);
+      }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // ------------------------------------------------------- products
+      constexpr uint32_t idesc = idesc_bf16_f32(2 * kBM, kBN, 0, 0);
+      uint32_t n_consumed = 0;
+      bool issued = false, failed = false;
+      // the four steps of a k-block: both halves sharing A (half < 0), or one half
+      auto products = [&](int stage, int half, bool first) {
+        const uint32_t sa = smem_u32(sA + stage * kABytes);
+        const uint32_t sb = smem_u32(sB + stage * kBBytes);
+#pragma unroll
+        for (int k = 0; k < kBK / 16; ++k) {
+          const uint64_t ad = smem_desc_sw128(sa + 32u * k, 16u, 1024u);
+          const uint64_t bd0 = smem_desc_sw128(sb + 32u * k, 16u, 1024u);
+          const uint64_t bd1 = smem_desc_sw128(sb + kBHalf + 32u * k, 16u, 1024u);
+          const uint32_t add = (!first || k > 0) ? 1u : 0u;
+          if (half < 0) {
+            tc_mma_bf16_pair_a_fill(tmem_base, ad, bd0, idesc, add);
+            tc_mma_bf16_pair_a_lastuse(tmem_base + kBN, ad, bd1, idesc, add);
+          } else {
+            tc_mma_bf16_pair(tmem_base + half * kBN, ad, half ? bd1 : bd0, idesc, add);
+          }
+        }
+      };
+      int it = 0;
+      for (int u = pair; u < units && !failed; u += npairs, ++it) {
+        const uint32_t tph = (it & 1) ^ 1u;
+        if (!mbar_wait_bounded_cluster(tempty0_bar, tph, a.ctrl, a.timeout_ns)) {
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+        // while the second half is still being read, the first half's products
+        // of the k-blocks that are there (their stages stay until the second
+        // half's products have read them too)
+        int ahead = 0;
+        const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+        for (uint32_t spin = 0; !mbar_try_wait_cluster(tempty1_bar, tph); ++spin) {
+          if (ahead < kStages && ahead < a.kb_total) {
+            const uint32_t n = n_consumed + static_cast<uint32_t>(ahead);
+            if (mbar_try_wait_cluster(full_bar(n % kStages), (n / kStages) & 1u)) {
+              tc_fence_after();
+              products(n % kStages, 0, ahead == 0);
+              issued = true;
+              ++ahead;
+              continue;
+            }
+          }
+          if ((spin & 63u) == 0u && (ld_volatile_u32(a.ctrl) != 0u || globaltimer_ns() - t0 > a.timeout_ns)) {
+            atomicCAS(a.ctrl, 0u, kErrTimeout);
+            failed = true;
+            break;
+          }
+        }
+        if (failed) break;
+        tc_fence_after();
+        for (int j = 0; j < ahead; ++j) {
+          const int stage = (n_consumed + static_cast<uint32_t>(j)) % kStages;
+          products(stage, 1, j == 0);
+          tc_commit_pair_multicast(empty_bar(stage), 0x3);
+        }
+        n_consumed += static_cast<uint32_t>(ahead);
+        for (int kb = ahead; kb < a.kb_total; ++kb) {
+          const int stage = n_consumed % kStages;
+          if (!mbar_wait_bounded_cluster(full_bar(stage), (n_consumed / kStages) & 1u, a.ctrl, a.timeout_ns)) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+          products(stage, -1, kb == 0);
+          issued = true;
+          tc_commit_pair_multicast(empty_bar(stage), 0x3);
+          ++n_consumed;
+        }
+        if (failed) break;
+        tc_commit_pair_multicast(tfull_bar, 0x3);
+      }
+      if (failed && issued) {
+        tc_commit_pair(drain_bar);
+        drain_wait(drain_bar, 0, a.timeout_ns);
+      }
+    }
+  } else {
+    warpgroup_regs_inc<kRegsEpi>();
+    // ---------------------------------------------------------- epilogue
+    const int grp = (warp - 4) >> 2;
+    const int wq = warp & 3;               // TMEM lanes 32 wq .. 32 wq + 31
+    const int row = wq * 32 + lane;
+    const bool leader = threadIdx.x == (grp + 1) * kEpiThreads;
+    const uint32_t bar = 1u + static_cast<uint32_t>(grp);
+    uint8_t* buf = sE + grp * kEpiBytes;
+    const float c = a.c;
+    int it = 0;
+    for (int u = pair; u < units; u += npairs, ++it) {
+      const bool ok = mbar_wait_bounded_cluster(tfull_bar, it & 1, a.ctrl, a.timeout_ns);
+      if (named_bar_or(bar, kEpiThreads, !ok)) break;
+      tc_fence_after();
+      const int m0 = (u % a.num_m) * 2 * kBM + static_cast<int>(rank) * kBM;
+      const int n0 = (u / a.num_m) * 2 * kBN;
+      const int grow = m0 + row;
+      const bool rvalid = grow < a.rows;
+      ScoreRow q{0.f, 0.f, 0.f, 0.f, 0.f, -1};
+      if (GRADIENT && rvalid) q = a.row[grow];
+      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(wq * 32) << 16);
+      const size_t prow = static_cast<size_t>(grow) * a.groups;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        const int col = half * kBN + grp * 128;
+        const int c0 = n0 + col;
+        uint32_t r[4][32];
+        if (c0 < a.cols) {  // uniform
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(tbase + col + 32 * i, r[i]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_regs_ready(r[i]);
+        }
+        tc_fence_before();
+        const uint32_t free_bar = half ? tempty1_bar : tempty0_bar;
+        if (rank == 0)
+          mbar_arrive(free_bar);
+        else
+          mbar_arrive_cluster(mapa_shared(free_bar, 0));
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const int cg = c0 + 64 * g;
+          if (cg >= a.cols) continue;  // uniform
+          const Group v{r[2 * g], r[2 * g + 1]};
+          uint32_t w[32];
+          bool store = true;
+          if constexpr (GRADIENT) {
+            const int k = q.target >= cg && q.target < cg + 64 ? q.target - cg : -1;
+            group_gradient(v, q, c, k, a.dcorr + grow, rvalid, w);
+          } else {
+            store = a.store != 0;
+            float2* part = a.partials + prow + cg / 64;
+            float* part_s = a.part_s + prow + cg / 64;
+            if (store)
+              group_stats<true>(v, a.cols - cg, c, part, part_s, rvalid, w);
+            else
+              group_stats<false>(v, a.cols - cg, c, part, part_s, rvalid, w);
+          }
+          if (store) {
+            if (leader) bulk_wait_group_read<0>();
+            named_bar_sync(bar, kEpiThreads);
+            stage_row(buf, row, w);
+            fence_proxy_async_smem();
+            named_bar_sync(bar, kEpiThreads);
+            if (leader) {
+              tma_store_2d(&tmO, smem_u32(buf), cg, m0);
+              bulk_commit_group();
+            }
+            __syncwarp();
+          }
+        }
+      }
+    }
+    if (leader) bulk_wait_group<0>();
+  }
+
+  __syncwarp();
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves while the pair's products may touch its memory
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+template <int GRADIENT>
+cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& to, const ScoreGemmArgs& args,
+                   int pairs, cudaStream_t s) {
+  auto kern = score_gemm_kernel<GRADIENT>;
+  // an increase of registers waits until the block's pool holds them
+  static const bool fits = [](auto k) {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, k) == cudaSuccess &&
+           at.numRegs * kThreads >= static_cast<int>(128 * kRegsCtl + 256 * kRegsEpi);
+  }(kern);
+  if (!fits) return cudaErrorInvalidConfiguration;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
+  if (e != cudaSuccess) return e;
+  kern<<<2 * pairs, kThreads, kSmemBytes, s>>>(ta, tb, to, args);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_score_gemm(int gradient, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
+                              const ScoreGemmArgs& args, int pairs, cudaStream_t s) {
+  return gradient ? launch<1>(a, b, o, args, pairs, s) : launch<0>(a, b, o, args, pairs, s);
+}
+
+int score_gemm_max_clusters() {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaFuncSetAttribute(score_gemm_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(kSmemBytes)) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, score_gemm_kernel<0>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return n;
+}
+
+}  // namespace flce

@@ -28,7 +28,9 @@ KERNEL_KINDS = ["count_valid", "gemm_logits_lse", "lse_combine", "dlogits_inplac
                 "gemm_dlogits_recompute", "gemm_dx", "dx_split_reduce", "gemm_dw",
                 "loss_finalize", "simt_gemm_f32", "simt_tile_stats_f32", "gemm_dx_dw",
                 "device_result", "combine_dlogits", "h2d_copy", "route", "route_finish",
-                "route_backward", "muon_momentum", "muon_prepare", "muon_steps", "muon_small"]
+                "route_backward", "muon_momentum", "muon_prepare", "muon_steps", "muon_small",
+                "score_stats", "score_gradient", "score_rows", "score_dlogits", "score_other",
+                "distill_rows"]
 
 
 class FlceError(RuntimeError):
@@ -92,6 +94,22 @@ class MuonMatrix(ctypes.Structure):
                 ("ld_update", ctypes.c_int64)]
 
 
+class LogprobsArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("W", ctypes.c_void_p), ("t", ctypes.c_void_p), ("N", ctypes.c_int64),
+                ("H", ctypes.c_int64), ("V", ctypes.c_int64), ("ignore_index", ctypes.c_int64),
+                ("temperature", ctypes.c_double), ("top", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("logprobs", ctypes.c_void_p), ("entropy", ctypes.c_void_p), ("stats", ctypes.c_void_p),
+                ("top_logprobs", ctypes.c_void_p), ("top_ids", ctypes.c_void_p), ("kept", ctypes.c_void_p)]
+
+
+class DistillArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("W", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("logits", ctypes.c_void_p),
+                ("N", ctypes.c_int64), ("H", ctypes.c_int64), ("V", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("ld_ids", ctypes.c_int64), ("ld_logits", ctypes.c_int64), ("logits_dtype", ctypes.c_int32),
+                ("dw_dtype", ctypes.c_int32), ("temperature", ctypes.c_double), ("loss", ctypes.c_void_p),
+                ("token_loss", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("dW", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -146,6 +164,12 @@ def load() -> ctypes.CDLL:
                                           u64, u32, vp]),
         "flce_muon_update": (i32, [vp, ctypes.POINTER(MuonArgs), ctypes.POINTER(MuonMatrix), i32, vp,
                                    u64, vp]),
+        "flce_logprobs_kept_bytes": (u64, [vp, i64, i64]),
+        "flce_logprobs_workspace_bytes": (u64, [vp, ctypes.POINTER(LogprobsArgs), i32, i32]),
+        "flce_logprobs_forward": (i32, [vp, ctypes.POINTER(LogprobsArgs), vp, u64, vp]),
+        "flce_logprobs_backward": (i32, [vp, ctypes.POINTER(LogprobsArgs), vp, vp, vp, vp, i32, vp, u64, vp]),
+        "flce_distill_workspace_bytes": (u64, [vp, ctypes.POINTER(DistillArgs)]),
+        "flce_distill": (i32, [vp, ctypes.POINTER(DistillArgs), vp, u64, vp]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(lib, name)
@@ -354,8 +378,9 @@ class FLCE:
 
     def async_status(self) -> None:
         """Wait for the current stream; raise FlceError for a device-side
-        error recorded by forward_backward_async, forward_backward_shard and
-        muon_update calls on this handle since the last check."""
+        error recorded by forward_backward_async, forward_backward_shard,
+        muon_update, token_logprobs and distill calls on this handle since the
+        last check."""
         import torch
         st = self.lib.flce_async_status(self.h, _stream_ptr(torch.device("cuda", self.device)))
         self._check(st, "flce_async_status")
@@ -510,8 +535,8 @@ def cached_handle(device_index: int, dtype: str = "bf16") -> FLCE:
 
 def async_status(device=None) -> None:
     """Wait for the device's current stream; raise FlceError for a device-side
-    error that a call without a handle of its own (muon_update, Muon.step, the
-    autograd functions) recorded since the last check. Such calls do not wait
+    error that a call without a handle of its own (muon_update, Muon.step,
+    token_logprobs, distill, the autograd functions) recorded since the last check. Such calls do not wait
     for their work, so their errors show here, or for an update in the next
     update."""
     import torch
