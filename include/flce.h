@@ -591,8 +591,9 @@ typedef struct flce_logprobs_args {
     int32_t reserved;            /* 0                                                  */
     float* logprobs;             /* device, N (with t)                                 */
     float* entropy;              /* device, N                                          */
-    float* stats;                /* device, N x 2, 8-byte aligned: largest x·Wᵀ of the row,
-                                    log of the sum of exp(z - largest / temperature)   */
+    float* stats;                /* device, N x 2, 8-byte aligned: for the backward (largest
+                                    x·Wᵀ of the row as the product gave it, log of the sum of
+                                    exp relative to it)                                */
     float* top_logprobs;         /* device, N x top                                    */
     int64_t* top_ids;            /* device, N x top                                    */
     void* kept;                  /* device, flce_logprobs_kept_bytes(), 256-byte aligned,

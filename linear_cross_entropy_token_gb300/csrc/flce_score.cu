@@ -9,8 +9,8 @@
 // M and log L are kept apart: one fp32 sum of both would lose log L's last bits
 // where logits are large.
 //
-// A single logit (the given token's, an alternative's, a teacher's entry's) is
-// summed again, in twice the bits of fp32: products of bf16 are exact in fp32 and
+// A single logit (the given token's or an alternative's) is summed again, in twice the
+// bits of fp32: products of bf16 are exact in fp32 and
 // every addition's rounding error is carried along. So equal logits stay equal and
 // the order of near-equal ones does not depend on how the product was tiled.
 #include <cuda_bf16.h>
@@ -42,8 +42,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 // A warp per (row, group): what the product's epilogue does of its accumulators.
 __global__ void __launch_bounds__(256) score_stats_f32_kernel(const float* __restrict__ z, int64_t ldv, int rows, int64_t V,
-                                                              int groups, float c, float2* __restrict__ partials,
-                                                              float* __restrict__ part_s) {
+                                                              int groups, float c, float inv_t,
+                                                              float2* __restrict__ partials, float* __restrict__ part_s) {
   const int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (u >= static_cast<int64_t>(rows) * groups) return;
@@ -55,8 +55,10 @@ __global__ void __launch_bounds__(256) score_stats_f32_kernel(const float* __res
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float y0 = max_nan((z0 - m) * c, -1000.f), y1 = max_nan((z1 - m) * c, -1000.f);
-  const float e0 = exp2f(y0), e1 = exp2f(y1);
+  const float e0 = expf(fmaxf((z0 - m) * inv_t, -700.f)), e1 = expf(fmaxf((z1 - m) * inv_t, -700.f));
+  // a NaN logit made y NaN, which the sum of y e shows
   float l = e0 + e1, s = fmaf(y0, e0, y1 * e1);
+  if (s != s) l = s;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -96,16 +98,62 @@ __device__ __forceinline__ float block_sum(float v, float* s) {
   return v;
 }
 
-// x . w in twice the bits of fp32, the same in all lanes of the warp
-__device__ __forceinline__ void two_sum(float& hi, float& lo, float p) {
-  const float s = __fadd_rn(hi, p);
-  const float b = __fsub_rn(s, hi);
-  lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(p, b)));
-  hi = s;
+// Two fp32 at once (the packed forms issue as one)
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// a - b (the product with -1 is exact)
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %2, %3, %1;" : "=l"(r) : "l"(a), "l"(b), "l"(0xBF800000BF800000ull));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
 }
 
-__device__ __forceinline__ double warp_dot(const __nv_bfloat16* x, const __nv_bfloat16* w, int64_t H, int lane) {
-  float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
+// A sum in twice the bits of fp32: hi is it rounded, lo what that leaves. fp64 would
+// do, at a sixty-fourth of fp32's rate: with it the sums over lanes and the ordering
+// took four fifths of a row's time.
+struct Pair {
+  float hi, lo;
+};
+
+// a + b, and what rounding it leaves
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b);
+  const float u = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, u)), __fsub_rn(b, u))};
+}
+
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  const Pair s = two_sum(a.hi, b.hi);
+  return two_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+
+// the same in all lanes: each step adds the same two numbers on both sides
+__device__ __forceinline__ Pair warp_sum(Pair v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Pair w = {__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)};
+    const bool first = (threadIdx.x & o) == 0;
+    v = add(first ? v : w, first ? w : v);
+  }
+  return v;
+}
+
+// x . w of a row each, by a warp
+__device__ __forceinline__ Pair warp_dot(const __nv_bfloat16* x, const __nv_bfloat16* w, int64_t H, int lane) {
+  uint64_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll 4
   for (int64_t h = lane * 8; h < H; h += 256) {
     const uint4 a = *reinterpret_cast<const uint4*>(x + h);
@@ -113,24 +161,31 @@ __device__ __forceinline__ double warp_dot(const __nv_bfloat16* x, const __nv_bf
     const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      two_sum(hi[i], lo[i], __fmul_rn(__uint_as_float(av[i] << 16), __uint_as_float(bv[i] << 16)));
-      two_sum(hi[i], lo[i], __fmul_rn(__uint_as_float(av[i] & 0xFFFF0000u), __uint_as_float(bv[i] & 0xFFFF0000u)));
+      // exact: eight bits times eight bits
+      const uint64_t p = mul2(pack2(av[i] << 16, av[i] & 0xFFFF0000u), pack2(bv[i] << 16, bv[i] & 0xFFFF0000u));
+      uint64_t& t = hi[i & 1];
+      const uint64_t s = add2(t, p);
+      const uint64_t u = sub2(s, t);
+      lo[i & 1] = add2(lo[i & 1], add2(sub2(t, sub2(s, u)), sub2(p, u)));
+      t = s;
     }
   }
-  double d = 0.0;
+  Pair v[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) d += static_cast<double>(hi[i]) + static_cast<double>(lo[i]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-  return d;
+  for (int i = 0; i < 4; ++i)
+    v[i] = two_sum(__uint_as_float(static_cast<uint32_t>(hi[i >> 1] >> (32 * (i & 1)))),
+                   __uint_as_float(static_cast<uint32_t>(lo[i >> 1] >> (32 * (i & 1)))));
+  return warp_sum(add(add(v[0], v[1]), add(v[2], v[3])));
 }
 
-__device__ __forceinline__ double warp_dot(const float* x, const float* w, int64_t H, int lane) {
-  double d = 0.0;
-  for (int64_t h = lane; h < H; h += 32) d = fma(static_cast<double>(x[h]), static_cast<double>(w[h]), d);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-  return d;
+__device__ __forceinline__ Pair warp_dot(const float* x, const float* w, int64_t H, int lane) {
+  Pair v = {0.f, 0.f};
+  for (int64_t h = lane; h < H; h += 32) {
+    const float p = __fmul_rn(x[h], w[h]), rest = __fmaf_rn(x[h], w[h], -p);
+    const Pair s = two_sum(v.hi, p);
+    v = {s.hi, __fadd_rn(v.lo, __fadd_rn(s.lo, rest))};
+  }
+  return warp_sum(two_sum(v.hi, v.lo));
 }
 
 // A key that orders floats (NaN above all, 0 below every value's)
@@ -140,36 +195,34 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// doubles likewise
-__device__ __forceinline__ uint64_t order_key(double v) {
-  if (v != v) return ~0ull;
-  if (v == 0.0) v = 0.0;  // one zero
-  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v));
-  return (b >> 63) ? ~b : (b | (1ull << 63));
+// Pairs likewise (one zero, in either part)
+__device__ __forceinline__ uint64_t order_key(Pair v) {
+  return (static_cast<uint64_t>(order_key(v.hi + 0.f)) << 32) | order_key(v.lo + 0.f);
 }
 
-constexpr int kRowThreads = 256;
 constexpr int kMaxCandidates = 128;
+constexpr int kMaxGroups = 256;
+static_assert(kScoreMaxTop <= kMaxCandidates, "room for the result");
 constexpr int kMaxValues = kScoreMaxTop * kScoreGroup;
 
+template <int THREADS>
 struct SelectSmem {
   int hist[256];
   int digit, above;
-  int warp_cnt[kRowThreads / 32];
-  int count, ties;
+  int warp_cnt[THREADS / 32];
 };
 
 // The k-th largest of n keys (k <= n) by its bytes from the top; `above` gets how
 // many are larger.
-template <class Key>
-__device__ __forceinline__ uint32_t block_select(int64_t n, int k, SelectSmem& s, int& above, Key&& key) {
+template <int THREADS, class Key>
+__device__ __noinline__ uint32_t block_select(int64_t n, int k, SelectSmem<THREADS>& s, int& above, Key key) {
   uint32_t prefix = 0;
   int rest = k;  // rank among the keys with the prefix
 #pragma unroll 1
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < 256; i += kRowThreads) s.hist[i] = 0;
+    for (int i = threadIdx.x; i < 256; i += THREADS) s.hist[i] = 0;
     __syncthreads();
-    for (int64_t i = threadIdx.x; i < n; i += kRowThreads) {
+    for (int64_t i = threadIdx.x; i < n; i += THREADS) {
       const uint32_t v = key(i);
       if (shift == 24 || (v >> (shift + 8)) == prefix) atomicAdd(&s.hist[(v >> shift) & 255u], 1);
     }
@@ -205,12 +258,12 @@ __device__ __forceinline__ uint32_t block_select(int64_t n, int k, SelectSmem& s
 
 // Positions 0 .. n - 1, in order, that `take` wants (2: always, 1: the first
 // `quota` of them), at most `room`; put(slot, position). Returns how many.
-template <class Take, class Put>
-__device__ __forceinline__ int block_collect(int64_t n, int quota, int room, SelectSmem& s, Take&& take, Put&& put) {
+template <int THREADS, class Take, class Put>
+__device__ __noinline__ int block_collect(int64_t n, int quota, int room, SelectSmem<THREADS>& s, Take take, Put put) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t below = (1u << lane) - 1u;
   int done = 0, tied = 0;
-  for (int64_t base = 0; base < n; base += kRowThreads) {
+  for (int64_t base = 0; base < n; base += THREADS) {
     const int64_t i = base + threadIdx.x;
     const int want = i < n ? take(i) : 0;
     const uint32_t tie = __ballot_sync(0xffffffffu, want == 1);
@@ -218,7 +271,7 @@ __device__ __forceinline__ int block_collect(int64_t n, int quota, int room, Sel
     if (lane == 0) s.warp_cnt[warp] = __popc(tie);
     __syncthreads();
     int rank = tied;
-    for (int w = 0; w < kRowThreads / 32; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
       if (w < warp) rank += s.warp_cnt[w];
       tied += s.warp_cnt[w];
     }
@@ -229,7 +282,7 @@ __device__ __forceinline__ int block_collect(int64_t n, int quota, int room, Sel
     if (lane == 0) s.warp_cnt[warp] = __popc(chosen);
     __syncthreads();
     int slot = done;
-    for (int w = 0; w < kRowThreads / 32; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
       if (w < warp) slot += s.warp_cnt[w];
       done += s.warp_cnt[w];
     }
@@ -242,29 +295,246 @@ __device__ __forceinline__ int block_collect(int64_t n, int quota, int room, Sel
 
 // ------------------------------------------------- log probabilities
 
-// A block per row. The top k logits lie in the k groups with the largest maxima
-// (ties to the lower group: each of those groups holds an element that comes
-// before any of another group). Their stored values, rounded, bound the logits
-// from both sides; whatever may be among the k largest is summed again exactly,
-// with the given token, and ordered by (logit, lowest id).
+// What a block finds the alternatives in
+template <int THREADS>
+struct TopSmem {
+  SelectSmem<THREADS> sel;
+  int group[kMaxGroups];
+  float lower[kMaxCandidates], upper[kMaxCandidates];
+  float value[kMaxValues];           // the careful way's
+  float gmax[kScoreMaxTop];
+  float border;
+  int groups, found, kept;
+};
+
+// A stored value's bounds: half a step of fp16 (with the fp32 steps around it) and
+// the product's own sum; -inf lies below fp16's range.
+template <class Z>
+__device__ __forceinline__ float stored_bound(float v, float gm, float M, float inv_c, float sign) {
+  if (sizeof(Z) == 2 && v == -INFINITY) return sign < 0.f ? v : fmaf(-65500.f, inv_c, gm);
+  float reach = fmaxf(fabsf(M), fabsf(v)) * 6.1e-5f;
+  if (sizeof(Z) == 2) reach = fmaf(gm - v, 5.5e-4f, fmaf(1.2e-7f, inv_c, reach));
+  return reach < INFINITY ? fmaf(sign, reach, v) : v;
+}
+
+// The ids of whatever may be among the row's `top` largest logits, to id, and how
+// many. m: the thread's largest group maximum.
 //
-// Bound by the latency of the selections and of the candidates' rows of W: about
-// k + 1 rows of W a token through L2, beside a product that costs V of them.
-template <class E, class Z, bool TOP>
-__global__ void __launch_bounds__(kRowThreads) score_rows_kernel(const ScoreRowsArgs a) {
-  __shared__ float s_red[kRowThreads / 32];
-  __shared__ SelectSmem s_sel;
-  __shared__ int s_group[kScoreMaxTop];
-  __shared__ float s_value[TOP ? kMaxValues : 1];
-  __shared__ float s_gmax[kScoreMaxTop];
+// The quick way: the top-th largest of the threads' maxima, cut to 20 bits by halving
+// the range with counts, is a border that at least `top` logits reach. Groups whose maximum reaches it, then their columns
+// whose upper bound does, then of those (a few more than `top`) the ones that reach
+// the top-th largest lower bound. Lists are filled in any order: what they hold
+// does not depend on it, and the order of the result comes from the exact logits.
+// Returns -1 where lists overflow (many equal or nearly equal logits) or the row
+// has fewer maxima than `top`, or no finite largest logit.
+template <class Z, int THREADS>
+__device__ __forceinline__ int quick_candidates(const ScoreRowsArgs& a, const float2* part, const Z* z, float m, float M,
+                                                TopSmem<THREADS>& s, int64_t* id) {
+  if (!(fabsf(M) < INFINITY) || a.top > min(a.groups, THREADS)) return -1;  // uniform
+  const uint32_t own = static_cast<int>(threadIdx.x) < a.groups ? order_key(m) : 0u;
+  if (threadIdx.x == 0) s.groups = s.found = s.kept = 0;
+  // to 20 bits of the key, from below
+  uint32_t reached = 0;
+#pragma unroll 1
+  for (uint32_t bit = 1u << 31; bit >= 1u << 12; bit >>= 1)
+    if (__syncthreads_count(own >= (reached | bit)) >= a.top) reached |= bit;
+  const float key_value = __uint_as_float((reached & 0x80000000u) ? reached & 0x7FFFFFFFu : ~reached);
+  const float border = key_value - fmaxf(fabsf(M), fabsf(key_value)) * 6.1e-5f;
+  const float gborder = border - fmaxf(fabsf(M), fabsf(key_value)) * 6.1e-5f;
+  if (m >= gborder)
+    for (int g = threadIdx.x; g < a.groups; g += THREADS)
+      if (part[g].x >= gborder) {
+        const int at = atomicAdd(&s.groups, 1);
+        if (at < kMaxGroups) s.group[at] = g;
+      }
+  __syncthreads();
+  const int ng = s.groups;
+  if (ng > kMaxGroups) return -1;
+  // eight lanes to a group, eight columns to a lane
+  for (int i = threadIdx.x >> 3; i < ng; i += THREADS / 8) {
+    const int64_t j = static_cast<int64_t>(s.group[i]) * kScoreGroup + 8 * (threadIdx.x & 7);
+    const float gm = part[s.group[i]].x;
+    float v[8];
+    if constexpr (sizeof(Z) == 2) {
+      const uint4 y = *reinterpret_cast<const uint4*>(z + j);
+      const uint32_t yv[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&yv[u]));
+        v[2 * u] = fmaf(f.x, a.inv_c, gm);
+        v[2 * u + 1] = fmaf(f.y, a.inv_c, gm);
+      }
+    } else {
+      const float4 f = *reinterpret_cast<const float4*>(z + j), h = *reinterpret_cast<const float4*>(z + j + 4);
+      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w, v[4] = h.x, v[5] = h.y, v[6] = h.z, v[7] = h.w;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (j + u >= a.V) continue;
+      const float upper = stored_bound<Z>(v[u], gm, M, a.inv_c, 1.f);
+      if (upper < border) continue;
+      const int at = atomicAdd(&s.found, 1);
+      if (at < kMaxCandidates) {
+        id[at] = j + u;
+        s.upper[at] = upper;
+        s.lower[at] = stored_bound<Z>(v[u], gm, M, a.inv_c, -1.f);
+      }
+    }
+  }
+  __syncthreads();
+  const int n = s.found;
+  if (n > kMaxCandidates) return -1;
+  const int i = threadIdx.x;
+  float lower = 0.f, upper = 0.f;
+  int64_t own_id = 0;
+  if (i < n) {
+    lower = s.lower[i];
+    upper = s.upper[i];
+    own_id = id[i];
+    int place = 0;
+    for (int j = 0; j < n; ++j) place += s.lower[j] > lower || (s.lower[j] == lower && j < i);
+    if (place == a.top - 1) s.border = lower;
+  }
+  __syncthreads();
+  if (i < n && upper >= s.border) id[atomicAdd(&s.kept, 1)] = own_id;
+  __syncthreads();
+  return s.kept;
+}
+
+// The careful way: the `top` groups with the largest maxima (ties to the lower
+// group: each holds an element that comes before any of another group), in order,
+// and of their columns those whose upper bound reaches the top-th largest lower
+// bound; where those are more than can be summed again, the largest stored values,
+// ties to the lowest id.
+template <class Z, int THREADS>
+__device__ __noinline__ int careful_candidates(const ScoreRowsArgs& a, const float2* part, const Z* z, float M,
+                                               TopSmem<THREADS>& s, int64_t* id) {
+  const int kg = min(a.top, a.groups);
+  int above;
+  const uint32_t gkey = block_select<THREADS>(a.groups, kg, s.sel, above, [&](int64_t g) { return order_key(part[g].x); });
+  block_collect<THREADS>(a.groups, kg - above, kg, s.sel,
+                         [&](int64_t g) {
+                           const uint32_t v = order_key(part[g].x);
+                           return v > gkey ? 2 : (v == gkey ? 1 : 0);
+                         },
+                         [&](int slot, int64_t g) {
+                           s.group[slot] = static_cast<int>(g);
+                           s.gmax[slot] = part[g].x;
+                         });
+  __syncthreads();
+  const int nv = kg * kScoreGroup;
+  auto column = [&](int64_t i) { return static_cast<int64_t>(s.group[i >> 6]) * kScoreGroup + (i & 63); };
+  if (threadIdx.x == 0) s.found = 0;
+  for (int i = threadIdx.x; i < nv; i += THREADS) {
+    const int64_t j = column(i);
+    float v = -INFINITY;
+    if (j < a.V) {
+      if constexpr (sizeof(Z) == 2)
+        v = fmaf(__half2float(z[j]), a.inv_c, s.gmax[i >> 6]);
+      else
+        v = z[j];
+    }
+    s.value[i] = v;
+  }
+  __syncthreads();
+  auto bound = [&](int64_t i, float sign) { return order_key(stored_bound<Z>(s.value[i], s.gmax[i >> 6], M, a.inv_c, sign)); };
+  const uint32_t least =
+      block_select<THREADS>(nv, a.top, s.sel, above, [&](int64_t i) { return column(i) < a.V ? bound(i, -1.f) : 0u; });
+  auto maybe = [&](int64_t i) { return column(i) < a.V && bound(i, 1.f) >= least ? 2 : 0; };
+  auto put = [&](int slot, int64_t i) { id[slot] = column(i); };
+  int many = 0;
+  for (int i = threadIdx.x; i < nv; i += THREADS) many += maybe(i) != 0;
+  if (many) atomicAdd(&s.found, many);
+  __syncthreads();
+  if (s.found <= kMaxCandidates) return block_collect<THREADS>(nv, 0, kMaxCandidates, s.sel, maybe, put);
+  const uint32_t key = block_select<THREADS>(nv, kMaxCandidates, s.sel, above,
+                                             [&](int64_t i) { return column(i) < a.V ? order_key(s.value[i]) : 0u; });
+  return block_collect<THREADS>(nv, kMaxCandidates - above, kMaxCandidates, s.sel,
+                                [&](int64_t i) {
+                                  if (column(i) >= a.V) return 0;
+                                  const uint32_t v = order_key(s.value[i]);
+                                  return v > key ? 2 : (v == key ? 1 : 0);
+                                },
+                                put);
+}
+
+// log p of an exact logit: M is short of what the product lost
+__device__ __forceinline__ float score_log_p(const ScoreRowsArgs& a, Pair z, float M, float log_L) {
+  return fmaf((z.hi - M) + (z.lo - M * a.loss), a.inv_temperature, -log_L);
+}
+
+__device__ __forceinline__ void report(const uint32_t* ctrl, uint32_t* host_error) {
+  const uint32_t code = ld_volatile_u32(ctrl);
+  if (code != 0) *reinterpret_cast<volatile uint32_t*>(host_error) = code;
+}
+
+// Without alternatives: a warp per row, its partials read once for the maximum and
+// again, from L1 or L2, for the sums.
+constexpr int kWarpRows = 4;
+
+template <class E>
+__global__ void __launch_bounds__(32 * kWarpRows) score_warp_rows_kernel(const ScoreRowsArgs a) {
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && threadIdx.x == 0) report(a.ctrl, a.host_error);
+  if (r >= a.rows) return;
+  const int64_t t = a.t ? a.t[r] : -1;
+  if (a.t && t == a.ignore_index) {
+    if (lane == 0) {
+      a.logprobs[r] = 0.f;
+      a.entropy[r] = 0.f;
+      a.stats[r] = make_float2(0.f, 0.f);
+    }
+    return;
+  }
+  const bool bad = a.t && (t < 0 || t >= a.V);
+  const float2* part = a.partials + r * a.groups;
+  const float* part_s = a.part_s + r * a.groups;
+  const float scale = a.scale;
+  float m = -INFINITY;
+#pragma unroll 8
+  for (int g = lane; g < a.groups; g += 32) m = max_nan(m, part[g].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float M = m;
+  float L = 0.f, S = 0.f;
+#pragma unroll 8
+  for (int g = lane; g < a.groups; g += 32) {
+    const float2 p = part[g];
+    const float d = p.x - M, w = expf(max_nan(d * scale, -700.f));
+    L = fmaf(w, p.y, L);
+    S = fmaf(w, fmaf(max_nan(d * a.c, -1000.f), p.y, part_s[g]), S);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    L += __shfl_xor_sync(0xffffffffu, L, o);
+    S += __shfl_xor_sync(0xffffffffu, S, o);
+  }
+  const float log_L = logf(L);
+  Pair z = {0.f, 0.f};
+  if (a.t && !bad)
+    z = warp_dot(static_cast<const E*>(a.x) + r * a.H, static_cast<const E*>(a.W) + t * a.H, a.H, lane);
+  if (lane != 0) return;
+  if (a.t) a.logprobs[r] = bad ? NAN : score_log_p(a, z, M, log_L);
+  a.entropy[r] = log_L - kLn2 * S / L;
+  a.stats[r] = make_float2(M, log_L);
+  if (bad) *reinterpret_cast<volatile uint32_t*>(a.host_error) = kErrBadTarget;
+}
+
+// A block per row. Whatever may be among the row's largest logits is summed again
+// exactly, with the given token, and ordered by (logit, lowest id).
+//
+// Bound by latency: the statistics' sums, the search's steps, and the candidates'
+// rows of W (top + 1 of them and a few), beside a product that reads V of them.
+template <class E, class Z, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) score_rows_kernel(const ScoreRowsArgs a) {
+  __shared__ float s_red[THREADS / 32];
   __shared__ int64_t s_id[kMaxCandidates];
-  __shared__ double s_dot[kMaxCandidates + 1];
+  __shared__ Pair s_dot[kMaxCandidates + 1];
+  __shared__ TopSmem<THREADS> s_top;
   const int64_t r = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (r == 0 && threadIdx.x == 0) {
-    const uint32_t code = ld_volatile_u32(a.ctrl);
-    if (code != 0) *reinterpret_cast<volatile uint32_t*>(a.host_error) = code;
-  }
+  if (r == 0 && threadIdx.x == 0) report(a.ctrl, a.host_error);
   const int64_t t = a.t ? a.t[r] : -1;
   if (a.t && t == a.ignore_index) {
     if (threadIdx.x == 0) {
@@ -272,7 +542,7 @@ __global__ void __launch_bounds__(kRowThreads) score_rows_kernel(const ScoreRows
       a.entropy[r] = 0.f;
       a.stats[r] = make_float2(0.f, 0.f);
     }
-    if (TOP && threadIdx.x < a.top) {
+    if (threadIdx.x < a.top) {
       a.top_logprobs[r * a.top + threadIdx.x] = 0.f;
       a.top_ids[r * a.top + threadIdx.x] = -1;
     }
@@ -282,111 +552,51 @@ __global__ void __launch_bounds__(kRowThreads) score_rows_kernel(const ScoreRows
   const float2* part = a.partials + r * a.groups;
   const float* part_s = a.part_s + r * a.groups;
   float m = -INFINITY;
-  for (int g = threadIdx.x; g < a.groups; g += kRowThreads) m = max_nan(m, part[g].x);
-  const float M = block_max<kRowThreads>(m, s_red);
+  for (int g = threadIdx.x; g < a.groups; g += THREADS) m = max_nan(m, part[g].x);
+  const float M = block_max<THREADS>(m, s_red);
+  const float scale = a.scale;
   float L = 0.f, S = 0.f;
-  for (int g = threadIdx.x; g < a.groups; g += kRowThreads) {
+  for (int g = threadIdx.x; g < a.groups; g += THREADS) {
     const float2 p = part[g];
-    const float d = max_nan((p.x - M) * a.c, -1000.f), w = ex2(d);
+    const float d = p.x - M, w = expf(max_nan(d * scale, -700.f));
     L = fmaf(w, p.y, L);
-    S = fmaf(w, fmaf(d, p.y, part_s[g]), S);
+    S = fmaf(w, fmaf(max_nan(d * a.c, -1000.f), p.y, part_s[g]), S);
   }
-  L = block_sum<kRowThreads>(L, s_red);
-  S = block_sum<kRowThreads>(S, s_red);
+  L = block_sum<THREADS>(L, s_red);
+  S = block_sum<THREADS>(S, s_red);
   const float log_L = logf(L);
   const E* x = static_cast<const E*>(a.x) + r * a.H;
   const E* W = static_cast<const E*>(a.W);
 
-  int n = 0;
-  if constexpr (TOP) {
-    const int kg = min(a.top, a.groups);
-    int above;
-    const uint32_t gkey = block_select(a.groups, kg, s_sel, above, [&](int64_t g) { return order_key(part[g].x); });
-    block_collect(a.groups, kg - above, kg, s_sel,
-                  [&](int64_t g) {
-                    const uint32_t v = order_key(part[g].x);
-                    return v > gkey ? 2 : (v == gkey ? 1 : 0);
-                  },
-                  [&](int slot, int64_t g) {
-                    s_group[slot] = static_cast<int>(g);
-                    s_gmax[slot] = part[g].x;
-                  });
+  const Z* z = static_cast<const Z*>(a.z) + r * a.ldv;
+  int n = quick_candidates<Z, THREADS>(a, part, z, m, M, s_top, s_id);
+  if (n < 0) {
     __syncthreads();
-    const int nv = kg * kScoreGroup;
-    const Z* z = static_cast<const Z*>(a.z) + r * a.ldv;
-    for (int i = threadIdx.x; i < nv; i += kRowThreads) {
-      const int64_t j = static_cast<int64_t>(s_group[i >> 6]) * kScoreGroup + (i & 63);
-      float v = -INFINITY;
-      if (j < a.V) {
-        if constexpr (sizeof(Z) == 2)
-          v = fmaf(__half2float(z[j]), a.inv_c, s_gmax[i >> 6]);
-        else
-          v = z[j];
-      }
-      s_value[i] = v;
-    }
-    __syncthreads();
-    // a stored value's bounds: half a step of fp16 (with the fp32 steps around it)
-    // and the product's own sum; -inf lies below fp16's range
-    auto bound = [&](int i, float sign) {
-      const float gm = s_gmax[i >> 6], v = s_value[i];
-      if (sizeof(Z) == 2 && v == -INFINITY) return sign < 0.f ? v : fmaf(-65500.f, a.inv_c, gm);
-      float reach = fmaxf(fabsf(M), fabsf(v)) * 6.1e-5f;
-      if (sizeof(Z) == 2) reach = fmaf(gm - v, 5.5e-4f, fmaf(1.2e-7f, a.inv_c, reach));
-      return reach < INFINITY ? fmaf(sign, reach, v) : v;
-    };
-    auto there = [&](int i) { return static_cast<int64_t>(s_group[i >> 6]) * kScoreGroup + (i & 63) < a.V; };
-    const uint32_t least =
-        block_select(nv, a.top, s_sel, above, [&](int64_t i) { return there(i) ? order_key(bound(static_cast<int>(i), -1.f)) : 0u; });
-    auto maybe = [&](int64_t i) { return there(i) && order_key(bound(static_cast<int>(i), 1.f)) >= least ? 2 : 0; };
-    auto put = [&](int slot, int64_t i) { s_id[slot] = static_cast<int64_t>(s_group[i >> 6]) * kScoreGroup + (i & 63); };
-    int many = 0;
-    for (int i = threadIdx.x; i < nv; i += kRowThreads) many += maybe(i) != 0;
-    many = static_cast<int>(block_sum<kRowThreads>(static_cast<float>(many), s_red));
-    if (many <= kMaxCandidates) {
-      n = block_collect(nv, 0, kMaxCandidates, s_sel, maybe, put);
-    } else {
-      // more than can be summed again (nearly equal logits): the largest stored
-      // ones, ties to the lowest id
-      const uint32_t key = block_select(nv, kMaxCandidates, s_sel, above,
-                                        [&](int64_t i) { return there(i) ? order_key(s_value[i]) : 0u; });
-      n = block_collect(nv, kMaxCandidates - above, kMaxCandidates, s_sel,
-                        [&](int64_t i) {
-                          if (!there(i)) return 0;
-                          const uint32_t v = order_key(s_value[i]);
-                          return v > key ? 2 : (v == key ? 1 : 0);
-                        },
-                        put);
-    }
-    __syncthreads();
+    n = careful_candidates<Z, THREADS>(a, part, z, M, s_top, s_id);
   }
+  __syncthreads();
   // the given token's logit behind the candidates'
   const int dots = n + (a.t && !bad ? 1 : 0);
-  for (int i = warp; i < dots; i += kRowThreads / 32) {
-    const double d = warp_dot(x, W + (i < n ? s_id[i] : t) * a.H, a.H, lane);
+  for (int i = warp; i < dots; i += THREADS / 32) {
+    const Pair d = warp_dot(x, W + (i < n ? s_id[i] : t) * a.H, a.H, lane);
     if (lane == 0) s_dot[i] = d;
   }
   __syncthreads();
-  auto log_p = [&](double z) {
-    return static_cast<float>((z - static_cast<double>(M)) * a.inv_temperature - static_cast<double>(log_L));
-  };
-  if constexpr (TOP) {
-    if (threadIdx.x < n) {
-      const uint64_t own = order_key(s_dot[threadIdx.x]);
-      const int64_t id = s_id[threadIdx.x];
-      int rank = 0;
-      for (int i = 0; i < n; ++i) {
-        const uint64_t v = order_key(s_dot[i]);
-        rank += v > own || (v == own && s_id[i] < id);
-      }
-      if (rank < a.top) {
-        a.top_logprobs[r * a.top + rank] = log_p(s_dot[threadIdx.x]);
-        a.top_ids[r * a.top + rank] = id;
-      }
+  if (threadIdx.x < n) {
+    const uint64_t own = order_key(s_dot[threadIdx.x]);
+    const int64_t id = s_id[threadIdx.x];
+    int rank = 0;
+    for (int i = 0; i < n; ++i) {
+      const uint64_t v = order_key(s_dot[i]);
+      rank += v > own || (v == own && s_id[i] < id);
+    }
+    if (rank < a.top) {
+      a.top_logprobs[r * a.top + rank] = score_log_p(a, s_dot[threadIdx.x], M, log_L);
+      a.top_ids[r * a.top + rank] = id;
     }
   }
   if (threadIdx.x == 0) {
-    if (a.t) a.logprobs[r] = bad ? NAN : log_p(s_dot[n]);
+    if (a.t) a.logprobs[r] = bad ? NAN : score_log_p(a, s_dot[n], M, log_L);
     a.entropy[r] = log_L - kLn2 * S / L;
     a.stats[r] = make_float2(M, log_L);
     if (bad) *reinterpret_cast<volatile uint32_t*>(a.host_error) = kErrBadTarget;
@@ -395,9 +605,10 @@ __global__ void __launch_bounds__(kRowThreads) score_rows_kernel(const ScoreRows
 
 // ------------------------------------------------------------ gradients
 
-// Copies 16-byte pieces, or 4-byte ones where a row is not made of those
+// Copies 16-byte pieces, or 4-byte ones where rows are not made of those (fp32 x may
+// start at any element)
 __device__ __forceinline__ void copy_row(const uint8_t* from, uint8_t* to, int64_t bytes, bool live) {
-  if (bytes % 16 == 0) {
+  if ((reinterpret_cast<uint64_t>(from) | reinterpret_cast<uint64_t>(to) | static_cast<uint64_t>(bytes)) % 16 == 0) {
     for (int64_t i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16)
       *reinterpret_cast<uint4*>(to + i) = live ? *reinterpret_cast<const uint4*>(from + i) : make_uint4(0, 0, 0, 0);
   } else {
@@ -416,14 +627,15 @@ __global__ void __launch_bounds__(128) score_prepare_kernel(const ScorePrepareAr
   const bool live = !ignored && !bad;
   if (threadIdx.x == 0) {
     if (bad) atomicCAS(a.ctrl, 0u, kErrBadTarget);
-    ScoreRow q{0.f, 0.f, 0.f, 0.f, 0.f, -1};
+    ScoreRow q{0.f, 0.f, 0.f, 0.f, 0.f, -1, 0.f};
     if (live) {
       const float2 st = a.stats[r];
-      const float inv = static_cast<float>(1.0 / a.temperature);
+      const float inv = a.inv_temperature;
       const float g = a.d_logprobs ? a.d_logprobs[r] : 0.f;
       const float h = a.d_entropy ? a.d_entropy[r] : 0.f;
       q.largest = st.x;
       q.log2_total = st.y * kLog2e;
+      q.inv_total = expf(-st.y);
       q.a = -inv * (a.d_entropy ? fmaf(h, a.entropy[r], g) : g);
       q.b = -inv * h * kLn2;
       q.add = inv * g;
@@ -468,13 +680,16 @@ __device__ __forceinline__ void dlogits8(const __half* z, __nv_bfloat16* d, int6
   *reinterpret_cast<uint4*>(d + j) = make_uint4(ov[0], ov[1], ov[2], ov[3]);
 }
 
-__device__ __forceinline__ void dlogits4(const float* z, float* d, int64_t j, int64_t V, float c, const ScoreRow& q) {
+// fp32: p from the natural exponential, whose argument has no factor to round
+__device__ __forceinline__ void dlogits4(const float* z, float* d, int64_t j, int64_t V, float c, float inv_t,
+                                         const ScoreRow& q) {
   const float4 in = *reinterpret_cast<const float4*>(z + j);
   float v[4] = {in.x, in.y, in.z, in.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float t = max_nan(fmaf(v[i] - q.largest, c, -q.log2_total), -1000.f);
-    v[i] = j + i < V ? exp2f(t) * fmaf(q.b, t, q.a) : 0.f;
+    const float u = v[i] - q.largest;
+    const float t = max_nan(fmaf(u, c, -q.log2_total), -1000.f);
+    v[i] = j + i < V ? expf(max_nan(u * inv_t, -700.f)) * q.inv_total * fmaf(q.b, t, q.a) : 0.f;
     if (j + i == q.target) v[i] += q.add;
   }
   *reinterpret_cast<float4*>(d + j) = make_float4(v[0], v[1], v[2], v[3]);
@@ -498,7 +713,7 @@ __global__ void __launch_bounds__(kDlogitsThreads) score_dlogits_bf16_kernel(
 }
 
 __global__ void __launch_bounds__(kDlogitsThreads) score_dlogits_f32_kernel(const float* z, float* d, int64_t ldv, int64_t V,
-                                                                           float c, const ScoreRow* __restrict__ row) {
+                                                                           float c, float inv_t, const ScoreRow* __restrict__ row) {
   const int64_t r = blockIdx.x;
   const ScoreRow q = row[r];
   const int64_t j = (static_cast<int64_t>(blockIdx.y) * kDlogitsThreads + threadIdx.x) * 4;
@@ -507,7 +722,7 @@ __global__ void __launch_bounds__(kDlogitsThreads) score_dlogits_f32_kernel(cons
     *reinterpret_cast<float4*>(d + r * ldv + j) = make_float4(0.f, 0.f, 0.f, 0.f);
     return;
   }
-  dlogits4(z + r * ldv, d + r * ldv, j, V, c, q);
+  dlogits4(z + r * ldv, d + r * ldv, j, V, c, inv_t, q);
 }
 
 // dx: the sum of the splits in their order, with the target's entry put right,
@@ -546,7 +761,7 @@ __global__ void __launch_bounds__(256) score_cast_kernel(const float4* __restric
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (i >= n8) return;
   const float4 a = __ldcs(in + 2 * i), b = __ldcs(in + 2 * i + 1);
-  __nv_bfloat162 v[4] = {__floats2bfloat162_rn(a.x, a.y), __floats2bfloat162_rn(a.z, a.w), __floats2bfloat162_rn(b.x, b.y),
+  alignas(16) __nv_bfloat162 v[4] = {__floats2bfloat162_rn(a.x, a.y), __floats2bfloat162_rn(a.z, a.w), __floats2bfloat162_rn(b.x, b.y),
                          __floats2bfloat162_rn(b.z, b.w)};
   __stcs(out + i, *reinterpret_cast<uint4*>(v));
 }
@@ -598,10 +813,58 @@ __global__ void __launch_bounds__(256) distill_live_kernel(const int64_t* __rest
   }
 }
 
-__global__ void __launch_bounds__(128) distill_mask_kernel(const uint8_t* __restrict__ x, uint8_t* __restrict__ xm,
-                                                           const uint8_t* __restrict__ live, int64_t row_bytes) {
+// A block per row. The entries that count are put in order of their ids (those that
+// share one, of their slots) by counting the ones before each.
+constexpr int kPrepareThreads = 128;
+
+__global__ void __launch_bounds__(kPrepareThreads) distill_prepare_kernel(const DistillPrepareArgs a) {
+  __shared__ int s_id[kScoreMaxTeacher], s_sorted[kScoreMaxTeacher];
   const int64_t r = blockIdx.x;
-  copy_row(x + r * row_bytes, xm + r * row_bytes, row_bytes, live[r] != 0);
+  const bool live = a.live[r] != 0;
+  if (a.xm)
+    copy_row(static_cast<const uint8_t*>(a.x) + r * a.row_bytes, static_cast<uint8_t*>(a.xm) + r * a.row_bytes, a.row_bytes,
+             live);
+  if (!a.parts) return;
+  uint2* parts = a.parts + r * a.num_tiles;
+  if (!live) {
+    for (int w = threadIdx.x; w < a.num_tiles; w += kPrepareThreads) parts[w] = make_uint2(0u, 0u);
+    return;
+  }
+  constexpr int kNone = 0x7FFFFFFF;
+  for (int e = threadIdx.x; e < a.k; e += kPrepareThreads) {
+    const int64_t id = a.ids[r * a.ld_ids + e];
+    s_id[e] = teacher_there(id, teacher_logit(a.logits, r * a.ld_logits + e, a.dtype)) ? static_cast<int>(id) : kNone;
+    s_sorted[e] = kNone;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.k; e += kPrepareThreads) {
+    const int id = s_id[e];
+    if (id == kNone) continue;
+    int place = 0;
+    for (int i = 0; i < a.k; ++i) place += s_id[i] < id || (s_id[i] == id && i < e);
+    s_sorted[place] = id;
+    a.entries[r * a.k + place] = make_int2(id, e);
+  }
+  __syncthreads();
+  for (int w = threadIdx.x; w < a.num_tiles; w += kPrepareThreads) {
+    uint64_t at = 0;
+    int lo = 0;
+#pragma unroll 1
+    for (int j = 0; j <= 4; ++j) {
+      // the first entry that is not before the part
+      const int64_t from = static_cast<int64_t>(w) * kScoreTileColumns + j * kScorePart;
+      int hi = a.k;
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (s_sorted[mid] < from)
+          lo = mid + 1;
+        else
+          hi = mid;
+      }
+      at |= static_cast<uint64_t>(lo) << (9 * j);
+    }
+    parts[w] = make_uint2(static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32));
+  }
 }
 
 constexpr int kDistillThreads = 512;
@@ -609,17 +872,16 @@ constexpr int kDistillThreads = 512;
 // A block per row: the row's log-sum-exp from its groups, the entries' logits, the
 // loss T^2 sum_e q_e (log q_e - log p_e), and with the gradient the row of stored
 // logits overwritten by d = (T / n) (p - q), first everywhere, then at the entries
-// (from their exact logits; entries that share an id add up).
-// Bound by the stored logits' way through HBM (2 bytes read, 2 written a logit) and,
-// where there are many entries, by their rows of W through L2.
+// (from their unrounded logits; entries that share an id add up). The entries'
+// logits are the product's fp32 sums, which its epilogue picked: summing them again
+// took a row of W each, 1.2 ms of a 4096-token chunk at 64 entries instead of 0.4.
+// Bound by the stored logits' way through HBM (2 bytes read, 2 written a logit).
 template <class E, bool GRADIENT>
 __global__ void __launch_bounds__(kDistillThreads) distill_rows_kernel(const DistillArgs a) {
   __shared__ float s_red[kDistillThreads / 32];
-  __shared__ double s_z[kScoreMaxTeacher];
   __shared__ int64_t s_id[kScoreMaxTeacher];
   __shared__ float s_q[kScoreMaxTeacher];
   const int64_t r = blockIdx.x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr bool bf16 = sizeof(E) == 2;
   constexpr int kVec = bf16 ? 8 : 4;
   uint8_t* zrow = static_cast<uint8_t*>(a.z) + r * a.ldv * sizeof(E);
@@ -641,24 +903,19 @@ __global__ void __launch_bounds__(kDistillThreads) distill_rows_kernel(const Dis
     if (there) top = max_nan(top, v);
   }
   top = block_max<kDistillThreads>(top, s_red);
-  const E* x = static_cast<const E*>(a.x) + r * a.H;
-  for (int e = warp; e < a.k; e += kDistillThreads / 32)
-    if (s_id[e] >= 0) {
-      const double d = warp_dot(x, static_cast<const E*>(a.W) + s_id[e] * a.H, a.H, lane);
-      if (lane == 0) s_z[e] = d;
-    }
   const float2* part = a.partials + r * a.groups;
   float m = -INFINITY;
   for (int g = threadIdx.x; g < a.groups; g += kDistillThreads) m = max_nan(m, part[g].x);
   const float M = block_max<kDistillThreads>(m, s_red);
+  const float scale = a.scale;
   float L = 0.f;
   for (int g = threadIdx.x; g < a.groups; g += kDistillThreads) {
     const float2 p = part[g];
-    L = fmaf(ex2(max_nan((p.x - M) * a.c, -1000.f)), p.y, L);
+    L = fmaf(expf(max_nan((p.x - M) * scale, -700.f)), p.y, L);
   }
   L = block_sum<kDistillThreads>(L, s_red);
   const float log_L = logf(L);
-  const float inv = static_cast<float>(1.0 / a.temperature);
+  const float inv = a.inv_temperature;
   float q = 0.f;
   const int e = threadIdx.x;  // k <= kScoreMaxTeacher <= kDistillThreads
   const bool there = e < a.k && s_id[e] >= 0;
@@ -668,29 +925,30 @@ __global__ void __launch_bounds__(kDistillThreads) distill_rows_kernel(const Dis
   q /= total;
   float log_p = 0.f, term = 0.f;
   if (there) {
-    log_p = static_cast<float>((s_z[e] - static_cast<double>(M)) / a.temperature - static_cast<double>(log_L));
+    const float z = bf16 ? a.picked[r * a.k + e] : reinterpret_cast<const float*>(zrow)[s_id[e]];
+    log_p = fmaf(z - M, scale, -log_L);
     term = q > 0.f || q != q ? q * (rel - logf(total) - log_p) : 0.f;
     s_q[e] = q;
   }
   term = block_sum<kDistillThreads>(term, s_red);
-  if (threadIdx.x == 0) a.token_loss[r] = static_cast<float>(a.temperature * a.temperature) * term;
+  if (threadIdx.x == 0) a.token_loss[r] = a.temperature * a.temperature * term;
   if constexpr (GRADIENT) {
-    const float scale = static_cast<float>(a.temperature / static_cast<double>(a.ctrl[kCtrlNValid]));
-    ScoreRow row{M, log_L * kLog2e, scale, 0.f, 0.f, -1};
+    const float factor = a.temperature / static_cast<float>(a.ctrl[kCtrlNValid]);
+    ScoreRow row{M, log_L * kLog2e, factor, 0.f, 0.f, -1, expf(-log_L)};
     if (!(fabsf(row.log2_total) < INFINITY) || !(fabsf(M) < INFINITY)) row.a = NAN;
     for (int64_t j = threadIdx.x * kVec; j < a.ldv; j += kDistillThreads * kVec) {
       if constexpr (bf16)
         dlogits8(reinterpret_cast<const __half*>(zrow), reinterpret_cast<__nv_bfloat16*>(zrow), j, a.V,
                  part[j / kScoreGroup].x, a.c, row, nullptr);
       else
-        dlogits4(reinterpret_cast<const float*>(zrow), reinterpret_cast<float*>(zrow), j, a.V, a.c, row);
+        dlogits4(reinterpret_cast<const float*>(zrow), reinterpret_cast<float*>(zrow), j, a.V, a.c, inv, row);
     }
     __syncthreads();
     if (there) {
       float all = 0.f;
       for (int i = 0; i < a.k; ++i)
         if (s_id[i] == s_id[e]) all += s_q[i];
-      const float d = scale * (expf(log_p) - all);
+      const float d = factor * (expf(log_p) - all);
       if constexpr (bf16)
         reinterpret_cast<__nv_bfloat16*>(zrow)[s_id[e]] = __float2bfloat16_rn(d);
       else
@@ -701,39 +959,45 @@ __global__ void __launch_bounds__(kDistillThreads) distill_rows_kernel(const Dis
 
 __global__ void __launch_bounds__(1024) distill_finish_kernel(const float* __restrict__ token_loss, int64_t N,
                                                               const uint32_t* ctrl, float* loss, uint32_t* host_error) {
-  __shared__ double s_sum[32];
-  double s = 0.0;
-  for (int64_t i = threadIdx.x; i < N; i += 1024) s += static_cast<double>(token_loss[i]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = s;
+  __shared__ Pair s_sum[32];
+  Pair v = {0.f, 0.f};
+  for (int64_t i = threadIdx.x; i < N; i += 1024) v = add(v, {token_loss[i], 0.f});
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = v;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    s = 0.0;
-    for (int w = 0; w < 32; ++w) s += s_sum[w];
-    const uint32_t n = ctrl[kCtrlNValid], code = ctrl[kCtrlError];
-    *loss = code != 0 ? NAN : (n > 0 ? static_cast<float>(s / static_cast<double>(n)) : 0.f);
-    if (code != 0) *reinterpret_cast<volatile uint32_t*>(host_error) = code;
+  if (threadIdx.x < 32) {
+    v = warp_sum(s_sum[threadIdx.x]);
+    if (threadIdx.x == 0) {
+      const uint32_t n = ctrl[kCtrlNValid], code = ctrl[kCtrlError];
+      *loss = code != 0 ? NAN : (n > 0 ? v.hi / static_cast<float>(n) : 0.f);
+      if (code != 0) *reinterpret_cast<volatile uint32_t*>(host_error) = code;
+    }
   }
 }
 
-template <class E, class Z>
-cudaError_t launch_rows(const ScoreRowsArgs& a, cudaStream_t s) {
-  if (a.top > 0)
-    score_rows_kernel<E, Z, true><<<a.rows, kRowThreads, 0, s>>>(a);
-  else
-    score_rows_kernel<E, Z, false><<<a.rows, kRowThreads, 0, s>>>(a);
-  return cudaGetLastError();
-}
+// With few rows a row's latency counts, and large blocks take its candidates at
+// once; with many, eight blocks of 128 threads share an SM.
+constexpr int kFewRows = 304;
 
 unsigned blocks_of(int64_t n, int64_t per) { return static_cast<unsigned>((n + per - 1) / per); }
 
+template <class E, class Z>
+cudaError_t launch_rows(const ScoreRowsArgs& a, cudaStream_t s) {
+  if (a.top == 0)
+    score_warp_rows_kernel<E><<<blocks_of(a.rows, kWarpRows), 32 * kWarpRows, 0, s>>>(a);
+  else if (a.rows <= kFewRows)
+    score_rows_kernel<E, Z, 1024><<<a.rows, 1024, 0, s>>>(a);
+  else
+    score_rows_kernel<E, Z, 128><<<a.rows, 128, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
-cudaError_t launch_score_stats_f32(const float* z, int64_t ldv, int rows, int64_t V, int groups, float c, float2* partials,
-                                   float* part_s, cudaStream_t s) {
+cudaError_t launch_score_stats_f32(const float* z, int64_t ldv, int rows, int64_t V, int groups, float c, float inv_temperature,
+                                   float2* partials, float* part_s, cudaStream_t s) {
   score_stats_f32_kernel<<<blocks_of(static_cast<int64_t>(rows) * groups, 8), 256, 0, s>>>(z, ldv, rows, V, groups, c,
-                                                                                         partials, part_s);
+                                                                                         inv_temperature, partials, part_s);
   return cudaGetLastError();
 }
 
@@ -747,14 +1011,14 @@ cudaError_t launch_score_prepare(const ScorePrepareArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_score_dlogits(int bf16, const void* z, const float2* partials, int groups, void* d, int64_t ldv, int rows,
-                                 int64_t V, float c, const ScoreRow* row, float* dcorr, cudaStream_t s) {
+                                 int64_t V, float c, float inv_temperature, const ScoreRow* row, float* dcorr, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(rows), blocks_of(ldv, kDlogitsThreads * (bf16 ? 8 : 4)));
   if (bf16)
     score_dlogits_bf16_kernel<<<grid, kDlogitsThreads, 0, s>>>(static_cast<const __half*>(z), partials, groups,
                                                               static_cast<__nv_bfloat16*>(d), ldv, V, c, row, dcorr);
   else
     score_dlogits_f32_kernel<<<grid, kDlogitsThreads, 0, s>>>(static_cast<const float*>(z), static_cast<float*>(d), ldv, V, c,
-                                                             row);
+                                                             inv_temperature, row);
   return cudaGetLastError();
 }
 
@@ -796,8 +1060,8 @@ cudaError_t launch_distill_live(const int64_t* ids, int64_t ld_ids, const void* 
   return cudaGetLastError();
 }
 
-cudaError_t launch_distill_mask(const void* x, void* xm, const uint8_t* live, int rows, int64_t row_bytes, cudaStream_t s) {
-  distill_mask_kernel<<<rows, 128, 0, s>>>(static_cast<const uint8_t*>(x), static_cast<uint8_t*>(xm), live, row_bytes);
+cudaError_t launch_distill_prepare(const DistillPrepareArgs& a, cudaStream_t s) {
+  distill_prepare_kernel<<<a.rows, kPrepareThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 

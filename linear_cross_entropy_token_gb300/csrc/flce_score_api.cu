@@ -39,11 +39,13 @@ Kept kept_layout(bool bf16, int64_t N, int64_t V) {
 struct Plan {
   int64_t chunk = 0, ldv = 0, groups = 0, splits = 1;
   int64_t tile_n_dx = 0, tile_n_dw = 0;  // columns of the backward products' tiles
-  uint64_t ctrl = 0, z = 0, partials = 0, part_s = 0, row = 0, dcorr = 0, xm = 0, live = 0, dw = 0, total = 0;
+  uint64_t ctrl = 0, z = 0, partials = 0, part_s = 0, row = 0, dcorr = 0, xm = 0, live = 0, parts = 0, entries = 0,
+           picked = 0, dw = 0, total = 0;
 };
 
 struct Needs {
-  bool z, stats, gradient, dx, dw_cast, live;
+  bool z, stats, gradient, dx, dw_cast;
+  int64_t teacher;  // entries a row
 };
 
 // Gradients: chunks, tile shapes and splits are the loss's plan with both
@@ -99,7 +101,14 @@ flce_status make_plan(flce_handle_t h, int64_t N, int64_t H, int64_t V, const Ne
     p.xm = take(c * H * es);
     if (q.dw_cast) p.dw = take(static_cast<uint64_t>(V) * H * 4);
   }
-  if (q.live) p.live = take(static_cast<uint64_t>(std::max<int64_t>(N, 1)));
+  if (q.teacher) {
+    p.live = take(static_cast<uint64_t>(std::max<int64_t>(N, 1)));
+    if (bf16) {
+      p.parts = take(c * cdiv(V, kScoreTileColumns) * sizeof(uint2));
+      p.entries = take(c * q.teacher * sizeof(int2));
+      p.picked = take(c * q.teacher * 4);
+    }
+  }
   p.total = off;
   *out = p;
   return FLCE_OK;
@@ -161,8 +170,14 @@ struct Product {
   int rows;
   int64_t H, V;
   const Plan* p;
-  float c;
+  float c;                 // times the product's gain
+  float inv_temperature;
   uint32_t* ctrl;
+  // columns to pick
+  const uint2* parts = nullptr;
+  const int2* entries = nullptr;
+  float* picked = nullptr;
+  int k = 0;
 };
 
 // z of a chunk and its statistics: stored to z where given
@@ -176,7 +191,8 @@ flce_status run_stats(flce_handle_t h, const Product& q, void* z, float2* partia
                                      q.p->ldv, q.rows, q.V, q.H, 0, 1, nullptr, s));
     if (partials)
       FLCE_LAUNCH(FLCE_K_SCORE_STATS, 0.0, 4 * dr * dV + 12 * dr * groups,
-                  launch_score_stats_f32(zf, q.p->ldv, q.rows, q.V, groups, q.c, partials, part_s, s));
+                  launch_score_stats_f32(zf, q.p->ldv, q.rows, q.V, groups, q.c, q.inv_temperature,
+                                         partials, part_s, s));
     return FLCE_OK;
   }
   CUtensorMap mx, mw, mz;
@@ -197,10 +213,14 @@ flce_status run_stats(flce_handle_t h, const Product& q, void* z, float2* partia
   a.c = q.c;
   a.partials = partials;
   a.part_s = part_s;
+  a.parts = q.parts;
+  a.entries = q.entries;
+  a.picked = q.picked;
+  a.k = q.k;
   a.ctrl = q.ctrl;
   a.timeout_ns = h->timeout_ns;
   FLCE_LAUNCH(FLCE_K_SCORE_STATS, 2 * dr * dH * dV, 2 * (dr + dV) * dH + (z ? 2 * dr * dV : 0) + 12 * dr * groups,
-              launch_score_gemm(0, mx, mw, mz, a, std::min(a.num_m * a.num_n, h->score_clusters), s));
+              launch_score_gemm(q.parts ? kScorePick : kScoreStats, mx, mw, mz, a, std::min(a.num_m * a.num_n, h->score_clusters), s));
   return FLCE_OK;
 }
 
@@ -226,7 +246,7 @@ flce_status run_gradient(flce_handle_t h, const Product& q, void* d, const Score
   a.ctrl = q.ctrl;
   a.timeout_ns = h->timeout_ns;
   FLCE_LAUNCH(FLCE_K_SCORE_GRADIENT, 2 * dr * dH * dV, 2 * (dr + dV) * dH + 2 * dr * dV,
-              launch_score_gemm(1, mx, mw, md, a, std::min(a.num_m * a.num_n, h->score_clusters), s));
+              launch_score_gemm(kScoreGradient, mx, mw, md, a, std::min(a.num_m * a.num_n, h->score_clusters), s));
   return FLCE_OK;
 }
 
@@ -406,10 +426,11 @@ flce_status flce_logprobs_forward(flce_handle_t h, const flce_logprobs_args* r, 
   st = clear_ctrl(h, ctrl, s);
   if (st != FLCE_OK) return st;
   const Kept K = kept_layout(bf16, r->N, r->V);
-  const double c = kLog2e / r->temperature;
+  const double gain = bf16 ? score_gain(r->H) : 1.0, c = gain * kLog2e / r->temperature;
+  const float inv_t = static_cast<float>(1.0 / r->temperature);
   for (int64_t off = 0; off < r->N; off += p.chunk) {
     const int rows = static_cast<int>(std::min(p.chunk, r->N - off));
-    const Product q{static_cast<const uint8_t*>(r->x) + off * r->H * es, r->W, rows, r->H, r->V, &p, static_cast<float>(c), ctrl};
+    const Product q{static_cast<const uint8_t*>(r->x) + off * r->H * es, r->W, rows, r->H, r->V, &p, static_cast<float>(c), inv_t, ctrl};
     void* z = kept ? kept + off * p.ldv * es : (r->top > 0 || !bf16) ? ws + p.z : nullptr;
     float2* partials = reinterpret_cast<float2*>(kept ? kept + K.partials + off * p.groups * 8 : ws + p.partials);
     float* part_s = reinterpret_cast<float*>(ws + p.part_s);
@@ -426,7 +447,9 @@ flce_status flce_logprobs_forward(flce_handle_t h, const flce_logprobs_args* r, 
     a.ignore_index = r->ignore_index;
     a.c = static_cast<float>(c);
     a.inv_c = static_cast<float>(1.0 / c);
-    a.inv_temperature = 1.0 / r->temperature;
+    a.inv_temperature = inv_t;
+    a.scale = static_cast<float>(gain / r->temperature);
+    a.loss = static_cast<float>(gain - 1.0);
     a.x = q.x;
     a.W = r->W;
     a.t = r->t ? r->t + off : nullptr;
@@ -476,7 +499,9 @@ flce_status flce_logprobs_backward(flce_handle_t h, const flce_logprobs_args* r,
   st = clear_ctrl(h, ctrl, s);
   if (st != FLCE_OK) return st;
   const Kept K = kept_layout(bf16, r->N, r->V);
-  const float c = static_cast<float>(kLog2e / r->temperature);
+  const double gain = bf16 ? score_gain(r->H) : 1.0;
+  const float c = static_cast<float>(gain * kLog2e / r->temperature);
+  const float inv_t = static_cast<float>(1.0 / r->temperature);
   const bool cast = dW && dw_dtype == FLCE_DTYPE_BF16;
   ScoreRow* row = reinterpret_cast<ScoreRow*>(ws + p.row);
   float* dcorr = reinterpret_cast<float*>(ws + p.dcorr);
@@ -491,7 +516,7 @@ flce_status flce_logprobs_backward(flce_handle_t h, const flce_logprobs_args* r,
     a.H = r->H;
     a.V = r->V;
     a.ignore_index = r->ignore_index;
-    a.temperature = r->temperature;
+    a.inv_temperature = inv_t;
     a.x = static_cast<const uint8_t*>(r->x) + off * r->H * es;
     a.xm = ws + p.xm;
     a.t = r->t + off;
@@ -503,12 +528,12 @@ flce_status flce_logprobs_backward(flce_handle_t h, const flce_logprobs_args* r,
     a.dcorr = dcorr;
     a.ctrl = ctrl;
     FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 2.0 * dr * r->H * es + 50.0 * dr, launch_score_prepare(a, s));
-    const Product q{ws + p.xm, r->W, rows, r->H, r->V, &p, c, ctrl};
+    const Product q{ws + p.xm, r->W, rows, r->H, r->V, &p, c, inv_t, ctrl};
     if (kept) {
       FLCE_LAUNCH(FLCE_K_SCORE_DLOGITS, 0.0, 2.0 * es * dr * dV,
                   launch_score_dlogits(bf16, kept + off * p.ldv * es,
                                        reinterpret_cast<const float2*>(kept + K.partials) + off * p.groups,
-                                       static_cast<int>(p.groups), d, p.ldv, rows, r->V, c, row, dcorr, s));
+                                       static_cast<int>(p.groups), d, p.ldv, rows, r->V, c, inv_t, row, dcorr, s));
     } else if (bf16) {
       st = run_gradient(h, q, d, row, dcorr, s);
       if (st != FLCE_OK) return st;
@@ -516,7 +541,7 @@ flce_status flce_logprobs_backward(flce_handle_t h, const flce_logprobs_args* r,
       st = run_stats(h, q, d, nullptr, nullptr, s);
       if (st != FLCE_OK) return st;
       FLCE_LAUNCH(FLCE_K_SCORE_DLOGITS, 0.0, 2.0 * es * dr * dV,
-                  launch_score_dlogits(0, d, nullptr, 0, d, p.ldv, rows, r->V, c, row, dcorr, s));
+                  launch_score_dlogits(0, d, nullptr, 0, d, p.ldv, rows, r->V, c, inv_t, row, dcorr, s));
     }
     const Backward b{d,
                      reinterpret_cast<float*>(ws + p.partials),
@@ -559,7 +584,8 @@ static flce_status distill_check(flce_handle_t h, const flce_distill_args* r) {
 
 static flce_status distill_plan(flce_handle_t h, const flce_distill_args* r, Plan* p) {
   Needs q{};
-  q.stats = q.live = true;
+  q.stats = true;
+  q.teacher = r->K;
   q.gradient = r->dx || r->dW;
   q.z = q.gradient || !is_bf16(h);
   q.dx = r->dx != nullptr;
@@ -604,7 +630,9 @@ flce_status flce_distill(flce_handle_t h, const flce_distill_args* r, void* work
   if (st != FLCE_OK) return st;
   const bool gradient = r->dx || r->dW;
   const bool cast = r->dW && r->dw_dtype == FLCE_DTYPE_BF16;
-  const float c = static_cast<float>(kLog2e / r->temperature);
+  const double gain = bf16 ? score_gain(r->H) : 1.0;
+  const float c = static_cast<float>(gain * kLog2e / r->temperature);
+  const float inv_t = static_cast<float>(1.0 / r->temperature);
   int32_t claims = 0;
   if (r->N == 0) {
     st = zero_dw(h, r->dW, r->dw_dtype, r->V, r->H, s);
@@ -618,12 +646,35 @@ flce_status flce_distill(flce_handle_t h, const flce_distill_args* r, void* work
     const int rows = static_cast<int>(std::min(p.chunk, r->N - off));
     const double dr = rows, dV = static_cast<double>(r->V);
     const void* x = static_cast<const uint8_t*>(r->x) + off * r->H * es;
-    if (gradient) {
-      FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 2.0 * dr * r->H * es,
-                  launch_distill_mask(x, ws + p.xm, live + off, rows, r->H * es, s));
-      x = ws + p.xm;
+    const int64_t* ids = r->ids + off * r->ld_ids;
+    const void* logits = static_cast<const uint8_t*>(r->logits) + off * r->ld_logits * ls;
+    Product q{x, r->W, rows, r->H, r->V, &p, c, inv_t, ctrl};
+    if (bf16) {
+      q.parts = reinterpret_cast<const uint2*>(ws + p.parts);
+      q.entries = reinterpret_cast<const int2*>(ws + p.entries);
+      q.picked = reinterpret_cast<float*>(ws + p.picked);
+      q.k = static_cast<int>(r->K);
     }
-    const Product q{x, r->W, rows, r->H, r->V, &p, c, ctrl};
+    if (gradient) q.x = ws + p.xm;
+    if (bf16 || gradient) {
+      DistillPrepareArgs a{};
+      a.rows = rows;
+      a.k = static_cast<int>(r->K);
+      a.dtype = r->logits_dtype;
+      a.num_tiles = static_cast<int>(cdiv(r->V, kScoreTileColumns));
+      a.row_bytes = r->H * static_cast<int64_t>(es);
+      a.ld_ids = r->ld_ids;
+      a.ld_logits = r->ld_logits;
+      a.x = x;
+      a.xm = gradient ? ws + p.xm : nullptr;
+      a.ids = ids;
+      a.logits = logits;
+      a.live = live + off;
+      a.parts = bf16 ? reinterpret_cast<uint2*>(ws + p.parts) : nullptr;
+      a.entries = bf16 ? reinterpret_cast<int2*>(ws + p.entries) : nullptr;
+      FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, (gradient ? 2.0 * dr * r->H * es : 0.0) + dr * r->K * (16.0 + ls),
+                  launch_distill_prepare(a, s));
+    }
     void* z = gradient || !bf16 ? ws + p.z : nullptr;
     float2* partials = reinterpret_cast<float2*>(ws + p.partials);
     st = run_stats(h, q, z, partials, reinterpret_cast<float*>(ws + p.part_s), s);
@@ -635,24 +686,24 @@ flce_status flce_distill(flce_handle_t h, const flce_distill_args* r, void* work
     a.bf16 = bf16;
     a.dtype = r->logits_dtype;
     a.gradient = gradient;
-    a.H = r->H;
     a.V = r->V;
     a.ldv = p.ldv;
     a.ld_ids = r->ld_ids;
     a.ld_logits = r->ld_logits;
     a.c = c;
-    a.temperature = r->temperature;
-    a.x = x;
-    a.W = r->W;
-    a.ids = r->ids + off * r->ld_ids;
-    a.logits = static_cast<const uint8_t*>(r->logits) + off * r->ld_logits * ls;
+    a.temperature = static_cast<float>(r->temperature);
+    a.inv_temperature = inv_t;
+    a.scale = static_cast<float>(gain / r->temperature);
+    a.ids = ids;
+    a.logits = logits;
     a.partials = partials;
+    a.picked = q.picked;
     a.z = z;
     a.live = live + off;
     a.token_loss = r->token_loss + off;
     a.ctrl = ctrl;
     FLCE_LAUNCH(FLCE_K_DISTILL_ROWS, 0.0,
-                dr * (r->K * (8.0 + ls + static_cast<double>(r->H) * es) + 8.0 * p.groups) + (gradient ? 2.0 * es * dr * dV : 0.0),
+                dr * (r->K * (12.0 + ls) + 8.0 * p.groups) + (gradient ? 2.0 * es * dr * dV : 0.0),
                 launch_distill_rows(a, s));
     if (gradient) {
       const Backward b{z,

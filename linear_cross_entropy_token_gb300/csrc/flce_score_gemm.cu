@@ -1,17 +1,19 @@
 // The product z = x Wt of the LM-head operators (flce_score.h) on tcgen05, with
 // what becomes of z in its epilogue: the statistics of each row's softmax and
-// entropy, or the gradient of the logits.
+// entropy (and z at picked columns), or the gradient of the logits.
 //
 // 256 x 512 tiles on CTA pairs, as the loss runs them: per 16-deep step two
 // tcgen05.mma.cta_group::2 (M 256, N 256) share A through the collector, a
 // four-stage ring of TMA loads, the 512 accumulator columns filling TMEM. The
-// accumulator is handed back in two halves of 256 columns. Each of the two
-// epilogue warpgroups takes 128 columns of a half into registers (128 of its 224
-// a thread), hands the half back and only then computes: the exponentials of the
-// first half run while the next tile's first products already do, those of the
-// second half under the next tile's main loop. The loss's epilogue rounds z to
-// bf16 to hold a row's 256 columns in registers at once; here every sum is of the
-// fp32 accumulators, since log probabilities are compared with each other.
+// accumulator is handed back in two halves of 256 columns. An epilogue warpgroup has
+// two groups of 64 columns in each half. It takes three of the four into registers
+// (192 of its 232 a thread), hands the first half back, computes the first group's
+// exponentials, takes the fourth into its registers and hands the second half back:
+// so the accumulator is held for a quarter of the arithmetic, while the next tile's
+// first products run on the half that is free. (Two groups at a time held it for
+// half of the arithmetic: 104 us at 2048 x 1024 x 32000.) The loss's epilogue rounds
+// z to bf16 to hold all four at once; here every sum is of the fp32 accumulators,
+// since log probabilities are compared with each other.
 //
 // Mathematics. With c = log2(e) / temperature and, per 64 columns, the largest m:
 // y = (z - m) c, and the sums l of 2^y and s of y 2^y give the log-sum-exp and
@@ -49,7 +51,7 @@ constexpr int kThreads = 384;
 constexpr int kEpiThreads = 128;
 // registers move from the loading and issuing warpgroup to the two epilogues;
 // the split must fit what the launch holds (checked on the host)
-constexpr uint32_t kRegsCtl = 56, kRegsEpi = 224;
+constexpr uint32_t kRegsCtl = 40, kRegsEpi = 232;
 constexpr int kLaunchRegs = 168;
 static_assert(128 * kRegsCtl + 256 * kRegsEpi <= kThreads * kLaunchRegs, "register split");
 
@@ -73,11 +75,11 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64
     if (globaltimer_ns() - t0 > timeout_ns) return;
 }
 
-// One row of a 128-row x 128-byte staging tile in the 128-byte swizzle
-__device__ __forceinline__ void stage_row(uint8_t* buf, int r, const uint32_t (&w)[32]) {
-  uint4* at = reinterpret_cast<uint4*>(buf + r * 128);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) at[j ^ (r & 7)] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+// Eight 16-bit columns, the j-th such piece of a row of a 128-row x 128-byte staging
+// tile in the 128-byte swizzle. Each piece is staged as it is computed: a group's 32
+// words at once would take registers that three groups of logits leave no room for.
+__device__ __forceinline__ void stage_piece(uint8_t* buf, int row, int j, const uint32_t (&w)[4]) {
+  reinterpret_cast<uint4*>(buf + row * 128)[j ^ (row & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // 64 columns from two 32-register loads
@@ -86,11 +88,8 @@ struct Group {
   uint32_t (&hi)[32];
 };
 
-// The statistics of 64 columns of this thread's row, ncv of them valid; with
-// w, y packed as fp16.
-template <bool STORE>
-__device__ __forceinline__ void group_stats(Group g, int ncv, float c, float2* part, float* part_s, bool rvalid,
-                                            uint32_t (&w)[32]) {
+// The largest of 64 columns of this thread's row, ncv of them valid
+__device__ __forceinline__ float group_max(Group g, int ncv) {
   if (ncv < 64) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
@@ -104,27 +103,36 @@ __device__ __forceinline__ void group_stats(Group g, int ncv, float c, float2* p
 #pragma unroll
   for (int i = 4; i < 32; ++i)
     m4[i & 3] = max_nan(m4[i & 3], max_nan(__uint_as_float(g.lo[i]), __uint_as_float(g.hi[i])));
-  const float m = max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3]));
+  return max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3]));
+}
+
+// Their statistics relative to it, and y staged as fp16
+template <bool STORE>
+__device__ __forceinline__ void group_stats(Group g, float m, float c, float2* part, float* part_s, bool rvalid,
+                                            uint8_t* buf, int row) {
   float l[4] = {0.f, 0.f, 0.f, 0.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     uint32_t (&r)[32] = half ? g.hi : g.lo;
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      const float d0 = (__uint_as_float(r[i]) - m) * c, d1 = (__uint_as_float(r[i + 1]) - m) * c;
-      // at -1000 the exponential is 0 and y 2^y is too, which -inf would make NaN
-      const float y0 = max_nan(d0, -1000.f), y1 = max_nan(d1, -1000.f);
-      const float e0 = ex2(y0), e1 = ex2(y1);
-      l[i & 3] += e0;
-      l[(i + 1) & 3] += e1;
-      s[i & 3] = fmaf(y0, e0, s[i & 3]);
-      s[(i + 1) & 3] = fmaf(y1, e1, s[(i + 1) & 3]);
-      if (STORE) {
+    for (int j = 0; j < 4; ++j) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 8 * j; i < 8 * j + 8; i += 2) {
+        const float d0 = (__uint_as_float(r[i]) - m) * c, d1 = (__uint_as_float(r[i + 1]) - m) * c;
+        // at -1000 the exponential is 0 and y 2^y is too, which -inf would make NaN
+        const float y0 = max_nan(d0, -1000.f), y1 = max_nan(d1, -1000.f);
+        const float e0 = ex2(y0), e1 = ex2(y1);
+        l[i & 3] += e0;
+        l[(i + 1) & 3] += e1;
+        s[i & 3] = fmaf(y0, e0, s[i & 3]);
+        s[(i + 1) & 3] = fmaf(y1, e1, s[(i + 1) & 3]);
         // 11 bits of a distance to the group's largest: what the gradient's
         // exponentials and the search for alternatives need of it
-        __half2 h = __floats2half2_rn(d0, d1);
-        w[half * 16 + i / 2] = *reinterpret_cast<uint32_t*>(&h);
+        const __half2 h = __floats2half2_rn(d0, d1);
+        w[(i & 7) / 2] = *reinterpret_cast<const uint32_t*>(&h);
       }
+      if (STORE) stage_piece(buf, row, 4 * half + j, w);
     }
   }
   if (rvalid) {
@@ -133,49 +141,69 @@ __device__ __forceinline__ void group_stats(Group g, int ncv, float c, float2* p
   }
 }
 
-// The gradient of 64 columns of this thread's row as bf16; k: the target's
+// The gradient of 64 columns of this thread's row staged as bf16; k: the target's
 // column among them, or -1.
 __device__ __forceinline__ void group_gradient(Group g, const ScoreRow& q, float c, int k, float* dcorr, bool rvalid,
-                                               uint32_t (&w)[32]) {
+                                               uint8_t* buf, int row) {
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     uint32_t (&r)[32] = half ? g.hi : g.lo;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float t = max_nan(fmaf(__uint_as_float(r[i]) - q.largest, c, -q.log2_total), -1000.f);
-      r[i] = __float_as_uint(ex2(t) * fmaf(q.b, t, q.a));
-    }
-  }
-  if (k >= 0) {
-    // the fp32 part of the target's entry that bf16 leaves goes to dx
-    float left = 0.f;
+    for (int j = 0; j < 4; ++j) {
+      float v[8];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if (i == k) {
-        const float v = __uint_as_float(g.lo[i]) + q.add;
-        g.lo[i] = __float_as_uint(v);
-        left = v - __bfloat162float(__float2bfloat16_rn(v));
+      for (int i = 0; i < 8; ++i) {
+        const float t = max_nan(fmaf(__uint_as_float(r[8 * j + i]) - q.largest, c, -q.log2_total), -1000.f);
+        v[i] = ex2(t) * fmaf(q.b, t, q.a);
       }
-      if (i + 32 == k) {
-        const float v = __uint_as_float(g.hi[i]) + q.add;
-        g.hi[i] = __float_as_uint(v);
-        left = v - __bfloat162float(__float2bfloat16_rn(v));
+      if (k >> 3 == 4 * half + j) {
+        // the fp32 part of the target's entry that bf16 leaves goes to dx
+        float left = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i == (k & 7)) {
+            v[i] += q.add;
+            left = v[i] - __bfloat162float(__float2bfloat16_rn(v[i]));
+          }
+        if (rvalid) *dcorr = left;
       }
-    }
-    if (rvalid) *dcorr = left;
-  }
+      uint32_t w[4];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    uint32_t (&r)[32] = half ? g.hi : g.lo;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-      w[half * 16 + i] = *reinterpret_cast<uint32_t*>(&v);
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      stage_piece(buf, row, 4 * half + j, w);
     }
   }
 }
 
-template <int GRADIENT>
+// This thread's value of column i of its group, i by thread: registers cannot be
+// indexed, so halves are chosen between bit by bit (63 selections).
+template <int N>
+__device__ __forceinline__ uint32_t column_of(const uint32_t* r, int i) {
+  if constexpr (N == 1) {
+    return r[0];
+  } else {
+    const uint32_t lo = column_of<N / 2>(r, i), hi = column_of<N / 2>(r + N / 2, i);
+    return (i & (N / 2)) ? hi : lo;
+  }
+}
+
+// z at the picked ones of this thread's 64 columns from cg on: entries first .. end - 1
+// are its part's, of which few are in it (64 a row of 128256: one in 30 threads has one).
+__device__ __forceinline__ void pick_columns(Group g, const ScoreGemmArgs& a, int first, int end, int64_t grow, int cg) {
+  for (int e = first; __any_sync(0xffffffffu, e < end); ++e) {
+    const int2 en = e < end ? a.entries[grow * a.k + e] : make_int2(-1, 0);
+    const bool here = en.x >= cg && en.x < cg + 64;
+    if (!__any_sync(0xffffffffu, here)) continue;
+    const int i = en.x - cg;
+    const uint32_t lo = column_of<32>(g.lo, i), hi = column_of<32>(g.hi, i);
+    if (here) a.picked[grow * a.k + en.y] = __uint_as_float((i & 32) ? hi : lo);
+  }
+}
+
+template <int MODE, bool STORE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     score_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmO, const ScoreGemmArgs a) {
@@ -356,61 +384,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int n0 = (u / a.num_m) * 2 * kBN;
       const int grow = m0 + row;
       const bool rvalid = grow < a.rows;
-      ScoreRow q{0.f, 0.f, 0.f, 0.f, 0.f, -1};
-      if (GRADIENT && rvalid) q = a.row[grow];
-      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(wq * 32) << 16);
-      const size_t prow = static_cast<size_t>(grow) * a.groups;
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        const int col = half * kBN + grp * 128;
-        const int c0 = n0 + col;
-        uint32_t r[4][32];
-        if (c0 < a.cols) {  // uniform
+      ScoreRow q{0.f, 0.f, 0.f, 0.f, 0.f, -1, 0.f};
+      if (MODE == kScoreGradient && rvalid) q = a.row[grow];
+      int first[2] = {0, 0}, end[2] = {0, 0};  // this warpgroup's part of either half
+      if (MODE == kScorePick && rvalid) {
+        const uint2 pp = a.parts[static_cast<int64_t>(grow) * a.num_n + u / a.num_m];
+        const uint64_t at = static_cast<uint64_t>(pp.x) | (static_cast<uint64_t>(pp.y) << 32);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(tbase + col + 32 * i, r[i]);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_regs_ready(r[i]);
-        }
-        tc_fence_before();
-        const uint32_t free_bar = half ? tempty1_bar : tempty0_bar;
-        if (rank == 0)
-          mbar_arrive(free_bar);
-        else
-          mbar_arrive_cluster(mapa_shared(free_bar, 0));
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const int cg = c0 + 64 * g;
-          if (cg >= a.cols) continue;  // uniform
-          const Group v{r[2 * g], r[2 * g + 1]};
-          uint32_t w[32];
-          bool store = true;
-          if constexpr (GRADIENT) {
-            const int k = q.target >= cg && q.target < cg + 64 ? q.target - cg : -1;
-            group_gradient(v, q, c, k, a.dcorr + grow, rvalid, w);
-          } else {
-            store = a.store != 0;
-            float2* part = a.partials + prow + cg / 64;
-            float* part_s = a.part_s + prow + cg / 64;
-            if (store)
-              group_stats<true>(v, a.cols - cg, c, part, part_s, rvalid, w);
-            else
-              group_stats<false>(v, a.cols - cg, c, part, part_s, rvalid, w);
-          }
-          if (store) {
-            if (leader) bulk_wait_group_read<0>();
-            named_bar_sync(bar, kEpiThreads);
-            stage_row(buf, row, w);
-            fence_proxy_async_smem();
-            named_bar_sync(bar, kEpiThreads);
-            if (leader) {
-              tma_store_2d(&tmO, smem_u32(buf), cg, m0);
-              bulk_commit_group();
-            }
-            __syncwarp();
-          }
+        for (int half = 0; half < 2; ++half) {
+          first[half] = static_cast<int>(at >> (9 * (2 * half + grp))) & 511;
+          end[half] = static_cast<int>(at >> (9 * (2 * half + grp + 1))) & 511;
         }
       }
+      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(wq * 32) << 16);
+      const size_t prow = static_cast<size_t>(grow) * a.groups;
+      // tile column of group i: two in each half
+      auto col_of = [&](int i) { return (i < 2 ? 0 : kBN) + grp * 128 + (i & 1) * 64; };
+      uint32_t r[3][2][32];
+      auto load = [&](int i, uint32_t (&to)[2][32]) {
+        if (n0 + col_of(i) < a.cols) {  // uniform
+          tmem_ld_32x32b_x32(tbase + col_of(i), to[0]);
+          tmem_ld_32x32b_x32(tbase + col_of(i) + 32, to[1]);
+        }
+      };
+      auto release = [&](uint32_t b) {
+        tc_fence_before();
+        if (rank == 0)
+          mbar_arrive(b);
+        else
+          mbar_arrive_cluster(mapa_shared(b, 0));
+      };
+      auto process = [&](int i, uint32_t (&from)[2][32]) {
+        const int cg = n0 + col_of(i);
+        if (cg >= a.cols) return;  // uniform
+        const Group v{from[0], from[1]};
+        if constexpr (MODE == kScorePick) pick_columns(v, a, first[i >> 1], end[i >> 1], grow, cg);
+        float m = 0.f;
+        if constexpr (MODE != kScoreGradient) m = group_max(v, a.cols - cg);
+        if constexpr (STORE) {
+          // the copy that still reads the staging tile
+          if (leader) bulk_wait_group_read<0>();
+          named_bar_sync(bar, kEpiThreads);
+        }
+        if constexpr (MODE == kScoreGradient) {
+          const int k = q.target >= cg && q.target < cg + 64 ? q.target - cg : -1;
+          group_gradient(v, q, c, k, a.dcorr + grow, rvalid, buf, row);
+        } else {
+          group_stats<STORE>(v, m, c, a.partials + prow + cg / 64, a.part_s + prow + cg / 64, rvalid, buf, row);
+        }
+        if constexpr (STORE) {
+          fence_proxy_async_smem();
+          named_bar_sync(bar, kEpiThreads);
+          if (leader) {
+            tma_store_2d(&tmO, smem_u32(buf), cg, m0);
+            bulk_commit_group();
+          }
+          __syncwarp();
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < 3; ++i) load(i, r[i]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        tmem_regs_ready(r[i][0]);
+        tmem_regs_ready(r[i][1]);
+      }
+      release(tempty0_bar);
+      process(0, r[0]);
+      load(3, r[0]);
+      tmem_ld_wait();
+      tmem_regs_ready(r[0][0]);
+      tmem_regs_ready(r[0][1]);
+      release(tempty1_bar);
+      process(1, r[1]);
+      process(2, r[2]);
+      process(3, r[0]);
     }
     if (leader) bulk_wait_group<0>();
   }
@@ -424,10 +473,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int GRADIENT>
+template <int MODE, bool STORE>
 cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& to, const ScoreGemmArgs& args,
                    int pairs, cudaStream_t s) {
-  auto kern = score_gemm_kernel<GRADIENT>;
+  auto kern = score_gemm_kernel<MODE, STORE>;
   // an increase of registers waits until the block's pool holds them
   static const bool fits = [](auto k) {
     cudaFuncAttributes at;
@@ -444,9 +493,18 @@ cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorM
 
 }  // namespace
 
-cudaError_t launch_score_gemm(int gradient, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
+cudaError_t launch_score_gemm(int mode, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
                               const ScoreGemmArgs& args, int pairs, cudaStream_t s) {
-  return gradient ? launch<1>(a, b, o, args, pairs, s) : launch<0>(a, b, o, args, pairs, s);
+  switch (mode) {
+    case kScoreStats:
+      return args.store ? launch<kScoreStats, true>(a, b, o, args, pairs, s)
+                        : launch<kScoreStats, false>(a, b, o, args, pairs, s);
+    case kScorePick:
+      return args.store ? launch<kScorePick, true>(a, b, o, args, pairs, s)
+                        : launch<kScorePick, false>(a, b, o, args, pairs, s);
+    case kScoreGradient: return launch<kScoreGradient, true>(a, b, o, args, pairs, s);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 int score_gemm_max_clusters() {
@@ -462,9 +520,9 @@ int score_gemm_max_clusters() {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaFuncSetAttribute(score_gemm_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(score_gemm_kernel<kScoreStats, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(kSmemBytes)) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, score_gemm_kernel<0>, &cfg) != cudaSuccess) {
+      cudaOccupancyMaxActiveClusters(&n, score_gemm_kernel<kScoreStats, false>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
