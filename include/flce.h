@@ -209,9 +209,10 @@ enum {
     FLCE_K_SCORE_GRADIENT = 23,  /* x·Wᵀ with the gradient of the logits as epilogue    */
     FLCE_K_SCORE_ROWS = 24,      /* log probabilities, entropy and alternatives per row */
     FLCE_K_SCORE_DLOGITS = 25,   /* gradient of the logits from kept ones               */
-    FLCE_K_SCORE_OTHER = 26,     /* row constants, masked copies, casts, reports        */
+    FLCE_K_SCORE_OTHER = 26,     /* order of rows, row constants, copies, reports        */
     FLCE_K_DISTILL_ROWS = 27,    /* distillation's losses and gradient rows             */
-    FLCE_K_NUM_KINDS = 28
+    FLCE_K_SCORE_BACKWARD = 28,  /* dx and dW of a chunk in one launch                  */
+    FLCE_K_NUM_KINDS = 29
 };
 
 typedef struct flce_kernel_profile {

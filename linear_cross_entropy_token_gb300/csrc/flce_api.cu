@@ -601,10 +601,6 @@ int shape_for(flce_handle_t h, int64_t tile_n) {
   return tile_n == 2 * kBN ? kShapeWide : kShapePair;
 }
 
-}  // namespace
-
-namespace flce {
-
 // One GEMM on tile shape `shape`; sets num_m and num_n from the extents (M
 // rows, args.cols columns) and the grid from the work units (persistent
 // CTAs, or CTA pairs).
@@ -622,10 +618,6 @@ cudaError_t launch_gemm(flce_handle_t h, int shape, int kind, const CUtensorMap&
   if (shape == kShapePair) return launch_umma_pair(kind, a, b, o, args, slots, s);
   return launch_umma(kind, a, b, o, args, slots, s);
 }
-
-}  // namespace flce
-
-namespace {
 
 // Device copies of a call's host inputs, in one buffer (grown as needed).
 struct Staged {
@@ -1215,6 +1207,7 @@ const char* flce_kernel_name(int32_t kind) {
     case FLCE_K_SCORE_DLOGITS: return "score_dlogits";
     case FLCE_K_SCORE_OTHER: return "score_other";
     case FLCE_K_DISTILL_ROWS: return "distill_rows";
+    case FLCE_K_SCORE_BACKWARD: return "score_backward";
     default: return "?";
   }
 }

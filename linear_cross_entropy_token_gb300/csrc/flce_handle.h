@@ -135,14 +135,12 @@ inline flce_status fail(flce_handle_t h, flce_status st, const char* fmt, ...) {
 // device-side error (kCtrlSticky is the training-step operators').
 constexpr int kHostScoreError = 14;
 
-// flce_api.cu: pieces of the loss's backward that other operators run too
+// flce_api.cu: what other operators' launches need too
 bool map_bf16_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes, uint32_t box_inner,
                  uint32_t box_outer, std::string* why);
 bool map_f32_3d(CUtensorMap* m, void* base, uint64_t cols, uint64_t rows, uint64_t planes, uint64_t row_bytes,
                 uint64_t plane_bytes, std::string* why);
 int group_for(flce_handle_t h, int shape, int num_m, int num_n, int num_s, int slots);
-cudaError_t launch_gemm(flce_handle_t h, int shape, int kind, const CUtensorMap& a, const CUtensorMap& b,
-                        const CUtensorMap& o, UmmaArgs args, int64_t M, cudaStream_t s);
 
 struct DeviceGuard {
   int prev = -1;

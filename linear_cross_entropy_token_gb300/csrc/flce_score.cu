@@ -16,9 +16,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "flce_internal.h"
-#include "flce_score.h"
-#include "ptx.cuh"
+#include "flce_score.cuh"
 
 namespace flce {
 namespace {
@@ -26,27 +24,83 @@ namespace {
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float ex2(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
+// ----------------------------------------------------- rows that count
+
+// The call's row that is a chunk's i-th
+__device__ __forceinline__ int64_t row_of(const ScoreChunk& q, int64_t i) { return q.order ? q.order[q.off + i] : q.off + i; }
+
+// Where the zeros behind a chunk's rows end: a multiple of the products' 256 rows. A
+// chunk without rows needs none, but the first one's product runs whatever there is.
+__device__ __forceinline__ int tail_end(const ScoreChunk& q, int rows) {
+  if (rows == 0 && q.off > 0) return 0;
+  return min(q.rows, (max(rows, 1) + 255) / 256 * 256);
 }
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
+// One block: 1024 rows at a time, each warp's and then each thread's place by counts.
+// A few microseconds for a batch, which the products of the rows left out repay from
+// the first 256 on.
+__global__ void __launch_bounds__(1024) score_order_kernel(const int64_t* __restrict__ t, int64_t ignore_index,
+                                                           const uint8_t* __restrict__ live, int64_t N,
+                                                           int32_t* __restrict__ order, uint32_t* count) {
+  __shared__ int s_count[2][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int done = 0, turn = 0;
+  auto counts = [&](int64_t i) { return i < N && (t ? t[i] != ignore_index : live[i] != 0); };
+  bool next = counts(threadIdx.x);
+  for (int64_t base = 0; base < N; base += 1024, turn ^= 1) {
+    const bool in = next;
+    next = counts(base + 1024 + threadIdx.x);
+    const uint32_t mask = __ballot_sync(0xffffffffu, in);
+    if (lane == 0) s_count[turn][warp] = __popc(mask);
+    __syncthreads();  // the other turn's counts are read by now
+    int own = s_count[turn][lane], upto = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    const int before = __shfl_sync(0xffffffffu, upto - own, warp);
+    if (in) order[done + before + __popc(mask & ((1u << lane) - 1u))] = static_cast<int32_t>(base + threadIdx.x);
+    done += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  if (threadIdx.x == 0) *count = static_cast<uint32_t>(done);
+}
+
+// Fills 16-byte pieces, or 4-byte ones
+__device__ __forceinline__ void zero_row(uint8_t* to, int64_t bytes, int thread, int threads) {
+  if ((reinterpret_cast<uint64_t>(to) | static_cast<uint64_t>(bytes)) % 16 == 0) {
+    for (int64_t i = thread * 16; i < bytes; i += threads * 16) *reinterpret_cast<uint4*>(to + i) = make_uint4(0, 0, 0, 0);
+  } else {
+    for (int64_t i = thread * 4; i < bytes; i += threads * 4) *reinterpret_cast<uint32_t*>(to + i) = 0u;
+  }
+}
+
+// A warp per row
+__global__ void __launch_bounds__(128) score_skip_kernel(const ScoreSkipArgs a) {
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (r >= a.N || (a.t ? a.t[r] != a.ignore_index : a.live[r] != 0)) return;
+  if (a.dx) zero_row(static_cast<uint8_t*>(a.dx) + r * a.row_bytes, a.row_bytes, lane, 32);
+  if (lane == 0) {
+    if (a.logprobs) a.logprobs[r] = 0.f;
+    if (a.entropy) a.entropy[r] = 0.f;
+    if (a.stats) a.stats[r] = make_float2(0.f, 0.f);
+  }
+  for (int i = lane; i < a.top; i += 32) {
+    a.top_logprobs[r * a.top + i] = 0.f;
+    a.top_ids[r * a.top + i] = -1;
+  }
 }
 
 // ------------------------------------------------------- fp32 statistics
 
 // A warp per (row, group): what the product's epilogue does of its accumulators.
-__global__ void __launch_bounds__(256) score_stats_f32_kernel(const float* __restrict__ z, int64_t ldv, int rows, int64_t V,
+__global__ void __launch_bounds__(256) score_stats_f32_kernel(const ScoreChunk chunk, const float* __restrict__ z, int64_t ldv, int64_t V,
                                                               int groups, float c, float inv_t,
                                                               float2* __restrict__ partials, float* __restrict__ part_s) {
   const int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  if (u >= static_cast<int64_t>(rows) * groups) return;
+  if (u >= static_cast<int64_t>(chunk_rows(chunk.live, chunk.off, chunk.rows)) * groups) return;
   const int64_t r = u / groups, g = u - r * groups;
   const float* at = z + r * ldv;
   const int64_t j = g * kScoreGroup + lane;
@@ -151,41 +205,58 @@ __device__ __forceinline__ Pair warp_sum(Pair v) {
   return v;
 }
 
-// x . w of a row each, by a warp
-__device__ __forceinline__ Pair warp_dot(const __nv_bfloat16* x, const __nv_bfloat16* w, int64_t H, int lane) {
-  uint64_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll 4
+// x . w0 and x . w1 of a row each, by a warp
+__device__ __forceinline__ void warp_dot2(const __nv_bfloat16* x, const __nv_bfloat16* w0, const __nv_bfloat16* w1, int64_t H,
+                                          int lane, Pair (&out)[2]) {
+  uint64_t hi[2][2] = {{0, 0}, {0, 0}}, lo[2][2] = {{0, 0}, {0, 0}};
+#pragma unroll 2
   for (int64_t h = lane * 8; h < H; h += 256) {
     const uint4 a = *reinterpret_cast<const uint4*>(x + h);
-    const uint4 b = *reinterpret_cast<const uint4*>(w + h);
-    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+    const uint4 b[2] = {*reinterpret_cast<const uint4*>(w0 + h), *reinterpret_cast<const uint4*>(w1 + h)};
+    const uint32_t av[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      // exact: eight bits times eight bits
-      const uint64_t p = mul2(pack2(av[i] << 16, av[i] & 0xFFFF0000u), pack2(bv[i] << 16, bv[i] & 0xFFFF0000u));
-      uint64_t& t = hi[i & 1];
-      const uint64_t s = add2(t, p);
-      const uint64_t u = sub2(s, t);
-      lo[i & 1] = add2(lo[i & 1], add2(sub2(t, sub2(s, u)), sub2(p, u)));
-      t = s;
+      const uint64_t xv = pack2(av[i] << 16, av[i] & 0xFFFF0000u);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t bv = i == 0 ? b[q].x : i == 1 ? b[q].y : i == 2 ? b[q].z : b[q].w;
+        // exact: eight bits times eight bits
+        const uint64_t p = mul2(xv, pack2(bv << 16, bv & 0xFFFF0000u));
+        uint64_t& t = hi[q][i & 1];
+        const uint64_t s = add2(t, p);
+        const uint64_t u = sub2(s, t);
+        lo[q][i & 1] = add2(lo[q][i & 1], add2(sub2(t, sub2(s, u)), sub2(p, u)));
+        t = s;
+      }
     }
   }
-  Pair v[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    v[i] = two_sum(__uint_as_float(static_cast<uint32_t>(hi[i >> 1] >> (32 * (i & 1)))),
-                   __uint_as_float(static_cast<uint32_t>(lo[i >> 1] >> (32 * (i & 1)))));
-  return warp_sum(add(add(v[0], v[1]), add(v[2], v[3])));
+  for (int q = 0; q < 2; ++q) {
+    Pair v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = two_sum(__uint_as_float(static_cast<uint32_t>(hi[q][i >> 1] >> (32 * (i & 1)))),
+                     __uint_as_float(static_cast<uint32_t>(lo[q][i >> 1] >> (32 * (i & 1)))));
+    out[q] = add(add(v[0], v[1]), add(v[2], v[3]));
+  }
+  out[0] = warp_sum(out[0]);
+  out[1] = warp_sum(out[1]);
 }
 
-__device__ __forceinline__ Pair warp_dot(const float* x, const float* w, int64_t H, int lane) {
-  Pair v = {0.f, 0.f};
+__device__ __forceinline__ void warp_dot2(const float* x, const float* w0, const float* w1, int64_t H, int lane,
+                                          Pair (&out)[2]) {
+  const float* w[2] = {w0, w1};
+  out[0] = out[1] = {0.f, 0.f};
   for (int64_t h = lane; h < H; h += 32) {
-    const float p = __fmul_rn(x[h], w[h]), rest = __fmaf_rn(x[h], w[h], -p);
-    const Pair s = two_sum(v.hi, p);
-    v = {s.hi, __fadd_rn(v.lo, __fadd_rn(s.lo, rest))};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const float p = __fmul_rn(x[h], w[q][h]), rest = __fmaf_rn(x[h], w[q][h], -p);
+      const Pair s = two_sum(out[q].hi, p);
+      out[q] = {s.hi, __fadd_rn(out[q].lo, __fadd_rn(s.lo, rest))};
+    }
   }
-  return warp_sum(two_sum(v.hi, v.lo));
+#pragma unroll
+  for (int q = 0; q < 2; ++q) out[q] = warp_sum(two_sum(out[q].hi, out[q].lo));
 }
 
 // A key that orders floats (NaN above all, 0 below every value's)
@@ -474,10 +545,11 @@ constexpr int kWarpRows = 4;
 
 template <class E>
 __global__ void __launch_bounds__(32 * kWarpRows) score_warp_rows_kernel(const ScoreRowsArgs a) {
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5);
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && threadIdx.x == 0) report(a.ctrl, a.host_error);
-  if (r >= a.rows) return;
+  if (i >= chunk_rows(a.chunk.live, a.chunk.off, a.chunk.rows)) return;
+  const int64_t r = row_of(a.chunk, i);
   const int64_t t = a.t ? a.t[r] : -1;
   if (a.t && t == a.ignore_index) {
     if (lane == 0) {
@@ -488,8 +560,8 @@ __global__ void __launch_bounds__(32 * kWarpRows) score_warp_rows_kernel(const S
     return;
   }
   const bool bad = a.t && (t < 0 || t >= a.V);
-  const float2* part = a.partials + r * a.groups;
-  const float* part_s = a.part_s + r * a.groups;
+  const float2* part = a.partials + i * a.groups;
+  const float* part_s = a.part_s + i * a.groups;
   const float scale = a.scale;
   float m = -INFINITY;
 #pragma unroll 8
@@ -511,11 +583,11 @@ __global__ void __launch_bounds__(32 * kWarpRows) score_warp_rows_kernel(const S
     S += __shfl_xor_sync(0xffffffffu, S, o);
   }
   const float log_L = logf(L);
-  Pair z = {0.f, 0.f};
-  if (a.t && !bad)
-    z = warp_dot(static_cast<const E*>(a.x) + r * a.H, static_cast<const E*>(a.W) + t * a.H, a.H, lane);
+  Pair z[2] = {};
+  const E* w = static_cast<const E*>(a.W) + (a.t && !bad ? t : 0) * a.H;
+  if (a.t && !bad) warp_dot2(static_cast<const E*>(a.x) + r * a.H, w, w, a.H, lane, z);
   if (lane != 0) return;
-  if (a.t) a.logprobs[r] = bad ? NAN : score_log_p(a, z, M, log_L);
+  if (a.t) a.logprobs[r] = bad ? NAN : score_log_p(a, z[0], M, log_L);
   a.entropy[r] = log_L - kLn2 * S / L;
   a.stats[r] = make_float2(M, log_L);
   if (bad) *reinterpret_cast<volatile uint32_t*>(a.host_error) = kErrBadTarget;
@@ -531,10 +603,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) score_rows_kernel(con
   __shared__ float s_red[THREADS / 32];
   __shared__ int64_t s_id[kMaxCandidates];
   __shared__ Pair s_dot[kMaxCandidates + 1];
+  __shared__ uint64_t s_order[kMaxCandidates + 1];
   __shared__ TopSmem<THREADS> s_top;
-  const int64_t r = blockIdx.x;
+  const int64_t i = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (r == 0 && threadIdx.x == 0) report(a.ctrl, a.host_error);
+  if (i == 0 && threadIdx.x == 0) report(a.ctrl, a.host_error);
+  if (i >= chunk_rows(a.chunk.live, a.chunk.off, a.chunk.rows)) return;
+  const int64_t r = row_of(a.chunk, i);
   const int64_t t = a.t ? a.t[r] : -1;
   if (a.t && t == a.ignore_index) {
     if (threadIdx.x == 0) {
@@ -549,8 +624,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) score_rows_kernel(con
     return;
   }
   const bool bad = a.t && (t < 0 || t >= a.V);
-  const float2* part = a.partials + r * a.groups;
-  const float* part_s = a.part_s + r * a.groups;
+  const float2* part = a.partials + i * a.groups;
+  const float* part_s = a.part_s + i * a.groups;
   float m = -INFINITY;
   for (int g = threadIdx.x; g < a.groups; g += THREADS) m = max_nan(m, part[g].x);
   const float M = block_max<THREADS>(m, s_red);
@@ -568,7 +643,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) score_rows_kernel(con
   const E* x = static_cast<const E*>(a.x) + r * a.H;
   const E* W = static_cast<const E*>(a.W);
 
-  const Z* z = static_cast<const Z*>(a.z) + r * a.ldv;
+  const Z* z = static_cast<const Z*>(a.z) + i * a.ldv;
   int n = quick_candidates<Z, THREADS>(a, part, z, m, M, s_top, s_id);
   if (n < 0) {
     __syncthreads();
@@ -577,19 +652,29 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) score_rows_kernel(con
   __syncthreads();
   // the given token's logit behind the candidates'
   const int dots = n + (a.t && !bad ? 1 : 0);
-  for (int i = warp; i < dots; i += THREADS / 32) {
-    const Pair d = warp_dot(x, W + (i < n ? s_id[i] : t) * a.H, a.H, lane);
-    if (lane == 0) s_dot[i] = d;
+  // two at a time, which share x and hide each other's latency
+  for (int d = warp; d < dots; d += 2 * (THREADS / 32)) {
+    const int e = d + THREADS / 32;
+    const E* w0 = W + (d < n ? s_id[d] : t) * a.H;
+    const E* w1 = e < dots ? W + (e < n ? s_id[e] : t) * a.H : w0;
+    Pair v[2];
+    warp_dot2(x, w0, w1, a.H, lane, v);
+    if (lane == 0) {
+      s_dot[d] = v[0];
+      s_order[d] = order_key(v[0]);
+      if (e < dots) {
+        s_dot[e] = v[1];
+        s_order[e] = order_key(v[1]);
+      }
+    }
   }
   __syncthreads();
   if (threadIdx.x < n) {
-    const uint64_t own = order_key(s_dot[threadIdx.x]);
+    const uint64_t own = s_order[threadIdx.x];
     const int64_t id = s_id[threadIdx.x];
     int rank = 0;
-    for (int i = 0; i < n; ++i) {
-      const uint64_t v = order_key(s_dot[i]);
-      rank += v > own || (v == own && s_id[i] < id);
-    }
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) rank += s_order[j] > own || (s_order[j] == own && s_id[j] < id);
     if (rank < a.top) {
       a.top_logprobs[r * a.top + rank] = score_log_p(a, s_dot[threadIdx.x], M, log_L);
       a.top_ids[r * a.top + rank] = id;
@@ -607,13 +692,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) score_rows_kernel(con
 
 // Copies 16-byte pieces, or 4-byte ones where rows are not made of those (fp32 x may
 // start at any element)
-__device__ __forceinline__ void copy_row(const uint8_t* from, uint8_t* to, int64_t bytes, bool live) {
+__device__ __forceinline__ void copy_row(const uint8_t* from, uint8_t* to, int64_t bytes) {
   if ((reinterpret_cast<uint64_t>(from) | reinterpret_cast<uint64_t>(to) | static_cast<uint64_t>(bytes)) % 16 == 0) {
     for (int64_t i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16)
-      *reinterpret_cast<uint4*>(to + i) = live ? *reinterpret_cast<const uint4*>(from + i) : make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(to + i) = *reinterpret_cast<const uint4*>(from + i);
   } else {
     for (int64_t i = threadIdx.x * 4; i < bytes; i += blockDim.x * 4)
-      *reinterpret_cast<uint32_t*>(to + i) = live ? *reinterpret_cast<const uint32_t*>(from + i) : 0u;
+      *reinterpret_cast<uint32_t*>(to + i) = *reinterpret_cast<const uint32_t*>(from + i);
   }
 }
 
@@ -621,35 +706,42 @@ __device__ __forceinline__ void copy_row(const uint8_t* from, uint8_t* to, int64
 // Rows that do not count get zeros, and a zero row of x, so that nothing that
 // stands there (it may be NaN) reaches dW.
 __global__ void __launch_bounds__(128) score_prepare_kernel(const ScorePrepareArgs a) {
-  const int64_t r = blockIdx.x;
-  const int64_t t = a.t[r];
-  const bool ignored = t == a.ignore_index, bad = !ignored && (t < 0 || t >= a.V);
-  const bool live = !ignored && !bad;
-  if (threadIdx.x == 0) {
-    if (bad) atomicCAS(a.ctrl, 0u, kErrBadTarget);
-    ScoreRow q{0.f, 0.f, 0.f, 0.f, 0.f, -1, 0.f};
-    if (live) {
-      const float2 st = a.stats[r];
-      const float inv = a.inv_temperature;
-      const float g = a.d_logprobs ? a.d_logprobs[r] : 0.f;
-      const float h = a.d_entropy ? a.d_entropy[r] : 0.f;
-      q.largest = st.x;
-      q.log2_total = st.y * kLog2e;
-      q.inv_total = expf(-st.y);
-      q.a = -inv * (a.d_entropy ? fmaf(h, a.entropy[r], g) : g);
-      q.b = -inv * h * kLn2;
-      q.add = inv * g;
-      q.target = static_cast<int32_t>(t);
-      // what the exponentials' lower limit would hide
-      if (!(fabsf(q.log2_total) < INFINITY) || !(fabsf(q.largest) < INFINITY)) q.a = NAN;
+  const int64_t i = blockIdx.x;
+  const int rows = chunk_rows(a.chunk.live, a.chunk.off, a.chunk.rows);
+  if (i >= rows && (!a.tail || i >= tail_end(a.chunk, rows))) return;
+  const int64_t r = i < rows ? row_of(a.chunk, i) : 0;
+  bool live = i < rows && (!a.alive || a.alive[r] != 0);
+  if (a.t) {
+    const int64_t t = live ? a.t[r] : 0;
+    const bool ignored = live && t == a.ignore_index, bad = live && !ignored && (t < 0 || t >= a.V);
+    live = live && !ignored && !bad;
+    if (threadIdx.x == 0) {
+      if (bad) atomicCAS(a.ctrl, 0u, kErrBadTarget);
+      ScoreRow q{0.f, 0.f, 0.f, 0.f, 0.f, -1, 0.f};
+      if (live) {
+        const float2 st = a.stats[r];
+        const float inv = a.inv_temperature;
+        const float g = a.d_logprobs ? a.d_logprobs[r] : 0.f;
+        const float h = a.d_entropy ? a.d_entropy[r] : 0.f;
+        q.largest = st.x;
+        q.log2_total = st.y * kLog2e;
+        q.inv_total = expf(-st.y);
+        q.a = -inv * (a.d_entropy ? fmaf(h, a.entropy[r], g) : g);
+        q.b = -inv * h * kLn2;
+        q.add = inv * g;
+        q.target = static_cast<int32_t>(t);
+        // what the exponentials' lower limit would hide
+        if (!(fabsf(q.log2_total) < INFINITY) || !(fabsf(q.largest) < INFINITY)) q.a = NAN;
+      }
+      a.row[i] = q;
+      a.dcorr[i] = 0.f;
     }
-    a.row[r] = q;
-    a.dcorr[r] = 0.f;
   }
-  if (a.xm) {
-    const int64_t bytes = a.H * (a.bf16 ? 2 : 4);
-    copy_row(static_cast<const uint8_t*>(a.x) + r * bytes, static_cast<uint8_t*>(a.xm) + r * bytes, bytes, live);
-  }
+  uint8_t* to = static_cast<uint8_t*>(a.xm) + i * a.row_bytes;
+  if (live)
+    copy_row(static_cast<const uint8_t*>(a.x) + r * a.row_bytes, to, a.row_bytes);
+  else
+    zero_row(to, a.row_bytes, threadIdx.x, blockDim.x);
 }
 
 // Eight columns of a row's gradient from the stored logits. The padding behind the
@@ -699,9 +791,10 @@ __device__ __forceinline__ void dlogits4(const float* z, float* d, int64_t j, in
 constexpr int kDlogitsThreads = 256;
 
 __global__ void __launch_bounds__(kDlogitsThreads) score_dlogits_bf16_kernel(
-    const __half* z, const float2* __restrict__ partials, int groups, __nv_bfloat16* d, int64_t ldv, int64_t V, float c,
+    const ScoreChunk chunk, const __half* z, const float2* __restrict__ partials, int groups, __nv_bfloat16* d, int64_t ldv, int64_t V, float c,
     const ScoreRow* __restrict__ row, float* __restrict__ dcorr) {
   const int64_t r = blockIdx.x;
+  if (r >= tail_end(chunk, chunk_rows(chunk.live, chunk.off, chunk.rows))) return;
   const ScoreRow q = row[r];
   const int64_t j = (static_cast<int64_t>(blockIdx.y) * kDlogitsThreads + threadIdx.x) * 8;
   if (j >= ldv) return;
@@ -712,9 +805,10 @@ __global__ void __launch_bounds__(kDlogitsThreads) score_dlogits_bf16_kernel(
   dlogits8(z + r * ldv, d + r * ldv, j, V, partials[r * groups + j / kScoreGroup].x, c, q, dcorr + r);
 }
 
-__global__ void __launch_bounds__(kDlogitsThreads) score_dlogits_f32_kernel(const float* z, float* d, int64_t ldv, int64_t V,
+__global__ void __launch_bounds__(kDlogitsThreads) score_dlogits_f32_kernel(const ScoreChunk chunk, const float* z, float* d, int64_t ldv, int64_t V,
                                                                            float c, float inv_t, const ScoreRow* __restrict__ row) {
   const int64_t r = blockIdx.x;
+  if (r >= tail_end(chunk, chunk_rows(chunk.live, chunk.off, chunk.rows))) return;
   const ScoreRow q = row[r];
   const int64_t j = (static_cast<int64_t>(blockIdx.y) * kDlogitsThreads + threadIdx.x) * 4;
   if (j >= ldv) return;
@@ -727,13 +821,13 @@ __global__ void __launch_bounds__(kDlogitsThreads) score_dlogits_f32_kernel(cons
 
 // dx: the sum of the splits in their order, with the target's entry put right,
 // rounded once. H % 8 == 0.
-__global__ void __launch_bounds__(128) score_dx_kernel(const float* __restrict__ part, int splits, int64_t split_stride,
+__global__ void __launch_bounds__(128) score_dx_kernel(const ScoreChunk chunk, const float* __restrict__ part, int splits, int64_t split_stride,
                                                        int64_t H, const __nv_bfloat16* __restrict__ W,
                                                        const ScoreRow* __restrict__ row, const float* __restrict__ dcorr,
                                                        __nv_bfloat16* __restrict__ dx) {
   const int64_t r = blockIdx.x;
   const int64_t h = (static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * 4;
-  if (h >= H) return;
+  if (h >= H || r >= chunk_rows(chunk.live, chunk.off, chunk.rows)) return;
   const int64_t i = r * H + h;
   float4 acc = *reinterpret_cast<const float4*>(part + i);
   for (int s = 1; s < splits; ++s) {
@@ -753,23 +847,10 @@ __global__ void __launch_bounds__(128) score_dx_kernel(const float* __restrict__
     acc.w = fmaf(__uint_as_float(wv.y & 0xFFFF0000u), c, acc.w);
   }
   __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
-  *reinterpret_cast<uint2*>(dx + i) = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+  *reinterpret_cast<uint2*>(dx + row_of(chunk, r) * H + h) = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
 }
 
-// fp32 to bf16, eight a thread (n % 8 == 0)
-__global__ void __launch_bounds__(256) score_cast_kernel(const float4* __restrict__ in, uint4* __restrict__ out, int64_t n8) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= n8) return;
-  const float4 a = __ldcs(in + 2 * i), b = __ldcs(in + 2 * i + 1);
-  alignas(16) __nv_bfloat162 v[4] = {__floats2bfloat162_rn(a.x, a.y), __floats2bfloat162_rn(a.z, a.w), __floats2bfloat162_rn(b.x, b.y),
-                         __floats2bfloat162_rn(b.z, b.w)};
-  __stcs(out + i, *reinterpret_cast<uint4*>(v));
-}
-
-__global__ void score_report_kernel(const uint32_t* ctrl, uint32_t* host_error) {
-  const uint32_t code = ld_volatile_u32(ctrl);
-  if (code != 0) *reinterpret_cast<volatile uint32_t*>(host_error) = code;
-}
+__global__ void score_report_kernel(const uint32_t* ctrl, uint32_t* host_error) { report(ctrl, host_error); }
 
 // --------------------------------------------------------- distillation
 
@@ -786,8 +867,7 @@ __device__ __forceinline__ bool teacher_there(int64_t id, float logit) { return 
 __global__ void __launch_bounds__(256) distill_live_kernel(const int64_t* __restrict__ ids, int64_t ld_ids,
                                                            const void* __restrict__ logits, int64_t ld_logits, int dtype,
                                                            int64_t N, int k, int64_t V, uint8_t* __restrict__ live,
-                                                           uint32_t* ctrl) {
-  __shared__ int s_live[8];
+                                                           float* __restrict__ token_loss, uint32_t* ctrl) {
   const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   bool any = false, bad = false;
@@ -800,44 +880,31 @@ __global__ void __launch_bounds__(256) distill_live_kernel(const int64_t* __rest
     }
   any = __any_sync(0xffffffffu, any);
   bad = __any_sync(0xffffffffu, bad);
-  if (lane == 0) {
-    s_live[threadIdx.x >> 5] = r < N && any;
-    if (r < N) live[r] = any && !bad;
+  if (lane == 0 && r < N) {
+    live[r] = any && !bad;
+    if (!any || bad) token_loss[r] = 0.f;
     if (bad) atomicCAS(ctrl + kCtrlError, 0u, kErrBadTarget);
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int n = 0;
-    for (int w = 0; w < 8; ++w) n += s_live[w];
-    if (n) atomicAdd(ctrl + kCtrlNValid, static_cast<uint32_t>(n));
   }
 }
 
 // A block per row. The entries that count are put in order of their ids (those that
 // share one, of their slots) by counting the ones before each.
-constexpr int kPrepareThreads = 128;
+constexpr int kPickThreads = 128;
 
-__global__ void __launch_bounds__(kPrepareThreads) distill_prepare_kernel(const DistillPrepareArgs a) {
+__global__ void __launch_bounds__(kPickThreads) distill_pick_kernel(const DistillPickArgs a) {
   __shared__ int s_id[kScoreMaxTeacher], s_sorted[kScoreMaxTeacher];
   const int64_t r = blockIdx.x;
-  const bool live = a.live[r] != 0;
-  if (a.xm)
-    copy_row(static_cast<const uint8_t*>(a.x) + r * a.row_bytes, static_cast<uint8_t*>(a.xm) + r * a.row_bytes, a.row_bytes,
-             live);
-  if (!a.parts) return;
+  if (r >= chunk_rows(a.chunk.live, a.chunk.off, a.chunk.rows)) return;
+  const int64_t from_row = row_of(a.chunk, r);
   uint2* parts = a.parts + r * a.num_tiles;
-  if (!live) {
-    for (int w = threadIdx.x; w < a.num_tiles; w += kPrepareThreads) parts[w] = make_uint2(0u, 0u);
-    return;
-  }
   constexpr int kNone = 0x7FFFFFFF;
-  for (int e = threadIdx.x; e < a.k; e += kPrepareThreads) {
-    const int64_t id = a.ids[r * a.ld_ids + e];
-    s_id[e] = teacher_there(id, teacher_logit(a.logits, r * a.ld_logits + e, a.dtype)) ? static_cast<int>(id) : kNone;
+  for (int e = threadIdx.x; e < a.k; e += kPickThreads) {
+    const int64_t id = a.ids[from_row * a.ld_ids + e];
+    s_id[e] = teacher_there(id, teacher_logit(a.logits, from_row * a.ld_logits + e, a.dtype)) ? static_cast<int>(id) : kNone;
     s_sorted[e] = kNone;
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.k; e += kPrepareThreads) {
+  for (int e = threadIdx.x; e < a.k; e += kPickThreads) {
     const int id = s_id[e];
     if (id == kNone) continue;
     int place = 0;
@@ -846,7 +913,7 @@ __global__ void __launch_bounds__(kPrepareThreads) distill_prepare_kernel(const 
     a.entries[r * a.k + place] = make_int2(id, e);
   }
   __syncthreads();
-  for (int w = threadIdx.x; w < a.num_tiles; w += kPrepareThreads) {
+  for (int w = threadIdx.x; w < a.num_tiles; w += kPickThreads) {
     uint64_t at = 0;
     int lo = 0;
 #pragma unroll 1
@@ -881,15 +948,18 @@ __global__ void __launch_bounds__(kDistillThreads) distill_rows_kernel(const Dis
   __shared__ float s_red[kDistillThreads / 32];
   __shared__ int64_t s_id[kScoreMaxTeacher];
   __shared__ float s_q[kScoreMaxTeacher];
-  const int64_t r = blockIdx.x;
+  const int64_t i = blockIdx.x;
   constexpr bool bf16 = sizeof(E) == 2;
   constexpr int kVec = bf16 ? 8 : 4;
-  uint8_t* zrow = static_cast<uint8_t*>(a.z) + r * a.ldv * sizeof(E);
-  if (!a.live[r]) {
-    if (threadIdx.x == 0) a.token_loss[r] = 0.f;
-    if (GRADIENT)
-      for (int64_t j = threadIdx.x * kVec; j < a.ldv; j += kDistillThreads * kVec)
-        *reinterpret_cast<uint4*>(zrow + j * sizeof(E)) = make_uint4(0, 0, 0, 0);
+  uint8_t* zrow = static_cast<uint8_t*>(a.z) + i * a.ldv * sizeof(E);
+  const int rows = chunk_rows(a.chunk.live, a.chunk.off, a.chunk.rows);
+  if (i >= rows) {
+    if (GRADIENT && i < tail_end(a.chunk, rows)) zero_row(zrow, a.ldv * sizeof(E), threadIdx.x, kDistillThreads);
+    return;
+  }
+  const int64_t r = row_of(a.chunk, i);
+  if (a.alive && !a.alive[r]) {
+    if (GRADIENT) zero_row(zrow, a.ldv * sizeof(E), threadIdx.x, kDistillThreads);
     return;
   }
   // entries that do not count have id -1 from here on
@@ -903,7 +973,7 @@ __global__ void __launch_bounds__(kDistillThreads) distill_rows_kernel(const Dis
     if (there) top = max_nan(top, v);
   }
   top = block_max<kDistillThreads>(top, s_red);
-  const float2* part = a.partials + r * a.groups;
+  const float2* part = a.partials + i * a.groups;
   float m = -INFINITY;
   for (int g = threadIdx.x; g < a.groups; g += kDistillThreads) m = max_nan(m, part[g].x);
   const float M = block_max<kDistillThreads>(m, s_red);
@@ -925,7 +995,7 @@ __global__ void __launch_bounds__(kDistillThreads) distill_rows_kernel(const Dis
   q /= total;
   float log_p = 0.f, term = 0.f;
   if (there) {
-    const float z = bf16 ? a.picked[r * a.k + e] : reinterpret_cast<const float*>(zrow)[s_id[e]];
+    const float z = bf16 ? a.picked[i * a.k + e] : reinterpret_cast<const float*>(zrow)[s_id[e]];
     log_p = fmaf(z - M, scale, -log_L);
     term = q > 0.f || q != q ? q * (rel - logf(total) - log_p) : 0.f;
     s_q[e] = q;
@@ -946,8 +1016,8 @@ __global__ void __launch_bounds__(kDistillThreads) distill_rows_kernel(const Dis
     __syncthreads();
     if (there) {
       float all = 0.f;
-      for (int i = 0; i < a.k; ++i)
-        if (s_id[i] == s_id[e]) all += s_q[i];
+      for (int j = 0; j < a.k; ++j)
+        if (s_id[j] == s_id[e]) all += s_q[j];
       const float d = factor * (expf(log_p) - all);
       if constexpr (bf16)
         reinterpret_cast<__nv_bfloat16*>(zrow)[s_id[e]] = __float2bfloat16_rn(d);
@@ -984,20 +1054,31 @@ unsigned blocks_of(int64_t n, int64_t per) { return static_cast<unsigned>((n + p
 template <class E, class Z>
 cudaError_t launch_rows(const ScoreRowsArgs& a, cudaStream_t s) {
   if (a.top == 0)
-    score_warp_rows_kernel<E><<<blocks_of(a.rows, kWarpRows), 32 * kWarpRows, 0, s>>>(a);
-  else if (a.rows <= kFewRows)
-    score_rows_kernel<E, Z, 1024><<<a.rows, 1024, 0, s>>>(a);
+    score_warp_rows_kernel<E><<<blocks_of(a.chunk.rows, kWarpRows), 32 * kWarpRows, 0, s>>>(a);
+  else if (a.chunk.rows <= kFewRows)
+    score_rows_kernel<E, Z, 1024><<<a.chunk.rows, 1024, 0, s>>>(a);
   else
-    score_rows_kernel<E, Z, 128><<<a.rows, 128, 0, s>>>(a);
+    score_rows_kernel<E, Z, 128><<<a.chunk.rows, 128, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_score_stats_f32(const float* z, int64_t ldv, int rows, int64_t V, int groups, float c, float inv_temperature,
-                                   float2* partials, float* part_s, cudaStream_t s) {
-  score_stats_f32_kernel<<<blocks_of(static_cast<int64_t>(rows) * groups, 8), 256, 0, s>>>(z, ldv, rows, V, groups, c,
-                                                                                         inv_temperature, partials, part_s);
+cudaError_t launch_score_stats_f32(const ScoreChunk& chunk, const float* z, int64_t ldv, int64_t V, int groups, float c,
+                                   float inv_temperature, float2* partials, float* part_s, cudaStream_t s) {
+  score_stats_f32_kernel<<<blocks_of(static_cast<int64_t>(chunk.rows) * groups, 8), 256, 0, s>>>(
+      chunk, z, ldv, V, groups, c, inv_temperature, partials, part_s);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_score_order(const int64_t* t, int64_t ignore_index, const uint8_t* live, int64_t N, int32_t* order,
+                               uint32_t* count, cudaStream_t s) {
+  score_order_kernel<<<1, 1024, 0, s>>>(t, ignore_index, live, N, order, count);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_score_skip(const ScoreSkipArgs& a, cudaStream_t s) {
+  score_skip_kernel<<<blocks_of(a.N, 4), 128, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -1006,31 +1087,27 @@ cudaError_t launch_score_rows(const ScoreRowsArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_score_prepare(const ScorePrepareArgs& a, cudaStream_t s) {
-  score_prepare_kernel<<<a.rows, 128, 0, s>>>(a);
+  score_prepare_kernel<<<a.chunk.rows, 128, 0, s>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t launch_score_dlogits(int bf16, const void* z, const float2* partials, int groups, void* d, int64_t ldv, int rows,
-                                 int64_t V, float c, float inv_temperature, const ScoreRow* row, float* dcorr, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(rows), blocks_of(ldv, kDlogitsThreads * (bf16 ? 8 : 4)));
+cudaError_t launch_score_dlogits(int bf16, const ScoreChunk& chunk, const void* z, const float2* partials, int groups, void* d,
+                                 int64_t ldv, int64_t V, float c, float inv_temperature, const ScoreRow* row, float* dcorr,
+                                 cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(chunk.rows), blocks_of(ldv, kDlogitsThreads * (bf16 ? 8 : 4)));
   if (bf16)
-    score_dlogits_bf16_kernel<<<grid, kDlogitsThreads, 0, s>>>(static_cast<const __half*>(z), partials, groups,
+    score_dlogits_bf16_kernel<<<grid, kDlogitsThreads, 0, s>>>(chunk, static_cast<const __half*>(z), partials, groups,
                                                               static_cast<__nv_bfloat16*>(d), ldv, V, c, row, dcorr);
   else
-    score_dlogits_f32_kernel<<<grid, kDlogitsThreads, 0, s>>>(static_cast<const float*>(z), static_cast<float*>(d), ldv, V, c,
-                                                             inv_temperature, row);
+    score_dlogits_f32_kernel<<<grid, kDlogitsThreads, 0, s>>>(chunk, static_cast<const float*>(z), static_cast<float*>(d), ldv,
+                                                             V, c, inv_temperature, row);
   return cudaGetLastError();
 }
 
-cudaError_t launch_score_dx(const float* part, int splits, int64_t split_stride, int rows, int64_t H, const void* W,
-                            const ScoreRow* row, const float* dcorr, void* dx, cudaStream_t s) {
-  score_dx_kernel<<<dim3(static_cast<unsigned>(rows), blocks_of(H, 512)), 128, 0, s>>>(
-      part, splits, split_stride, H, static_cast<const __nv_bfloat16*>(W), row, dcorr, static_cast<__nv_bfloat16*>(dx));
-  return cudaGetLastError();
-}
-
-cudaError_t launch_score_cast(const float* in, void* out, int64_t n, cudaStream_t s) {
-  score_cast_kernel<<<blocks_of(n / 8, 256), 256, 0, s>>>(reinterpret_cast<const float4*>(in), static_cast<uint4*>(out), n / 8);
+cudaError_t launch_score_dx(const ScoreChunk& chunk, const float* part, int splits, int64_t split_stride, int64_t H,
+                            const void* W, const ScoreRow* row, const float* dcorr, void* dx, cudaStream_t s) {
+  score_dx_kernel<<<dim3(static_cast<unsigned>(chunk.rows), blocks_of(H, 512)), 128, 0, s>>>(
+      chunk, part, splits, split_stride, H, static_cast<const __nv_bfloat16*>(W), row, dcorr, static_cast<__nv_bfloat16*>(dx));
   return cudaGetLastError();
 }
 
@@ -1040,28 +1117,30 @@ cudaError_t launch_score_report(const uint32_t* ctrl, uint32_t* host_error, cuda
 }
 
 cudaError_t launch_distill_rows(const DistillArgs& a, cudaStream_t s) {
+  const int rows = a.chunk.rows;
   if (a.bf16) {
     if (a.gradient)
-      distill_rows_kernel<__nv_bfloat16, true><<<a.rows, kDistillThreads, 0, s>>>(a);
+      distill_rows_kernel<__nv_bfloat16, true><<<rows, kDistillThreads, 0, s>>>(a);
     else
-      distill_rows_kernel<__nv_bfloat16, false><<<a.rows, kDistillThreads, 0, s>>>(a);
+      distill_rows_kernel<__nv_bfloat16, false><<<rows, kDistillThreads, 0, s>>>(a);
   } else {
     if (a.gradient)
-      distill_rows_kernel<float, true><<<a.rows, kDistillThreads, 0, s>>>(a);
+      distill_rows_kernel<float, true><<<rows, kDistillThreads, 0, s>>>(a);
     else
-      distill_rows_kernel<float, false><<<a.rows, kDistillThreads, 0, s>>>(a);
+      distill_rows_kernel<float, false><<<rows, kDistillThreads, 0, s>>>(a);
   }
   return cudaGetLastError();
 }
 
 cudaError_t launch_distill_live(const int64_t* ids, int64_t ld_ids, const void* logits, int64_t ld_logits, int dtype,
-                                int64_t N, int k, int64_t V, uint8_t* live, uint32_t* ctrl, cudaStream_t s) {
-  distill_live_kernel<<<blocks_of(N, 8), 256, 0, s>>>(ids, ld_ids, logits, ld_logits, dtype, N, k, V, live, ctrl);
+                                int64_t N, int k, int64_t V, uint8_t* live, float* token_loss, uint32_t* ctrl,
+                                cudaStream_t s) {
+  distill_live_kernel<<<blocks_of(N, 8), 256, 0, s>>>(ids, ld_ids, logits, ld_logits, dtype, N, k, V, live, token_loss, ctrl);
   return cudaGetLastError();
 }
 
-cudaError_t launch_distill_prepare(const DistillPrepareArgs& a, cudaStream_t s) {
-  distill_prepare_kernel<<<a.rows, kPrepareThreads, 0, s>>>(a);
+cudaError_t launch_distill_pick(const DistillPickArgs& a, cudaStream_t s) {
+  distill_pick_kernel<<<a.chunk.rows, kPickThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -29,9 +29,12 @@ struct ScoreRow {
 
 // One product z = x Wt on 256 x 512 tiles of CTA pairs, and what becomes of z.
 struct ScoreGemmArgs {
-  int32_t num_m, num_n;          // tiles
+  int32_t num_n;                 // tiles of columns
   int32_t kb_total;              // 64-deep k-blocks
-  int32_t rows, cols;            // valid rows; V
+  int32_t rows, cols;            // rows of the chunk; V
+  int32_t least;                 // rows that are computed whatever `live` says (0 or 1)
+  const uint32_t* live;          // how many of the call's rows count, or null: all do
+  int64_t off;                   // the chunk's first row, of those
   int32_t groups;                // partials per row: ceil(V / 64)
   int32_t store;                 // statistics: also store the scaled logits
   float c;                       // log2(e) / temperature, times score_gain(H)
@@ -70,68 +73,126 @@ int score_gemm_max_clusters();
 // leave a tenth of that.
 inline double score_gain(int64_t H) { return 1.0 + 0.13 / 8388608.0 * (static_cast<double>(H) / 16.0); }
 
+// ------------------------------------------------ flce_score_backward.cu
+
+struct ScoreBackwardMaps {
+  CUtensorMap d, w, part;        // dx = d W: d (box 64 x 128), W (64 x 64), fp32 partial sums (32 x 128 x 1)
+  CUtensorMap dt, x, dw32, dw16; // dW = dt x: d (64 x 64), x (64 x 64), fp32 (32 x 128 x 1), bf16 (64 x 128)
+};
+struct ScoreBackwardArgs {
+  int32_t rows;                  // of the chunk; d and x hold zeros from the rows that count up to a multiple of 256
+  int32_t H, V;
+  int32_t dx, dw;                // which of the products
+  int32_t splits, kb_v, kb_per_split;  // of dx's sum over V
+  int32_t group_m;               // tile rows per group, of dx
+  int32_t dw_bf16;               // the last chunk stores dW as bf16
+  int32_t last;                  // without `live`: this is the last chunk
+  const uint32_t* live;          // as ScoreGemmArgs
+  int64_t off;
+  const float* dw_sum;           // dw_bf16: what dw32 describes
+  int32_t* claims;               // zero: the chunk's counter of units
+  uint32_t* ctrl;
+  uint64_t timeout_ns;
+};
+cudaError_t launch_score_backward(const ScoreBackwardMaps& maps, const ScoreBackwardArgs& args, int pairs, cudaStream_t s);
+
 // --------------------------------------------------------- flce_score.cu
 
+// A chunk: rows off .. off + rows - 1 of the rows that count (`live` of them), each
+// the order[i]-th of the call; order null: all rows count, as they stand.
+struct ScoreChunk {
+  int32_t rows;
+  int64_t off;
+  const int32_t* order;
+  const uint32_t* live;
+};
+
 // The statistics of fp32 logits, as the product's epilogue takes them.
-cudaError_t launch_score_stats_f32(const float* z, int64_t ldv, int rows, int64_t V, int groups, float c,
+cudaError_t launch_score_stats_f32(const ScoreChunk& chunk, const float* z, int64_t ldv, int64_t V, int groups, float c,
                                    float inv_temperature, float2* partials, float* part_s, cudaStream_t s);
 
+// The rows that count, in order, and how many: t[i] != ignore_index, or live[i] != 0
+// where t is null.
+cudaError_t launch_score_order(const int64_t* t, int64_t ignore_index, const uint8_t* live, int64_t N, int32_t* order,
+                               uint32_t* count, cudaStream_t s);
+// What the rows that do not count get: zeros (any of the outputs may be null)
+struct ScoreSkipArgs {
+  int64_t N, ignore_index;
+  const int64_t* t;
+  const uint8_t* live;           // where t is null
+  int32_t top;
+  float* logprobs;
+  float* entropy;
+  float2* stats;
+  float* top_logprobs;
+  int64_t* top_ids;
+  void* dx;
+  int64_t row_bytes;             // of dx
+};
+cudaError_t launch_score_skip(const ScoreSkipArgs& a, cudaStream_t s);
+
 struct ScoreRowsArgs {
-  int32_t rows, top, groups;
+  ScoreChunk chunk;
+  int32_t top, groups;
   int32_t bf16;                  // x and W bf16 and z stored as fp16 y, or all fp32
   int64_t H, V, ldv, ignore_index;
   float c, inv_c;                // log2(e) / temperature, times gain
   float inv_temperature;
   float scale;                   // inv_temperature times gain
   float loss;                    // gain - 1
-  const void* x;                 // this chunk's rows
+  const void* x;                 // the call's, by row, as are t and the outputs
   const void* W;
   const int64_t* t;              // null: no given tokens
-  const float2* partials;
+  const float2* partials;        // by row of the chunk
   const float* part_s;
   const void* z;                 // [rows][ldv] fp16 y, or fp32 z; read for alternatives only
   float* logprobs;
   float* entropy;
   float2* stats;                 // largest z, log of the sum of exp((z - largest) / temperature)
-  float* top_logprobs;           // [rows][top]
+  float* top_logprobs;           // [N][top]
   int64_t* top_ids;
   const uint32_t* ctrl;
   uint32_t* host_error;          // pinned host word
 };
 cudaError_t launch_score_rows(const ScoreRowsArgs& a, cudaStream_t s);
 
-// rowc and, with xm, a copy of x whose rows that do not count are zero
+// A chunk's rows before a product: those of x that count side by side, with zeros
+// behind them up to a multiple of 256 rows (tail), or zeros in the place of those
+// that do not (order null).
+// With t: what the gradient of each row is made of.
 struct ScorePrepareArgs {
-  int32_t rows;
-  int32_t bf16;
-  int64_t H, V, ignore_index;
-  float inv_temperature;
+  ScoreChunk chunk;
+  int32_t tail;
+  int64_t row_bytes;
   const void* x;
-  void* xm;                      // may be null
-  const int64_t* t;
+  void* xm;
+  const uint8_t* alive;          // order null: zero where a row does not count, or null
+  // gradient
+  int64_t V, ignore_index;
+  float inv_temperature;
+  const int64_t* t;              // null: rows of x alone
   const float2* stats;
   const float* entropy;          // read where d_entropy is given
   const float* d_logprobs;       // may be null
   const float* d_entropy;        // may be null
-  ScoreRow* row;
+  ScoreRow* row;                 // by row of the chunk
   float* dcorr;
   uint32_t* ctrl;
 };
 cudaError_t launch_score_prepare(const ScorePrepareArgs& a, cudaStream_t s);
 
 // d from kept logits: y as fp16 with its groups' largest (partials), or fp32 z
-cudaError_t launch_score_dlogits(int bf16, const void* z, const float2* partials, int groups, void* d, int64_t ldv,
-                                 int rows, int64_t V, float c, float inv_temperature, const ScoreRow* row, float* dcorr,
+cudaError_t launch_score_dlogits(int bf16, const ScoreChunk& chunk, const void* z, const float2* partials, int groups, void* d,
+                                 int64_t ldv, int64_t V, float c, float inv_temperature, const ScoreRow* row, float* dcorr,
                                  cudaStream_t s);
-
-cudaError_t launch_score_dx(const float* part, int splits, int64_t split_stride, int rows, int64_t H, const void* W,
-                            const ScoreRow* row, const float* dcorr, void* dx, cudaStream_t s);
-cudaError_t launch_score_cast(const float* in, void* out, int64_t n, cudaStream_t s);
+cudaError_t launch_score_dx(const ScoreChunk& chunk, const float* part, int splits, int64_t split_stride, int64_t H,
+                            const void* W, const ScoreRow* row, const float* dcorr, void* dx, cudaStream_t s);
 // hands ctrl's error on to the host's word
 cudaError_t launch_score_report(const uint32_t* ctrl, uint32_t* host_error, cudaStream_t s);
 
 struct DistillArgs {
-  int32_t rows, k, groups;
+  ScoreChunk chunk;
+  int32_t k, groups;
   int32_t bf16;
   int32_t dtype;                 // of the teacher's logits
   int32_t gradient;              // 1: z becomes d, in place
@@ -139,34 +200,32 @@ struct DistillArgs {
   float c;                       // log2(e) / temperature, times gain
   float temperature, inv_temperature;
   float scale;                   // inv_temperature times gain
-  const int64_t* ids;            // this chunk's
+  const int64_t* ids;            // the call's, by row, as are logits and token_loss
   const void* logits;
-  const float2* partials;
+  const float2* partials;        // by row of the chunk
   const float* picked;           // [rows][k]: z of the entries that count (fp32: taken from z)
   void* z;                       // [rows][ldv] fp16 y / fp32 z in, bf16 / fp32 d out
-  const uint8_t* live;           // [rows]
-  float* token_loss;             // [rows]
-  uint32_t* ctrl;                // kCtrlNValid: rows that count
+  float* token_loss;
+  const uint8_t* alive;          // as ScorePrepareArgs
+  const uint32_t* ctrl;          // kCtrlNValid: rows that count
 };
 cudaError_t launch_distill_rows(const DistillArgs& a, cudaStream_t s);
-// which of N rows have an entry, how many (ctrl), and ids out of range (ctrl's error)
+// which of N rows have an entry; the others' losses; ids out of range (ctrl's error;
+// their rows do not count)
 cudaError_t launch_distill_live(const int64_t* ids, int64_t ld_ids, const void* logits, int64_t ld_logits, int dtype,
-                                int64_t N, int k, int64_t V, uint8_t* live, uint32_t* ctrl, cudaStream_t s);
-
-// A chunk's rows before their product: a copy of x whose rows that do not count are
-// zero (xm not null), and the columns to pick (parts not null; ScoreGemmArgs)
-struct DistillPrepareArgs {
-  int32_t rows, k, dtype, num_tiles;
-  int64_t row_bytes, ld_ids, ld_logits;
-  const void* x;
-  void* xm;
-  const int64_t* ids;
+                                int64_t N, int k, int64_t V, uint8_t* live, float* token_loss, uint32_t* ctrl,
+                                cudaStream_t s);
+// the columns to pick of a chunk's rows (ScoreGemmArgs)
+struct DistillPickArgs {
+  ScoreChunk chunk;
+  int32_t k, dtype, num_tiles;
+  int64_t ld_ids, ld_logits;
+  const int64_t* ids;            // the call's
   const void* logits;
-  const uint8_t* live;
   uint2* parts;
   int2* entries;
 };
-cudaError_t launch_distill_prepare(const DistillPrepareArgs& a, cudaStream_t s);
+cudaError_t launch_distill_pick(const DistillPickArgs& a, cudaStream_t s);
 cudaError_t launch_distill_finish(const float* token_loss, int64_t N, const uint32_t* ctrl, float* loss,
                                   uint32_t* host_error, cudaStream_t s);
 

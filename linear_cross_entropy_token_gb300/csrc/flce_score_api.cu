@@ -38,15 +38,21 @@ Kept kept_layout(bool bf16, int64_t N, int64_t V) {
 // workspace's parts.
 struct Plan {
   int64_t chunk = 0, ldv = 0, groups = 0, splits = 1;
-  int64_t tile_n_dx = 0, tile_n_dw = 0;  // columns of the backward products' tiles
-  uint64_t ctrl = 0, z = 0, partials = 0, part_s = 0, row = 0, dcorr = 0, xm = 0, live = 0, parts = 0, entries = 0,
-           picked = 0, dw = 0, total = 0;
+  bool compact = false;  // chunks are of the rows that count
+  uint64_t ctrl = 0, claims = 0, lead = 0, z = 0, partials = 0, part_s = 0, row = 0, dcorr = 0, xm = 0, order = 0, live = 0,
+           parts = 0, entries = 0, picked = 0, dw = 0, total = 0;
 };
 
 struct Needs {
-  bool z, stats, gradient, dx, dw_cast;
+  bool z, stats, gradient, dx, dw_sum;
+  bool masked;      // some rows may not count
   int64_t teacher;  // entries a row
 };
+
+// Rows that do not count are left out of the products where that can spare a tile of
+// 256 rows (bf16; fp32 inputs are small models', whose products know no row count of
+// the device's).
+constexpr int64_t kCompactRows = 256;
 
 // Gradients: chunks, tile shapes and splits are the loss's plan with both
 // products in one launch. Forward alone: as many tokens as the budget holds, in
@@ -67,8 +73,6 @@ flce_status make_plan(flce_handle_t h, int64_t N, int64_t H, int64_t V, const Ne
     if (st != FLCE_OK) return fail(h, st, "no chunk of these sizes fits the HBM budget");
     p.chunk = lp.chunk;
     p.splits = lp.dx_splits;
-    p.tile_n_dx = lp.tile_n_dx;
-    p.tile_n_dw = lp.tile_n_dw;
   } else {
     const uint64_t budget = h->cfg.hbm_budget_bytes ? h->cfg.hbm_budget_bytes : kDefaultBudget;
     const uint64_t a_row = (q.z ? p.ldv * es : 0) + (q.stats ? p.groups * 12ull : 0);
@@ -88,7 +92,11 @@ flce_status make_plan(flce_handle_t h, int64_t N, int64_t H, int64_t V, const Ne
     return at;
   };
   const uint64_t c = static_cast<uint64_t>(p.chunk);
-  p.ctrl = take(kCtrlWords * 4);
+  p.compact = bf16 && q.masked && (N > kCompactRows || q.teacher > 0);
+  // the control block and the chunks' counters of units, cleared together
+  p.claims = kCtrlWords * 4;
+  p.lead = p.claims + (q.gradient && c > 0 ? static_cast<uint64_t>(cdiv(N, p.chunk)) * 4 : 0);
+  p.ctrl = take(p.lead);
   if (q.z) p.z = take(c * p.ldv * es);
   // the statistics' partials are last read before dx's partial sums are written
   const bool dx_parts = q.dx && (bf16 || p.splits > 1);
@@ -98,9 +106,10 @@ flce_status make_plan(flce_handle_t h, int64_t N, int64_t H, int64_t V, const Ne
   if (q.gradient) {
     p.row = take(c * sizeof(ScoreRow));
     p.dcorr = take(c * 4);
-    p.xm = take(c * H * es);
-    if (q.dw_cast) p.dw = take(static_cast<uint64_t>(V) * H * 4);
+    if (q.dw_sum) p.dw = take(static_cast<uint64_t>(V) * H * 4);
   }
+  if (q.gradient || p.compact) p.xm = take(c * H * es);
+  if (q.masked) p.order = take(static_cast<uint64_t>(std::max<int64_t>(N, 1)) * 4);
   if (q.teacher) {
     p.live = take(static_cast<uint64_t>(std::max<int64_t>(N, 1)));
     if (bf16) {
@@ -145,29 +154,24 @@ flce_status check_workspace(flce_handle_t h, const void* ws, uint64_t bytes, uin
   return FLCE_OK;
 }
 
-// The pairs that run at once. The backward's products run on both pair shapes,
-// whatever shape the handle's loss was created with.
+// The pairs that run at once (whatever tile shape the handle's loss was created with)
 flce_status ensure_clusters(flce_handle_t h) {
   if (!is_bf16(h)) return FLCE_OK;
-  if (h->score_clusters == 0) {
-    if (h->wide_clusters <= 0) h->wide_clusters = umma_wide_max_clusters();
-    if (h->pair_clusters <= 0) h->pair_clusters = umma_pair_max_clusters();
-    h->score_clusters = score_gemm_max_clusters();
-  }
-  if (h->score_clusters <= 0 || h->wide_clusters <= 0 || h->pair_clusters <= 0)
+  if (h->score_clusters == 0) h->score_clusters = score_gemm_max_clusters();
+  if (h->score_clusters <= 0)
     return fail(h, FLCE_ERR_UNSUPPORTED, "no CTA pair fits the device");
   return FLCE_OK;
 }
 
-flce_status clear_ctrl(flce_handle_t h, uint32_t* ctrl, cudaStream_t s) {
-  const cudaError_t e = cudaMemsetAsync(ctrl, 0, kCtrlWords * 4, s);
+flce_status clear_ctrl(flce_handle_t h, uint32_t* ctrl, uint64_t bytes, cudaStream_t s) {
+  const cudaError_t e = cudaMemsetAsync(ctrl, 0, bytes, s);
   return e == cudaSuccess ? FLCE_OK : fail(h, FLCE_ERR_CUDA, "memset: %s", cudaGetErrorString(e));
 }
 
 struct Product {
-  const void* x;
+  const void* x;   // the chunk's rows
   const void* W;
-  int rows;
+  ScoreChunk chunk;
   int64_t H, V;
   const Plan* p;
   float c;                 // times the product's gain
@@ -182,31 +186,33 @@ struct Product {
 
 // z of a chunk and its statistics: stored to z where given
 flce_status run_stats(flce_handle_t h, const Product& q, void* z, float2* partials, float* part_s, cudaStream_t s) {
-  const double dr = q.rows, dH = static_cast<double>(q.H), dV = static_cast<double>(q.V);
+  const double dr = q.chunk.rows, dH = static_cast<double>(q.H), dV = static_cast<double>(q.V);
   const int groups = static_cast<int>(q.p->groups);
   if (!is_bf16(h)) {
     float* zf = static_cast<float*>(z);
     FLCE_LAUNCH(FLCE_K_SIMT_GEMM, 2 * dr * dH * dV, 4 * (dr * dH + dV * dH + dr * dV),
                 launch_simt_gemm_f32(static_cast<const float*>(q.x), q.H, 1, static_cast<const float*>(q.W), 1, q.H, zf,
-                                     q.p->ldv, q.rows, q.V, q.H, 0, 1, nullptr, s));
+                                     q.p->ldv, q.chunk.rows, q.V, q.H, 0, 1, nullptr, s));
     if (partials)
       FLCE_LAUNCH(FLCE_K_SCORE_STATS, 0.0, 4 * dr * dV + 12 * dr * groups,
-                  launch_score_stats_f32(zf, q.p->ldv, q.rows, q.V, groups, q.c, q.inv_temperature,
+                  launch_score_stats_f32(q.chunk, zf, q.p->ldv, q.V, groups, q.c, q.inv_temperature,
                                          partials, part_s, s));
     return FLCE_OK;
   }
   CUtensorMap mx, mw, mz;
   std::string why;
-  if (!map_bf16_2d(&mx, q.x, q.H, q.rows, q.H * 2, 64, 128, &why) || !map_bf16_2d(&mw, q.W, q.H, q.V, q.H * 2, 64, 128, &why))
+  if (!map_bf16_2d(&mx, q.x, q.H, q.chunk.rows, q.H * 2, 64, 128, &why) || !map_bf16_2d(&mw, q.W, q.H, q.V, q.H * 2, 64, 128, &why))
     return fail(h, FLCE_ERR_INVALID_ARG, "%s", why.c_str());
   mz = mx;  // not used without a store
-  if (z && !map_bf16_2d(&mz, z, q.V, q.rows, q.p->ldv * 2, 64, 128, &why))
+  if (z && !map_bf16_2d(&mz, z, q.V, q.chunk.rows, q.p->ldv * 2, 64, 128, &why))
     return fail(h, FLCE_ERR_INVALID_ARG, "%s", why.c_str());
   ScoreGemmArgs a{};
-  a.num_m = static_cast<int>(cdiv(q.rows, kTileRows));
+  const int num_m = static_cast<int>(cdiv(q.chunk.rows, kTileRows));
   a.num_n = static_cast<int>(cdiv(q.V, 2 * kBN));
   a.kb_total = static_cast<int>(cdiv(q.H, kBK));
-  a.rows = q.rows;
+  a.rows = q.chunk.rows;
+  a.live = q.chunk.live;
+  a.off = q.chunk.off;
   a.cols = static_cast<int>(q.V);
   a.groups = groups;
   a.store = z != nullptr;
@@ -220,124 +226,110 @@ flce_status run_stats(flce_handle_t h, const Product& q, void* z, float2* partia
   a.ctrl = q.ctrl;
   a.timeout_ns = h->timeout_ns;
   FLCE_LAUNCH(FLCE_K_SCORE_STATS, 2 * dr * dH * dV, 2 * (dr + dV) * dH + (z ? 2 * dr * dV : 0) + 12 * dr * groups,
-              launch_score_gemm(q.parts ? kScorePick : kScoreStats, mx, mw, mz, a, std::min(a.num_m * a.num_n, h->score_clusters), s));
+              launch_score_gemm(q.parts ? kScorePick : kScoreStats, mx, mw, mz, a, std::min(num_m * a.num_n, h->score_clusters), s));
   return FLCE_OK;
 }
 
 // d of a chunk straight from the product
 flce_status run_gradient(flce_handle_t h, const Product& q, void* d, const ScoreRow* row, float* dcorr, cudaStream_t s) {
-  const double dr = q.rows, dH = static_cast<double>(q.H), dV = static_cast<double>(q.V);
+  const double dr = q.chunk.rows, dH = static_cast<double>(q.H), dV = static_cast<double>(q.V);
   CUtensorMap mx, mw, md;
   std::string why;
-  if (!map_bf16_2d(&mx, q.x, q.H, q.rows, q.H * 2, 64, 128, &why) ||
+  if (!map_bf16_2d(&mx, q.x, q.H, q.chunk.rows, q.H * 2, 64, 128, &why) ||
       !map_bf16_2d(&mw, q.W, q.H, q.V, q.H * 2, 64, 128, &why) ||
-      !map_bf16_2d(&md, d, q.V, q.rows, q.p->ldv * 2, 64, 128, &why))
+      !map_bf16_2d(&md, d, q.V, q.chunk.rows, q.p->ldv * 2, 64, 128, &why))
     return fail(h, FLCE_ERR_INVALID_ARG, "%s", why.c_str());
   ScoreGemmArgs a{};
-  a.num_m = static_cast<int>(cdiv(q.rows, kTileRows));
+  const int num_m = static_cast<int>(cdiv(q.chunk.rows, kTileRows));
   a.num_n = static_cast<int>(cdiv(q.V, 2 * kBN));
   a.kb_total = static_cast<int>(cdiv(q.H, kBK));
-  a.rows = q.rows;
+  a.rows = q.chunk.rows;
+  a.live = q.chunk.live;
+  a.off = q.chunk.off;
   a.cols = static_cast<int>(q.V);
   a.groups = static_cast<int>(q.p->groups);
   a.c = q.c;
+  a.least = q.chunk.off == 0;  // zeros, where no row of the call counts
   a.row = row;
   a.dcorr = dcorr;
   a.ctrl = q.ctrl;
   a.timeout_ns = h->timeout_ns;
   FLCE_LAUNCH(FLCE_K_SCORE_GRADIENT, 2 * dr * dH * dV, 2 * (dr + dV) * dH + 2 * dr * dV,
-              launch_score_gemm(kScoreGradient, mx, mw, md, a, std::min(a.num_m * a.num_n, h->score_clusters), s));
+              launch_score_gemm(kScoreGradient, mx, mw, md, a, std::min(num_m * a.num_n, h->score_clusters), s));
   return FLCE_OK;
 }
 
-// dx = d W and dW (+)= dt x of a chunk, whichever is asked for. q.x: rows that do
-// not count are zero. row null: no entry to put right.
+// dx = d W and dW (+)= dt x of a chunk, whichever is asked for. row null: no entry to
+// put right.
 struct Backward {
   const void* d;
   float* part;         // dx's partial sums
-  void* dx;            // this chunk's rows, or null
-  float* dW;           // fp32, or null
+  void* dx;            // the call's, or null
+  void* dW;            // or null
+  int32_t dw_dtype;
+  float* dw_sum;       // bf16 dW: the chunks' sum so far
   const ScoreRow* row;
   const float* dcorr;
-  bool first;          // the call's first chunk
-  int32_t* claims;     // of the call's one-launch backwards so far
+  bool last;
+  int32_t* claims;     // the chunk's counter of units
 };
 
 flce_status run_backward(flce_handle_t h, const Product& q, const Backward& b, cudaStream_t s) {
-  const double dr = q.rows, dH = static_cast<double>(q.H), dV = static_cast<double>(q.V);
+  const double dr = q.chunk.rows, dH = static_cast<double>(q.H), dV = static_cast<double>(q.V);
   const int64_t H = q.H, V = q.V, ldv = q.p->ldv;
-  const int rows = q.rows;
-  const double dx_bytes = 2 * dr * dV + 2 * dV * dH + 4.0 * q.p->splits * dr * dH;
-  const double dw_bytes = 2 * dr * dV + 2 * dr * dH + (b.first ? 4.0 : 8.0) * dV * dH;
+  const int rows = q.chunk.rows;
+  const bool first = q.chunk.off == 0, to16 = b.dW && b.dw_dtype == FLCE_DTYPE_BF16;
+  const double dx_bytes = b.dx ? 2 * dr * dV + 2 * dV * dH + 4.0 * q.p->splits * dr * dH : 0.0;
+  const double dw_bytes = b.dW ? 2 * dr * dV + 2 * dr * dH + ((first ? 4.0 : 8.0) - (to16 && b.last ? 2.0 : 0.0)) * dV * dH : 0.0;
   if (!is_bf16(h)) {
     const float* d = static_cast<const float*>(b.d);
     if (b.dx)
       FLCE_LAUNCH(FLCE_K_SIMT_GEMM, 2 * dr * dV * dH, 2 * dx_bytes,
-                  launch_simt_gemm_f32(d, ldv, 1, static_cast<const float*>(q.W), H, 1, static_cast<float*>(b.dx), H, rows, H,
-                                       V, 0, static_cast<int>(q.p->splits), b.part, s));
+                  launch_simt_gemm_f32(d, ldv, 1, static_cast<const float*>(q.W), H, 1,
+                                       static_cast<float*>(b.dx) + q.chunk.off * H, H, rows, H, V, 0,
+                                       static_cast<int>(q.p->splits), b.part, s));
     if (b.dW)
       FLCE_LAUNCH(FLCE_K_SIMT_GEMM, 2 * dr * dV * dH, 2 * dw_bytes,
-                  launch_simt_gemm_f32(d, 1, ldv, static_cast<const float*>(q.x), H, 1, b.dW, H, V, H, rows, b.first ? 0 : 1,
-                                       1, nullptr, s));
+                  launch_simt_gemm_f32(d, 1, ldv, static_cast<const float*>(q.x), H, 1, static_cast<float*>(b.dW), H, V, H,
+                                       rows, first ? 0 : 1, 1, nullptr, s));
     return FLCE_OK;
   }
   std::string why;
-  DualMaps maps;
-  const int kb_v = static_cast<int>(cdiv(V, kBK));
-  const int kbps = static_cast<int>(cdiv(kb_v, q.p->splits));
-  const int S = static_cast<int>(cdiv(kb_v, kbps));
-  if (!map_bf16_2d(&maps.a[0], b.d, V, rows, ldv * 2, 64, 128, &why) ||
-      !map_bf16_2d(&maps.b[0], q.W, H, V, H * 2, 64, 64, &why) ||
-      (b.dx && !map_f32_3d(&maps.o[0], b.part, H, rows, S, H * 4, static_cast<uint64_t>(q.p->chunk) * H * 4, &why)) ||
-      !map_bf16_2d(&maps.a[1], b.d, V, rows, ldv * 2, 64, 64, &why) ||
-      !map_bf16_2d(&maps.b[1], q.x, H, rows, H * 2, 64, 64, &why) ||
-      (b.dW && !map_f32_3d(&maps.o[1], b.dW, H, V, 1, H * 4, static_cast<uint64_t>(V) * H * 4, &why)))
+  ScoreBackwardArgs a{};
+  a.kb_v = static_cast<int>(cdiv(V, kBK));
+  a.kb_per_split = static_cast<int>(cdiv(a.kb_v, q.p->splits));
+  a.splits = static_cast<int>(cdiv(a.kb_v, a.kb_per_split));
+  ScoreBackwardMaps m{};
+  float* dw32 = to16 ? b.dw_sum : static_cast<float*>(b.dW);
+  if (!map_bf16_2d(&m.d, b.d, V, rows, ldv * 2, 64, 128, &why) || !map_bf16_2d(&m.w, q.W, H, V, H * 2, 64, 64, &why) ||
+      (b.dx &&
+       !map_f32_3d(&m.part, b.part, H, rows, a.splits, H * 4, static_cast<uint64_t>(q.p->chunk) * H * 4, &why)) ||
+      !map_bf16_2d(&m.dt, b.d, V, rows, ldv * 2, 64, 64, &why) || !map_bf16_2d(&m.x, q.x, H, rows, H * 2, 64, 64, &why) ||
+      (dw32 && !map_f32_3d(&m.dw32, dw32, H, V, 1, H * 4, static_cast<uint64_t>(V) * H * 4, &why)) ||
+      (to16 && !map_bf16_2d(&m.dw16, b.dW, H, V, H * 2, 64, 128, &why)))
     return fail(h, FLCE_ERR_INVALID_ARG, "%s", why.c_str());
-  DualArgs a{};
-  UmmaArgs& dx = a.p[0];
-  dx.num_s = S;
-  dx.kb_total = kb_v;
-  dx.kb_per_split = kbps;
-  dx.raster = 2;
-  dx.rows = rows;
-  dx.cols = static_cast<int>(H);
-  dx.ctrl = q.ctrl;
-  dx.timeout_ns = h->timeout_ns;
-  UmmaArgs& dw = a.p[1];
-  dw = dx;
-  dw.num_s = 1;
-  dw.kb_total = dw.kb_per_split = static_cast<int>(cdiv(rows, kBK));
-  dw.raster = 1;
-  dw.rows = static_cast<int>(V);
-  dw.reduce_add = b.first ? 0 : 1;
-  auto shape_of = [](int64_t cols) { return cols == 2 * kBN ? kShapeWide : kShapePair; };
-  if (b.dx && b.dW) {
-    const int shape = shape_of(q.p->tile_n_dx);
-    const bool wide = shape == kShapeWide;
-    const int64_t tile = wide ? 2 * kBN : kBN;
-    const int slots = wide ? h->wide_clusters : h->pair_clusters;
-    dx.num_m = static_cast<int>(cdiv(rows, kTileRows));
-    dw.num_m = static_cast<int>(cdiv(V, kTileRows));
-    dx.num_n = dw.num_n = static_cast<int>(cdiv(H, tile));
-    a.units0 = dx.num_m * dx.num_n * S;
-    dx.group_m = group_for(h, shape, dx.num_m, dx.num_n, S, std::min(a.units0, slots));
-    a.sched_ctr = reinterpret_cast<int32_t*>(q.ctrl + kCtrlSched);
-    a.sched_base = *b.claims;
-    const int units = a.units0 + dw.num_m * dw.num_n;
-    const int pairs = std::min(units, slots);
-    FLCE_LAUNCH(FLCE_K_GEMM_DX_DW, 4 * dr * dV * dH, dx_bytes + dw_bytes,
-                wide ? launch_umma_wide_dual(maps, a, pairs, s) : launch_umma_pair_dual(maps, a, pairs, s));
-    *b.claims += units + pairs;
-  } else if (b.dx) {
-    FLCE_LAUNCH(FLCE_K_GEMM_DX, 2 * dr * dV * dH, dx_bytes,
-                launch_gemm(h, shape_of(q.p->tile_n_dx), kUmmaDxF32, maps.a[0], maps.b[0], maps.o[0], dx, rows, s));
-  } else if (b.dW) {
-    FLCE_LAUNCH(FLCE_K_GEMM_DW, 2 * dr * dV * dH, dw_bytes,
-                launch_gemm(h, shape_of(q.p->tile_n_dw), kUmmaDw, maps.a[1], maps.b[1], maps.o[1], dw, V, s));
-  }
+  a.rows = rows;
+  a.H = static_cast<int>(H);
+  a.V = static_cast<int>(V);
+  a.dx = b.dx != nullptr;
+  a.dw = b.dW != nullptr;
+  const int num_m = static_cast<int>(cdiv(rows, kTileRows)), num_n = static_cast<int>(cdiv(H, 2 * kBN));
+  const int units0 = a.dx ? num_m * num_n * a.splits : 0;
+  const int units = units0 + (a.dw ? static_cast<int>(cdiv(V, kTileRows)) * num_n : 0);
+  a.group_m = a.dx ? group_for(h, kShapeWide, num_m, num_n, a.splits, std::min(units0, h->score_clusters)) : 1;
+  a.dw_bf16 = to16;
+  a.last = b.last;
+  a.live = q.chunk.live;
+  a.off = q.chunk.off;
+  a.dw_sum = dw32;
+  a.claims = b.claims;
+  a.ctrl = q.ctrl;
+  a.timeout_ns = h->timeout_ns;
+  FLCE_LAUNCH(FLCE_K_SCORE_BACKWARD, 2 * dr * dV * dH * (a.dx + a.dw), dx_bytes + dw_bytes,
+              launch_score_backward(m, a, std::min(units, h->score_clusters), s));
   if (b.dx)
-    FLCE_LAUNCH(FLCE_K_DX_REDUCE, 0.0, 4.0 * S * dr * dH + 4 * dr * dH,
-                launch_score_dx(b.part, S, q.p->chunk * H, rows, H, q.W, b.row, b.dcorr, b.dx, s));
+    FLCE_LAUNCH(FLCE_K_DX_REDUCE, 0.0, 4.0 * a.splits * dr * dH + 4 * dr * dH,
+                launch_score_dx(q.chunk, b.part, a.splits, q.p->chunk * H, H, q.W, b.row, b.dcorr, b.dx, s));
   return FLCE_OK;
 }
 
@@ -367,15 +359,55 @@ flce_status logprobs_check(flce_handle_t h, const flce_logprobs_args* r, bool ba
 
 flce_status logprobs_plan(flce_handle_t h, const flce_logprobs_args* r, bool backward, int32_t dw_dtype, bool dx, Plan* p) {
   Needs q{};
+  q.masked = r->t != nullptr;
   if (backward) {
     q.z = q.gradient = true;
     q.dx = dx;
-    q.dw_cast = dw_dtype == FLCE_DTYPE_BF16;
+    q.dw_sum = dw_dtype == FLCE_DTYPE_BF16;
   } else {
     q.z = !r->kept && (r->top > 0 || !is_bf16(h));
     q.stats = true;
   }
   return make_plan(h, r->N, r->H, r->V, q, p);
+}
+
+// The rows that count in order, what the others get, and the chunks of the former
+flce_status logprobs_rows(flce_handle_t h, const flce_logprobs_args* r, const Plan& p, uint8_t* ws, void* dx, bool backward,
+                          cudaStream_t s) {
+  if (!p.compact) return FLCE_OK;
+  const double n = static_cast<double>(r->N);
+  FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 12.0 * n,
+              launch_score_order(r->t, r->ignore_index, nullptr, r->N, reinterpret_cast<int32_t*>(ws + p.order),
+                                 reinterpret_cast<uint32_t*>(ws + p.ctrl) + kCtrlNValid, s));
+  if (backward && !dx) return FLCE_OK;
+  ScoreSkipArgs a{};
+  a.N = r->N;
+  a.ignore_index = r->ignore_index;
+  a.t = r->t;
+  if (backward) {
+    a.dx = dx;
+    a.row_bytes = r->H * 2;
+  } else {
+    a.top = r->top;
+    a.logprobs = r->logprobs;
+    a.entropy = r->entropy;
+    a.stats = reinterpret_cast<float2*>(r->stats);
+    a.top_logprobs = r->top_logprobs;
+    a.top_ids = r->top_ids;
+  }
+  FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 8.0 * n, launch_score_skip(a, s));
+  return FLCE_OK;
+}
+
+ScoreChunk chunk_of(const Plan& p, uint8_t* ws, int64_t off, int64_t N) {
+  ScoreChunk q{};
+  q.rows = static_cast<int32_t>(std::min(p.chunk, N - off));
+  q.off = off;
+  if (p.compact) {
+    q.order = reinterpret_cast<const int32_t*>(ws + p.order);
+    q.live = reinterpret_cast<const uint32_t*>(ws + p.ctrl) + kCtrlNValid;
+  }
+  return q;
 }
 
 }  // namespace
@@ -423,21 +455,33 @@ flce_status flce_logprobs_forward(flce_handle_t h, const flce_logprobs_args* r, 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint8_t* kept = static_cast<uint8_t*>(r->kept);
   uint32_t* ctrl = reinterpret_cast<uint32_t*>(ws + p.ctrl);
-  st = clear_ctrl(h, ctrl, s);
+  st = clear_ctrl(h, ctrl, p.lead, s);
+  if (st != FLCE_OK) return st;
+  st = logprobs_rows(h, r, p, ws, nullptr, false, s);
   if (st != FLCE_OK) return st;
   const Kept K = kept_layout(bf16, r->N, r->V);
   const double gain = bf16 ? score_gain(r->H) : 1.0, c = gain * kLog2e / r->temperature;
   const float inv_t = static_cast<float>(1.0 / r->temperature);
   for (int64_t off = 0; off < r->N; off += p.chunk) {
-    const int rows = static_cast<int>(std::min(p.chunk, r->N - off));
-    const Product q{static_cast<const uint8_t*>(r->x) + off * r->H * es, r->W, rows, r->H, r->V, &p, static_cast<float>(c), inv_t, ctrl};
+    const ScoreChunk chunk = chunk_of(p, ws, off, r->N);
+    const void* x = static_cast<const uint8_t*>(r->x) + off * r->H * es;
+    if (p.compact) {
+      x = ws + p.xm;
+      ScorePrepareArgs a{};
+      a.chunk = chunk;
+      a.row_bytes = r->H * static_cast<int64_t>(es);
+      a.x = r->x;
+      a.xm = ws + p.xm;
+      FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 2.0 * chunk.rows * r->H * es, launch_score_prepare(a, s));
+    }
+    const Product q{x, r->W, chunk, r->H, r->V, &p, static_cast<float>(c), inv_t, ctrl};
     void* z = kept ? kept + off * p.ldv * es : (r->top > 0 || !bf16) ? ws + p.z : nullptr;
     float2* partials = reinterpret_cast<float2*>(kept ? kept + K.partials + off * p.groups * 8 : ws + p.partials);
     float* part_s = reinterpret_cast<float*>(ws + p.part_s);
     st = run_stats(h, q, z, partials, part_s, s);
     if (st != FLCE_OK) return st;
     ScoreRowsArgs a{};
-    a.rows = rows;
+    a.chunk = chunk;
     a.top = r->top;
     a.groups = static_cast<int>(p.groups);
     a.bf16 = bf16;
@@ -450,20 +494,20 @@ flce_status flce_logprobs_forward(flce_handle_t h, const flce_logprobs_args* r, 
     a.inv_temperature = inv_t;
     a.scale = static_cast<float>(gain / r->temperature);
     a.loss = static_cast<float>(gain - 1.0);
-    a.x = q.x;
+    a.x = r->x;
     a.W = r->W;
-    a.t = r->t ? r->t + off : nullptr;
+    a.t = r->t;
     a.partials = partials;
     a.part_s = part_s;
     a.z = z;
-    a.logprobs = r->logprobs ? r->logprobs + off : nullptr;
-    a.entropy = r->entropy + off;
-    a.stats = reinterpret_cast<float2*>(r->stats) + off;
-    a.top_logprobs = r->top_logprobs ? r->top_logprobs + off * r->top : nullptr;
-    a.top_ids = r->top_ids ? r->top_ids + off * r->top : nullptr;
+    a.logprobs = r->logprobs;
+    a.entropy = r->entropy;
+    a.stats = reinterpret_cast<float2*>(r->stats);
+    a.top_logprobs = r->top_logprobs;
+    a.top_ids = r->top_ids;
     a.ctrl = ctrl;
     a.host_error = h->host_ctrl + kHostScoreError;
-    FLCE_LAUNCH(FLCE_K_SCORE_ROWS, 0.0, rows * (12.0 * p.groups + (r->top + 1.0) * r->H * es + 12.0 * r->top + 28.0),
+    FLCE_LAUNCH(FLCE_K_SCORE_ROWS, 0.0, chunk.rows * (12.0 * p.groups + (r->top + 1.0) * r->H * es + 12.0 * r->top + 28.0),
                 launch_score_rows(a, s));
   }
   return FLCE_OK;
@@ -496,44 +540,45 @@ flce_status flce_logprobs_backward(flce_handle_t h, const flce_logprobs_args* r,
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const uint8_t* kept = static_cast<const uint8_t*>(r->kept);
   uint32_t* ctrl = reinterpret_cast<uint32_t*>(ws + p.ctrl);
-  st = clear_ctrl(h, ctrl, s);
+  st = clear_ctrl(h, ctrl, p.lead, s);
+  if (st != FLCE_OK) return st;
+  st = logprobs_rows(h, r, p, ws, dx, true, s);
   if (st != FLCE_OK) return st;
   const Kept K = kept_layout(bf16, r->N, r->V);
   const double gain = bf16 ? score_gain(r->H) : 1.0;
   const float c = static_cast<float>(gain * kLog2e / r->temperature);
   const float inv_t = static_cast<float>(1.0 / r->temperature);
-  const bool cast = dW && dw_dtype == FLCE_DTYPE_BF16;
   ScoreRow* row = reinterpret_cast<ScoreRow*>(ws + p.row);
   float* dcorr = reinterpret_cast<float*>(ws + p.dcorr);
   void* d = ws + p.z;
-  int32_t claims = 0;
-  for (int64_t off = 0; off < r->N; off += p.chunk) {
-    const int rows = static_cast<int>(std::min(p.chunk, r->N - off));
-    const double dr = rows, dV = static_cast<double>(r->V);
+  int32_t* claims = reinterpret_cast<int32_t*>(ws + p.claims);
+  for (int64_t off = 0; off < r->N; off += p.chunk, ++claims) {
+    const ScoreChunk chunk = chunk_of(p, ws, off, r->N);
+    const double dr = chunk.rows, dV = static_cast<double>(r->V);
     ScorePrepareArgs a{};
-    a.rows = rows;
-    a.bf16 = bf16;
-    a.H = r->H;
+    a.chunk = chunk;
+    a.tail = 1;
+    a.row_bytes = r->H * static_cast<int64_t>(es);
+    a.x = r->x;
+    a.xm = ws + p.xm;
     a.V = r->V;
     a.ignore_index = r->ignore_index;
     a.inv_temperature = inv_t;
-    a.x = static_cast<const uint8_t*>(r->x) + off * r->H * es;
-    a.xm = ws + p.xm;
-    a.t = r->t + off;
-    a.stats = reinterpret_cast<const float2*>(r->stats) + off;
-    a.entropy = r->entropy + off;
-    a.d_logprobs = d_logprobs ? d_logprobs + off : nullptr;
-    a.d_entropy = d_entropy ? d_entropy + off : nullptr;
+    a.t = r->t;
+    a.stats = reinterpret_cast<const float2*>(r->stats);
+    a.entropy = r->entropy;
+    a.d_logprobs = d_logprobs;
+    a.d_entropy = d_entropy;
     a.row = row;
     a.dcorr = dcorr;
     a.ctrl = ctrl;
     FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 2.0 * dr * r->H * es + 50.0 * dr, launch_score_prepare(a, s));
-    const Product q{ws + p.xm, r->W, rows, r->H, r->V, &p, c, inv_t, ctrl};
+    const Product q{ws + p.xm, r->W, chunk, r->H, r->V, &p, c, inv_t, ctrl};
     if (kept) {
       FLCE_LAUNCH(FLCE_K_SCORE_DLOGITS, 0.0, 2.0 * es * dr * dV,
-                  launch_score_dlogits(bf16, kept + off * p.ldv * es,
+                  launch_score_dlogits(bf16, chunk, kept + off * p.ldv * es,
                                        reinterpret_cast<const float2*>(kept + K.partials) + off * p.groups,
-                                       static_cast<int>(p.groups), d, p.ldv, rows, r->V, c, inv_t, row, dcorr, s));
+                                       static_cast<int>(p.groups), d, p.ldv, r->V, c, inv_t, row, dcorr, s));
     } else if (bf16) {
       st = run_gradient(h, q, d, row, dcorr, s);
       if (st != FLCE_OK) return st;
@@ -541,22 +586,13 @@ flce_status flce_logprobs_backward(flce_handle_t h, const flce_logprobs_args* r,
       st = run_stats(h, q, d, nullptr, nullptr, s);
       if (st != FLCE_OK) return st;
       FLCE_LAUNCH(FLCE_K_SCORE_DLOGITS, 0.0, 2.0 * es * dr * dV,
-                  launch_score_dlogits(0, d, nullptr, 0, d, p.ldv, rows, r->V, c, inv_t, row, dcorr, s));
+                  launch_score_dlogits(0, chunk, d, nullptr, 0, d, p.ldv, r->V, c, inv_t, row, dcorr, s));
     }
-    const Backward b{d,
-                     reinterpret_cast<float*>(ws + p.partials),
-                     dx ? static_cast<uint8_t*>(dx) + off * r->H * es : nullptr,
-                     !dW ? nullptr : cast ? reinterpret_cast<float*>(ws + p.dw) : static_cast<float*>(dW),
-                     row,
-                     dcorr,
-                     off == 0,
-                     &claims};
+    const Backward b{d,   reinterpret_cast<float*>(ws + p.partials), dx, dW, dw_dtype, reinterpret_cast<float*>(ws + p.dw), row,
+                     dcorr, off + p.chunk >= r->N, claims};
     st = run_backward(h, q, b, s);
     if (st != FLCE_OK) return st;
   }
-  const double el = static_cast<double>(r->V) * r->H;
-  if (cast)
-    FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 6.0 * el, launch_score_cast(reinterpret_cast<float*>(ws + p.dw), dW, r->V * r->H, s));
   FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 4.0, launch_score_report(ctrl, h->host_ctrl + kHostScoreError, s));
   return FLCE_OK;
 } catch (...) {
@@ -589,7 +625,8 @@ static flce_status distill_plan(flce_handle_t h, const flce_distill_args* r, Pla
   q.gradient = r->dx || r->dW;
   q.z = q.gradient || !is_bf16(h);
   q.dx = r->dx != nullptr;
-  q.dw_cast = r->dW && r->dw_dtype == FLCE_DTYPE_BF16;
+  q.dw_sum = r->dW && r->dw_dtype == FLCE_DTYPE_BF16;
+  q.masked = true;
   return make_plan(h, r->N, r->H, r->V, q, p);
 }
 
@@ -626,61 +663,72 @@ flce_status flce_distill(flce_handle_t h, const flce_distill_args* r, void* work
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint32_t* ctrl = reinterpret_cast<uint32_t*>(ws + p.ctrl);
   uint8_t* live = ws + p.live;
-  st = clear_ctrl(h, ctrl, s);
+  st = clear_ctrl(h, ctrl, p.lead, s);
   if (st != FLCE_OK) return st;
   const bool gradient = r->dx || r->dW;
-  const bool cast = r->dW && r->dw_dtype == FLCE_DTYPE_BF16;
   const double gain = bf16 ? score_gain(r->H) : 1.0;
   const float c = static_cast<float>(gain * kLog2e / r->temperature);
   const float inv_t = static_cast<float>(1.0 / r->temperature);
-  int32_t claims = 0;
+  const double n = static_cast<double>(r->N);
+  int32_t* claims = reinterpret_cast<int32_t*>(ws + p.claims);
   if (r->N == 0) {
     st = zero_dw(h, r->dW, r->dw_dtype, r->V, r->H, s);
     if (st != FLCE_OK) return st;
   } else {
-    FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, static_cast<double>(r->N) * r->K * (8 + ls),
+    FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, n * r->K * (8 + ls),
                 launch_distill_live(r->ids, r->ld_ids, r->logits, r->ld_logits, r->logits_dtype, r->N, static_cast<int>(r->K),
-                                    r->V, live, ctrl, s));
-  }
-  for (int64_t off = 0; off < r->N; off += p.chunk) {
-    const int rows = static_cast<int>(std::min(p.chunk, r->N - off));
-    const double dr = rows, dV = static_cast<double>(r->V);
-    const void* x = static_cast<const uint8_t*>(r->x) + off * r->H * es;
-    const int64_t* ids = r->ids + off * r->ld_ids;
-    const void* logits = static_cast<const uint8_t*>(r->logits) + off * r->ld_logits * ls;
-    Product q{x, r->W, rows, r->H, r->V, &p, c, inv_t, ctrl};
-    if (bf16) {
-      q.parts = reinterpret_cast<const uint2*>(ws + p.parts);
-      q.entries = reinterpret_cast<const int2*>(ws + p.entries);
-      q.picked = reinterpret_cast<float*>(ws + p.picked);
-      q.k = static_cast<int>(r->K);
+                                    r->V, live, r->token_loss, ctrl, s));
+    FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 5.0 * n,
+                launch_score_order(nullptr, 0, live, r->N, reinterpret_cast<int32_t*>(ws + p.order), ctrl + kCtrlNValid, s));
+    if (p.compact && r->dx) {
+      ScoreSkipArgs a{};
+      a.N = r->N;
+      a.live = live;
+      a.dx = r->dx;
+      a.row_bytes = r->H * 2;
+      FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, n, launch_score_skip(a, s));
     }
-    if (gradient) q.x = ws + p.xm;
+  }
+  for (int64_t off = 0; off < r->N; off += p.chunk, ++claims) {
+    const ScoreChunk chunk = chunk_of(p, ws, off, r->N);
+    const double dr = chunk.rows, dV = static_cast<double>(r->V);
+    const void* x = static_cast<const uint8_t*>(r->x) + off * r->H * es;
     if (bf16 || gradient) {
-      DistillPrepareArgs a{};
-      a.rows = rows;
+      ScorePrepareArgs a{};
+      a.chunk = chunk;
+      a.tail = gradient;
+      a.row_bytes = r->H * static_cast<int64_t>(es);
+      a.x = r->x;
+      a.xm = ws + p.xm;
+      a.alive = bf16 ? nullptr : live;
+      x = ws + p.xm;
+      FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 2.0 * dr * r->H * es, launch_score_prepare(a, s));
+    }
+    Product q{x, r->W, chunk, r->H, r->V, &p, c, inv_t, ctrl};
+    if (bf16) {
+      DistillPickArgs a{};
+      a.chunk = chunk;
       a.k = static_cast<int>(r->K);
       a.dtype = r->logits_dtype;
       a.num_tiles = static_cast<int>(cdiv(r->V, kScoreTileColumns));
-      a.row_bytes = r->H * static_cast<int64_t>(es);
       a.ld_ids = r->ld_ids;
       a.ld_logits = r->ld_logits;
-      a.x = x;
-      a.xm = gradient ? ws + p.xm : nullptr;
-      a.ids = ids;
-      a.logits = logits;
-      a.live = live + off;
-      a.parts = bf16 ? reinterpret_cast<uint2*>(ws + p.parts) : nullptr;
-      a.entries = bf16 ? reinterpret_cast<int2*>(ws + p.entries) : nullptr;
-      FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, (gradient ? 2.0 * dr * r->H * es : 0.0) + dr * r->K * (16.0 + ls),
-                  launch_distill_prepare(a, s));
+      a.ids = r->ids;
+      a.logits = r->logits;
+      a.parts = reinterpret_cast<uint2*>(ws + p.parts);
+      a.entries = reinterpret_cast<int2*>(ws + p.entries);
+      FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, dr * (r->K * (16.0 + ls) + 8.0 * a.num_tiles), launch_distill_pick(a, s));
+      q.parts = a.parts;
+      q.entries = a.entries;
+      q.picked = reinterpret_cast<float*>(ws + p.picked);
+      q.k = a.k;
     }
     void* z = gradient || !bf16 ? ws + p.z : nullptr;
     float2* partials = reinterpret_cast<float2*>(ws + p.partials);
     st = run_stats(h, q, z, partials, reinterpret_cast<float*>(ws + p.part_s), s);
     if (st != FLCE_OK) return st;
     DistillArgs a{};
-    a.rows = rows;
+    a.chunk = chunk;
     a.k = static_cast<int>(r->K);
     a.groups = static_cast<int>(p.groups);
     a.bf16 = bf16;
@@ -694,34 +742,25 @@ flce_status flce_distill(flce_handle_t h, const flce_distill_args* r, void* work
     a.temperature = static_cast<float>(r->temperature);
     a.inv_temperature = inv_t;
     a.scale = static_cast<float>(gain / r->temperature);
-    a.ids = ids;
-    a.logits = logits;
+    a.ids = r->ids;
+    a.logits = r->logits;
     a.partials = partials;
     a.picked = q.picked;
     a.z = z;
-    a.live = live + off;
-    a.token_loss = r->token_loss + off;
+    a.token_loss = r->token_loss;
+    a.alive = bf16 ? nullptr : live;
     a.ctrl = ctrl;
     FLCE_LAUNCH(FLCE_K_DISTILL_ROWS, 0.0,
                 dr * (r->K * (12.0 + ls) + 8.0 * p.groups) + (gradient ? 2.0 * es * dr * dV : 0.0),
                 launch_distill_rows(a, s));
     if (gradient) {
-      const Backward b{z,
-                       reinterpret_cast<float*>(ws + p.partials),
-                       r->dx ? static_cast<uint8_t*>(r->dx) + off * r->H * es : nullptr,
-                       !r->dW ? nullptr : cast ? reinterpret_cast<float*>(ws + p.dw) : static_cast<float*>(r->dW),
-                       nullptr,
-                       nullptr,
-                       off == 0,
-                       &claims};
+      const Backward b{z,       reinterpret_cast<float*>(ws + p.partials), r->dx, r->dW, r->dw_dtype,
+                       reinterpret_cast<float*>(ws + p.dw), nullptr, nullptr, off + p.chunk >= r->N, claims};
       st = run_backward(h, q, b, s);
       if (st != FLCE_OK) return st;
     }
   }
-  if (cast && r->N > 0)
-    FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 6.0 * r->V * r->H,
-                launch_score_cast(reinterpret_cast<float*>(ws + p.dw), r->dW, r->V * r->H, s));
-  FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 4.0 * r->N,
+  FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 4.0 * n,
               launch_distill_finish(r->token_loss, r->N, ctrl, r->loss, h->host_ctrl + kHostScoreError, s));
   return FLCE_OK;
 } catch (...) {

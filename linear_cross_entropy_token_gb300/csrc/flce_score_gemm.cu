@@ -31,56 +31,13 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "flce_internal.h"
-#include "flce_score.h"
-#include "ptx.cuh"
+#include "flce_score.cuh"
 
 namespace flce {
 namespace {
 
-constexpr int kStages = 4;
-constexpr uint32_t kABytes = kBM * kBK * 2;       // 128 rows of x
-constexpr uint32_t kBBytes = kBN * kBK * 2;       // 256 columns (rows of W)
-constexpr uint32_t kBHalf = kBBytes / 2;
-constexpr uint32_t kStageBytes = kABytes + kBBytes;
-constexpr uint32_t kEpiBytes = 128 * 128;         // 128 rows x 128 bytes
-constexpr uint32_t kSmemBytes = 1024 + kStages * kStageBytes + 2 * kEpiBytes + (2 * kStages + 4) * 8 + 16;
+constexpr uint32_t kSmemBytes = 1024 + kRing * (kRingA + kRingB) + 2 * kStagingBytes + (2 * kRing + 4) * 8 + 16;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-constexpr uint32_t kTmemCols = 512;
-constexpr int kThreads = 384;
-constexpr int kEpiThreads = 128;
-// registers move from the loading and issuing warpgroup to the two epilogues;
-// the split must fit what the launch holds (checked on the host)
-constexpr uint32_t kRegsCtl = 40, kRegsEpi = 232;
-constexpr int kLaunchRegs = 168;
-static_assert(128 * kRegsCtl + 256 * kRegsEpi <= kThreads * kLaunchRegs, "register split");
-
-__device__ __forceinline__ float ex2(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-
-// the larger, NaN if either is
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
-  const uint64_t t0 = globaltimer_ns();
-#pragma unroll 1
-  while (!mbar_try_wait(bar, parity))
-    if (globaltimer_ns() - t0 > timeout_ns) return;
-}
-
-// Eight 16-bit columns, the j-th such piece of a row of a 128-row x 128-byte staging
-// tile in the 128-byte swizzle. Each piece is staged as it is computed: a group's 32
-// words at once would take registers that three groups of logits leave no room for.
-__device__ __forceinline__ void stage_piece(uint8_t* buf, int row, int j, const uint32_t (&w)[4]) {
-  reinterpret_cast<uint4*>(buf + row * 128)[j ^ (row & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 // 64 columns from two 32-register loads
 struct Group {
@@ -204,24 +161,24 @@ __device__ __forceinline__ void pick_columns(Group g, const ScoreGemmArgs& a, in
 }
 
 template <int MODE, bool STORE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     score_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmO, const ScoreGemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sA = smem;
-  uint8_t* sB = smem + kStages * kABytes;
-  uint8_t* sE = sB + kStages * kBBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sE + 2 * kEpiBytes);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4);
+  uint8_t* sB = smem + kRing * kRingA;
+  uint8_t* sE = sB + kRing * kRingB;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sE + 2 * kStagingBytes);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kRing + 4);
 
   const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
-  auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };
-  const uint32_t tfull_bar = bar0 + 8u * (2 * kStages);
-  const uint32_t tempty0_bar = bar0 + 8u * (2 * kStages + 1);
-  const uint32_t tempty1_bar = bar0 + 8u * (2 * kStages + 2);
-  const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 3);
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kRing + s); };
+  const uint32_t tfull_bar = bar0 + 8u * (2 * kRing);
+  const uint32_t tempty0_bar = bar0 + 8u * (2 * kRing + 1);
+  const uint32_t tempty1_bar = bar0 + 8u * (2 * kRing + 2);
+  const uint32_t drain_bar = bar0 + 8u * (2 * kRing + 3);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -230,13 +187,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int npairs = static_cast<int>(num_clusters_x());
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kRing; ++s) {
       mbar_init(full_bar(s), 1);   // used in CTA 0: both CTAs' loads land here
       mbar_init(empty_bar(s), 1);  // each CTA's own, released by the products' commit
     }
     mbar_init(tfull_bar, 1);
-    mbar_init(tempty0_bar, 2 * 2 * kEpiThreads);  // used in CTA 0: both CTAs' two epilogues
-    mbar_init(tempty1_bar, 2 * 2 * kEpiThreads);
+    mbar_init(tempty0_bar, 2 * 2 * kWarpgroup);  // used in CTA 0: both CTAs' two epilogues
+    mbar_init(tempty1_bar, 2 * 2 * kWarpgroup);
     mbar_init(drain_bar, 1);
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -245,7 +202,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_map(&tmO);
   }
   if (warp == 1) {
-    tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
+    tmem_alloc_pair(smem_u32(tmem_slot), kAccumulatorColumns);
     tmem_relinquish_pair();
   }
   __syncthreads();
@@ -254,34 +211,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
 
   // rows fastest: the pairs that run together share columns of W
-  const int units = a.num_m * a.num_n;
+  const int rows = max(chunk_rows(a.live, a.off, a.rows), a.least);
+  const int num_m = (rows + 2 * kBM - 1) / (2 * kBM);
+  const int units = num_m * a.num_n;
   if (warp < 4) {
-    warpgroup_regs_dec<kRegsCtl>();
+    warpgroup_regs_dec<kRegsControl>();
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------------- loads
       uint32_t n_issued = 0;
       bool failed = false;
       for (int u = pair; u < units && !failed; u += npairs) {
-        const int mA = (u % a.num_m) * 2 * kBM + static_cast<int>(rank) * kBM;
-        const int nB = (u / a.num_m) * 2 * kBN + static_cast<int>(rank) * (kBN / 2);
+        const int mA = (u % num_m) * 2 * kBM + static_cast<int>(rank) * kBM;
+        const int nB = (u / num_m) * 2 * kBN + static_cast<int>(rank) * (kBN / 2);
         for (int kb = 0; kb < a.kb_total; ++kb) {
-          const uint32_t stage = n_issued % kStages;
-          if (!mbar_wait_bounded_cluster(empty_bar(stage), ((n_issued / kStages) & 1u) ^ 1u, a.ctrl, a.timeout_ns)) {
+          const uint32_t stage = n_issued % kRing;
+          if (!mbar_wait_bounded_cluster(empty_bar(stage), ((n_issued / kRing) & 1u) ^ 1u, a.ctrl, a.timeout_ns)) {
             failed = true;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * kStageBytes);
+          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * (kRingA + kRingB));
           const uint32_t fb = mapa_shared(full_bar(stage), 0);
-          const uint32_t sb = smem_u32(sB + stage * kBBytes);
-          tma_load_2d_pair(smem_u32(sA + stage * kABytes), &tmA, fb, kb * kBK, mA);
+          const uint32_t sb = smem_u32(sB + stage * kRingB);
+          tma_load_2d_pair(smem_u32(sA + stage * kRingA), &tmA, fb, kb * kBK, mA);
           tma_load_2d_pair(sb, &tmB, fb, kb * kBK, nB);
-          tma_load_2d_pair(sb + kBHalf, &tmB, fb, kb * kBK, nB + kBN);
+          tma_load_2d_pair(sb + kRingHalfB, &tmB, fb, kb * kBK, nB + kBN);
           ++n_issued;
         }
       }
       if (failed && rank == 0) {
-        const uint32_t first = n_issued > kStages ? n_issued - kStages : 0;
-        for (uint32_t i = first; i < n_issued; ++i) drain_wait(full_bar(i % kStages), (i / kStages) & 1u, a.timeout_ns);
+        const uint32_t first = n_issued > kRing ? n_issued - kRing : 0;
+        for (uint32_t i = first; i < n_issued; ++i) drain_wait(full_bar(i % kRing), (i / kRing) & 1u, a.timeout_ns);
       }
     } else if (warp == 1 && lane == 0 && rank == 0) {
       // ------------------------------------------------------- products
@@ -290,13 +249,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool issued = false, failed = false;
       // the four steps of a k-block: both halves sharing A (half < 0), or one half
       auto products = [&](int stage, int half, bool first) {
-        const uint32_t sa = smem_u32(sA + stage * kABytes);
-        const uint32_t sb = smem_u32(sB + stage * kBBytes);
+        const uint32_t sa = smem_u32(sA + stage * kRingA);
+        const uint32_t sb = smem_u32(sB + stage * kRingB);
 #pragma unroll
         for (int k = 0; k < kBK / 16; ++k) {
           const uint64_t ad = smem_desc_sw128(sa + 32u * k, 16u, 1024u);
           const uint64_t bd0 = smem_desc_sw128(sb + 32u * k, 16u, 1024u);
-          const uint64_t bd1 = smem_desc_sw128(sb + kBHalf + 32u * k, 16u, 1024u);
+          const uint64_t bd1 = smem_desc_sw128(sb + kRingHalfB + 32u * k, 16u, 1024u);
           const uint32_t add = (!first || k > 0) ? 1u : 0u;
           if (half < 0) {
             tc_mma_bf16_pair_a_fill(tmem_base, ad, bd0, idesc, add);
@@ -321,11 +280,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint64_t t0 = globaltimer_ns();
 #pragma unroll 1
         for (uint32_t spin = 0; !mbar_try_wait_cluster(tempty1_bar, tph); ++spin) {
-          if (ahead < kStages && ahead < a.kb_total) {
+          if (ahead < kRing && ahead < a.kb_total) {
             const uint32_t n = n_consumed + static_cast<uint32_t>(ahead);
-            if (mbar_try_wait_cluster(full_bar(n % kStages), (n / kStages) & 1u)) {
+            if (mbar_try_wait_cluster(full_bar(n % kRing), (n / kRing) & 1u)) {
               tc_fence_after();
-              products(n % kStages, 0, ahead == 0);
+              products(n % kRing, 0, ahead == 0);
               issued = true;
               ++ahead;
               continue;
@@ -340,14 +299,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (failed) break;
         tc_fence_after();
         for (int j = 0; j < ahead; ++j) {
-          const int stage = (n_consumed + static_cast<uint32_t>(j)) % kStages;
+          const int stage = (n_consumed + static_cast<uint32_t>(j)) % kRing;
           products(stage, 1, j == 0);
           tc_commit_pair_multicast(empty_bar(stage), 0x3);
         }
         n_consumed += static_cast<uint32_t>(ahead);
         for (int kb = ahead; kb < a.kb_total; ++kb) {
-          const int stage = n_consumed % kStages;
-          if (!mbar_wait_bounded_cluster(full_bar(stage), (n_consumed / kStages) & 1u, a.ctrl, a.timeout_ns)) {
+          const int stage = n_consumed % kRing;
+          if (!mbar_wait_bounded_cluster(full_bar(stage), (n_consumed / kRing) & 1u, a.ctrl, a.timeout_ns)) {
             failed = true;
             break;
           }
@@ -366,29 +325,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    warpgroup_regs_inc<kRegsEpi>();
+    warpgroup_regs_inc<kRegsEpilogue>();
     // ---------------------------------------------------------- epilogue
     const int grp = (warp - 4) >> 2;
     const int wq = warp & 3;               // TMEM lanes 32 wq .. 32 wq + 31
     const int row = wq * 32 + lane;
-    const bool leader = threadIdx.x == (grp + 1) * kEpiThreads;
+    const bool leader = threadIdx.x == (grp + 1) * kWarpgroup;
     const uint32_t bar = 1u + static_cast<uint32_t>(grp);
-    uint8_t* buf = sE + grp * kEpiBytes;
+    uint8_t* buf = sE + grp * kStagingBytes;
     const float c = a.c;
     int it = 0;
     for (int u = pair; u < units; u += npairs, ++it) {
       const bool ok = mbar_wait_bounded_cluster(tfull_bar, it & 1, a.ctrl, a.timeout_ns);
-      if (named_bar_or(bar, kEpiThreads, !ok)) break;
+      if (named_bar_or(bar, kWarpgroup, !ok)) break;
       tc_fence_after();
-      const int m0 = (u % a.num_m) * 2 * kBM + static_cast<int>(rank) * kBM;
-      const int n0 = (u / a.num_m) * 2 * kBN;
+      const int m0 = (u % num_m) * 2 * kBM + static_cast<int>(rank) * kBM;
+      const int n0 = (u / num_m) * 2 * kBN;
       const int grow = m0 + row;
-      const bool rvalid = grow < a.rows;
+      const bool rvalid = grow < rows;
       ScoreRow q{0.f, 0.f, 0.f, 0.f, 0.f, -1, 0.f};
       if (MODE == kScoreGradient && rvalid) q = a.row[grow];
       int first[2] = {0, 0}, end[2] = {0, 0};  // this warpgroup's part of either half
       if (MODE == kScorePick && rvalid) {
-        const uint2 pp = a.parts[static_cast<int64_t>(grow) * a.num_n + u / a.num_m];
+        const uint2 pp = a.parts[static_cast<int64_t>(grow) * a.num_n + u / num_m];
         const uint64_t at = static_cast<uint64_t>(pp.x) | (static_cast<uint64_t>(pp.y) << 32);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -409,10 +368,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       auto release = [&](uint32_t b) {
         tc_fence_before();
-        if (rank == 0)
-          mbar_arrive(b);
-        else
-          mbar_arrive_cluster(mapa_shared(b, 0));
+        arrive_even(b, rank);
       };
       auto process = [&](int i, uint32_t (&from)[2][32]) {
         const int cg = n0 + col_of(i);
@@ -424,7 +380,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if constexpr (STORE) {
           // the copy that still reads the staging tile
           if (leader) bulk_wait_group_read<0>();
-          named_bar_sync(bar, kEpiThreads);
+          named_bar_sync(bar, kWarpgroup);
         }
         if constexpr (MODE == kScoreGradient) {
           const int k = q.target >= cg && q.target < cg + 64 ? q.target - cg : -1;
@@ -434,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if constexpr (STORE) {
           fence_proxy_async_smem();
-          named_bar_sync(bar, kEpiThreads);
+          named_bar_sync(bar, kWarpgroup);
           if (leader) {
             tma_store_2d(&tmO, smem_u32(buf), cg, m0);
             bulk_commit_group();
@@ -469,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();  // neither CTA leaves while the pair's products may touch its memory
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, kTmemCols);
+    tmem_dealloc_pair(tmem_base, kAccumulatorColumns);
   }
 }
 
@@ -477,17 +433,12 @@ template <int MODE, bool STORE>
 cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& to, const ScoreGemmArgs& args,
                    int pairs, cudaStream_t s) {
   auto kern = score_gemm_kernel<MODE, STORE>;
-  // an increase of registers waits until the block's pool holds them
-  static const bool fits = [](auto k) {
-    cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, k) == cudaSuccess &&
-           at.numRegs * kThreads >= static_cast<int>(128 * kRegsCtl + 256 * kRegsEpi);
-  }(kern);
+  static const bool fits = registers_fit(kern);
   if (!fits) return cudaErrorInvalidConfiguration;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
   if (e != cudaSuccess) return e;
-  kern<<<2 * pairs, kThreads, kSmemBytes, s>>>(ta, tb, to, args);
+  kern<<<2 * pairs, kPairThreads, kSmemBytes, s>>>(ta, tb, to, args);
   return cudaGetLastError();
 }
 
@@ -510,7 +461,7 @@ cudaError_t launch_score_gemm(int mode, const CUtensorMap& a, const CUtensorMap&
 int score_gemm_max_clusters() {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(kPairThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmemBytes;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;

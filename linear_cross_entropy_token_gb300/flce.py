@@ -30,7 +30,7 @@ KERNEL_KINDS = ["count_valid", "gemm_logits_lse", "lse_combine", "dlogits_inplac
                 "device_result", "combine_dlogits", "h2d_copy", "route", "route_finish",
                 "route_backward", "muon_momentum", "muon_prepare", "muon_steps", "muon_small",
                 "score_stats", "score_gradient", "score_rows", "score_dlogits", "score_other",
-                "distill_rows"]
+                "distill_rows", "score_backward"]
 
 
 class FlceError(RuntimeError):
