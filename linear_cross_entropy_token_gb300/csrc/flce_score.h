@@ -3,6 +3,7 @@
 // teacher's top logits.
 #pragma once
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -72,6 +73,26 @@ int score_gemm_max_clusters();
 // log-sum-exp with them: 3.8e-6 at 4096 columns, where rounding to nearest would
 // leave a tenth of that.
 inline double score_gain(int64_t H) { return 1.0 + 0.13 / 8388608.0 * (static_cast<double>(H) / 16.0); }
+
+// ----------------------------------------------------- flce_score_few.cu
+
+// The statistics for at most kScoreFew rows
+constexpr int kScoreFew = 64;
+struct ScoreFewArgs {
+  int32_t rows, padded;          // tokens; rounded up to 16
+  int32_t cols, groups;          // V; partials per row
+  int32_t kb_total;
+  int32_t tiles, stages, tmem_columns;  // filled in by the launch
+  float c;
+  int64_t ldv;
+  __half* z;                     // [rows][ldv] fp16 y, or null
+  float2* partials;
+  float* part_s;
+  uint32_t* ctrl;
+  uint64_t timeout_ns;
+};
+// w: W (box 64 x 128), x: x (box 64 x padded)
+cudaError_t launch_score_few(const CUtensorMap& w, const CUtensorMap& x, ScoreFewArgs args, int sms, cudaStream_t s);
 
 // ------------------------------------------------ flce_score_backward.cu
 

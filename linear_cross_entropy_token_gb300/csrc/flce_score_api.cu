@@ -203,6 +203,26 @@ flce_status run_stats(flce_handle_t h, const Product& q, void* z, float2* partia
   std::string why;
   if (!map_bf16_2d(&mx, q.x, q.H, q.chunk.rows, q.H * 2, 64, 128, &why) || !map_bf16_2d(&mw, q.W, q.H, q.V, q.H * 2, 64, 128, &why))
     return fail(h, FLCE_ERR_INVALID_ARG, "%s", why.c_str());
+  if (q.chunk.rows <= kScoreFew && !q.parts && !q.chunk.live) {
+    ScoreFewArgs f{};
+    f.rows = q.chunk.rows;
+    f.padded = (q.chunk.rows + 15) / 16 * 16;
+    f.cols = static_cast<int>(q.V);
+    f.groups = groups;
+    f.kb_total = static_cast<int>(cdiv(q.H, kBK));
+    f.c = q.c;
+    f.ldv = q.p->ldv;
+    f.z = static_cast<__half*>(z);
+    f.partials = partials;
+    f.part_s = part_s;
+    f.ctrl = q.ctrl;
+    f.timeout_ns = h->timeout_ns;
+    if (!map_bf16_2d(&mx, q.x, q.H, q.chunk.rows, q.H * 2, 64, f.padded, &why))
+      return fail(h, FLCE_ERR_INVALID_ARG, "%s", why.c_str());
+    FLCE_LAUNCH(FLCE_K_SCORE_STATS, 2 * dr * dH * dV, 2 * (dr + dV) * dH + (z ? 2 * dr * dV : 0) + 12 * dr * groups,
+                launch_score_few(mw, mx, f, h->num_sms, s));
+    return FLCE_OK;
+  }
   mz = mx;  // not used without a store
   if (z && !map_bf16_2d(&mz, z, q.V, q.chunk.rows, q.p->ldv * 2, 64, 128, &why))
     return fail(h, FLCE_ERR_INVALID_ARG, "%s", why.c_str());

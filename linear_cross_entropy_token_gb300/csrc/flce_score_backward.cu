@@ -202,6 +202,67 @@ __device__ __forceinline__ void epilogue_bf16(const CUtensorMap* map, const floa
   }
 }
 
+// The loads of a unit's k-blocks: this CTA's 128 rows of A (d along its rows, or its
+// columns for dW) and its 128 columns of either half of B.
+template <bool DW, bool BOTH>
+__device__ __forceinline__ bool load_unit(const ScoreBackwardMaps& maps, int kb0, int kb1, int mA, int nB, uint32_t rank,
+                                          const uint8_t* sA, const uint8_t* sB, uint32_t full0, uint32_t empty0,
+                                          uint32_t& n_issued, uint32_t* ctrl, uint64_t timeout_ns) {
+  const CUtensorMap* ma = DW ? &maps.dt : &maps.d;
+  const CUtensorMap* mb = DW ? &maps.x : &maps.w;
+  for (int kb = kb0; kb < kb1; ++kb) {
+    const uint32_t stage = n_issued % kRing;
+    if (!mbar_wait_bounded_cluster(empty0 + 8u * stage, ((n_issued / kRing) & 1u) ^ 1u, ctrl, timeout_ns)) return false;
+    const uint32_t full = full0 + 8u * stage;
+    if (rank == 0) mbar_arrive_expect_tx(full, 2 * (kRingA + (BOTH ? kRingB : kRingHalfB)));
+    const uint32_t fb = mapa_shared(full, 0);
+    const uint32_t sa = smem_u32(sA + stage * kRingA), sb = smem_u32(sB + stage * kRingB);
+    const int k0 = kb * kBK;
+    if (DW) {
+      tma_load_2d_pair(sa, ma, fb, mA, k0);
+      tma_load_2d_pair(sa + 8192, ma, fb, mA + 64, k0);
+    } else {
+      tma_load_2d_pair(sa, ma, fb, k0, mA);
+    }
+    tma_load_2d_pair(sb, mb, fb, nB, k0);
+    tma_load_2d_pair(sb + 8192, mb, fb, nB + 64, k0);
+    if (BOTH) {
+      tma_load_2d_pair(sb + kRingHalfB, mb, fb, nB + kBN, k0);
+      tma_load_2d_pair(sb + kRingHalfB + 8192, mb, fb, nB + kBN + 64, k0);
+    }
+    ++n_issued;
+  }
+  return true;
+}
+
+// Its products
+template <bool DW, bool BOTH>
+__device__ __forceinline__ bool issue_unit(int blocks, uint32_t tmem_base, const uint8_t* sA, const uint8_t* sB, uint32_t full0,
+                                           uint32_t empty0, uint32_t& n_consumed, uint32_t* ctrl, uint64_t timeout_ns) {
+  constexpr uint32_t idesc = idesc_bf16_f32(2 * kBM, kBN, DW ? 1 : 0, 1);
+  for (int i = 0; i < blocks; ++i) {
+    const uint32_t stage = n_consumed % kRing;
+    if (!mbar_wait_bounded_cluster(full0 + 8u * stage, (n_consumed / kRing) & 1u, ctrl, timeout_ns)) return false;
+    tc_fence_after();
+    const uint32_t sa = smem_u32(sA + stage * kRingA), sb = smem_u32(sB + stage * kRingB);
+#pragma unroll
+    for (int k = 0; k < kBK / 16; ++k) {
+      const uint64_t ad = DW ? smem_desc_sw128(sa + 2048u * k, 8192u, 1024u) : smem_desc_sw128(sa + 32u * k, 16u, 1024u);
+      const uint64_t bd = smem_desc_sw128(sb + 2048u * k, 8192u, 1024u);
+      const uint32_t add = (i > 0 || k > 0) ? 1u : 0u;
+      if (BOTH) {
+        tc_mma_bf16_pair_a_fill(tmem_base, ad, bd, idesc, add);
+        tc_mma_bf16_pair_a_lastuse(tmem_base + kBN, ad, smem_desc_sw128(sb + kRingHalfB + 2048u * k, 8192u, 1024u), idesc, add);
+      } else {
+        tc_mma_bf16_pair(tmem_base, ad, bd, idesc, add);
+      }
+    }
+    tc_commit_pair_multicast(empty0 + 8u * stage, 0x3);
+    ++n_consumed;
+  }
+  return true;
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     score_backward_kernel(const __grid_constant__ ScoreBackwardMaps maps, const __grid_constant__ ScoreBackwardArgs a) {
   Shape p;
@@ -256,6 +317,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     fence_mbar_init();
     fence_proxy_async_smem();
+    tma_prefetch_map(&maps.d);
+    tma_prefetch_map(&maps.w);
+    tma_prefetch_map(&maps.dt);
+    tma_prefetch_map(&maps.x);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), kAccumulatorColumns);
@@ -313,32 +378,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const bool both = both_halves(t);
         const int mA = t.m * 2 * kBM + static_cast<int>(rank) * kBM;
         const int nB = t.n * 2 * kBN + static_cast<int>(rank) * (kBN / 2);
-        const CUtensorMap* ma = t.dw ? &maps.dt : &maps.d;
-        const CUtensorMap* mb = t.dw ? &maps.x : &maps.w;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          const uint32_t stage = n_issued % kRing;
-          if (!mbar_wait_bounded_cluster(empty_bar(stage), ((n_issued / kRing) & 1u) ^ 1u, a.ctrl, a.timeout_ns)) {
-            failed = true;
-            break;
-          }
-          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * (kRingA + (both ? kRingB : kRingHalfB)));
-          const uint32_t fb = mapa_shared(full_bar(stage), 0);
-          const uint32_t sa = smem_u32(sA + stage * kRingA), sb = smem_u32(sB + stage * kRingB);
-          const int k0 = kb * kBK;
-          if (t.dw) {
-            tma_load_2d_pair(sa, ma, fb, mA, k0);
-            tma_load_2d_pair(sa + 8192, ma, fb, mA + 64, k0);
-          } else {
-            tma_load_2d_pair(sa, ma, fb, k0, mA);
-          }
-          tma_load_2d_pair(sb, mb, fb, nB, k0);
-          tma_load_2d_pair(sb + 8192, mb, fb, nB + 64, k0);
-          if (both) {
-            tma_load_2d_pair(sb + kRingHalfB, mb, fb, nB + kBN, k0);
-            tma_load_2d_pair(sb + kRingHalfB + 8192, mb, fb, nB + kBN + 64, k0);
-          }
-          ++n_issued;
-        }
+        const bool ok = t.dw ? (both ? load_unit<true, true>(maps, kb0, kb1, mA, nB, rank, sA, sB, full_bar(0), empty_bar(0),
+                                                             n_issued, a.ctrl, a.timeout_ns)
+                                     : load_unit<true, false>(maps, kb0, kb1, mA, nB, rank, sA, sB, full_bar(0), empty_bar(0),
+                                                              n_issued, a.ctrl, a.timeout_ns))
+                             : (both ? load_unit<false, true>(maps, kb0, kb1, mA, nB, rank, sA, sB, full_bar(0), empty_bar(0),
+                                                              n_issued, a.ctrl, a.timeout_ns)
+                                     : load_unit<false, false>(maps, kb0, kb1, mA, nB, rank, sA, sB, full_bar(0), empty_bar(0),
+                                                               n_issued, a.ctrl, a.timeout_ns));
+        if (!ok) failed = true;
       }
       if (failed && rank == 0) {
         const uint32_t first = n_issued > kRing ? n_issued - kRing : 0;
@@ -346,7 +394,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
     } else if (warp == 1 && lane == 0 && rank == 0) {
       // ------------------------------------------------------- products
-      constexpr uint32_t idesc_dx = idesc_bf16_f32(2 * kBM, kBN, 0, 1), idesc_dw = idesc_bf16_f32(2 * kBM, kBN, 1, 1);
       uint32_t n_consumed = 0;
       bool issued = false, failed = false;
       for (int it = 0; !failed; ++it) {
@@ -365,32 +412,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t idesc = t.dw ? idesc_dw : idesc_dx;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          const int stage = n_consumed % kRing;
-          if (!mbar_wait_bounded_cluster(full_bar(stage), (n_consumed / kRing) & 1u, a.ctrl, a.timeout_ns)) {
-            failed = true;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(sA + stage * kRingA), sb = smem_u32(sB + stage * kRingB);
-#pragma unroll
-          for (int k = 0; k < kBK / 16; ++k) {
-            const uint64_t ad = t.dw ? smem_desc_sw128(sa + 2048u * k, 8192u, 1024u) : smem_desc_sw128(sa + 32u * k, 16u, 1024u);
-            const uint64_t bd = smem_desc_sw128(sb + 2048u * k, 8192u, 1024u);
-            const uint32_t add = (kb > kb0 || k > 0) ? 1u : 0u;
-            if (both) {
-              tc_mma_bf16_pair_a_fill(tmem_base, ad, bd, idesc, add);
-              tc_mma_bf16_pair_a_lastuse(tmem_base + kBN, ad, smem_desc_sw128(sb + kRingHalfB + 2048u * k, 8192u, 1024u), idesc,
-                                         add);
-            } else {
-              tc_mma_bf16_pair(tmem_base, ad, bd, idesc, add);
-            }
-          }
-          issued = true;
-          tc_commit_pair_multicast(empty_bar(stage), 0x3);
-          ++n_consumed;
-        }
+        const bool ok = t.dw ? (both ? issue_unit<true, true>(kb1 - kb0, tmem_base, sA, sB, full_bar(0), empty_bar(0), n_consumed,
+                                                              a.ctrl, a.timeout_ns)
+                                     : issue_unit<true, false>(kb1 - kb0, tmem_base, sA, sB, full_bar(0), empty_bar(0),
+                                                               n_consumed, a.ctrl, a.timeout_ns))
+                             : (both ? issue_unit<false, true>(kb1 - kb0, tmem_base, sA, sB, full_bar(0), empty_bar(0),
+                                                               n_consumed, a.ctrl, a.timeout_ns)
+                                     : issue_unit<false, false>(kb1 - kb0, tmem_base, sA, sB, full_bar(0), empty_bar(0),
+                                                                n_consumed, a.ctrl, a.timeout_ns));
+        issued = true;
+        if (!ok) failed = true;
         if (failed) break;
         tc_commit_pair_multicast(tfull_bar, 0x3);
       }

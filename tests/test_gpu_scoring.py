@@ -276,3 +276,19 @@ def test_token_out_of_range():
             f.async_status()
         assert e.value.status == 4 and (dx[4] == 0).all() and not dW.isnan().any()
     f.async_status()
+
+
+@pytest.mark.parametrize("N", [16, 33, 48, 64, 65])
+@pytest.mark.parametrize("H,V", [(64, 129), (520, 20000), (2048, 5003)])
+def test_few_rows(N, H, V):
+    """Decoding batches, whose product has the tokens on its other side."""
+    x, W, t, _ = make_head(N, H, V, "bf16", seed=N + V)
+    t[N // 2] = -100
+    ref = Reference(x, W, 0.9)
+    for top in (0, 20):
+        check_forward(score(x, W, t, temperature=0.9, top=top), ref, t, top, t != -100)
+    r = score(x, W, t, temperature=0.9, keep_logits=True)
+    import linear_cross_entropy_token_gb300 as f
+    a = torch.linspace(-1, 1, N, device="cuda")
+    d = ref.d_scores(t.clamp(min=0), a.double(), 0 * a.double()) * (t != -100)[:, None]
+    check_gradients(*f.token_logprobs_backward(r, x, W, t, a), d, x, W, kept_distance(ref.raw, 1 / (0.9 * math.log(2))))
