@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libflce.so")
 SOURCES = ["flce_api.cu", "flce_umma.cu", "flce_rows.cu", "flce_simt.cu", "flce_static.cu",
            "flce_route.cu", "flce_muon.cu", "flce_muon_small.cu",
            "flce_train_api.cu", "flce_score.cu", "flce_score_gemm.cu",
-           "flce_score_backward.cu", "flce_score_few.cu", "flce_score_api.cu"]
+           "flce_score_backward.cu", "flce_score_few.cu", "flce_score_f32.cu",
+           "flce_score_api.cu"]
 HEADERS = ["ptx.cuh", "flce_internal.h", "flce_handle.h", "flce_train.h",
            "flce_muon.cuh", "flce_score.h", "flce_score.cuh"]
 

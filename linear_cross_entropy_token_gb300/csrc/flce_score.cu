@@ -92,38 +92,6 @@ __global__ void __launch_bounds__(128) score_skip_kernel(const ScoreSkipArgs a) 
   }
 }
 
-// ------------------------------------------------------- fp32 statistics
-
-// A warp per (row, group): what the product's epilogue does of its accumulators.
-__global__ void __launch_bounds__(256) score_stats_f32_kernel(const ScoreChunk chunk, const float* __restrict__ z, int64_t ldv, int64_t V,
-                                                              int groups, float c, float inv_t,
-                                                              float2* __restrict__ partials, float* __restrict__ part_s) {
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (u >= static_cast<int64_t>(chunk_rows(chunk.live, chunk.off, chunk.rows)) * groups) return;
-  const int64_t r = u / groups, g = u - r * groups;
-  const float* at = z + r * ldv;
-  const int64_t j = g * kScoreGroup + lane;
-  const float z0 = j < V ? at[j] : -INFINITY, z1 = j + 32 < V ? at[j + 32] : -INFINITY;
-  float m = max_nan(z0, z1);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float y0 = max_nan((z0 - m) * c, -1000.f), y1 = max_nan((z1 - m) * c, -1000.f);
-  const float e0 = expf(fmaxf((z0 - m) * inv_t, -700.f)), e1 = expf(fmaxf((z1 - m) * inv_t, -700.f));
-  // a NaN logit made y NaN, which the sum of y e shows
-  float l = e0 + e1, s = fmaf(y0, e0, y1 * e1);
-  if (s != s) l = s;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    l += __shfl_xor_sync(0xffffffffu, l, o);
-    s += __shfl_xor_sync(0xffffffffu, s, o);
-  }
-  if (lane == 0) {
-    partials[u] = make_float2(m, l);
-    part_s[u] = s;
-  }
-}
-
 // --------------------------------------------------------- shared pieces
 
 template <int THREADS>
@@ -205,6 +173,24 @@ __device__ __forceinline__ Pair warp_sum(Pair v) {
   return v;
 }
 
+// (hi, lo) += x w: the products of bf16 are exact, and lo collects what each addition
+// to hi rounds away
+__device__ __forceinline__ void add_product(uint64_t& hi, uint64_t& lo, uint64_t x, uint32_t w) {
+  const uint64_t p = mul2(x, pack2(w << 16, w & 0xFFFF0000u));
+  const uint64_t s = add2(hi, p), u = sub2(s, hi);
+  lo = add2(lo, add2(sub2(hi, sub2(s, u)), sub2(p, u)));
+  hi = s;
+}
+
+__device__ __forceinline__ Pair joined(const uint64_t (&hi)[2], const uint64_t (&lo)[2]) {
+  Pair v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = two_sum(__uint_as_float(static_cast<uint32_t>(hi[i >> 1] >> (32 * (i & 1)))),
+                   __uint_as_float(static_cast<uint32_t>(lo[i >> 1] >> (32 * (i & 1)))));
+  return add(add(v[0], v[1]), add(v[2], v[3]));
+}
+
 // x . w0 and x . w1 of a row each, by a warp
 __device__ __forceinline__ void warp_dot2(const __nv_bfloat16* x, const __nv_bfloat16* w0, const __nv_bfloat16* w1, int64_t H,
                                           int lane, Pair (&out)[2]) {
@@ -219,28 +205,39 @@ __device__ __forceinline__ void warp_dot2(const __nv_bfloat16* x, const __nv_bfl
       const uint64_t xv = pack2(av[i] << 16, av[i] & 0xFFFF0000u);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const uint32_t bv = i == 0 ? b[q].x : i == 1 ? b[q].y : i == 2 ? b[q].z : b[q].w;
-        // exact: eight bits times eight bits
-        const uint64_t p = mul2(xv, pack2(bv << 16, bv & 0xFFFF0000u));
-        uint64_t& t = hi[q][i & 1];
-        const uint64_t s = add2(t, p);
-        const uint64_t u = sub2(s, t);
-        lo[q][i & 1] = add2(lo[q][i & 1], add2(sub2(t, sub2(s, u)), sub2(p, u)));
-        t = s;
+        add_product(hi[q][i & 1], lo[q][i & 1], xv, i == 0 ? b[q].x : i == 1 ? b[q].y : i == 2 ? b[q].z : b[q].w);
       }
     }
   }
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    Pair v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = two_sum(__uint_as_float(static_cast<uint32_t>(hi[q][i >> 1] >> (32 * (i & 1)))),
-                     __uint_as_float(static_cast<uint32_t>(lo[q][i >> 1] >> (32 * (i & 1)))));
-    out[q] = add(add(v[0], v[1]), add(v[2], v[3]));
-  }
+  out[0] = joined(hi[0], lo[0]);
+  out[1] = joined(hi[1], lo[1]);
   out[0] = warp_sum(out[0]);
   out[1] = warp_sum(out[1]);
+}
+
+// x . w
+__device__ __forceinline__ Pair warp_dot(const __nv_bfloat16* x, const __nv_bfloat16* w, int64_t H, int lane) {
+  uint64_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll 4
+  for (int64_t h = lane * 8; h < H; h += 256) {
+    const uint4 a = *reinterpret_cast<const uint4*>(x + h);
+    const uint4 b = *reinterpret_cast<const uint4*>(w + h);
+    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      add_product(hi[i & 1], lo[i & 1], pack2(av[i] << 16, av[i] & 0xFFFF0000u), bv[i]);
+  }
+  return warp_sum(joined(hi, lo));
+}
+
+__device__ __forceinline__ Pair warp_dot(const float* x, const float* w, int64_t H, int lane) {
+  Pair v = {0.f, 0.f};
+  for (int64_t h = lane; h < H; h += 32) {
+    const float p = __fmul_rn(x[h], w[h]), rest = __fmaf_rn(x[h], w[h], -p);
+    const Pair s = two_sum(v.hi, p);
+    v = {s.hi, __fadd_rn(v.lo, __fadd_rn(s.lo, rest))};
+  }
+  return warp_sum(two_sum(v.hi, v.lo));
 }
 
 __device__ __forceinline__ void warp_dot2(const float* x, const float* w0, const float* w1, int64_t H, int lane,
@@ -273,8 +270,8 @@ __device__ __forceinline__ uint64_t order_key(Pair v) {
 
 constexpr int kMaxCandidates = 128;
 constexpr int kMaxGroups = 256;
+constexpr int kMaxima = 128;
 static_assert(kScoreMaxTop <= kMaxCandidates, "room for the result");
-constexpr int kMaxValues = kScoreMaxTop * kScoreGroup;
 
 template <int THREADS>
 struct SelectSmem {
@@ -370,9 +367,9 @@ __device__ __noinline__ int block_collect(int64_t n, int quota, int room, Select
 template <int THREADS>
 struct TopSmem {
   SelectSmem<THREADS> sel;
+  uint32_t key[kMaxima];
   int group[kMaxGroups];
   float lower[kMaxCandidates], upper[kMaxCandidates];
-  float value[kMaxValues];           // the careful way's
   float gmax[kScoreMaxTop];
   float border;
   int groups, found, kept;
@@ -391,33 +388,53 @@ __device__ __forceinline__ float stored_bound(float v, float gm, float M, float 
 // The ids of whatever may be among the row's `top` largest logits, to id, and how
 // many. m: the thread's largest group maximum.
 //
-// The quick way: the top-th largest of the threads' maxima, cut to 20 bits by halving
-// the range with counts, is a border that at least `top` logits reach. Groups whose maximum reaches it, then their columns
-// whose upper bound does, then of those (a few more than `top`) the ones that reach
-// the top-th largest lower bound. Lists are filled in any order: what they hold
+// The quick way: the top-th largest of 128 maxima (each of some groups), cut to 20
+// bits by halving the range with counts, is a border that at least `top` logits reach.
+// Groups whose maximum reaches it, then their columns whose upper bound does, then of
+// those (a few more than `top`) the ones that reach the top-th largest lower bound. Lists are filled in any order: what they hold
 // does not depend on it, and the order of the result comes from the exact logits.
 // Returns -1 where lists overflow (many equal or nearly equal logits) or the row
 // has fewer maxima than `top`, or no finite largest logit.
 template <class Z, int THREADS>
 __device__ __forceinline__ int quick_candidates(const ScoreRowsArgs& a, const float2* part, const Z* z, float m, float M,
                                                 TopSmem<THREADS>& s, int64_t* id) {
-  if (!(fabsf(M) < INFINITY) || a.top > min(a.groups, THREADS)) return -1;  // uniform
-  const uint32_t own = static_cast<int>(threadIdx.x) < a.groups ? order_key(m) : 0u;
+  if (!(fabsf(M) < INFINITY) || a.top > min(a.groups, kMaxima)) return -1;  // uniform
+  if (threadIdx.x < kMaxima) s.key[threadIdx.x] = 0u;
   if (threadIdx.x == 0) s.groups = s.found = s.kept = 0;
-  // to 20 bits of the key, from below
-  uint32_t reached = 0;
+  __syncthreads();
+  if (static_cast<int>(threadIdx.x) < a.groups) atomicMax(&s.key[threadIdx.x % kMaxima], order_key(m));
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    uint32_t own[kMaxima / 32];
+#pragma unroll
+    for (int i = 0; i < kMaxima / 32; ++i) own[i] = s.key[32 * i + threadIdx.x];
+    // to 20 bits of the key, from below
+    uint32_t reached = 0;
 #pragma unroll 1
-  for (uint32_t bit = 1u << 31; bit >= 1u << 12; bit >>= 1)
-    if (__syncthreads_count(own >= (reached | bit)) >= a.top) reached |= bit;
-  const float key_value = __uint_as_float((reached & 0x80000000u) ? reached & 0x7FFFFFFFu : ~reached);
+    for (uint32_t bit = 1u << 31; bit >= 1u << 12; bit >>= 1) {
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < kMaxima / 32; ++i) n += __popc(__ballot_sync(0xffffffffu, own[i] >= (reached | bit)));
+      if (n >= a.top) reached |= bit;
+    }
+    if (threadIdx.x == 0) s.border = __uint_as_float((reached & 0x80000000u) ? reached & 0x7FFFFFFFu : ~reached);
+  }
+  __syncthreads();
+  const float key_value = s.border;
   const float border = key_value - fmaxf(fabsf(M), fabsf(key_value)) * 6.1e-5f;
   const float gborder = border - fmaxf(fabsf(M), fabsf(key_value)) * 6.1e-5f;
   if (m >= gborder)
-    for (int g = threadIdx.x; g < a.groups; g += THREADS)
-      if (part[g].x >= gborder) {
-        const int at = atomicAdd(&s.groups, 1);
-        if (at < kMaxGroups) s.group[at] = g;
-      }
+    for (int g = threadIdx.x; g < a.groups; g += 8 * THREADS) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = g + i * THREADS < a.groups ? part[g + i * THREADS].x : -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (v[i] >= gborder && g + i * THREADS < a.groups) {
+          const int at = atomicAdd(&s.groups, 1);
+          if (at < kMaxGroups) s.group[at] = g + i * THREADS;
+        }
+    }
   __syncthreads();
   const int ng = s.groups;
   if (ng > kMaxGroups) return -1;
@@ -495,20 +512,16 @@ __device__ __noinline__ int careful_candidates(const ScoreRowsArgs& a, const flo
   __syncthreads();
   const int nv = kg * kScoreGroup;
   auto column = [&](int64_t i) { return static_cast<int64_t>(s.group[i >> 6]) * kScoreGroup + (i & 63); };
-  if (threadIdx.x == 0) s.found = 0;
-  for (int i = threadIdx.x; i < nv; i += THREADS) {
+  auto value = [&](int64_t i) {  // read again each time: keeping them took room from other rows' blocks
     const int64_t j = column(i);
-    float v = -INFINITY;
-    if (j < a.V) {
-      if constexpr (sizeof(Z) == 2)
-        v = fmaf(__half2float(z[j]), a.inv_c, s.gmax[i >> 6]);
-      else
-        v = z[j];
-    }
-    s.value[i] = v;
-  }
+    if constexpr (sizeof(Z) == 2)
+      return fmaf(__half2float(z[j]), a.inv_c, s.gmax[i >> 6]);
+    else
+      return z[j];
+  };
+  if (threadIdx.x == 0) s.found = 0;
   __syncthreads();
-  auto bound = [&](int64_t i, float sign) { return order_key(stored_bound<Z>(s.value[i], s.gmax[i >> 6], M, a.inv_c, sign)); };
+  auto bound = [&](int64_t i, float sign) { return order_key(stored_bound<Z>(value(i), s.gmax[i >> 6], M, a.inv_c, sign)); };
   const uint32_t least =
       block_select<THREADS>(nv, a.top, s.sel, above, [&](int64_t i) { return column(i) < a.V ? bound(i, -1.f) : 0u; });
   auto maybe = [&](int64_t i) { return column(i) < a.V && bound(i, 1.f) >= least ? 2 : 0; };
@@ -519,11 +532,11 @@ __device__ __noinline__ int careful_candidates(const ScoreRowsArgs& a, const flo
   __syncthreads();
   if (s.found <= kMaxCandidates) return block_collect<THREADS>(nv, 0, kMaxCandidates, s.sel, maybe, put);
   const uint32_t key = block_select<THREADS>(nv, kMaxCandidates, s.sel, above,
-                                             [&](int64_t i) { return column(i) < a.V ? order_key(s.value[i]) : 0u; });
+                                             [&](int64_t i) { return column(i) < a.V ? order_key(value(i)) : 0u; });
   return block_collect<THREADS>(nv, kMaxCandidates - above, kMaxCandidates, s.sel,
                                 [&](int64_t i) {
                                   if (column(i) >= a.V) return 0;
-                                  const uint32_t v = order_key(s.value[i]);
+                                  const uint32_t v = order_key(value(i));
                                   return v > key ? 2 : (v == key ? 1 : 0);
                                 },
                                 put);
@@ -583,11 +596,11 @@ __global__ void __launch_bounds__(32 * kWarpRows) score_warp_rows_kernel(const S
     S += __shfl_xor_sync(0xffffffffu, S, o);
   }
   const float log_L = logf(L);
-  Pair z[2] = {};
-  const E* w = static_cast<const E*>(a.W) + (a.t && !bad ? t : 0) * a.H;
-  if (a.t && !bad) warp_dot2(static_cast<const E*>(a.x) + r * a.H, w, w, a.H, lane, z);
+  Pair z = {0.f, 0.f};
+  if (a.t && !bad)
+    z = warp_dot(static_cast<const E*>(a.x) + r * a.H, static_cast<const E*>(a.W) + t * a.H, a.H, lane);
   if (lane != 0) return;
-  if (a.t) a.logprobs[r] = bad ? NAN : score_log_p(a, z[0], M, log_L);
+  if (a.t) a.logprobs[r] = bad ? NAN : score_log_p(a, z, M, log_L);
   a.entropy[r] = log_L - kLn2 * S / L;
   a.stats[r] = make_float2(M, log_L);
   if (bad) *reinterpret_cast<volatile uint32_t*>(a.host_error) = kErrBadTarget;
@@ -627,10 +640,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) score_rows_kernel(con
   const float2* part = a.partials + i * a.groups;
   const float* part_s = a.part_s + i * a.groups;
   float m = -INFINITY;
+#pragma unroll 8
   for (int g = threadIdx.x; g < a.groups; g += THREADS) m = max_nan(m, part[g].x);
   const float M = block_max<THREADS>(m, s_red);
   const float scale = a.scale;
   float L = 0.f, S = 0.f;
+#pragma unroll 4
   for (int g = threadIdx.x; g < a.groups; g += THREADS) {
     const float2 p = part[g];
     const float d = p.x - M, w = expf(max_nan(d * scale, -700.f));
@@ -656,9 +671,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) score_rows_kernel(con
   for (int d = warp; d < dots; d += 2 * (THREADS / 32)) {
     const int e = d + THREADS / 32;
     const E* w0 = W + (d < n ? s_id[d] : t) * a.H;
-    const E* w1 = e < dots ? W + (e < n ? s_id[e] : t) * a.H : w0;
     Pair v[2];
-    warp_dot2(x, w0, w1, a.H, lane, v);
+    if (e < dots)
+      warp_dot2(x, w0, W + (e < n ? s_id[e] : t) * a.H, a.H, lane, v);
+    else
+      v[0] = warp_dot(x, w0, a.H, lane);
     if (lane == 0) {
       s_dot[d] = v[0];
       s_order[d] = order_key(v[0]);
@@ -746,30 +763,57 @@ __global__ void __launch_bounds__(128) score_prepare_kernel(const ScorePrepareAr
 
 // Eight columns of a row's gradient from the stored logits. The padding behind the
 // last column (ldv is a multiple of 64) becomes zero.
-__device__ __forceinline__ void dlogits8(const __half* z, __nv_bfloat16* d, int64_t j, int64_t V, float gmax, float c,
+__device__ __forceinline__ void dlogits8(uint4 in, __nv_bfloat16* d, int64_t j, int64_t V, float gmax, float c,
                                          const ScoreRow& q, float* dcorr) {
-  const uint4 in = *reinterpret_cast<const uint4*>(z + j);
   const uint32_t iv[4] = {in.x, in.y, in.z, in.w};
   const float shift = fmaf(gmax - q.largest, c, -q.log2_total);
-  uint32_t ov[4];
+  float v[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&iv[i]));
-    float v[2] = {y.x, y.y};
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int64_t col = j + 2 * i + u;
-      const float t = max_nan(v[u] + shift, -1000.f);
-      v[u] = col < V ? ex2(t) * fmaf(q.b, t, q.a) : 0.f;
-      if (col == q.target) {
-        v[u] += q.add;
-        if (dcorr) *dcorr = v[u] - __bfloat162float(__float2bfloat16_rn(v[u]));
-      }
-    }
-    __nv_bfloat162 o = __floats2bfloat162_rn(v[0], v[1]);
-    ov[i] = *reinterpret_cast<uint32_t*>(&o);
+    const float t0 = max_nan(y.x + shift, -1000.f), t1 = max_nan(y.y + shift, -1000.f);
+    v[2 * i] = ex2(t0) * fmaf(q.b, t0, q.a);
+    v[2 * i + 1] = ex2(t1) * fmaf(q.b, t1, q.a);
   }
-  *reinterpret_cast<uint4*>(d + j) = make_uint4(ov[0], ov[1], ov[2], ov[3]);
+  if (j + 8 > V) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (j + i >= V) v[i] = 0.f;
+  }
+  if (q.target >= j && q.target < j + 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (j + i == q.target) {
+        v[i] += q.add;
+        if (dcorr) *dcorr = v[i] - __bfloat162float(__float2bfloat16_rn(v[i]));
+      }
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 o = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&o);
+  }
+  *reinterpret_cast<uint4*>(d + j) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The same of several pieces, `step` columns apart: their loads are all under way
+// before the first is used (HBM wants some 64 bytes in flight a thread).
+constexpr int kPieces = 4;
+
+__device__ __forceinline__ void dlogits_pieces(const __half* z, __nv_bfloat16* d, int64_t j, int64_t step, int64_t ldv,
+                                               int64_t V, const float2* part, float c, const ScoreRow& q, float* dcorr) {
+  uint4 in[kPieces];
+  float gmax[kPieces];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i)
+    if (j + i * step < ldv) {
+      in[i] = __ldcs(reinterpret_cast<const uint4*>(z + j + i * step));
+      gmax[i] = part[(j + i * step) / kScoreGroup].x;
+    }
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i)
+    if (j + i * step < ldv) dlogits8(in[i], d, j + i * step, V, gmax[i], c, q, dcorr);
 }
 
 // fp32: p from the natural exponential, whose argument has no factor to round
@@ -796,13 +840,15 @@ __global__ void __launch_bounds__(kDlogitsThreads) score_dlogits_bf16_kernel(
   const int64_t r = blockIdx.x;
   if (r >= tail_end(chunk, chunk_rows(chunk.live, chunk.off, chunk.rows))) return;
   const ScoreRow q = row[r];
-  const int64_t j = (static_cast<int64_t>(blockIdx.y) * kDlogitsThreads + threadIdx.x) * 8;
-  if (j >= ldv) return;
+  const int64_t j = (static_cast<int64_t>(blockIdx.y) * kPieces * kDlogitsThreads + threadIdx.x) * 8;
   if (q.a == 0.f && q.b == 0.f && q.add == 0.f) {
-    *reinterpret_cast<uint4*>(d + r * ldv + j) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if (j + i * kDlogitsThreads * 8 < ldv)
+        *reinterpret_cast<uint4*>(d + r * ldv + j + i * kDlogitsThreads * 8) = make_uint4(0, 0, 0, 0);
     return;
   }
-  dlogits8(z + r * ldv, d + r * ldv, j, V, partials[r * groups + j / kScoreGroup].x, c, q, dcorr + r);
+  dlogits_pieces(z + r * ldv, d + r * ldv, j, kDlogitsThreads * 8, ldv, V, partials + r * groups, c, q, dcorr + r);
 }
 
 __global__ void __launch_bounds__(kDlogitsThreads) score_dlogits_f32_kernel(const ScoreChunk chunk, const float* z, float* d, int64_t ldv, int64_t V,
@@ -934,7 +980,7 @@ __global__ void __launch_bounds__(kPickThreads) distill_pick_kernel(const Distil
   }
 }
 
-constexpr int kDistillThreads = 512;
+constexpr int kDistillThreads = 256;
 
 // A block per row: the row's log-sum-exp from its groups, the entries' logits, the
 // loss T^2 sum_e q_e (log q_e - log p_e), and with the gradient the row of stored
@@ -950,7 +996,6 @@ __global__ void __launch_bounds__(kDistillThreads) distill_rows_kernel(const Dis
   __shared__ float s_q[kScoreMaxTeacher];
   const int64_t i = blockIdx.x;
   constexpr bool bf16 = sizeof(E) == 2;
-  constexpr int kVec = bf16 ? 8 : 4;
   uint8_t* zrow = static_cast<uint8_t*>(a.z) + i * a.ldv * sizeof(E);
   const int rows = chunk_rows(a.chunk.live, a.chunk.off, a.chunk.rows);
   if (i >= rows) {
@@ -1006,11 +1051,12 @@ __global__ void __launch_bounds__(kDistillThreads) distill_rows_kernel(const Dis
     const float factor = a.temperature / static_cast<float>(a.ctrl[kCtrlNValid]);
     ScoreRow row{M, log_L * kLog2e, factor, 0.f, 0.f, -1, expf(-log_L)};
     if (!(fabsf(row.log2_total) < INFINITY) || !(fabsf(M) < INFINITY)) row.a = NAN;
-    for (int64_t j = threadIdx.x * kVec; j < a.ldv; j += kDistillThreads * kVec) {
-      if constexpr (bf16)
-        dlogits8(reinterpret_cast<const __half*>(zrow), reinterpret_cast<__nv_bfloat16*>(zrow), j, a.V,
-                 part[j / kScoreGroup].x, a.c, row, nullptr);
-      else
+    if constexpr (bf16) {
+      for (int64_t j = threadIdx.x * 8; j < a.ldv; j += kPieces * kDistillThreads * 8)
+        dlogits_pieces(reinterpret_cast<const __half*>(zrow), reinterpret_cast<__nv_bfloat16*>(zrow), j, kDistillThreads * 8,
+                       a.ldv, a.V, part, a.c, row, nullptr);
+    } else {
+      for (int64_t j = threadIdx.x * 4; j < a.ldv; j += kDistillThreads * 4)
         dlogits4(reinterpret_cast<const float*>(zrow), reinterpret_cast<float*>(zrow), j, a.V, a.c, inv, row);
     }
     __syncthreads();
@@ -1064,13 +1110,6 @@ cudaError_t launch_rows(const ScoreRowsArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_score_stats_f32(const ScoreChunk& chunk, const float* z, int64_t ldv, int64_t V, int groups, float c,
-                                   float inv_temperature, float2* partials, float* part_s, cudaStream_t s) {
-  score_stats_f32_kernel<<<blocks_of(static_cast<int64_t>(chunk.rows) * groups, 8), 256, 0, s>>>(
-      chunk, z, ldv, V, groups, c, inv_temperature, partials, part_s);
-  return cudaGetLastError();
-}
-
 cudaError_t launch_score_order(const int64_t* t, int64_t ignore_index, const uint8_t* live, int64_t N, int32_t* order,
                                uint32_t* count, cudaStream_t s) {
   score_order_kernel<<<1, 1024, 0, s>>>(t, ignore_index, live, N, order, count);
@@ -1094,7 +1133,7 @@ cudaError_t launch_score_prepare(const ScorePrepareArgs& a, cudaStream_t s) {
 cudaError_t launch_score_dlogits(int bf16, const ScoreChunk& chunk, const void* z, const float2* partials, int groups, void* d,
                                  int64_t ldv, int64_t V, float c, float inv_temperature, const ScoreRow* row, float* dcorr,
                                  cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(chunk.rows), blocks_of(ldv, kDlogitsThreads * (bf16 ? 8 : 4)));
+  const dim3 grid(static_cast<unsigned>(chunk.rows), blocks_of(ldv, kDlogitsThreads * (bf16 ? 8 * kPieces : 4)));
   if (bf16)
     score_dlogits_bf16_kernel<<<grid, kDlogitsThreads, 0, s>>>(chunk, static_cast<const __half*>(z), partials, groups,
                                                               static_cast<__nv_bfloat16*>(d), ldv, V, c, row, dcorr);

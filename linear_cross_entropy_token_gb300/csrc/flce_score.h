@@ -94,6 +94,26 @@ struct ScoreFewArgs {
 // w: W (box 64 x 128), x: x (box 64 x padded)
 cudaError_t launch_score_few(const CUtensorMap& w, const CUtensorMap& x, ScoreFewArgs args, int sms, cudaStream_t s);
 
+// ----------------------------------------------------- flce_score_f32.cu
+
+// C[m][n] (+)= sum over k of A(m, k) B(k, n) in fp32, operands by strides
+struct ScoreF32Args {
+  const float* A;
+  const float* B;
+  float* C;
+  int64_t sam, sak, sbk, sbn, ldc, M, N, K;
+  int32_t accumulate;
+  float* part;                   // splits x M x N, or null
+  // statistics of C's 64-column groups (no splits), or null
+  float2* partials;
+  float* part_s;
+  int32_t groups;
+  float c, inv_temperature;
+  int64_t k_per_split;           // filled in by the launch
+};
+int score_f32_splits(int64_t M, int64_t N, int64_t K, int sms, int64_t most);
+cudaError_t launch_score_f32(ScoreF32Args args, int splits, cudaStream_t s);
+
 // ------------------------------------------------ flce_score_backward.cu
 
 struct ScoreBackwardMaps {
@@ -127,10 +147,6 @@ struct ScoreChunk {
   const int32_t* order;
   const uint32_t* live;
 };
-
-// The statistics of fp32 logits, as the product's epilogue takes them.
-cudaError_t launch_score_stats_f32(const ScoreChunk& chunk, const float* z, int64_t ldv, int64_t V, int groups, float c,
-                                   float inv_temperature, float2* partials, float* part_s, cudaStream_t s);
 
 // The rows that count, in order, and how many: t[i] != ignore_index, or live[i] != 0
 // where t is null.

@@ -73,6 +73,11 @@ flce_status make_plan(flce_handle_t h, int64_t N, int64_t H, int64_t V, const Ne
     if (st != FLCE_OK) return fail(h, st, "no chunk of these sizes fits the HBM budget");
     p.chunk = lp.chunk;
     p.splits = lp.dx_splits;
+    if (!bf16 && p.chunk > 0) {  // the partial sums take at most an eighth of the budget
+      const uint64_t budget = h->cfg.hbm_budget_bytes ? h->cfg.hbm_budget_bytes : kDefaultBudget;
+      p.splits = score_f32_splits(p.chunk, H, V, h->num_sms,
+                                  static_cast<int64_t>(budget / 8 / (static_cast<uint64_t>(p.chunk) * H * 4)));
+    }
   } else {
     const uint64_t budget = h->cfg.hbm_budget_bytes ? h->cfg.hbm_budget_bytes : kDefaultBudget;
     const uint64_t a_row = (q.z ? p.ldv * es : 0) + (q.stats ? p.groups * 12ull : 0);
@@ -189,14 +194,23 @@ flce_status run_stats(flce_handle_t h, const Product& q, void* z, float2* partia
   const double dr = q.chunk.rows, dH = static_cast<double>(q.H), dV = static_cast<double>(q.V);
   const int groups = static_cast<int>(q.p->groups);
   if (!is_bf16(h)) {
-    float* zf = static_cast<float*>(z);
-    FLCE_LAUNCH(FLCE_K_SIMT_GEMM, 2 * dr * dH * dV, 4 * (dr * dH + dV * dH + dr * dV),
-                launch_simt_gemm_f32(static_cast<const float*>(q.x), q.H, 1, static_cast<const float*>(q.W), 1, q.H, zf,
-                                     q.p->ldv, q.chunk.rows, q.V, q.H, 0, 1, nullptr, s));
-    if (partials)
-      FLCE_LAUNCH(FLCE_K_SCORE_STATS, 0.0, 4 * dr * dV + 12 * dr * groups,
-                  launch_score_stats_f32(q.chunk, zf, q.p->ldv, q.V, groups, q.c, q.inv_temperature,
-                                         partials, part_s, s));
+    ScoreF32Args a{};
+    a.A = static_cast<const float*>(q.x);
+    a.B = static_cast<const float*>(q.W);
+    a.C = static_cast<float*>(z);
+    a.sam = a.sbn = q.H;
+    a.sak = a.sbk = 1;
+    a.ldc = q.p->ldv;
+    a.M = q.chunk.rows;
+    a.N = q.V;
+    a.K = q.H;
+    a.partials = partials;
+    a.part_s = part_s;
+    a.groups = groups;
+    a.c = q.c;
+    a.inv_temperature = q.inv_temperature;
+    FLCE_LAUNCH(FLCE_K_SCORE_STATS, 2 * dr * dH * dV, 4 * (dr * dH + dV * dH + dr * dV) + 12 * dr * groups,
+                launch_score_f32(a, 1, s));
     return FLCE_OK;
   }
   CUtensorMap mx, mw, mz;
@@ -303,15 +317,32 @@ flce_status run_backward(flce_handle_t h, const Product& q, const Backward& b, c
   const double dw_bytes = b.dW ? 2 * dr * dV + 2 * dr * dH + ((first ? 4.0 : 8.0) - (to16 && b.last ? 2.0 : 0.0)) * dV * dH : 0.0;
   if (!is_bf16(h)) {
     const float* d = static_cast<const float*>(b.d);
-    if (b.dx)
-      FLCE_LAUNCH(FLCE_K_SIMT_GEMM, 2 * dr * dV * dH, 2 * dx_bytes,
-                  launch_simt_gemm_f32(d, ldv, 1, static_cast<const float*>(q.W), H, 1,
-                                       static_cast<float*>(b.dx) + q.chunk.off * H, H, rows, H, V, 0,
-                                       static_cast<int>(q.p->splits), b.part, s));
-    if (b.dW)
-      FLCE_LAUNCH(FLCE_K_SIMT_GEMM, 2 * dr * dV * dH, 2 * dw_bytes,
-                  launch_simt_gemm_f32(d, 1, ldv, static_cast<const float*>(q.x), H, 1, static_cast<float*>(b.dW), H, V, H,
-                                       rows, first ? 0 : 1, 1, nullptr, s));
+    ScoreF32Args a{};
+    a.A = d;
+    a.N = a.ldc = H;
+    a.sbk = H;
+    a.sbn = 1;
+    if (b.dx) {
+      a.sam = ldv;
+      a.sak = 1;
+      a.B = static_cast<const float*>(q.W);
+      a.C = static_cast<float*>(b.dx) + q.chunk.off * H;
+      a.M = rows;
+      a.K = V;
+      a.part = b.part;
+      FLCE_LAUNCH(FLCE_K_SIMT_GEMM, 2 * dr * dV * dH, 2 * dx_bytes, launch_score_f32(a, static_cast<int>(q.p->splits), s));
+    }
+    if (b.dW) {
+      a.sam = 1;
+      a.sak = ldv;
+      a.B = static_cast<const float*>(q.x);
+      a.C = static_cast<float*>(b.dW);
+      a.M = V;
+      a.K = rows;
+      a.part = nullptr;
+      a.accumulate = !first;
+      FLCE_LAUNCH(FLCE_K_SIMT_GEMM, 2 * dr * dV * dH, 2 * dw_bytes, launch_score_f32(a, 1, s));
+    }
     return FLCE_OK;
   }
   std::string why;
