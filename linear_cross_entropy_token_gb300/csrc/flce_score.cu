@@ -36,13 +36,43 @@ __device__ __forceinline__ int tail_end(const ScoreChunk& q, int rows) {
   return min(q.rows, (max(rows, 1) + 255) / 256 * 256);
 }
 
-// One block: 1024 rows at a time, each warp's and then each thread's place by counts.
-// A few microseconds for a batch, which the products of the rows left out repay from
-// the first 256 on.
-__global__ void __launch_bounds__(1024) score_order_kernel(const int64_t* __restrict__ t, int64_t ignore_index,
-                                                           const uint8_t* __restrict__ live, int64_t N,
-                                                           int32_t* __restrict__ order, uint32_t* count) {
+// Fills 16-byte pieces, or 4-byte ones
+__device__ __forceinline__ void zero_row(uint8_t* to, int64_t bytes, int thread, int threads) {
+  if ((reinterpret_cast<uint64_t>(to) | static_cast<uint64_t>(bytes)) % 16 == 0) {
+    for (int64_t i = thread * 16; i < bytes; i += threads * 16) *reinterpret_cast<uint4*>(to + i) = make_uint4(0, 0, 0, 0);
+  } else {
+    for (int64_t i = thread * 4; i < bytes; i += threads * 4) *reinterpret_cast<uint32_t*>(to + i) = 0u;
+  }
+}
+
+// What a row gets that does not count: by a warp
+__device__ __forceinline__ void skip_row(const ScoreOrderArgs& a, int64_t r, int lane) {
+  if (r >= a.N || (a.t ? a.t[r] != a.ignore_index : a.live[r] != 0)) return;
+  if (a.dx) zero_row(static_cast<uint8_t*>(a.dx) + r * a.row_bytes, a.row_bytes, lane, 32);
+  if (lane == 0) {
+    if (a.logprobs) a.logprobs[r] = 0.f;
+    if (a.entropy) a.entropy[r] = 0.f;
+    if (a.stats) a.stats[r] = make_float2(0.f, 0.f);
+  }
+  for (int i = lane; i < a.top; i += 32) {
+    a.top_logprobs[r * a.top + i] = 0.f;
+    a.top_ids[r * a.top + i] = -1;
+  }
+}
+
+// The first block puts the rows in order, 1024 at a time, each warp's and then each
+// thread's place by counts: a few microseconds for a batch, which the products of the
+// rows left out repay from the first 256 on. The others see to the rows left out.
+__global__ void __launch_bounds__(1024) score_order_kernel(const ScoreOrderArgs a) {
   __shared__ int s_count[2][32];
+  if (blockIdx.x > 0) {
+    skip_row(a, (static_cast<int64_t>(blockIdx.x) - 1) * 32 + (threadIdx.x >> 5), threadIdx.x & 31);
+    return;
+  }
+  const int64_t* t = a.t;
+  const uint8_t* live = a.live;
+  const int64_t N = a.N, ignore_index = a.ignore_index;
+  int32_t* order = a.order;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int done = 0, turn = 0;
   auto counts = [&](int64_t i) { return i < N && (t ? t[i] != ignore_index : live[i] != 0); };
@@ -63,33 +93,7 @@ __global__ void __launch_bounds__(1024) score_order_kernel(const int64_t* __rest
     if (in) order[done + before + __popc(mask & ((1u << lane) - 1u))] = static_cast<int32_t>(base + threadIdx.x);
     done += __shfl_sync(0xffffffffu, upto, 31);
   }
-  if (threadIdx.x == 0) *count = static_cast<uint32_t>(done);
-}
-
-// Fills 16-byte pieces, or 4-byte ones
-__device__ __forceinline__ void zero_row(uint8_t* to, int64_t bytes, int thread, int threads) {
-  if ((reinterpret_cast<uint64_t>(to) | static_cast<uint64_t>(bytes)) % 16 == 0) {
-    for (int64_t i = thread * 16; i < bytes; i += threads * 16) *reinterpret_cast<uint4*>(to + i) = make_uint4(0, 0, 0, 0);
-  } else {
-    for (int64_t i = thread * 4; i < bytes; i += threads * 4) *reinterpret_cast<uint32_t*>(to + i) = 0u;
-  }
-}
-
-// A warp per row
-__global__ void __launch_bounds__(128) score_skip_kernel(const ScoreSkipArgs a) {
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (r >= a.N || (a.t ? a.t[r] != a.ignore_index : a.live[r] != 0)) return;
-  if (a.dx) zero_row(static_cast<uint8_t*>(a.dx) + r * a.row_bytes, a.row_bytes, lane, 32);
-  if (lane == 0) {
-    if (a.logprobs) a.logprobs[r] = 0.f;
-    if (a.entropy) a.entropy[r] = 0.f;
-    if (a.stats) a.stats[r] = make_float2(0.f, 0.f);
-  }
-  for (int i = lane; i < a.top; i += 32) {
-    a.top_logprobs[r * a.top + i] = 0.f;
-    a.top_ids[r * a.top + i] = -1;
-  }
+  if (threadIdx.x == 0) *a.count = static_cast<uint32_t>(done);
 }
 
 // --------------------------------------------------------- shared pieces
@@ -816,18 +820,12 @@ __device__ __forceinline__ void dlogits_pieces(const __half* z, __nv_bfloat16* d
     if (j + i * step < ldv) dlogits8(in[i], d, j + i * step, V, gmax[i], c, q, dcorr);
 }
 
-// fp32: p from the natural exponential, whose argument has no factor to round
 __device__ __forceinline__ void dlogits4(const float* z, float* d, int64_t j, int64_t V, float c, float inv_t,
                                          const ScoreRow& q) {
   const float4 in = *reinterpret_cast<const float4*>(z + j);
   float v[4] = {in.x, in.y, in.z, in.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float u = v[i] - q.largest;
-    const float t = max_nan(fmaf(u, c, -q.log2_total), -1000.f);
-    v[i] = j + i < V ? expf(max_nan(u * inv_t, -700.f)) * q.inv_total * fmaf(q.b, t, q.a) : 0.f;
-    if (j + i == q.target) v[i] += q.add;
-  }
+  for (int i = 0; i < 4; ++i) v[i] = j + i < V ? dlogit_f32(v[i], j + i, c, inv_t, q) : 0.f;
   *reinterpret_cast<float4*>(d + j) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
@@ -870,8 +868,10 @@ __global__ void __launch_bounds__(kDlogitsThreads) score_dlogits_f32_kernel(cons
 __global__ void __launch_bounds__(128) score_dx_kernel(const ScoreChunk chunk, const float* __restrict__ part, int splits, int64_t split_stride,
                                                        int64_t H, const __nv_bfloat16* __restrict__ W,
                                                        const ScoreRow* __restrict__ row, const float* __restrict__ dcorr,
-                                                       __nv_bfloat16* __restrict__ dx) {
+                                                       __nv_bfloat16* __restrict__ dx, const uint32_t* ctrl,
+                                                       uint32_t* host_error) {
   const int64_t r = blockIdx.x;
+  if (host_error && r == 0 && blockIdx.y == 0 && threadIdx.x == 0) report(ctrl, host_error);
   const int64_t h = (static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * 4;
   if (h >= H || r >= chunk_rows(chunk.live, chunk.off, chunk.rows)) return;
   const int64_t i = r * H + h;
@@ -913,7 +913,7 @@ __device__ __forceinline__ bool teacher_there(int64_t id, float logit) { return 
 __global__ void __launch_bounds__(256) distill_live_kernel(const int64_t* __restrict__ ids, int64_t ld_ids,
                                                            const void* __restrict__ logits, int64_t ld_logits, int dtype,
                                                            int64_t N, int k, int64_t V, uint8_t* __restrict__ live,
-                                                           float* __restrict__ token_loss, uint32_t* ctrl) {
+                                                           float* __restrict__ token_loss, uint32_t* ctrl, bool count) {
   const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   bool any = false, bad = false;
@@ -930,6 +930,7 @@ __global__ void __launch_bounds__(256) distill_live_kernel(const int64_t* __rest
     live[r] = any && !bad;
     if (!any || bad) token_loss[r] = 0.f;
     if (bad) atomicCAS(ctrl + kCtrlError, 0u, kErrBadTarget);
+    if (count && any && !bad) atomicAdd(ctrl + kCtrlNValid, 1u);
   }
 }
 
@@ -1110,14 +1111,9 @@ cudaError_t launch_rows(const ScoreRowsArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_score_order(const int64_t* t, int64_t ignore_index, const uint8_t* live, int64_t N, int32_t* order,
-                               uint32_t* count, cudaStream_t s) {
-  score_order_kernel<<<1, 1024, 0, s>>>(t, ignore_index, live, N, order, count);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_score_skip(const ScoreSkipArgs& a, cudaStream_t s) {
-  score_skip_kernel<<<blocks_of(a.N, 4), 128, 0, s>>>(a);
+cudaError_t launch_score_order(const ScoreOrderArgs& a, cudaStream_t s) {
+  const bool skip = a.dx || a.logprobs || a.entropy;
+  score_order_kernel<<<1 + (skip ? blocks_of(a.N, 32) : 0), 1024, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -1144,9 +1140,11 @@ cudaError_t launch_score_dlogits(int bf16, const ScoreChunk& chunk, const void* 
 }
 
 cudaError_t launch_score_dx(const ScoreChunk& chunk, const float* part, int splits, int64_t split_stride, int64_t H,
-                            const void* W, const ScoreRow* row, const float* dcorr, void* dx, cudaStream_t s) {
+                            const void* W, const ScoreRow* row, const float* dcorr, void* dx, const uint32_t* ctrl,
+                            uint32_t* host_error, cudaStream_t s) {
   score_dx_kernel<<<dim3(static_cast<unsigned>(chunk.rows), blocks_of(H, 512)), 128, 0, s>>>(
-      chunk, part, splits, split_stride, H, static_cast<const __nv_bfloat16*>(W), row, dcorr, static_cast<__nv_bfloat16*>(dx));
+      chunk, part, splits, split_stride, H, static_cast<const __nv_bfloat16*>(W), row, dcorr, static_cast<__nv_bfloat16*>(dx), ctrl,
+      host_error);
   return cudaGetLastError();
 }
 
@@ -1173,8 +1171,9 @@ cudaError_t launch_distill_rows(const DistillArgs& a, cudaStream_t s) {
 
 cudaError_t launch_distill_live(const int64_t* ids, int64_t ld_ids, const void* logits, int64_t ld_logits, int dtype,
                                 int64_t N, int k, int64_t V, uint8_t* live, float* token_loss, uint32_t* ctrl,
-                                cudaStream_t s) {
-  distill_live_kernel<<<blocks_of(N, 8), 256, 0, s>>>(ids, ld_ids, logits, ld_logits, dtype, N, k, V, live, token_loss, ctrl);
+                                bool count, cudaStream_t s) {
+  distill_live_kernel<<<blocks_of(N, 8), 256, 0, s>>>(ids, ld_ids, logits, ld_logits, dtype, N, k, V, live, token_loss, ctrl,
+                                                      count);
   return cudaGetLastError();
 }
 

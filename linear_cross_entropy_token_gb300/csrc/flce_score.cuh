@@ -23,6 +23,15 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// The gradient of one fp32 logit in column j: p from the natural exponential, whose
+// argument has no factor to round
+__device__ __forceinline__ float dlogit_f32(float z, int64_t j, float c, float inv_t, const ScoreRow& q) {
+  const float u = z - q.largest;
+  const float t = max_nan(fmaf(u, c, -q.log2_total), -1000.f);
+  const float d = expf(max_nan(u * inv_t, -700.f)) * q.inv_total * fmaf(q.b, t, q.a);
+  return j == q.target ? d + q.add : d;
+}
+
 // ---------------------------------------------------------------- products
 
 // The ring of a CTA of a pair on 256 x 512 tiles: four 64-deep k-blocks of its 128

@@ -104,15 +104,25 @@ struct ScoreF32Args {
   int64_t sam, sak, sbk, sbn, ldc, M, N, K;
   int32_t accumulate;
   float* part;                   // splits x M x N, or null
-  // statistics of C's 64-column groups (no splits), or null
+  // z = x Wt: the statistics of its 64-column groups, or with `row` their gradient
+  // in z's place
   float2* partials;
   float* part_s;
   int32_t groups;
   float c, inv_temperature;
-  int64_t k_per_split;           // filled in by the launch
+  const ScoreRow* row;
+  int64_t k_per_split;           // filled in by the launches, as what follows
+  int32_t vectors_a, vectors_b;
+};
+struct ScoreF32Pair {
+  ScoreF32Args p[2];
+  int64_t blocks0;               // of the first
 };
 int score_f32_splits(int64_t M, int64_t N, int64_t K, int sms, int64_t most);
-cudaError_t launch_score_f32(ScoreF32Args args, int splits, cudaStream_t s);
+// z with its statistics or as its gradient
+cudaError_t launch_score_f32(ScoreF32Args args, cudaStream_t s);
+// dx (its sum over V in splits) and dW, either may be null, in one launch
+cudaError_t launch_score_f32_backward(const ScoreF32Args* dx, int splits, const ScoreF32Args* dw, cudaStream_t s);
 
 // ------------------------------------------------ flce_score_backward.cu
 
@@ -149,14 +159,13 @@ struct ScoreChunk {
 };
 
 // The rows that count, in order, and how many: t[i] != ignore_index, or live[i] != 0
-// where t is null.
-cudaError_t launch_score_order(const int64_t* t, int64_t ignore_index, const uint8_t* live, int64_t N, int32_t* order,
-                               uint32_t* count, cudaStream_t s);
-// What the rows that do not count get: zeros (any of the outputs may be null)
-struct ScoreSkipArgs {
+// where t is null. The rows that do not get zeros in what is given of the outputs.
+struct ScoreOrderArgs {
   int64_t N, ignore_index;
   const int64_t* t;
-  const uint8_t* live;           // where t is null
+  const uint8_t* live;
+  int32_t* order;
+  uint32_t* count;
   int32_t top;
   float* logprobs;
   float* entropy;
@@ -166,7 +175,7 @@ struct ScoreSkipArgs {
   void* dx;
   int64_t row_bytes;             // of dx
 };
-cudaError_t launch_score_skip(const ScoreSkipArgs& a, cudaStream_t s);
+cudaError_t launch_score_order(const ScoreOrderArgs& a, cudaStream_t s);
 
 struct ScoreRowsArgs {
   ScoreChunk chunk;
@@ -222,8 +231,10 @@ cudaError_t launch_score_prepare(const ScorePrepareArgs& a, cudaStream_t s);
 cudaError_t launch_score_dlogits(int bf16, const ScoreChunk& chunk, const void* z, const float2* partials, int groups, void* d,
                                  int64_t ldv, int64_t V, float c, float inv_temperature, const ScoreRow* row, float* dcorr,
                                  cudaStream_t s);
+// host_error not null: the call's last launch, which hands ctrl's error on to it
 cudaError_t launch_score_dx(const ScoreChunk& chunk, const float* part, int splits, int64_t split_stride, int64_t H,
-                            const void* W, const ScoreRow* row, const float* dcorr, void* dx, cudaStream_t s);
+                            const void* W, const ScoreRow* row, const float* dcorr, void* dx, const uint32_t* ctrl,
+                            uint32_t* host_error, cudaStream_t s);
 // hands ctrl's error on to the host's word
 cudaError_t launch_score_report(const uint32_t* ctrl, uint32_t* host_error, cudaStream_t s);
 
@@ -248,10 +259,10 @@ struct DistillArgs {
 };
 cudaError_t launch_distill_rows(const DistillArgs& a, cudaStream_t s);
 // which of N rows have an entry; the others' losses; ids out of range (ctrl's error;
-// their rows do not count)
+// their rows do not count). count: and how many (kCtrlNValid)
 cudaError_t launch_distill_live(const int64_t* ids, int64_t ld_ids, const void* logits, int64_t ld_logits, int dtype,
                                 int64_t N, int k, int64_t V, uint8_t* live, float* token_loss, uint32_t* ctrl,
-                                cudaStream_t s);
+                                bool count, cudaStream_t s);
 // the columns to pick of a chunk's rows (ScoreGemmArgs)
 struct DistillPickArgs {
   ScoreChunk chunk;

@@ -189,28 +189,33 @@ struct Product {
   int k = 0;
 };
 
+ScoreF32Args f32_logits(const Product& q, void* z) {
+  ScoreF32Args a{};
+  a.A = static_cast<const float*>(q.x);
+  a.B = static_cast<const float*>(q.W);
+  a.C = static_cast<float*>(z);
+  a.sam = a.sbn = q.H;
+  a.sak = a.sbk = 1;
+  a.ldc = q.p->ldv;
+  a.M = q.chunk.rows;
+  a.N = q.V;
+  a.K = q.H;
+  a.c = q.c;
+  a.inv_temperature = q.inv_temperature;
+  return a;
+}
+
 // z of a chunk and its statistics: stored to z where given
 flce_status run_stats(flce_handle_t h, const Product& q, void* z, float2* partials, float* part_s, cudaStream_t s) {
   const double dr = q.chunk.rows, dH = static_cast<double>(q.H), dV = static_cast<double>(q.V);
   const int groups = static_cast<int>(q.p->groups);
   if (!is_bf16(h)) {
-    ScoreF32Args a{};
-    a.A = static_cast<const float*>(q.x);
-    a.B = static_cast<const float*>(q.W);
-    a.C = static_cast<float*>(z);
-    a.sam = a.sbn = q.H;
-    a.sak = a.sbk = 1;
-    a.ldc = q.p->ldv;
-    a.M = q.chunk.rows;
-    a.N = q.V;
-    a.K = q.H;
+    ScoreF32Args a = f32_logits(q, z);
     a.partials = partials;
     a.part_s = part_s;
     a.groups = groups;
-    a.c = q.c;
-    a.inv_temperature = q.inv_temperature;
     FLCE_LAUNCH(FLCE_K_SCORE_STATS, 2 * dr * dH * dV, 4 * (dr * dH + dV * dH + dr * dV) + 12 * dr * groups,
-                launch_score_f32(a, 1, s));
+                launch_score_f32(a, s));
     return FLCE_OK;
   }
   CUtensorMap mx, mw, mz;
@@ -267,6 +272,12 @@ flce_status run_stats(flce_handle_t h, const Product& q, void* z, float2* partia
 // d of a chunk straight from the product
 flce_status run_gradient(flce_handle_t h, const Product& q, void* d, const ScoreRow* row, float* dcorr, cudaStream_t s) {
   const double dr = q.chunk.rows, dH = static_cast<double>(q.H), dV = static_cast<double>(q.V);
+  if (!is_bf16(h)) {
+    ScoreF32Args a = f32_logits(q, d);
+    a.row = row;
+    FLCE_LAUNCH(FLCE_K_SCORE_GRADIENT, 2 * dr * dH * dV, 4 * (dr * dH + dV * dH + dr * dV), launch_score_f32(a, s));
+    return FLCE_OK;
+  }
   CUtensorMap mx, mw, md;
   std::string why;
   if (!map_bf16_2d(&mx, q.x, q.H, q.chunk.rows, q.H * 2, 64, 128, &why) ||
@@ -317,32 +328,22 @@ flce_status run_backward(flce_handle_t h, const Product& q, const Backward& b, c
   const double dw_bytes = b.dW ? 2 * dr * dV + 2 * dr * dH + ((first ? 4.0 : 8.0) - (to16 && b.last ? 2.0 : 0.0)) * dV * dH : 0.0;
   if (!is_bf16(h)) {
     const float* d = static_cast<const float*>(b.d);
-    ScoreF32Args a{};
-    a.A = d;
-    a.N = a.ldc = H;
-    a.sbk = H;
-    a.sbn = 1;
-    if (b.dx) {
-      a.sam = ldv;
-      a.sak = 1;
-      a.B = static_cast<const float*>(q.W);
-      a.C = static_cast<float*>(b.dx) + q.chunk.off * H;
-      a.M = rows;
-      a.K = V;
-      a.part = b.part;
-      FLCE_LAUNCH(FLCE_K_SIMT_GEMM, 2 * dr * dV * dH, 2 * dx_bytes, launch_score_f32(a, static_cast<int>(q.p->splits), s));
-    }
-    if (b.dW) {
-      a.sam = 1;
-      a.sak = ldv;
-      a.B = static_cast<const float*>(q.x);
-      a.C = static_cast<float*>(b.dW);
-      a.M = V;
-      a.K = rows;
-      a.part = nullptr;
-      a.accumulate = !first;
-      FLCE_LAUNCH(FLCE_K_SIMT_GEMM, 2 * dr * dV * dH, 2 * dw_bytes, launch_score_f32(a, 1, s));
-    }
+    ScoreF32Args dx{}, dw{};
+    dx.A = dw.A = d;
+    dx.N = dx.ldc = dx.sbk = dw.N = dw.ldc = dw.sbk = H;
+    dx.sbn = dw.sbn = 1;
+    dx.sam = dw.sak = ldv;
+    dx.sak = dw.sam = 1;
+    dx.B = static_cast<const float*>(q.W);
+    dx.C = static_cast<float*>(b.dx) + q.chunk.off * H;
+    dx.M = dw.K = rows;
+    dx.K = dw.M = V;
+    dx.part = b.part;
+    dw.B = static_cast<const float*>(q.x);
+    dw.C = static_cast<float*>(b.dW);
+    dw.accumulate = !first;
+    FLCE_LAUNCH(FLCE_K_SCORE_BACKWARD, 2 * dr * dV * dH * ((b.dx != nullptr) + (b.dW != nullptr)), 2 * (dx_bytes + dw_bytes),
+                launch_score_f32_backward(b.dx ? &dx : nullptr, static_cast<int>(q.p->splits), b.dW ? &dw : nullptr, s));
     return FLCE_OK;
   }
   std::string why;
@@ -380,7 +381,8 @@ flce_status run_backward(flce_handle_t h, const Product& q, const Backward& b, c
               launch_score_backward(m, a, std::min(units, h->score_clusters), s));
   if (b.dx)
     FLCE_LAUNCH(FLCE_K_DX_REDUCE, 0.0, 4.0 * a.splits * dr * dH + 4 * dr * dH,
-                launch_score_dx(q.chunk, b.part, a.splits, q.p->chunk * H, H, q.W, b.row, b.dcorr, b.dx, s));
+                launch_score_dx(q.chunk, b.part, a.splits, q.p->chunk * H, H, q.W, b.row, b.dcorr, b.dx, q.ctrl,
+                                b.last && b.row ? h->host_ctrl + kHostScoreError : nullptr, s));
   return FLCE_OK;
 }
 
@@ -427,14 +429,12 @@ flce_status logprobs_rows(flce_handle_t h, const flce_logprobs_args* r, const Pl
                           cudaStream_t s) {
   if (!p.compact) return FLCE_OK;
   const double n = static_cast<double>(r->N);
-  FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 12.0 * n,
-              launch_score_order(r->t, r->ignore_index, nullptr, r->N, reinterpret_cast<int32_t*>(ws + p.order),
-                                 reinterpret_cast<uint32_t*>(ws + p.ctrl) + kCtrlNValid, s));
-  if (backward && !dx) return FLCE_OK;
-  ScoreSkipArgs a{};
+  ScoreOrderArgs a{};
   a.N = r->N;
   a.ignore_index = r->ignore_index;
   a.t = r->t;
+  a.order = reinterpret_cast<int32_t*>(ws + p.order);
+  a.count = reinterpret_cast<uint32_t*>(ws + p.ctrl) + kCtrlNValid;
   if (backward) {
     a.dx = dx;
     a.row_bytes = r->H * 2;
@@ -446,7 +446,7 @@ flce_status logprobs_rows(flce_handle_t h, const flce_logprobs_args* r, const Pl
     a.top_logprobs = r->top_logprobs;
     a.top_ids = r->top_ids;
   }
-  FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 8.0 * n, launch_score_skip(a, s));
+  FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 20.0 * n, launch_score_order(a, s));
   return FLCE_OK;
 }
 
@@ -630,21 +630,17 @@ flce_status flce_logprobs_backward(flce_handle_t h, const flce_logprobs_args* r,
                   launch_score_dlogits(bf16, chunk, kept + off * p.ldv * es,
                                        reinterpret_cast<const float2*>(kept + K.partials) + off * p.groups,
                                        static_cast<int>(p.groups), d, p.ldv, r->V, c, inv_t, row, dcorr, s));
-    } else if (bf16) {
+    } else {
       st = run_gradient(h, q, d, row, dcorr, s);
       if (st != FLCE_OK) return st;
-    } else {
-      st = run_stats(h, q, d, nullptr, nullptr, s);
-      if (st != FLCE_OK) return st;
-      FLCE_LAUNCH(FLCE_K_SCORE_DLOGITS, 0.0, 2.0 * es * dr * dV,
-                  launch_score_dlogits(0, chunk, d, nullptr, 0, d, p.ldv, r->V, c, inv_t, row, dcorr, s));
     }
     const Backward b{d,   reinterpret_cast<float*>(ws + p.partials), dx, dW, dw_dtype, reinterpret_cast<float*>(ws + p.dw), row,
                      dcorr, off + p.chunk >= r->N, claims};
     st = run_backward(h, q, b, s);
     if (st != FLCE_OK) return st;
   }
-  FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 4.0, launch_score_report(ctrl, h->host_ctrl + kHostScoreError, s));
+  if (!dx || !bf16)  // else dx's last launch has
+    FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 4.0, launch_score_report(ctrl, h->host_ctrl + kHostScoreError, s));
   return FLCE_OK;
 } catch (...) {
   return FLCE_ERR_BUDGET;
@@ -728,16 +724,16 @@ flce_status flce_distill(flce_handle_t h, const flce_distill_args* r, void* work
   } else {
     FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, n * r->K * (8 + ls),
                 launch_distill_live(r->ids, r->ld_ids, r->logits, r->ld_logits, r->logits_dtype, r->N, static_cast<int>(r->K),
-                                    r->V, live, r->token_loss, ctrl, s));
-    FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 5.0 * n,
-                launch_score_order(nullptr, 0, live, r->N, reinterpret_cast<int32_t*>(ws + p.order), ctrl + kCtrlNValid, s));
-    if (p.compact && r->dx) {
-      ScoreSkipArgs a{};
+                                    r->V, live, r->token_loss, ctrl, !p.compact, s));
+    if (p.compact) {
+      ScoreOrderArgs a{};
       a.N = r->N;
       a.live = live;
+      a.order = reinterpret_cast<int32_t*>(ws + p.order);
+      a.count = ctrl + kCtrlNValid;
       a.dx = r->dx;
       a.row_bytes = r->H * 2;
-      FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, n, launch_score_skip(a, s));
+      FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 6.0 * n, launch_score_order(a, s));
     }
   }
   for (int64_t off = 0; off < r->N; off += p.chunk, ++claims) {
