@@ -622,7 +622,8 @@ flce_status flce_logprobs_forward(flce_handle_t h, const flce_logprobs_args* arg
 
 /* dx (N x H, the handle's dtype) and dW (V x H, dw_dtype: FLCE_DTYPE_FP32, or
  * BF16 on a bf16 handle) from the gradients of logprobs and entropy (N fp32
- * each, or NULL). Either output may be NULL, and its product is not run. args
+ * each, or NULL). Either output may be NULL, and its product is not run; they
+ * share no memory with each other or the inputs. args
  * are those of the forward with stats, entropy (read where d_entropy is given)
  * and kept unchanged; without kept the logits are computed again.
  *   d z_j = (1 / temperature) (d_logprob (1(j = t) - p_j)
@@ -666,8 +667,9 @@ typedef struct flce_distill_args {
 /* Workspace bytes of flce_distill (0: bad argument). Host only. */
 uint64_t flce_distill_workspace_bytes(flce_handle_t h, const flce_distill_args* args);
 
-/* The loss, and the gradients whose pointers are given. The workspace (device,
- * 256-byte aligned) is the caller's.
+/* The loss, and the gradients whose pointers are given (they share no memory with
+ * each other or the inputs). The workspace (device, 256-byte aligned) is the
+ * caller's.
  * Errors: INVALID_ARG, UNSUPPORTED, BUDGET (workspace), CUDA; flce_async_status. */
 flce_status flce_distill(flce_handle_t h, const flce_distill_args* args, void* workspace, uint64_t workspace_bytes,
                          void* stream);

@@ -382,10 +382,10 @@ struct TopSmem {
 // A stored value's bounds: half a step of fp16 (with the fp32 steps around it) and
 // the product's own sum; -inf lies below fp16's range.
 template <class Z>
-__device__ __forceinline__ float stored_bound(float v, float gm, float M, float inv_c, float sign) {
-  if (sizeof(Z) == 2 && v == -INFINITY) return sign < 0.f ? v : fmaf(-65500.f, inv_c, gm);
+__device__ __forceinline__ float stored_bound(float v, float gm, float M, float sign) {
+  if (sizeof(Z) == 2 && v == -INFINITY) return sign < 0.f ? v : gm - 65500.f;
   float reach = fmaxf(fabsf(M), fabsf(v)) * 6.1e-5f;
-  if (sizeof(Z) == 2) reach = fmaf(gm - v, 5.5e-4f, fmaf(1.2e-7f, inv_c, reach));
+  if (sizeof(Z) == 2) reach = fmaf(gm - v, 5.5e-4f, reach + 6e-8f);
   return reach < INFINITY ? fmaf(sign, reach, v) : v;
 }
 
@@ -453,8 +453,8 @@ __device__ __forceinline__ int quick_candidates(const ScoreRowsArgs& a, const fl
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&yv[u]));
-        v[2 * u] = fmaf(f.x, a.inv_c, gm);
-        v[2 * u + 1] = fmaf(f.y, a.inv_c, gm);
+        v[2 * u] = gm + f.x;
+        v[2 * u + 1] = gm + f.y;
       }
     } else {
       const float4 f = *reinterpret_cast<const float4*>(z + j), h = *reinterpret_cast<const float4*>(z + j + 4);
@@ -463,13 +463,13 @@ __device__ __forceinline__ int quick_candidates(const ScoreRowsArgs& a, const fl
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       if (j + u >= a.V) continue;
-      const float upper = stored_bound<Z>(v[u], gm, M, a.inv_c, 1.f);
+      const float upper = stored_bound<Z>(v[u], gm, M, 1.f);
       if (upper < border) continue;
       const int at = atomicAdd(&s.found, 1);
       if (at < kMaxCandidates) {
         id[at] = j + u;
         s.upper[at] = upper;
-        s.lower[at] = stored_bound<Z>(v[u], gm, M, a.inv_c, -1.f);
+        s.lower[at] = stored_bound<Z>(v[u], gm, M, -1.f);
       }
     }
   }
@@ -519,13 +519,13 @@ __device__ __noinline__ int careful_candidates(const ScoreRowsArgs& a, const flo
   auto value = [&](int64_t i) {  // read again each time: keeping them took room from other rows' blocks
     const int64_t j = column(i);
     if constexpr (sizeof(Z) == 2)
-      return fmaf(__half2float(z[j]), a.inv_c, s.gmax[i >> 6]);
+      return s.gmax[i >> 6] + __half2float(z[j]);
     else
       return z[j];
   };
   if (threadIdx.x == 0) s.found = 0;
   __syncthreads();
-  auto bound = [&](int64_t i, float sign) { return order_key(stored_bound<Z>(value(i), s.gmax[i >> 6], M, a.inv_c, sign)); };
+  auto bound = [&](int64_t i, float sign) { return order_key(stored_bound<Z>(value(i), s.gmax[i >> 6], M, sign)); };
   const uint32_t least =
       block_select<THREADS>(nv, a.top, s.sel, above, [&](int64_t i) { return column(i) < a.V ? bound(i, -1.f) : 0u; });
   auto maybe = [&](int64_t i) { return column(i) < a.V && bound(i, 1.f) >= least ? 2 : 0; };
@@ -552,7 +552,8 @@ __device__ __forceinline__ float score_log_p(const ScoreRowsArgs& a, Pair z, flo
 }
 
 __device__ __forceinline__ void report(const uint32_t* ctrl, uint32_t* host_error) {
-  const uint32_t code = ld_volatile_u32(ctrl);
+  uint32_t code = ld_volatile_u32(ctrl + kCtrlError);
+  if (code == 0) code = ld_volatile_u32(ctrl + kCtrlBadId);
   if (code != 0) *reinterpret_cast<volatile uint32_t*>(host_error) = code;
 }
 
@@ -737,7 +738,7 @@ __global__ void __launch_bounds__(128) score_prepare_kernel(const ScorePrepareAr
     const bool ignored = live && t == a.ignore_index, bad = live && !ignored && (t < 0 || t >= a.V);
     live = live && !ignored && !bad;
     if (threadIdx.x == 0) {
-      if (bad) atomicCAS(a.ctrl, 0u, kErrBadTarget);
+      if (bad) a.ctrl[kCtrlBadId] = kErrBadTarget;
       ScoreRow q{0.f, 0.f, 0.f, 0.f, 0.f, -1, 0.f};
       if (live) {
         const float2 st = a.stats[r];
@@ -775,7 +776,7 @@ __device__ __forceinline__ void dlogits8(uint4 in, __nv_bfloat16* d, int64_t j, 
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&iv[i]));
-    const float t0 = max_nan(y.x + shift, -1000.f), t1 = max_nan(y.y + shift, -1000.f);
+    const float t0 = max_nan(fmaf(y.x, c, shift), -1000.f), t1 = max_nan(fmaf(y.y, c, shift), -1000.f);
     v[2 * i] = ex2(t0) * fmaf(q.b, t0, q.a);
     v[2 * i + 1] = ex2(t1) * fmaf(q.b, t1, q.a);
   }
@@ -929,7 +930,7 @@ __global__ void __launch_bounds__(256) distill_live_kernel(const int64_t* __rest
   if (lane == 0 && r < N) {
     live[r] = any && !bad;
     if (!any || bad) token_loss[r] = 0.f;
-    if (bad) atomicCAS(ctrl + kCtrlError, 0u, kErrBadTarget);
+    if (bad) ctrl[kCtrlBadId] = kErrBadTarget;
     if (count && any && !bad) atomicAdd(ctrl + kCtrlNValid, 1u);
   }
 }
@@ -1085,9 +1086,9 @@ __global__ void __launch_bounds__(1024) distill_finish_kernel(const float* __res
   if (threadIdx.x < 32) {
     v = warp_sum(s_sum[threadIdx.x]);
     if (threadIdx.x == 0) {
-      const uint32_t n = ctrl[kCtrlNValid], code = ctrl[kCtrlError];
+      const uint32_t n = ctrl[kCtrlNValid], code = ctrl[kCtrlError] | ctrl[kCtrlBadId];
       *loss = code != 0 ? NAN : (n > 0 ? v.hi / static_cast<float>(n) : 0.f);
-      if (code != 0) *reinterpret_cast<volatile uint32_t*>(host_error) = code;
+      report(ctrl, host_error);
     }
   }
 }

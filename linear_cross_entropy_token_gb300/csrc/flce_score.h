@@ -15,6 +15,10 @@ constexpr int kScoreMaxTop = 64;
 constexpr int kScoreMaxTeacher = 256;
 constexpr int kScoreGroup = 64;          // vocabulary columns per partial
 
+// Word of a call's control block for a token id out of range: not kCtrlError's, at
+// which the products' waits give up (the other rows' results stand).
+constexpr int kCtrlBadId = 8;
+
 // What a row's gradient is made of: with t = log2 p = (z - largest) c - log2_total,
 // d_j = 2^t (a + b t), plus `add` at the target's column.
 struct ScoreRow {
@@ -37,7 +41,7 @@ struct ScoreGemmArgs {
   const uint32_t* live;          // how many of the call's rows count, or null: all do
   int64_t off;                   // the chunk's first row, of those
   int32_t groups;                // partials per row: ceil(V / 64)
-  int32_t store;                 // statistics: also store the scaled logits
+  int32_t store;                 // statistics: also store the logits
   float c;                       // log2(e) / temperature, times score_gain(H)
   float2* partials;              // [rows][groups]: largest z, sum of 2^((z - largest) c)
   float* part_s;                 // [rows][groups]: sum of y 2^y, y = (z - largest) c
@@ -53,7 +57,8 @@ struct ScoreGemmArgs {
   uint64_t timeout_ns;
 };
 
-// kScoreStats: the statistics, and with `store` y as fp16 [rows][ldv] (o); kScorePick:
+// kScoreStats: the statistics, and with `store` z as fp16 [rows][ldv], relative to
+// its group's largest (o); kScorePick:
 // those and z of picked columns; kScoreGradient: d as bf16 [rows][ldv] (o).
 // a: x (box 64 x 128), b: W (box 64 x 128), o: box 64 x 128
 enum ScoreMode : int { kScoreStats = 0, kScoreGradient = 1, kScorePick = 2 };
@@ -85,7 +90,7 @@ struct ScoreFewArgs {
   int32_t tiles, stages, tmem_columns;  // filled in by the launch
   float c;
   int64_t ldv;
-  __half* z;                     // [rows][ldv] fp16 y, or null
+  __half* z;                     // [rows][ldv] as ScoreGemmArgs' stored, or null
   float2* partials;
   float* part_s;
   uint32_t* ctrl;
@@ -180,9 +185,9 @@ cudaError_t launch_score_order(const ScoreOrderArgs& a, cudaStream_t s);
 struct ScoreRowsArgs {
   ScoreChunk chunk;
   int32_t top, groups;
-  int32_t bf16;                  // x and W bf16 and z stored as fp16 y, or all fp32
+  int32_t bf16;                  // x and W bf16 and z stored as fp16, or all fp32
   int64_t H, V, ldv, ignore_index;
-  float c, inv_c;                // log2(e) / temperature, times gain
+  float c;                       // log2(e) / temperature, times gain
   float inv_temperature;
   float scale;                   // inv_temperature times gain
   float loss;                    // gain - 1
@@ -191,7 +196,7 @@ struct ScoreRowsArgs {
   const int64_t* t;              // null: no given tokens
   const float2* partials;        // by row of the chunk
   const float* part_s;
-  const void* z;                 // [rows][ldv] fp16 y, or fp32 z; read for alternatives only
+  const void* z;                 // [rows][ldv] fp16 z - its group's largest, or fp32 z; read for alternatives only
   float* logprobs;
   float* entropy;
   float2* stats;                 // largest z, log of the sum of exp((z - largest) / temperature)
@@ -227,7 +232,7 @@ struct ScorePrepareArgs {
 };
 cudaError_t launch_score_prepare(const ScorePrepareArgs& a, cudaStream_t s);
 
-// d from kept logits: y as fp16 with its groups' largest (partials), or fp32 z
+// d from kept logits: fp16 relative to their groups' largest (partials), or fp32 z
 cudaError_t launch_score_dlogits(int bf16, const ScoreChunk& chunk, const void* z, const float2* partials, int groups, void* d,
                                  int64_t ldv, int64_t V, float c, float inv_temperature, const ScoreRow* row, float* dcorr,
                                  cudaStream_t s);
@@ -252,7 +257,7 @@ struct DistillArgs {
   const void* logits;
   const float2* partials;        // by row of the chunk
   const float* picked;           // [rows][k]: z of the entries that count (fp32: taken from z)
-  void* z;                       // [rows][ldv] fp16 y / fp32 z in, bf16 / fp32 d out
+  void* z;                       // [rows][ldv] fp16 / fp32 z in, bf16 / fp32 d out
   float* token_loss;
   const uint8_t* alive;          // as ScorePrepareArgs
   const uint32_t* ctrl;          // kCtrlNValid: rows that count

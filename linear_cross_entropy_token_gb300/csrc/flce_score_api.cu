@@ -541,7 +541,6 @@ flce_status flce_logprobs_forward(flce_handle_t h, const flce_logprobs_args* r, 
     a.ldv = p.ldv;
     a.ignore_index = r->ignore_index;
     a.c = static_cast<float>(c);
-    a.inv_c = static_cast<float>(1.0 / c);
     a.inv_temperature = inv_t;
     a.scale = static_cast<float>(gain / r->temperature);
     a.loss = static_cast<float>(gain - 1.0);

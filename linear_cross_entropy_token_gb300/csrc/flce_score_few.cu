@@ -200,8 +200,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-          const float d0 = (z[i] - m) * a.c, d1 = (z[i + 1] - m) * a.c;
-          const float y0 = max_nan(d0, -1000.f), y1 = max_nan(d1, -1000.f);
+          const float d0 = z[i] - m, d1 = z[i + 1] - m;
+          const float y0 = max_nan(d0 * a.c, -1000.f), y1 = max_nan(d1 * a.c, -1000.f);
           const float e0 = ex2(y0), e1 = ex2(y1);
           l += e0 + e1;
           s = fmaf(y0, e0, fmaf(y1, e1, s));

@@ -63,7 +63,7 @@ __device__ __forceinline__ float group_max(Group g, int ncv) {
   return max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3]));
 }
 
-// Their statistics relative to it, and y staged as fp16
+// Their statistics relative to it, and z - m staged as fp16
 template <bool STORE>
 __device__ __forceinline__ void group_stats(Group g, float m, float c, float2* part, float* part_s, bool rvalid,
                                             uint8_t* buf, int row) {
@@ -76,9 +76,9 @@ __device__ __forceinline__ void group_stats(Group g, float m, float c, float2* p
       uint32_t w[4];
 #pragma unroll
       for (int i = 8 * j; i < 8 * j + 8; i += 2) {
-        const float d0 = (__uint_as_float(r[i]) - m) * c, d1 = (__uint_as_float(r[i + 1]) - m) * c;
+        const float d0 = __uint_as_float(r[i]) - m, d1 = __uint_as_float(r[i + 1]) - m;
         // at -1000 the exponential is 0 and y 2^y is too, which -inf would make NaN
-        const float y0 = max_nan(d0, -1000.f), y1 = max_nan(d1, -1000.f);
+        const float y0 = max_nan(d0 * c, -1000.f), y1 = max_nan(d1 * c, -1000.f);
         const float e0 = ex2(y0), e1 = ex2(y1);
         l[i & 3] += e0;
         l[(i + 1) & 3] += e1;

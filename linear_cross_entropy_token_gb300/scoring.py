@@ -121,8 +121,15 @@ def _vector(name, t, n, dev):
     return t.data_ptr()
 
 
-def _gradient(name, want, like, dtypes):
-    """The tensor of a gradient: None for no gradient, a new one for True, or the caller's."""
+def _overlap(a, b) -> bool:
+    """Whether two contiguous tensors share memory."""
+    first, second = a.data_ptr(), b.data_ptr()
+    return (first < second + b.numel() * b.element_size() and second < first + a.numel() * a.element_size())
+
+
+def _gradient(name, want, like, dtypes, read=()):
+    """The tensor of a gradient: None for no gradient, a new one for True, or the
+    caller's, which may share no memory with what the call reads."""
     if want is None or want is False:
         return None
     if want is True:
@@ -131,6 +138,8 @@ def _gradient(name, want, like, dtypes):
             or want.device != like.device or not want.is_contiguous()):
         raise ValueError(f"{name} must be True, None or a contiguous tensor of shape {tuple(like.shape)}, "
                          f"{' or '.join(str(d) for d in dtypes)}, on {like.device}")
+    if any(t is not None and t.is_contiguous() and t.device == want.device and _overlap(want, t) for t in read):
+        raise ValueError(f"{name} must not share memory with the inputs or the other gradient")
     return want
 
 
@@ -193,7 +202,8 @@ def token_logprobs_backward(r: TokenLogprobs, x: torch.Tensor, W: torch.Tensor, 
 
     dx, dW: True for a new tensor of the type of x or W, None to leave that
     gradient (and its product) out, or the tensor to write: dW may be float32
-    for bfloat16 W. They are overwritten.
+    for bfloat16 W. They are overwritten, and may share no memory with the
+    inputs.
     """
     if t is None:
         raise ValueError("the backward needs the tokens")
@@ -206,8 +216,9 @@ def token_logprobs_backward(r: TokenLogprobs, x: torch.Tensor, W: torch.Tensor, 
         raise ValueError("the kept logits are of other sizes")
     p_logprobs = _vector("d_logprobs", d_logprobs, N, dev)
     p_entropy = _vector("d_entropy", d_entropy, N, dev)
-    out_x = _gradient("dx", dx, x, (x.dtype,))
-    out_W = _gradient("dW", dW, W, tuple({W.dtype, torch.float32}))
+    read = (x, W, t, d_logprobs, d_entropy, r.entropy, r.stats, r.kept)
+    out_x = _gradient("dx", dx, x, (x.dtype,), read)
+    out_W = _gradient("dW", dW, W, tuple({W.dtype, torch.float32}), (*read, out_x))
     a = r.bind(x, W, t, 0)
     ref = ctypes.byref(a)
     nbytes = int(h.lib.flce_logprobs_workspace_bytes(h.h, ref, 1, _dw_code(out_W)))
@@ -235,8 +246,8 @@ def distill(x: torch.Tensor, W: torch.Tensor, ids: torch.Tensor, logits: torch.T
     ld_ids, ld_logits = check_distill_tensors(x, W, ids, logits, temperature)
     h = _handle(x, handle)
     N, V, dev = x.shape[0], W.shape[0], x.device
-    out_x = _gradient("dx", dx, x, (x.dtype,)) if backward else None
-    out_W = _gradient("dW", dW, W, tuple({W.dtype, torch.float32})) if backward else None
+    out_x = _gradient("dx", dx, x, (x.dtype,), (x, W, ids, logits)) if backward else None
+    out_W = _gradient("dW", dW, W, tuple({W.dtype, torch.float32}), (x, W, ids, logits, out_x)) if backward else None
     loss = torch.empty((), dtype=torch.float32, device=dev)
     token_loss = torch.empty(N, dtype=torch.float32, device=dev)
     a = DistillArgs(x.data_ptr(), W.data_ptr(), ids.data_ptr(), logits.data_ptr(), N, x.shape[1], V, ids.shape[1],

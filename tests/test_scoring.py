@@ -149,6 +149,11 @@ def test_gradient_tensors():
             _gradient("dW", bad, W, both)
     with pytest.raises(ValueError):
         _gradient("dx", torch.zeros(20, 16), W, (torch.bfloat16,))
+    flat = torch.zeros(40, 16, dtype=torch.bfloat16)
+    assert _gradient("dW", flat[20:], flat[:20], both, (flat[:20], None)).data_ptr() == flat[20:].data_ptr()
+    for shared in (flat[:20], flat[19:39]):
+        with pytest.raises(ValueError):
+            _gradient("dW", flat[:20], W, both, (W, shared))
     for bad in (torch.zeros(5), torch.zeros(6).half(), torch.zeros(12)[::2], torch.zeros(6, device="meta"), torch.zeros(6, 1)):
         with pytest.raises(ValueError):
             _vector("d_logprobs", bad, 6, torch.device("cpu"))
