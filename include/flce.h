@@ -624,8 +624,8 @@ flce_status flce_logprobs_forward(flce_handle_t h, const flce_logprobs_args* arg
  * BF16 on a bf16 handle) from the gradients of logprobs and entropy (N fp32
  * each, or NULL). Either output may be NULL, and its product is not run; they
  * share no memory with each other or the inputs. args
- * are those of the forward with stats, entropy (read where d_entropy is given)
- * and kept unchanged; without kept the logits are computed again.
+ * are those of the forward with logprobs, stats, entropy (read where d_entropy
+ * is given) and kept unchanged; without kept the logits are computed again.
  *   d z_j = (1 / temperature) (d_logprob (1(j = t) - p_j)
  *                              - d_entropy p_j (log p_j + entropy))
  * rounded to bf16 on a bf16 handle (the target's entry in full for dx), sums

@@ -724,7 +724,8 @@ __device__ __forceinline__ void copy_row(const uint8_t* from, uint8_t* to, int64
   }
 }
 
-// d_j = (1 / temperature) (g [j = t] - p_j (g + h (log p_j + H))), as a + b log2 p.
+// d_j = (1 / temperature) (g [j = t] - p_j (g + h (log p_j + H))), as a + b log2 p, and
+// whole at the target.
 // Rows that do not count get zeros, and a zero row of x, so that nothing that
 // stands there (it may be NaN) reaches dW.
 __global__ void __launch_bounds__(128) score_prepare_kernel(const ScorePrepareArgs a) {
@@ -750,13 +751,16 @@ __global__ void __launch_bounds__(128) score_prepare_kernel(const ScorePrepareAr
         q.inv_total = expf(-st.y);
         q.a = -inv * (a.d_entropy ? fmaf(h, a.entropy[r], g) : g);
         q.b = -inv * h * kLn2;
-        q.add = inv * g;
         q.target = static_cast<int32_t>(t);
+        // the target's entry, from its exact logit: g (1 - p) without cancellation
+        const float lp = a.logprobs[r];
+        q.at = -inv * (g * expm1f(lp) + (a.d_entropy ? h * expf(lp) * (lp + a.entropy[r]) : 0.f));
         // what the exponentials' lower limit would hide
-        if (!(fabsf(q.log2_total) < INFINITY) || !(fabsf(q.largest) < INFINITY)) q.a = NAN;
+        if (!(fabsf(q.log2_total) < INFINITY) || !(fabsf(q.largest) < INFINITY)) q.a = q.at = NAN;
       }
       a.row[i] = q;
-      a.dcorr[i] = 0.f;
+      // what bf16 leaves of it goes to dx
+      a.dcorr[i] = q.at - __bfloat162float(__float2bfloat16_rn(q.at));
     }
   }
   uint8_t* to = static_cast<uint8_t*>(a.xm) + i * a.row_bytes;
@@ -769,7 +773,7 @@ __global__ void __launch_bounds__(128) score_prepare_kernel(const ScorePrepareAr
 // Eight columns of a row's gradient from the stored logits. The padding behind the
 // last column (ldv is a multiple of 64) becomes zero.
 __device__ __forceinline__ void dlogits8(uint4 in, __nv_bfloat16* d, int64_t j, int64_t V, float gmax, float c,
-                                         const ScoreRow& q, float* dcorr) {
+                                         const ScoreRow& q) {
   const uint32_t iv[4] = {in.x, in.y, in.z, in.w};
   const float shift = fmaf(gmax - q.largest, c, -q.log2_total);
   float v[8];
@@ -785,14 +789,6 @@ __device__ __forceinline__ void dlogits8(uint4 in, __nv_bfloat16* d, int64_t j, 
     for (int i = 0; i < 8; ++i)
       if (j + i >= V) v[i] = 0.f;
   }
-  if (q.target >= j && q.target < j + 8) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (j + i == q.target) {
-        v[i] += q.add;
-        if (dcorr) *dcorr = v[i] - __bfloat162float(__float2bfloat16_rn(v[i]));
-      }
-  }
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -807,7 +803,7 @@ __device__ __forceinline__ void dlogits8(uint4 in, __nv_bfloat16* d, int64_t j, 
 constexpr int kPieces = 4;
 
 __device__ __forceinline__ void dlogits_pieces(const __half* z, __nv_bfloat16* d, int64_t j, int64_t step, int64_t ldv,
-                                               int64_t V, const float2* part, float c, const ScoreRow& q, float* dcorr) {
+                                               int64_t V, const float2* part, float c, const ScoreRow& q) {
   uint4 in[kPieces];
   float gmax[kPieces];
 #pragma unroll
@@ -818,7 +814,7 @@ __device__ __forceinline__ void dlogits_pieces(const __half* z, __nv_bfloat16* d
     }
 #pragma unroll
   for (int i = 0; i < kPieces; ++i)
-    if (j + i * step < ldv) dlogits8(in[i], d, j + i * step, V, gmax[i], c, q, dcorr);
+    if (j + i * step < ldv) dlogits8(in[i], d, j + i * step, V, gmax[i], c, q);
 }
 
 __device__ __forceinline__ void dlogits4(const float* z, float* d, int64_t j, int64_t V, float c, float inv_t,
@@ -835,19 +831,19 @@ constexpr int kDlogitsThreads = 256;
 
 __global__ void __launch_bounds__(kDlogitsThreads) score_dlogits_bf16_kernel(
     const ScoreChunk chunk, const __half* z, const float2* __restrict__ partials, int groups, __nv_bfloat16* d, int64_t ldv, int64_t V, float c,
-    const ScoreRow* __restrict__ row, float* __restrict__ dcorr) {
+    const ScoreRow* __restrict__ row) {
   const int64_t r = blockIdx.x;
   if (r >= tail_end(chunk, chunk_rows(chunk.live, chunk.off, chunk.rows))) return;
   const ScoreRow q = row[r];
   const int64_t j = (static_cast<int64_t>(blockIdx.y) * kPieces * kDlogitsThreads + threadIdx.x) * 8;
-  if (q.a == 0.f && q.b == 0.f && q.add == 0.f) {
+  if (q.a == 0.f && q.b == 0.f) {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i)
       if (j + i * kDlogitsThreads * 8 < ldv)
         *reinterpret_cast<uint4*>(d + r * ldv + j + i * kDlogitsThreads * 8) = make_uint4(0, 0, 0, 0);
     return;
   }
-  dlogits_pieces(z + r * ldv, d + r * ldv, j, kDlogitsThreads * 8, ldv, V, partials + r * groups, c, q, dcorr + r);
+  dlogits_pieces(z + r * ldv, d + r * ldv, j, kDlogitsThreads * 8, ldv, V, partials + r * groups, c, q);
 }
 
 __global__ void __launch_bounds__(kDlogitsThreads) score_dlogits_f32_kernel(const ScoreChunk chunk, const float* z, float* d, int64_t ldv, int64_t V,
@@ -857,11 +853,20 @@ __global__ void __launch_bounds__(kDlogitsThreads) score_dlogits_f32_kernel(cons
   const ScoreRow q = row[r];
   const int64_t j = (static_cast<int64_t>(blockIdx.y) * kDlogitsThreads + threadIdx.x) * 4;
   if (j >= ldv) return;
-  if (q.a == 0.f && q.b == 0.f && q.add == 0.f) {
+  if (q.a == 0.f && q.b == 0.f) {
     *reinterpret_cast<float4*>(d + r * ldv + j) = make_float4(0.f, 0.f, 0.f, 0.f);
     return;
   }
   dlogits4(z + r * ldv, d + r * ldv, j, V, c, inv_t, q);
+}
+
+// The targets' entries, a thread a row
+__global__ void __launch_bounds__(256) score_target_kernel(const ScoreChunk chunk, __nv_bfloat16* d, int64_t ldv,
+                                                           const ScoreRow* __restrict__ row) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= chunk_rows(chunk.live, chunk.off, chunk.rows)) return;
+  const ScoreRow q = row[i];
+  if (q.target >= 0) d[i * ldv + q.target] = __float2bfloat16_rn(q.at);
 }
 
 // dx: the sum of the splits in their order, with the target's entry put right,
@@ -1056,7 +1061,7 @@ __global__ void __launch_bounds__(kDistillThreads) distill_rows_kernel(const Dis
     if constexpr (bf16) {
       for (int64_t j = threadIdx.x * 8; j < a.ldv; j += kPieces * kDistillThreads * 8)
         dlogits_pieces(reinterpret_cast<const __half*>(zrow), reinterpret_cast<__nv_bfloat16*>(zrow), j, kDistillThreads * 8,
-                       a.ldv, a.V, part, a.c, row, nullptr);
+                       a.ldv, a.V, part, a.c, row);
     } else {
       for (int64_t j = threadIdx.x * 4; j < a.ldv; j += kDistillThreads * 4)
         dlogits4(reinterpret_cast<const float*>(zrow), reinterpret_cast<float*>(zrow), j, a.V, a.c, inv, row);
@@ -1128,15 +1133,20 @@ cudaError_t launch_score_prepare(const ScorePrepareArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_score_dlogits(int bf16, const ScoreChunk& chunk, const void* z, const float2* partials, int groups, void* d,
-                                 int64_t ldv, int64_t V, float c, float inv_temperature, const ScoreRow* row, float* dcorr,
+                                 int64_t ldv, int64_t V, float c, float inv_temperature, const ScoreRow* row,
                                  cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(chunk.rows), blocks_of(ldv, kDlogitsThreads * (bf16 ? 8 * kPieces : 4)));
   if (bf16)
     score_dlogits_bf16_kernel<<<grid, kDlogitsThreads, 0, s>>>(chunk, static_cast<const __half*>(z), partials, groups,
-                                                              static_cast<__nv_bfloat16*>(d), ldv, V, c, row, dcorr);
+                                                              static_cast<__nv_bfloat16*>(d), ldv, V, c, row);
   else
     score_dlogits_f32_kernel<<<grid, kDlogitsThreads, 0, s>>>(chunk, static_cast<const float*>(z), static_cast<float*>(d), ldv,
                                                              V, c, inv_temperature, row);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_score_target(const ScoreChunk& chunk, void* d, int64_t ldv, const ScoreRow* row, cudaStream_t s) {
+  score_target_kernel<<<blocks_of(chunk.rows, 256), 256, 0, s>>>(chunk, static_cast<__nv_bfloat16*>(d), ldv, row);
   return cudaGetLastError();
 }
 

@@ -29,7 +29,7 @@ __device__ __forceinline__ float dlogit_f32(float z, int64_t j, float c, float i
   const float u = z - q.largest;
   const float t = max_nan(fmaf(u, c, -q.log2_total), -1000.f);
   const float d = expf(max_nan(u * inv_t, -700.f)) * q.inv_total * fmaf(q.b, t, q.a);
-  return j == q.target ? d + q.add : d;
+  return j == q.target ? q.at : d;
 }
 
 // ---------------------------------------------------------------- products
@@ -41,6 +41,8 @@ constexpr uint32_t kRingA = kBM * kBK * 2;
 constexpr uint32_t kRingB = kBN * kBK * 2;
 constexpr uint32_t kRingHalfB = kRingB / 2;
 constexpr uint32_t kStagingBytes = 128 * 128;  // 128 rows x 128 bytes
+// Each warp stages and copies out its own 32 rows: no warp waits for another
+constexpr uint32_t kWarpStaging = kStagingBytes / 4;
 constexpr uint32_t kAccumulatorColumns = 512;
 // warpgroup 0 loads and issues; two epilogue warpgroups of 128 threads
 constexpr int kPairThreads = 384;
@@ -67,7 +69,7 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64
 }
 
 // Eight 16-bit columns, the j-th such piece of a row of a 128-row x 128-byte staging
-// tile in the 128-byte swizzle. Each piece is staged as it is computed: a group's 32
+// tile (or a warp's 32 rows of it) in the 128-byte swizzle. Each piece is staged as it is computed: a group's 32
 // words at once would take registers that three groups of sums leave no room for.
 __device__ __forceinline__ void stage_piece(uint8_t* buf, int row, int j, const uint32_t (&w)[4]) {
   reinterpret_cast<uint4*>(buf + row * 128)[j ^ (row & 7)] = make_uint4(w[0], w[1], w[2], w[3]);

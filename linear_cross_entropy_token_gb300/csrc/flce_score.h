@@ -20,12 +20,12 @@ constexpr int kScoreGroup = 64;          // vocabulary columns per partial
 constexpr int kCtrlBadId = 8;
 
 // What a row's gradient is made of: with t = log2 p = (z - largest) c - log2_total,
-// d_j = 2^t (a + b t), plus `add` at the target's column.
+// d_j = 2^t (a + b t), and `at` at the target's column.
 struct ScoreRow {
   float largest;       // of the row's logits, as the product gave them
   float log2_total;    // log2 of the sum of 2^((z - largest) c)
   float a, b;
-  float add;
+  float at;
   int32_t target;      // column, -1: none
   float inv_total;     // fp32 logits: p = exp((z - largest) / temperature) inv_total
 };
@@ -52,7 +52,6 @@ struct ScoreGemmArgs {
   const int2* entries;           // [rows][k]: column, slot
   float* picked;                 // [rows][k]: z of each slot
   int32_t k;
-  float* dcorr;                  // gradient: [rows] what rounding took from the target's entry
   uint32_t* ctrl;                // word 0: first error
   uint64_t timeout_ns;
 };
@@ -60,7 +59,7 @@ struct ScoreGemmArgs {
 // kScoreStats: the statistics, and with `store` z as fp16 [rows][ldv], relative to
 // its group's largest (o); kScorePick:
 // those and z of picked columns; kScoreGradient: d as bf16 [rows][ldv] (o).
-// a: x (box 64 x 128), b: W (box 64 x 128), o: box 64 x 128
+// a: x (box 64 x 128), b: W (box 64 x 128), o: box 64 x 32
 enum ScoreMode : int { kScoreStats = 0, kScoreGradient = 1, kScorePick = 2 };
 constexpr int kScoreTileColumns = 512;
 constexpr int kScorePart = 128;
@@ -223,6 +222,7 @@ struct ScorePrepareArgs {
   float inv_temperature;
   const int64_t* t;              // null: rows of x alone
   const float2* stats;
+  const float* logprobs;
   const float* entropy;          // read where d_entropy is given
   const float* d_logprobs;       // may be null
   const float* d_entropy;        // may be null
@@ -234,8 +234,10 @@ cudaError_t launch_score_prepare(const ScorePrepareArgs& a, cudaStream_t s);
 
 // d from kept logits: fp16 relative to their groups' largest (partials), or fp32 z
 cudaError_t launch_score_dlogits(int bf16, const ScoreChunk& chunk, const void* z, const float2* partials, int groups, void* d,
-                                 int64_t ldv, int64_t V, float c, float inv_temperature, const ScoreRow* row, float* dcorr,
+                                 int64_t ldv, int64_t V, float c, float inv_temperature, const ScoreRow* row,
                                  cudaStream_t s);
+// bf16 d's entries at the targets
+cudaError_t launch_score_target(const ScoreChunk& chunk, void* d, int64_t ldv, const ScoreRow* row, cudaStream_t s);
 // host_error not null: the call's last launch, which hands ctrl's error on to it
 cudaError_t launch_score_dx(const ScoreChunk& chunk, const float* part, int splits, int64_t split_stride, int64_t H,
                             const void* W, const ScoreRow* row, const float* dcorr, void* dx, const uint32_t* ctrl,

@@ -243,7 +243,7 @@ flce_status run_stats(flce_handle_t h, const Product& q, void* z, float2* partia
     return FLCE_OK;
   }
   mz = mx;  // not used without a store
-  if (z && !map_bf16_2d(&mz, z, q.V, q.chunk.rows, q.p->ldv * 2, 64, 128, &why))
+  if (z && !map_bf16_2d(&mz, z, q.V, q.chunk.rows, q.p->ldv * 2, 64, 32, &why))
     return fail(h, FLCE_ERR_INVALID_ARG, "%s", why.c_str());
   ScoreGemmArgs a{};
   const int num_m = static_cast<int>(cdiv(q.chunk.rows, kTileRows));
@@ -270,7 +270,7 @@ flce_status run_stats(flce_handle_t h, const Product& q, void* z, float2* partia
 }
 
 // d of a chunk straight from the product
-flce_status run_gradient(flce_handle_t h, const Product& q, void* d, const ScoreRow* row, float* dcorr, cudaStream_t s) {
+flce_status run_gradient(flce_handle_t h, const Product& q, void* d, const ScoreRow* row, cudaStream_t s) {
   const double dr = q.chunk.rows, dH = static_cast<double>(q.H), dV = static_cast<double>(q.V);
   if (!is_bf16(h)) {
     ScoreF32Args a = f32_logits(q, d);
@@ -282,7 +282,7 @@ flce_status run_gradient(flce_handle_t h, const Product& q, void* d, const Score
   std::string why;
   if (!map_bf16_2d(&mx, q.x, q.H, q.chunk.rows, q.H * 2, 64, 128, &why) ||
       !map_bf16_2d(&mw, q.W, q.H, q.V, q.H * 2, 64, 128, &why) ||
-      !map_bf16_2d(&md, d, q.V, q.chunk.rows, q.p->ldv * 2, 64, 128, &why))
+      !map_bf16_2d(&md, d, q.V, q.chunk.rows, q.p->ldv * 2, 64, 32, &why))
     return fail(h, FLCE_ERR_INVALID_ARG, "%s", why.c_str());
   ScoreGemmArgs a{};
   const int num_m = static_cast<int>(cdiv(q.chunk.rows, kTileRows));
@@ -296,7 +296,6 @@ flce_status run_gradient(flce_handle_t h, const Product& q, void* d, const Score
   a.c = q.c;
   a.least = q.chunk.off == 0;  // zeros, where no row of the call counts
   a.row = row;
-  a.dcorr = dcorr;
   a.ctrl = q.ctrl;
   a.timeout_ns = h->timeout_ns;
   FLCE_LAUNCH(FLCE_K_SCORE_GRADIENT, 2 * dr * dH * dV, 2 * (dr + dV) * dH + 2 * dr * dV,
@@ -616,6 +615,7 @@ flce_status flce_logprobs_backward(flce_handle_t h, const flce_logprobs_args* r,
     a.inv_temperature = inv_t;
     a.t = r->t;
     a.stats = reinterpret_cast<const float2*>(r->stats);
+    a.logprobs = r->logprobs;
     a.entropy = r->entropy;
     a.d_logprobs = d_logprobs;
     a.d_entropy = d_entropy;
@@ -628,11 +628,12 @@ flce_status flce_logprobs_backward(flce_handle_t h, const flce_logprobs_args* r,
       FLCE_LAUNCH(FLCE_K_SCORE_DLOGITS, 0.0, 2.0 * es * dr * dV,
                   launch_score_dlogits(bf16, chunk, kept + off * p.ldv * es,
                                        reinterpret_cast<const float2*>(kept + K.partials) + off * p.groups,
-                                       static_cast<int>(p.groups), d, p.ldv, r->V, c, inv_t, row, dcorr, s));
+                                       static_cast<int>(p.groups), d, p.ldv, r->V, c, inv_t, row, s));
     } else {
-      st = run_gradient(h, q, d, row, dcorr, s);
+      st = run_gradient(h, q, d, row, s);
       if (st != FLCE_OK) return st;
     }
+    if (bf16) FLCE_LAUNCH(FLCE_K_SCORE_OTHER, 0.0, 34.0 * dr, launch_score_target(chunk, d, p.ldv, row, s));
     const Backward b{d,   reinterpret_cast<float*>(ws + p.partials), dx, dW, dw_dtype, reinterpret_cast<float*>(ws + p.dw), row,
                      dcorr, off + p.chunk >= r->N, claims};
     st = run_backward(h, q, b, s);

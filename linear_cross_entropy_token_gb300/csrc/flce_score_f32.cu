@@ -12,9 +12,9 @@
 //
 // What bounds it: issue (the multiply-adds are four fifths of its instructions) for
 // long sums; fp32 inputs are small models', where latency does. 256 x 128 x 4096, us
-// a product under ncu: 11 to 12; with element-wise asynchronous copies instead of
-// vectors 15 to 17 (half of the instructions were theirs), the loss's kernel for such
-// inputs (4 x 4 outputs a thread, blocks of 16) 20.
+// a product under a profiler: 14 to 18; with element-wise asynchronous copies instead
+// of vectors half of the instructions were theirs; the loss's kernel for such inputs
+// (4 x 4 outputs a thread, blocks of 16) 20.
 #include <algorithm>
 
 #include "flce_score.cuh"

@@ -13,7 +13,8 @@
 // A tile's accumulator has a column of W a lane and a token a register; the epilogue
 // turns it over in shared memory, and four threads take 64 columns of a token.
 //
-// Measured (one token / 48 tokens, x of 4096 columns): see the table in the design notes' place below.
+// Measured at 4096 x 128256: one token 180 us (5.8 TB/s) where the pair tiles take 238,
+// 48 tokens 212 where they take 216; at 64 tokens the two meet.
 #include <cuda_fp16.h>
 
 #include <algorithm>

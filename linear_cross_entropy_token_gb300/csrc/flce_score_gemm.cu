@@ -6,20 +6,29 @@
 // tcgen05.mma.cta_group::2 (M 256, N 256) share A through the collector, a
 // four-stage ring of TMA loads, the 512 accumulator columns filling TMEM. The
 // accumulator is handed back in two halves of 256 columns. An epilogue warpgroup has
-// two groups of 64 columns in each half. It takes three of the four into registers
-// (192 of its 232 a thread), hands the first half back, computes the first group's
-// exponentials, takes the fourth into its registers and hands the second half back:
-// so the accumulator is held for a quarter of the arithmetic, while the next tile's
-// first products run on the half that is free. (Two groups at a time held it for
-// half of the arithmetic: 104 us at 2048 x 1024 x 32000.) The loss's epilogue rounds
-// z to bf16 to hold all four at once; here every sum is of the fp32 accumulators,
-// since log probabilities are compared with each other.
+// two groups of 64 columns in each half. For the statistics alone and the gradient it
+// takes three of the four into registers (192 of its 232 a thread), hands the first
+// half back, computes the first group's exponentials, takes the fourth into its
+// registers and hands the second half back: so the accumulator is held for a quarter
+// of the arithmetic, while the next tile's first products run on the half that is
+// free. (Two groups at a time held it for half of it: 104 us instead of 90 at 2048 x
+// 1024 x 32000.) The loss's epilogue rounds z to bf16 to hold all four at once; here
+// every sum is of the fp32 accumulators, since log probabilities are compared with
+// each other. What is stored goes out by the warp: 32 rows of 64 columns in its own
+// staging tile, one TMA store, no barrier among warps (by the warpgroup the gradient
+// at 2048 x 64 x 32000 took 90 us instead of 49, at 1024 columns of x 121 instead of
+// 96, the stored statistics 106 instead of 104).
+//
+// Measured, us for 2048 rows x H x 32000 columns, H = 64 / 1024 / 4096: statistics 45 /
+// 90 / 282, with the logits stored 57 / 104 / 295, with 64 picked columns 59 at 64, the
+// gradient 49 / 96 / 290; 4096 x 4096 x 128256: 2190 / 2400 / 2380 (1.96 to 1.8
+// PFLOP/s, the power cap).
 //
 // Mathematics. With c = log2(e) / temperature and, per 64 columns, the largest m:
 // y = (z - m) c, and the sums l of 2^y and s of y 2^y give the log-sum-exp and
 // E[y] of the row (joined over the columns by flce_score.cu). The gradient of a
-// row is d = p (a + b log2 p) with p = 2^((z - M) c - log2 L), plus `add` at the
-// target: ScoreRow.
+// row is d = p (a + b log2 p) with p = 2^((z - M) c - log2 L), but for the target's
+// column: ScoreRow.
 //
 // What bounds it: the tensor cores (and the power cap) from some 256 rows on,
 // below that the reads of W. The exponentials take 4096 of a tile's cycles at 16 a
@@ -45,15 +54,14 @@ struct Group {
   uint32_t (&hi)[32];
 };
 
-// The largest of 64 columns of this thread's row, ncv of them valid
-__device__ __forceinline__ float group_max(Group g, int ncv) {
-  if (ncv < 64) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if (i >= ncv) g.lo[i] = 0xFF800000u;  // -inf: adds nothing
-      if (i + 32 >= ncv) g.hi[i] = 0xFF800000u;
-    }
-  }
+// -inf, which adds nothing, in this thread's lane of a column of the accumulator
+__device__ __forceinline__ void tmem_clear(uint32_t taddr) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(0xFF800000u) : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The largest of 64 columns of this thread's row
+__device__ __forceinline__ float group_max(Group g) {
   float m4[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) m4[j] = max_nan(__uint_as_float(g.lo[j]), __uint_as_float(g.hi[j]));
@@ -98,10 +106,10 @@ __device__ __forceinline__ void group_stats(Group g, float m, float c, float2* p
   }
 }
 
-// The gradient of 64 columns of this thread's row staged as bf16; k: the target's
-// column among them, or -1.
-__device__ __forceinline__ void group_gradient(Group g, const ScoreRow& q, float c, int k, float* dcorr, bool rvalid,
-                                               uint8_t* buf, int row) {
+// The gradient of 64 columns of this thread's row staged as bf16 (but for the target's
+// entry, which launch_score_target writes: found here, it took code that the
+// instruction cache did not hold)
+__device__ __forceinline__ void group_gradient(Group g, const ScoreRow& q, float c, uint8_t* buf, int row) {
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     uint32_t (&r)[32] = half ? g.hi : g.lo;
@@ -112,17 +120,6 @@ __device__ __forceinline__ void group_gradient(Group g, const ScoreRow& q, float
       for (int i = 0; i < 8; ++i) {
         const float t = max_nan(fmaf(__uint_as_float(r[8 * j + i]) - q.largest, c, -q.log2_total), -1000.f);
         v[i] = ex2(t) * fmaf(q.b, t, q.a);
-      }
-      if (k >> 3 == 4 * half + j) {
-        // the fp32 part of the target's entry that bf16 leaves goes to dx
-        float left = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i == (k & 7)) {
-            v[i] += q.add;
-            left = v[i] - __bfloat162float(__float2bfloat16_rn(v[i]));
-          }
-        if (rvalid) *dcorr = left;
       }
       uint32_t w[4];
 #pragma unroll
@@ -330,15 +327,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int grp = (warp - 4) >> 2;
     const int wq = warp & 3;               // TMEM lanes 32 wq .. 32 wq + 31
     const int row = wq * 32 + lane;
-    const bool leader = threadIdx.x == (grp + 1) * kWarpgroup;
     const uint32_t bar = 1u + static_cast<uint32_t>(grp);
-    uint8_t* buf = sE + grp * kStagingBytes;
+    uint8_t* buf = sE + (warp - 4) * kWarpStaging;
     const float c = a.c;
     int it = 0;
     for (int u = pair; u < units; u += npairs, ++it) {
-      const bool ok = mbar_wait_bounded_cluster(tfull_bar, it & 1, a.ctrl, a.timeout_ns);
-      if (named_bar_or(bar, kWarpgroup, !ok)) break;
-      tc_fence_after();
       const int m0 = (u % num_m) * 2 * kBM + static_cast<int>(rank) * kBM;
       const int n0 = (u / num_m) * 2 * kBN;
       const int grow = m0 + row;
@@ -355,11 +348,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           end[half] = static_cast<int>(at >> (9 * (2 * half + grp + 1))) & 511;
         }
       }
+      const bool ok = mbar_wait_bounded_cluster(tfull_bar, it & 1, a.ctrl, a.timeout_ns);
+      if (named_bar_or(bar, kWarpgroup, !ok)) break;
+      tc_fence_after();
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(wq * 32) << 16);
       const size_t prow = static_cast<size_t>(grow) * a.groups;
       // tile column of group i: two in each half
       auto col_of = [&](int i) { return (i < 2 ? 0 : kBN) + grp * 128 + (i & 1) * 64; };
-      uint32_t r[3][2][32];
+      // two ahead where storing or picking takes registers too: three left too few for
+      // the arithmetic to overlap itself (68 us instead of 56 at 2048 x 64 x 32000)
+      constexpr int kAhead = MODE == kScoreGradient || (MODE == kScoreStats && !STORE) ? 3 : 2;
+      uint32_t r[kAhead][2][32];
       auto load = [&](int i, uint32_t (&to)[2][32]) {
         if (n0 + col_of(i) < a.cols) {  // uniform
           tmem_ld_32x32b_x32(tbase + col_of(i), to[0]);
@@ -376,48 +375,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const Group v{from[0], from[1]};
         if constexpr (MODE == kScorePick) pick_columns(v, a, first[i >> 1], end[i >> 1], grow, cg);
         float m = 0.f;
-        if constexpr (MODE != kScoreGradient) m = group_max(v, a.cols - cg);
+        if constexpr (MODE != kScoreGradient) m = group_max(v);
         if constexpr (STORE) {
-          // the copy that still reads the staging tile
-          if (leader) bulk_wait_group_read<0>();
-          named_bar_sync(bar, kWarpgroup);
+          // the copy that still reads the warp's staging tile
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
         }
         if constexpr (MODE == kScoreGradient) {
-          const int k = q.target >= cg && q.target < cg + 64 ? q.target - cg : -1;
-          group_gradient(v, q, c, k, a.dcorr + grow, rvalid, buf, row);
+          group_gradient(v, q, c, buf, lane);
         } else {
-          group_stats<STORE>(v, m, c, a.partials + prow + cg / 64, a.part_s + prow + cg / 64, rvalid, buf, row);
+          group_stats<STORE>(v, m, c, a.partials + prow + cg / 64, a.part_s + prow + cg / 64, rvalid, buf, lane);
         }
         if constexpr (STORE) {
           fence_proxy_async_smem();
-          named_bar_sync(bar, kWarpgroup);
-          if (leader) {
-            tma_store_2d(&tmO, smem_u32(buf), cg, m0);
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tmO, smem_u32(buf), cg, m0 + 32 * wq);
             bulk_commit_group();
           }
           __syncwarp();
         }
       };
-#pragma unroll
-      for (int i = 0; i < 3; ++i) load(i, r[i]);
-      tmem_ld_wait();
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        tmem_regs_ready(r[i][0]);
-        tmem_regs_ready(r[i][1]);
+      if (MODE != kScoreGradient && n0 + 2 * kBN > a.cols) {
+        // a ragged last group: its columns past the last become -inf in place (masks
+        // on registers would be code in every tile's way)
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i)
+#pragma unroll 1
+          for (int col = max(a.cols - n0, col_of(i)); col < col_of(i) + 64 && n0 + col_of(i) < a.cols; ++col)
+            tmem_clear(tbase + col);
+        tmem_st_wait();
       }
-      release(tempty0_bar);
-      process(0, r[0]);
-      load(3, r[0]);
+      auto ready = [&](uint32_t (&v)[2][32]) {
+        tmem_regs_ready(v[0]);
+        tmem_regs_ready(v[1]);
+      };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) load(i, r[i]);
       tmem_ld_wait();
-      tmem_regs_ready(r[0][0]);
-      tmem_regs_ready(r[0][1]);
-      release(tempty1_bar);
-      process(1, r[1]);
-      process(2, r[2]);
-      process(3, r[0]);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) ready(r[i]);
+      release(tempty0_bar);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        process(i, r[i % kAhead]);
+        if (i + kAhead < 4) {
+          load(i + kAhead, r[i % kAhead]);
+          tmem_ld_wait();
+          ready(r[i % kAhead]);
+          if (i + kAhead == 3) release(tempty1_bar);
+        }
+      }
     }
-    if (leader) bulk_wait_group<0>();
+    if (lane == 0) bulk_wait_group<0>();
   }
 
   __syncwarp();

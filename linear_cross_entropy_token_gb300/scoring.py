@@ -198,7 +198,8 @@ def token_logprobs(x: torch.Tensor, W: torch.Tensor, t=None, temperature: float 
 def token_logprobs_backward(r: TokenLogprobs, x: torch.Tensor, W: torch.Tensor, t: torch.Tensor, d_logprobs=None,
                             d_entropy=None, dx=True, dW=True, handle: FLCE = None):
     """(dx, dW) from the gradients of r.logprobs and r.entropy, (N,) float32
-    each; None stands for zero. x, W and t are those that r was made from.
+    each; None stands for zero. x, W and t are those that r was made from, and r's
+    tensors are as they were.
 
     dx, dW: True for a new tensor of the type of x or W, None to leave that
     gradient (and its product) out, or the tensor to write: dW may be float32
