@@ -577,8 +577,9 @@ flce_status flce_muon_update(flce_handle_t h, const flce_muon_args* args, const 
  * logits lie as near to the border as their fp32 sums can tell is the choice
  * theirs.) A token whose t is ignore_index gets zeros, ids -1 and no gradient,
  * whatever its row of x holds; a t out of [0, V) gets NaN, and
- * flce_async_status reports BAD_TARGET. A NaN or infinite logit makes its
- * row's results NaN (the ids stay in [0, V)). Results repeat bit for bit. No
+ * flce_async_status reports BAD_TARGET. A token whose logit is -inf has
+ * probability 0. A NaN or +inf logit, or a row of -inf alone, makes its row's
+ * results NaN (the ids stay in [0, V)). Results repeat bit for bit. No
  * host synchronisation; capturable. */
 #define FLCE_SCORE_MAX_TOP 64
 typedef struct flce_logprobs_args {

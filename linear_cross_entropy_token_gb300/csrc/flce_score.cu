@@ -161,9 +161,15 @@ __device__ __forceinline__ Pair two_sum(float a, float b) {
   return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, u)), __fsub_rn(b, u))};
 }
 
+// hi + lo; an infinite hi leaves no rest
+__device__ __forceinline__ Pair settled(float hi, float lo) {
+  const Pair s = two_sum(hi, lo);
+  return fabsf(hi) < INFINITY ? s : Pair{hi, 0.f};
+}
+
 __device__ __forceinline__ Pair add(Pair a, Pair b) {
   const Pair s = two_sum(a.hi, b.hi);
-  return two_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+  return settled(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
 }
 
 // the same in all lanes: each step adds the same two numbers on both sides
@@ -190,7 +196,7 @@ __device__ __forceinline__ Pair joined(const uint64_t (&hi)[2], const uint64_t (
   Pair v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    v[i] = two_sum(__uint_as_float(static_cast<uint32_t>(hi[i >> 1] >> (32 * (i & 1)))),
+    v[i] = settled(__uint_as_float(static_cast<uint32_t>(hi[i >> 1] >> (32 * (i & 1)))),
                    __uint_as_float(static_cast<uint32_t>(lo[i >> 1] >> (32 * (i & 1)))));
   return add(add(v[0], v[1]), add(v[2], v[3]));
 }
@@ -241,7 +247,7 @@ __device__ __forceinline__ Pair warp_dot(const float* x, const float* w, int64_t
     const Pair s = two_sum(v.hi, p);
     v = {s.hi, __fadd_rn(v.lo, __fadd_rn(s.lo, rest))};
   }
-  return warp_sum(two_sum(v.hi, v.lo));
+  return warp_sum(settled(v.hi, v.lo));
 }
 
 __device__ __forceinline__ void warp_dot2(const float* x, const float* w0, const float* w1, int64_t H, int lane,
@@ -257,7 +263,7 @@ __device__ __forceinline__ void warp_dot2(const float* x, const float* w0, const
     }
   }
 #pragma unroll
-  for (int q = 0; q < 2; ++q) out[q] = warp_sum(two_sum(out[q].hi, out[q].lo));
+  for (int q = 0; q < 2; ++q) out[q] = warp_sum(settled(out[q].hi, out[q].lo));
 }
 
 // A key that orders floats (NaN above all, 0 below every value's)
@@ -398,7 +404,7 @@ __device__ __forceinline__ float stored_bound(float v, float gm, float M, float 
 // those (a few more than `top`) the ones that reach the top-th largest lower bound. Lists are filled in any order: what they hold
 // does not depend on it, and the order of the result comes from the exact logits.
 // Returns -1 where lists overflow (many equal or nearly equal logits) or the row
-// has fewer maxima than `top`, or no finite largest logit.
+// has fewer maxima, or fewer finite ones, than `top`, or no finite largest logit.
 template <class Z, int THREADS>
 __device__ __forceinline__ int quick_candidates(const ScoreRowsArgs& a, const float2* part, const Z* z, float m, float M,
                                                 TopSmem<THREADS>& s, int64_t* id) {
@@ -425,6 +431,7 @@ __device__ __forceinline__ int quick_candidates(const ScoreRowsArgs& a, const fl
   }
   __syncthreads();
   const float key_value = s.border;
+  if (!(fabsf(key_value) < INFINITY)) return -1;  // uniform: fewer logits than `top` are finite
   const float border = key_value - fmaxf(fabsf(M), fabsf(key_value)) * 6.1e-5f;
   const float gborder = border - fmaxf(fabsf(M), fabsf(key_value)) * 6.1e-5f;
   if (m >= gborder)
@@ -753,7 +760,7 @@ __global__ void __launch_bounds__(128) score_prepare_kernel(const ScorePrepareAr
         q.b = -inv * h * kLn2;
         q.target = static_cast<int32_t>(t);
         // the target's entry, from its exact logit: g (1 - p) without cancellation
-        const float lp = a.logprobs[r];
+        const float lp = max_nan(a.logprobs[r], -1000.f);  // of probability 0 either way
         q.at = -inv * (g * expm1f(lp) + (a.d_entropy ? h * expf(lp) * (lp + a.entropy[r]) : 0.f));
         // what the exponentials' lower limit would hide
         if (!(fabsf(q.log2_total) < INFINITY) || !(fabsf(q.largest) < INFINITY)) q.a = q.at = NAN;
@@ -1053,7 +1060,7 @@ __global__ void __launch_bounds__(kDistillThreads) distill_rows_kernel(const Dis
     s_q[e] = q;
   }
   term = block_sum<kDistillThreads>(term, s_red);
-  if (threadIdx.x == 0) a.token_loss[r] = a.temperature * a.temperature * term;
+  if (threadIdx.x == 0) a.token_loss[r] = a.temperature * (a.temperature * term);
   if constexpr (GRADIENT) {
     const float factor = a.temperature / static_cast<float>(a.ctrl[kCtrlNValid]);
     ScoreRow row{M, log_L * kLog2e, factor, 0.f, 0.f, -1, expf(-log_L)};

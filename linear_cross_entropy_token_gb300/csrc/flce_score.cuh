@@ -23,13 +23,18 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// What a group's logits are taken relative to: its largest, or where all are -inf (the
+// columns of masked tokens) nothing, so that -inf stays what they are
+__device__ __forceinline__ float group_base(float largest) { return largest == -INFINITY ? 0.f : largest; }
+
 // The gradient of one fp32 logit in column j: p from the natural exponential, whose
 // argument has no factor to round
 __device__ __forceinline__ float dlogit_f32(float z, int64_t j, float c, float inv_t, const ScoreRow& q) {
   const float u = z - q.largest;
   const float t = max_nan(fmaf(u, c, -q.log2_total), -1000.f);
   const float d = expf(max_nan(u * inv_t, -700.f)) * q.inv_total * fmaf(q.b, t, q.a);
-  return j == q.target ? q.at : d;
+  // a row without a gradient has none, whatever its logits are
+  return j == q.target ? q.at : q.a == 0.f && q.b == 0.f ? 0.f : d;
 }
 
 // ---------------------------------------------------------------- products

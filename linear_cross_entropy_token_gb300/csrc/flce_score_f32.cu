@@ -160,11 +160,12 @@ __global__ void __launch_bounds__(kThreads, 4) score_f32_kernel(const __grid_con
       }
 #pragma unroll
       for (int o = 1; o < 16; o <<= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float base = group_base(mx);
       float l = 0.f, s = 0.f;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         // the natural exponential's argument has no factor to round; NaN stays NaN
-        const float d = z[c] - mx, e = expf(max_nan(d * a.inv_temperature, -700.f));
+        const float d = z[c] - base, e = expf(max_nan(d * a.inv_temperature, -700.f));
         l += e;
         s = fmaf(max_nan(d * a.c, -1000.f), e, s);
       }

@@ -197,11 +197,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         }
         m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const float base = group_base(m);
         float l = 0.f, s = 0.f;
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-          const float d0 = z[i] - m, d1 = z[i + 1] - m;
+          const float d0 = z[i] - base, d1 = z[i + 1] - base;
           const float y0 = max_nan(d0 * a.c, -1000.f), y1 = max_nan(d1 * a.c, -1000.f);
           const float e0 = ex2(y0), e1 = ex2(y1);
           l += e0 + e1;

@@ -76,6 +76,7 @@ template <bool STORE>
 __device__ __forceinline__ void group_stats(Group g, float m, float c, float2* part, float* part_s, bool rvalid,
                                             uint8_t* buf, int row) {
   float l[4] = {0.f, 0.f, 0.f, 0.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+  const float base = group_base(m);
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     uint32_t (&r)[32] = half ? g.hi : g.lo;
@@ -84,7 +85,7 @@ __device__ __forceinline__ void group_stats(Group g, float m, float c, float2* p
       uint32_t w[4];
 #pragma unroll
       for (int i = 8 * j; i < 8 * j + 8; i += 2) {
-        const float d0 = __uint_as_float(r[i]) - m, d1 = __uint_as_float(r[i + 1]) - m;
+        const float d0 = __uint_as_float(r[i]) - base, d1 = __uint_as_float(r[i + 1]) - base;
         // at -1000 the exponential is 0 and y 2^y is too, which -inf would make NaN
         const float y0 = max_nan(d0 * c, -1000.f), y1 = max_nan(d1 * c, -1000.f);
         const float e0 = ex2(y0), e1 = ex2(y1);
@@ -129,6 +130,12 @@ __device__ __forceinline__ void group_gradient(Group g, const ScoreRow& q, float
       }
       stage_piece(buf, row, 4 * half + j, w);
     }
+  }
+  // a row without a gradient, whatever its logits are: 0 times them may be NaN
+  if (q.a == 0.f && q.b == 0.f) {
+    const uint32_t zero[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j) stage_piece(buf, row, j, zero);
   }
 }
 

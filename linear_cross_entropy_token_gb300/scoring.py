@@ -121,10 +121,18 @@ def _vector(name, t, n, dev):
     return t.data_ptr()
 
 
+def _span(a):
+    """First and last byte of a tensor's memory, from its strides."""
+    if a.numel() == 0:
+        return a.data_ptr(), a.data_ptr()
+    last = sum((n - 1) * s for n, s in zip(a.shape, a.stride()))
+    return a.data_ptr(), a.data_ptr() + (last + 1) * a.element_size()
+
+
 def _overlap(a, b) -> bool:
-    """Whether two contiguous tensors share memory."""
-    first, second = a.data_ptr(), b.data_ptr()
-    return (first < second + b.numel() * b.element_size() and second < first + a.numel() * a.element_size())
+    """Whether the memory of one tensor reaches into that of the other."""
+    (a0, a1), (b0, b1) = _span(a), _span(b)
+    return a0 < b1 and b0 < a1
 
 
 def _gradient(name, want, like, dtypes, read=()):
@@ -138,7 +146,7 @@ def _gradient(name, want, like, dtypes, read=()):
             or want.device != like.device or not want.is_contiguous()):
         raise ValueError(f"{name} must be True, None or a contiguous tensor of shape {tuple(like.shape)}, "
                          f"{' or '.join(str(d) for d in dtypes)}, on {like.device}")
-    if any(t is not None and t.is_contiguous() and t.device == want.device and _overlap(want, t) for t in read):
+    if any(t is not None and t.device == want.device and _overlap(want, t) for t in read):
         raise ValueError(f"{name} must not share memory with the inputs or the other gradient")
     return want
 
@@ -217,7 +225,7 @@ def token_logprobs_backward(r: TokenLogprobs, x: torch.Tensor, W: torch.Tensor, 
         raise ValueError("the kept logits are of other sizes")
     p_logprobs = _vector("d_logprobs", d_logprobs, N, dev)
     p_entropy = _vector("d_entropy", d_entropy, N, dev)
-    read = (x, W, t, d_logprobs, d_entropy, r.entropy, r.stats, r.kept)
+    read = (x, W, t, d_logprobs, d_entropy, r.logprobs, r.entropy, r.stats, r.kept)
     out_x = _gradient("dx", dx, x, (x.dtype,), read)
     out_W = _gradient("dW", dW, W, tuple({W.dtype, torch.float32}), (*read, out_x))
     a = r.bind(x, W, t, 0)
