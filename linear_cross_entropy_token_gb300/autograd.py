@@ -144,6 +144,12 @@ def route(logits: torch.Tensor, k: int, valid=None, offsets=None, renormalize: b
     return RouteFunction.apply(logits, k, valid, offsets, renormalize, handle)
 
 
+def _without_graph(*tensors):
+    """The tensors, of which none asks for a gradient where none is recorded: needs_input_grad
+    does not see no_grad."""
+    return tensors if torch.is_grad_enabled() else tuple(t.detach() for t in tensors)
+
+
 class TokenLogprobsFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, W, t, temperature, top, ignore_index, keep_logits, handle):
@@ -185,7 +191,10 @@ def token_logprobs(x: torch.Tensor, W: torch.Tensor, t: torch.Tensor, temperatur
     Gradients reach x and W from logprobs and entropy; the alternatives carry
     none. Neither direction synchronises the host; an input that needs no
     gradient costs no product. keep_logits holds the logits until the backward,
-    which else computes them again."""
+    which else computes them again. A backward pass that is captured into a CUDA
+    graph needs leaves that no graph of autograd from outside the capture still
+    holds; scoring.token_logprobs_backward asks for nothing of the kind."""
+    x, W = _without_graph(x, W)
     return TokenLogprobsFunction.apply(x, W, t, temperature, top, ignore_index, keep_logits, handle)
 
 
@@ -212,5 +221,7 @@ def linear_distillation(x: torch.Tensor, W: torch.Tensor, ids: torch.Tensor, log
     """Distillation from a teacher's top logits, fused as linear_cross_entropy is:
     the forward computes the gradients too and the backward scales them. Returns
     the loss of scoring.distill, a 0-dim float32 tensor; never synchronises the
-    host. The teacher gets no gradient."""
+    host. The teacher gets no gradient. To capture a step into a CUDA graph, see
+    token_logprobs; scoring.distill is the call without autograd."""
+    x, W = _without_graph(x, W)
     return LinearDistillationFunction.apply(x, W, ids, logits, temperature, handle)

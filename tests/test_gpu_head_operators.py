@@ -59,6 +59,28 @@ def test_gradients_that_are_not_asked_for():
         assert not linear_distillation(x, W, t[:, None], torch.zeros(300, 1, device="cuda")).requires_grad
 
 
+def test_evaluating_parameters_computes_no_gradients():
+    import linear_cross_entropy_token_gb300 as f
+    from linear_cross_entropy_token_gb300.autograd import linear_distillation, token_logprobs
+    x, W, t, ids, z, _ = inputs(3)
+    h = f.FLCE("bf16", 0)
+
+    def launches(call):
+        before = h.launch_count()
+        call()
+        return h.launch_count() - before
+
+    want = launches(lambda: f.distill(x, W, ids, z, backward=False, handle=h))
+    a, b = x.clone().requires_grad_(), W.clone().requires_grad_()
+    with torch.no_grad():
+        assert launches(lambda: linear_distillation(a, b, ids, z, handle=h)) == want
+        held = torch.cuda.memory_allocated()
+        r = token_logprobs(a, b, t, keep_logits=True, handle=h)
+        assert torch.cuda.memory_allocated() - held < x.shape[0] * W.shape[0]
+    assert not r[0].requires_grad
+    assert launches(lambda: linear_distillation(a, b, ids, z, handle=h)) > want
+
+
 def test_one_hot_teacher_is_the_cross_entropy():
     """Distillation from one entry a token, the loss it trains beside, and the log probabilities agree."""
     import linear_cross_entropy_token_gb300 as f
