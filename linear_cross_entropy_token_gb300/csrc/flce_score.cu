@@ -1106,7 +1106,9 @@ __global__ void __launch_bounds__(1024) distill_finish_kernel(const float* __res
 }
 
 // With few rows a row's latency counts, and large blocks take its candidates at
-// once; with many, eight blocks of 128 threads share an SM.
+// once; with many, eight blocks of 128 threads share an SM. Scoring with 20 alternatives
+// at 4096 x 128256, 1024 / 128 threads: 212 / 247 us for 48 rows, 358 / 372 for 304, 568 /
+// 530 for 700 (1024 x 32000: 42 / 46, 78 / 69, 138 / 89).
 constexpr int kFewRows = 304;
 
 unsigned blocks_of(int64_t n, int64_t per) { return static_cast<unsigned>((n + per - 1) / per); }

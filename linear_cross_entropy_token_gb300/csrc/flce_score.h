@@ -80,8 +80,10 @@ inline double score_gain(int64_t H) { return 1.0 + 0.13 / 8388608.0 * (static_ca
 
 // ----------------------------------------------------- flce_score_few.cu
 
-// The statistics for at most kScoreFew rows
-constexpr int kScoreFew = 64;
+// The statistics for at most kScoreFew rows: the two kernels meet at 128 (scoring 4096 x
+// 128256 in a captured graph: 212 us here and 230 on pair tiles at 64 rows, 216 and 231
+// at 96, 225 and 232 at 128; 1024 x 32000: 36 and 38, 38 and 40, 40 and 40)
+constexpr int kScoreFew = 128;
 struct ScoreFewArgs {
   int32_t rows, padded;          // tokens; rounded up to 16
   int32_t cols, groups;          // V; partials per row

@@ -51,7 +51,9 @@ struct Needs {
 
 // Rows that do not count are left out of the products where that can spare a tile of
 // 256 rows (bf16; fp32 inputs are small models', whose products know no row count of
-// the device's).
+// the device's). Scoring 4096 x 128256, left out / computed all the same: 241 / 239 us for
+// 256 rows half of which count, 244 / 343 for 512 of which 205 do, 637 / 627 for 1024
+// that all do (1024 x 32000: 44 / 40, 45 / 50, 77 / 71).
 constexpr int64_t kCompactRows = 256;
 
 // Gradients: chunks, tile shapes and splits are the loss's plan with both

@@ -14,7 +14,10 @@
 // turns it over in shared memory, and four threads take 64 columns of a token.
 //
 // Measured at 4096 x 128256: one token 180 us (5.8 TB/s) where the pair tiles take 238,
-// 48 tokens 212 where they take 216; at 64 tokens the two meet.
+// 128 tokens 193 where they take 200. Time grows with W's bytes at 6.5 TB/s, above some
+// 20 us that a cold start takes (much of it the write-back of what L2 held). Even shares
+// of k-blocks a CTA instead of whole tiles, joined where two meet, gained nothing: 181
+// us, and at 64 tokens 7 more.
 #include <cuda_fp16.h>
 
 #include <algorithm>

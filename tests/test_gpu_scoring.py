@@ -292,3 +292,13 @@ def test_few_rows(N, H, V):
     a = torch.linspace(-1, 1, N, device="cuda")
     d = ref.d_scores(t.clamp(min=0), a.double(), 0 * a.double()) * (t != -100)[:, None]
     check_gradients(*f.token_logprobs_backward(r, x, W, t, a), d, x, W, kept_distance(ref.raw, 1 / (0.9 * math.log(2))))
+
+
+@pytest.mark.parametrize("N", [80, 97, 128, 129])
+@pytest.mark.parametrize("H,V", [(72, 300), (1024, 20011)])
+def test_up_to_128_rows(N, H, V):
+    x, W, t, g = make_head(N, H, V, "bf16", seed=N)
+    t[torch.rand(N, generator=g) < 0.1] = -100
+    live = t >= 0
+    for top, keep in ((0, False), (7, True)):
+        check_forward(score(x, W, t, top=top, keep_logits=keep), Reference(x, W), t, top, live)
