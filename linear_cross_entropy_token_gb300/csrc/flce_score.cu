@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(128) score_prepare_kernel(const ScorePrepareAr
         const float inv = a.inv_temperature;
         const float g = a.d_logprobs ? a.d_logprobs[r] : 0.f;
         const float h = a.d_entropy ? a.d_entropy[r] : 0.f;
-        q.largest = st.x;
+        q.largest = st.x * a.largest_scale;
         q.log2_total = st.y * kLog2e;
         q.inv_total = expf(-st.y);
         q.a = -inv * (a.d_entropy ? fmaf(h, a.entropy[r], g) : g);

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/flce.h"
 
 namespace flce {
@@ -71,12 +73,15 @@ int score_gemm_max_clusters();
 // every 16-deep step: by half a last place on average, 2^-24 of a binade's upper
 // end. A sum that ends at z has been at z k / n after k of its n steps on average
 // (products come in no order), so it loses 2^-24 z (average over a binade 0.72) n / 2
-// in all: 2^-23 n 0.18. Measured at 64 to 8192 columns: 0.10 to 0.13, the share
-// rising to 0.133 (those bits that a step's aligned products keep below the last
-// place are not cut). It matters because all logits of a row shrink alike and their
+// in all: 2^-23 n 0.18. Measured: 0.10 at 64 columns, 0.135 at 1024, 0.135 to 0.14 at
+// 2048 to 8192 (those bits that a step's aligned products keep below the last place
+// are not cut). It matters because all logits of a row shrink alike and their
 // log-sum-exp with them: 3.8e-6 at 4096 columns, where rounding to nearest would
-// leave a tenth of that.
-inline double score_gain(int64_t H) { return 1.0 + 0.13 / 8388608.0 * (static_cast<double>(H) / 16.0); }
+// leave a tenth of that. A sum that is taken in parts loses as much less (0.128 to
+// 0.13 by the part).
+inline double score_gain(int64_t H, int parts = 1) {
+  return 1.0 + (parts > 1 ? 0.13 : 0.136) / 8388608.0 * (static_cast<double>(H) / 16.0) / parts;
+}
 
 // ----------------------------------------------------- flce_score_few.cu
 
@@ -84,10 +89,16 @@ inline double score_gain(int64_t H) { return 1.0 + 0.13 / 8388608.0 * (static_ca
 // 128256 in a captured graph: 212 us here and 230 on pair tiles at 64 rows, 216 and 231
 // at 96, 225 and 232 at 128; 1024 x 32000: 36 and 38, 38 and 40, 40 and 40)
 constexpr int kScoreFew = 128;
+// The parts that a sum is taken in, each in TMEM columns of its own (two tiles' at once)
+inline int score_few_parts(int64_t rows, int64_t H) {
+  const int64_t padded = (rows + 15) / 16 * 16, blocks = (H + kBK - 1) / kBK;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({4, 256 / std::max<int64_t>(padded, 1), blocks})));
+}
 struct ScoreFewArgs {
   int32_t rows, padded;          // tokens; rounded up to 16
   int32_t cols, groups;          // V; partials per row
   int32_t kb_total;
+  int32_t parts;                 // score_few_parts()
   int32_t tiles, stages, tmem_columns;  // filled in by the launch
   float c;
   int64_t ldv;
@@ -222,6 +233,7 @@ struct ScorePrepareArgs {
   // gradient
   int64_t V, ignore_index;
   float inv_temperature;
+  float largest_scale;           // from the forward's product to the gradient's
   const int64_t* t;              // null: rows of x alone
   const float2* stats;
   const float* logprobs;

@@ -39,6 +39,7 @@ Kept kept_layout(bool bf16, int64_t N, int64_t V) {
 struct Plan {
   int64_t chunk = 0, ldv = 0, groups = 0, splits = 1;
   bool compact = false;  // chunks are of the rows that count
+  int few_parts = 0;     // above 0: the statistics' product is flce_score_few.cu's
   uint64_t ctrl = 0, claims = 0, lead = 0, z = 0, partials = 0, part_s = 0, row = 0, dcorr = 0, xm = 0, order = 0, live = 0,
            parts = 0, entries = 0, picked = 0, dw = 0, total = 0;
 };
@@ -99,6 +100,7 @@ flce_status make_plan(flce_handle_t h, int64_t N, int64_t H, int64_t V, const Ne
     return at;
   };
   const uint64_t c = static_cast<uint64_t>(p.chunk);
+  if (bf16 && q.stats && !q.teacher && N <= kScoreFew) p.few_parts = score_few_parts(N, H);
   p.compact = bf16 && q.masked && (N > kCompactRows || q.teacher > 0);
   // the control block and the chunks' counters of units, cleared together
   p.claims = kCtrlWords * 4;
@@ -224,13 +226,14 @@ flce_status run_stats(flce_handle_t h, const Product& q, void* z, float2* partia
   std::string why;
   if (!map_bf16_2d(&mx, q.x, q.H, q.chunk.rows, q.H * 2, 64, 128, &why) || !map_bf16_2d(&mw, q.W, q.H, q.V, q.H * 2, 64, 128, &why))
     return fail(h, FLCE_ERR_INVALID_ARG, "%s", why.c_str());
-  if (q.chunk.rows <= kScoreFew && !q.parts && !q.chunk.live) {
+  if (q.p->few_parts > 0) {
     ScoreFewArgs f{};
     f.rows = q.chunk.rows;
     f.padded = (q.chunk.rows + 15) / 16 * 16;
     f.cols = static_cast<int>(q.V);
     f.groups = groups;
     f.kb_total = static_cast<int>(cdiv(q.H, kBK));
+    f.parts = q.p->few_parts;
     f.c = q.c;
     f.ldv = q.p->ldv;
     f.z = static_cast<__half*>(z);
@@ -425,6 +428,11 @@ flce_status logprobs_plan(flce_handle_t h, const flce_logprobs_args* r, bool bac
   return make_plan(h, r->N, r->H, r->V, q, p);
 }
 
+// What the forward's product of z lacks
+double logprobs_gain(flce_handle_t h, const flce_logprobs_args* r) {
+  return !is_bf16(h) ? 1.0 : score_gain(r->H, r->N <= kScoreFew ? score_few_parts(r->N, r->H) : 1);
+}
+
 // The rows that count in order, what the others get, and the chunks of the former
 flce_status logprobs_rows(flce_handle_t h, const flce_logprobs_args* r, const Plan& p, uint8_t* ws, void* dx, bool backward,
                           cudaStream_t s) {
@@ -512,7 +520,7 @@ flce_status flce_logprobs_forward(flce_handle_t h, const flce_logprobs_args* r, 
   st = logprobs_rows(h, r, p, ws, nullptr, false, s);
   if (st != FLCE_OK) return st;
   const Kept K = kept_layout(bf16, r->N, r->V);
-  const double gain = bf16 ? score_gain(r->H) : 1.0, c = gain * kLog2e / r->temperature;
+  const double gain = logprobs_gain(h, r), c = gain * kLog2e / r->temperature;
   const float inv_t = static_cast<float>(1.0 / r->temperature);
   for (int64_t off = 0; off < r->N; off += p.chunk) {
     const ScoreChunk chunk = chunk_of(p, ws, off, r->N);
@@ -596,7 +604,8 @@ flce_status flce_logprobs_backward(flce_handle_t h, const flce_logprobs_args* r,
   st = logprobs_rows(h, r, p, ws, dx, true, s);
   if (st != FLCE_OK) return st;
   const Kept K = kept_layout(bf16, r->N, r->V);
-  const double gain = bf16 ? score_gain(r->H) : 1.0;
+  // kept logits are the forward's; the product of those computed again is its own
+  const double kept_gain = logprobs_gain(h, r), gain = kept || !bf16 ? kept_gain : score_gain(r->H);
   const float c = static_cast<float>(gain * kLog2e / r->temperature);
   const float inv_t = static_cast<float>(1.0 / r->temperature);
   ScoreRow* row = reinterpret_cast<ScoreRow*>(ws + p.row);
@@ -615,6 +624,7 @@ flce_status flce_logprobs_backward(flce_handle_t h, const flce_logprobs_args* r,
     a.V = r->V;
     a.ignore_index = r->ignore_index;
     a.inv_temperature = inv_t;
+    a.largest_scale = static_cast<float>(kept_gain / gain);
     a.t = r->t;
     a.stats = reinterpret_cast<const float2*>(r->stats);
     a.logprobs = r->logprobs;

