@@ -553,9 +553,13 @@ __device__ __noinline__ int careful_candidates(const ScoreRowsArgs& a, const flo
                                 put);
 }
 
-// log p of an exact logit: M is short of what the product lost
-__device__ __forceinline__ float score_log_p(const ScoreRowsArgs& a, Pair z, float M, float log_L) {
-  return fmaf((z.hi - M) + (z.lo - M * a.loss), a.inv_temperature, -log_L);
+// log p of an exact logit: M is short of what the product lost. A column that has more
+// than half of the row's probability (only one can) is the 1 in L; with its exact logit
+// there too, 1 - p keeps its bits where the product's error of M is more than that.
+__device__ __forceinline__ float score_log_p(const ScoreRowsArgs& a, Pair z, float M, float L, float log_L) {
+  const float above = (z.hi - M) + (z.lo - M * a.loss), d = above * a.inv_temperature;
+  if (L < 1.9f && d > -0.05f) return -log1pf(fmaxf(L - 1.f, 0.f) * expf(-d));
+  return fmaf(above, a.inv_temperature, -log_L);
 }
 
 __device__ __forceinline__ void report(const uint32_t* ctrl, uint32_t* host_error) {
@@ -612,7 +616,7 @@ __global__ void __launch_bounds__(32 * kWarpRows) score_warp_rows_kernel(const S
   if (a.t && !bad)
     z = warp_dot(static_cast<const E*>(a.x) + r * a.H, static_cast<const E*>(a.W) + t * a.H, a.H, lane);
   if (lane != 0) return;
-  if (a.t) a.logprobs[r] = bad ? NAN : score_log_p(a, z, M, log_L);
+  if (a.t) a.logprobs[r] = bad ? NAN : score_log_p(a, z, M, L, log_L);
   a.entropy[r] = log_L - kLn2 * S / L;
   a.stats[r] = make_float2(M, log_L);
   if (bad) *reinterpret_cast<volatile uint32_t*>(a.host_error) = kErrBadTarget;
@@ -705,12 +709,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) score_rows_kernel(con
 #pragma unroll 4
     for (int j = 0; j < n; ++j) rank += s_order[j] > own || (s_order[j] == own && s_id[j] < id);
     if (rank < a.top) {
-      a.top_logprobs[r * a.top + rank] = score_log_p(a, s_dot[threadIdx.x], M, log_L);
+      a.top_logprobs[r * a.top + rank] = score_log_p(a, s_dot[threadIdx.x], M, L, log_L);
       a.top_ids[r * a.top + rank] = id;
     }
   }
   if (threadIdx.x == 0) {
-    if (a.t) a.logprobs[r] = bad ? NAN : score_log_p(a, s_dot[n], M, log_L);
+    if (a.t) a.logprobs[r] = bad ? NAN : score_log_p(a, s_dot[n], M, L, log_L);
     a.entropy[r] = log_L - kLn2 * S / L;
     a.stats[r] = make_float2(M, log_L);
     if (bad) *reinterpret_cast<volatile uint32_t*>(a.host_error) = kErrBadTarget;

@@ -302,3 +302,35 @@ def test_up_to_128_rows(N, H, V):
     live = t >= 0
     for top, keep in ((0, False), (7, True)):
         check_forward(score(x, W, t, top=top, keep_logits=keep), Reference(x, W), t, top, live)
+
+
+@pytest.mark.parametrize("top", [0, 2])
+@pytest.mark.parametrize("N,H,dtype", [(40, 183, "fp32"), (40, 512, "bf16"), (300, 512, "bf16")])
+def test_near_certain_tokens(N, H, dtype, top):
+    """What is left of a probability close to 1 comes from the other tokens, not from the largest logit's error."""
+    import linear_cross_entropy_token_gb300 as f
+    g = torch.Generator().manual_seed(H)
+    V = 800
+    W = (torch.randn(V, H, generator=g) * 1.3 / math.sqrt(H)).to(DT[dtype])
+    t = torch.randint(0, V, (N,), generator=g)
+    x = torch.randn(N, H, generator=g) + 17.0 * W[t].float() / (1.3 ** 2)
+    x, W, t = x.to(DT[dtype]).cuda(), W.cuda(), t.cuda()
+    ref = Reference(x, W)
+    want = ref.lp.gather(1, t[:, None])[:, 0]
+    sure = want > -1e-3
+    assert sure.sum() > N / 2
+    r = score(x, W, t, top=top)
+    # L, a sum in [1, 2), is rounded by at most 2^-24 at each addition that its largest term meets: 16 of a
+    # group's four sums, 2 that join them, one of the row's and 5 that join its lanes, 24 in all (3e-7, five of
+    # them, was too few); and the other tokens' logits' errors
+    err = 24 * 2.0 ** -24 + want.abs() * (2 * ref.sum_error() + 4e-6)
+    assert ((r.logprobs - want).abs() <= err)[sure].all()
+    if top:
+        assert torch.equal(r.top_ids[sure, 0], t[sure]) and torch.equal(r.top_logprobs[sure, 0], r.logprobs[sure])
+    da = torch.ones(N, device="cuda")
+    _, dW = f.token_logprobs_backward(r, x, W, t, d_logprobs=da, dx=None, dW=torch.empty(V, H, device="cuda"))
+    d = ref.d_scores(t, da.double(), torch.zeros(N, dtype=torch.float64, device="cuda"))
+    if dtype == "fp32":
+        off = torch.zeros_like(d).scatter_add(1, t[:, None], err[:, None]) + d.abs() * (2 * ref.sum_error()[:, None] + 4e-6)
+        tol = off.T @ x.double().abs() + 1e-6 * d.abs().T @ x.double().abs()
+        assert ((dW - d.T @ x.double()).abs() <= tol).all()
